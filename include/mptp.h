@@ -357,6 +357,63 @@ MP_API mp_status mp_attn_fwd(const mp_bf16* X, const mp_bf16* Wqkv, const mp_bf1
                       uint32_t* d_status, void* stream);
 
 /*
+ * Gated feed-forward block: both projections, the activation and the product in one kernel.
+ *   [G | U] = X W,  Y = act(G) * U,  Z = sum_i Y_i Wd_i
+ * with W [h, 2f] = [Wg | Wu]. Shard i of t owns columns [i f/t, (i+1) f/t) of Wg and of Wu and
+ * the same rows of Wd; the g sum runs in the K-loop in ascending order, as in mp_mlp_fwd.
+ * act: MP_ACT_SILU g / (1 + e^-g), or MP_ACT_GELU the exact erf GeLU; Y is computed in fp32
+ * from the fp32 accumulators of G and U.
+ *   X [T, h], W [h, 2f], Wd [f, h]           inputs
+ *   Z [T, h], Y [T, f]                       outputs
+ *   GU_save [T, 2f] or NULL                  output: [G | U] rounded to bf16; needed by mp_glu_bwd
+ *   Size rules: T >= 0; h % 64 == 0; f % t == 0; (f / t) % 64 == 0; t >= 1.
+ */
+#define MP_ACT_SILU 0
+#define MP_ACT_GELU 1
+MP_API mp_status mp_glu_fwd(const mp_bf16* X, const mp_bf16* W, const mp_bf16* Wd,
+                     mp_bf16* Z, mp_bf16* Y, mp_bf16* GU_save,
+                     int T, int h, int f, int t, int act,
+                     uint32_t* d_status, void* stream);
+
+/*
+ * Its backward, from GU_save and Y of the forward:
+ *   dY = dZ Wd^T (never stored);  dG = dY * U * act'(G);  dU = dY * act(G);
+ *   dX = [dG | dU] W^T (the f sum in the K-loop);  dW = X^T [dG | dU];  dWd = Y^T dZ.
+ *   X [T,h], W [h,2f], Wd [f,h], GU [T,2f], Y [T,f], dZ [T,h]   inputs
+ *   dX [T,h], dW [h,2f], dWd [f,h]                              outputs
+ *   dGU_ws [T,2f]                  workspace (caller-owned); holds [dG | dU] (bf16) on return
+ *   Size rules as mp_glu_fwd. T = 0 zeroes dW and dWd. Streams as mp_mlp_bwd.
+ */
+MP_API mp_status mp_glu_bwd(const mp_bf16* X, const mp_bf16* W, const mp_bf16* Wd,
+                     const mp_bf16* GU, const mp_bf16* Y, const mp_bf16* dZ,
+                     mp_bf16* dX, mp_bf16* dW, mp_bf16* dWd, mp_bf16* dGU_ws,
+                     int T, int h, int f, int t, int act,
+                     uint32_t* d_status, void* stream);
+
+/*
+ * Rotary positions with up to four axes (time, height, width, ...), for every head of x.
+ * A head's rotated elements form sections[0] + ... + sections[axes-1] = n pairs (a, b), pair i at
+ * elements (i, i + n), or (2i, 2i + 1) with MP_ROPE_INTERLEAVED; axis k owns the k-th run of
+ * sections[k] consecutive pairs. Pair i becomes (a cos A - b sin A, b cos A + a sin A),
+ *   A = pos[axis][token] * base^(-i / n), or with MP_ROPE_PER_AXIS base^(-j / sections[axis])
+ *   for the j-th pair of its axis.
+ * MP_ROPE_INVERSE rotates back by -A: the gradient of the rotation. Elements [2n, d) pass through.
+ * Angles are exact to 2^-20 turns for every int32 position (64-bit binary fractions of a turn).
+ *   x, y [T, heads, d], rows ldx, ldy elements apart (views of a packed projection are fine);
+ *   y may be x itself (then ldx == ldy), and must not overlap it otherwise. pos [axes, T] int32.
+ *   sections: `axes` ints in host memory, read during the call.
+ *   Size rules: 1 <= axes <= 4; sections[k] >= 0; n >= 4, n % 4 == 0; 2n <= d <= 256; d % 8 == 0;
+ *   ldx, ldy >= heads * d and multiples of 8.
+ */
+#define MP_ROPE_INTERLEAVED 0x1u
+#define MP_ROPE_PER_AXIS 0x2u
+#define MP_ROPE_INVERSE 0x4u
+MP_API mp_status mp_rope_axes(const mp_bf16* x, mp_bf16* y, const int32_t* pos,
+                       int T, int heads, int d, long long ldx, long long ldy,
+                       int axes, const int* sections, double base, uint32_t flags,
+                       void* stream);
+
+/*
  * mp_vocab_ce for callers that cannot allocate device memory. The paper has no
  * counterpart to this entry point; it exists for callers whose device memory is
  * owned by another pool (a serving runtime that reserves HBM at start-up and

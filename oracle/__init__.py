@@ -25,6 +25,10 @@ The cross-entropy backward (``ce_bwd``) is not spelled out on the pages, which
 train the model but describe only the forward fusion; it is the plain derivative
 of the softmax cross-entropy, pinned by finite differences.
 
+The gated block, the rotation with several axes and the packed attention with its
+gradients are written from the definitions in their modules, and pinned by finite
+differences, closed forms and the ops they reduce to.
+
 Pins (tests marked "not gpu"): GELU values printed in [p5] §2.2, the [p5] §3.1
 worked example and its wrong row cut, closed forms of GELU, finite differences
 of the backward, brute-force softmax cross-entropy on tiny vocabularies, the
@@ -47,6 +51,9 @@ from .ce import (ce_loss, ce_partition_triples, ce_combine, ce_loss_partitioned,
 from .padding import pad_vocab
 from .embed import embed_sharded
 from .attn import attention_heads, attn_fwd, attn_fwd_sharded, attn_fwd_rows
+from .attn_varlen import attn_varlen_fwd, attn_varlen_bwd
+from .glu import glu_act, glu_fwd, glu_bwd, glu_sharded_fwd
+from .rope import rope, rope_angles
 
 __all__ = [
     "gelu", "gelu_prime", "std_normal_cdf", "std_normal_pdf",
@@ -56,4 +63,7 @@ __all__ = [
     "ce_bwd_sampled",
     "pad_vocab", "embed_sharded",
     "attention_heads", "attn_fwd", "attn_fwd_sharded", "attn_fwd_rows",
+    "attn_varlen_fwd", "attn_varlen_bwd",
+    "glu_act", "glu_fwd", "glu_bwd", "glu_sharded_fwd",
+    "rope", "rope_angles",
 ]

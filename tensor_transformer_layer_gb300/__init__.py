@@ -38,7 +38,7 @@ EXPORTS = ("mp_mlp_fwd", "mp_mlp_bwd", "mp_mlp_fwd_shards", "mp_mlp_bwd_shards",
            "mp_vocab_ce_combine", "mp_status_string", "mp_status_from_device", "mp_version",
            "mp_vocab_ce_noalloc", "mp_vocab_ce_bwd_workspace_bytes", "mp_vocab_ce_bwd_workspace_bytes_one_pass",
            "mp_vocab_ce_bwd", "mp_vocab_ce_lse", "mp_vocab_ce_bwd_lse", "mp_vocab_embed",
-           "mp_attn_fwd")
+           "mp_attn_fwd", "mp_glu_fwd", "mp_glu_bwd", "mp_rope_axes")
 
 
 class MptpError(RuntimeError):
@@ -50,6 +50,7 @@ class MptpError(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 
 
 def lib() -> ctypes.CDLL:
@@ -94,6 +95,12 @@ def lib() -> ctypes.CDLL:
         L.mp_vocab_ce_bwd_lse.restype = _I
         L.mp_attn_fwd.argtypes = [_P] * 6 + [_I, _I, _I, _I, _I, _P, _P]
         L.mp_attn_fwd.restype = _I
+        L.mp_glu_fwd.argtypes = [_P] * 6 + [_I] * 5 + [_P, _P]
+        L.mp_glu_fwd.restype = _I
+        L.mp_glu_bwd.argtypes = [_P] * 10 + [_I] * 5 + [_P, _P]
+        L.mp_glu_bwd.restype = _I
+        L.mp_rope_axes.argtypes = [_P, _P, _P, _I, _I, _I, _L, _L, _I, _P, ctypes.c_double, ctypes.c_uint32, _P]
+        L.mp_rope_axes.restype = _I
         L.mp_vocab_embed.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P]
         L.mp_vocab_embed.restype = _I
         L.mp_vocab_ce_noalloc.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]
@@ -374,6 +381,78 @@ def mp_attn_fwd(X, Wqkv, Wo, out, QKV, O, *, b: int, s: int, heads: int, t: int,
         _ptr(out, "out", shape=(T, h)), _ptr(QKV, "QKV", shape=(T, 3 * h)), _ptr(O, "O", shape=(T, h)),
         int(b), int(s), h, int(heads), int(t), _status_ptr(d_status), _stream(stream))
     _check("mp_attn_fwd", code)
+
+
+ACTS = {"silu": 0, "gelu": 1}
+
+
+def _act(act):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def mp_glu_fwd(X, W, Wd, Z, Y, GU_save=None, *, t: int, act: str = "silu", d_status=None, stream=None) -> None:
+    """Gated feed-forward block: [G | U] = X W, Y = act(G) * U, Z = Y Wd; W [h, 2f], act "silu" or "gelu"."""
+    T, h = X.shape
+    f = Wd.shape[0]
+    code = lib().mp_glu_fwd(
+        _ptr(X, "X", shape=(T, h)), _ptr(W, "W", shape=(h, 2 * f)), _ptr(Wd, "Wd", shape=(f, h)),
+        _ptr(Z, "Z", shape=(T, h)), _ptr(Y, "Y", shape=(T, f)),
+        _ptr(GU_save, "GU_save", shape=(T, 2 * f), allow_none=True), T, h, f, int(t), _act(act),
+        _status_ptr(d_status), _stream(stream))
+    _check("mp_glu_fwd", code)
+
+
+def mp_glu_bwd(X, W, Wd, GU, Y, dZ, dX, dW, dWd, dGU_ws, *, t: int, act: str = "silu", d_status=None,
+               stream=None) -> None:
+    """Backward of mp_glu_fwd from its GU_save and Y: dX [T,h], dW [h,2f], dWd [f,h]; dGU_ws [T,2f] workspace."""
+    T, h = X.shape
+    f = Wd.shape[0]
+    code = lib().mp_glu_bwd(
+        _ptr(X, "X", shape=(T, h)), _ptr(W, "W", shape=(h, 2 * f)), _ptr(Wd, "Wd", shape=(f, h)),
+        _ptr(GU, "GU", shape=(T, 2 * f)), _ptr(Y, "Y", shape=(T, f)), _ptr(dZ, "dZ", shape=(T, h)),
+        _ptr(dX, "dX", shape=(T, h)), _ptr(dW, "dW", shape=(h, 2 * f)), _ptr(dWd, "dWd", shape=(f, h)),
+        _ptr(dGU_ws, "dGU_ws", shape=(T, 2 * f)), T, h, f, int(t), _act(act), _status_ptr(d_status), _stream(stream))
+    _check("mp_glu_bwd", code)
+
+
+def _heads_view(x, name, shape=None):
+    """Pointer and row pitch of a bf16 [tokens, heads, d] tensor whose heads are packed in each row (a view of
+    some heads of a wider row is fine)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != 3 or (shape is not None and tuple(x.shape) != tuple(shape)):
+        want = "[tokens, heads, d]" if shape is None else tuple(shape)
+        raise ValueError(f"{name} must have shape {want}, got {tuple(x.shape)}")
+    T, heads, d = x.shape
+    if x.numel() == 0:
+        return None, heads * d
+    if (d > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != d):
+        raise ValueError(f"{name}: each token's heads must be contiguous (strides (any, d, 1))")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    pitch = x.stride(0) if T > 1 else heads * d
+    if pitch < heads * d:
+        raise ValueError(f"{name}: rows overlap (pitch {pitch} < {heads * d})")
+    return x.data_ptr(), pitch
+
+
+def mp_rope_axes(x, y, pos, *, sections, base: float = 10000.0, interleaved: bool = False, per_axis: bool = False,
+                 inverse: bool = False, stream=None) -> None:
+    """Rotary positions with up to four axes: y = x with each head's pairs rotated by pos[axis] * frequency.
+    x, y [T, heads, d] (rows may be strided; y may be x), pos [axes, T] int32, sections: pairs of each axis.
+    inverse rotates back (the gradient)."""
+    T, heads, d = x.shape
+    px, ldx = _heads_view(x, "x")
+    py, ldy = _heads_view(y, "y", shape=(T, heads, d))
+    sec = [int(v) for v in sections]
+    flags = (1 if interleaved else 0) | (2 if per_axis else 0) | (4 if inverse else 0)
+    code = lib().mp_rope_axes(px, py, _ptr(pos, "pos", dtype=torch.int32, shape=(len(sec), T)), T, heads, d, ldx, ldy,
+                              len(sec), (_I * max(len(sec), 1))(*sec), float(base), flags, _stream(stream))
+    _check("mp_rope_axes", code)
 
 
 def mp_status_from_device(bits: int) -> int:

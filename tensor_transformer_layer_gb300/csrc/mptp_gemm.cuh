@@ -74,6 +74,15 @@ enum EpiKind : int {
     EPI_DZ = 4,     // o0 = bf16(dloss * (exp(acc - lse) - [col == target])), 0 on padding columns
     EPI_ACC = 5,    // fp32 accumulation across launches into `acc` (tensor map o1); the last launch
                     // stores bf16 o0
+    EPI_GLU = 6,    // tile = BN/2 gate columns | the same BN/2 up columns: o0 = bf16(act(gate) up);
+                    // o1, o2 (when has_out1) = bf16 gate, up
+    EPI_DGLU = 7,   // acc = dY: o0 = bf16(dY up act'(gate)), o1 = bf16(dY act(gate)); aux = bf16 gate, up
+};
+
+// Activation of the gated epilogues.
+enum ActKind : int {
+    ACT_SILU = 0,  // g / (1 + e^-g)
+    ACT_GELU = 1,  // g Phi(g)
 };
 
 enum AccMode : int {
@@ -100,7 +109,9 @@ struct GemmArgs {
     // epilogue operands that are not written through tensor maps
     const __nv_bfloat16* aux; // U for GeLU'
     long long ld_aux;
-    int has_out1;             // GeLU: also store U (tensor map o1)
+    int has_out1;             // GeLU: also store U (tensor map o1); gated: also gate and up (o1, o2)
+    int act;                  // gated epilogues: ActKind
+    int glu_f;                // gated epilogues: columns from a gate column to its up column
     // cross-entropy epilogues
     const int32_t* target;
     float* ws;                // [P][3][M] fp32: max, sum-exp, target logit
@@ -122,6 +133,7 @@ struct TmapSet {
     CUtensorMap b;
     CUtensorMap o0;
     CUtensorMap o1;
+    CUtensorMap o2;
 };
 
 constexpr size_t SMEM_LIMIT = 232448;  // opt-in shared memory per block on sm_103
@@ -151,6 +163,7 @@ struct GemmCfg {
     static_assert(NE == 4 || NE == 8, "4 or 8 epilogue warps");
     static_assert(EPI != EPI_CE || NE == 4, "cross-entropy epilogue keeps one thread per row");
     static_assert(EPI != EPI_ACC || NE == 4, "accumulating epilogue uses four warps");
+    static_assert(EPI != EPI_GLU || BN == 256, "gated tiles: 128 gate and 128 up columns");
 };
 
 struct Ctl {
@@ -254,6 +267,34 @@ __device__ __forceinline__ float2 gelu_prime2(float2 u) {
     const NormalCdfPdf2 t = normal_tail2(u);
     const float2 cdf = make_float2(u.x >= 0.0f ? 1.0f + t.nq.x : -t.nq.x, u.y >= 0.0f ? 1.0f + t.nq.y : -t.nq.y);
     return fma2(u, mul2(t.e, make_float2(INV_SQRT_2PI, INV_SQRT_2PI)), cdf);
+}
+
+// Activation of the gate and its derivative, two values at a time, from one exponential.
+//   SiLU: s = 1 / (1 + e^-g);  act = g s,  act' = s (1 + g (1 - s))
+//   GeLU: act = max(g, 0) - |g| q,  act' = Phi(g) + g phi(g)  (normal_tail2)
+__device__ __forceinline__ float2 silu_sigmoid2(float2 g) {
+    constexpr float NEG_LOG2E = -1.4426950408889634f;
+    const float2 w = mul2(g, make_float2(NEG_LOG2E, NEG_LOG2E));
+    return make_float2(rcp_approx(1.0f + ex2_approx(w.x)), rcp_approx(1.0f + ex2_approx(w.y)));
+}
+__device__ __forceinline__ float2 glu_act2(float2 g, int act) {
+    if (act == ACT_SILU) return mul2(g, silu_sigmoid2(g));
+    return gelu2(g);
+}
+__device__ __forceinline__ void glu_act_grad2(float2 g, int act, float2& a, float2& da) {
+    if (act == ACT_SILU) {
+        const float2 s = silu_sigmoid2(g);
+        a = mul2(g, s);
+        // s + (g s) (1 - s)
+        da = fma2(a, make_float2(1.0f - s.x, 1.0f - s.y), s);
+    } else {
+        constexpr float INV_SQRT_2PI = 0.39894228040143268f;
+        const NormalCdfPdf2 t = normal_tail2(g);
+        a = fma2(t.a, t.nq, make_float2(fmaxf(g.x, 0.0f), fmaxf(g.y, 0.0f)));
+        const float2 cdf =
+            make_float2(g.x >= 0.0f ? 1.0f + t.nq.x : -t.nq.x, g.y >= 0.0f ? 1.0f + t.nq.y : -t.nq.y);
+        da = fma2(g, mul2(t.e, make_float2(INV_SQRT_2PI, INV_SQRT_2PI)), cdf);
+    }
 }
 
 // One warp writes its 32 rows x 32 columns of bf16 (thread = row) into one of its
@@ -360,8 +401,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<BN, EPI, NE>
         prefetch_tensormap(&maps.a);
         prefetch_tensormap(&maps.b);
         if (EPI != EPI_CE) prefetch_tensormap(&maps.o0);
-        if ((EPI == EPI_GELU && args.has_out1) || (EPI == EPI_ACC && args.acc_mode <= ACC_MID))
+        if (((EPI == EPI_GELU || EPI == EPI_GLU) && args.has_out1) || EPI == EPI_DGLU ||
+            (EPI == EPI_ACC && args.acc_mode <= ACC_MID))
             prefetch_tensormap(&maps.o1);
+        if (EPI == EPI_GLU && args.has_out1) prefetch_tensormap(&maps.o2);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
@@ -393,7 +436,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<BN, EPI, NE>
                 const int n_blk0 = ucol * args.tiles_per_unit;
                 const int arow = m_blk * 2 * BM + static_cast<int>(rank) * BM;  // this CTA's A rows
                 for (int nt = 0; nt < args.tiles_per_unit && ok; ++nt) {
-                    const int bcol = (n_blk0 + nt) * BN + static_cast<int>(rank) * BNH;  // this CTA's B columns
+                    // This CTA's B columns: its half of the tile; gated, the gate columns in the
+                    // leader and the up columns of the same outputs in its peer.
+                    const int bcol = EPI == EPI_GLU ? (n_blk0 + nt) * BNH + static_cast<int>(rank) * args.glu_f
+                                                    : (n_blk0 + nt) * BN + static_cast<int>(rank) * BNH;
                     for (int kb = p.kb_begin; kb < p.kb_end; ++kb) {
                         if (!wait_bounded(&empty_bar[stage], phase ^ 1u, ctl)) {
                             ok = false;
@@ -542,7 +588,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<BN, EPI, NE>
                 const int n_blk = n_blk0 + nt;
                 // Chunk pipeline: the TMEM load (and, for GeLU', the U row segment) of
                 // chunk cc+1 is in flight while chunk cc is computed and stored.
-                auto issue = [&](int cc, uint32_t (&rr)[32], uint32_t (&uu)[16]) {
+                constexpr int NAUX = EPI == EPI_DGLU ? 32 : 16;
+                auto issue = [&](int cc, uint32_t (&rr)[32], uint32_t (&uu)[NAUX]) {
                     const int c = c_begin + cc;
                     if constexpr (EPI == EPI_DGELU) {
                         const int col0 = n_blk * BN + c * 32;
@@ -561,9 +608,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<BN, EPI, NE>
                             for (int j = 0; j < 16; ++j) uu[j] = 0u;
                         }
                     }
+                    if constexpr (EPI == EPI_DGLU) {
+                        const int col0 = n_blk * BN + c * 32;
+                        if (row_ok && col0 < p.N) {
+                            const __nv_bfloat16* at = args.aux + row * args.ld_aux + col0;
+                            const uint4* gs = reinterpret_cast<const uint4*>(at);
+                            const uint4* us = reinterpret_cast<const uint4*>(at + args.glu_f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint4 w = gs[j], v = us[j];
+                                uu[4 * j + 0] = w.x;
+                                uu[4 * j + 1] = w.y;
+                                uu[4 * j + 2] = w.z;
+                                uu[4 * j + 3] = w.w;
+                                uu[16 + 4 * j + 0] = v.x;
+                                uu[16 + 4 * j + 1] = v.y;
+                                uu[16 + 4 * j + 2] = v.z;
+                                uu[16 + 4 * j + 3] = v.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) uu[j] = 0u;
+                        }
+                    }
                     tmem_ld32(tmem_base + lane_addr + buf * BN + c * 32, rr);
                 };
-                auto finish = [&](int cc, const uint32_t (&r)[32], const uint32_t (&uw)[16]) {
+                auto finish = [&](int cc, const uint32_t (&r)[32], const uint32_t (&uw)[NAUX]) {
                     const int c = c_begin + cc;
                     const int col0 = n_blk * BN + c * 32;
                     if (col0 >= p.N) return;  // ragged N tail (whole 32-column chunks)
@@ -597,6 +667,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<BN, EPI, NE>
                             pk[j] = pack_bf16x2(g.x, g.y);
                         }
                         stage_and_store(tmO0, stg, sbuf, lane, pk, col0, row0);
+                    } else if constexpr (EPI == EPI_DGLU) {
+                        uint32_t pg[16], pu[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 dy = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                            float2 a, da;
+                            glu_act_grad2(make_float2(bf16_lo(uw[j]), bf16_hi(uw[j])), args.act, a, da);
+                            const float2 dg =
+                                mul2(mul2(dy, make_float2(bf16_lo(uw[16 + j]), bf16_hi(uw[16 + j]))), da);
+                            const float2 du = mul2(dy, a);
+                            pg[j] = pack_bf16x2(dg.x, dg.y);
+                            pu[j] = pack_bf16x2(du.x, du.y);
+                        }
+                        stage_and_store(tmO0, stg, sbuf, lane, pg, col0, row0);
+                        stage_and_store(&maps.o1, stg, sbuf, lane, pu, col0, row0);
                     } else if constexpr (EPI == EPI_DZ) {
                         // dZ = dloss * (softmax - onehot) on valid columns, 0 on padding.
                         constexpr float LOG2E = 1.4426950408889634f;
@@ -677,7 +762,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<BN, EPI, NE>
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
                 };
-                uint32_t ra[32], rb[32], ua[16], ub[16];
+                if constexpr (EPI == EPI_GLU) {
+                    // Columns [0, BNH) of the accumulator are gates, [BNH, BN) the ups of the same
+                    // outputs: 32 outputs at a time, the next 32 in flight meanwhile.
+                    constexpr int MINE = MY_CHUNKS / 2;
+                    const int c0 = (e >> 2) * MINE;
+                    const uint32_t at = tmem_base + lane_addr + buf * BN + c0 * 32;
+                    auto gated = [&](int cc, const uint32_t (&g)[32], const uint32_t (&up)[32]) {
+                        const int col0 = n_blk * BNH + (c0 + cc) * 32;
+                        if (col0 >= p.N) return;
+                        uint32_t pk[16];
+                        if (args.has_out1) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                pk[j] = pack_bf16x2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
+                            stage_and_store(&maps.o1, stg, sbuf, lane, pk, col0, row0);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                pk[j] = pack_bf16x2(__uint_as_float(up[2 * j]), __uint_as_float(up[2 * j + 1]));
+                            stage_and_store(&maps.o2, stg, sbuf, lane, pk, col0, row0);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 a = glu_act2(
+                                make_float2(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1])), args.act);
+                            const float2 y =
+                                mul2(a, make_float2(__uint_as_float(up[2 * j]), __uint_as_float(up[2 * j + 1])));
+                            pk[j] = pack_bf16x2(y.x, y.y);
+                        }
+                        stage_and_store(tmO0, stg, sbuf, lane, pk, col0, row0);
+                    };
+                    uint32_t ga[32], xa[32], gb[32], xb[32];
+                    tmem_ld32(at, ga);
+                    tmem_ld32(at + BNH, xa);
+#pragma unroll 1
+                    for (int cc = 0; cc < MINE; cc += 2) {
+                        tmem_ld_wait(ga);
+                        reg_fence32(xa);
+                        tmem_ld32(at + (cc + 1) * 32, gb);
+                        tmem_ld32(at + BNH + (cc + 1) * 32, xb);
+                        gated(cc, ga, xa);
+                        tmem_ld_wait(gb);
+                        reg_fence32(xb);
+                        if (cc + 2 < MINE) {
+                            tmem_ld32(at + (cc + 2) * 32, ga);
+                            tmem_ld32(at + BNH + (cc + 2) * 32, xa);
+                        } else {
+                            release();
+                        }
+                        gated(cc + 1, gb, xb);
+                    }
+                    continue;
+                }
+                uint32_t ra[32], rb[32], ua[NAUX], ub[NAUX];
                 issue(0, ra, ua);
 #pragma unroll 1
                 for (int cc = 0; cc < MY_CHUNKS; cc += 2) {

@@ -1,0 +1,150 @@
+// Entry points of the gated feed-forward block: mp_glu_fwd and mp_glu_bwd.
+//
+//   [G | U] = X [Wg | Wu],  Y = act(G) * U,  Z = Y Wd        act: SiLU or the erf GeLU
+//   dY = dZ Wd^T,  dG = dY * U * act'(G),  dU = dY * act(G)
+//   dX = [dG | dU] [Wg | Wu]^T,  dWg = X^T dG,  dWu = X^T dU,  dWd = Y^T dZ
+//
+// The block is split for tensor parallelism as the GeLU block is ("Megatron-LM: Training
+// Multi-Billion Parameter Language Models Using Model Parallelism", section 3.4): shard i owns
+// columns [i f/t, (i+1) f/t) of Wg and of Wu and the same rows of Wd. The shards' partial outputs
+// (the g sum of Z, the f sum of dX) are added inside the K-loop.
+//
+// Forward: both projections, the activation and the product are one launch. A CTA pair's tile is
+// 256 tokens x (128 gate + 128 up columns of the same outputs): the leader loads gate columns and its
+// peer up columns, one tcgen05.mma (M = 256, N = 256) multiplies both, and each epilogue thread finds
+// a token's gate and up values in its own TMEM lane, 128 columns apart, in fp32. So G and U are
+// rounded only where the caller keeps them for the backward pass; Y comes from the fp32 values.
+// Then Z is one row-parallel GEMM over Y.
+// Backward: one GEMM gives dY, whose epilogue reads G and U and writes dG and dU (dY never reaches
+// memory); dX, dW and dWd are three GEMMs, side by side where that is shorter (mptp_mlp_host.cuh).
+#include "mptp_mlp_host.cuh"
+
+using namespace mptp;
+
+namespace {
+
+bool bad_act(int act) { return act != MP_ACT_SILU && act != MP_ACT_GELU; }
+
+}  // namespace
+
+extern "C" mp_status mp_glu_fwd(const mp_bf16* X, const mp_bf16* W, const mp_bf16* Wd, mp_bf16* Z, mp_bf16* Y,
+                                mp_bf16* GU_save, int T, int h, int f, int t, int act, uint32_t* d_status,
+                                void* stream) {
+    mp_status st = check_mlp_shape(T, h, f, t);
+    if (st != MP_OK) return st;
+    if (bad_act(act)) return MP_ERR_INVALID_ARG;
+    if (f > 0x3fffffff) return MP_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MP_OK;
+    if (!X || !W || !Wd || !Z || !Y) return MP_ERR_INVALID_ARG;
+    const void* ptrs[] = {X, W, Wd, Z, Y, GU_save};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return MP_ERR_MISALIGNED;
+    if (d_status && (reinterpret_cast<uintptr_t>(d_status) & 3u)) return MP_ERR_MISALIGNED;
+    int sms = 0;
+    if ((st = check_device(&sms)) != MP_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const double Tb = 2.0 * T, hb = 2.0 * h;
+    const size_t f2 = size_t(2) * f;
+
+    // [G | U] = X W and Y = act(G) * U, tiles of 128 outputs.
+    TmapSet m1{};
+    int b1 = 0;
+    if (!make_tmap_bf16(&m1.a, X, h, T, h, 64, BM) || !(b1 = make_tmap_mn_operand(&m1.b, W, f2, h, f2)) ||
+        !make_tmap_bf16_out(&m1.o0, Y, f, T, f) ||
+        (GU_save && (!make_tmap_bf16_out(&m1.o1, GU_save, f, T, f2) || !make_tmap_bf16_out(&m1.o2, GU_save + f, f, T, f2))))
+        return MP_ERR_CUDA;
+    GemmArgs a1 = launch_args(d_status);
+    a1.pr = problem(T, f, 128, 0, h / BK, false, true, Tb * h, 2 * hb * f);
+    a1.pr.b_mn = b1;
+    a1.has_out1 = GU_save ? 1 : 0;
+    a1.act = act;
+    a1.glu_f = f;
+    if (launch_gelu_epi<EPI_GLU>(m1, a1, sms, s) != cudaSuccess) return MP_ERR_CUDA;
+
+    // Z = sum_i Y_i Wd_i, shards in ascending order in the K-loop (the g sum).
+    TmapSet m2{};
+    int b2 = 0;
+    if (!make_tmap_bf16(&m2.a, Y, f, T, f, 64, BM) || !(b2 = make_tmap_mn_operand(&m2.b, Wd, h, f, h)) ||
+        !make_tmap_bf16_out(&m2.o0, Z, h, T, h))
+        return MP_ERR_CUDA;
+    GemmArgs a2 = launch_args(d_status);
+    a2.pr = problem(T, h, 256, 0, f / BK, false, true, Tb * f, hb * f);
+    a2.pr.b_mn = b2;
+    const bool split2 = use_split<256>(T, h, f / BK, sms);
+    if ((split2 ? launch_gemm_split<256, SPLIT_PAIRS>(m2, a2, sms, s) : launch_gemm_tc<256, EPI_STORE, 4>(m2, a2, sms, s)) !=
+        cudaSuccess)
+        return MP_ERR_CUDA;
+    return MP_OK;
+}
+
+extern "C" mp_status mp_glu_bwd(const mp_bf16* X, const mp_bf16* W, const mp_bf16* Wd, const mp_bf16* GU,
+                                const mp_bf16* Y, const mp_bf16* dZ, mp_bf16* dX, mp_bf16* dW, mp_bf16* dWd,
+                                mp_bf16* dGU_ws, int T, int h, int f, int t, int act, uint32_t* d_status,
+                                void* stream) {
+    mp_status st = check_mlp_shape(T, h, f, t);
+    if (st != MP_OK) return st;
+    if (bad_act(act)) return MP_ERR_INVALID_ARG;
+    if (f > 0x3fffffff) return MP_ERR_UNSUPPORTED_SHAPE;
+    if (!W || !Wd || !dW || !dWd) return MP_ERR_INVALID_ARG;
+    if (T > 0 && (!X || !GU || !Y || !dZ || !dX || !dGU_ws)) return MP_ERR_INVALID_ARG;
+    const void* ptrs[] = {X, W, Wd, GU, Y, dZ, dX, dW, dWd, dGU_ws};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return MP_ERR_MISALIGNED;
+    if (d_status && (reinterpret_cast<uintptr_t>(d_status) & 3u)) return MP_ERR_MISALIGNED;
+    int sms = 0;
+    if ((st = check_device(&sms)) != MP_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t f2 = size_t(2) * f;
+    if (T == 0) {
+        // Empty batch: the weight gradients are sums over zero tokens.
+        if (cudaMemsetAsync(dW, 0, size_t(h) * f2 * 2, s) != cudaSuccess ||
+            cudaMemsetAsync(dWd, 0, size_t(f) * h * 2, s) != cudaSuccess)
+            return MP_ERR_CUDA;
+        return MP_OK;
+    }
+    const double Tb = 2.0 * T, hb = 2.0 * h;
+
+    // dY = dZ Wd^T; dG, dU in its epilogue.
+    TmapSet m3{};
+    if (!make_tmap_bf16(&m3.a, dZ, h, T, h, 64, BM) || !make_tmap_bf16(&m3.b, Wd, h, f, h, 64, 128) ||
+        !make_tmap_bf16_out(&m3.o0, dGU_ws, f, T, f2) || !make_tmap_bf16_out(&m3.o1, dGU_ws + f, f, T, f2))
+        return MP_ERR_CUDA;
+    GemmArgs a3 = launch_args(d_status);
+    a3.pr = problem(T, f, 256, 0, h / BK, false, false, Tb * h, 2.0 * f * h);
+    a3.aux = reinterpret_cast<const __nv_bfloat16*>(GU);
+    a3.ld_aux = static_cast<long long>(f2);
+    a3.act = act;
+    a3.glu_f = f;
+    if (launch_gelu_epi<EPI_DGLU>(m3, a3, sms, s) != cudaSuccess) return MP_ERR_CUDA;
+
+    // dX = dGU W^T: gate blocks, then up blocks, shards ascending in each (the f sum).
+    TmapSet m4{};
+    if (!make_tmap_bf16(&m4.a, dGU_ws, f2, T, f2, 64, BM) || !make_tmap_bf16(&m4.b, W, f2, h, f2, 64, K4_BN / 2) ||
+        !make_tmap_bf16_out(&m4.o0, dX, h, T, h))
+        return MP_ERR_CUDA;
+    GemmArgs a4 = launch_args(d_status);
+    a4.pr = problem(T, h, K4_BN, 0, 2 * (f / BK), false, false, 2 * Tb * f, 2 * hb * f);
+
+    // dW = X^T dGU (both operands MN-major).
+    TmapSet m5{};
+    int a5f = 0, b5f = 0;
+    if (!(a5f = make_tmap_mn_operand(&m5.a, X, h, T, h)) || !(b5f = make_tmap_mn_operand(&m5.b, dGU_ws, f2, T, f2)) ||
+        !make_tmap_bf16_out(&m5.o0, dW, f2, h, f2))
+        return MP_ERR_CUDA;
+    GemmArgs a5 = launch_args(d_status);
+    a5.pr = problem(h, 2 * f, 256, 0, ceil_div(T, BK), true, true, Tb * h, 2 * Tb * f);
+    a5.pr.a_mn = a5f;
+    a5.pr.b_mn = b5f;
+
+    // dWd = Y^T dZ (both operands MN-major).
+    TmapSet m6{};
+    int a6f = 0, b6f = 0;
+    if (!(a6f = make_tmap_mn_operand(&m6.a, Y, f, T, f)) || !(b6f = make_tmap_mn_operand(&m6.b, dZ, h, T, h)) ||
+        !make_tmap_bf16_out(&m6.o0, dWd, h, f, h))
+        return MP_ERR_CUDA;
+    GemmArgs a6 = launch_args(d_status);
+    a6.pr = problem(f, h, 256, 0, ceil_div(T, BK), true, true, Tb * f, Tb * h);
+    a6.pr.a_mn = a6f;
+    a6.pr.b_mn = b6f;
+    return launch_grad_gemms(m4, a4, W, static_cast<int>(f2), m5, a5, m6, a6, sms, s);
+}
