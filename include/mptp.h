@@ -71,7 +71,8 @@ typedef enum mp_status {
     MP_ERR_CUDA = 5,              /* a CUDA runtime/driver call failed */
     MP_ERR_TIMEOUT = 6,           /* device bit MP_DEV_TIMEOUT was found (see mp_status_from_device) */
     MP_ERR_TARGET_RANGE = 7,      /* device bit MP_DEV_TARGET_RANGE was found */
-    MP_ERR_WORKSPACE = 8          /* workspace too small */
+    MP_ERR_WORKSPACE = 8,         /* workspace too small */
+    MP_ERR_SEQ_RANGE = 9          /* device bit MP_DEV_SEQ_RANGE was found */
 } mp_status;
 
 typedef uint16_t mp_bf16; /* raw bfloat16 bits */
@@ -79,6 +80,7 @@ typedef uint16_t mp_bf16; /* raw bfloat16 bits */
 /* Bits OR-ed into *d_status by the kernels. */
 #define MP_DEV_TIMEOUT 0x1u
 #define MP_DEV_TARGET_RANGE 0x2u
+#define MP_DEV_SEQ_RANGE 0x4u
 
 /*
  * Forward of the sharded MLP block.
@@ -412,6 +414,50 @@ MP_API mp_status mp_rope_axes(const mp_bf16* x, mp_bf16* y, const int32_t* pos,
                        int T, int heads, int d, long long ldx, long long ldy,
                        int axes, const int* sections, double base, uint32_t flags,
                        void* stream);
+
+/*
+ * Attention over packed sequences, forward: sequence i owns query rows [cu_q[i], cu_q[i+1]) and key
+ * rows [cu_k[i], cu_k[i+1]); query head j reads key head j / (heads / kv_heads).
+ *   S = scale Q K^T,  LSE = log sum_k exp S,  O = exp(S - LSE) V
+ * causal != 0: the last query of a sequence sees its last key, so query i sees keys
+ * 0 .. i + (keys - queries). A row that sees no key gets O = 0 and LSE = -inf. Rows outside every
+ * sequence are not written. Values of other sequences (infinities and NaN included) reach no row.
+ *   Q, O [Tq, heads, d], K, V [Tk, kv_heads, d] bf16: a row's heads are contiguous, rows are ldq, ldo,
+ *   ldk, ldv elements apart (views of a packed projection are fine); LSE [heads, Tq] fp32.
+ *   cu_q, cu_k [nseq + 1] int32 in device memory, ascending, within the tensors; max_q, max_k: at
+ *   least the longest sequence's rows. A sequence that breaks this is left out (its outputs are not
+ *   written) and sets MP_DEV_SEQ_RANGE.
+ *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; max_q <= Tq, max_k <= Tk; pitches at
+ *   least a row and multiples of 8; scale > 0 and finite.
+ */
+MP_API mp_status mp_attn_varlen_fwd(const mp_bf16* Q, const mp_bf16* K, const mp_bf16* V,
+                             mp_bf16* O, float* LSE,
+                             const int32_t* cu_q, const int32_t* cu_k,
+                             int nseq, int Tq, int Tk, int max_q, int max_k,
+                             int heads, int kv_heads, int d,
+                             long long ldq, long long ldk, long long ldv, long long ldo,
+                             int causal, float scale,
+                             uint32_t* d_status, void* stream);
+
+/*
+ * Its backward, from O and LSE of the forward. The probabilities are recomputed tile by tile:
+ *   P = exp(S - LSE),  delta = rowsum(dO * O),  dV = P^T dO,  dP = dO V^T,
+ *   dS = P * (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q
+ * dK and dV of a shared key head are the sums over its query heads. Deterministic: no atomics.
+ *   dO, dQ [Tq, heads, d], dK, dV [Tk, kv_heads, d] with pitches lddo, lddq, lddk, lddv;
+ *   delta_ws [heads, Tq] fp32: workspace (caller-owned); holds delta on return.
+ *   Everything else as mp_attn_varlen_fwd; a row that saw no key gives no gradient and gets dQ = 0.
+ */
+MP_API mp_status mp_attn_varlen_bwd(const mp_bf16* Q, const mp_bf16* K, const mp_bf16* V,
+                             const mp_bf16* O, const float* LSE, const mp_bf16* dO,
+                             mp_bf16* dQ, mp_bf16* dK, mp_bf16* dV, float* delta_ws,
+                             const int32_t* cu_q, const int32_t* cu_k,
+                             int nseq, int Tq, int Tk, int max_q, int max_k,
+                             int heads, int kv_heads, int d,
+                             long long ldq, long long ldk, long long ldv, long long ldo,
+                             long long lddo, long long lddq, long long lddk, long long lddv,
+                             int causal, float scale,
+                             uint32_t* d_status, void* stream);
 
 /*
  * mp_vocab_ce for callers that cannot allocate device memory. The paper has no

@@ -27,10 +27,11 @@ LIB_PATH = os.path.join(_PKG, "_lib", "libmptp.so")
 MP_OK = 0
 MP_DEV_TIMEOUT = 0x1
 MP_DEV_TARGET_RANGE = 0x2
+MP_DEV_SEQ_RANGE = 0x4
 STATUS_NAMES = {
     0: "MP_OK", 1: "MP_ERR_INVALID_ARG", 2: "MP_ERR_UNSUPPORTED_SHAPE", 3: "MP_ERR_MISALIGNED",
     4: "MP_ERR_NO_DEVICE", 5: "MP_ERR_CUDA", 6: "MP_ERR_TIMEOUT", 7: "MP_ERR_TARGET_RANGE",
-    8: "MP_ERR_WORKSPACE",
+    8: "MP_ERR_WORKSPACE", 9: "MP_ERR_SEQ_RANGE",
 }
 # Every symbol include/mptp.h declares.
 EXPORTS = ("mp_mlp_fwd", "mp_mlp_bwd", "mp_mlp_fwd_shards", "mp_mlp_bwd_shards", "mp_mlp_fused_workspace_bytes",
@@ -38,7 +39,8 @@ EXPORTS = ("mp_mlp_fwd", "mp_mlp_bwd", "mp_mlp_fwd_shards", "mp_mlp_bwd_shards",
            "mp_vocab_ce_combine", "mp_status_string", "mp_status_from_device", "mp_version",
            "mp_vocab_ce_noalloc", "mp_vocab_ce_bwd_workspace_bytes", "mp_vocab_ce_bwd_workspace_bytes_one_pass",
            "mp_vocab_ce_bwd", "mp_vocab_ce_lse", "mp_vocab_ce_bwd_lse", "mp_vocab_embed",
-           "mp_attn_fwd", "mp_glu_fwd", "mp_glu_bwd", "mp_rope_axes")
+           "mp_attn_fwd", "mp_glu_fwd", "mp_glu_bwd", "mp_rope_axes",
+           "mp_attn_varlen_fwd", "mp_attn_varlen_bwd")
 
 
 class MptpError(RuntimeError):
@@ -101,6 +103,11 @@ def lib() -> ctypes.CDLL:
         L.mp_glu_bwd.restype = _I
         L.mp_rope_axes.argtypes = [_P, _P, _P, _I, _I, _I, _L, _L, _I, _P, ctypes.c_double, ctypes.c_uint32, _P]
         L.mp_rope_axes.restype = _I
+        _F = ctypes.c_float
+        L.mp_attn_varlen_fwd.argtypes = [_P] * 7 + [_I] * 8 + [_L] * 4 + [_I, _F, _P, _P]
+        L.mp_attn_varlen_fwd.restype = _I
+        L.mp_attn_varlen_bwd.argtypes = [_P] * 12 + [_I] * 8 + [_L] * 8 + [_I, _F, _P, _P]
+        L.mp_attn_varlen_bwd.restype = _I
         L.mp_vocab_embed.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P]
         L.mp_vocab_embed.restype = _I
         L.mp_vocab_ce_noalloc.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]
@@ -453,6 +460,52 @@ def mp_rope_axes(x, y, pos, *, sections, base: float = 10000.0, interleaved: boo
     code = lib().mp_rope_axes(px, py, _ptr(pos, "pos", dtype=torch.int32, shape=(len(sec), T)), T, heads, d, ldx, ldy,
                               len(sec), (_I * max(len(sec), 1))(*sec), float(base), flags, _stream(stream))
     _check("mp_rope_axes", code)
+
+
+def _packed_shapes(Q, K, cu_q, cu_k):
+    if not isinstance(Q, torch.Tensor) or not isinstance(K, torch.Tensor) or Q.dim() != 3 or K.dim() != 3:
+        raise ValueError("Q and K must be [tokens, heads, d] tensors")
+    if Q.shape[2] != K.shape[2]:
+        raise ValueError(f"Q and K must have the same head width, got {Q.shape[2]} and {K.shape[2]}")
+    nseq = cu_q.shape[0] - 1
+    if nseq < 0:
+        raise ValueError("cu_q must have at least one entry")
+    return (nseq, Q.shape[0], K.shape[0], Q.shape[1], K.shape[1], Q.shape[2],
+            _ptr(cu_q, "cu_q", dtype=torch.int32, shape=(nseq + 1,)),
+            _ptr(cu_k, "cu_k", dtype=torch.int32, shape=(nseq + 1,)))
+
+
+def mp_attn_varlen_fwd(Q, K, V, O, LSE, cu_q, cu_k, *, max_q: int, max_k: int, causal: bool, scale: float | None = None,
+                       d_status=None, stream=None) -> None:
+    """Attention over packed sequences: O [Tq, heads, d] and LSE [heads, Tq] fp32 from Q [Tq, heads, d], K, V
+    [Tk, kv_heads, d] (rows may be strided). cu_q, cu_k [nseq + 1] int32: sequence i owns rows cu[i] .. cu[i+1]-1;
+    max_q, max_k: at least the longest. causal: the last query sees the last key. scale: 1 / sqrt(d) by default."""
+    nseq, Tq, Tk, heads, kv, d, pcq, pck = _packed_shapes(Q, K, cu_q, cu_k)
+    (pq, ldq), (pk, ldk) = _heads_view(Q, "Q"), _heads_view(K, "K")
+    (pv, ldv), (po, ldo) = _heads_view(V, "V", (Tk, kv, d)), _heads_view(O, "O", (Tq, heads, d))
+    code = lib().mp_attn_varlen_fwd(
+        pq, pk, pv, po, _ptr(LSE, "LSE", dtype=torch.float32, shape=(heads, Tq)), pcq, pck, nseq, Tq, Tk, int(max_q),
+        int(max_k), heads, kv, d, ldq, ldk, ldv, ldo, 1 if causal else 0, d ** -0.5 if scale is None else float(scale),
+        _status_ptr(d_status), _stream(stream))
+    _check("mp_attn_varlen_fwd", code)
+
+
+def mp_attn_varlen_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, delta_ws, cu_q, cu_k, *, max_q: int, max_k: int, causal: bool,
+                       scale: float | None = None, d_status=None, stream=None) -> None:
+    """Backward of mp_attn_varlen_fwd from its O and LSE: dQ, dK, dV (rows may be strided, e.g. the parts of a
+    packed projection's gradient); delta_ws [heads, Tq] fp32 workspace."""
+    nseq, Tq, Tk, heads, kv, d, pcq, pck = _packed_shapes(Q, K, cu_q, cu_k)
+    qs, ks = (Tq, heads, d), (Tk, kv, d)
+    (pq, ldq), (pk, ldk), (pv, ldv) = _heads_view(Q, "Q"), _heads_view(K, "K"), _heads_view(V, "V", ks)
+    (po, ldo), (pdo, lddo) = _heads_view(O, "O", qs), _heads_view(dO, "dO", qs)
+    (pdq, lddq), (pdk, lddk), (pdv, lddv) = (_heads_view(dQ, "dQ", qs), _heads_view(dK, "dK", ks),
+                                             _heads_view(dV, "dV", ks))
+    f32 = dict(dtype=torch.float32, shape=(heads, Tq))
+    code = lib().mp_attn_varlen_bwd(
+        pq, pk, pv, po, _ptr(LSE, "LSE", **f32), pdo, pdq, pdk, pdv, _ptr(delta_ws, "delta_ws", **f32), pcq, pck, nseq,
+        Tq, Tk, int(max_q), int(max_k), heads, kv, d, ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv, 1 if causal else 0,
+        d ** -0.5 if scale is None else float(scale), _status_ptr(d_status), _stream(stream))
+    _check("mp_attn_varlen_bwd", code)
 
 
 def mp_status_from_device(bits: int) -> int:

@@ -1,0 +1,194 @@
+// What the kernels of the packed attention (forward, query gradient, key and value gradients) share:
+// the sequences' spans, tile sizes, tile loads, the clearing of rows behind a sequence's end, and the
+// store of a warp's 32 rows.
+//
+// Tiles are 128 rows of D columns, loaded as D/32 boxes of 32 columns with the 64-byte swizzle. The
+// same tile serves as a K-major operand (D is the summed dimension) and as an MN-major one (its rows
+// are summed), so nothing is transposed.
+#pragma once
+
+#include "mptp_gemm.cuh"
+#include "mptp_internal.h"
+
+namespace mptp {
+
+constexpr uint32_t DEV_SEQ_RANGE = 0x4u;
+constexpr int AV_TILE = 128;     // rows per tile
+constexpr int AV_THREADS = 384;  // warpgroup 0: loads, MMA, helpers; 1 and 2: softmax
+
+template <int D>
+struct AvTile {
+    static_assert(D == 64 || D == 96 || D == 128, "head width");
+    static constexpr int NB = D / 32;              // 32-column boxes
+    static constexpr int BOX = AV_TILE * 64;       // bytes of one box
+    static constexpr int BYTES = NB * BOX;         // bytes of one tile
+    // Registers a thread in warpgroup 0 and in the softmax warpgroups (setmaxnreg); the launch gives
+    // 384 x 168.
+    static constexpr int REGS_CTRL = 72;
+    static constexpr int REGS_SOFTMAX = 208;
+    static_assert(128 * REGS_CTRL + 256 * REGS_SOFTMAX <= AV_THREADS * 168, "register split");
+};
+
+struct AvArgs {
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int nseq, Tq, Tk, max_q, max_k;
+    int heads, kv_heads, group;  // group = heads / kv_heads
+    int causal;
+    float scale, scale_log2;     // scale_log2 = scale * log2(e)
+    uint32_t* status;
+    unsigned long long budget_ns;
+};
+
+// Rows of one sequence. A span that is not inside the tensors or longer than the caller's maximum is
+// reported and left out (nothing of it is read or written).
+struct AvSpan {
+    int q0, nq, k0, nk;
+};
+__device__ __forceinline__ bool av_span(const AvArgs& a, int seq, AvSpan& s) {
+    const int q0 = a.cu_q[seq], q1 = a.cu_q[seq + 1], k0 = a.cu_k[seq], k1 = a.cu_k[seq + 1];
+    if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk || q1 - q0 > a.max_q || k1 - k0 > a.max_k) {
+        if (threadIdx.x == 0 && a.status) atomicOr(a.status, DEV_SEQ_RANGE);
+        return false;
+    }
+    s = {q0, q1 - q0, k0, k1 - k0};
+    return true;
+}
+
+// One tile (rows from `row`, D columns from `col`) into shared memory, counted on `bar`.
+template <int D>
+__device__ __forceinline__ void av_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int col, int row) {
+    using C = AvTile<D>;
+    mbar_arrive_expect_tx(bar, C::BYTES);
+#pragma unroll
+    for (int c = 0; c < C::NB; ++c) tma_load_2d(dst + c * C::BOX, map, bar, col + c * 32, row);
+}
+
+// One warp clears rows [from, 128) of a tile in shared memory. A tile that reaches past its sequence
+// holds the next one's rows: their products with zero weights would still carry infinities and NaN.
+template <int D>
+__device__ __forceinline__ void av_clear_rows(uint8_t* tile, int from, int lane) {
+    using C = AvTile<D>;
+    for (int i = from * 4 + lane; i < AV_TILE * 4; i += 32)
+#pragma unroll
+        for (int c = 0; c < C::NB; ++c)
+            *reinterpret_cast<uint4*>(tile + c * C::BOX + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();  // the tensor core reads them through the async proxy
+    __syncwarp();
+}
+
+// Chunks [c0, c1) (32 columns each) of a warp's 32 accumulator rows, times f, as bf16: through shared
+// memory and TMA where all 32 rows belong to the sequence (rows_ok = 32), else row by row. `acc` is the
+// warp's TMEM address, `stg` its 2 KB boxes, one per chunk of the tile.
+__device__ __forceinline__ void av_store_rows(uint32_t acc, float f, int c0, int c1, uint8_t* stg,
+                                              const CUtensorMap* map, int col, int row, __nv_bfloat16* out,
+                                              long long ld, int rows_ok, int lane) {
+    const int sw = (lane >> 1) & 3;
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+        uint32_t o[32];
+        tmem_ld32(acc + c * 32, o);
+        tmem_wait_ld();
+        reg_fence32(o);
+        uint4 w[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            w[v] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * v]) * f, __uint_as_float(o[8 * v + 1]) * f),
+                              pack_bf16x2(__uint_as_float(o[8 * v + 2]) * f, __uint_as_float(o[8 * v + 3]) * f),
+                              pack_bf16x2(__uint_as_float(o[8 * v + 4]) * f, __uint_as_float(o[8 * v + 5]) * f),
+                              pack_bf16x2(__uint_as_float(o[8 * v + 6]) * f, __uint_as_float(o[8 * v + 7]) * f));
+        if (rows_ok >= 32) {
+            uint8_t* r = stg + c * 2048 + lane * 64;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4*>(r + ((v ^ sw) << 4)) = w[v];
+        } else if (lane < rows_ok) {
+            uint4* r = reinterpret_cast<uint4*>(out + static_cast<long long>(row + lane) * ld + col + c * 32);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) r[v] = w[v];
+        }
+    }
+    if (rows_ok >= 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            for (int c = c0; c < c1; ++c) tma_store_2d(map, stg + c * 2048, col + c * 32, row);
+            bulk_commit_group();
+            bulk_wait_group<0>();  // written before the CTA exits
+        }
+        __syncwarp();
+    }
+}
+
+// The same rows as zeros.
+__device__ __forceinline__ void av_store_zero_rows(int c0, int c1, int col, int row, __nv_bfloat16* out, long long ld,
+                                                   int rows_ok, int lane) {
+    if (lane >= rows_ok) return;
+    uint4* r = reinterpret_cast<uint4*>(out + static_cast<long long>(row + lane) * ld + col);
+    for (int i = c0 * 4; i < c1 * 4; ++i) r[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Key tiles that a tile of queries [i0, i0 + 128) of a sequence sees (causal: the last query sees the
+// last key).
+__device__ __forceinline__ int av_key_tiles(const AvSpan& s, int i0, int causal) {
+    if (i0 >= s.nq) return 0;
+    int keys = s.nk;
+    if (causal) {
+        const int last = min(i0 + AV_TILE, s.nq) + (s.nk - s.nq);
+        keys = min(keys, last);
+    }
+    return keys > 0 ? (keys + AV_TILE - 1) / AV_TILE : 0;
+}
+
+// 16-bit A operand of a TMEM product: 16 rows' worth (8 columns) of step k. Each softmax warpgroup
+// writes its 64 columns' values, packed, over the first half of its own 64 fp32 columns.
+__device__ __forceinline__ uint32_t av_a_step(uint32_t base, int k) { return base + (k >> 2) * 64 + (k & 3) * 8; }
+
+inline bool av_tmap(CUtensorMap* m, const void* base, int cols, int rows, long long ld) {
+    return make_tmap_bf16_sw64(m, base, cols, rows, ld, 32, AV_TILE);
+}
+
+// Sizes, pitches and pointers that the forward and the backward refuse alike.
+inline mp_status av_check(int nseq, int Tq, int Tk, int max_q, int max_k, int heads, int kv_heads, int d, float scale) {
+    if (nseq < 0 || Tq < 0 || Tk < 0 || max_q < 0 || max_k < 0 || heads <= 0 || kv_heads <= 0 || d <= 0 ||
+        !(scale > 0.0f) || !(scale <= 3.0e38f))
+        return MP_ERR_INVALID_ARG;
+    if (heads % kv_heads != 0 || (d != 64 && d != 96 && d != 128) || max_q > Tq || max_k > Tk ||
+        static_cast<long long>(heads) * d > 0x3fffffff)
+        return MP_ERR_UNSUPPORTED_SHAPE;
+    // CTAs of the largest launch: one per sequence, head and tile of the longest sequence
+    const long long tiles = (max_q > max_k ? max_q : max_k) / AV_TILE + 1;
+    if (tiles * nseq > 0x7fffffffLL / heads) return MP_ERR_UNSUPPORTED_SHAPE;
+    return MP_OK;
+}
+inline bool av_bad_pitch(long long ld, long long row) { return ld < row || ld % 8 != 0 || ld > (1LL << 36); }
+
+inline AvArgs av_args(const int32_t* cu_q, const int32_t* cu_k, int nseq, int Tq, int Tk, int max_q, int max_k,
+                      int heads, int kv_heads, int causal, float scale, uint32_t* status) {
+    AvArgs a{};
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.nseq = nseq;
+    a.Tq = Tq;
+    a.Tk = Tk;
+    a.max_q = max_q;
+    a.max_k = max_k;
+    a.heads = heads;
+    a.kv_heads = kv_heads;
+    a.group = heads / kv_heads;
+    a.causal = causal;
+    a.scale = scale;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.status = status;
+    a.budget_ns = wait_budget_ns();
+    return a;
+}
+
+template <typename Kern, typename... Args>
+inline cudaError_t av_launch(Kern kern, long long blocks, size_t smem, cudaStream_t s, Args... args) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(AV_THREADS), smem, s, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace mptp

@@ -1,0 +1,790 @@
+// Entry point of the packed attention's backward: mp_attn_varlen_bwd.
+//
+//   P = exp(scale Q K^T - LSE)          recomputed tile by tile, never stored
+//   delta = rowsum(dO * O)
+//   dV = P^T dO,  dP = dO V^T,  dS = P * (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q
+//
+// Two kernels, each with its own recomputation of S and dP: one walks a query tile's keys and keeps
+// dQ in tensor memory, the other walks a key tile's queries and keeps dK and dV there. That is seven
+// products per pair of tiles where five would do, but no gradient is summed across CTAs: no atomics,
+// no fp32 gradient in memory, a fixed order and so the same bits every run. (One kernel with five
+// products would also be bound by shared memory: at D = 128 its dS goes through it once more and 64 KB
+// of fp32 dQ per pair of tiles leave through it, against 64 KB a tile of K or Q loads for each here.)
+//
+// dQ kernel: CTA = (sequence, query head, 128 queries). Per key tile S = Q K^T, dP = dO V^T and
+//   dQ += dS K with dS (bf16) read from tensor memory. S has two buffers, so S(j+1) and dP(j+1) run while
+//   the softmax warps are at tile j. The CTA first computes its rows' delta and leaves it for the
+//   other kernel. Where a single key tile holds all that the rows see, delta is summed as P dP instead,
+//   which is the same without O's rounding to bf16: rows of few keys sit there, whose O is large and whose
+//   dP - delta cancels most (two keys, D = 128: dQ's error 8.0e-3 of its norm from O, 2.6e-3 from P dP).
+// dK, dV kernel: CTA = (sequence, key head, 128 keys), over the queries of every head of the group (so
+//   shared key heads need no sum across CTAs either). Scores are computed transposed, S^T = K Q^T and
+//   dP^T = V dO^T, one key per TMEM lane: P^T and dS^T are then A operands in tensor memory as they
+//   stand, dV += P^T dO and dK += dS^T Q, and dO and Q serve as loaded (MN-major). At D = 128 the four
+//   accumulators take all 512 columns; the products of one half of the softmax (dV, S) run while the
+//   warps are at the other half (dK, dP).
+// In both, a softmax thread has one row and 64 of its 128 columns.
+//
+// P and dS are rounded to bf16 for their products (the tensor core's operand type); the exponent,
+// delta, and every sum are fp32. Hidden pairs are replaced by zero after the arithmetic, and rows of a
+// tile behind the sequence's end are cleared in shared memory where they would be summed over.
+#include <type_traits>
+
+#include "mptp_attn_varlen.cuh"
+
+namespace mptp {
+
+__device__ __forceinline__ void softmax_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// A row's log-sum-exp in exp2 units, +inf (every probability 0) where it saw no key.
+__device__ __forceinline__ float lse_to_log2(float lse) {
+    return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+}
+
+// ------------------------------------------------------------------------------------------------
+// dQ (and delta)
+// ------------------------------------------------------------------------------------------------
+template <int D>
+struct AvDqCfg {
+    using T = AvTile<D>;
+    static constexpr int KST = D == 128 ? 3 : 4;  // a K tile serves S(j) and, later, dQ(j)
+    static constexpr int VST = D == 64 ? 4 : D == 96 ? 3 : 2;
+    static constexpr int NUM_BARS = 2 + 2 * KST + 2 * VST + 2 + 5 + 1;
+    static constexpr size_t SMEM = 1024 + (2 + KST + VST) * size_t(T::BYTES) + 2 * AV_TILE * 4 + 8 * NUM_BARS + 16;
+    static_assert(SMEM <= SMEM_LIMIT, "shared memory per block");
+    static constexpr uint32_t TMEM_COLS = 512;  // S(even), S(odd) at 0, 128; dP at 256; dQ at 384
+};
+
+template <int D>
+__global__ void __launch_bounds__(AV_THREADS, 1)
+    attn_varlen_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                          const __grid_constant__ CUtensorMap tmdQ, const __nv_bfloat16* O, long long ldo,
+                          const __nv_bfloat16* dO, long long lddo, const float* LSE, float* delta, __nv_bfloat16* dQ,
+                          long long lddq, int ntiles, const AvArgs args) {
+    using Cfg = AvDqCfg<D>;
+    using T = AvTile<D>;
+    constexpr int NB = T::NB, KST = Cfg::KST, VST = Cfg::VST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sQ = smem;
+    uint8_t* sdO = sQ + T::BYTES;
+    uint8_t* sK = sdO + T::BYTES;
+    uint8_t* sV = sK + KST * T::BYTES;
+    float* part = reinterpret_cast<float*>(sV + VST * T::BYTES);  // [2][128] halves of delta
+    uint64_t* bars = reinterpret_cast<uint64_t*>(part + 2 * AV_TILE);
+    uint64_t* q_full = bars;
+    uint64_t* do_full = bars + 1;
+    uint64_t* k_full = bars + 2;
+    uint64_t* k_empty = k_full + KST;
+    uint64_t* v_full = k_empty + KST;
+    uint64_t* v_empty = v_full + VST;
+    uint64_t* s_full = v_empty + VST;  // [2]
+    uint64_t* dp_full = s_full + 2;
+    uint64_t* dp_read = dp_full + 1;   // the softmax warps have dP(j) in registers
+    uint64_t* ds_full = dp_read + 1;   // dS(j) is in tensor memory
+    uint64_t* dq_full = ds_full + 1;
+    uint64_t* part_full = dq_full + 1; // both halves of delta from one key tile
+    uint64_t* drain_bar = part_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int per_tile = args.nseq * args.heads;
+    const int qt = ntiles - 1 - static_cast<int>(blockIdx.x) / per_tile;  // longest (causal) first
+    const int rem = static_cast<int>(blockIdx.x) % per_tile;
+    const int seq = rem / args.heads;
+    const int head = rem % args.heads;
+    const int kv_col = head / args.group * D;
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+    AvSpan sp;
+    if (!av_span(args, seq, sp) || qt * AV_TILE >= sp.nq) return;
+    const int i0 = qt * AV_TILE;
+    const int n = av_key_tiles(sp, i0, args.causal);
+    const int k_tail = n * AV_TILE > sp.nk ? sp.nk - (n - 1) * AV_TILE : AV_TILE;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(do_full, 1);
+        for (int i = 0; i < KST; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < VST; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+        }
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        mbar_init(dp_full, 1);
+        mbar_init(dp_read, 8);
+        mbar_init(ds_full, 8);
+        mbar_init(dq_full, 1);
+        mbar_init(part_full, 8);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0u;
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+        if (n > 0) {
+            av_load<D>(sK, &tmK, &k_full[0], kv_col, sp.k0);
+            av_load<D>(sQ, &tmQ, q_full, head * D, sp.q0 + i0);
+            av_load<D>(sV, &tmV, &v_full[0], kv_col, sp.k0);
+            av_load<D>(sdO, &tmdO, do_full, head * D, sp.q0 + i0);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Ctl ctl{args.status, abort_flag, args.budget_ns};
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool got = wait_bounded(bar, parity, ctl);
+        return __all_sync(0xffffffffu, got) != 0;
+    };
+
+    if (warp < 4) {
+        reg_dealloc<T::REGS_CTRL>();
+        if (warp == 0) {
+            if (lane == 0) {
+                // ---------------- TMA producer ----------------
+                bool ok = true;
+                for (int j = 1; j < n && ok; ++j) {
+                    int st = j % KST;
+                    ok = wait_bounded(&k_empty[st], ((j / KST) & 1) ^ 1u, ctl);
+                    if (!ok) break;
+                    av_load<D>(sK + st * T::BYTES, &tmK, &k_full[st], kv_col, sp.k0 + j * AV_TILE);
+                    st = j % VST;
+                    ok = wait_bounded(&v_empty[st], ((j / VST) & 1) ^ 1u, ctl);
+                    if (!ok) break;
+                    av_load<D>(sV + st * T::BYTES, &tmV, &v_full[st], kv_col, sp.k0 + j * AV_TILE);
+                }
+            }
+        } else if (warp == 1) {
+            // ---------------- MMA issuer ----------------
+            constexpr uint32_t IDESC_S = make_idesc_bf16(AV_TILE, AV_TILE, false, false);
+            constexpr uint32_t IDESC_DQ = make_idesc_bf16(AV_TILE, D, false, true);
+            const uint64_t q_desc = make_sdesc_sw64(smem_u32(sQ), 16, 512);
+            const uint64_t do_desc = make_sdesc_sw64(smem_u32(sdO), 16, 512);
+            const uint64_t k_desc = make_sdesc_sw64(smem_u32(sK), 16, 512);
+            const uint64_t kt_desc = make_sdesc_sw64(smem_u32(sK), T::BOX, 512);  // keys summed over
+            const uint64_t v_desc = make_sdesc_sw64(smem_u32(sV), 16, 512);
+            auto score = [&](uint32_t d, uint64_t a, uint64_t b) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 1) * T::BOX + (k & 1) * 32) >> 4;
+                    umma_bf16_elect(d, a + off, b + off, IDESC_S, k > 0 ? 1u : 0u);
+                }
+            };
+            auto k_wait = [&](int j) {
+                if (!wait_all(&k_full[j % KST], (j / KST) & 1)) return false;
+                if (j == n - 1 && k_tail < AV_TILE) av_clear_rows<D>(sK + (j % KST) * T::BYTES, k_tail, lane);
+                return true;
+            };
+            auto s_mma = [&](int j) {
+                score(tmem_base + (j & 1) * 128, q_desc, k_desc + static_cast<uint32_t>(((j % KST) * T::BYTES) >> 4));
+                umma_commit_elect(&s_full[j & 1]);
+            };
+            auto dp_mma = [&](int j) {
+                score(tmem_base + 256, do_desc, v_desc + static_cast<uint32_t>(((j % VST) * T::BYTES) >> 4));
+                umma_commit_elect(dp_full);
+                umma_commit_elect(&v_empty[j % VST]);
+            };
+            bool ok = n > 0 && wait_all(q_full, 0) && k_wait(0);
+            if (ok) {
+                tc_fence_after();
+                s_mma(0);
+                ok = wait_all(do_full, 0) && wait_all(&v_full[0], 0);
+                if (ok) {
+                    tc_fence_after();
+                    dp_mma(0);
+                }
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                if (j + 1 < n) {
+                    // S(j+1) overwrites dS(j-1), whose product was issued before it.
+                    if (!(ok = k_wait(j + 1))) break;
+                    tc_fence_after();
+                    s_mma(j + 1);
+                    if (!(ok = wait_all(&v_full[(j + 1) % VST], ((j + 1) / VST) & 1) && wait_all(dp_read, j & 1))) break;
+                    tc_fence_after();
+                    dp_mma(j + 1);
+                }
+                if (!(ok = wait_all(ds_full, j & 1))) break;
+                tc_fence_after();
+                const uint64_t kd = kt_desc + static_cast<uint32_t>(((j % KST) * T::BYTES) >> 4);
+                const uint32_t acc0 = j > 0 ? 1u : 0u;
+#pragma unroll
+                for (int k = 0; k < AV_TILE / 16; ++k)
+                    umma_bf16_ts_elect(tmem_base + 384, av_a_step(tmem_base + (j & 1) * 128, k), kd + ((k * 1024) >> 4),
+                                       IDESC_DQ, k > 0 ? 1u : acc0);
+                umma_commit_elect(&k_empty[j % KST]);
+            }
+            if (ok) umma_commit_elect(dq_full);
+            umma_commit_elect(drain_bar);
+            wait_drain(drain_bar, 0, args.status);
+        }
+    } else {
+        reg_alloc<T::REGS_SOFTMAX>();
+        // ---------------- softmax: warps 4..7 key columns 0..63, warps 8..11 columns 64..127 ----------------
+        const int hf = (warp - 4) >> 2;
+        const int q = warp & 3;
+        const int w0 = i0 + q * 32;
+        const int qi = w0 + lane;
+        const int rows_ok = min(32, sp.nq - w0);
+        const bool row_ok = lane < rows_ok;
+        const long long row = sp.q0 + qi;
+        // delta: each half of the warps sums half of the row's columns (or, in the loop, of its keys)
+        const bool one_tile = n == 1;
+        float dl = 0.0f;
+        if (!one_tile) {
+            float sum = 0.0f;
+            if (row_ok) {
+                const uint4* po = reinterpret_cast<const uint4*>(O + row * ldo + head * D + hf * (D / 2));
+                const uint4* pd = reinterpret_cast<const uint4*>(dO + row * lddo + head * D + hf * (D / 2));
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint4 a = po[i], b = pd[i];
+                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        sum = fmaf(bf16_lo(aw[k]), bf16_lo(bw[k]), sum);
+                        sum = fmaf(bf16_hi(aw[k]), bf16_hi(bw[k]), sum);
+                    }
+                }
+            }
+            part[hf * AV_TILE + q * 32 + lane] = sum;
+            softmax_warps_sync();  // no warp has left: there was no wait before it
+            dl = part[q * 32 + lane] + part[AV_TILE + q * 32 + lane];
+        }
+        const long long at = static_cast<long long>(head) * args.Tq + row;
+        const float lse2 = row_ok ? lse_to_log2(LSE[at]) : INFINITY;
+        const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+        const uint32_t s_addr = tmem_base + lane_addr + hf * 64;
+        const uint32_t dp_addr = tmem_base + lane_addr + 256 + hf * 64;
+        const int off = sp.nk - sp.nq;
+        const int see = args.causal ? min(sp.nk, qi + off + 1) : sp.nk;
+        const int see_w = args.causal ? min(sp.nk, w0 + off + 1) : sp.nk;
+        const float2 c2v = make_float2(args.scale_log2, args.scale_log2);
+        const float2 nl = make_float2(-lse2, -lse2);
+        bool ok = true;
+        for (int j = 0; j < n && ok; ++j) {
+            const uint32_t s_buf = s_addr + (j & 1) * 128;
+            if (!(ok = wait_all(&s_full[j & 1], (j >> 1) & 1))) break;
+            tc_fence_after();
+            uint32_t p[2][32];
+            tmem_ld32(s_buf, p[0]);
+            tmem_ld32(s_buf + 32, p[1]);
+            tmem_wait_ld();
+            reg_fence32(p[0]);
+            reg_fence32(p[1]);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                uint32_t& a = p[(2 * k) >> 5][(2 * k) & 31];
+                uint32_t& b = p[(2 * k + 1) >> 5][(2 * k + 1) & 31];
+                const float2 x = fma2(make_float2(__uint_as_float(a), __uint_as_float(b)), c2v, nl);
+                a = __float_as_uint(ex2_approx(x.x));
+                b = __float_as_uint(ex2_approx(x.y));
+            }
+            if (!(ok = wait_all(dp_full, j & 1))) break;
+            tc_fence_after();
+            uint32_t t[2][32];
+            tmem_ld32(dp_addr, t[0]);
+            tmem_ld32(dp_addr + 32, t[1]);
+            tmem_wait_ld();
+            reg_fence32(t[0]);
+            reg_fence32(t[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dp_read);
+            uint32_t w[32];
+            const int lim = see - j * AV_TILE - hf * 64;  // visible columns of this thread
+            if (one_tile) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 64; ++k) {
+                    const float v = __uint_as_float(p[k >> 5][k & 31]) * __uint_as_float(t[k >> 5][k & 31]);
+                    sum += k < lim ? v : 0.0f;
+                }
+                part[hf * AV_TILE + q * 32 + lane] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(part_full);
+                if (!(ok = wait_all(part_full, 0))) break;
+                dl = part[q * 32 + lane] + part[AV_TILE + q * 32 + lane];
+            }
+            const float2 nd = make_float2(-dl, -dl);
+            auto grad = [&](auto masked) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float2 pr = make_float2(__uint_as_float(p[(2 * k) >> 5][(2 * k) & 31]),
+                                                  __uint_as_float(p[(2 * k + 1) >> 5][(2 * k + 1) & 31]));
+                    const float2 dp = make_float2(__uint_as_float(t[(2 * k) >> 5][(2 * k) & 31]),
+                                                  __uint_as_float(t[(2 * k + 1) >> 5][(2 * k + 1) & 31]));
+                    float2 ds = mul2(pr, add2(dp, nd));
+                    if (decltype(masked)::value) {
+                        ds.x = 2 * k < lim ? ds.x : 0.0f;
+                        ds.y = 2 * k + 1 < lim ? ds.y : 0.0f;
+                    }
+                    w[k] = pack_bf16x2(ds.x, ds.y);
+                }
+            };
+            if (see_w < j * AV_TILE + hf * 64 + 64)
+                grad(std::true_type{});
+            else
+                grad(std::false_type{});
+            tmem_st32(s_buf, w);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ds_full);
+        }
+        if (ok && row_ok && hf == 0) delta[at] = dl;
+        if (ok && rows_ok > 0) {
+            constexpr int HALF = (NB + 1) / 2;
+            const int c0 = hf ? HALF : 0, c1 = hf ? NB : HALF;
+            const int r0 = sp.q0 + w0;
+            if (n == 0) {
+                av_store_zero_rows(c0, c1, head * D, r0, dQ, lddq, rows_ok, lane);
+            } else if (wait_all(dq_full, 0)) {
+                tc_fence_after();
+                av_store_rows(tmem_base + lane_addr + 384, args.scale, c0, c1, sQ + q * (NB * 2048), &tmdQ, head * D, r0,
+                              dQ, lddq, rows_ok, lane);
+            }
+        }
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        if (threadIdx.x == 0) spin_ns(ABORT_SETTLE_NS);
+        __syncthreads();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// dK, dV
+// ------------------------------------------------------------------------------------------------
+template <int D>
+struct AvDkvCfg {
+    using T = AvTile<D>;
+    static constexpr int QST = D == 128 ? 3 : 4;  // a Q tile serves S(i) and, later, dK(i)
+    static constexpr int OST = D == 64 ? 4 : D == 96 ? 3 : 2;  // dO: dP(i), then dV(i)
+    static constexpr int SST = 2;                 // row statistics
+    static constexpr int NUM_BARS = 1 + 2 * QST + 2 * OST + 2 * SST + 5 + 1;
+    // 512-byte alignment is what the 64-byte swizzle needs; at D = 128 no more fits
+    static constexpr size_t SMEM = 512 + (2 + QST + OST) * size_t(T::BYTES) + SST * 2 * AV_TILE * 4 + 8 * NUM_BARS + 16;
+    static_assert(SMEM <= SMEM_LIMIT, "shared memory per block");
+    static constexpr uint32_t TMEM_COLS = 512;  // S^T at 0, dP^T at 128, dV at 256, dK at 384
+};
+
+template <int D>
+__global__ void __launch_bounds__(AV_THREADS, 1)
+    attn_varlen_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                           const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
+                           const float* LSE, const float* delta, __nv_bfloat16* dK, long long lddk, __nv_bfloat16* dV,
+                           long long lddv, const AvArgs args) {
+    using Cfg = AvDkvCfg<D>;
+    using T = AvTile<D>;
+    constexpr int NB = T::NB, QST = Cfg::QST, OST = Cfg::OST, SST = Cfg::SST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) & ~uintptr_t(511));
+    uint8_t* sK = smem;
+    uint8_t* sV = sK + T::BYTES;
+    uint8_t* sQ = sV + T::BYTES;
+    uint8_t* sdO = sQ + QST * T::BYTES;
+    float* stats = reinterpret_cast<float*>(sdO + OST * T::BYTES);  // [SST][-lse2: 128 | -delta: 128]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(stats + SST * 2 * AV_TILE);
+    uint64_t* kv_full = bars;
+    uint64_t* q_full = bars + 1;
+    uint64_t* q_empty = q_full + QST;
+    uint64_t* do_full = q_empty + QST;
+    uint64_t* do_empty = do_full + OST;
+    uint64_t* st_full = do_empty + OST;
+    uint64_t* st_empty = st_full + SST;
+    uint64_t* s_full = st_empty + SST;
+    uint64_t* dp_full = s_full + 1;
+    uint64_t* p_full = dp_full + 1;
+    uint64_t* ds_full = p_full + 1;
+    uint64_t* fin_full = ds_full + 1;
+    uint64_t* drain_bar = fin_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int per_tile = args.nseq * args.kv_heads;
+    const int kt = static_cast<int>(blockIdx.x) / per_tile;  // the first keys have the most queries (causal)
+    const int rem = static_cast<int>(blockIdx.x) % per_tile;
+    const int seq = rem / args.kv_heads;
+    const int kvh = rem % args.kv_heads;
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+    AvSpan sp;
+    if (!av_span(args, seq, sp) || kt * AV_TILE >= sp.nk) return;
+    const int j0 = kt * AV_TILE;
+    const int off = sp.nk - sp.nq;
+    // query tiles [t0, t1) see some key of this tile
+    const int t1 = (sp.nq + AV_TILE - 1) / AV_TILE;
+    const int t0 = args.causal ? max(0, j0 - off) / AV_TILE : 0;
+    const int per_head = max(0, t1 - t0);
+    const int n = per_head * args.group;
+    const int q_tail = t1 * AV_TILE > sp.nq ? sp.nq - (t1 - 1) * AV_TILE : AV_TILE;
+    // iteration it: head it / per_head of the group, query tile t0 + it % per_head
+    auto col_of = [&](int it) { return (kvh * args.group + it / per_head) * D; };
+    auto row_of = [&](int it) { return (t0 + it % per_head) * AV_TILE; };
+    auto is_tail = [&](int it) { return q_tail < AV_TILE && it % per_head == per_head - 1; };
+
+    if (threadIdx.x == 0) {
+        mbar_init(kv_full, 2);
+        for (int i = 0; i < QST; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+        }
+        for (int i = 0; i < OST; ++i) {
+            mbar_init(&do_full[i], 1);
+            mbar_init(&do_empty[i], 1);
+        }
+        for (int i = 0; i < SST; ++i) {
+            mbar_init(&st_full[i], 1);
+            mbar_init(&st_empty[i], 8);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(p_full, 8);
+        mbar_init(ds_full, 8);
+        mbar_init(fin_full, 1);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0u;
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+        if (n > 0) {
+            av_load<D>(sK, &tmK, kv_full, kvh * D, sp.k0 + j0);
+            av_load<D>(sQ, &tmQ, &q_full[0], col_of(0), sp.q0 + row_of(0));
+            av_load<D>(sV, &tmV, kv_full, kvh * D, sp.k0 + j0);
+            av_load<D>(sdO, &tmdO, &do_full[0], col_of(0), sp.q0 + row_of(0));
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Ctl ctl{args.status, abort_flag, args.budget_ns};
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool got = wait_bounded(bar, parity, ctl);
+        return __all_sync(0xffffffffu, got) != 0;
+    };
+
+    if (warp < 4) {
+        reg_dealloc<T::REGS_CTRL>();
+        if (warp == 0) {
+            if (lane == 0) {
+                // ---------------- TMA producer ----------------
+                bool ok = true;
+                for (int it = 1; it < n && ok; ++it) {
+                    int st = it % QST;
+                    ok = wait_bounded(&q_empty[st], ((it / QST) & 1) ^ 1u, ctl);
+                    if (!ok) break;
+                    av_load<D>(sQ + st * T::BYTES, &tmQ, &q_full[st], col_of(it), sp.q0 + row_of(it));
+                    st = it % OST;
+                    ok = wait_bounded(&do_empty[st], ((it / OST) & 1) ^ 1u, ctl);
+                    if (!ok) break;
+                    av_load<D>(sdO + st * T::BYTES, &tmdO, &do_full[st], col_of(it), sp.q0 + row_of(it));
+                }
+            }
+        } else if (warp == 1) {
+            // ---------------- MMA issuer ----------------
+            constexpr uint32_t IDESC_S = make_idesc_bf16(AV_TILE, AV_TILE, false, false);
+            constexpr uint32_t IDESC_G = make_idesc_bf16(AV_TILE, D, false, true);
+            const uint64_t k_desc = make_sdesc_sw64(smem_u32(sK), 16, 512);
+            const uint64_t v_desc = make_sdesc_sw64(smem_u32(sV), 16, 512);
+            const uint64_t q_desc = make_sdesc_sw64(smem_u32(sQ), 16, 512);
+            const uint64_t qt_desc = make_sdesc_sw64(smem_u32(sQ), T::BOX, 512);  // queries summed over
+            const uint64_t do_desc = make_sdesc_sw64(smem_u32(sdO), 16, 512);
+            const uint64_t dot_desc = make_sdesc_sw64(smem_u32(sdO), T::BOX, 512);
+            auto score = [&](uint32_t d, uint64_t a, uint64_t b) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t o = ((k >> 1) * T::BOX + (k & 1) * 32) >> 4;
+                    umma_bf16_elect(d, a + o, b + o, IDESC_S, k > 0 ? 1u : 0u);
+                }
+            };
+            auto grad = [&](uint32_t d, uint32_t a, uint64_t b, bool first) {
+#pragma unroll
+                for (int k = 0; k < AV_TILE / 16; ++k)
+                    umma_bf16_ts_elect(d, av_a_step(a, k), b + ((k * 1024) >> 4), IDESC_G, k > 0 || !first ? 1u : 0u);
+            };
+            auto q_off = [&](int it) { return static_cast<uint32_t>(((it % QST) * T::BYTES) >> 4); };
+            auto do_off = [&](int it) { return static_cast<uint32_t>(((it % OST) * T::BYTES) >> 4); };
+            auto q_wait = [&](int it) {
+                if (!wait_all(&q_full[it % QST], (it / QST) & 1)) return false;
+                if (is_tail(it)) av_clear_rows<D>(sQ + (it % QST) * T::BYTES, q_tail, lane);
+                return true;
+            };
+            auto do_wait = [&](int it) {
+                if (!wait_all(&do_full[it % OST], (it / OST) & 1)) return false;
+                if (is_tail(it)) av_clear_rows<D>(sdO + (it % OST) * T::BYTES, q_tail, lane);
+                return true;
+            };
+            auto s_mma = [&](int it) {
+                score(tmem_base, k_desc, q_desc + q_off(it));
+                umma_commit_elect(s_full);
+            };
+            auto dp_mma = [&](int it) {
+                score(tmem_base + 128, v_desc, do_desc + do_off(it));
+                umma_commit_elect(dp_full);
+            };
+            bool ok = n > 0 && wait_all(kv_full, 0) && q_wait(0);
+            if (ok) {
+                tc_fence_after();
+                s_mma(0);
+                if ((ok = do_wait(0))) {
+                    tc_fence_after();
+                    dp_mma(0);
+                }
+            }
+            for (int it = 0; it < n && ok; ++it) {
+                if (!(ok = wait_all(p_full, it & 1))) break;
+                tc_fence_after();
+                grad(tmem_base + 256, tmem_base, dot_desc + do_off(it), it == 0);  // dV += P^T dO
+                umma_commit_elect(&do_empty[it % OST]);
+                if (it + 1 < n) {
+                    // S^T(i+1) overwrites P^T(i), whose product was issued before it.
+                    if (!(ok = q_wait(it + 1))) break;
+                    tc_fence_after();
+                    s_mma(it + 1);
+                }
+                if (!(ok = wait_all(ds_full, it & 1))) break;
+                tc_fence_after();
+                grad(tmem_base + 384, tmem_base + 128, qt_desc + q_off(it), it == 0);  // dK += dS^T Q
+                umma_commit_elect(&q_empty[it % QST]);
+                if (it + 1 < n) {
+                    if (!(ok = do_wait(it + 1))) break;
+                    tc_fence_after();
+                    dp_mma(it + 1);
+                }
+            }
+            if (ok) umma_commit_elect(fin_full);
+            umma_commit_elect(drain_bar);
+            wait_drain(drain_bar, 0, args.status);
+        } else if (warp == 2) {
+            // ---------------- row statistics of each query tile ----------------
+            for (int it = 0; it < n; ++it) {
+                const int st = it % SST;
+                if (!wait_all(&st_empty[st], ((it / SST) & 1) ^ 1u)) break;
+                const int i0 = row_of(it);
+                const long long at = static_cast<long long>(kvh * args.group + it / per_head) * args.Tq + sp.q0 + i0;
+                float* s = stats + st * 2 * AV_TILE;
+#pragma unroll
+                for (int r = lane; r < AV_TILE; r += 32) {
+                    const bool row_ok = i0 + r < sp.nq;
+                    s[r] = row_ok ? -lse_to_log2(LSE[at + r]) : -INFINITY;
+                    s[AV_TILE + r] = row_ok ? -delta[at + r] : 0.0f;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&st_full[st]);
+            }
+        }
+    } else {
+        reg_alloc<T::REGS_SOFTMAX>();
+        // ---------------- softmax: warps 4..7 query columns 0..63, warps 8..11 columns 64..127 ----------------
+        const int hf = (warp - 4) >> 2;
+        const int q = warp & 3;
+        const int w0 = j0 + q * 32;   // first key of this warp, in its sequence
+        const int rows_ok = min(32, sp.nk - w0);
+        const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+        const uint32_t s_addr = tmem_base + lane_addr + hf * 64;
+        const uint32_t dp_addr = s_addr + 128;
+        const float2 c2v = make_float2(args.scale_log2, args.scale_log2);
+        bool ok = true;
+        for (int it = 0; it < n && ok; ++it) {
+            const int st = it % SST;
+            const float* nl = stats + st * 2 * AV_TILE + hf * 64;
+            const float* nd = nl + AV_TILE;
+            if (!(ok = wait_all(&st_full[st], (it / SST) & 1) && wait_all(s_full, it & 1))) break;
+            tc_fence_after();
+            uint32_t p[2][32], w[32];
+            tmem_ld32(s_addr, p[0]);
+            tmem_ld32(s_addr + 32, p[1]);
+            tmem_wait_ld();
+            reg_fence32(p[0]);
+            reg_fence32(p[1]);
+            // causal: this key is visible from column lo on; lo_w, the most, is the warp's last key's
+            const int lo_w = args.causal ? w0 + 31 - off - row_of(it) - hf * 64 : 0;
+            const int lo = lo_w - 31 + lane;
+            auto prob = [&](auto masked) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    const float4 l4 = *reinterpret_cast<const float4*>(nl + 2 * k);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t& a = p[(2 * (k + e)) >> 5][(2 * (k + e)) & 31];
+                        uint32_t& b = p[(2 * (k + e) + 1) >> 5][(2 * (k + e) + 1) & 31];
+                        const float2 x = fma2(make_float2(__uint_as_float(a), __uint_as_float(b)), c2v,
+                                              e ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+                        float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        if (decltype(masked)::value) {
+                            pr.x = 2 * (k + e) >= lo ? pr.x : 0.0f;
+                            pr.y = 2 * (k + e) + 1 >= lo ? pr.y : 0.0f;
+                        }
+                        a = __float_as_uint(pr.x);
+                        b = __float_as_uint(pr.y);
+                        w[k + e] = pack_bf16x2(pr.x, pr.y);
+                    }
+                }
+            };
+            if (args.causal && lo_w > 0)
+                prob(std::true_type{});
+            else
+                prob(std::false_type{});
+            tmem_st32(s_addr, w);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full);
+            if (!(ok = wait_all(dp_full, it & 1))) break;
+            tc_fence_after();
+            uint32_t t[2][32];
+            tmem_ld32(dp_addr, t[0]);
+            tmem_ld32(dp_addr + 32, t[1]);
+            tmem_wait_ld();
+            reg_fence32(t[0]);
+            reg_fence32(t[1]);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+                const float4 d4 = *reinterpret_cast<const float4*>(nd + 2 * k);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = 2 * (k + e);
+                    const float2 dp = make_float2(__uint_as_float(t[c >> 5][c & 31]), __uint_as_float(t[c >> 5][(c & 31) + 1]));
+                    const float2 pr = make_float2(__uint_as_float(p[c >> 5][c & 31]), __uint_as_float(p[c >> 5][(c & 31) + 1]));
+                    const float2 ds = mul2(pr, add2(dp, e ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y)));
+                    w[k + e] = pack_bf16x2(ds.x, ds.y);
+                }
+            }
+            tmem_st32(dp_addr, w);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&st_empty[st]);
+                mbar_arrive(ds_full);
+            }
+        }
+        if (ok && rows_ok > 0) {
+            // warps 4..7 write dV, warps 8..11 dK; K's and V's tiles are free for the staging
+            __nv_bfloat16* out = hf ? dK : dV;
+            const long long ld = hf ? lddk : lddv;
+            if (n == 0) {
+                av_store_zero_rows(0, NB, kvh * D, sp.k0 + w0, out, ld, rows_ok, lane);
+            } else if (wait_all(fin_full, 0)) {
+                tc_fence_after();
+                av_store_rows(tmem_base + lane_addr + (hf ? 384 : 256), hf ? args.scale : 1.0f, 0, NB,
+                              (hf ? sK : sV) + q * (NB * 2048), hf ? &tmdK : &tmdV, kvh * D, sp.k0 + w0, out, ld,
+                              rows_ok, lane);
+            }
+        }
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        if (threadIdx.x == 0) spin_ns(ABORT_SETTLE_NS);
+        __syncthreads();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+struct AvBwdMaps {
+    CUtensorMap q, k, v, d_o, dq, dk, dv;
+};
+
+template <int D>
+static cudaError_t launch_bwd(const AvBwdMaps& m, const mp_bf16* O, long long ldo, const mp_bf16* dO, long long lddo,
+                              const float* LSE, float* delta, mp_bf16* dQ, long long lddq, mp_bf16* dK, long long lddk,
+                              mp_bf16* dV, long long lddv, const AvArgs& a, cudaStream_t s) {
+    auto bf = [](auto* p) { return reinterpret_cast<__nv_bfloat16*>(const_cast<mp_bf16*>(p)); };
+    const int qtiles = ceil_div(a.max_q, AV_TILE), ktiles = ceil_div(a.max_k, AV_TILE);
+    cudaError_t e = cudaSuccess;
+    if (qtiles > 0)
+        e = av_launch(attn_varlen_dq_kernel<D>, static_cast<long long>(qtiles) * a.nseq * a.heads, AvDqCfg<D>::SMEM, s, m.q,
+                      m.k, m.v, m.d_o, m.dq, static_cast<const __nv_bfloat16*>(bf(O)), ldo,
+                      static_cast<const __nv_bfloat16*>(bf(dO)), lddo, LSE, delta, bf(dQ), lddq, qtiles, a);
+    if (e == cudaSuccess && ktiles > 0)
+        e = av_launch(attn_varlen_dkv_kernel<D>, static_cast<long long>(ktiles) * a.nseq * a.kv_heads, AvDkvCfg<D>::SMEM, s,
+                      m.q, m.k, m.v, m.d_o, m.dk, m.dv, LSE, static_cast<const float*>(delta), bf(dK), lddk, bf(dV),
+                      lddv, a);
+    return e;
+}
+
+}  // namespace mptp
+
+using namespace mptp;
+
+extern "C" mp_status mp_attn_varlen_bwd(const mp_bf16* Q, const mp_bf16* K, const mp_bf16* V, const mp_bf16* O,
+                                        const float* LSE, const mp_bf16* dO, mp_bf16* dQ, mp_bf16* dK, mp_bf16* dV,
+                                        float* delta_ws, const int32_t* cu_q, const int32_t* cu_k, int nseq, int Tq,
+                                        int Tk, int max_q, int max_k, int heads, int kv_heads, int d, long long ldq,
+                                        long long ldk, long long ldv, long long ldo, long long lddo, long long lddq,
+                                        long long lddk, long long lddv, int causal, float scale, uint32_t* d_status,
+                                        void* stream) {
+    mp_status st = av_check(nseq, Tq, Tk, max_q, max_k, heads, kv_heads, d, scale);
+    if (st != MP_OK) return st;
+    const long long qw = static_cast<long long>(heads) * d, kw = static_cast<long long>(kv_heads) * d;
+    if (av_bad_pitch(ldq, qw) || av_bad_pitch(ldo, qw) || av_bad_pitch(lddo, qw) || av_bad_pitch(lddq, qw) ||
+        av_bad_pitch(ldk, kw) || av_bad_pitch(ldv, kw) || av_bad_pitch(lddk, kw) || av_bad_pitch(lddv, kw))
+        return MP_ERR_UNSUPPORTED_SHAPE;
+    if (nseq == 0 || (max_q == 0 && max_k == 0)) return MP_OK;
+    if (!cu_q || !cu_k || (Tq > 0 && (!Q || !O || !LSE || !dO || !dQ || !delta_ws)) || (Tk > 0 && (!K || !V || !dK || !dV)))
+        return MP_ERR_INVALID_ARG;
+    const void* ptrs[] = {Q, K, V, O, dO, dQ, dK, dV};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return MP_ERR_MISALIGNED;
+    const void* words[] = {LSE, delta_ws, cu_q, cu_k, d_status};
+    for (const void* p : words)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return MP_ERR_MISALIGNED;
+    int sms = 0;
+    if ((st = check_device(&sms)) != MP_OK) return st;
+
+    // A side without rows is never loaded or stored: its maps take the other side's tensors.
+    const int qc = static_cast<int>(qw), kc = static_cast<int>(kw);
+    AvBwdMaps m{};
+    bool ok = true;
+    if (Tq > 0)
+        ok = av_tmap(&m.q, Q, qc, Tq, ldq) && av_tmap(&m.d_o, dO, qc, Tq, lddo) && make_tmap_bf16_out(&m.dq, dQ, qc, Tq, lddq);
+    if (ok && Tk > 0)
+        ok = av_tmap(&m.k, K, kc, Tk, ldk) && av_tmap(&m.v, V, kc, Tk, ldv) && make_tmap_bf16_out(&m.dk, dK, kc, Tk, lddk) &&
+             make_tmap_bf16_out(&m.dv, dV, kc, Tk, lddv);
+    if (!ok) return MP_ERR_CUDA;
+    if (Tq == 0) m.q = m.d_o = m.dq = m.k;
+    if (Tk == 0) m.k = m.v = m.dk = m.dv = m.q;
+    const AvArgs a = av_args(cu_q, cu_k, nseq, Tq, Tk, max_q, max_k, heads, kv_heads, causal ? 1 : 0, scale, d_status);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        d == 64   ? launch_bwd<64>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, s)
+        : d == 96 ? launch_bwd<96>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, s)
+                  : launch_bwd<128>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, s);
+    return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
+}

@@ -266,6 +266,7 @@ extern "C" const char* mp_status_string(mp_status s) {
         case MP_ERR_CUDA: return "MP_ERR_CUDA: a CUDA call failed";
         case MP_ERR_TIMEOUT: return "MP_ERR_TIMEOUT: a bounded wait inside a kernel ran out";
         case MP_ERR_TARGET_RANGE: return "MP_ERR_TARGET_RANGE: a target id is outside [0, v_valid)";
+        case MP_ERR_SEQ_RANGE: return "MP_ERR_SEQ_RANGE: a sequence's rows lie outside the tensors or exceed the given maximum";
         case MP_ERR_WORKSPACE: return "MP_ERR_WORKSPACE: workspace smaller than required";
     }
     return "MP_ERR_UNKNOWN";
@@ -274,6 +275,7 @@ extern "C" const char* mp_status_string(mp_status s) {
 extern "C" mp_status mp_status_from_device(uint32_t bits) {
     if (bits & MP_DEV_TIMEOUT) return MP_ERR_TIMEOUT;
     if (bits & MP_DEV_TARGET_RANGE) return MP_ERR_TARGET_RANGE;
+    if (bits & MP_DEV_SEQ_RANGE) return MP_ERR_SEQ_RANGE;
     return MP_OK;
 }
 

@@ -81,3 +81,40 @@ def test_binding_refusals():
 def test_no_device_answer(L):
     assert _glu(L) == 4
     assert _rope(L) == 4
+
+
+def _attn(L, nseq=2, Tq=300, Tk=300, max_q=200, max_k=200, heads=4, kv=2, d=64, ld=None, causal=1, scale=0.125, Q=FAKE,
+          K=FAKE, O=FAKE, LSE=FAKE, cu=FAKE, st=None):
+    ld = ld or {}
+    q, k = heads * d, kv * d
+    lq, lk = ld.get("q", q), ld.get("k", k)
+    fwd = L.mp_attn_varlen_fwd(Q, K, FAKE, O, LSE, cu, FAKE, nseq, Tq, Tk, max_q, max_k, heads, kv, d, lq, lk,
+                               ld.get("v", k), ld.get("o", q), causal, scale, st, None)
+    bwd = L.mp_attn_varlen_bwd(Q, K, FAKE, O, LSE, FAKE, FAKE, FAKE, FAKE, FAKE, cu, FAKE, nseq, Tq, Tk, max_q, max_k,
+                               heads, kv, d, lq, lk, ld.get("v", k), ld.get("o", q), q, q, k, k, causal, scale, st, None)
+    assert fwd == bwd
+    return fwd
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(nseq=-1), 1), (dict(Tq=-1), 1), (dict(Tk=-1), 1), (dict(max_q=-1), 1), (dict(heads=0), 1), (dict(kv=0), 1),
+    (dict(d=0), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1),
+    (dict(d=80), 2), (dict(heads=3), 2), (dict(max_q=301), 2), (dict(max_k=301), 2), (dict(ld={"q": 255}), 2),
+    (dict(ld={"q": 260}), 2), (dict(ld={"k": 120}), 2), (dict(ld={"v": 132}), 2), (dict(ld={"o": 248}), 2),
+    (dict(nseq=2147483647, Tq=2147483647, max_q=2147483647), 2), (dict(heads=1 << 24, kv=1 << 24), 2),
+    (dict(Q=None), 1), (dict(K=None), 1), (dict(O=None), 1), (dict(LSE=None), 1), (dict(cu=None), 1),
+    (dict(Q=BAD), 3), (dict(K=BAD), 3), (dict(O=BAD), 3), (dict(LSE=BAD), 3), (dict(cu=BAD), 3), (dict(st=BAD), 3),
+])
+def test_attn_varlen_refusals(L, kw, code):
+    assert _attn(L, **kw) == code
+
+
+def test_attn_varlen_no_sequences_is_a_noop(L):
+    assert _attn(L, nseq=0, Q=None, cu=None) == 0
+    assert _attn(L, max_q=0, max_k=0, Q=None, cu=None) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device answer")
+def test_attn_varlen_no_device_answer(L):
+    assert _attn(L) == 4
