@@ -21,8 +21,9 @@
 //   shared key heads need no sum across CTAs either). Scores are computed transposed, S^T = K Q^T and
 //   dP^T = V dO^T, one key per TMEM lane: P^T and dS^T are then A operands in tensor memory as they
 //   stand, dV += P^T dO and dK += dS^T Q, and dO and Q serve as loaded (MN-major). At D = 128 the four
-//   accumulators take all 512 columns; the products of one half of the softmax (dV, S) run while the
-//   warps are at the other half (dK, dP).
+//   accumulators take all 512 columns: P^T lies over S^T, so S(i+1) follows dV(i), and the products of one
+//   half of the softmax (dV, S) run while the warps are at the other half (dK, dP). At D <= 96 P^T has
+//   columns of its own, and S(i+1) runs as soon as the warps have S(i) in registers.
 // In both, a softmax thread has one row and 64 of its 128 columns.
 //
 // P and dS are rounded to bf16 for their products (the tensor core's operand type); the exponent,
@@ -382,11 +383,17 @@ struct AvDkvCfg {
     static constexpr int QST = D == 128 ? 3 : 4;  // a Q tile serves S(i) and, later, dK(i)
     static constexpr int OST = D == 64 ? 4 : D == 96 ? 3 : 2;  // dO: dP(i), then dV(i)
     static constexpr int SST = 2;                 // row statistics
-    static constexpr int NUM_BARS = 1 + 2 * QST + 2 * OST + 2 * SST + 5 + 1;
+    static constexpr int NUM_BARS = 1 + 2 * QST + 2 * OST + 2 * SST + 7 + 1;
     // 512-byte alignment is what the 64-byte swizzle needs; at D = 128 no more fits
     static constexpr size_t SMEM = 512 + (2 + QST + OST) * size_t(T::BYTES) + SST * 2 * AV_TILE * 4 + 8 * NUM_BARS + 16;
     static_assert(SMEM <= SMEM_LIMIT, "shared memory per block");
-    static constexpr uint32_t TMEM_COLS = 512;  // S^T at 0, dP^T at 128, dV at 256, dK at 384
+    // S^T at 0, dP^T at 128, dV at 256, dK behind it; P^T over S^T or, where it fits, at 448
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t DK_COL = 256 + D;
+    static constexpr bool OWN_P = D <= 96;
+    // columns from one warpgroup's 16-bit values to the other's (64 of each): packed, or in each half of S^T
+    static constexpr uint32_t P_COL = OWN_P ? 448 : 0;
+    static constexpr uint32_t P_HALF = OWN_P ? 32 : 64;
 };
 
 template <int D>
@@ -419,7 +426,9 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     uint64_t* p_full = dp_full + 1;
     uint64_t* ds_full = p_full + 1;
     uint64_t* fin_full = ds_full + 1;
-    uint64_t* drain_bar = fin_full + 1;
+    uint64_t* s_read = fin_full + 1;   // OWN_P: the softmax warps have S^T(i) in registers
+    uint64_t* dv_done = s_read + 1;    // OWN_P: P^T(i) has been used
+    uint64_t* drain_bar = dv_done + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
@@ -443,10 +452,18 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int per_head = max(0, t1 - t0);
     const int n = per_head * args.group;
     const int q_tail = t1 * AV_TILE > sp.nq ? sp.nq - (t1 - 1) * AV_TILE : AV_TILE;
-    // iteration it: head it / per_head of the group, query tile t0 + it % per_head
-    auto col_of = [&](int it) { return (kvh * args.group + it / per_head) * D; };
-    auto row_of = [&](int it) { return (t0 + it % per_head) * AV_TILE; };
-    auto is_tail = [&](int it) { return q_tail < AV_TILE && it % per_head == per_head - 1; };
+    // Iterations: the group's heads in turn, of each the query tiles t0 .. t1 - 1. Every role walks them
+    // with counters (a division an iteration was a tenth of the loop).
+    struct Walk {
+        int head, tile, t0, t1;
+        __device__ __forceinline__ void next() {
+            if (++tile == t1) {
+                tile = t0;
+                ++head;
+            }
+        }
+    };
+    const Walk first{kvh * args.group, t0, t0, t1};
 
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 2);
@@ -467,15 +484,17 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         mbar_init(p_full, 8);
         mbar_init(ds_full, 8);
         mbar_init(fin_full, 1);
+        mbar_init(s_read, 8);
+        mbar_init(dv_done, 1);
         mbar_init(drain_bar, 1);
         *abort_flag = 0u;
         fence_mbarrier_init();
         fence_proxy_async_smem();
         if (n > 0) {
             av_load<D>(sK, &tmK, kv_full, kvh * D, sp.k0 + j0);
-            av_load<D>(sQ, &tmQ, &q_full[0], col_of(0), sp.q0 + row_of(0));
+            av_load<D>(sQ, &tmQ, &q_full[0], first.head * D, sp.q0 + t0 * AV_TILE);
             av_load<D>(sV, &tmV, kv_full, kvh * D, sp.k0 + j0);
-            av_load<D>(sdO, &tmdO, &do_full[0], col_of(0), sp.q0 + row_of(0));
+            av_load<D>(sdO, &tmdO, &do_full[0], first.head * D, sp.q0 + t0 * AV_TILE);
         }
     }
     if (warp == 1) {
@@ -498,15 +517,17 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             if (lane == 0) {
                 // ---------------- TMA producer ----------------
                 bool ok = true;
+                Walk w = first;
                 for (int it = 1; it < n && ok; ++it) {
+                    w.next();
                     int st = it % QST;
                     ok = wait_bounded(&q_empty[st], ((it / QST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sQ + st * T::BYTES, &tmQ, &q_full[st], col_of(it), sp.q0 + row_of(it));
+                    av_load<D>(sQ + st * T::BYTES, &tmQ, &q_full[st], w.head * D, sp.q0 + w.tile * AV_TILE);
                     st = it % OST;
                     ok = wait_bounded(&do_empty[st], ((it / OST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sdO + st * T::BYTES, &tmdO, &do_full[st], col_of(it), sp.q0 + row_of(it));
+                    av_load<D>(sdO + st * T::BYTES, &tmdO, &do_full[st], w.head * D, sp.q0 + w.tile * AV_TILE);
                 }
             }
         } else if (warp == 1) {
@@ -526,21 +547,22 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     umma_bf16_elect(d, a + o, b + o, IDESC_S, k > 0 ? 1u : 0u);
                 }
             };
-            auto grad = [&](uint32_t d, uint32_t a, uint64_t b, bool first) {
+            auto grad = [&](uint32_t d, uint32_t a, uint32_t half, uint64_t b, bool fresh) {
 #pragma unroll
                 for (int k = 0; k < AV_TILE / 16; ++k)
-                    umma_bf16_ts_elect(d, av_a_step(a, k), b + ((k * 1024) >> 4), IDESC_G, k > 0 || !first ? 1u : 0u);
+                    umma_bf16_ts_elect(d, a + (k >> 2) * half + (k & 3) * 8, b + ((k * 1024) >> 4), IDESC_G,
+                                       k > 0 || !fresh ? 1u : 0u);
             };
             auto q_off = [&](int it) { return static_cast<uint32_t>(((it % QST) * T::BYTES) >> 4); };
             auto do_off = [&](int it) { return static_cast<uint32_t>(((it % OST) * T::BYTES) >> 4); };
-            auto q_wait = [&](int it) {
-                if (!wait_all(&q_full[it % QST], (it / QST) & 1)) return false;
-                if (is_tail(it)) av_clear_rows<D>(sQ + (it % QST) * T::BYTES, q_tail, lane);
-                return true;
-            };
-            auto do_wait = [&](int it) {
-                if (!wait_all(&do_full[it % OST], (it / OST) & 1)) return false;
-                if (is_tail(it)) av_clear_rows<D>(sdO + (it % OST) * T::BYTES, q_tail, lane);
+            Walk ahead = first;  // the iteration whose tiles have been waited for
+            auto tiles_wait = [&](int it) {
+                if (!wait_all(&q_full[it % QST], (it / QST) & 1) || !wait_all(&do_full[it % OST], (it / OST) & 1))
+                    return false;
+                if (q_tail < AV_TILE && ahead.tile == t1 - 1) {
+                    av_clear_rows<D>(sQ + (it % QST) * T::BYTES, q_tail, lane);
+                    av_clear_rows<D>(sdO + (it % OST) * T::BYTES, q_tail, lane);
+                }
                 return true;
             };
             auto s_mma = [&](int it) {
@@ -551,55 +573,73 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 score(tmem_base + 128, v_desc, do_desc + do_off(it));
                 umma_commit_elect(dp_full);
             };
-            bool ok = n > 0 && wait_all(kv_full, 0) && q_wait(0);
+            auto dv_mma = [&](int it) {
+                grad(tmem_base + 256, tmem_base + Cfg::P_COL, Cfg::P_HALF, dot_desc + do_off(it), it == 0);
+                umma_commit_elect(&do_empty[it % OST]);
+                if (Cfg::OWN_P) umma_commit_elect(dv_done);
+            };
+            bool ok = n > 0 && wait_all(kv_full, 0) && tiles_wait(0);
             if (ok) {
                 tc_fence_after();
                 s_mma(0);
-                if ((ok = do_wait(0))) {
-                    tc_fence_after();
-                    dp_mma(0);
-                }
+                dp_mma(0);
             }
             for (int it = 0; it < n && ok; ++it) {
-                if (!(ok = wait_all(p_full, it & 1))) break;
-                tc_fence_after();
-                grad(tmem_base + 256, tmem_base, dot_desc + do_off(it), it == 0);  // dV += P^T dO
-                umma_commit_elect(&do_empty[it % OST]);
-                if (it + 1 < n) {
-                    // S^T(i+1) overwrites P^T(i), whose product was issued before it.
-                    if (!(ok = q_wait(it + 1))) break;
+                // The next tiles are waited for (and a tail cleared) before this iteration's softmax is, so
+                // that nothing lies between the products that follow it.
+                const bool more = it + 1 < n;
+                if (more) {
+                    ahead.next();
+                    if (!(ok = tiles_wait(it + 1))) break;
+                }
+                if (Cfg::OWN_P && more) {
+                    if (!(ok = wait_all(s_read, it & 1))) break;
                     tc_fence_after();
                     s_mma(it + 1);
                 }
+                if (!(ok = wait_all(p_full, it & 1))) break;
+                tc_fence_after();
+                dv_mma(it);                           // dV += P^T dO
+                if (!Cfg::OWN_P && more) s_mma(it + 1);  // over P^T(i), whose product was issued before it
                 if (!(ok = wait_all(ds_full, it & 1))) break;
                 tc_fence_after();
-                grad(tmem_base + 384, tmem_base + 128, qt_desc + q_off(it), it == 0);  // dK += dS^T Q
+                grad(tmem_base + Cfg::DK_COL, tmem_base + 128, 64, qt_desc + q_off(it), it == 0);  // dK += dS^T Q
                 umma_commit_elect(&q_empty[it % QST]);
-                if (it + 1 < n) {
-                    if (!(ok = do_wait(it + 1))) break;
-                    tc_fence_after();
-                    dp_mma(it + 1);
-                }
+                if (more) dp_mma(it + 1);
             }
             if (ok) umma_commit_elect(fin_full);
             umma_commit_elect(drain_bar);
             wait_drain(drain_bar, 0, args.status);
         } else if (warp == 2) {
             // ---------------- row statistics of each query tile ----------------
+            // One iteration's values are in registers before the buffer of the one before last is free.
+            Walk w = first;
+            constexpr int PER = AV_TILE / 32;
+            float l[PER], dd[PER];
+            auto fetch = [&]() {
+                const int i0 = w.tile * AV_TILE + lane;
+                const long long at = static_cast<long long>(w.head) * args.Tq + sp.q0 + i0;
+#pragma unroll
+                for (int r = 0; r < PER; ++r) {
+                    const bool row_ok = i0 + r * 32 < sp.nq;
+                    l[r] = row_ok ? LSE[at + r * 32] : -INFINITY;
+                    dd[r] = row_ok ? delta[at + r * 32] : 0.0f;
+                }
+            };
+            if (n > 0) fetch();
             for (int it = 0; it < n; ++it) {
                 const int st = it % SST;
                 if (!wait_all(&st_empty[st], ((it / SST) & 1) ^ 1u)) break;
-                const int i0 = row_of(it);
-                const long long at = static_cast<long long>(kvh * args.group + it / per_head) * args.Tq + sp.q0 + i0;
-                float* s = stats + st * 2 * AV_TILE;
+                float* s = stats + st * 2 * AV_TILE + lane;
 #pragma unroll
-                for (int r = lane; r < AV_TILE; r += 32) {
-                    const bool row_ok = i0 + r < sp.nq;
-                    s[r] = row_ok ? -lse_to_log2(LSE[at + r]) : -INFINITY;
-                    s[AV_TILE + r] = row_ok ? -delta[at + r] : 0.0f;
+                for (int r = 0; r < PER; ++r) {
+                    s[r * 32] = -lse_to_log2(l[r]);
+                    s[AV_TILE + r * 32] = -dd[r];
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&st_full[st]);
+                w.next();
+                if (it + 1 < n) fetch();
             }
         }
     } else {
@@ -613,6 +653,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         const uint32_t s_addr = tmem_base + lane_addr + hf * 64;
         const uint32_t dp_addr = s_addr + 128;
         const float2 c2v = make_float2(args.scale_log2, args.scale_log2);
+        const uint32_t p_addr = tmem_base + lane_addr + Cfg::P_COL + hf * Cfg::P_HALF;
+        Walk at = first;
         bool ok = true;
         for (int it = 0; it < n && ok; ++it) {
             const int st = it % SST;
@@ -626,8 +668,13 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             tmem_wait_ld();
             reg_fence32(p[0]);
             reg_fence32(p[1]);
+            if (Cfg::OWN_P) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_read);
+            }
             // causal: this key is visible from column lo on; lo_w, the most, is the warp's last key's
-            const int lo_w = args.causal ? w0 + 31 - off - row_of(it) - hf * 64 : 0;
+            const int lo_w = args.causal ? w0 + 31 - off - at.tile * AV_TILE - hf * 64 : 0;
             const int lo = lo_w - 31 + lane;
             auto prob = [&](auto masked) {
 #pragma unroll
@@ -654,7 +701,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 prob(std::true_type{});
             else
                 prob(std::false_type{});
-            tmem_st32(s_addr, w);
+            if (Cfg::OWN_P && it > 0 && !(ok = wait_all(dv_done, (it - 1) & 1))) break;
+            tmem_st32(p_addr, w);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -687,6 +735,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 mbar_arrive(&st_empty[st]);
                 mbar_arrive(ds_full);
             }
+            at.next();
         }
         if (ok && rows_ok > 0) {
             // warps 4..7 write dV, warps 8..11 dK; K's and V's tiles are free for the staging
@@ -696,7 +745,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 av_store_zero_rows(0, NB, kvh * D, sp.k0 + w0, out, ld, rows_ok, lane);
             } else if (wait_all(fin_full, 0)) {
                 tc_fence_after();
-                av_store_rows(tmem_base + lane_addr + (hf ? 384 : 256), hf ? args.scale : 1.0f, 0, NB,
+                av_store_rows(tmem_base + lane_addr + (hf ? Cfg::DK_COL : 256), hf ? args.scale : 1.0f, 0, NB,
                               (hf ? sK : sV) + q * (NB * 2048), hf ? &tmdK : &tmdV, kvh * D, sp.k0 + w0, out, ld,
                               rows_ok, lane);
             }
