@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int kv_col = head / args.group * D;
 
     grid_dependency_wait();
-    grid_launch_dependents();
     AvSpan sp;
     if (!av_span(args, seq, sp) || qt * AV_TILE >= sp.nq) return;
     const int i0 = qt * AV_TILE;
@@ -144,6 +143,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    grid_launch_dependents();  // once this CTA holds its tensor memory: a dependent may want some too
     const Ctl ctl{args.status, abort_flag, args.budget_ns};
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
         const bool got = wait_bounded(bar, parity, ctl);
@@ -441,7 +441,6 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int kvh = rem % args.kv_heads;
 
     grid_dependency_wait();
-    grid_launch_dependents();
     AvSpan sp;
     if (!av_span(args, seq, sp) || kt * AV_TILE >= sp.nk) return;
     const int j0 = kt * AV_TILE;
@@ -505,6 +504,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    grid_launch_dependents();  // once this CTA holds its tensor memory: a dependent may want some too
     const Ctl ctl{args.status, abort_flag, args.budget_ns};
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
         const bool got = wait_bounded(bar, parity, ctl);

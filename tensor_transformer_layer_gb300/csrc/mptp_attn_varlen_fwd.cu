@@ -73,7 +73,6 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int kv_col = head / args.group * D;
 
     grid_dependency_wait();  // the sequences' offsets, like the tensors, may come from the kernel before
-    grid_launch_dependents();
     AvSpan sp;
     if (!av_span(args, seq, sp) || pr * 2 * AV_TILE >= sp.nq) return;
     const int qt[2] = {2 * pr, 2 * pr + 1};
@@ -113,6 +112,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    grid_launch_dependents();  // once this CTA holds its tensor memory: a dependent may want some too
     const Ctl ctl{args.status, abort_flag, args.budget_ns};
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
         const bool got = wait_bounded(bar, parity, ctl);

@@ -1,0 +1,372 @@
+// GEMM for few tokens: C[T, N] = A[T, K] W[K, N] with T <= 128, bound by reading W once.
+//
+// The roles of the operands are swapped against the large GEMM: the weight's columns are the rows of
+// the product (M = 128 of them, W as stored is the MN-major operand) and the tokens its columns, padded
+// to 16, so a CTA computes C^T[128, T] and a tile holds no more tokens than there are. (A 256 x 256 tile
+// would multiply mostly padding, and few such tiles exist: 6 to 48 for h = 1536 or f = 6144, a part of
+// the chip's 76 CTA pairs, each of which then reads a long K range alone.)
+//
+// The K range of a block of columns is split over the CTAs of a cluster, the largest size up to eight
+// whose clusters are all resident at once. Each CTA sends its fp32 partial sums through distributed
+// shared memory (four tokens a store) to the CTA that finishes those tokens, which adds them in rank
+// order: deterministic, in one launch and without a workspace.
+//
+//   warp 0: TMA producer, a ring of stages of 64 K rows x 128 columns (gated: 2 x 128) and the tokens' 64
+//           K elements. Before it waits for the previous kernel it asks L2 for the first stages' weights.
+//   warp 1: TMEM, MMA issue.   warps 2..5: partial sums out, reduction, epilogue.
+//
+// Epilogues: plain store, or gated: 128 gate columns and the 128 up columns of the same outputs have an
+// accumulator each, so that a thread finds both in its TMEM lane; Y = act(gate) up is computed where the
+// sums meet (GU also stored when asked for).
+#pragma once
+
+#include <atomic>
+
+#include "mptp_gemm.cuh"
+#include "mptp_internal.h"
+
+namespace mptp {
+
+constexpr int FEW_MAX_T = 128;
+constexpr int FEW_MAX_STAGES = 8;
+constexpr int FEW_THREADS = 192;
+constexpr int FEW_W_BYTES = 64 * 64 * 2;  // a block of 64 K rows x 64 columns
+
+struct FewArgs {
+    int T, npad;             // tokens; padded to 16
+    int kb;                  // K blocks of 64
+    int cols;                // output columns (gated: f)
+    int w_cols;              // columns of W
+    int up_off;              // gated: columns of W from a gate to its up
+    int cluster, stages;
+    int act;
+    __nv_bfloat16* out;      // [T, cols]
+    __nv_bfloat16* gu;       // gated, nullable: [T, 2 cols]
+    uint32_t* status;
+    unsigned long long budget_ns;
+};
+
+__host__ __device__ inline size_t few_stage_bytes(bool gated, int npad) { return (gated ? 4 : 2) * FEW_W_BYTES + size_t(npad) * 128; }
+// Tokens that each CTA of a cluster finishes: whole groups of four.
+__host__ __device__ inline int few_slice(int npad, int cluster) { return (npad / 4 + cluster - 1) / cluster * 4; }
+// Partial sums that a CTA receives: from every rank, its slice's tokens x 128 columns (x 2, gated).
+__host__ __device__ inline size_t few_red_bytes(bool gated, int npad, int cluster) {
+    return size_t(cluster) * few_slice(npad, cluster) * 128 * 4 * (gated ? 2 : 1);
+}
+// The partial sums take the ring's place once every CTA of the cluster has used its stages.
+__host__ __device__ inline size_t few_ring_bytes(bool gated, int npad, int cluster, int stages) {
+    const size_t ring = stages * few_stage_bytes(gated, npad), red = few_red_bytes(gated, npad, cluster);
+    return ring > red ? ring : red;
+}
+inline size_t few_smem_bytes(bool gated, int npad, int cluster, int stages) {
+    return 1024 + few_ring_bytes(gated, npad, cluster, stages) + 8 * (2 * FEW_MAX_STAGES + 2) + 16;
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                               const __grid_constant__ CUtensorMap tmA,
+                                                               const FewArgs args) {
+    constexpr int NACC = GATED ? 2 : 1;            // accumulators: gate and up
+    constexpr int W_STAGE = 2 * NACC * FEW_W_BYTES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int npad = args.npad, stages = args.stages, cluster = args.cluster;
+    const int slice = few_slice(npad, cluster);
+    uint8_t* sW = smem;                            // stage s at s * W_STAGE
+    uint8_t* sA = smem + stages * W_STAGE;         // stage s at s * npad * 128
+    // [source rank][four tokens of the slice][accumulator][128 columns] x 4 tokens
+    float4* red = reinterpret_cast<float4*>(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + few_ring_bytes(GATED, npad, cluster, stages));
+    uint64_t* full = bars;
+    uint64_t* empty = bars + FEW_MAX_STAGES;
+    uint64_t* acc_full = bars + 2 * FEW_MAX_STAGES;
+    uint64_t* drain_bar = acc_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int block = static_cast<int>(blockIdx.x) / cluster;
+    const int kb0 = args.kb * rank / cluster, kb1 = args.kb * (rank + 1) / cluster;
+    const uint32_t need_cols = NACC * npad;
+    const uint32_t tmem_cols = need_cols <= 32 ? 32u : need_cols <= 64 ? 64u : need_cols <= 128 ? 128u : 256u;
+
+    // Weight columns of the stage's i-th 64-wide block. A last block behind the columns reads zeros (or,
+    // gated, columns of the ups, whose results are not stored).
+    auto w_col = [&](int i) { return block * 128 + (i & 1) * 64 + (i >> 1) * args.up_off; };
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmA);
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0u;
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+        // Into L2 only: whatever the previous kernel may still write is read after the wait below.
+        for (int kb = kb0; kb < kb1 && kb < kb0 + stages; ++kb)
+#pragma unroll
+            for (int i = 0; i < 2 * NACC; ++i)
+                if (w_col(i) < args.w_cols) tma_prefetch_2d(&tmW, w_col(i), kb * BK);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Ctl ctl{args.status, abort_flag, args.budget_ns};
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bounded(&empty[st], ph ^ 1u, ctl)) break;
+                mbar_arrive_expect_tx(&full[st], W_STAGE + npad * 128);
+#pragma unroll
+                for (int i = 0; i < 2 * NACC; ++i)
+                    tma_load_2d(sW + st * W_STAGE + i * FEW_W_BYTES, &tmW, &full[st], w_col(i), kb * BK);
+                tma_load_2d(sA + st * npad * 128, &tmA, &full[st], kb * BK, 0);
+                if (++st == stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = make_idesc_bf16(128, npad, true, false);
+        const uint64_t w_desc = make_sdesc_sw128(smem_u32(sW), FEW_W_BYTES, 1024);
+        const uint64_t a_desc = make_sdesc_sw128(smem_u32(sA), 16, 1024);
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const bool got = wait_bounded(&full[st], ph, ctl);
+            if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
+            tc_fence_after();
+            const uint64_t wd = w_desc + static_cast<uint32_t>((st * W_STAGE) >> 4);
+            const uint64_t ad = a_desc + static_cast<uint32_t>((st * npad * 128) >> 4);
+#pragma unroll
+            for (int k = 0; k < BK / UMMA_K; ++k)
+#pragma unroll
+                for (int c = 0; c < NACC; ++c)
+                    umma_bf16_elect(tmem_base + c * npad, wd + c * (2 * FEW_W_BYTES >> 4) + k * (2048 >> 4),
+                                    ad + k * (32 >> 4), idesc, kb > kb0 || k > 0 ? 1u : 0u);
+            umma_commit_elect(&empty[st]);
+            if (++st == stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+        if (ok) umma_commit_elect(acc_full);
+        umma_commit_elect(drain_bar);
+        wait_drain(drain_bar, 0, args.status);
+    }
+    const int q = warp & 3;
+    const int col = q * 32 + lane;  // column of the block
+    bool got = true;
+    if (warp >= 2) {
+        got = wait_bounded(acc_full, 0, ctl);
+        got = __all_sync(0xffffffffu, got) != 0;
+    }
+    __syncwarp();
+    if (cluster > 1) cluster_sync_all();  // every CTA of the cluster has used its ring: it may be written over
+    if (warp >= 2) {
+        // This CTA's partial sums, four tokens at a time, to the CTAs that finish them.
+        if (got) {
+            tc_fence_after();
+            const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+            int owner = 0, at = 0;  // the four tokens' CTA, and their place in its slice
+#pragma unroll 1
+            for (int c = 0; c < args.T; c += 16) {
+                uint32_t v[NACC][16];
+#pragma unroll
+                for (int i = 0; i < NACC; ++i) tmem_ld16(t_addr + i * npad + c, v[i]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < NACC; ++i) reg_fence16(v[i]);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (c + 4 * g < args.T) {
+                        float4* dst = red + ((rank * (slice / 4) + at) * NACC) * 128 + col;
+                        const uint32_t to = cluster > 1 ? mapa_shared(smem_u32(dst), owner) : smem_u32(dst);
+#pragma unroll
+                        for (int i = 0; i < NACC; ++i)
+                            st_cluster_v4(to + i * 2048, v[i][4 * g], v[i][4 * g + 1], v[i][4 * g + 2], v[i][4 * g + 3]);
+                    }
+                    if (++at == slice / 4) {
+                        at = 0;
+                        ++owner;
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (cluster > 1)
+        cluster_sync_all();  // releases the partial sums, acquires the others'
+    else
+        __syncthreads();
+    if (warp >= 2 && *abort_flag == 0u && block * 128 + col < args.cols) {
+        const int c0 = rank * slice, c1 = min(args.T, c0 + slice);
+        __nv_bfloat16* out = args.out + block * 128 + col;
+#pragma unroll 2
+        for (int c = c0; c < c1; c += 4) {
+            float4 sum[NACC];
+#pragma unroll
+            for (int i = 0; i < NACC; ++i) sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float4* p = red + ((c - c0) / 4 * NACC) * 128 + col;
+            for (int s = 0; s < cluster; ++s, p += slice / 4 * NACC * 128)
+#pragma unroll
+                for (int i = 0; i < NACC; ++i) {
+                    const float4 v = p[i * 128];
+                    sum[i].x += v.x;
+                    sum[i].y += v.y;
+                    sum[i].z += v.z;
+                    sum[i].w += v.w;
+                }
+            const float a[4] = {sum[0].x, sum[0].y, sum[0].z, sum[0].w};
+            float y[4] = {a[0], a[1], a[2], a[3]};
+            if constexpr (GATED) {
+                const float u[4] = {sum[1].x, sum[1].y, sum[1].z, sum[1].w};
+                const float2 lo = mul2(glu_act2(make_float2(a[0], a[1]), args.act), make_float2(u[0], u[1]));
+                const float2 hi = mul2(glu_act2(make_float2(a[2], a[3]), args.act), make_float2(u[2], u[3]));
+                y[0] = lo.x, y[1] = lo.y, y[2] = hi.x, y[3] = hi.y;
+                if (args.gu) {
+                    __nv_bfloat16* gu = args.gu + static_cast<long long>(c) * 2 * args.cols + block * 128 + col;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e, gu += 2 * args.cols)
+                        if (c + e < c1) {
+                            gu[0] = __float2bfloat16(a[e]);
+                            gu[args.cols] = __float2bfloat16(u[e]);
+                        }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < c1) out[static_cast<long long>(c + e) * args.cols] = __float2bfloat16(y[e]);
+        }
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        if (threadIdx.x == 0) spin_ns(ABORT_SETTLE_NS);
+        __syncthreads();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem_base, tmem_cols);
+    }
+}
+
+// Clusters of `cluster` CTAs of this kernel that are resident at once.
+template <bool GATED>
+inline int few_resident_clusters(int cluster, size_t smem, int num_sms) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster * num_sms, 1, 1);
+    cfg.blockDim = dim3(FEW_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_few_kernel<GATED>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+// C[T, cols] = A[T, K] W[K, ...]; W's rows are `ldw` columns wide.
+template <bool GATED>
+inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* out, mp_bf16* gu, int T, int K, int cols,
+                                 int ldw, int act, uint32_t* status, int num_sms, cudaStream_t stream) {
+    FewArgs a{};
+    a.T = T;
+    a.npad = ceil_div(T, 16) * 16;
+    a.kb = K / BK;
+    a.cols = cols;
+    a.w_cols = ldw;
+    a.up_off = cols;
+    a.act = act;
+    a.out = reinterpret_cast<__nv_bfloat16*>(out);
+    a.gu = reinterpret_cast<__nv_bfloat16*>(gu);
+    a.status = status;
+    a.budget_ns = wait_budget_ns();
+    CUtensorMap tw, ta;
+    if (!make_tmap_bf16(&tw, W, ldw, K, ldw, 64, 64) || !make_tmap_bf16(&ta, A, K, T, K, 64, a.npad)) return MP_ERR_CUDA;
+    auto kern = gemm_few_kernel<GATED>;
+    const int blocks = ceil_div(cols, 128);
+    auto fit_stages = [&](int cluster) {
+        int n = FEW_MAX_STAGES;
+        while (few_smem_bytes(GATED, a.npad, cluster, n) > SMEM_LIMIT) --n;
+        return n;
+    };
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_LIMIT)) != cudaSuccess)
+        return MP_ERR_CUDA;
+    // How many clusters of a size are resident depends on the device alone (one CTA an SM): looked up once.
+    static std::atomic<int> cached[16][9];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    a.cluster = 1;
+    for (int c = 8; c > 1; --c) {
+        if (a.kb < 2 * c) continue;
+        std::atomic<int>* slot = dev < 16 ? &cached[dev][c] : nullptr;
+        int n = slot ? slot->load(std::memory_order_relaxed) : 0;
+        if (n == 0) {
+            n = few_resident_clusters<GATED>(c, SMEM_LIMIT, num_sms);
+            if (slot) slot->store(n > 0 ? n : -1, std::memory_order_relaxed);
+        }
+        if (blocks <= n) {
+            a.cluster = c;
+            break;
+        }
+    }
+    a.stages = fit_stages(a.cluster);
+    const size_t smem = few_smem_bytes(GATED, a.npad, a.cluster, a.stages);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks * a.cluster);
+    cfg.blockDim = dim3(FEW_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = a.cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tw, ta, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
+}
+
+}  // namespace mptp

@@ -17,6 +17,7 @@
 // Then Z is one row-parallel GEMM over Y.
 // Backward: one GEMM gives dY, whose epilogue reads G and U and writes dG and dU (dY never reaches
 // memory); dX, dW and dWd are three GEMMs, side by side where that is shorter (mptp_mlp_host.cuh).
+#include "mptp_gemm_few.cuh"
 #include "mptp_mlp_host.cuh"
 
 using namespace mptp;
@@ -45,6 +46,10 @@ extern "C" mp_status mp_glu_fwd(const mp_bf16* X, const mp_bf16* W, const mp_bf1
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const double Tb = 2.0 * T, hb = 2.0 * h;
     const size_t f2 = size_t(2) * f;
+    if (T <= FEW_MAX_T) {
+        st = launch_gemm_few<true>(X, W, Y, GU_save, T, h, f, static_cast<int>(f2), act, d_status, sms, s);
+        return st != MP_OK ? st : launch_gemm_few<false>(Y, Wd, Z, nullptr, T, f, h, h, act, d_status, sms, s);
+    }
 
     // [G | U] = X W and Y = act(G) * U, tiles of 128 outputs.
     TmapSet m1{};
