@@ -130,6 +130,10 @@ def status_string(code: int) -> str:
 
 
 def _ptr(x, name, dtype=torch.bfloat16, shape=None, allow_none=False):
+    # What a right call passes, in as few steps as it takes; everything else is told apart below.
+    if type(x) is torch.Tensor and x.dtype is dtype and (shape is None or x.shape == shape) and x.is_cuda and \
+            x.is_contiguous():
+        return x.data_ptr() or None
     if x is None:
         if allow_none:
             return None
@@ -149,7 +153,8 @@ def _ptr(x, name, dtype=torch.bfloat16, shape=None, allow_none=False):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream, without building the Stream object (0.2 against 2.9 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -429,21 +434,25 @@ def _heads_view(x, name, shape=None):
     some heads of a wider row is fine)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype != torch.bfloat16:
+    if x.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
-    if x.dim() != 3 or (shape is not None and tuple(x.shape) != tuple(shape)):
+    size = x.shape
+    if len(size) != 3 or (shape is not None and size != shape):
         want = "[tokens, heads, d]" if shape is None else tuple(shape)
-        raise ValueError(f"{name} must have shape {want}, got {tuple(x.shape)}")
-    T, heads, d = x.shape
-    if x.numel() == 0:
-        return None, heads * d
-    if (d > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != d):
+        raise ValueError(f"{name} must have shape {want}, got {tuple(size)}")
+    T, heads, d = size
+    row = heads * d
+    if T == 0 or row == 0:
+        return None, row
+    pitch, step, unit = x.stride()
+    if (d > 1 and unit != 1) or (heads > 1 and step != d):
         raise ValueError(f"{name}: each token's heads must be contiguous (strides (any, d, 1))")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    pitch = x.stride(0) if T > 1 else heads * d
-    if pitch < heads * d:
-        raise ValueError(f"{name}: rows overlap (pitch {pitch} < {heads * d})")
+    if T == 1:
+        pitch = row
+    elif pitch < row:
+        raise ValueError(f"{name}: rows overlap (pitch {pitch} < {row})")
     return x.data_ptr(), pitch
 
 
