@@ -645,6 +645,9 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     } else {
         reg_alloc<T::REGS_SOFTMAX>();
         // ---------------- softmax: warps 4..7 query columns 0..63, warps 8..11 columns 64..127 ----------------
+        // The scores are read as matrix fragments, four keys of a thread with 16 columns each, rather than one
+        // key with 64: the statistics go by column, and a thread then fetches 16 of each from shared memory
+        // instead of 64 (with 64, those loads took 1290 of an iteration's cycles on the load pipe).
         const int hf = (warp - 4) >> 2;
         const int q = warp & 3;
         const int w0 = j0 + q * 32;   // first key of this warp, in its sequence
@@ -658,13 +661,18 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         bool ok = true;
         for (int it = 0; it < n && ok; ++it) {
             const int st = it % SST;
-            const float* nl = stats + st * 2 * AV_TILE + hf * 64;
-            const float* nd = nl + AV_TILE;
+            // this thread's columns 8 i + 2 (lane % 4), + 1 of its warps' half of the tile
+            const float2* nl = reinterpret_cast<const float2*>(stats + st * 2 * AV_TILE + hf * 64) + (lane & 3);
+            const float2* nd = nl + AV_TILE / 2;
             if (!(ok = wait_all(&st_full[st], (it / SST) & 1) && wait_all(s_full, it & 1))) break;
             tc_fence_after();
-            uint32_t p[2][32], w[32];
-            tmem_ld32(s_addr, p[0]);
-            tmem_ld32(s_addr + 32, p[1]);
+            // 32 keys x 64 queries of the warp as two fragments of 16 keys: keys f * 16 + e * 8 + lane / 4
+            uint32_t p[2][32], w[2][16];
+            tmem_ld_frag64(s_addr, p[0]);
+            tmem_ld_frag64(s_addr + (16u << 16), p[1]);
+            float2 row[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) row[i] = nl[i * 4];
             tmem_wait_ld();
             reg_fence32(p[0]);
             reg_fence32(p[1]);
@@ -673,61 +681,61 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_read);
             }
-            // causal: this key is visible from column lo on; lo_w, the most, is the warp's last key's
+            // causal: a key is visible from column lo on; lo_w, the most, is the warp's last key's
             const int lo_w = args.causal ? w0 + 31 - off - at.tile * AV_TILE - hf * 64 : 0;
-            const int lo = lo_w - 31 + lane;
+            const int lo = lo_w - 31 + (lane >> 2) - 2 * (lane & 3);  // of key lane / 4, against column 8 i + c
             auto prob = [&](auto masked) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    const float4 l4 = *reinterpret_cast<const float4*>(nl + 2 * k);
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t& a = p[(2 * (k + e)) >> 5][(2 * (k + e)) & 31];
-                        uint32_t& b = p[(2 * (k + e) + 1) >> 5][(2 * (k + e) + 1) & 31];
-                        const float2 x = fma2(make_float2(__uint_as_float(a), __uint_as_float(b)), c2v,
-                                              e ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+                    for (int fe = 0; fe < 4; ++fe) {
+                        const int f = fe >> 1, e = fe & 1;
+                        uint32_t& a = p[f][4 * i + 2 * e];
+                        uint32_t& b = p[f][4 * i + 2 * e + 1];
+                        const float2 x = fma2(make_float2(__uint_as_float(a), __uint_as_float(b)), c2v, row[i]);
                         float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                         if (decltype(masked)::value) {
-                            pr.x = 2 * (k + e) >= lo ? pr.x : 0.0f;
-                            pr.y = 2 * (k + e) + 1 >= lo ? pr.y : 0.0f;
+                            pr.x = 8 * i >= lo + f * 16 + e * 8 ? pr.x : 0.0f;
+                            pr.y = 8 * i + 1 >= lo + f * 16 + e * 8 ? pr.y : 0.0f;
                         }
                         a = __float_as_uint(pr.x);
                         b = __float_as_uint(pr.y);
-                        w[k + e] = pack_bf16x2(pr.x, pr.y);
+                        w[f][2 * i + e] = pack_bf16x2(pr.x, pr.y);
                     }
-                }
             };
             if (args.causal && lo_w > 0)
                 prob(std::true_type{});
             else
                 prob(std::false_type{});
             if (Cfg::OWN_P && it > 0 && !(ok = wait_all(dv_done, (it - 1) & 1))) break;
-            tmem_st32(p_addr, w);
+            tmem_st_frag32(p_addr, w[0]);
+            tmem_st_frag32(p_addr + (16u << 16), w[1]);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_full);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) row[i] = nd[i * 4];
             if (!(ok = wait_all(dp_full, it & 1))) break;
             tc_fence_after();
             uint32_t t[2][32];
-            tmem_ld32(dp_addr, t[0]);
-            tmem_ld32(dp_addr + 32, t[1]);
+            tmem_ld_frag64(dp_addr, t[0]);
+            tmem_ld_frag64(dp_addr + (16u << 16), t[1]);
             tmem_wait_ld();
             reg_fence32(t[0]);
             reg_fence32(t[1]);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-                const float4 d4 = *reinterpret_cast<const float4*>(nd + 2 * k);
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = 2 * (k + e);
-                    const float2 dp = make_float2(__uint_as_float(t[c >> 5][c & 31]), __uint_as_float(t[c >> 5][(c & 31) + 1]));
-                    const float2 pr = make_float2(__uint_as_float(p[c >> 5][c & 31]), __uint_as_float(p[c >> 5][(c & 31) + 1]));
-                    const float2 ds = mul2(pr, add2(dp, e ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y)));
-                    w[k + e] = pack_bf16x2(ds.x, ds.y);
+                for (int fe = 0; fe < 4; ++fe) {
+                    const int f = fe >> 1, e = fe & 1, k = 4 * i + 2 * e;
+                    const float2 dp = make_float2(__uint_as_float(t[f][k]), __uint_as_float(t[f][k + 1]));
+                    const float2 pr = make_float2(__uint_as_float(p[f][k]), __uint_as_float(p[f][k + 1]));
+                    const float2 ds = mul2(pr, add2(dp, row[i]));
+                    w[f][2 * i + e] = pack_bf16x2(ds.x, ds.y);
                 }
-            }
-            tmem_st32(dp_addr, w);
+            tmem_st_frag32(dp_addr, w[0]);
+            tmem_st_frag32(dp_addr + (16u << 16), w[1]);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
