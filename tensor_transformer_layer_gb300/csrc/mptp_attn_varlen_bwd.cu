@@ -50,7 +50,7 @@ struct AvDqCfg {
     using T = AvTile<D>;
     static constexpr int KST = D == 128 ? 3 : 4;  // a K tile serves S(j) and, later, dQ(j)
     static constexpr int VST = D == 64 ? 4 : D == 96 ? 3 : 2;
-    static constexpr int NUM_BARS = 2 + 2 * KST + 2 * VST + 2 + 5 + 1;
+    static constexpr int NUM_BARS = 2 + 2 * KST + 2 * VST + 2 + 6 + 1;
     static constexpr size_t SMEM = 1024 + (2 + KST + VST) * size_t(T::BYTES) + 2 * AV_TILE * 4 + 8 * NUM_BARS + 16;
     static_assert(SMEM <= SMEM_LIMIT, "shared memory per block");
     static constexpr uint32_t TMEM_COLS = 512;  // S(even), S(odd) at 0, 128; dP at 256; dQ at 384
@@ -83,8 +83,10 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     uint64_t* s_full = v_empty + VST;  // [2]
     uint64_t* dp_full = s_full + 2;
     uint64_t* dp_read = dp_full + 1;   // the softmax warps have dP(j) in registers
-    uint64_t* ds_full = dp_read + 1;   // dS(j) is in tensor memory
-    uint64_t* dq_full = ds_full + 1;
+    // dS(j) is in tensor memory: one barrier for even and one for odd j, since a warp may be done with
+    // dS(j+1) (its dP(j+1) waits for dP(j) to be read only) while another still writes dS(j)
+    uint64_t* ds_full = dp_read + 1;   // [2]
+    uint64_t* dq_full = ds_full + 2;
     uint64_t* part_full = dq_full + 1; // both halves of delta from one key tile
     uint64_t* drain_bar = part_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
@@ -121,7 +123,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         mbar_init(&s_full[1], 1);
         mbar_init(dp_full, 1);
         mbar_init(dp_read, 8);
-        mbar_init(ds_full, 8);
+        mbar_init(&ds_full[0], 8);
+        mbar_init(&ds_full[1], 8);
         mbar_init(dq_full, 1);
         mbar_init(part_full, 8);
         mbar_init(drain_bar, 1);
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     tc_fence_after();
                     dp_mma(j + 1);
                 }
-                if (!(ok = wait_all(ds_full, j & 1))) break;
+                if (!(ok = wait_all(&ds_full[j & 1], (j >> 1) & 1))) break;
                 tc_fence_after();
                 const uint64_t kd = kt_desc + static_cast<uint32_t>(((j % KST) * T::BYTES) >> 4);
                 const uint32_t acc0 = j > 0 ? 1u : 0u;
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(ds_full);
+            if (lane == 0) mbar_arrive(&ds_full[j & 1]);
         }
         if (ok && row_ok && hf == 0) delta[at] = dl;
         if (ok && rows_ok > 0) {
