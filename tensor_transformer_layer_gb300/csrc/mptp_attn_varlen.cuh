@@ -14,6 +14,7 @@ namespace mptp {
 
 constexpr uint32_t DEV_SEQ_RANGE = 0x4u;
 constexpr int AV_TILE = 128;     // rows per tile
+constexpr int AV_MAX_CLUSTER = 8;
 constexpr int AV_THREADS = 384;  // warpgroup 0: loads, MMA, helpers; 1 and 2: softmax
 
 template <int D>
@@ -157,7 +158,7 @@ inline mp_status av_check(int nseq, int Tq, int Tk, int max_q, int max_k, int he
         return MP_ERR_UNSUPPORTED_SHAPE;
     // CTAs of the largest launch: one per sequence, head and tile of the longest sequence
     const long long tiles = (max_q > max_k ? max_q : max_k) / AV_TILE + 1;
-    if (tiles * nseq > 0x7fffffffLL / heads) return MP_ERR_UNSUPPORTED_SHAPE;
+    if (tiles * nseq > 0x7fffffffLL / AV_MAX_CLUSTER / heads) return MP_ERR_UNSUPPORTED_SHAPE;
     return MP_OK;
 }
 inline bool av_bad_pitch(long long ld, long long row) { return ld < row || ld % 8 != 0 || ld > (1LL << 36); }
@@ -183,11 +184,26 @@ inline AvArgs av_args(const int32_t* cu_q, const int32_t* cu_k, int nseq, int Tq
     return a;
 }
 
+// `blocks` CTAs in clusters of `cluster`.
 template <typename Kern, typename... Args>
-inline cudaError_t av_launch(Kern kern, long long blocks, size_t smem, cudaStream_t s, Args... args) {
+inline cudaError_t av_launch(Kern kern, long long blocks, int cluster, size_t smem, cudaStream_t s, Args... args) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(AV_THREADS), smem, s, args...);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(AV_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

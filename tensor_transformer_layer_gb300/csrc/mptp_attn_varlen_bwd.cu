@@ -24,6 +24,9 @@
 //   accumulators take all 512 columns: P^T lies over S^T, so S(i+1) follows dV(i), and the products of one
 //   half of the softmax (dV, S) run while the warps are at the other half (dK, dP). At D <= 96 P^T has
 //   columns of its own, and S(i+1) runs as soon as the warps have S(i) in registers.
+//   Where whole key tiles would balance badly (few of them, many queries each), a cluster of two to eight CTAs
+//   shares one: each takes a part of its (head, query tile) pairs, and the fp32 sums are joined through
+//   distributed shared memory in rank order.
 // In both, a softmax thread has one row and 64 of its 128 columns.
 //
 // P and dS are rounded to bf16 for their products (the tensor core's operand type); the exponent,
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                            const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
                            const float* LSE, const float* delta, __nv_bfloat16* dK, long long lddk, __nv_bfloat16* dV,
-                           long long lddv, const AvArgs args) {
+                           long long lddv, int cluster, const AvArgs args) {
     using Cfg = AvDkvCfg<D>;
     using T = AvTile<D>;
     constexpr int NB = T::NB, QST = Cfg::QST, OST = Cfg::OST, SST = Cfg::SST;
@@ -438,8 +441,10 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int per_tile = args.nseq * args.kv_heads;
-    const int kt = static_cast<int>(blockIdx.x) / per_tile;  // the first keys have the most queries (causal)
-    const int rem = static_cast<int>(blockIdx.x) % per_tile;
+    const int item = static_cast<int>(blockIdx.x) / cluster;
+    const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int kt = item / per_tile;  // the first keys have the most queries (causal)
+    const int rem = item % per_tile;
     const int seq = rem / args.kv_heads;
     const int kvh = rem % args.kv_heads;
 
@@ -452,7 +457,11 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int t1 = (sp.nq + AV_TILE - 1) / AV_TILE;
     const int t0 = args.causal ? max(0, j0 - off) / AV_TILE : 0;
     const int per_head = max(0, t1 - t0);
-    const int n = per_head * args.group;
+    const int n_all = per_head * args.group;
+    // this CTA's part of the iterations
+    auto part_begin = [&](int r) { return static_cast<int>(static_cast<long long>(n_all) * r / cluster); };
+    const int it0 = part_begin(rank);
+    const int n = part_begin(rank + 1) - it0;
     const int q_tail = t1 * AV_TILE > sp.nq ? sp.nq - (t1 - 1) * AV_TILE : AV_TILE;
     // Iterations: the group's heads in turn, of each the query tiles t0 .. t1 - 1. Every role walks them
     // with counters (a division an iteration was a tenth of the loop).
@@ -465,7 +474,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             }
         }
     };
-    const Walk first{kvh * args.group, t0, t0, t1};
+    const Walk first{kvh * args.group + (n > 0 ? it0 / per_head : 0), t0 + (n > 0 ? it0 % per_head : 0), t0, t1};
 
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 2);
@@ -494,9 +503,9 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         fence_proxy_async_smem();
         if (n > 0) {
             av_load<D>(sK, &tmK, kv_full, kvh * D, sp.k0 + j0);
-            av_load<D>(sQ, &tmQ, &q_full[0], first.head * D, sp.q0 + t0 * AV_TILE);
+            av_load<D>(sQ, &tmQ, &q_full[0], first.head * D, sp.q0 + first.tile * AV_TILE);
             av_load<D>(sV, &tmV, kv_full, kvh * D, sp.k0 + j0);
-            av_load<D>(sdO, &tmdO, &do_full[0], first.head * D, sp.q0 + t0 * AV_TILE);
+            av_load<D>(sdO, &tmdO, &do_full[0], first.head * D, sp.q0 + first.tile * AV_TILE);
         }
     }
     if (warp == 1) {
@@ -748,10 +757,10 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             }
             at.next();
         }
-        if (ok && rows_ok > 0) {
+        __nv_bfloat16* out = hf ? dK : dV;
+        const long long ld = hf ? lddk : lddv;
+        if (ok && cluster == 1 && rows_ok > 0) {
             // warps 4..7 write dV, warps 8..11 dK; K's and V's tiles are free for the staging
-            __nv_bfloat16* out = hf ? dK : dV;
-            const long long ld = hf ? lddk : lddv;
             if (n == 0) {
                 av_store_zero_rows(0, NB, kvh * D, sp.k0 + w0, out, ld, rows_ok, lane);
             } else if (wait_all(fin_full, 0)) {
@@ -760,7 +769,77 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                               (hf ? sK : sV) + q * (NB * 2048), hf ? &tmdK : &tmdV, kvh * D, sp.k0 + w0, out, ld,
                               rows_ok, lane);
             }
+        } else if (ok && n > 0) {
+            ok = wait_all(fin_full, 0);
+            tc_fence_after();
         }
+        if (cluster > 1) {
+            // Chunk c (32 columns) of dV or dK is finished by rank (hf NB + c) % cluster. The others send it
+            // their rows, eight pieces of 16 bytes a row, into the ring of Q and dO tiles:
+            // [source rank][chunk of the owner][piece][128 keys].
+            constexpr int CHUNK = 8 * AV_TILE;
+            const int owned = (2 * NB + cluster - 1) / cluster;
+            float4* recv = reinterpret_cast<float4*>(sQ);
+            const uint32_t acc = tmem_base + lane_addr + (hf ? Cfg::DK_COL : 256);
+            __syncwarp();
+            cluster_sync_all();  // every CTA of the cluster has used its ring
+            for (int c = 0; c < NB && ok && n > 0; ++c) {
+                const int id = hf * NB + c, owner = id % cluster;
+                if (owner == rank) continue;
+                uint32_t o[32];
+                tmem_ld32(acc + c * 32, o);
+                tmem_ld_wait(o);
+                const uint32_t to = mapa_shared(
+                    smem_u32(recv + (rank * owned + id / cluster) * CHUNK + q * 32 + lane), owner);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    st_cluster_v4(to + k * (AV_TILE * 16), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+            __syncwarp();
+            cluster_sync_all();
+            const float f = hf ? args.scale : 1.0f;
+            for (int c = 0; c < NB && ok; ++c) {
+                const int id = hf * NB + c;
+                if (id % cluster != rank) continue;
+                uint32_t mine[32];
+                if (n > 0) {
+                    tmem_ld32(acc + c * 32, mine);
+                    tmem_ld_wait(mine);
+                }
+                float sum[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) sum[k] = 0.0f;
+                for (int r = 0; r < cluster; ++r) {
+                    if (part_begin(r + 1) == part_begin(r)) continue;  // a rank without a part has no sums
+                    const float4* from = recv + (r * owned + id / cluster) * CHUNK + q * 32 + lane;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 v = r == rank ? make_float4(__uint_as_float(mine[4 * k]), __uint_as_float(mine[4 * k + 1]),
+                                                                 __uint_as_float(mine[4 * k + 2]), __uint_as_float(mine[4 * k + 3]))
+                                                   : from[k * AV_TILE];
+                        sum[4 * k] += v.x;
+                        sum[4 * k + 1] += v.y;
+                        sum[4 * k + 2] += v.z;
+                        sum[4 * k + 3] += v.w;
+                    }
+                }
+                if (lane < rows_ok) {
+                    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<long long>(sp.k0 + w0 + lane) * ld + kvh * D + c * 32);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dst[k] = make_uint4(pack_bf16x2(sum[8 * k] * f, sum[8 * k + 1] * f),
+                                            pack_bf16x2(sum[8 * k + 2] * f, sum[8 * k + 3] * f),
+                                            pack_bf16x2(sum[8 * k + 4] * f, sum[8 * k + 5] * f),
+                                            pack_bf16x2(sum[8 * k + 6] * f, sum[8 * k + 7] * f));
+                }
+            }
+        }
+    }
+    if (cluster > 1 && warp < 4) {
+        // (the softmax warps' two barriers)
+        __syncwarp();
+        cluster_sync_all();
+        cluster_sync_all();
     }
 
     // ---------------- teardown ----------------
@@ -777,6 +856,36 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     }
 }
 
+// CTAs that share a key tile. The estimate, in iterations (a head's query tile each): the larger of the longest
+// CTA and of all the work over the SMs that clusters of this size can use, where each CTA costs three
+// iterations more than its own, and one of a cluster seven to ten (its set-up, the join, and SMs that wait for
+// the cluster's others). Lengths are on the device: the sum over the sequences is taken between that of equal
+// ones and that of the longest. Measured with 1, 2, 4, 8 CTAs a tile: 16,384 causal queries, eight heads on two,
+// d = 128 (256 tiles, the longest 512 iterations) 782, 727, 785, 1083 us; eight packed documents, 16 heads on
+// four, d = 96 (272 tiles, the longest 76) 109, 112, 161, 335 us.
+static int dkv_cluster(const AvArgs& a, int sms) {
+    const double tiles = a.Tk / double(AV_TILE) + 0.5 * a.nseq;
+    const double longest = double(a.group) * ceil_div(a.max_q, AV_TILE);
+    const double mean = double(a.Tq) / a.nseq;
+    const double total = tiles * a.heads * (0.5 * (a.max_q + mean) / AV_TILE + 0.5) * (a.causal ? 0.5 : 1.0);
+    const double usable[4] = {1.0, 1.0, 0.95, 0.79};  // of the SMs: 152, 152, 144, 120
+    const double extra[4] = {3.0, 7.0, 8.0, 10.0};
+    int best = 1;
+    double least = 0.0;
+    for (int i = 0; i < 4; ++i) {
+        const int c = 1 << i;
+        if (c > 1 && longest < 4 * c) break;
+        const double even = (total + tiles * a.kv_heads * c * extra[i]) / (sms * usable[i]);
+        const double part = longest / c + extra[i];
+        const double est = even > part ? even : part;
+        if (i == 0 || est < 0.95 * least) {
+            best = c;
+            least = est;
+        }
+    }
+    return best;
+}
+
 struct AvBwdMaps {
     CUtensorMap q, k, v, d_o, dq, dk, dv;
 };
@@ -784,18 +893,20 @@ struct AvBwdMaps {
 template <int D>
 static cudaError_t launch_bwd(const AvBwdMaps& m, const mp_bf16* O, long long ldo, const mp_bf16* dO, long long lddo,
                               const float* LSE, float* delta, mp_bf16* dQ, long long lddq, mp_bf16* dK, long long lddk,
-                              mp_bf16* dV, long long lddv, const AvArgs& a, cudaStream_t s) {
+                              mp_bf16* dV, long long lddv, const AvArgs& a, int sms, cudaStream_t s) {
     auto bf = [](auto* p) { return reinterpret_cast<__nv_bfloat16*>(const_cast<mp_bf16*>(p)); };
     const int qtiles = ceil_div(a.max_q, AV_TILE), ktiles = ceil_div(a.max_k, AV_TILE);
     cudaError_t e = cudaSuccess;
     if (qtiles > 0)
-        e = av_launch(attn_varlen_dq_kernel<D>, static_cast<long long>(qtiles) * a.nseq * a.heads, AvDqCfg<D>::SMEM, s, m.q,
+        e = av_launch(attn_varlen_dq_kernel<D>, static_cast<long long>(qtiles) * a.nseq * a.heads, 1, AvDqCfg<D>::SMEM, s, m.q,
                       m.k, m.v, m.d_o, m.dq, static_cast<const __nv_bfloat16*>(bf(O)), ldo,
                       static_cast<const __nv_bfloat16*>(bf(dO)), lddo, LSE, delta, bf(dQ), lddq, qtiles, a);
-    if (e == cudaSuccess && ktiles > 0)
-        e = av_launch(attn_varlen_dkv_kernel<D>, static_cast<long long>(ktiles) * a.nseq * a.kv_heads, AvDkvCfg<D>::SMEM, s,
-                      m.q, m.k, m.v, m.d_o, m.dk, m.dv, LSE, static_cast<const float*>(delta), bf(dK), lddk, bf(dV),
-                      lddv, a);
+    if (e == cudaSuccess && ktiles > 0) {
+        const int cluster = dkv_cluster(a, sms);
+        e = av_launch(attn_varlen_dkv_kernel<D>, static_cast<long long>(ktiles) * a.nseq * a.kv_heads * cluster, cluster,
+                      AvDkvCfg<D>::SMEM, s, m.q, m.k, m.v, m.d_o, m.dk, m.dv, LSE, static_cast<const float*>(delta),
+                      bf(dK), lddk, bf(dV), lddv, cluster, a);
+    }
     return e;
 }
 
@@ -843,8 +954,8 @@ extern "C" mp_status mp_attn_varlen_bwd(const mp_bf16* Q, const mp_bf16* K, cons
     const AvArgs a = av_args(cu_q, cu_k, nseq, Tq, Tk, max_q, max_k, heads, kv_heads, causal ? 1 : 0, scale, d_status);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
-        d == 64   ? launch_bwd<64>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, s)
-        : d == 96 ? launch_bwd<96>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, s)
-                  : launch_bwd<128>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, s);
+        d == 64   ? launch_bwd<64>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, sms, s)
+        : d == 96 ? launch_bwd<96>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, sms, s)
+                  : launch_bwd<128>(m, O, ldo, dO, lddo, LSE, delta_ws, dQ, lddq, dK, lddk, dV, lddv, a, sms, s);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }

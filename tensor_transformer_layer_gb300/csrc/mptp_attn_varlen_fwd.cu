@@ -375,11 +375,11 @@ extern "C" mp_status mp_attn_varlen_fwd(const mp_bf16* Q, const mp_bf16* K, cons
     __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(O);
     cudaError_t e;
     if (d == 64)
-        e = av_launch(attn_varlen_fwd_kernel<64>, blocks, AvFwdCfg<64>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs, a);
+        e = av_launch(attn_varlen_fwd_kernel<64>, blocks, 1, AvFwdCfg<64>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs, a);
     else if (d == 96)
-        e = av_launch(attn_varlen_fwd_kernel<96>, blocks, AvFwdCfg<96>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs, a);
+        e = av_launch(attn_varlen_fwd_kernel<96>, blocks, 1, AvFwdCfg<96>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs, a);
     else
-        e = av_launch(attn_varlen_fwd_kernel<128>, blocks, AvFwdCfg<128>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs,
+        e = av_launch(attn_varlen_fwd_kernel<128>, blocks, 1, AvFwdCfg<128>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs,
                       a);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }

@@ -62,10 +62,6 @@ inline size_t few_smem_bytes(bool gated, int npad, int cluster, int stages) {
     return 1024 + few_ring_bytes(gated, npad, cluster, stages) + 8 * (2 * FEW_MAX_STAGES + 2) + 16;
 }
 
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
                  "r"(x), "r"(y)

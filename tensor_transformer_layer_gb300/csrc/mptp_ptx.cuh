@@ -91,6 +91,12 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// 16 bytes into the shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 // Arrive on an mbarrier given by its shared::cluster address (possibly in the peer
 // CTA), default (release, CTA-scope) semantics: the only thing published through it
 // is the completion of this thread's tcgen05.ld, which tcgen05.fence orders.

@@ -287,3 +287,22 @@ def test_attn_varlen_zero_wait_budget(monkeypatch):
     got = _run(inp, cu, cu, True)
     for k in want:
         assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("lens,heads,kv", [
+    ([600], 4, 2),            # two CTAs a key tile
+    ([1000], 2, 1),           # four
+    ([1000], 8, 1),           # eight
+    ([130, 900, 5], 6, 1),    # parts that end inside a head; sequences with fewer iterations than CTAs
+])
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_attn_varlen_shared_key_tiles(lens, heads, kv, d):
+    # few key tiles with many queries each: clusters of CTAs share a tile and join their sums
+    cu = _cu(lens)
+    inp = _inputs(sum(lens), sum(lens), heads, kv, d, seed=23400 + heads + d)
+    for causal in (True, False):
+        got = _run(inp, cu, cu, causal)
+        _check(got, inp, cu, cu, causal)
+        again = _run(inp, cu, cu, causal)
+        for k in got:
+            assert torch.equal(got[k], again[k]), k
