@@ -12,8 +12,8 @@
 // of fp32 dQ per pair of tiles leave through it, against 64 KB a tile of K or Q loads for each here.)
 //
 // dQ kernel: CTA = (sequence, query head, 128 queries). Per key tile S = Q K^T, dP = dO V^T and
-//   dQ += dS K with dS (bf16) read from tensor memory. S has two buffers, so S(j+1) and dP(j+1) run while
-//   the softmax warps are at tile j. The CTA first computes its rows' delta and leaves it for the
+//   dQ += dS K with dS (bf16) read from tensor memory. S has two buffers and is computed two tiles ahead,
+//   so the softmax warps go from dS(j) to S(j+1) at once. The CTA first computes its rows' delta and leaves it for the
 //   other kernel. Where a single key tile holds all that the rows see, delta is summed as P dP instead,
 //   which is the same without O's rounding to bf16: rows of few keys sit there, whose O is large and whose
 //   dP - delta cancels most (two keys, D = 128: dQ's error 8.0e-3 of its norm from O, 2.6e-3 from P dP).
@@ -22,8 +22,8 @@
 //   dP^T = V dO^T, one key per TMEM lane: P^T and dS^T are then A operands in tensor memory as they
 //   stand, dV += P^T dO and dK += dS^T Q, and dO and Q serve as loaded (MN-major). At D = 128 the four
 //   accumulators take all 512 columns: P^T lies over S^T, so S(i+1) follows dV(i), and the products of one
-//   half of the softmax (dV, S) run while the warps are at the other half (dK, dP). At D <= 96 P^T has
-//   columns of its own, and S(i+1) runs as soon as the warps have S(i) in registers.
+//   half of the softmax (dV, S) run while the warps are at the other half (dK, dP). At D <= 96 there is room
+//   for a second S^T or for P^T beside it: S^T runs ahead and the warps never wait for it.
 //   Where whole key tiles would balance badly (few of them, many queries each), a cluster of two to eight CTAs
 //   shares one: each takes a part of its (head, query tile) pairs, and the fp32 sums are joined through
 //   distributed shared memory in rank order.
@@ -53,7 +53,7 @@ struct AvDqCfg {
     using T = AvTile<D>;
     static constexpr int KST = D == 128 ? 3 : 4;  // a K tile serves S(j) and, later, dQ(j)
     static constexpr int VST = D == 64 ? 4 : D == 96 ? 3 : 2;
-    static constexpr int NUM_BARS = 2 + 2 * KST + 2 * VST + 2 + 6 + 1;
+    static constexpr int NUM_BARS = 2 + 2 * KST + 2 * VST + 2 + 4 + 1;
     static constexpr size_t SMEM = 1024 + (2 + KST + VST) * size_t(T::BYTES) + 2 * AV_TILE * 4 + 8 * NUM_BARS + 16;
     static_assert(SMEM <= SMEM_LIMIT, "shared memory per block");
     static constexpr uint32_t TMEM_COLS = 512;  // S(even), S(odd) at 0, 128; dP at 256; dQ at 384
@@ -85,11 +85,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     uint64_t* v_empty = v_full + VST;
     uint64_t* s_full = v_empty + VST;  // [2]
     uint64_t* dp_full = s_full + 2;
-    uint64_t* dp_read = dp_full + 1;   // the softmax warps have dP(j) in registers
-    // dS(j) is in tensor memory: one barrier for even and one for odd j, since a warp may be done with
-    // dS(j+1) (its dP(j+1) waits for dP(j) to be read only) while another still writes dS(j)
-    uint64_t* ds_full = dp_read + 1;   // [2]
-    uint64_t* dq_full = ds_full + 2;
+    uint64_t* ds_full = dp_full + 1;   // dS(j) is in tensor memory
+    uint64_t* dq_full = ds_full + 1;
     uint64_t* part_full = dq_full + 1; // both halves of delta from one key tile
     uint64_t* drain_bar = part_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
@@ -125,9 +122,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
         mbar_init(dp_full, 1);
-        mbar_init(dp_read, 8);
-        mbar_init(&ds_full[0], 8);
-        mbar_init(&ds_full[1], 8);
+        mbar_init(ds_full, 8);
         mbar_init(dq_full, 1);
         mbar_init(part_full, 8);
         mbar_init(drain_bar, 1);
@@ -213,18 +208,19 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     dp_mma(0);
                 }
             }
-            for (int j = 0; j < n && ok; ++j) {
-                if (j + 1 < n) {
-                    // S(j+1) overwrites dS(j-1), whose product was issued before it.
-                    if (!(ok = k_wait(j + 1))) break;
-                    tc_fence_after();
-                    s_mma(j + 1);
-                    if (!(ok = wait_all(&v_full[(j + 1) % VST], ((j + 1) / VST) & 1) && wait_all(dp_read, j & 1))) break;
-                    tc_fence_after();
-                    dp_mma(j + 1);
-                }
-                if (!(ok = wait_all(&ds_full[j & 1], (j >> 1) & 1))) break;
+            // One wait on the softmax an iteration, and three products behind it: dP(j+1), which it needs next,
+            // dQ(j), and S(j+2) over dS(j) once that has been used. (With a wait before each of the products the
+            // tensor core ran dry at every one: 2140 cycles an iteration at D = 128, 1536 of them products.)
+            if (ok && n > 1 && (ok = k_wait(1))) {
                 tc_fence_after();
+                s_mma(1);
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const bool more = j + 1 < n;
+                if (more && !(ok = wait_all(&v_full[(j + 1) % VST], ((j + 1) / VST) & 1))) break;
+                if (!(ok = wait_all(ds_full, j & 1))) break;
+                tc_fence_after();
+                if (more) dp_mma(j + 1);
                 const uint64_t kd = kt_desc + static_cast<uint32_t>(((j % KST) * T::BYTES) >> 4);
                 const uint32_t acc0 = j > 0 ? 1u : 0u;
 #pragma unroll
@@ -232,6 +228,11 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     umma_bf16_ts_elect(tmem_base + 384, av_a_step(tmem_base + (j & 1) * 128, k), kd + ((k * 1024) >> 4),
                                        IDESC_DQ, k > 0 ? 1u : acc0);
                 umma_commit_elect(&k_empty[j % KST]);
+                if (j + 2 < n) {
+                    if (!(ok = k_wait(j + 2))) break;
+                    tc_fence_after();
+                    s_mma(j + 2);
+                }
             }
             if (ok) umma_commit_elect(dq_full);
             umma_commit_elect(drain_bar);
@@ -307,9 +308,6 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             tmem_wait_ld();
             reg_fence32(t[0]);
             reg_fence32(t[1]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dp_read);
             uint32_t w[32];
             const int lim = see - j * AV_TILE - hf * 64;  // visible columns of this thread
             if (one_tile) {
@@ -349,7 +347,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_full[j & 1]);
+            if (lane == 0) mbar_arrive(ds_full);
         }
         if (ok && row_ok && hf == 0) delta[at] = dl;
         if (ok && rows_ok > 0) {
@@ -389,26 +387,33 @@ struct AvDkvCfg {
     static constexpr int QST = D == 128 ? 3 : 4;  // a Q tile serves S(i) and, later, dK(i)
     static constexpr int OST = D == 64 ? 4 : D == 96 ? 3 : 2;  // dO: dP(i), then dV(i)
     static constexpr int SST = 2;                 // row statistics
-    static constexpr int NUM_BARS = 1 + 2 * QST + 2 * OST + 2 * SST + 7 + 1;
+    static constexpr int NUM_BARS = 1 + 2 * QST + 2 * OST + 2 * SST + 8 + 1;
     // 512-byte alignment is what the 64-byte swizzle needs; at D = 128 no more fits
     static constexpr size_t SMEM = 512 + (2 + QST + OST) * size_t(T::BYTES) + SST * 2 * AV_TILE * 4 + 8 * NUM_BARS + 16;
     static_assert(SMEM <= SMEM_LIMIT, "shared memory per block");
-    // S^T at 0, dP^T at 128, dV at 256, dK behind it; P^T over S^T or, where it fits, at 448
+    // Columns of tensor memory, all 512 of them: S^T (twice at D = 64), dP^T, dV, dK; P^T over its S^T or, at
+    // D = 96, beside it; dS^T over dP^T or, at D = 64, beside P^T in the S^T that both come from
     static constexpr uint32_t TMEM_COLS = 512;
-    static constexpr uint32_t DK_COL = 256 + D;
-    static constexpr bool OWN_P = D <= 96;
+    static constexpr int S_BUFS = D == 64 ? 2 : 1;
+    static constexpr bool OWN_P = D == 96;
+    static constexpr bool BATCH = D <= 96;  // S^T(i+1) does not wait for P^T(i)
+    static constexpr uint32_t DP_COL = 128 * S_BUFS;
+    static constexpr uint32_t DV_COL = DP_COL + 128;
+    static constexpr uint32_t DK_COL = DV_COL + D;
     // columns from one warpgroup's 16-bit values to the other's (64 of each): packed, or in each half of S^T
     static constexpr uint32_t P_COL = OWN_P ? 448 : 0;
     static constexpr uint32_t P_HALF = OWN_P ? 32 : 64;
+    static constexpr bool DS_IN_S = S_BUFS == 2;
 };
 
-template <int D>
+template <int D, bool JOIN>
 __global__ void __launch_bounds__(AV_THREADS, 1)
     attn_varlen_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                            const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
                            const float* LSE, const float* delta, __nv_bfloat16* dK, long long lddk, __nv_bfloat16* dV,
-                           long long lddv, int cluster, const AvArgs args) {
+                           long long lddv, int cluster_size, const AvArgs args) {
+    const int cluster = JOIN ? cluster_size : 1;
     using Cfg = AvDkvCfg<D>;
     using T = AvTile<D>;
     constexpr int NB = T::NB, QST = Cfg::QST, OST = Cfg::OST, SST = Cfg::SST;
@@ -427,12 +432,12 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     uint64_t* do_empty = do_full + OST;
     uint64_t* st_full = do_empty + OST;
     uint64_t* st_empty = st_full + SST;
-    uint64_t* s_full = st_empty + SST;
-    uint64_t* dp_full = s_full + 1;
+    uint64_t* s_full = st_empty + SST;  // [2]: one per buffer of S^T
+    uint64_t* dp_full = s_full + 2;
     uint64_t* p_full = dp_full + 1;
     uint64_t* ds_full = p_full + 1;
     uint64_t* fin_full = ds_full + 1;
-    uint64_t* s_read = fin_full + 1;   // OWN_P: the softmax warps have S^T(i) in registers
+    uint64_t* s_read = fin_full + 1;   // one S^T buffer, BATCH: the softmax warps have S^T(i) in registers
     uint64_t* dv_done = s_read + 1;    // OWN_P: P^T(i) has been used
     uint64_t* drain_bar = dv_done + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int lane = threadIdx.x & 31;
     const int per_tile = args.nseq * args.kv_heads;
     const int item = static_cast<int>(blockIdx.x) / cluster;
-    const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int rank = JOIN ? static_cast<int>(cluster_ctarank()) : 0;
     const int kt = item / per_tile;  // the first keys have the most queries (causal)
     const int rem = item % per_tile;
     const int seq = rem / args.kv_heads;
@@ -490,7 +495,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             mbar_init(&st_full[i], 1);
             mbar_init(&st_empty[i], 8);
         }
-        mbar_init(s_full, 1);
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
         mbar_init(dp_full, 1);
         mbar_init(p_full, 8);
         mbar_init(ds_full, 8);
@@ -577,18 +583,25 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 }
                 return true;
             };
+            auto s_buf = [&](int it) { return Cfg::S_BUFS == 2 ? (it & 1) : 0; };
             auto s_mma = [&](int it) {
-                score(tmem_base, k_desc, q_desc + q_off(it));
-                umma_commit_elect(s_full);
+                score(tmem_base + s_buf(it) * 128, k_desc, q_desc + q_off(it));
+                umma_commit_elect(&s_full[s_buf(it)]);
             };
             auto dp_mma = [&](int it) {
-                score(tmem_base + 128, v_desc, do_desc + do_off(it));
+                score(tmem_base + Cfg::DP_COL, v_desc, do_desc + do_off(it));
                 umma_commit_elect(dp_full);
             };
-            auto dv_mma = [&](int it) {
-                grad(tmem_base + 256, tmem_base + Cfg::P_COL, Cfg::P_HALF, dot_desc + do_off(it), it == 0);
+            auto dv_mma = [&](int it) {  // dV += P^T dO
+                grad(tmem_base + Cfg::DV_COL, tmem_base + (Cfg::OWN_P ? Cfg::P_COL : s_buf(it) * 128), Cfg::P_HALF,
+                     dot_desc + do_off(it), it == 0);
                 umma_commit_elect(&do_empty[it % OST]);
                 if (Cfg::OWN_P) umma_commit_elect(dv_done);
+            };
+            auto dk_mma = [&](int it) {  // dK += dS^T Q
+                grad(tmem_base + Cfg::DK_COL, tmem_base + (Cfg::DS_IN_S ? s_buf(it) * 128 + 32 : Cfg::DP_COL), 64,
+                     qt_desc + q_off(it), it == 0);
+                umma_commit_elect(&q_empty[it % QST]);
             };
             bool ok = n > 0 && wait_all(kv_full, 0) && tiles_wait(0);
             if (ok) {
@@ -596,28 +609,44 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 s_mma(0);
                 dp_mma(0);
             }
-            for (int it = 0; it < n && ok; ++it) {
-                // The next tiles are waited for (and a tail cleared) before this iteration's softmax is, so
-                // that nothing lies between the products that follow it.
-                const bool more = it + 1 < n;
-                if (more) {
+            if constexpr (Cfg::BATCH) {
+                // One wait on the softmax an iteration, and all its products behind it, dP^T (which the softmax
+                // needs next) as soon as its columns are free; S^T runs two iterations ahead.
+                auto s_ahead = [&](int it) -> bool {  // S^T(it): over P^T(it-2), or once S^T(it-1) has been read
                     ahead.next();
-                    if (!(ok = tiles_wait(it + 1))) break;
-                }
-                if (Cfg::OWN_P && more) {
-                    if (!(ok = wait_all(s_read, it & 1))) break;
+                    if (!tiles_wait(it) || (Cfg::S_BUFS == 1 && !wait_all(s_read, (it - 1) & 1))) return false;
                     tc_fence_after();
-                    s_mma(it + 1);
+                    s_mma(it);
+                    return true;
+                };
+                if (ok && n > 1) ok = s_ahead(1);
+                for (int it = 0; it < n && ok; ++it) {
+                    if (!(ok = wait_all(ds_full, it & 1))) break;
+                    tc_fence_after();
+                    if (!Cfg::DS_IN_S) dk_mma(it);
+                    if (it + 1 < n) dp_mma(it + 1);
+                    dv_mma(it);
+                    if (Cfg::DS_IN_S) dk_mma(it);
+                    if (it + 2 < n) ok = s_ahead(it + 2);
                 }
-                if (!(ok = wait_all(p_full, it & 1))) break;
-                tc_fence_after();
-                dv_mma(it);                           // dV += P^T dO
-                if (!Cfg::OWN_P && more) s_mma(it + 1);  // over P^T(i), whose product was issued before it
-                if (!(ok = wait_all(ds_full, it & 1))) break;
-                tc_fence_after();
-                grad(tmem_base + Cfg::DK_COL, tmem_base + 128, 64, qt_desc + q_off(it), it == 0);  // dK += dS^T Q
-                umma_commit_elect(&q_empty[it % QST]);
-                if (more) dp_mma(it + 1);
+            } else {
+                for (int it = 0; it < n && ok; ++it) {
+                    // The next tiles are waited for (and a tail cleared) before this iteration's softmax is, so
+                    // that nothing lies between the products that follow it.
+                    const bool more = it + 1 < n;
+                    if (more) {
+                        ahead.next();
+                        if (!(ok = tiles_wait(it + 1))) break;
+                    }
+                    if (!(ok = wait_all(p_full, it & 1))) break;
+                    tc_fence_after();
+                    dv_mma(it);
+                    if (more) s_mma(it + 1);  // over P^T(i), whose product was issued before it
+                    if (!(ok = wait_all(ds_full, it & 1))) break;
+                    tc_fence_after();
+                    dk_mma(it);
+                    if (more) dp_mma(it + 1);
+                }
             }
             if (ok) umma_commit_elect(fin_full);
             umma_commit_elect(drain_bar);
@@ -665,10 +694,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         const int w0 = j0 + q * 32;   // first key of this warp, in its sequence
         const int rows_ok = min(32, sp.nk - w0);
         const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
-        const uint32_t s_addr = tmem_base + lane_addr + hf * 64;
-        const uint32_t dp_addr = s_addr + 128;
+        const uint32_t dp_addr = tmem_base + lane_addr + Cfg::DP_COL + hf * 64;
         const float2 c2v = make_float2(args.scale_log2, args.scale_log2);
-        const uint32_t p_addr = tmem_base + lane_addr + Cfg::P_COL + hf * Cfg::P_HALF;
         Walk at = first;
         bool ok = true;
         for (int it = 0; it < n && ok; ++it) {
@@ -676,7 +703,13 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             // this thread's columns 8 i + 2 (lane % 4), + 1 of its warps' half of the tile
             const float2* nl = reinterpret_cast<const float2*>(stats + st * 2 * AV_TILE + hf * 64) + (lane & 3);
             const float2* nd = nl + AV_TILE / 2;
-            if (!(ok = wait_all(&st_full[st], (it / SST) & 1) && wait_all(s_full, it & 1))) break;
+            const int sb = Cfg::S_BUFS == 2 ? (it & 1) : 0;
+            const uint32_t s_addr = tmem_base + lane_addr + sb * 128 + hf * 64;
+            const uint32_t p_addr = Cfg::OWN_P ? tmem_base + lane_addr + Cfg::P_COL + hf * Cfg::P_HALF : s_addr;
+            const uint32_t ds_addr = Cfg::DS_IN_S ? s_addr + 32 : dp_addr;
+            if (!(ok = wait_all(&st_full[st], (it / SST) & 1) &&
+                       wait_all(&s_full[sb], (Cfg::S_BUFS == 2 ? it >> 1 : it) & 1)))
+                break;
             tc_fence_after();
             // 32 keys x 64 queries of the warp as two fragments of 16 keys: keys f * 16 + e * 8 + lane / 4
             uint32_t p[2][32], w[2][16];
@@ -688,7 +721,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             tmem_wait_ld();
             reg_fence32(p[0]);
             reg_fence32(p[1]);
-            if (Cfg::OWN_P) {
+            if (Cfg::BATCH && Cfg::S_BUFS == 1) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_read);
@@ -722,10 +755,12 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             if (Cfg::OWN_P && it > 0 && !(ok = wait_all(dv_done, (it - 1) & 1))) break;
             tmem_st_frag32(p_addr, w[0]);
             tmem_st_frag32(p_addr + (16u << 16), w[1]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
+            if (!Cfg::BATCH) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) row[i] = nd[i * 4];
             if (!(ok = wait_all(dp_full, it & 1))) break;
@@ -746,8 +781,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     const float2 ds = mul2(pr, add2(dp, row[i]));
                     w[f][2 * i + e] = pack_bf16x2(ds.x, ds.y);
                 }
-            tmem_st_frag32(dp_addr, w[0]);
-            tmem_st_frag32(dp_addr + (16u << 16), w[1]);
+            tmem_st_frag32(ds_addr, w[0]);
+            tmem_st_frag32(ds_addr + (16u << 16), w[1]);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -759,28 +794,29 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         }
         __nv_bfloat16* out = hf ? dK : dV;
         const long long ld = hf ? lddk : lddv;
-        if (ok && cluster == 1 && rows_ok > 0) {
+        if (!JOIN && ok && rows_ok > 0) {
             // warps 4..7 write dV, warps 8..11 dK; K's and V's tiles are free for the staging
             if (n == 0) {
                 av_store_zero_rows(0, NB, kvh * D, sp.k0 + w0, out, ld, rows_ok, lane);
             } else if (wait_all(fin_full, 0)) {
                 tc_fence_after();
-                av_store_rows(tmem_base + lane_addr + (hf ? Cfg::DK_COL : 256), hf ? args.scale : 1.0f, 0, NB,
+                av_store_rows(tmem_base + lane_addr + (hf ? Cfg::DK_COL : Cfg::DV_COL), hf ? args.scale : 1.0f, 0, NB,
                               (hf ? sK : sV) + q * (NB * 2048), hf ? &tmdK : &tmdV, kvh * D, sp.k0 + w0, out, ld,
                               rows_ok, lane);
             }
-        } else if (ok && n > 0) {
-            ok = wait_all(fin_full, 0);
-            tc_fence_after();
         }
-        if (cluster > 1) {
+        if constexpr (JOIN) {
+            if (ok && n > 0) {
+                ok = wait_all(fin_full, 0);
+                tc_fence_after();
+            }
             // Chunk c (32 columns) of dV or dK is finished by rank (hf NB + c) % cluster. The others send it
             // their rows, eight pieces of 16 bytes a row, into the ring of Q and dO tiles:
             // [source rank][chunk of the owner][piece][128 keys].
             constexpr int CHUNK = 8 * AV_TILE;
             const int owned = (2 * NB + cluster - 1) / cluster;
             float4* recv = reinterpret_cast<float4*>(sQ);
-            const uint32_t acc = tmem_base + lane_addr + (hf ? Cfg::DK_COL : 256);
+            const uint32_t acc = tmem_base + lane_addr + (hf ? Cfg::DK_COL : Cfg::DV_COL);
             __syncwarp();
             cluster_sync_all();  // every CTA of the cluster has used its ring
             for (int c = 0; c < NB && ok && n > 0; ++c) {
@@ -835,7 +871,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             }
         }
     }
-    if (cluster > 1 && warp < 4) {
+    if (JOIN && warp < 4) {
         // (the softmax warps' two barriers)
         __syncwarp();
         cluster_sync_all();
@@ -878,7 +914,7 @@ static int dkv_cluster(const AvArgs& a, int sms) {
         const double even = (total + tiles * a.kv_heads * c * extra[i]) / (sms * usable[i]);
         const double part = longest / c + extra[i];
         const double est = even > part ? even : part;
-        if (i == 0 || est < 0.95 * least) {
+        if (i == 0 || est < 0.9 * least) {
             best = c;
             least = est;
         }
@@ -903,9 +939,10 @@ static cudaError_t launch_bwd(const AvBwdMaps& m, const mp_bf16* O, long long ld
                       static_cast<const __nv_bfloat16*>(bf(dO)), lddo, LSE, delta, bf(dQ), lddq, qtiles, a);
     if (e == cudaSuccess && ktiles > 0) {
         const int cluster = dkv_cluster(a, sms);
-        e = av_launch(attn_varlen_dkv_kernel<D>, static_cast<long long>(ktiles) * a.nseq * a.kv_heads * cluster, cluster,
-                      AvDkvCfg<D>::SMEM, s, m.q, m.k, m.v, m.d_o, m.dk, m.dv, LSE, static_cast<const float*>(delta),
-                      bf(dK), lddk, bf(dV), lddv, cluster, a);
+        auto kern = cluster > 1 ? attn_varlen_dkv_kernel<D, true> : attn_varlen_dkv_kernel<D, false>;
+        e = av_launch(kern, static_cast<long long>(ktiles) * a.nseq * a.kv_heads * cluster, cluster, AvDkvCfg<D>::SMEM, s,
+                      m.q, m.k, m.v, m.d_o, m.dk, m.dv, LSE, static_cast<const float*>(delta), bf(dK), lddk, bf(dV),
+                      lddv, cluster, a);
     }
     return e;
 }
