@@ -112,15 +112,13 @@ extern "C" mp_status mp_glu_bwd(const mp_bf16* X, const mp_bf16* W, const mp_bf1
     // dY = dZ Wd^T; dG, dU in its epilogue.
     TmapSet m3{};
     if (!make_tmap_bf16(&m3.a, dZ, h, T, h, 64, BM) || !make_tmap_bf16(&m3.b, Wd, h, f, h, 64, 128) ||
-        !make_tmap_bf16_out(&m3.o0, dGU_ws, f, T, f2) || !make_tmap_bf16_out(&m3.o1, dGU_ws + f, f, T, f2))
+        !make_tmap_bf16_out(&m3.o0, dGU_ws, f, T, f2) || !make_tmap_bf16_out(&m3.o1, dGU_ws + f, f, T, f2) ||
+        !make_tmap_bf16_out(&m3.x0, GU, f, T, f2) || !make_tmap_bf16_out(&m3.x1, GU + f, f, T, f2))
         return MP_ERR_CUDA;
     GemmArgs a3 = launch_args(d_status);
     a3.pr = problem(T, f, 256, 0, h / BK, false, false, Tb * h, 2.0 * f * h);
-    a3.aux = reinterpret_cast<const __nv_bfloat16*>(GU);
-    a3.ld_aux = static_cast<long long>(f2);
     a3.act = act;
-    a3.glu_f = f;
-    if (launch_gelu_epi<EPI_DGLU>(m3, a3, sms, s) != cudaSuccess) return MP_ERR_CUDA;
+    if (launch_gemm_tc<256, EPI_DGLU, 4>(m3, a3, sms, s) != cudaSuccess) return MP_ERR_CUDA;
 
     // dX = dGU W^T: gate blocks, then up blocks, shards ascending in each (the f sum).
     TmapSet m4{};
