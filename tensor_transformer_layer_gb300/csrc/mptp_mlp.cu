@@ -153,7 +153,7 @@ extern "C" mp_status mp_mlp_bwd_shards(const mp_bf16* X, const mp_bf16* A, const
     a6.pr.a_mn = a6f;
     a6.pr.b_mn = b6f;
 
-    return launch_grad_gemms(m4, a4, A, f, m5, a5, m6, a6, sms, s);
+    return launch_grad_gemms(m4, a4, K4_BN, A, f, m5, a5, m6, a6, sms, s);
 }
 
 extern "C" mp_status mp_mlp_bwd(const mp_bf16* X, const mp_bf16* A, const mp_bf16* B, const mp_bf16* U,

@@ -111,10 +111,16 @@ inline GemmArgs launch_args(uint32_t* status) {
     return a;
 }
 
+// K4 with tiles of `bn` columns (224 or 256; outputs do not depend on it).
+inline cudaError_t launch_k4(int bn, const TmapSet& m, const GemmArgs& a, int sms, cudaStream_t s, int max_pairs = 0) {
+    return bn == K4_BN ? launch_gemm_tc<K4_BN, EPI_STORE, 4>(m, a, sms, s, max_pairs)
+                       : launch_gemm_tc<256, EPI_STORE, 4>(m, a, sms, s, max_pairs);
+}
+
 // dX, dA and dB of a block's backward (K4, K5a, K5b): one after another, or side by side on
-// disjoint CTA pairs. m4 / a4 hold K4 with K4_BN-wide tiles over the K-major weight W [h, ldw], whose
-// operand map is rebuilt for 256-wide tiles where K4 runs split.
-inline mp_status launch_grad_gemms(TmapSet& m4, GemmArgs& a4, const mp_bf16* W, int ldw, const TmapSet& m5,
+// disjoint CTA pairs. m4 / a4 hold K4 with bn4-wide tiles (K4_BN or 256) over the K-major weight
+// W [h, ldw], whose operand map is rebuilt for 256-wide tiles where K4 runs split.
+inline mp_status launch_grad_gemms(TmapSet& m4, GemmArgs& a4, int bn4, const mp_bf16* W, int ldw, const TmapSet& m5,
                                    const GemmArgs& a5, const TmapSet& m6, const GemmArgs& a6, int sms,
                                    cudaStream_t s) {
     const int h = a4.pr.N;
@@ -139,7 +145,7 @@ inline mp_status launch_grad_gemms(TmapSet& m4, GemmArgs& a4, const mp_bf16* W, 
                       cudaStreamWaitEvent(ss->s[0], ss->fork, 0) == cudaSuccess &&
                       cudaStreamWaitEvent(ss->s[1], ss->fork, 0) == cudaSuccess;
             if (!ok) return MP_ERR_CUDA;
-            ok = launch_gemm_tc<K4_BN, EPI_STORE, 4>(m4, a4, sms, s, split[0]) == cudaSuccess;
+            ok = launch_k4(bn4, m4, a4, sms, s, split[0]) == cudaSuccess;
             ok = launch_gemm_tc<256, EPI_STORE, 4>(m5, a5, sms, ss->s[0], split[1]) == cudaSuccess && ok;
             ok = launch_gemm_tc<256, EPI_STORE, 4>(m6, a6, sms, ss->s[1], split[2]) == cudaSuccess && ok;
             // Join even after a failed launch, so the caller's stream never runs ahead of the side streams.
@@ -149,14 +155,14 @@ inline mp_status launch_grad_gemms(TmapSet& m4, GemmArgs& a4, const mp_bf16* W, 
             return ok ? MP_OK : MP_ERR_CUDA;
         }
     }
-    const bool split4 = use_split<K4_BN>(a4.pr.M, h, a4.pr.kb_end - a4.pr.kb_begin, sms);
+    const int L4 = a4.pr.kb_end - a4.pr.kb_begin;
+    const bool split4 = bn4 == K4_BN ? use_split<K4_BN>(a4.pr.M, h, L4, sms) : use_split<256>(a4.pr.M, h, L4, sms);
     if (split4) {
         // The split kernel's 256-wide tiles: B boxes of 128 rows per CTA.
         if (!make_tmap_bf16(&m4.b, W, ldw, h, ldw, 64, 128)) return MP_ERR_CUDA;
         a4.pr.num_units = a4.pr.num_m_blocks * ceil_div(h, 256);
     }
-    if ((split4 ? launch_gemm_split<256, SPLIT_PAIRS>(m4, a4, sms, s) : launch_gemm_tc<K4_BN, EPI_STORE, 4>(m4, a4, sms, s)) !=
-            cudaSuccess ||
+    if ((split4 ? launch_gemm_split<256, SPLIT_PAIRS>(m4, a4, sms, s) : launch_k4(bn4, m4, a4, sms, s)) != cudaSuccess ||
         launch_gemm_tc<256, EPI_STORE, 4>(m5, a5, sms, s) != cudaSuccess ||
         launch_gemm_tc<256, EPI_STORE, 4>(m6, a6, sms, s) != cudaSuccess)
         return MP_ERR_CUDA;
