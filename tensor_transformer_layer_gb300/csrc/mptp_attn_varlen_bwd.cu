@@ -248,28 +248,49 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         const int rows_ok = min(32, sp.nq - w0);
         const bool row_ok = lane < rows_ok;
         const long long row = sp.q0 + qi;
-        // delta: each half of the warps sums half of the row's columns (or, in the loop, of its keys)
+        // delta: each warp sums 16 rows, whole rows side by side (16 bytes a lane). Row by row, a row to a thread,
+        // the loads took 8000 cycles at D = 96: the shared memory leaves no cache to hold the lines for the next
+        // piece. With one key tile the loop sums it instead.
         const bool one_tile = n == 1;
         float dl = 0.0f;
         if (!one_tile) {
-            float sum = 0.0f;
-            if (row_ok) {
-                const uint4* po = reinterpret_cast<const uint4*>(O + row * ldo + head * D + hf * (D / 2));
-                const uint4* pd = reinterpret_cast<const uint4*>(dO + row * lddo + head * D + hf * (D / 2));
+            constexpr int LANES = D / 8, ROWS = 32 / LANES;  // lanes a row, rows a load
+            const int r = lane / LANES;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint4 a = po[i], b = pd[i];
-                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+            for (int i = 0; i < 16; i += 4 * ROWS) {
+                uint4 a[4], b[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int m = (warp - 4) * 16 + i + u * ROWS + r;
+                    a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < ROWS && i + u * ROWS + r < 16 && i0 + m < sp.nq) {
+                        const long long at = sp.q0 + i0 + m;
+                        const int c = head * D + lane % LANES * 8;
+                        a[u] = *reinterpret_cast<const uint4*>(O + at * ldo + c);
+                        b[u] = *reinterpret_cast<const uint4*>(dO + at * lddo + c);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+                    float sum = 0.0f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         sum = fmaf(bf16_lo(aw[k]), bf16_lo(bw[k]), sum);
                         sum = fmaf(bf16_hi(aw[k]), bf16_hi(bw[k]), sum);
                     }
+                    // the row's lanes, in a fixed order: its first lane ends with the sum
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) {
+                        const float v = __shfl_down_sync(0xffffffffu, sum, o);
+                        if (lane % LANES + o < LANES) sum += v;
+                    }
+                    if (r < ROWS && lane % LANES == 0 && i + u * ROWS + r < 16)
+                        part[(warp - 4) * 16 + i + u * ROWS + r] = sum;
                 }
             }
-            part[hf * AV_TILE + q * 32 + lane] = sum;
             softmax_warps_sync();  // no warp has left: there was no wait before it
-            dl = part[q * 32 + lane] + part[AV_TILE + q * 32 + lane];
+            dl = part[q * 32 + lane];
         }
         const long long at = static_cast<long long>(head) * args.Tq + row;
         const float lse2 = row_ok ? lse_to_log2(LSE[at]) : INFINITY;
