@@ -56,13 +56,13 @@ __device__ __forceinline__ bool av_span(const AvArgs& a, int seq, AvSpan& s) {
     return true;
 }
 
-// One tile (rows from `row`, D columns from `col`) into shared memory, counted on `bar`.
+// One tile (rows from `row`, head `head` of the matrix) into shared memory, counted on `bar`: D/32 boxes by one
+// load.
 template <int D>
-__device__ __forceinline__ void av_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int col, int row) {
+__device__ __forceinline__ void av_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
     using C = AvTile<D>;
     mbar_arrive_expect_tx(bar, C::BYTES);
-#pragma unroll
-    for (int c = 0; c < C::NB; ++c) tma_load_2d(dst + c * C::BOX, map, bar, col + c * 32, row);
+    tma_load_3d(dst, map, bar, 0, row, head * C::NB);
 }
 
 // One warp clears rows [from, 128) of a tile in shared memory. A tile that reaches past its sequence
@@ -114,7 +114,7 @@ __device__ __forceinline__ void av_store_rows(uint32_t acc, float f, int c0, int
         if (lane == 0) {
             for (int c = c0; c < c1; ++c) tma_store_2d(map, stg + c * 2048, col + c * 32, row);
             bulk_commit_group();
-            bulk_wait_group<0>();  // written before the CTA exits
+            bulk_wait_group_read<0>();  // the staging is read before the CTA exits; the grid's end has it written
         }
         __syncwarp();
     }
@@ -144,8 +144,8 @@ __device__ __forceinline__ int av_key_tiles(const AvSpan& s, int i0, int causal)
 // writes its 64 columns' values, packed, over the first half of its own 64 fp32 columns.
 __device__ __forceinline__ uint32_t av_a_step(uint32_t base, int k) { return base + (k >> 2) * 64 + (k & 3) * 8; }
 
-inline bool av_tmap(CUtensorMap* m, const void* base, int cols, int rows, long long ld) {
-    return make_tmap_bf16_sw64(m, base, cols, rows, ld, 32, AV_TILE);
+inline bool av_tmap(CUtensorMap* m, const void* base, int cols, int rows, long long ld, int d) {
+    return make_tmap_bf16_sw64_3d(m, base, cols, rows, ld, AV_TILE, d / 32);
 }
 
 // Sizes, pitches and pointers that the forward and the backward refuse alike.

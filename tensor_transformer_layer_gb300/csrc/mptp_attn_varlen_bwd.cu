@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int rem = static_cast<int>(blockIdx.x) % per_tile;
     const int seq = rem / args.heads;
     const int head = rem % args.heads;
-    const int kv_col = head / args.group * D;
+    const int kvh = head / args.group;
 
     grid_dependency_wait();
     AvSpan sp;
@@ -107,6 +107,32 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int i0 = qt * AV_TILE;
     const int n = av_key_tiles(sp, i0, args.causal);
     const int k_tail = n * AV_TILE > sp.nk ? sp.nk - (n - 1) * AV_TILE : AV_TILE;
+
+    // The softmax warps' rows of LSE, O and dO are asked for before the set-up, which takes as long as they do.
+    // delta = rowsum(dO * O): each warp sums 16 rows, whole rows side by side, 16 bytes a lane. (Row by row, a row
+    // to a thread, they took 8000 cycles at D = 96: the shared memory leaves no cache to hold a line for the next
+    // piece.) With one key tile the loop sums delta instead.
+    const bool one_tile = n == 1;
+    constexpr int LANES = D / 8, ROWS = 32 / LANES, LOADS = 16 / ROWS;  // lanes a row, rows a load, loads a warp
+    uint4 o_part[LOADS], do_part[LOADS];
+    const long long row_at = static_cast<long long>(head) * args.Tq + sp.q0 + i0 + (warp & 3) * 32 + lane;
+    float lse = -INFINITY;
+    if (warp >= 4) {
+        if (i0 + (warp & 3) * 32 + lane < sp.nq) lse = LSE[row_at];
+        if (!one_tile) {
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) {
+                const int m = (warp - 4) * 16 + u * ROWS + lane / LANES;
+                o_part[u] = do_part[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (lane / LANES < ROWS && i0 + m < sp.nq) {
+                    const long long at = sp.q0 + i0 + m;
+                    const int c = head * D + lane % LANES * 8;
+                    o_part[u] = *reinterpret_cast<const uint4*>(O + at * ldo + c);
+                    do_part[u] = *reinterpret_cast<const uint4*>(dO + at * lddo + c);
+                }
+            }
+        }
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -130,10 +156,10 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         fence_mbarrier_init();
         fence_proxy_async_smem();
         if (n > 0) {
-            av_load<D>(sK, &tmK, &k_full[0], kv_col, sp.k0);
-            av_load<D>(sQ, &tmQ, q_full, head * D, sp.q0 + i0);
-            av_load<D>(sV, &tmV, &v_full[0], kv_col, sp.k0);
-            av_load<D>(sdO, &tmdO, do_full, head * D, sp.q0 + i0);
+            av_load<D>(sK, &tmK, &k_full[0], kvh, sp.k0);
+            av_load<D>(sQ, &tmQ, q_full, head, sp.q0 + i0);
+            av_load<D>(sV, &tmV, &v_full[0], kvh, sp.k0);
+            av_load<D>(sdO, &tmdO, do_full, head, sp.q0 + i0);
         }
     }
     if (warp == 1) {
@@ -161,11 +187,11 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     int st = j % KST;
                     ok = wait_bounded(&k_empty[st], ((j / KST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sK + st * T::BYTES, &tmK, &k_full[st], kv_col, sp.k0 + j * AV_TILE);
+                    av_load<D>(sK + st * T::BYTES, &tmK, &k_full[st], kvh, sp.k0 + j * AV_TILE);
                     st = j % VST;
                     ok = wait_bounded(&v_empty[st], ((j / VST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sV + st * T::BYTES, &tmV, &v_full[st], kv_col, sp.k0 + j * AV_TILE);
+                    av_load<D>(sV + st * T::BYTES, &tmV, &v_full[st], kvh, sp.k0 + j * AV_TILE);
                 }
             }
         } else if (warp == 1) {
@@ -247,53 +273,30 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         const int qi = w0 + lane;
         const int rows_ok = min(32, sp.nq - w0);
         const bool row_ok = lane < rows_ok;
-        const long long row = sp.q0 + qi;
-        // delta: each warp sums 16 rows, whole rows side by side (16 bytes a lane). Row by row, a row to a thread,
-        // the loads took 8000 cycles at D = 96: the shared memory leaves no cache to hold the lines for the next
-        // piece. With one key tile the loop sums it instead.
-        const bool one_tile = n == 1;
         float dl = 0.0f;
         if (!one_tile) {
-            constexpr int LANES = D / 8, ROWS = 32 / LANES;  // lanes a row, rows a load
-            const int r = lane / LANES;
 #pragma unroll
-            for (int i = 0; i < 16; i += 4 * ROWS) {
-                uint4 a[4], b[4];
+            for (int u = 0; u < LOADS; ++u) {
+                const uint32_t aw[4] = {o_part[u].x, o_part[u].y, o_part[u].z, o_part[u].w};
+                const uint32_t bw[4] = {do_part[u].x, do_part[u].y, do_part[u].z, do_part[u].w};
+                float sum = 0.0f;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int m = (warp - 4) * 16 + i + u * ROWS + r;
-                    a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < ROWS && i + u * ROWS + r < 16 && i0 + m < sp.nq) {
-                        const long long at = sp.q0 + i0 + m;
-                        const int c = head * D + lane % LANES * 8;
-                        a[u] = *reinterpret_cast<const uint4*>(O + at * ldo + c);
-                        b[u] = *reinterpret_cast<const uint4*>(dO + at * lddo + c);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    sum = fmaf(bf16_lo(aw[k]), bf16_lo(bw[k]), sum);
+                    sum = fmaf(bf16_hi(aw[k]), bf16_hi(bw[k]), sum);
                 }
+                // the row's lanes, in a fixed order: its first lane ends with the sum
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        sum = fmaf(bf16_lo(aw[k]), bf16_lo(bw[k]), sum);
-                        sum = fmaf(bf16_hi(aw[k]), bf16_hi(bw[k]), sum);
-                    }
-                    // the row's lanes, in a fixed order: its first lane ends with the sum
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) {
-                        const float v = __shfl_down_sync(0xffffffffu, sum, o);
-                        if (lane % LANES + o < LANES) sum += v;
-                    }
-                    if (r < ROWS && lane % LANES == 0 && i + u * ROWS + r < 16)
-                        part[(warp - 4) * 16 + i + u * ROWS + r] = sum;
+                for (int o = 8; o > 0; o >>= 1) {
+                    const float v = __shfl_down_sync(0xffffffffu, sum, o);
+                    if (lane % LANES + o < LANES) sum += v;
                 }
+                if (lane / LANES < ROWS && lane % LANES == 0) part[(warp - 4) * 16 + u * ROWS + lane / LANES] = sum;
             }
             softmax_warps_sync();  // no warp has left: there was no wait before it
             dl = part[q * 32 + lane];
         }
-        const long long at = static_cast<long long>(head) * args.Tq + row;
-        const float lse2 = row_ok ? lse_to_log2(LSE[at]) : INFINITY;
+        const float lse2 = lse_to_log2(lse);
         const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
         const uint32_t s_addr = tmem_base + lane_addr + hf * 64;
         const uint32_t dp_addr = tmem_base + lane_addr + 256 + hf * 64;
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(ds_full);
         }
-        if (ok && row_ok && hf == 0) delta[at] = dl;
+        if (ok && row_ok && hf == 0) delta[row_at] = dl;
         if (ok && rows_ok > 0) {
             constexpr int HALF = (NB + 1) / 2;
             const int c0 = hf ? HALF : 0, c1 = hf ? NB : HALF;
@@ -502,6 +505,22 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     };
     const Walk first{kvh * args.group + (n > 0 ? it0 / per_head : 0), t0 + (n > 0 ? it0 % per_head : 0), t0, t1};
 
+    // Row statistics of a query tile, four rows a lane of warp 2; the first are asked for before the set-up.
+    constexpr int ST_ROWS = AV_TILE / 32;
+    float st_lse[ST_ROWS], st_delta[ST_ROWS];
+    Walk st_walk = first;
+    auto st_fetch = [&]() {
+        const int i0 = st_walk.tile * AV_TILE + lane;
+        const long long at = static_cast<long long>(st_walk.head) * args.Tq + sp.q0 + i0;
+#pragma unroll
+        for (int r = 0; r < ST_ROWS; ++r) {
+            const bool row_ok = i0 + r * 32 < sp.nq;
+            st_lse[r] = row_ok ? LSE[at + r * 32] : -INFINITY;
+            st_delta[r] = row_ok ? delta[at + r * 32] : 0.0f;
+        }
+    };
+    if (warp == 2 && n > 0) st_fetch();
+
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 2);
         for (int i = 0; i < QST; ++i) {
@@ -529,10 +548,10 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         fence_mbarrier_init();
         fence_proxy_async_smem();
         if (n > 0) {
-            av_load<D>(sK, &tmK, kv_full, kvh * D, sp.k0 + j0);
-            av_load<D>(sQ, &tmQ, &q_full[0], first.head * D, sp.q0 + first.tile * AV_TILE);
-            av_load<D>(sV, &tmV, kv_full, kvh * D, sp.k0 + j0);
-            av_load<D>(sdO, &tmdO, &do_full[0], first.head * D, sp.q0 + first.tile * AV_TILE);
+            av_load<D>(sK, &tmK, kv_full, kvh, sp.k0 + j0);
+            av_load<D>(sQ, &tmQ, &q_full[0], first.head, sp.q0 + first.tile * AV_TILE);
+            av_load<D>(sV, &tmV, kv_full, kvh, sp.k0 + j0);
+            av_load<D>(sdO, &tmdO, &do_full[0], first.head, sp.q0 + first.tile * AV_TILE);
         }
     }
     if (warp == 1) {
@@ -562,11 +581,11 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     int st = it % QST;
                     ok = wait_bounded(&q_empty[st], ((it / QST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sQ + st * T::BYTES, &tmQ, &q_full[st], w.head * D, sp.q0 + w.tile * AV_TILE);
+                    av_load<D>(sQ + st * T::BYTES, &tmQ, &q_full[st], w.head, sp.q0 + w.tile * AV_TILE);
                     st = it % OST;
                     ok = wait_bounded(&do_empty[st], ((it / OST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sdO + st * T::BYTES, &tmdO, &do_full[st], w.head * D, sp.q0 + w.tile * AV_TILE);
+                    av_load<D>(sdO + st * T::BYTES, &tmdO, &do_full[st], w.head, sp.q0 + w.tile * AV_TILE);
                 }
             }
         } else if (warp == 1) {
@@ -675,33 +694,19 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         } else if (warp == 2) {
             // ---------------- row statistics of each query tile ----------------
             // One iteration's values are in registers before the buffer of the one before last is free.
-            Walk w = first;
-            constexpr int PER = AV_TILE / 32;
-            float l[PER], dd[PER];
-            auto fetch = [&]() {
-                const int i0 = w.tile * AV_TILE + lane;
-                const long long at = static_cast<long long>(w.head) * args.Tq + sp.q0 + i0;
-#pragma unroll
-                for (int r = 0; r < PER; ++r) {
-                    const bool row_ok = i0 + r * 32 < sp.nq;
-                    l[r] = row_ok ? LSE[at + r * 32] : -INFINITY;
-                    dd[r] = row_ok ? delta[at + r * 32] : 0.0f;
-                }
-            };
-            if (n > 0) fetch();
             for (int it = 0; it < n; ++it) {
                 const int st = it % SST;
                 if (!wait_all(&st_empty[st], ((it / SST) & 1) ^ 1u)) break;
                 float* s = stats + st * 2 * AV_TILE + lane;
 #pragma unroll
-                for (int r = 0; r < PER; ++r) {
-                    s[r * 32] = -lse_to_log2(l[r]);
-                    s[AV_TILE + r * 32] = -dd[r];
+                for (int r = 0; r < ST_ROWS; ++r) {
+                    s[r * 32] = -lse_to_log2(st_lse[r]);
+                    s[AV_TILE + r * 32] = -st_delta[r];
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&st_full[st]);
-                w.next();
-                if (it + 1 < n) fetch();
+                st_walk.next();
+                if (it + 1 < n) st_fetch();
             }
         }
     } else {
@@ -1002,9 +1007,9 @@ extern "C" mp_status mp_attn_varlen_bwd(const mp_bf16* Q, const mp_bf16* K, cons
     AvBwdMaps m{};
     bool ok = true;
     if (Tq > 0)
-        ok = av_tmap(&m.q, Q, qc, Tq, ldq) && av_tmap(&m.d_o, dO, qc, Tq, lddo) && make_tmap_bf16_out(&m.dq, dQ, qc, Tq, lddq);
+        ok = av_tmap(&m.q, Q, qc, Tq, ldq, d) && av_tmap(&m.d_o, dO, qc, Tq, lddo, d) && make_tmap_bf16_out(&m.dq, dQ, qc, Tq, lddq);
     if (ok && Tk > 0)
-        ok = av_tmap(&m.k, K, kc, Tk, ldk) && av_tmap(&m.v, V, kc, Tk, ldv) && make_tmap_bf16_out(&m.dk, dK, kc, Tk, lddk) &&
+        ok = av_tmap(&m.k, K, kc, Tk, ldk, d) && av_tmap(&m.v, V, kc, Tk, ldv, d) && make_tmap_bf16_out(&m.dk, dK, kc, Tk, lddk) &&
              make_tmap_bf16_out(&m.dv, dV, kc, Tk, lddv);
     if (!ok) return MP_ERR_CUDA;
     if (Tq == 0) m.q = m.d_o = m.dq = m.k;

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int rem = static_cast<int>(blockIdx.x) % per_pair;
     const int seq = rem / args.heads;
     const int head = rem % args.heads;
-    const int kv_col = head / args.group * D;
+    const int kvh = head / args.group;
 
     grid_dependency_wait();  // the sequences' offsets, like the tensors, may come from the kernel before
     AvSpan sp;
@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         fence_mbarrier_init();
         fence_proxy_async_smem();
         // The first loads overlap the rest of the set-up.
-        if (n > 0) av_load<D>(sK, &tmK, &k_full[0], kv_col, sp.k0);
+        if (n > 0) av_load<D>(sK, &tmK, &k_full[0], kvh, sp.k0);
         for (int g = 0; g < 2; ++g)
-            if (nt[g] > 0) av_load<D>(sQ + g * T::BYTES, &tmQ, &q_full[g], head * D, sp.q0 + qt[g] * AV_TILE);
+            if (nt[g] > 0) av_load<D>(sQ + g * T::BYTES, &tmQ, &q_full[g], head, sp.q0 + qt[g] * AV_TILE);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                                 int stages) -> bool {
                     const int st = j % stages;
                     if (!wait_bounded(&empty[st], ((j / stages) & 1) ^ 1u, ctl)) return false;
-                    av_load<D>(ring + st * T::BYTES, map, &full[st], kv_col, sp.k0 + j * AV_TILE);
+                    av_load<D>(ring + st * T::BYTES, map, &full[st], kvh, sp.k0 + j * AV_TILE);
                     return true;
                 };
                 bool ok = true;
@@ -364,9 +364,9 @@ extern "C" mp_status mp_attn_varlen_fwd(const mp_bf16* Q, const mp_bf16* K, cons
 
     CUtensorMap tq, tk, tv, to;
     // Without keys the maps of K and V are never used: they take Q's.
-    if (!av_tmap(&tq, Q, static_cast<int>(qw), Tq, ldq) || !make_tmap_bf16_out(&to, O, qw, Tq, ldo) ||
-        !(Tk > 0 ? av_tmap(&tk, K, static_cast<int>(kw), Tk, ldk) && av_tmap(&tv, V, static_cast<int>(kw), Tk, ldv)
-                 : av_tmap(&tk, Q, static_cast<int>(qw), Tq, ldq) && av_tmap(&tv, Q, static_cast<int>(qw), Tq, ldq)))
+    if (!av_tmap(&tq, Q, static_cast<int>(qw), Tq, ldq, d) || !make_tmap_bf16_out(&to, O, qw, Tq, ldo) ||
+        !(Tk > 0 ? av_tmap(&tk, K, static_cast<int>(kw), Tk, ldk, d) && av_tmap(&tv, V, static_cast<int>(kw), Tk, ldv, d)
+                 : av_tmap(&tk, Q, static_cast<int>(qw), Tq, ldq, d) && av_tmap(&tv, Q, static_cast<int>(qw), Tq, ldq, d)))
         return MP_ERR_CUDA;
     const AvArgs a = av_args(cu_q, cu_k, nseq, Tq, Tk, max_q, max_k, heads, kv_heads, causal ? 1 : 0, scale, d_status);
     const int npairs = ceil_div(max_q, 2 * AV_TILE);

@@ -23,6 +23,11 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t
 bool make_tmap_bf16_sw64(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_elems,
                          uint32_t box_inner, uint32_t box_outer);
 
+// The same matrix as a 3-D map of 32-column blocks (64-byte swizzle), box of box_outer rows x `blocks` blocks:
+// one load brings a tile as consecutive 32-wide boxes. inner must be a multiple of 32.
+bool make_tmap_bf16_sw64_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_elems,
+                            uint32_t box_outer, uint32_t blocks);
+
 // Tensor map for an epilogue output: 32 x 32 boxes, 64-byte swizzle (the layout
 // the epilogue stages rows in before its TMA store).
 // MN-major operand [outer rows, inner columns] as a 3-D map of 64-column blocks (SW128), box of
