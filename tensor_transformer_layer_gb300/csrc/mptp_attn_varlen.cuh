@@ -140,6 +140,16 @@ __device__ __forceinline__ int av_key_tiles(const AvSpan& s, int i0, int causal)
     return keys > 0 ? (keys + AV_TILE - 1) / AV_TILE : 0;
 }
 
+// The tile of queries that a CTA at `level` of the grid takes (tiles of `rows` rows; negative: none). Larger work
+// first: where the mask is causal, later tiles see more keys. Sequences whose queries continue a prefix of their own
+// length are counted from their own ends, the others from the longest one's, so that tiles of the same number of
+// keys come together. (Four prompts of 33 to 1025 queries on 1024 to 2048 keys: the forward 38 us with the longest
+// one's end for all, 32 so; two clips of 3510 and 1755 queries would lose a seventh with their own ends.)
+__device__ __forceinline__ int av_query_tile(const AvArgs& a, const AvSpan& s, int rows, int ntiles, int level) {
+    const int n = a.causal && a.max_k > a.max_q ? (s.nq + rows - 1) / rows : ntiles;
+    return n - 1 - level;
+}
+
 // 16-bit A operand of a TMEM product: 16 rows' worth (8 columns) of step k. Each softmax warpgroup
 // writes its 64 columns' values, packed, over the first half of its own 64 fp32 columns.
 __device__ __forceinline__ uint32_t av_a_step(uint32_t base, int k) { return base + (k >> 2) * 64 + (k & 3) * 8; }

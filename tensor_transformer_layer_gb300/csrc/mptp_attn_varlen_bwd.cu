@@ -95,7 +95,6 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int per_tile = args.nseq * args.heads;
-    const int qt = ntiles - 1 - static_cast<int>(blockIdx.x) / per_tile;  // longest (causal) first
     const int rem = static_cast<int>(blockIdx.x) % per_tile;
     const int seq = rem / args.heads;
     const int head = rem % args.heads;
@@ -103,7 +102,9 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 
     grid_dependency_wait();
     AvSpan sp;
-    if (!av_span(args, seq, sp) || qt * AV_TILE >= sp.nq) return;
+    if (!av_span(args, seq, sp)) return;
+    const int qt = av_query_tile(args, sp, AV_TILE, ntiles, static_cast<int>(blockIdx.x) / per_tile);
+    if (qt < 0 || qt * AV_TILE >= sp.nq) return;
     const int i0 = qt * AV_TILE;
     const int n = av_key_tiles(sp, i0, args.causal);
     const int k_tail = n * AV_TILE > sp.nk ? sp.nk - (n - 1) * AV_TILE : AV_TILE;

@@ -64,9 +64,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    // Longest pairs (most key tiles, where causal) first; heads of one sequence side by side.
-    const int per_pair = args.nseq * args.heads;
-    const int pr = npairs - 1 - static_cast<int>(blockIdx.x) / per_pair;
+    const int per_pair = args.nseq * args.heads;  // heads of one sequence side by side
     const int rem = static_cast<int>(blockIdx.x) % per_pair;
     const int seq = rem / args.heads;
     const int head = rem % args.heads;
@@ -74,7 +72,9 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 
     grid_dependency_wait();  // the sequences' offsets, like the tensors, may come from the kernel before
     AvSpan sp;
-    if (!av_span(args, seq, sp) || pr * 2 * AV_TILE >= sp.nq) return;
+    if (!av_span(args, seq, sp)) return;
+    const int pr = av_query_tile(args, sp, 2 * AV_TILE, npairs, static_cast<int>(blockIdx.x) / per_pair);
+    if (pr < 0 || pr * 2 * AV_TILE >= sp.nq) return;
     const int qt[2] = {2 * pr, 2 * pr + 1};
     const int nt[2] = {av_key_tiles(sp, qt[0] * AV_TILE, args.causal), av_key_tiles(sp, qt[1] * AV_TILE, args.causal)};
     const int n = max(nt[0], nt[1]);
