@@ -144,7 +144,7 @@ __device__ __forceinline__ int av_key_tiles(const AvSpan& s, int i0, int causal)
 // first: where the mask is causal, later tiles see more keys. Sequences whose queries continue a prefix of their own
 // length are counted from their own ends, the others from the longest one's, so that tiles of the same number of
 // keys come together. (Four prompts of 33 to 1025 queries on 1024 to 2048 keys: the forward 38 us with the longest
-// one's end for all, 32 so; two clips of 3510 and 1755 queries would lose a seventh with their own ends.)
+// one's end for all, 30 so; two clips of 3510 and 1755 queries would lose a seventh with their own ends.)
 __device__ __forceinline__ int av_query_tile(const AvArgs& a, const AvSpan& s, int rows, int ntiles, int level) {
     const int n = a.causal && a.max_k > a.max_q ? (s.nq + rows - 1) / rows : ntiles;
     return n - 1 - level;

@@ -1,4 +1,5 @@
-// GEMM for few tokens: C[T, N] = A[T, K] W[K, N] with T <= 128, bound by reading W once.
+// GEMM for few tokens: C[T, N] = A[T, K] W[K, N], bound by reading W once. Up to 128 tokens are one slice of the
+// grid; more take a slice per 128, which find W in L2.
 //
 // The roles of the operands are swapped against the large GEMM: the weight's columns are the rows of
 // the product (M = 128 of them, W as stored is the MN-major operand) and the tokens its columns, padded
@@ -27,13 +28,14 @@
 
 namespace mptp {
 
-constexpr int FEW_MAX_T = 128;
+constexpr int FEW_SLICE = 128;   // tokens of a slice, at most
 constexpr int FEW_MAX_STAGES = 8;
 constexpr int FEW_THREADS = 192;
 constexpr int FEW_W_BYTES = 64 * 64 * 2;  // a block of 64 K rows x 64 columns
 
 struct FewArgs {
-    int T, npad;             // tokens; padded to 16
+    int T, npad;             // tokens; tokens of a slice, a multiple of 16
+    int blocks;              // blocks of 128 columns
     int kb;                  // K blocks of 64
     int cols;                // output columns (gated: f)
     int w_cols;              // columns of W
@@ -68,6 +70,23 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
                  : "memory");
 }
 
+// Bounded wait whose probes do not suspend the thread, so that any budget is kept to, one below a probe's longest
+// suspension too. For the one wait of the epilogue's warps: the whole K range's time.
+__device__ __forceinline__ bool wait_polled(uint64_t* bar, uint32_t parity, const Ctl& c) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (mbar_test_wait(bar, parity)) return true;
+        if (*c.abort_flag) return false;
+        if (globaltimer_ns() - t0 > c.budget_ns) {
+            if (c.status) atomicOr(c.status, DEV_TIMEOUT);
+            *c.abort_flag = 1u;
+            return false;
+        }
+    }
+}
+
 template <bool GATED>
 __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                const __grid_constant__ CUtensorMap tmA,
@@ -93,7 +112,9 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int block = static_cast<int>(blockIdx.x) / cluster;
+    const int block = static_cast<int>(blockIdx.x) / cluster % args.blocks;
+    const int t0 = static_cast<int>(blockIdx.x) / cluster / args.blocks * npad;  // first token of the slice
+    const int T = min(npad, args.T - t0);
     const int kb0 = args.kb * rank / cluster, kb1 = args.kb * (rank + 1) / cluster;
     const uint32_t need_cols = NACC * npad;
     const uint32_t tmem_cols = need_cols <= 32 ? 32u : need_cols <= 64 ? 64u : need_cols <= 128 ? 128u : 256u;
@@ -141,7 +162,7 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < 2 * NACC; ++i)
                     tma_load_2d(sW + st * W_STAGE + i * FEW_W_BYTES, &tmW, &full[st], w_col(i), kb * BK);
-                tma_load_2d(sA + st * npad * 128, &tmA, &full[st], kb * BK, 0);
+                tma_load_2d(sA + st * npad * 128, &tmA, &full[st], kb * BK, t0);
                 if (++st == stages) {
                     st = 0;
                     ph ^= 1u;
@@ -181,7 +202,7 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
     const int col = q * 32 + lane;  // column of the block
     bool got = true;
     if (warp >= 2) {
-        got = wait_bounded(acc_full, 0, ctl);
+        got = wait_polled(acc_full, 0, ctl);
         got = __all_sync(0xffffffffu, got) != 0;
     }
     __syncwarp();
@@ -193,7 +214,7 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
             const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
             int owner = 0, at = 0;  // the four tokens' CTA, and their place in its slice
 #pragma unroll 1
-            for (int c = 0; c < args.T; c += 16) {
+            for (int c = 0; c < T; c += 16) {
                 uint32_t v[NACC][16];
 #pragma unroll
                 for (int i = 0; i < NACC; ++i) tmem_ld16(t_addr + i * npad + c, v[i]);
@@ -202,7 +223,7 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
                 for (int i = 0; i < NACC; ++i) reg_fence16(v[i]);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    if (c + 4 * g < args.T) {
+                    if (c + 4 * g < T) {
                         float4* dst = red + ((rank * (slice / 4) + at) * NACC) * 128 + col;
                         const uint32_t to = cluster > 1 ? mapa_shared(smem_u32(dst), owner) : smem_u32(dst);
 #pragma unroll
@@ -223,8 +244,9 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
     else
         __syncthreads();
     if (warp >= 2 && *abort_flag == 0u && block * 128 + col < args.cols) {
-        const int c0 = rank * slice, c1 = min(args.T, c0 + slice);
-        __nv_bfloat16* out = args.out + block * 128 + col;
+        const int c0 = rank * slice, c1 = min(T, c0 + slice);
+        const long long at = static_cast<long long>(t0) * args.cols + block * 128 + col;
+        __nv_bfloat16* out = args.out + at;
 #pragma unroll 2
         for (int c = c0; c < c1; c += 4) {
             float4 sum[NACC];
@@ -248,7 +270,7 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
                 const float2 hi = mul2(glu_act2(make_float2(a[2], a[3]), args.act), make_float2(u[2], u[3]));
                 y[0] = lo.x, y[1] = lo.y, y[2] = hi.x, y[3] = hi.y;
                 if (args.gu) {
-                    __nv_bfloat16* gu = args.gu + static_cast<long long>(c) * 2 * args.cols + block * 128 + col;
+                    __nv_bfloat16* gu = args.gu + static_cast<long long>(t0 + c) * 2 * args.cols + block * 128 + col;
 #pragma unroll
                     for (int e = 0; e < 4; ++e, gu += 2 * args.cols)
                         if (c + e < c1) {
@@ -305,7 +327,8 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
                                  int ldw, int act, uint32_t* status, int num_sms, cudaStream_t stream) {
     FewArgs a{};
     a.T = T;
-    a.npad = ceil_div(T, 16) * 16;
+    const int slices = ceil_div(T, FEW_SLICE);
+    a.npad = ceil_div(ceil_div(T, slices), 16) * 16;
     a.kb = K / BK;
     a.cols = cols;
     a.w_cols = ldw;
@@ -318,7 +341,8 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
     CUtensorMap tw, ta;
     if (!make_tmap_bf16(&tw, W, ldw, K, ldw, 64, 64) || !make_tmap_bf16(&ta, A, K, T, K, 64, a.npad)) return MP_ERR_CUDA;
     auto kern = gemm_few_kernel<GATED>;
-    const int blocks = ceil_div(cols, 128);
+    a.blocks = ceil_div(cols, 128);
+    const int clusters = a.blocks * slices;
     auto fit_stages = [&](int cluster) {
         int n = FEW_MAX_STAGES;
         while (few_smem_bytes(GATED, a.npad, cluster, n) > SMEM_LIMIT) --n;
@@ -339,7 +363,7 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
             n = few_resident_clusters<GATED>(c, SMEM_LIMIT, num_sms);
             if (slot) slot->store(n > 0 ? n : -1, std::memory_order_relaxed);
         }
-        if (blocks <= n) {
+        if (clusters <= n) {
             a.cluster = c;
             break;
         }
@@ -347,7 +371,7 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
     a.stages = fit_stages(a.cluster);
     const size_t smem = few_smem_bytes(GATED, a.npad, a.cluster, a.stages);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks * a.cluster);
+    cfg.gridDim = dim3(clusters * a.cluster);
     cfg.blockDim = dim3(FEW_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

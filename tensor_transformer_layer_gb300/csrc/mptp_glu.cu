@@ -14,7 +14,8 @@
 // peer up columns, one tcgen05.mma (M = 256, N = 256) multiplies both, and each epilogue thread finds
 // a token's gate and up values in its own TMEM lane, 128 columns apart, in fp32. So G and U are
 // rounded only where the caller keeps them for the backward pass; Y comes from the fp32 values.
-// Then Z is one row-parallel GEMM over Y.
+// Then Z is one row-parallel GEMM over Y. Few tokens take a kernel bound by reading the weights for both
+// (mptp_gemm_few.cuh).
 // Backward: one GEMM gives dY, whose epilogue reads G and U and writes dG and dU (dY never reaches
 // memory); dX, dW and dWd are three GEMMs, side by side where that is shorter (mptp_mlp_host.cuh).
 #include "mptp_gemm_few.cuh"
@@ -25,6 +26,14 @@ using namespace mptp;
 namespace {
 
 bool bad_act(int act) { return act != MP_ACT_SILU && act != MP_ACT_GELU; }
+
+// Whether the forward takes the kernel for few tokens. One slice always: at h = 2304, f = 6144 it takes 20 us for a
+// token and 34 us for 128, the large tiles 43 to 48 us. Two slices while the weights fit in L2, so that the second
+// one finds them there: 35 to 44 us for 129 to 256 tokens against 44 to 45 (h = 1536, f = 4096: 22 to 28 against 36);
+// with weights of 400 MB (h = f = 8192) they took 97 to 111 us against 84 to 87, and three slices lose at h = 2304.
+bool few_tokens(int T, int h, int f) {
+    return T <= FEW_SLICE || (T <= 2 * FEW_SLICE && 6LL * h * f <= (1LL << 27));
+}
 
 }  // namespace
 
@@ -46,7 +55,7 @@ extern "C" mp_status mp_glu_fwd(const mp_bf16* X, const mp_bf16* W, const mp_bf1
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const double Tb = 2.0 * T, hb = 2.0 * h;
     const size_t f2 = size_t(2) * f;
-    if (T <= FEW_MAX_T) {
+    if (few_tokens(T, h, f)) {
         st = launch_gemm_few<true>(X, W, Y, GU_save, T, h, f, static_cast<int>(f2), act, d_status, sms, s);
         return st != MP_OK ? st : launch_gemm_few<false>(Y, Wd, Z, nullptr, T, f, h, h, act, d_status, sms, s);
     }

@@ -72,6 +72,19 @@ def test_glu_matches_oracle(T, h, f, t, act):
     assert torch.equal(lean["Y"], got["Y"]) and torch.equal(lean["Z"], got["Z"])
 
 
+@pytest.mark.parametrize("T,h,f,t", [
+    (128, 256, 320, 1),      # one slice of the tokens, full
+    (130, 1536, 4096, 4),    # two: 80 and 50 tokens, each over several CTAs of a cluster
+    (159, 64, 64, 1),
+    (161, 320, 192, 1),      # 96 and 65
+    (241, 704, 1024, 2),     # 128 and 113
+    (255, 448, 576, 1),
+])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_glu_matches_oracle_where_the_tokens_are_cut(T, h, f, t, act):
+    test_glu_matches_oracle(T, h, f, t, act)
+
+
 def test_glu_does_not_depend_on_shards_and_repeats_exactly():
     inp = _inputs(300, 256, 1024, seed=21100)
     ref = _run(inp, 1, "silu")
