@@ -327,7 +327,13 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
                                  int ldw, int act, uint32_t* status, int num_sms, cudaStream_t stream) {
     FewArgs a{};
     a.T = T;
-    const int slices = ceil_div(T, FEW_SLICE);
+    a.blocks = ceil_div(cols, 128);
+    // Slices of tokens: as few as hold them all, but gated ones of 64 where clusters of two or more CTAs remain for
+    // each: the join of both accumulators' partial sums, not the weights, is the longer part there (128 tokens, the
+    // whole block: h = 1024, f = 2048 16.7 us against 21, h = 1536, f = 4096 22.3 against 24.6; h = 2304, f = 6144,
+    // where clusters of one remain, 34.4 against 33.8). The plain product gains nothing steady from them.
+    const bool halves = GATED && T > FEW_SLICE / 2 && T <= FEW_SLICE && a.blocks * 4 <= num_sms;
+    const int slices = halves ? 2 : ceil_div(T, FEW_SLICE);
     a.npad = ceil_div(ceil_div(T, slices), 16) * 16;
     a.kb = K / BK;
     a.cols = cols;
@@ -341,7 +347,6 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
     CUtensorMap tw, ta;
     if (!make_tmap_bf16(&tw, W, ldw, K, ldw, 64, 64) || !make_tmap_bf16(&ta, A, K, T, K, 64, a.npad)) return MP_ERR_CUDA;
     auto kern = gemm_few_kernel<GATED>;
-    a.blocks = ceil_div(cols, 128);
     const int clusters = a.blocks * slices;
     auto fit_stages = [&](int cluster) {
         int n = FEW_MAX_STAGES;

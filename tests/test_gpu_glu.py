@@ -73,7 +73,7 @@ def test_glu_matches_oracle(T, h, f, t, act):
 
 
 @pytest.mark.parametrize("T,h,f,t", [
-    (128, 256, 320, 1),      # one slice of the tokens, full
+    (128, 256, 320, 1),      # two slices of 64 for the gated product, one of 128 for the other
     (130, 1536, 4096, 4),    # two: 80 and 50 tokens, each over several CTAs of a cluster
     (159, 64, 64, 1),
     (161, 320, 192, 1),      # 96 and 65
