@@ -25,7 +25,7 @@ struct AvTile {
     static constexpr int BYTES = NB * BOX;         // bytes of one tile
     // Registers a thread in warpgroup 0 and in the softmax warpgroups (setmaxnreg); the launch gives
     // 384 x 168.
-    static constexpr int REGS_CTRL = 72;
+    static constexpr int REGS_CTRL = 88;
     static constexpr int REGS_SOFTMAX = 208;
     static_assert(128 * REGS_CTRL + 256 * REGS_SOFTMAX <= AV_THREADS * 168, "register split");
 };
