@@ -426,7 +426,8 @@ MP_API mp_status mp_rope_axes(const mp_bf16* x, mp_bf16* y, const int32_t* pos,
  *   ldk, ldv elements apart (views of a packed projection are fine); LSE [heads, Tq] fp32.
  *   cu_q, cu_k [nseq + 1] int32 in device memory, ascending, within the tensors; max_q, max_k: at
  *   least the longest sequence's rows. A sequence that breaks this is left out (its outputs are not
- *   written) and sets MP_DEV_SEQ_RANGE.
+ *   written) and sets MP_DEV_SEQ_RANGE; where offsets that descend make others overlap, rows of theirs
+ *   may be left out too.
  *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; max_q <= Tq, max_k <= Tk; pitches at
  *   least a row and multiples of 8; scale > 0 and finite.
  */

@@ -46,14 +46,50 @@ struct AvArgs {
 struct AvSpan {
     int q0, nq, k0, nk;
 };
-__device__ __forceinline__ bool av_span(const AvArgs& a, int seq, AvSpan& s) {
+__device__ __forceinline__ AvSpan av_span(const AvArgs& a, int seq) {
     const int q0 = a.cu_q[seq], q1 = a.cu_q[seq + 1], k0 = a.cu_k[seq], k1 = a.cu_k[seq + 1];
     if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk || q1 - q0 > a.max_q || k1 - k0 > a.max_k) {
-        if (threadIdx.x == 0 && a.status) atomicOr(a.status, DEV_SEQ_RANGE);
-        return false;
+        if (threadIdx.x < 32 && a.status) atomicOr(a.status, DEV_SEQ_RANGE);
+        return {0, 0, 0, 0};
     }
-    s = {q0, q1 - q0, k0, k1 - k0};
-    return true;
+    return {q0, q1 - q0, k0, k1 - k0};
+}
+
+// The sequence and tile at place `item` of the order in which CTAs take them; false where there are no so many. A
+// tile has ROWS rows, queries (OF_QUERIES) or keys. The sequences with the longest other side come first, of each the
+// tiles that meet most of it first, so that a launch ends with small work; sequences beyond 32 follow by 32. Each
+// warp finds the place by itself, a lane a sequence. (A grid of every sequence by the longest one's tiles needs no
+// search, but a CTA that finds no tile costs 0.6 to 1.1 us with its launch and shared memory: 64 sequences of 128
+// tokens with a maximum of 2432 took 101, 160 and 54 us in the three kernels, and take 49, 53 and 24. The order by
+// work exactly, a search over all sequences' tiles, lost 1 to 2 us a CTA to the search.)
+template <int ROWS, bool OF_QUERIES>
+__device__ __forceinline__ bool av_pick(const AvArgs& a, int item, AvSpan& sp, int& tile) {
+    const int lane = threadIdx.x & 31;
+    for (int base = 0; base < a.nseq; base += 32) {
+        const int m = min(32, a.nseq - base);
+        const AvSpan s = lane < m ? av_span(a, base + lane) : AvSpan{0, 0, 0, 0};
+        const int tiles = ((OF_QUERIES ? s.nq : s.nk) + ROWS - 1) / ROWS;
+        const int other = OF_QUERIES ? s.nk : s.nq;
+        const int all = __reduce_add_sync(0xffffffffu, tiles);
+        if (item >= all) {
+            item -= all;
+            continue;
+        }
+        int first = 0;  // tiles of the sequences before the lane's
+        for (int j = 0; j < m; ++j) {
+            const int v = __shfl_sync(0xffffffffu, tiles, j), w = __shfl_sync(0xffffffffu, other, j);
+            if (w > other || (w == other && j < lane)) first += v;
+        }
+        const int at = item - first;
+        const bool here = at >= 0 && at < tiles;
+        // Sums of one lane's value leave it in a uniform register, as the loops over tiles want it: with shuffles in
+        // their place the key gradients of 4096 tokens and 19 heads took 220 us at D = 128, with them 213.
+        auto value = [&](int v) { return __reduce_add_sync(0xffffffffu, here ? v : 0); };
+        sp = {value(s.q0), value(s.nq), value(s.k0), value(s.nk)};
+        tile = value(OF_QUERIES ? tiles - 1 - at : at);
+        return true;
+    }
+    return false;
 }
 
 // One tile (rows from `row`, head `head` of the matrix) into shared memory, counted on `bar`: D/32 boxes by one
@@ -140,16 +176,6 @@ __device__ __forceinline__ int av_key_tiles(const AvSpan& s, int i0, int causal)
     return keys > 0 ? (keys + AV_TILE - 1) / AV_TILE : 0;
 }
 
-// The tile of queries that a CTA at `level` of the grid takes (tiles of `rows` rows; negative: none). Larger work
-// first: where the mask is causal, later tiles see more keys. Sequences whose queries continue a prefix of their own
-// length are counted from their own ends, the others from the longest one's, so that tiles of the same number of
-// keys come together. (Four prompts of 33 to 1025 queries on 1024 to 2048 keys: the forward 38 us with the longest
-// one's end for all, 30 so; two clips of 3510 and 1755 queries would lose a seventh with their own ends.)
-__device__ __forceinline__ int av_query_tile(const AvArgs& a, const AvSpan& s, int rows, int ntiles, int level) {
-    const int n = a.causal && a.max_k > a.max_q ? (s.nq + rows - 1) / rows : ntiles;
-    return n - 1 - level;
-}
-
 // 16-bit A operand of a TMEM product: 16 rows' worth (8 columns) of step k. Each softmax warpgroup
 // writes its 64 columns' values, packed, over the first half of its own 64 fp32 columns.
 __device__ __forceinline__ uint32_t av_a_step(uint32_t base, int k) { return base + (k >> 2) * 64 + (k & 3) * 8; }
@@ -170,6 +196,11 @@ inline mp_status av_check(int nseq, int Tq, int Tk, int max_q, int max_k, int he
     const long long tiles = (max_q > max_k ? max_q : max_k) / AV_TILE + 1;
     if (tiles * nseq > 0x7fffffffLL / AV_MAX_CLUSTER / heads) return MP_ERR_UNSUPPORTED_SHAPE;
     return MP_OK;
+}
+// Tiles of `rows` rows that sequences of no more than T rows together, `longest` each, can have.
+inline long long av_max_tiles(int nseq, int T, int longest, int rows) {
+    const long long each = static_cast<long long>(nseq) * ceil_div(longest, rows), all = T / rows + static_cast<long long>(nseq);
+    return each < all ? each : all;
 }
 inline bool av_bad_pitch(long long ld, long long row) { return ld < row || ld % 8 != 0 || ld > (1LL << 36); }
 

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                           const __grid_constant__ CUtensorMap tmdQ, const __nv_bfloat16* O, long long ldo,
                           const __nv_bfloat16* dO, long long lddo, const float* LSE, float* delta, __nv_bfloat16* dQ,
-                          long long lddq, int ntiles, const AvArgs args) {
+                          long long lddq, const AvArgs args) {
     using Cfg = AvDqCfg<D>;
     using T = AvTile<D>;
     constexpr int NB = T::NB, KST = Cfg::KST, VST = Cfg::VST;
@@ -94,17 +94,14 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int per_tile = args.nseq * args.heads;
-    const int rem = static_cast<int>(blockIdx.x) % per_tile;
-    const int seq = rem / args.heads;
-    const int head = rem % args.heads;
+    const int head = static_cast<int>(blockIdx.x) % args.heads;
     const int kvh = head / args.group;
 
     grid_dependency_wait();
     AvSpan sp;
-    if (!av_span(args, seq, sp)) return;
-    const int qt = av_query_tile(args, sp, AV_TILE, ntiles, static_cast<int>(blockIdx.x) / per_tile);
-    if (qt < 0 || qt * AV_TILE >= sp.nq) return;
+    int qt;
+    if (!av_pick<AV_TILE, true>(args, static_cast<int>(blockIdx.x) / args.heads, sp, qt))
+        return;
     const int i0 = qt * AV_TILE;
     const int n = av_key_tiles(sp, i0, args.causal);
     const int k_tail = n * AV_TILE > sp.nk ? sp.nk - (n - 1) * AV_TILE : AV_TILE;
@@ -473,17 +470,14 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int per_tile = args.nseq * args.kv_heads;
     const int item = static_cast<int>(blockIdx.x) / cluster;
     const int rank = JOIN ? static_cast<int>(cluster_ctarank()) : 0;
-    const int kt = item / per_tile;  // the first keys have the most queries (causal)
-    const int rem = item % per_tile;
-    const int seq = rem / args.kv_heads;
-    const int kvh = rem % args.kv_heads;
+    const int kvh = item % args.kv_heads;
 
     grid_dependency_wait();
     AvSpan sp;
-    if (!av_span(args, seq, sp) || kt * AV_TILE >= sp.nk) return;
+    int kt;
+    if (!av_pick<AV_TILE, false>(args, item / args.kv_heads, sp, kt)) return;
     const int j0 = kt * AV_TILE;
     const int off = sp.nk - sp.nq;
     // query tiles [t0, t1) see some key of this tile
@@ -961,16 +955,16 @@ static cudaError_t launch_bwd(const AvBwdMaps& m, const mp_bf16* O, long long ld
                               const float* LSE, float* delta, mp_bf16* dQ, long long lddq, mp_bf16* dK, long long lddk,
                               mp_bf16* dV, long long lddv, const AvArgs& a, int sms, cudaStream_t s) {
     auto bf = [](auto* p) { return reinterpret_cast<__nv_bfloat16*>(const_cast<mp_bf16*>(p)); };
-    const int qtiles = ceil_div(a.max_q, AV_TILE), ktiles = ceil_div(a.max_k, AV_TILE);
+    const long long qtiles = av_max_tiles(a.nseq, a.Tq, a.max_q, AV_TILE), ktiles = av_max_tiles(a.nseq, a.Tk, a.max_k, AV_TILE);
     cudaError_t e = cudaSuccess;
     if (qtiles > 0)
-        e = av_launch(attn_varlen_dq_kernel<D>, static_cast<long long>(qtiles) * a.nseq * a.heads, 1, AvDqCfg<D>::SMEM, s, m.q,
+        e = av_launch(attn_varlen_dq_kernel<D>, qtiles * a.heads, 1, AvDqCfg<D>::SMEM, s, m.q,
                       m.k, m.v, m.d_o, m.dq, static_cast<const __nv_bfloat16*>(bf(O)), ldo,
-                      static_cast<const __nv_bfloat16*>(bf(dO)), lddo, LSE, delta, bf(dQ), lddq, qtiles, a);
+                      static_cast<const __nv_bfloat16*>(bf(dO)), lddo, LSE, delta, bf(dQ), lddq, a);
     if (e == cudaSuccess && ktiles > 0) {
         const int cluster = dkv_cluster(a, sms);
         auto kern = cluster > 1 ? attn_varlen_dkv_kernel<D, true> : attn_varlen_dkv_kernel<D, false>;
-        e = av_launch(kern, static_cast<long long>(ktiles) * a.nseq * a.kv_heads * cluster, cluster, AvDkvCfg<D>::SMEM, s,
+        e = av_launch(kern, ktiles * a.kv_heads * cluster, cluster, AvDkvCfg<D>::SMEM, s,
                       m.q, m.k, m.v, m.d_o, m.dk, m.dv, LSE, static_cast<const float*>(delta), bf(dK), lddk, bf(dV),
                       lddv, cluster, a);
     }

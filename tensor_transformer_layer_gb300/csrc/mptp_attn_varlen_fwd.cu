@@ -40,7 +40,7 @@ template <int D>
 __global__ void __launch_bounds__(AV_THREADS, 1)
     attn_varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                           __nv_bfloat16* O, long long ldo, float* LSE, int npairs, const AvArgs args) {
+                           __nv_bfloat16* O, long long ldo, float* LSE, const AvArgs args) {
     using Cfg = AvFwdCfg<D>;
     using T = AvTile<D>;
     constexpr int NB = T::NB, KST = Cfg::KST, VST = Cfg::VST;
@@ -64,17 +64,14 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int per_pair = args.nseq * args.heads;  // heads of one sequence side by side
-    const int rem = static_cast<int>(blockIdx.x) % per_pair;
-    const int seq = rem / args.heads;
-    const int head = rem % args.heads;
+    const int head = static_cast<int>(blockIdx.x) % args.heads;  // heads of one sequence side by side
     const int kvh = head / args.group;
 
     grid_dependency_wait();  // the sequences' offsets, like the tensors, may come from the kernel before
     AvSpan sp;
-    if (!av_span(args, seq, sp)) return;
-    const int pr = av_query_tile(args, sp, 2 * AV_TILE, npairs, static_cast<int>(blockIdx.x) / per_pair);
-    if (pr < 0 || pr * 2 * AV_TILE >= sp.nq) return;
+    int pr;
+    if (!av_pick<2 * AV_TILE, true>(args, static_cast<int>(blockIdx.x) / args.heads, sp, pr))
+        return;
     const int qt[2] = {2 * pr, 2 * pr + 1};
     const int nt[2] = {av_key_tiles(sp, qt[0] * AV_TILE, args.causal), av_key_tiles(sp, qt[1] * AV_TILE, args.causal)};
     const int n = max(nt[0], nt[1]);
@@ -369,17 +366,15 @@ extern "C" mp_status mp_attn_varlen_fwd(const mp_bf16* Q, const mp_bf16* K, cons
                  : av_tmap(&tk, Q, static_cast<int>(qw), Tq, ldq, d) && av_tmap(&tv, Q, static_cast<int>(qw), Tq, ldq, d)))
         return MP_ERR_CUDA;
     const AvArgs a = av_args(cu_q, cu_k, nseq, Tq, Tk, max_q, max_k, heads, kv_heads, causal ? 1 : 0, scale, d_status);
-    const int npairs = ceil_div(max_q, 2 * AV_TILE);
-    const long long blocks = static_cast<long long>(npairs) * nseq * heads;
+    const long long blocks = av_max_tiles(nseq, Tq, max_q, 2 * AV_TILE) * heads;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(O);
     cudaError_t e;
     if (d == 64)
-        e = av_launch(attn_varlen_fwd_kernel<64>, blocks, 1, AvFwdCfg<64>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs, a);
+        e = av_launch(attn_varlen_fwd_kernel<64>, blocks, 1, AvFwdCfg<64>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, a);
     else if (d == 96)
-        e = av_launch(attn_varlen_fwd_kernel<96>, blocks, 1, AvFwdCfg<96>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs, a);
+        e = av_launch(attn_varlen_fwd_kernel<96>, blocks, 1, AvFwdCfg<96>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, a);
     else
-        e = av_launch(attn_varlen_fwd_kernel<128>, blocks, 1, AvFwdCfg<128>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, npairs,
-                      a);
+        e = av_launch(attn_varlen_fwd_kernel<128>, blocks, 1, AvFwdCfg<128>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, a);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }

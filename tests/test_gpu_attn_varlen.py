@@ -122,6 +122,20 @@ def test_attn_varlen_many_tiles(d):
     _check(_run(inp, cu, cu, True), inp, cu, cu, True)
 
 
+@pytest.mark.parametrize("nseq", [32, 33, 71])
+@pytest.mark.parametrize("same,causal", [(True, True), (False, True), (False, False)])
+def test_attn_varlen_many_sequences(nseq, same, causal):
+    # more sequences than a warp has lanes, of all lengths from none to several tiles, the longest among the last
+    rng = np.random.default_rng(22550 + nseq)
+    q_lens = rng.choice([0, 1, 31, 128, 129, 200], nseq)
+    k_lens = q_lens if same else rng.choice([0, 1, 40, 128, 300], nseq)
+    q_lens[-2] = 600
+    k_lens[-2] = 600
+    cu_q, cu_k = _cu(q_lens), _cu(k_lens)
+    inp = _inputs(int(sum(q_lens)), int(sum(k_lens)), 2, 1, 64, seed=22560 + nseq)
+    _check(_run(inp, cu_q, cu_k, causal), inp, cu_q, cu_k, causal)
+
+
 def test_attn_varlen_scale_and_large_scores():
     # scores up to +-200 and a jump of the running maximum at every key tile
     lens = [400]
