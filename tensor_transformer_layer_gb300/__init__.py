@@ -432,6 +432,8 @@ def mp_glu_bwd(X, W, Wd, GU, Y, dZ, dX, dW, dWd, dGU_ws, *, t: int, act: str = "
 def _heads_view(x, name, shape=None):
     """Pointer and row pitch of a bf16 [tokens, heads, d] tensor whose heads are packed in each row (a view of
     some heads of a wider row is fine)."""
+    if type(x) is torch.Tensor and x.dtype is torch.bfloat16 and x.shape == shape and x.is_cuda and x.is_contiguous():
+        return x.data_ptr() or None, shape[1] * shape[2]
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if x.dtype is not torch.bfloat16:
@@ -472,16 +474,17 @@ def mp_rope_axes(x, y, pos, *, sections, base: float = 10000.0, interleaved: boo
 
 
 def _packed_shapes(Q, K, cu_q, cu_k):
-    if not isinstance(Q, torch.Tensor) or not isinstance(K, torch.Tensor) or Q.dim() != 3 or K.dim() != 3:
+    if not isinstance(Q, torch.Tensor) or not isinstance(K, torch.Tensor):
         raise ValueError("Q and K must be [tokens, heads, d] tensors")
-    if Q.shape[2] != K.shape[2]:
-        raise ValueError(f"Q and K must have the same head width, got {Q.shape[2]} and {K.shape[2]}")
+    qs, ks = Q.shape, K.shape
+    if len(qs) != 3 or len(ks) != 3:
+        raise ValueError("Q and K must be [tokens, heads, d] tensors")
+    if qs[2] != ks[2]:
+        raise ValueError(f"Q and K must have the same head width, got {qs[2]} and {ks[2]}")
     nseq = cu_q.shape[0] - 1
     if nseq < 0:
         raise ValueError("cu_q must have at least one entry")
-    return (nseq, Q.shape[0], K.shape[0], Q.shape[1], K.shape[1], Q.shape[2],
-            _ptr(cu_q, "cu_q", dtype=torch.int32, shape=(nseq + 1,)),
-            _ptr(cu_k, "cu_k", dtype=torch.int32, shape=(nseq + 1,)))
+    return (nseq, qs, ks, _ptr(cu_q, "cu_q", torch.int32, (nseq + 1,)), _ptr(cu_k, "cu_k", torch.int32, (nseq + 1,)))
 
 
 def mp_attn_varlen_fwd(Q, K, V, O, LSE, cu_q, cu_k, *, max_q: int, max_k: int, causal: bool, scale: float | None = None,
@@ -489,11 +492,12 @@ def mp_attn_varlen_fwd(Q, K, V, O, LSE, cu_q, cu_k, *, max_q: int, max_k: int, c
     """Attention over packed sequences: O [Tq, heads, d] and LSE [heads, Tq] fp32 from Q [Tq, heads, d], K, V
     [Tk, kv_heads, d] (rows may be strided). cu_q, cu_k [nseq + 1] int32: sequence i owns rows cu[i] .. cu[i+1]-1;
     max_q, max_k: at least the longest. causal: the last query sees the last key. scale: 1 / sqrt(d) by default."""
-    nseq, Tq, Tk, heads, kv, d, pcq, pck = _packed_shapes(Q, K, cu_q, cu_k)
-    (pq, ldq), (pk, ldk) = _heads_view(Q, "Q"), _heads_view(K, "K")
-    (pv, ldv), (po, ldo) = _heads_view(V, "V", (Tk, kv, d)), _heads_view(O, "O", (Tq, heads, d))
+    nseq, qs, ks, pcq, pck = _packed_shapes(Q, K, cu_q, cu_k)
+    (Tq, heads, d), (Tk, kv, _) = qs, ks
+    (pq, ldq), (pk, ldk) = _heads_view(Q, "Q", qs), _heads_view(K, "K", ks)
+    (pv, ldv), (po, ldo) = _heads_view(V, "V", ks), _heads_view(O, "O", qs)
     code = lib().mp_attn_varlen_fwd(
-        pq, pk, pv, po, _ptr(LSE, "LSE", dtype=torch.float32, shape=(heads, Tq)), pcq, pck, nseq, Tq, Tk, int(max_q),
+        pq, pk, pv, po, _ptr(LSE, "LSE", torch.float32, (heads, Tq)), pcq, pck, nseq, Tq, Tk, int(max_q),
         int(max_k), heads, kv, d, ldq, ldk, ldv, ldo, 1 if causal else 0, d ** -0.5 if scale is None else float(scale),
         _status_ptr(d_status), _stream(stream))
     _check("mp_attn_varlen_fwd", code)
@@ -503,15 +507,15 @@ def mp_attn_varlen_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, delta_ws, cu_q, cu_k, *,
                        scale: float | None = None, d_status=None, stream=None) -> None:
     """Backward of mp_attn_varlen_fwd from its O and LSE: dQ, dK, dV (rows may be strided, e.g. the parts of a
     packed projection's gradient); delta_ws [heads, Tq] fp32 workspace."""
-    nseq, Tq, Tk, heads, kv, d, pcq, pck = _packed_shapes(Q, K, cu_q, cu_k)
-    qs, ks = (Tq, heads, d), (Tk, kv, d)
-    (pq, ldq), (pk, ldk), (pv, ldv) = _heads_view(Q, "Q"), _heads_view(K, "K"), _heads_view(V, "V", ks)
+    nseq, qs, ks, pcq, pck = _packed_shapes(Q, K, cu_q, cu_k)
+    (Tq, heads, d), (Tk, kv, _) = qs, ks
+    (pq, ldq), (pk, ldk), (pv, ldv) = _heads_view(Q, "Q", qs), _heads_view(K, "K", ks), _heads_view(V, "V", ks)
     (po, ldo), (pdo, lddo) = _heads_view(O, "O", qs), _heads_view(dO, "dO", qs)
     (pdq, lddq), (pdk, lddk), (pdv, lddv) = (_heads_view(dQ, "dQ", qs), _heads_view(dK, "dK", ks),
                                              _heads_view(dV, "dV", ks))
-    f32 = dict(dtype=torch.float32, shape=(heads, Tq))
+    f32 = torch.float32, (heads, Tq)
     code = lib().mp_attn_varlen_bwd(
-        pq, pk, pv, po, _ptr(LSE, "LSE", **f32), pdo, pdq, pdk, pdv, _ptr(delta_ws, "delta_ws", **f32), pcq, pck, nseq,
+        pq, pk, pv, po, _ptr(LSE, "LSE", *f32), pdo, pdq, pdk, pdv, _ptr(delta_ws, "delta_ws", *f32), pcq, pck, nseq,
         Tq, Tk, int(max_q), int(max_k), heads, kv, d, ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv, 1 if causal else 0,
         d ** -0.5 if scale is None else float(scale), _status_ptr(d_status), _stream(stream))
     _check("mp_attn_varlen_bwd", code)
