@@ -13,6 +13,12 @@ Shapes (row-major, contiguous):
   mp_mlp_fwd_fused / mp_mlp_bwd_fused: the same, one launch per direction, with a zeroed
       uint8 workspace of mp_mlp_fused_workspace_bytes(T, h, f, t) bytes
   mp_vocab_ce(X[T,h], E[v_pad,h], target[T] int32, loss[T] fp32, workspace uint8, v_valid, t)
+  mp_rope_axes(x[T,heads,d], y[T,heads,d], pos[axes,T] int32, sections)
+  mp_attn_varlen_fwd(Q[Tq,heads,d], K[Tk,kv,d], V[Tk,kv,d], O[Tq,heads,d], LSE[heads,Tq] fp32, cu_q, cu_k int32)
+  mp_attn_varlen_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, delta_ws[heads,Tq] fp32, cu_q, cu_k)
+      (these three take rows of any pitch, e.g. parts of a packed projection)
+  mp_glu_fwd(X[T,h], W[h,2f], Wd[f,h], Z[T,h], Y[T,f], GU_save[T,2f] | None, t, act)
+  mp_glu_bwd(X, W, Wd, GU, Y, dZ[T,h], dX[T,h], dW[h,2f], dWd[f,h], dGU_ws[T,2f], t, act)
 """
 from __future__ import annotations
 

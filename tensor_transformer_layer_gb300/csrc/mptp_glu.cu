@@ -18,6 +18,9 @@
 // (mptp_gemm_few.cuh).
 // Backward: one GEMM gives dY, whose epilogue reads G and U and writes dG and dU (dY never reaches
 // memory); dX, dW and dWd are three GEMMs, side by side where that is shorter (mptp_mlp_host.cuh).
+// Bound by the tensor core: T = 8192, h = 2304, f = 6144, SiLU, 1.287 ms forward and backward, 1.62 PFLOP/s, 94 % of
+// the library's sustained rate for a plain product. Alone, the launches take 245 us ([G | U] and Y), 120 (Z), 157 (dG
+// and dU: 119 without the epilogue, whose gates, ups and gradients are 500 MB beside the K loop), 241, 240 and 122.
 #include "mptp_gemm_few.cuh"
 #include "mptp_mlp_host.cuh"
 
