@@ -1,5 +1,5 @@
-// GEMM for few tokens: C[T, N] = A[T, K] W[K, N], bound by reading W once. Up to 128 tokens are one slice of the
-// grid; more take a slice per 128, which find W in L2.
+// GEMM for few tokens: C[T, N] = A[T, K] W[K, N], bound by reading W once. Tokens beyond 128 take further slices of the
+// grid, which find W in L2.
 //
 // The roles of the operands are swapped against the large GEMM: the weight's columns are the rows of
 // the product (M = 128 of them, W as stored is the MN-major operand) and the tokens its columns, padded
@@ -14,10 +14,11 @@
 //
 //   warp 0: TMA producer, a ring of stages of 64 K rows x 128 columns (gated: 2 x 128) and the tokens' 64
 //           K elements. Before it waits for the previous kernel it asks L2 for the first stages' weights.
-//   warp 1: TMEM, MMA issue.   warps 2..5: partial sums out, reduction, epilogue.
+//   warp 1: TMEM, MMA issue.   the others: partial sums out, reduction, epilogue.
 //
-// One token through h = 1536, f = 4096 (37.7 MB of weights): both launches 12.5 us, 38 with the large tiles. While it
-// streams, a launch reads 7 TB/s; about 7 us go into the two launches' set-up, first loads and joins.
+// One token through h = 1536, f = 4096 (37.7 MB of weights): both launches 12.5 us, 38 with the large tiles; 77 tokens
+// through h = 2304, f = 6144 (85 MB) 25 us. While it streams, a launch reads 7 TB/s; about 7 us go into the two
+// launches' set-up, first loads and joins, and 0.07 us a token into the join.
 //
 // Epilogues: plain store, or gated: 128 gate columns and the 128 up columns of the same outputs have an
 // accumulator each, so that a thread finds both in its TMEM lane; Y = act(gate) up is computed where the
@@ -33,7 +34,8 @@ namespace mptp {
 
 constexpr int FEW_SLICE = 128;   // tokens of a slice, at most
 constexpr int FEW_MAX_STAGES = 8;
-constexpr int FEW_THREADS = 192;
+constexpr int FEW_MAX_PARTS = 2;  // warps of the epilogue per quarter of the tensor memory's lanes, at most
+constexpr int few_threads(int parts) { return 64 + parts * 128; }
 constexpr int FEW_W_BYTES = 64 * 64 * 2;  // a block of 64 K rows x 64 columns
 
 struct FewArgs {
@@ -44,6 +46,7 @@ struct FewArgs {
     int w_cols;              // columns of W
     int up_off;              // gated: columns of W from a gate to its up
     int cluster, stages;
+    int parts;               // warps of the epilogue a quarter of the lanes: shares of the tokens
     int act;
     __nv_bfloat16* out;      // [T, cols]
     __nv_bfloat16* gu;       // gated, nullable: [T, 2 cols]
@@ -91,7 +94,7 @@ __device__ __forceinline__ bool wait_polled(uint64_t* bar, uint32_t parity, cons
 }
 
 template <bool GATED>
-__global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_constant__ CUtensorMap tmW,
+__global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                const __grid_constant__ CUtensorMap tmA,
                                                                const FewArgs args) {
     constexpr int NACC = GATED ? 2 : 1;            // accumulators: gate and up
@@ -202,6 +205,8 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
         wait_drain(drain_bar, 0, args.status);
     }
     const int q = warp & 3;
+    const int part = (warp - 2) >> 2, parts = args.parts;
+    const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const int col = q * 32 + lane;  // column of the block
     bool got = true;
     if (warp >= 2) {
@@ -211,24 +216,23 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
     __syncwarp();
     if (cluster > 1) cluster_sync_all();  // every CTA of the cluster has used its ring: it may be written over
     if (warp >= 2) {
-        // This CTA's partial sums, four tokens at a time, to the CTAs that finish them.
+        // This CTA's partial sums, four tokens at a time, to the CTAs that finish them; its own tokens' stay.
         if (got) {
             tc_fence_after();
-            const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-            int owner = 0, at = 0;  // the four tokens' CTA, and their place in its slice
 #pragma unroll 1
-            for (int c = 0; c < T; c += 16) {
+            for (int c = part * 16; c < T && cluster > 1; c += parts * 16) {
                 uint32_t v[NACC][16];
 #pragma unroll
                 for (int i = 0; i < NACC; ++i) tmem_ld16(t_addr + i * npad + c, v[i]);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < NACC; ++i) reg_fence16(v[i]);
+                int owner = c / slice, at = (c - owner * slice) / 4;  // the four tokens' CTA, and their place there
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    if (c + 4 * g < T) {
+                    if (c + 4 * g < T && owner != rank) {
                         float4* dst = red + ((rank * (slice / 4) + at) * NACC) * 128 + col;
-                        const uint32_t to = cluster > 1 ? mapa_shared(smem_u32(dst), owner) : smem_u32(dst);
+                        const uint32_t to = mapa_shared(smem_u32(dst), owner);
 #pragma unroll
                         for (int i = 0; i < NACC; ++i)
                             st_cluster_v4(to + i * 2048, v[i][4 * g], v[i][4 * g + 1], v[i][4 * g + 2], v[i][4 * g + 3]);
@@ -246,45 +250,69 @@ __global__ void __launch_bounds__(FEW_THREADS) gemm_few_kernel(const __grid_cons
         cluster_sync_all();  // releases the partial sums, acquires the others'
     else
         __syncthreads();
-    if (warp >= 2 && *abort_flag == 0u && block * 128 + col < args.cols) {
+    if (warp >= 2 && *abort_flag == 0u && block * 128 + q * 32 < args.cols) {
+        // Eight tokens of a column at a time: their loads, then their arithmetic, then their stores. (Four at a time,
+        // through pointers that the stores might alias, took 800 cycles each.)
+        constexpr int G = 2;
         const int c0 = rank * slice, c1 = min(T, c0 + slice);
-        const long long at = static_cast<long long>(t0) * args.cols + block * 128 + col;
-        __nv_bfloat16* out = args.out + at;
+#pragma unroll 1
+        for (int c = c0 + part * 4 * G; c < c1; c += parts * 4 * G) {
+            uint32_t own[G][NACC][4];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (g == 0 || c + 4 * g < c1)
+#pragma unroll
+                    for (int i = 0; i < NACC; ++i) tmem_ld4(t_addr + i * npad + c + 4 * g, own[g][i]);
+            tmem_wait_ld();
+            float sum[G][NACC][4];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < NACC; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        asm volatile("" : "+r"(own[g][i][e]));
+                        sum[g][i][e] = __uint_as_float(own[g][i][e]);
+                    }
+            // own first, then the ranks behind it in turn: a fixed order for every token
 #pragma unroll 2
-        for (int c = c0; c < c1; c += 4) {
-            float4 sum[NACC];
+            for (int s = 1; s < cluster; ++s) {
+                const int from = rank + s - (rank + s >= cluster ? cluster : 0);
+                const uint32_t at = smem_u32(red) + (((from * slice + c - c0) / 4 * NACC) * 128 + col) * 16;
 #pragma unroll
-            for (int i = 0; i < NACC; ++i) sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const float4* p = red + ((c - c0) / 4 * NACC) * 128 + col;
-            for (int s = 0; s < cluster; ++s, p += slice / 4 * NACC * 128)
+                for (int g = 0; g < G; ++g)
+                    if (g == 0 || c + 4 * g < c1)
 #pragma unroll
-                for (int i = 0; i < NACC; ++i) {
-                    const float4 v = p[i * 128];
-                    sum[i].x += v.x;
-                    sum[i].y += v.y;
-                    sum[i].z += v.z;
-                    sum[i].w += v.w;
-                }
-            const float a[4] = {sum[0].x, sum[0].y, sum[0].z, sum[0].w};
-            float y[4] = {a[0], a[1], a[2], a[3]};
-            if constexpr (GATED) {
-                const float u[4] = {sum[1].x, sum[1].y, sum[1].z, sum[1].w};
-                const float2 lo = mul2(glu_act2(make_float2(a[0], a[1]), args.act), make_float2(u[0], u[1]));
-                const float2 hi = mul2(glu_act2(make_float2(a[2], a[3]), args.act), make_float2(u[2], u[3]));
-                y[0] = lo.x, y[1] = lo.y, y[2] = hi.x, y[3] = hi.y;
+                        for (int i = 0; i < NACC; ++i) {
+                            const float4 v = ld_shared_v4(at + (g * NACC + i) * 2048);
+                            sum[g][i][0] += v.x;
+                            sum[g][i][1] += v.y;
+                            sum[g][i][2] += v.z;
+                            sum[g][i][3] += v.w;
+                        }
+            }
+            float y[G * 4];
+#pragma unroll
+            for (int k = 0; k < G * 4; k += 2) {
+                float2 v = make_float2(sum[k / 4][0][k % 4], sum[k / 4][0][k % 4 + 1]);
+                if constexpr (GATED)
+                    v = mul2(glu_act2(v, args.act), make_float2(sum[k / 4][1][k % 4], sum[k / 4][1][k % 4 + 1]));
+                y[k] = v.x, y[k + 1] = v.y;
+            }
+            __nv_bfloat16* out = args.out + static_cast<long long>(t0 + c) * args.cols + block * 128 + col;
+#pragma unroll
+            for (int k = 0; k < G * 4; ++k, out += args.cols)
+                if (c + k < c1) *out = __float2bfloat16(y[k]);
+            if constexpr (GATED)
                 if (args.gu) {
                     __nv_bfloat16* gu = args.gu + static_cast<long long>(t0 + c) * 2 * args.cols + block * 128 + col;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e, gu += 2 * args.cols)
-                        if (c + e < c1) {
-                            gu[0] = __float2bfloat16(a[e]);
-                            gu[args.cols] = __float2bfloat16(u[e]);
+                    for (int k = 0; k < G * 4; ++k, gu += 2 * args.cols)
+                        if (c + k < c1) {
+                            gu[0] = __float2bfloat16(sum[k / 4][0][k % 4]);
+                            gu[args.cols] = __float2bfloat16(sum[k / 4][1][k % 4]);
                         }
                 }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < c1) out[static_cast<long long>(c + e) * args.cols] = __float2bfloat16(y[e]);
         }
     }
 
@@ -307,7 +335,7 @@ template <bool GATED>
 inline int few_resident_clusters(int cluster, size_t smem, int num_sms) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster * num_sms, 1, 1);
-    cfg.blockDim = dim3(FEW_THREADS, 1, 1);
+    cfg.blockDim = dim3(few_threads(FEW_MAX_PARTS), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -331,12 +359,14 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
     FewArgs a{};
     a.T = T;
     a.blocks = ceil_div(cols, 128);
-    // Slices of tokens: as few as hold them all, but gated ones of 64 where clusters of two or more CTAs remain for
-    // each: the join of both accumulators' partial sums, not the weights, is the longer part there (128 tokens, the
-    // whole block: h = 1024, f = 2048 16.7 us against 21, h = 1536, f = 4096 22.3 against 24.6; h = 2304, f = 6144,
-    // where clusters of one remain, 34.4 against 33.8). The plain product gains nothing steady from them.
-    const bool halves = GATED && T > FEW_SLICE / 2 && T <= FEW_SLICE && a.blocks * 4 <= num_sms;
-    const int slices = halves ? 2 : ceil_div(T, FEW_SLICE);
+    // Slices of tokens: as few as hold them all, then halves while clusters of some CTAs remain for each: the join of
+    // the partial sums grows with a slice's tokens and is the longer part where the weights are few. Measured for the
+    // whole block, 128 tokens, without and with halves: h = 1024, f = 2048 18.5 and 13.3 us, h = 1536, f = 4096 21.5
+    // and 18.1, h = 2304, f = 6144 28.7 and 27.7. Smaller slices, or smaller clusters, lose: the plain product's halves
+    // at clusters of two take 24.4 us against 21.9 for 256 tokens, h = 1536.
+    constexpr int LEAST = GATED ? 32 : 64, LEAST_CLUSTER = GATED ? 2 : 4;
+    int slices = ceil_div(T, FEW_SLICE);
+    while (ceil_div(T, 2 * slices) >= LEAST && a.blocks * 2 * slices * LEAST_CLUSTER <= num_sms) slices *= 2;
     a.npad = ceil_div(ceil_div(T, slices), 16) * 16;
     a.kb = K / BK;
     a.cols = cols;
@@ -377,10 +407,13 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
         }
     }
     a.stages = fit_stages(a.cluster);
+    // Eight warps finish the tokens where there are more than a few: 77 tokens, h = 2304, f = 6144 24.9 us against 26.1
+    // with four, one token 21.1 against 20.7. (Sixteen: 25.6 and 22.0.)
+    a.parts = T <= 32 ? 1 : FEW_MAX_PARTS;
     const size_t smem = few_smem_bytes(GATED, a.npad, a.cluster, a.stages);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(clusters * a.cluster);
-    cfg.blockDim = dim3(FEW_THREADS);
+    cfg.blockDim = dim3(few_threads(a.parts));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];

@@ -21,6 +21,8 @@
 // Bound by the tensor core: T = 8192, h = 2304, f = 6144, SiLU, 1.287 ms forward and backward, 1.62 PFLOP/s, 94 % of
 // the library's sustained rate for a plain product. Alone, the launches take 245 us ([G | U] and Y), 120 (Z), 157 (dG
 // and dU: 119 without the epilogue, whose gates, ups and gradients are 500 MB beside the K loop), 241, 240 and 122.
+#include <algorithm>
+
 #include "mptp_gemm_few.cuh"
 #include "mptp_mlp_host.cuh"
 
@@ -30,12 +32,14 @@ namespace {
 
 bool bad_act(int act) { return act != MP_ACT_SILU && act != MP_ACT_GELU; }
 
-// Whether the forward takes the kernel for few tokens. One slice always: at h = 2304, f = 6144 it takes 20 us for a
-// token and 34 us for 128, the large tiles 43 to 48 us. Two slices while the weights fit in L2, so that the second
-// one finds them there: 35 to 44 us for 129 to 256 tokens against 44 to 45 (h = 1536, f = 4096: 22 to 28 against 36);
-// with weights of 400 MB (h = f = 8192) they took 97 to 111 us against 84 to 87, and three slices lose at h = 2304.
-bool few_tokens(int T, int h, int f) {
-    return T <= FEW_SLICE || (T <= 2 * FEW_SLICE && 6LL * h * f <= (1LL << 27));
+// Whether the forward takes the kernel for few tokens. One slice of them always (h = 2304, f = 6144: 20 us for a token,
+// 28 for 128, the large tiles 44). More while every slice's blocks of columns have an SM each and the weights stay
+// below twice L2's size, so that a slice finds them there: 384 tokens 38 us against 55; h = 1536, f = 4096, 512 tokens
+// 28 against 38; h = 1024, f = 2048, 1024 tokens 21 against 30; h = 4096, f = 8192, 256 tokens 55 against 62. Beyond:
+// a second round of CTAs takes 62 us against 56 (513 tokens, h = 2304), 400 MB of weights 97 against 87 (256 tokens).
+bool few_tokens(int T, int h, int f, int sms) {
+    const int slices = ceil_div(T, FEW_SLICE);
+    return slices == 1 || (ceil_div(std::max(h, f), 128) <= sms / slices && 6LL * h * f <= (1LL << 28));
 }
 
 }  // namespace
@@ -58,7 +62,7 @@ extern "C" mp_status mp_glu_fwd(const mp_bf16* X, const mp_bf16* W, const mp_bf1
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const double Tb = 2.0 * T, hb = 2.0 * h;
     const size_t f2 = size_t(2) * f;
-    if (few_tokens(T, h, f)) {
+    if (few_tokens(T, h, f, sms)) {
         st = launch_gemm_few<true>(X, W, Y, GU_save, T, h, f, static_cast<int>(f2), act, d_status, sms, s);
         return st != MP_OK ? st : launch_gemm_few<false>(Y, Wd, Z, nullptr, T, f, h, h, act, d_status, sms, s);
     }

@@ -85,6 +85,27 @@ def test_glu_matches_oracle_where_the_tokens_are_cut(T, h, f, t, act):
     test_glu_matches_oracle(T, h, f, t, act)
 
 
+@pytest.mark.parametrize("T,h,f,t", [
+    (257, 704, 6592, 1),     # large tiles: too many blocks of columns for three slices; an odd number of 64
+    (1000, 384, 2496, 3),
+    (1300, 192, 2048, 4),
+    (2500, 320, 1024, 1),
+    (20000, 64, 64, 1),
+])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_glu_matches_oracle_on_large_tiles(T, h, f, t, act):
+    test_glu_matches_oracle(T, h, f, t, act)
+
+
+def test_glu_large_tiles_do_not_depend_on_shards():
+    inp = _inputs(2600, 256, 1024, seed=21150)
+    ref = _run(inp, 1, "silu")
+    for t in (2, 4, 8):
+        got = _run(inp, t, "silu")
+        for k in ref:
+            assert torch.equal(got[k], ref[k]), (t, k)
+
+
 def test_glu_does_not_depend_on_shards_and_repeats_exactly():
     inp = _inputs(300, 256, 1024, seed=21100)
     ref = _run(inp, 1, "silu")
@@ -154,6 +175,21 @@ def test_glu_wait_budget_exhaustion(monkeypatch):
     inp = _inputs(256, 4096, 512, seed=21400)
     d = {k: v.cuda() for k, v in inp.items()}
     Z, Y = _nan(256, 4096), _nan(256, 512)
+    st = status_tensor()
+    monkeypatch.setenv("MPTP_WAIT_BUDGET_NS", "0")
+    mp().mp_glu_fwd(d["X"], d["W"], d["Wd"], Z, Y, None, t=1, d_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) & mp().MP_DEV_TIMEOUT
+    monkeypatch.delenv("MPTP_WAIT_BUDGET_NS")
+    got = _run(inp, 1, "silu", save=False)
+    want = oracle.glu_fwd(*(f64(inp[k]) for k in ("X", "W", "Wd")), "silu")
+    assert rel_fro(f64(got["Z"].cpu()), want[2]) <= TOL["Z"]
+
+
+def test_glu_wait_budget_exhaustion_on_large_tiles(monkeypatch):
+    inp = _inputs(2600, 2048, 1024, seed=21500)
+    d = {k: v.cuda() for k, v in inp.items()}
+    Z, Y = _nan(2600, 2048), _nan(2600, 1024)
     st = status_tensor()
     monkeypatch.setenv("MPTP_WAIT_BUDGET_NS", "0")
     mp().mp_glu_fwd(d["X"], d["W"], d["Wd"], Z, Y, None, t=1, d_status=st)
