@@ -54,6 +54,13 @@ inline BwdSchedule bwd_schedule() {
 
 // Cost of one output tile in K-block times: its K blocks plus about two for the epilogue.
 constexpr int EPI_KB = 2;
+// What a tile costs at least, its epilogue's time (2.3 us of stores): with one K block, products of 64 tokens, a plan by
+// K blocks left 432 tiles to seven pairs beside a long product, 144 us.
+constexpr int TILE_MIN_KB = 9;
+inline int tile_cost(const GemmArgs& a) {
+    const int cost = a.pr.kb_end - a.pr.kb_begin + EPI_KB;
+    return cost > TILE_MIN_KB ? cost : TILE_MIN_KB;
+}
 
 // Epilogue warps of K1 and K3 (GeLU, GeLU'). A launch's last tile is epilogued after its last
 // MMA with nothing to hide behind: with few K blocks per CTA pair (the layer at T = 2048,
@@ -128,8 +135,7 @@ inline mp_status launch_grad_gemms(TmapSet& m4, GemmArgs& a4, int bn4, const mp_
     // schedules give bitwise identical results.
     const int pairs = resident_pairs<256, EPI_STORE, 4>(sms);
     const int units[3] = {a4.pr.num_units, a5.pr.num_units, a6.pr.num_units};
-    const int cost[3] = {a4.pr.kb_end - a4.pr.kb_begin + EPI_KB, a5.pr.kb_end - a5.pr.kb_begin + EPI_KB,
-                         a6.pr.kb_end - a6.pr.kb_begin + EPI_KB};
+    const int cost[3] = {tile_cost(a4), tile_cost(a5), tile_cost(a6)};
     int split[3] = {pairs, pairs, pairs};
     const BwdSchedule mode = bwd_schedule();
     bool overlap = false;
