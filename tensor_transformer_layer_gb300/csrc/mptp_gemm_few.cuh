@@ -2,15 +2,15 @@
 // grid, which find W in L2.
 //
 // The roles of the operands are swapped against the large GEMM: the weight's columns are the rows of
-// the product (M = 128 of them, W as stored is the MN-major operand) and the tokens its columns, padded
-// to 16, so a CTA computes C^T[128, T] and a tile holds no more tokens than there are. (A 256 x 256 tile
+// the product (M = 128 of them, W as stored is the MN-major operand; for W^T its rows, K-major) and the tokens its
+// columns, padded to 16, so a CTA computes C^T[128, T] and a tile holds no more tokens than there are. (A 256 x 256 tile
 // would multiply mostly padding, and few such tiles exist: 6 to 48 for h = 1536 or f = 6144, a part of
 // the chip's 76 CTA pairs, each of which then reads a long K range alone.)
 //
 // The K range of a block of columns is split over the CTAs of a cluster, the largest size up to eight
 // whose clusters are all resident at once. Each CTA sends its fp32 partial sums through distributed
-// shared memory (four tokens a store) to the CTA that finishes those tokens, which adds them in rank
-// order: deterministic, in one launch and without a workspace.
+// shared memory (four tokens a store) to the CTA that finishes those tokens, which adds them to its own in
+// a fixed order: deterministic, in one launch and without a workspace.
 //
 //   warp 0: TMA producer, a ring of stages of 64 K rows x 128 columns (gated: 2 x 128) and the tokens' 64
 //           K elements. Before it waits for the previous kernel it asks L2 for the first stages' weights.
@@ -20,7 +20,7 @@
 // through h = 2304, f = 6144 (85 MB) 25 us. While it streams, a launch reads 7 TB/s; about 7 us go into the two
 // launches' set-up, first loads and joins, and 0.07 us a token into the join.
 //
-// Epilogues: plain store, or gated: 128 gate columns and the 128 up columns of the same outputs have an
+// Epilogues: plain store; the gated block's gradients from dY, G and U; or gated: 128 gate columns and the 128 up columns of the same outputs have an
 // accumulator each, so that a thread finds both in its TMEM lane; Y = act(gate) up is computed where the
 // sums meet (GU also stored when asked for).
 #pragma once
@@ -32,6 +32,13 @@
 
 namespace mptp {
 
+// The weight is MN-major (its columns are the product's rows) or, transposed products, K-major (its rows are).
+enum FewKind {
+    FEW_PLAIN,    // C = A W
+    FEW_GATED,    // Y = act(A Wg) * (A Wu), GU kept where asked for
+    FEW_PLAIN_T,  // C = A W^T
+    FEW_DGLU,     // dY = A W^T; dG = dY U act'(G), dU = dY act(G)
+};
 constexpr int FEW_SLICE = 128;   // tokens of a slice, at most
 constexpr int FEW_MAX_STAGES = 8;
 constexpr int FEW_MAX_PARTS = 2;  // warps of the epilogue per quarter of the tensor memory's lanes, at most
@@ -48,8 +55,8 @@ struct FewArgs {
     int cluster, stages;
     int parts;               // warps of the epilogue a quarter of the lanes: shares of the tokens
     int act;
-    __nv_bfloat16* out;      // [T, cols]
-    __nv_bfloat16* gu;       // gated, nullable: [T, 2 cols]
+    __nv_bfloat16* out;      // [T, cols]; dGLU: [T, 2 cols]
+    __nv_bfloat16* gu;       // [T, 2 cols]; gated, nullable: written; dGLU: read
     uint32_t* status;
     unsigned long long budget_ns;
 };
@@ -93,10 +100,11 @@ __device__ __forceinline__ bool wait_polled(uint64_t* bar, uint32_t parity, cons
     }
 }
 
-template <bool GATED>
+template <int KIND>
 __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                const __grid_constant__ CUtensorMap tmA,
                                                                const FewArgs args) {
+    constexpr bool GATED = KIND == FEW_GATED, W_T = KIND == FEW_PLAIN_T || KIND == FEW_DGLU;
     constexpr int NACC = GATED ? 2 : 1;            // accumulators: gate and up
     constexpr int W_STAGE = 2 * NACC * FEW_W_BYTES;
     extern __shared__ uint8_t smem_raw[];
@@ -142,9 +150,13 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
         fence_proxy_async_smem();
         // Into L2 only: whatever the previous kernel may still write is read after the wait below.
         for (int kb = kb0; kb < kb1 && kb < kb0 + stages; ++kb)
+            if constexpr (W_T) {
+                tma_prefetch_2d(&tmW, kb * BK, block * 128);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 2 * NACC; ++i)
-                if (w_col(i) < args.w_cols) tma_prefetch_2d(&tmW, w_col(i), kb * BK);
+                for (int i = 0; i < 2 * NACC; ++i)
+                    if (w_col(i) < args.w_cols) tma_prefetch_2d(&tmW, w_col(i), kb * BK);
+            }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, tmem_cols);
@@ -165,9 +177,13 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wait_bounded(&empty[st], ph ^ 1u, ctl)) break;
                 mbar_arrive_expect_tx(&full[st], W_STAGE + npad * 128);
+                if constexpr (W_T) {
+                    tma_load_2d(sW + st * W_STAGE, &tmW, &full[st], kb * BK, block * 128);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 2 * NACC; ++i)
-                    tma_load_2d(sW + st * W_STAGE + i * FEW_W_BYTES, &tmW, &full[st], w_col(i), kb * BK);
+                    for (int i = 0; i < 2 * NACC; ++i)
+                        tma_load_2d(sW + st * W_STAGE + i * FEW_W_BYTES, &tmW, &full[st], w_col(i), kb * BK);
+                }
                 tma_load_2d(sA + st * npad * 128, &tmA, &full[st], kb * BK, t0);
                 if (++st == stages) {
                     st = 0;
@@ -176,8 +192,9 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
             }
         }
     } else if (warp == 1) {
-        const uint32_t idesc = make_idesc_bf16(128, npad, true, false);
-        const uint64_t w_desc = make_sdesc_sw128(smem_u32(sW), FEW_W_BYTES, 1024);
+        const uint32_t idesc = make_idesc_bf16(128, npad, !W_T, false);
+        const uint64_t w_desc = make_sdesc_sw128(smem_u32(sW), W_T ? 16 : FEW_W_BYTES, 1024);
+        constexpr int W_STEP = W_T ? 32 : 2048;  // bytes from one product's rows of K to the next's
         const uint64_t a_desc = make_sdesc_sw128(smem_u32(sA), 16, 1024);
         int st = 0;
         uint32_t ph = 0;
@@ -192,7 +209,7 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
             for (int k = 0; k < BK / UMMA_K; ++k)
 #pragma unroll
                 for (int c = 0; c < NACC; ++c)
-                    umma_bf16_elect(tmem_base + c * npad, wd + c * (2 * FEW_W_BYTES >> 4) + k * (2048 >> 4),
+                    umma_bf16_elect(tmem_base + c * npad, wd + c * (2 * FEW_W_BYTES >> 4) + k * (W_STEP >> 4),
                                     ad + k * (32 >> 4), idesc, kb > kb0 || k > 0 ? 1u : 0u);
             umma_commit_elect(&empty[st]);
             if (++st == stages) {
@@ -257,6 +274,15 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
         const int c0 = rank * slice, c1 = min(T, c0 + slice);
 #pragma unroll 1
         for (int c = c0 + part * 4 * G; c < c1; c += parts * 4 * G) {
+            float gate[G * 4], up[G * 4];
+            if constexpr (KIND == FEW_DGLU) {
+                const __nv_bfloat16* gu = args.gu + static_cast<long long>(t0 + c) * 2 * args.cols + block * 128 + col;
+#pragma unroll
+                for (int k = 0; k < G * 4; ++k, gu += 2 * args.cols) {
+                    gate[k] = c + k < c1 ? __bfloat162float(gu[0]) : 0.0f;
+                    up[k] = c + k < c1 ? __bfloat162float(gu[args.cols]) : 0.0f;
+                }
+            }
             uint32_t own[G][NACC][4];
 #pragma unroll
             for (int g = 0; g < G; ++g)
@@ -291,28 +317,47 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
                             sum[g][i][3] += v.w;
                         }
             }
-            float y[G * 4];
+            if constexpr (KIND == FEW_DGLU) {
+                __nv_bfloat16* out = args.out + static_cast<long long>(t0 + c) * 2 * args.cols + block * 128 + col;
 #pragma unroll
-            for (int k = 0; k < G * 4; k += 2) {
-                float2 v = make_float2(sum[k / 4][0][k % 4], sum[k / 4][0][k % 4 + 1]);
-                if constexpr (GATED)
-                    v = mul2(glu_act2(v, args.act), make_float2(sum[k / 4][1][k % 4], sum[k / 4][1][k % 4 + 1]));
-                y[k] = v.x, y[k + 1] = v.y;
-            }
-            __nv_bfloat16* out = args.out + static_cast<long long>(t0 + c) * args.cols + block * 128 + col;
-#pragma unroll
-            for (int k = 0; k < G * 4; ++k, out += args.cols)
-                if (c + k < c1) *out = __float2bfloat16(y[k]);
-            if constexpr (GATED)
-                if (args.gu) {
-                    __nv_bfloat16* gu = args.gu + static_cast<long long>(t0 + c) * 2 * args.cols + block * 128 + col;
-#pragma unroll
-                    for (int k = 0; k < G * 4; ++k, gu += 2 * args.cols)
-                        if (c + k < c1) {
-                            gu[0] = __float2bfloat16(sum[k / 4][0][k % 4]);
-                            gu[args.cols] = __float2bfloat16(sum[k / 4][1][k % 4]);
-                        }
+                for (int k = 0; k < G * 4; k += 2, out += 4 * args.cols) {
+                    const float2 dy = make_float2(sum[k / 4][0][k % 4], sum[k / 4][0][k % 4 + 1]);
+                    float2 act, slope;
+                    glu_act_grad2(make_float2(gate[k], gate[k + 1]), args.act, act, slope);
+                    const float2 dg = mul2(mul2(dy, make_float2(up[k], up[k + 1])), slope), du = mul2(dy, act);
+                    if (c + k < c1) {
+                        out[0] = __float2bfloat16(dg.x);
+                        out[args.cols] = __float2bfloat16(du.x);
+                    }
+                    if (c + k + 1 < c1) {
+                        out[2 * args.cols] = __float2bfloat16(dg.y);
+                        out[3 * args.cols] = __float2bfloat16(du.y);
+                    }
                 }
+            } else {
+                float y[G * 4];
+#pragma unroll
+                for (int k = 0; k < G * 4; k += 2) {
+                    float2 v = make_float2(sum[k / 4][0][k % 4], sum[k / 4][0][k % 4 + 1]);
+                    if constexpr (GATED)
+                        v = mul2(glu_act2(v, args.act), make_float2(sum[k / 4][1][k % 4], sum[k / 4][1][k % 4 + 1]));
+                    y[k] = v.x, y[k + 1] = v.y;
+                }
+                __nv_bfloat16* out = args.out + static_cast<long long>(t0 + c) * args.cols + block * 128 + col;
+#pragma unroll
+                for (int k = 0; k < G * 4; ++k, out += args.cols)
+                    if (c + k < c1) *out = __float2bfloat16(y[k]);
+                if constexpr (GATED)
+                    if (args.gu) {
+                        __nv_bfloat16* gu = args.gu + static_cast<long long>(t0 + c) * 2 * args.cols + block * 128 + col;
+#pragma unroll
+                        for (int k = 0; k < G * 4; ++k, gu += 2 * args.cols)
+                            if (c + k < c1) {
+                                gu[0] = __float2bfloat16(sum[k / 4][0][k % 4]);
+                                gu[args.cols] = __float2bfloat16(sum[k / 4][1][k % 4]);
+                            }
+                    }
+            }
         }
     }
 
@@ -331,7 +376,7 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
 }
 
 // Clusters of `cluster` CTAs of this kernel that are resident at once.
-template <bool GATED>
+template <int KIND>
 inline int few_resident_clusters(int cluster, size_t smem, int num_sms) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster * num_sms, 1, 1);
@@ -345,17 +390,18 @@ inline int few_resident_clusters(int cluster, size_t smem, int num_sms) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, gemm_few_kernel<GATED>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_few_kernel<KIND>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
     return n;
 }
 
-// C[T, cols] = A[T, K] W[K, ...]; W's rows are `ldw` columns wide.
-template <bool GATED>
+// C[T, cols] = A[T, K] W[K, ...], or A W^T with W [cols, K]; W's rows are `ldw` columns wide.
+template <int KIND>
 inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* out, mp_bf16* gu, int T, int K, int cols,
                                  int ldw, int act, uint32_t* status, int num_sms, cudaStream_t stream) {
+    constexpr bool GATED = KIND == FEW_GATED, W_T = KIND == FEW_PLAIN_T || KIND == FEW_DGLU;
     FewArgs a{};
     a.T = T;
     a.blocks = ceil_div(cols, 128);
@@ -378,8 +424,10 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
     a.status = status;
     a.budget_ns = wait_budget_ns();
     CUtensorMap tw, ta;
-    if (!make_tmap_bf16(&tw, W, ldw, K, ldw, 64, 64) || !make_tmap_bf16(&ta, A, K, T, K, 64, a.npad)) return MP_ERR_CUDA;
-    auto kern = gemm_few_kernel<GATED>;
+    if (!(W_T ? make_tmap_bf16(&tw, W, K, cols, ldw, 64, 128) : make_tmap_bf16(&tw, W, ldw, K, ldw, 64, 64)) ||
+        !make_tmap_bf16(&ta, A, K, T, K, 64, a.npad))
+        return MP_ERR_CUDA;
+    auto kern = gemm_few_kernel<KIND>;
     const int clusters = a.blocks * slices;
     auto fit_stages = [&](int cluster) {
         int n = FEW_MAX_STAGES;
@@ -398,7 +446,7 @@ inline mp_status launch_gemm_few(const mp_bf16* A, const mp_bf16* W, mp_bf16* ou
         std::atomic<int>* slot = dev < 16 ? &cached[dev][c] : nullptr;
         int n = slot ? slot->load(std::memory_order_relaxed) : 0;
         if (n == 0) {
-            n = few_resident_clusters<GATED>(c, SMEM_LIMIT, num_sms);
+            n = few_resident_clusters<KIND>(c, SMEM_LIMIT, num_sms);
             if (slot) slot->store(n > 0 ? n : -1, std::memory_order_relaxed);
         }
         if (clusters <= n) {

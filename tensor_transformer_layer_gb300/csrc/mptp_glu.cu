@@ -42,6 +42,10 @@ bool few_tokens(int T, int h, int f, int sms) {
     return slices == 1 || (ceil_div(std::max(h, f), 128) <= sms / slices && 6LL * h * f <= (1LL << 28));
 }
 
+// The backward takes it up to three slices: h = 2304, f = 6144 50 us against 86 with the large tiles for a token, 63 for
+// 128, 88 against 90 for 384, more than 100 against 88 for 512; h = 704, f = 3136 25 against 52, 31, 40 against 55.
+constexpr int FEW_BWD_SLICES = 3;
+
 }  // namespace
 
 extern "C" mp_status mp_glu_fwd(const mp_bf16* X, const mp_bf16* W, const mp_bf16* Wd, mp_bf16* Z, mp_bf16* Y,
@@ -63,8 +67,8 @@ extern "C" mp_status mp_glu_fwd(const mp_bf16* X, const mp_bf16* W, const mp_bf1
     const double Tb = 2.0 * T, hb = 2.0 * h;
     const size_t f2 = size_t(2) * f;
     if (few_tokens(T, h, f, sms)) {
-        st = launch_gemm_few<true>(X, W, Y, GU_save, T, h, f, static_cast<int>(f2), act, d_status, sms, s);
-        return st != MP_OK ? st : launch_gemm_few<false>(Y, Wd, Z, nullptr, T, f, h, h, act, d_status, sms, s);
+        st = launch_gemm_few<FEW_GATED>(X, W, Y, GU_save, T, h, f, static_cast<int>(f2), act, d_status, sms, s);
+        return st != MP_OK ? st : launch_gemm_few<FEW_PLAIN>(Y, Wd, Z, nullptr, T, f, h, h, act, d_status, sms, s);
     }
 
     // [G | U] = X W and Y = act(G) * U, tiles of 128 outputs.
@@ -125,6 +129,41 @@ extern "C" mp_status mp_glu_bwd(const mp_bf16* X, const mp_bf16* W, const mp_bf1
     }
     const double Tb = 2.0 * T, hb = 2.0 * h;
 
+    // dW = X^T dGU (both operands MN-major).
+    TmapSet m5{};
+    int a5f = 0, b5f = 0;
+    if (!(a5f = make_tmap_mn_operand(&m5.a, X, h, T, h)) || !(b5f = make_tmap_mn_operand(&m5.b, dGU_ws, f2, T, f2)) ||
+        !make_tmap_bf16_out(&m5.o0, dW, f2, h, f2))
+        return MP_ERR_CUDA;
+    GemmArgs a5 = launch_args(d_status);
+    a5.pr = problem(h, 2 * f, 256, 0, ceil_div(T, BK), true, true, Tb * h, 2 * Tb * f);
+    a5.pr.a_mn = a5f;
+    a5.pr.b_mn = b5f;
+
+    // dWd = Y^T dZ (both operands MN-major).
+    TmapSet m6{};
+    int a6f = 0, b6f = 0;
+    if (!(a6f = make_tmap_mn_operand(&m6.a, Y, f, T, f)) || !(b6f = make_tmap_mn_operand(&m6.b, dZ, h, T, h)) ||
+        !make_tmap_bf16_out(&m6.o0, dWd, h, f, h))
+        return MP_ERR_CUDA;
+    GemmArgs a6 = launch_args(d_status);
+    a6.pr = problem(f, h, 256, 0, ceil_div(T, BK), true, true, Tb * f, Tb * h);
+    a6.pr.a_mn = a6f;
+    a6.pr.b_mn = b6f;
+    if (T <= FEW_BWD_SLICES * FEW_SLICE && few_tokens(T, h, f, sms)) {
+        // dY with dG, dU, then dX by the kernel for few tokens. The weights' gradients are bound by their stores: eight
+        // epilogue warps, h = 2304, f = 6144, one token 50.5 us for all four launches against 57.7 with four.
+        st = launch_gemm_few<FEW_DGLU>(dZ, Wd, dGU_ws, const_cast<mp_bf16*>(GU), T, h, f, h, act, d_status, sms, s);
+        if (st == MP_OK)
+            st = launch_gemm_few<FEW_PLAIN_T>(dGU_ws, W, dX, nullptr, T, static_cast<int>(f2), h, static_cast<int>(f2), act,
+                                              d_status, sms, s);
+        if (st != MP_OK) return st;
+        return launch_gemm_tc<256, EPI_STORE, 8>(m5, a5, sms, s) == cudaSuccess &&
+                       launch_gemm_tc<256, EPI_STORE, 8>(m6, a6, sms, s) == cudaSuccess
+                   ? MP_OK
+                   : MP_ERR_CUDA;
+    }
+
     // dY = dZ Wd^T; dG, dU in its epilogue.
     TmapSet m3{};
     if (!make_tmap_bf16(&m3.a, dZ, h, T, h, 64, BM) || !make_tmap_bf16(&m3.b, Wd, h, f, h, 64, 128) ||
@@ -150,26 +189,5 @@ extern "C" mp_status mp_glu_bwd(const mp_bf16* X, const mp_bf16* W, const mp_bf1
     GemmArgs a4 = launch_args(d_status);
     a4.pr = problem(T, h, bn4, 0, 2 * (f / BK), false, false, 2 * Tb * f, 2 * hb * f);
 
-    // dW = X^T dGU (both operands MN-major).
-    TmapSet m5{};
-    int a5f = 0, b5f = 0;
-    if (!(a5f = make_tmap_mn_operand(&m5.a, X, h, T, h)) || !(b5f = make_tmap_mn_operand(&m5.b, dGU_ws, f2, T, f2)) ||
-        !make_tmap_bf16_out(&m5.o0, dW, f2, h, f2))
-        return MP_ERR_CUDA;
-    GemmArgs a5 = launch_args(d_status);
-    a5.pr = problem(h, 2 * f, 256, 0, ceil_div(T, BK), true, true, Tb * h, 2 * Tb * f);
-    a5.pr.a_mn = a5f;
-    a5.pr.b_mn = b5f;
-
-    // dWd = Y^T dZ (both operands MN-major).
-    TmapSet m6{};
-    int a6f = 0, b6f = 0;
-    if (!(a6f = make_tmap_mn_operand(&m6.a, Y, f, T, f)) || !(b6f = make_tmap_mn_operand(&m6.b, dZ, h, T, h)) ||
-        !make_tmap_bf16_out(&m6.o0, dWd, h, f, h))
-        return MP_ERR_CUDA;
-    GemmArgs a6 = launch_args(d_status);
-    a6.pr = problem(f, h, 256, 0, ceil_div(T, BK), true, true, Tb * f, Tb * h);
-    a6.pr.a_mn = a6f;
-    a6.pr.b_mn = b6f;
     return launch_grad_gemms(m4, a4, bn4, W, static_cast<int>(f2), m5, a5, m6, a6, sms, s);
 }

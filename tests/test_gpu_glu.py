@@ -199,3 +199,20 @@ def test_glu_wait_budget_exhaustion_on_large_tiles(monkeypatch):
     got = _run(inp, 1, "silu", save=False)
     want = oracle.glu_fwd(*(f64(inp[k]) for k in ("X", "W", "Wd")), "silu")
     assert rel_fro(f64(got["Z"].cpu()), want[2]) <= TOL["Z"]
+
+
+def test_glu_bwd_wait_budget_exhaustion_with_few_tokens(monkeypatch):
+    inp = _inputs(64, 4096, 512, seed=21600)
+    good = _run(inp, 1, "silu")
+    d = {k: v.cuda() for k, v in inp.items()}
+    o = {"dX": _nan(64, 4096), "dW": _nan(4096, 1024), "dWd": _nan(512, 4096), "dGU": _nan(64, 1024)}
+    st = status_tensor()
+    monkeypatch.setenv("MPTP_WAIT_BUDGET_NS", "0")
+    mp().mp_glu_bwd(d["X"], d["W"], d["Wd"], good["GU"], good["Y"], d["dZ"], o["dX"], o["dW"], o["dWd"], o["dGU"], t=1,
+                    act="silu", d_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) & mp().MP_DEV_TIMEOUT
+    monkeypatch.delenv("MPTP_WAIT_BUDGET_NS")
+    again = _run(inp, 1, "silu")
+    for k in good:
+        assert torch.equal(again[k], good[k]), k
