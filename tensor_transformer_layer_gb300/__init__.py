@@ -23,6 +23,7 @@ Shapes (row-major, contiguous):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -468,25 +469,32 @@ def _heads_view(x, name, shape=None):
     return x.data_ptr(), pitch
 
 
+@functools.lru_cache(maxsize=64)
+def _int_array(values):
+    """Length and C array of a tuple of ints (read only)."""
+    return len(values), (_I * max(len(values), 1))(*(int(v) for v in values))
+
+
 def mp_rope_axes(x, y, pos, *, sections, base: float = 10000.0, interleaved: bool = False, per_axis: bool = False,
                  inverse: bool = False, stream=None) -> None:
     """Rotary positions with up to four axes: y = x with each head's pairs rotated by pos[axis] * frequency.
     x, y [T, heads, d] (rows may be strided; y may be x), pos [axes, T] int32, sections: pairs of each axis.
     inverse rotates back (the gradient)."""
-    T, heads, d = x.shape
-    px, ldx = _heads_view(x, "x")
-    py, ldy = _heads_view(y, "y", shape=(T, heads, d))
-    sec = [int(v) for v in sections]
+    size = tuple(x.shape)
+    px, ldx = _heads_view(x, "x", size if len(size) == 3 else None)
+    py, ldy = _heads_view(y, "y", size)
+    T, heads, d = size
+    axes, sec = _int_array(tuple(sections))
     flags = (1 if interleaved else 0) | (2 if per_axis else 0) | (4 if inverse else 0)
-    code = lib().mp_rope_axes(px, py, _ptr(pos, "pos", dtype=torch.int32, shape=(len(sec), T)), T, heads, d, ldx, ldy,
-                              len(sec), (_I * max(len(sec), 1))(*sec), float(base), flags, _stream(stream))
+    code = lib().mp_rope_axes(px, py, _ptr(pos, "pos", torch.int32, (axes, T)), T, heads, d, ldx, ldy, axes, sec,
+                              float(base), flags, _stream(stream))
     _check("mp_rope_axes", code)
 
 
 def _packed_shapes(Q, K, cu_q, cu_k):
     if not isinstance(Q, torch.Tensor) or not isinstance(K, torch.Tensor):
         raise ValueError("Q and K must be [tokens, heads, d] tensors")
-    qs, ks = Q.shape, K.shape
+    qs, ks = tuple(Q.shape), tuple(K.shape)
     if len(qs) != 3 or len(ks) != 3:
         raise ValueError("Q and K must be [tokens, heads, d] tensors")
     if qs[2] != ks[2]:
