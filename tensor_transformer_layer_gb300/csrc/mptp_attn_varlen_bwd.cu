@@ -211,11 +211,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     umma_bf16_elect(d, a + off, b + off, IDESC_S, k > 0 ? 1u : 0u);
                 }
             };
-            auto k_wait = [&](int j) {
-                if (!wait_all(&k_full[j % KST], (j / KST) & 1)) return false;
-                if (j == n - 1 && k_tail < AV_TILE) av_clear_rows<D>(sK + (j % KST) * T::BYTES, k_tail, lane);
-                return true;
-            };
+            auto k_wait = [&](int j) { return wait_all(&k_full[j % KST], (j / KST) & 1); };
             auto s_mma = [&](int j) {
                 score(tmem_base + (j & 1) * 128, q_desc, k_desc + static_cast<uint32_t>(((j % KST) * T::BYTES) >> 4));
                 umma_commit_elect(&s_full[j & 1]);
@@ -245,6 +241,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             for (int j = 0; j < n && ok; ++j) {
                 const bool more = j + 1 < n;
                 if (more && !(ok = wait_all(&v_full[(j + 1) % VST], ((j + 1) / VST) & 1))) break;
+                // The foreign rows of the last key tile, which dQ sums over: S needs no clearing, its columns are masked.
+                if (!more && k_tail < AV_TILE) av_clear_rows<D>(sK + (j % KST) * T::BYTES, k_tail, lane);
                 if (!(ok = wait_all(ds_full, j & 1))) break;
                 tc_fence_after();
                 if (more) dp_mma(j + 1);
