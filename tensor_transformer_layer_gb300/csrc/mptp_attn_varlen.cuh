@@ -92,6 +92,19 @@ __device__ __forceinline__ bool av_pick(const AvArgs& a, int item, AvSpan& sp, i
     return false;
 }
 
+// A place in a ring of N tiles, counted along by the warp that issues the products.
+template <int N>
+struct AvRing {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == N) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
 // One tile (rows from `row`, head `head` of the matrix) into shared memory, counted on `bar`: D/32 boxes by one
 // load.
 template <int D>

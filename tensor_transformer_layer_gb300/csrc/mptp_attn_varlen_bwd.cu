@@ -29,8 +29,9 @@
 //   distributed shared memory in rank order.
 // In the first, a softmax thread has one row and 64 of its 128 columns; in the second, four keys' fragments.
 // Both are bound by the hand-overs between softmax and products (tensor core 65 to 67 % active at D = 128): 4096
-// tokens, 19 heads, not causal, dQ 116, 139, 166 us and dK with dV 140, 181, 213 us for D = 64, 96, 128 (1.05 to 1.47
-// and 1.16 to 1.53 PFLOP/s). Sixteen softmax warps of half the columns each were 1 to 10 % slower.
+// tokens, 19 heads, not causal, dQ 113, 132, 158 us and dK with dV 138, 179, 208 us for D = 64, 96, 128 (1.08 to 1.55
+// and 1.18 to 1.57 PFLOP/s). The warp that issues the products is on the way between them: rings counted along instead
+// of remainders, and no clearing between a wait and a product, took dQ from 139 and 166 us at D = 96 and 128. Sixteen softmax warps of half the columns each were 1 to 10 % slower.
 //
 // P and dS are rounded to bf16 for their products (the tensor core's operand type); the exponent,
 // delta, and every sum are fp32. Hidden pairs are replaced by zero after the arithmetic, and rows of a
@@ -211,52 +212,63 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     umma_bf16_elect(d, a + off, b + off, IDESC_S, k > 0 ? 1u : 0u);
                 }
             };
-            auto k_wait = [&](int j) { return wait_all(&k_full[j % KST], (j / KST) & 1); };
-            auto s_mma = [&](int j) {
-                score(tmem_base + (j & 1) * 128, q_desc, k_desc + static_cast<uint32_t>(((j % KST) * T::BYTES) >> 4));
-                umma_commit_elect(&s_full[j & 1]);
+            AvRing<KST> k_next, k_sum;  // K tiles of the next S and of the next dQ
+            AvRing<VST> v_next;
+            auto k_wait = [&]() { return wait_all(&k_full[k_next.st], k_next.ph); };
+            auto v_wait = [&]() { return wait_all(&v_full[v_next.st], v_next.ph); };
+            auto s_mma = [&](int buf) {
+                score(tmem_base + buf * 128, q_desc, k_desc + static_cast<uint32_t>((k_next.st * T::BYTES) >> 4));
+                umma_commit_elect(&s_full[buf]);
+                k_next.next();
             };
-            auto dp_mma = [&](int j) {
-                score(tmem_base + 256, do_desc, v_desc + static_cast<uint32_t>(((j % VST) * T::BYTES) >> 4));
+            auto dp_mma = [&]() {
+                score(tmem_base + 256, do_desc, v_desc + static_cast<uint32_t>((v_next.st * T::BYTES) >> 4));
                 umma_commit_elect(dp_full);
-                umma_commit_elect(&v_empty[j % VST]);
+                umma_commit_elect(&v_empty[v_next.st]);
+                v_next.next();
             };
-            bool ok = n > 0 && wait_all(q_full, 0) && k_wait(0);
+            bool ok = n > 0 && wait_all(q_full, 0) && k_wait();
             if (ok) {
                 tc_fence_after();
                 s_mma(0);
-                ok = wait_all(do_full, 0) && wait_all(&v_full[0], 0);
+                ok = wait_all(do_full, 0) && v_wait();
                 if (ok) {
                     tc_fence_after();
-                    dp_mma(0);
+                    dp_mma();
                 }
             }
             // One wait on the softmax an iteration, and three products behind it: dP(j+1), which it needs next,
             // dQ(j), and S(j+2) over dS(j) once that has been used. (With a wait before each of the products the
-            // tensor core ran dry at every one: 2140 cycles an iteration at D = 128, 1536 of them products.)
-            if (ok && n > 1 && (ok = k_wait(1))) {
+            // tensor core ran dry at every one: 2140 cycles an iteration at D = 128, 1536 of them products.) With
+            // four K tiles the one of S(j+2) is here before that wait.
+            constexpr bool K_EARLY = false;
+            if (ok && n > 1 && (ok = k_wait())) {
                 tc_fence_after();
                 s_mma(1);
             }
             for (int j = 0; j < n && ok; ++j) {
-                const bool more = j + 1 < n;
-                if (more && !(ok = wait_all(&v_full[(j + 1) % VST], ((j + 1) / VST) & 1))) break;
+                const bool more = j + 1 < n, ahead = j + 2 < n;
+                if (more && !(ok = v_wait())) break;
+                if (K_EARLY && ahead && !(ok = k_wait())) break;
                 // The foreign rows of the last key tile, which dQ sums over: S needs no clearing, its columns are masked.
-                if (!more && k_tail < AV_TILE) av_clear_rows<D>(sK + (j % KST) * T::BYTES, k_tail, lane);
+                if (!more && k_tail < AV_TILE) av_clear_rows<D>(sK + k_sum.st * T::BYTES, k_tail, lane);
                 if (!(ok = wait_all(ds_full, j & 1))) break;
                 tc_fence_after();
-                if (more) dp_mma(j + 1);
-                const uint64_t kd = kt_desc + static_cast<uint32_t>(((j % KST) * T::BYTES) >> 4);
+                if (more) dp_mma();
+                const uint64_t kd = kt_desc + static_cast<uint32_t>((k_sum.st * T::BYTES) >> 4);
                 const uint32_t acc0 = j > 0 ? 1u : 0u;
 #pragma unroll
                 for (int k = 0; k < AV_TILE / 16; ++k)
                     umma_bf16_ts_elect(tmem_base + 384, av_a_step(tmem_base + (j & 1) * 128, k), kd + ((k * 1024) >> 4),
                                        IDESC_DQ, k > 0 ? 1u : acc0);
-                umma_commit_elect(&k_empty[j % KST]);
-                if (j + 2 < n) {
-                    if (!(ok = k_wait(j + 2))) break;
-                    tc_fence_after();
-                    s_mma(j + 2);
+                umma_commit_elect(&k_empty[k_sum.st]);
+                k_sum.next();
+                if (ahead) {
+                    if (!K_EARLY) {
+                        if (!(ok = k_wait())) break;
+                        tc_fence_after();
+                    }
+                    s_mma(j & 1);
                 }
             }
             if (ok) umma_commit_elect(dq_full);
@@ -410,9 +422,6 @@ struct AvDkvCfg {
     static constexpr int QST = D == 128 ? 3 : 4;  // a Q tile serves S(i) and, later, dK(i)
     static constexpr int OST = D == 64 ? 4 : D == 96 ? 3 : 2;  // dO: dP(i), then dV(i)
     static constexpr int SST = 2;                 // row statistics
-    // Warpgroup 0 needs fewer registers than in the other kernels, and at D = 64 takes 140 us with these against 143.5
-    // (4096 tokens, 19 heads).
-    static constexpr int REGS_CTRL = 72;
     static constexpr int NUM_BARS = 1 + 2 * QST + 2 * OST + 2 * SST + 8 + 1;
     // 512-byte alignment is what the 64-byte swizzle needs; at D = 128 no more fits
     static constexpr size_t SMEM = 512 + (2 + QST + OST) * size_t(T::BYTES) + SST * 2 * AV_TILE * 4 + 8 * NUM_BARS + 16;
@@ -569,7 +578,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     };
 
     if (warp < 4) {
-        reg_dealloc<Cfg::REGS_CTRL>();
+        reg_dealloc<T::REGS_CTRL>();
         if (warp == 0) {
             if (lane == 0) {
                 // ---------------- TMA producer ----------------
@@ -610,50 +619,55 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     umma_bf16_ts_elect(d, a + (k >> 2) * half + (k & 3) * 8, b + ((k * 1024) >> 4), IDESC_G,
                                        k > 0 || !fresh ? 1u : 0u);
             };
-            auto q_off = [&](int it) { return static_cast<uint32_t>(((it % QST) * T::BYTES) >> 4); };
-            auto do_off = [&](int it) { return static_cast<uint32_t>(((it % OST) * T::BYTES) >> 4); };
+            AvRing<QST> q_ahead, q_sum;            // Q tiles of the next S^T and of the next dK
+            AvRing<OST> do_ahead, do_dp, do_sum;   // dO tiles waited for, of the next dP^T and of the next dV
+            auto off = [&](int st) { return static_cast<uint32_t>((st * T::BYTES) >> 4); };
             Walk ahead = first;  // the iteration whose tiles have been waited for
-            auto tiles_wait = [&](int it) {
-                if (!wait_all(&q_full[it % QST], (it / QST) & 1) || !wait_all(&do_full[it % OST], (it / OST) & 1))
-                    return false;
+            auto tiles_wait = [&]() {
+                if (!wait_all(&q_full[q_ahead.st], q_ahead.ph) || !wait_all(&do_full[do_ahead.st], do_ahead.ph)) return false;
                 if (q_tail < AV_TILE && ahead.tile == t1 - 1) {
-                    av_clear_rows<D>(sQ + (it % QST) * T::BYTES, q_tail, lane);
-                    av_clear_rows<D>(sdO + (it % OST) * T::BYTES, q_tail, lane);
+                    av_clear_rows<D>(sQ + q_ahead.st * T::BYTES, q_tail, lane);
+                    av_clear_rows<D>(sdO + do_ahead.st * T::BYTES, q_tail, lane);
                 }
+                do_ahead.next();
                 return true;
             };
             auto s_buf = [&](int it) { return Cfg::S_BUFS == 2 ? (it & 1) : 0; };
             auto s_mma = [&](int it) {
-                score(tmem_base + s_buf(it) * 128, k_desc, q_desc + q_off(it));
+                score(tmem_base + s_buf(it) * 128, k_desc, q_desc + off(q_ahead.st));
                 umma_commit_elect(&s_full[s_buf(it)]);
+                q_ahead.next();
             };
-            auto dp_mma = [&](int it) {
-                score(tmem_base + Cfg::DP_COL, v_desc, do_desc + do_off(it));
+            auto dp_mma = [&]() {
+                score(tmem_base + Cfg::DP_COL, v_desc, do_desc + off(do_dp.st));
                 umma_commit_elect(dp_full);
+                do_dp.next();
             };
             auto dv_mma = [&](int it) {  // dV += P^T dO
                 grad(tmem_base + Cfg::DV_COL, tmem_base + (Cfg::OWN_P ? Cfg::P_COL : s_buf(it) * 128), Cfg::P_HALF,
-                     dot_desc + do_off(it), it == 0);
-                umma_commit_elect(&do_empty[it % OST]);
+                     dot_desc + off(do_sum.st), it == 0);
+                umma_commit_elect(&do_empty[do_sum.st]);
+                do_sum.next();
                 if (Cfg::OWN_P) umma_commit_elect(dv_done);
             };
             auto dk_mma = [&](int it) {  // dK += dS^T Q
                 grad(tmem_base + Cfg::DK_COL, tmem_base + (Cfg::DS_IN_S ? s_buf(it) * 128 + 32 : Cfg::DP_COL), 64,
-                     qt_desc + q_off(it), it == 0);
-                umma_commit_elect(&q_empty[it % QST]);
+                     qt_desc + off(q_sum.st), it == 0);
+                umma_commit_elect(&q_empty[q_sum.st]);
+                q_sum.next();
             };
-            bool ok = n > 0 && wait_all(kv_full, 0) && tiles_wait(0);
+            bool ok = n > 0 && wait_all(kv_full, 0) && tiles_wait();
             if (ok) {
                 tc_fence_after();
                 s_mma(0);
-                dp_mma(0);
+                dp_mma();
             }
             if constexpr (Cfg::BATCH) {
                 // One wait on the softmax an iteration, and all its products behind it, dP^T (which the softmax
                 // needs next) as soon as its columns are free; S^T runs two iterations ahead.
                 auto s_ahead = [&](int it) -> bool {  // S^T(it): over P^T(it-2), or once S^T(it-1) has been read
                     ahead.next();
-                    if (!tiles_wait(it) || (Cfg::S_BUFS == 1 && !wait_all(s_read, (it - 1) & 1))) return false;
+                    if (!tiles_wait() || (Cfg::S_BUFS == 1 && !wait_all(s_read, (it - 1) & 1))) return false;
                     tc_fence_after();
                     s_mma(it);
                     return true;
@@ -663,7 +677,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     if (!(ok = wait_all(ds_full, it & 1))) break;
                     tc_fence_after();
                     if (!Cfg::DS_IN_S) dk_mma(it);
-                    if (it + 1 < n) dp_mma(it + 1);
+                    if (it + 1 < n) dp_mma();
                     dv_mma(it);
                     if (Cfg::DS_IN_S) dk_mma(it);
                     if (it + 2 < n) ok = s_ahead(it + 2);
@@ -675,7 +689,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     const bool more = it + 1 < n;
                     if (more) {
                         ahead.next();
-                        if (!(ok = tiles_wait(it + 1))) break;
+                        if (!(ok = tiles_wait())) break;
                     }
                     if (!(ok = wait_all(p_full, it & 1))) break;
                     tc_fence_after();
@@ -684,7 +698,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     if (!(ok = wait_all(ds_full, it & 1))) break;
                     tc_fence_after();
                     dk_mma(it);
-                    if (more) dp_mma(it + 1);
+                    if (more) dp_mma();
                 }
             }
             if (ok) umma_commit_elect(fin_full);
