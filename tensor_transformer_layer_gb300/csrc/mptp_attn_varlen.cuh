@@ -83,7 +83,7 @@ __device__ __forceinline__ bool av_pick(const AvArgs& a, int item, AvSpan& sp, i
         const int at = item - first;
         const bool here = at >= 0 && at < tiles;
         // Sums of one lane's value leave it in a uniform register, as the loops over tiles want it: with shuffles in
-        // their place the key gradients of 4096 tokens and 19 heads took 220 us at D = 128, with them 213.
+        // their place the key gradients of 4096 tokens and 19 heads took 220 us at D = 128, with them 213 at the time.
         auto value = [&](int v) { return __reduce_add_sync(0xffffffffu, here ? v : 0); };
         sp = {value(s.q0), value(s.nq), value(s.k0), value(s.nk)};
         tile = value(OF_QUERIES ? tiles - 1 - at : at);
