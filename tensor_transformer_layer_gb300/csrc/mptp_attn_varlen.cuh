@@ -238,6 +238,27 @@ inline AvArgs av_args(const int32_t* cu_q, const int32_t* cu_k, int nseq, int Tq
     return a;
 }
 
+// CTAs that share an item: 1, 2, 4 or 8, by the larger of the longest CTA and of all the work over the SMs that clusters of
+// the size can use. `items` CTAs without sharing, the longest of `longest` iterations, all of `total`; extra[i]: what a
+// CTA costs beside its iterations in clusters of 2^i; part_least: iterations that the longest keeps at least.
+inline int av_cluster(double items, double longest, double total, const double (&extra)[4], int part_least, int sms) {
+    const double usable[4] = {1.0, 1.0, 0.95, 0.79};  // of the SMs: 152, 152, 144, 120
+    int best = 1;
+    double least = 0.0;
+    for (int i = 0; i < 4; ++i) {
+        const int c = 1 << i;
+        if (c > 1 && longest < part_least * c) break;
+        const double even = (total + items * c * extra[i]) / (sms * usable[i]);
+        const double part = longest / c + extra[i];
+        const double est = even > part ? even : part;
+        if (i == 0 || est < 0.9 * least) {
+            best = c;
+            least = est;
+        }
+    }
+    return best;
+}
+
 // `blocks` CTAs in clusters of `cluster`.
 template <typename Kern, typename... Args>
 inline cudaError_t av_launch(Kern kern, long long blocks, int cluster, size_t smem, cudaStream_t s, Args... args) {

@@ -943,22 +943,8 @@ static int dkv_cluster(const AvArgs& a, int sms) {
     const double longest = double(a.group) * ceil_div(a.max_q, AV_TILE);
     const double mean = double(a.Tq) / a.nseq;
     const double total = tiles * a.heads * (0.5 * (a.max_q + mean) / AV_TILE + 0.5) * (a.causal ? 0.5 : 1.0);
-    const double usable[4] = {1.0, 1.0, 0.95, 0.79};  // of the SMs: 152, 152, 144, 120
     const double extra[4] = {3.0, 7.0, 8.0, 10.0};
-    int best = 1;
-    double least = 0.0;
-    for (int i = 0; i < 4; ++i) {
-        const int c = 1 << i;
-        if (c > 1 && longest < 4 * c) break;
-        const double even = (total + tiles * a.kv_heads * c * extra[i]) / (sms * usable[i]);
-        const double part = longest / c + extra[i];
-        const double est = even > part ? even : part;
-        if (i == 0 || est < 0.9 * least) {
-            best = c;
-            least = est;
-        }
-    }
-    return best;
+    return av_cluster(tiles * a.kv_heads, longest, total, extra, 4, sms);
 }
 
 struct AvBwdMaps {

@@ -19,6 +19,8 @@
 // 19 heads, not causal: 92, 100 and 112 us for D = 64, 96, 128 (0.88, 1.22, 1.46 PFLOP/s). At D = 64, P in columns of
 // its own, so that the next scores are computed beside the softmax, made this kernel 5 % faster and a training step no
 // faster; the two tiles taking turns at the exponentials made it 9 % slower.
+// Where few query tiles have long rows of keys, a cluster of two to eight CTAs shares a pair of query tiles: each takes a
+// part of its key tiles, and maxima, sums and fp32 outputs are joined through distributed shared memory in rank order.
 // Masked scores are replaced, not added to, so no value of a key outside a row's range reaches it. A
 // row without keys gets O = 0 and LSE = -inf.
 #include <type_traits>
@@ -38,14 +40,16 @@ struct AvFwdCfg {
     static constexpr int NUM_BARS = 2 + 2 * KST + 2 * VST + 2 * 3 + 1;
     static constexpr size_t SMEM = 1024 + (2 + KST + VST) * size_t(T::BYTES) + 8 * NUM_BARS + 16;
     static_assert(SMEM <= SMEM_LIMIT, "shared memory per block");
+    static_assert((KST + VST) * T::BYTES >= 8 * AV_TILE * 128, "a chunk of every part at the join");
     static constexpr uint32_t TMEM_COLS = 512;  // S_A, S_B at 0, 128; O_A, O_B at 256, 384
 };
 
-template <int D>
+template <int D, bool JOIN>
 __global__ void __launch_bounds__(AV_THREADS, 1)
     attn_varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                           __nv_bfloat16* O, long long ldo, float* LSE, const AvArgs args) {
+                           __nv_bfloat16* O, long long ldo, float* LSE, int cluster_size, const AvArgs args) {
+    const int cluster = JOIN ? cluster_size : 1;
     using Cfg = AvFwdCfg<D>;
     using T = AvTile<D>;
     constexpr int NB = T::NB, KST = Cfg::KST, VST = Cfg::VST;
@@ -69,18 +73,28 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int head = static_cast<int>(blockIdx.x) % args.heads;  // heads of one sequence side by side
+    const int item = static_cast<int>(blockIdx.x) / cluster;
+    const int rank = JOIN ? static_cast<int>(cluster_ctarank()) : 0;
+    const int head = item % args.heads;  // heads of one sequence side by side
     const int kvh = head / args.group;
 
     grid_dependency_wait();  // the sequences' offsets, like the tensors, may come from the kernel before
     AvSpan sp;
     int pr;
-    if (!av_pick<2 * AV_TILE, true>(args, static_cast<int>(blockIdx.x) / args.heads, sp, pr))
+    if (!av_pick<2 * AV_TILE, true>(args, item / args.heads, sp, pr))
         return;
     const int qt[2] = {2 * pr, 2 * pr + 1};
-    const int nt[2] = {av_key_tiles(sp, qt[0] * AV_TILE, args.causal), av_key_tiles(sp, qt[1] * AV_TILE, args.causal)};
-    const int n = max(nt[0], nt[1]);
-    const int v_tail = n * AV_TILE > sp.nk ? sp.nk - (n - 1) * AV_TILE : AV_TILE;  // own rows of the last tile
+    int nt[2] = {av_key_tiles(sp, qt[0] * AV_TILE, args.causal), av_key_tiles(sp, qt[1] * AV_TILE, args.causal)};
+    int n = max(nt[0], nt[1]);
+    int kb = 0;  // first key of this CTA's part, in the sequence
+    if constexpr (JOIN) {
+        const int b0 = n * rank / cluster, b1 = n * (rank + 1) / cluster;
+        for (int g = 0; g < 2; ++g) nt[g] = max(0, min(nt[g], b1) - b0);
+        n = max(nt[0], nt[1]);
+        kb = b0 * AV_TILE;
+    }
+    const int k_row = sp.k0 + kb;
+    const int v_tail = n * AV_TILE > sp.nk - kb ? sp.nk - kb - (n - 1) * AV_TILE : AV_TILE;  // own rows of the last tile
 
     if (threadIdx.x == 0) {
         for (int g = 0; g < 2; ++g) {
@@ -102,7 +116,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         fence_mbarrier_init();
         fence_proxy_async_smem();
         // The first loads overlap the rest of the set-up.
-        if (n > 0) av_load<D>(sK, &tmK, &k_full[0], kvh, sp.k0);
+        if (n > 0) av_load<D>(sK, &tmK, &k_full[0], kvh, k_row);
         for (int g = 0; g < 2; ++g)
             if (nt[g] > 0) av_load<D>(sQ + g * T::BYTES, &tmQ, &q_full[g], head, sp.q0 + qt[g] * AV_TILE);
     }
@@ -131,7 +145,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                                 int stages) -> bool {
                     const int st = j % stages;
                     if (!wait_bounded(&empty[st], ((j / stages) & 1) ^ 1u, ctl)) return false;
-                    av_load<D>(ring + st * T::BYTES, map, &full[st], kvh, sp.k0 + j * AV_TILE);
+                    av_load<D>(ring + st * T::BYTES, map, &full[st], kvh, k_row + j * AV_TILE);
                     return true;
                 };
                 bool ok = true;
@@ -221,10 +235,10 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         const uint32_t s_addr = tmem_base + lane_addr + g * 128;
         const uint32_t o_addr = tmem_base + lane_addr + 256 + g * 128;
         const float c2 = args.scale_log2;
-        // keys [0, see) are visible to this row; see_w to the warp's first row, the fewest
+        // keys [0, see) of this part are visible to this row; see_w to the warp's first row, the fewest
         const int off = sp.nk - sp.nq;
-        const int see = args.causal ? min(sp.nk, qi + off + 1) : sp.nk;
-        const int see_w = args.causal ? min(sp.nk, w0 + off + 1) : sp.nk;
+        const int see = (args.causal ? min(sp.nk, qi + off + 1) : sp.nk) - kb;
+        const int see_w = (args.causal ? min(sp.nk, w0 + off + 1) : sp.nk) - kb;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < ng && ok; ++j) {
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[g]);
         }
-        if (ok && rows_ok > 0) {
+        if (!JOIN && ok && rows_ok > 0) {
             const int row = sp.q0 + w0;
             if (lane < rows_ok)
                 LSE[static_cast<long long>(head) * args.Tq + row + lane] =
@@ -325,6 +339,101 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                               head * D, row, O, ldo, rows_ok, lane);
             }
         }
+        if constexpr (JOIN) {
+            if (ok && ng > 0) {
+                ok = wait_all(&o_full[g], 0);
+                tc_fence_after();
+            }
+            // Every row's maximum and sum go to all ranks. Chunk c (32 columns) of O_g is finished by rank
+            // (g NB + c) % cluster; the others send it their rows, eight pieces of 16 bytes a row, into the rings:
+            // [source rank][chunk of the owner][piece][128 rows].
+            constexpr int CHUNK = 8 * AV_TILE;
+            const int owned = (2 * NB + cluster - 1) / cluster;
+            const int tile_row = q * 32 + lane;
+            float2* stat = reinterpret_cast<float2*>(sQ) + g * AV_TILE + tile_row;  // [source rank][2][128]
+            float4* recv = reinterpret_cast<float4*>(sK);
+            __syncwarp();
+            cluster_sync_all();  // every CTA of the cluster has used its tiles
+            if (ok) {
+                for (int s = 0; s < cluster; ++s)
+                    st_cluster_v2(mapa_shared(smem_u32(stat + rank * 2 * AV_TILE), s), m, l);
+                for (int c = 0; c < NB && ng > 0; ++c) {
+                    const int id = g * NB + c, owner = id % cluster;
+                    if (owner == rank) continue;
+                    uint32_t o[32];
+                    tmem_ld32(o_addr + c * 32, o);
+                    tmem_ld_wait(o);
+                    const uint32_t to =
+                        mapa_shared(smem_u32(recv + (rank * owned + id / cluster) * CHUNK + tile_row), owner);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        st_cluster_v4(to + k * (AV_TILE * 16), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+            __syncwarp();
+            cluster_sync_all();
+            if (ok && *abort_flag == 0u && rows_ok > 0) {
+                float top = -INFINITY, sum = 0.0f;
+                for (int s = 0; s < cluster; ++s) top = fmaxf(top, stat[s * 2 * AV_TILE].x);
+                // a part's factor: zero where the row saw none of its keys, whose O_g may not have been computed
+                auto factor = [&](int s) {
+                    const float part = stat[s * 2 * AV_TILE].x;
+                    return part > -INFINITY ? ex2_approx((part - top) * c2) : 0.0f;
+                };
+                for (int s = 0; s < cluster; ++s) {
+                    const float f = factor(s);
+                    if (f > 0.0f) sum = fmaf(stat[s * 2 * AV_TILE].y, f, sum);
+                }
+                const int row = sp.q0 + w0 + lane;
+                if (rank == 0 && lane < rows_ok)
+                    LSE[static_cast<long long>(head) * args.Tq + row] =
+                        sum > 0.0f ? fmaf(top, args.scale, logf(sum)) : -INFINITY;
+                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                for (int c = 0; c < NB; ++c) {
+                    const int id = g * NB + c;
+                    if (id % cluster != rank) continue;
+                    uint32_t mine[32];
+                    if (ng > 0) {
+                        tmem_ld32(o_addr + c * 32, mine);
+                        tmem_ld_wait(mine);
+                    }
+                    float o[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+                    for (int s = 0; s < cluster; ++s) {
+                        const float f = factor(s);
+                        if (!(f > 0.0f)) continue;
+                        const float4* from = recv + (s * owned + id / cluster) * CHUNK + tile_row;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 v = s == rank ? make_float4(__uint_as_float(mine[4 * k]), __uint_as_float(mine[4 * k + 1]),
+                                                                     __uint_as_float(mine[4 * k + 2]),
+                                                                     __uint_as_float(mine[4 * k + 3]))
+                                                       : from[k * AV_TILE];
+                            o[4 * k] = fmaf(v.x, f, o[4 * k]);
+                            o[4 * k + 1] = fmaf(v.y, f, o[4 * k + 1]);
+                            o[4 * k + 2] = fmaf(v.z, f, o[4 * k + 2]);
+                            o[4 * k + 3] = fmaf(v.w, f, o[4 * k + 3]);
+                        }
+                    }
+                    if (lane < rows_ok) {
+                        uint4* dst = reinterpret_cast<uint4*>(O + static_cast<long long>(row) * ldo + head * D + c * 32);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                                pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                                pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                                pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                    }
+                }
+            }
+        }
+    }
+    if (JOIN && warp < 4) {
+        // (the softmax warps' two barriers)
+        __syncwarp();
+        cluster_sync_all();
+        cluster_sync_all();
     }
 
     // ---------------- teardown ----------------
@@ -339,6 +448,18 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
     }
+}
+
+// CTAs that share a pair of query tiles. The estimate, in iterations (a key tile each): a CTA costs 2.7 more than its
+// own (its set-up, first loads and store), one of a cluster 5.4, 6.4 or 10 (the join too). Measured with 1, 2, 4, 8: one
+// query on 16,384 keys, eight heads, d = 128, 175, 92, 50, 33 us; 4096 causal queries, d = 64, one head 45, 28, 19, 18,
+// eight heads 46, 36, 58, 112; four prompts of 33 to 1025 queries, 20 heads, d = 96, 29, 43, 80, 179.
+static int fwd_cluster(const AvArgs& a, int sms) {
+    const double items = double(av_max_tiles(a.nseq, a.Tq, a.max_q, 2 * AV_TILE)) * a.heads;
+    const double keys = 0.5 * (a.max_k + double(a.Tk) / a.nseq), hidden = a.causal ? 0.25 * (a.max_q + double(a.Tq) / a.nseq) : 0.0;
+    const double mean = (keys > hidden ? keys - hidden : 0.0) / AV_TILE + 0.5;
+    const double extra[4] = {2.7, 5.4, 6.4, 10.0};
+    return av_cluster(items, ceil_div(a.max_k, AV_TILE), items * mean, extra, 2, sms);
 }
 
 }  // namespace mptp
@@ -374,12 +495,13 @@ extern "C" mp_status mp_attn_varlen_fwd(const mp_bf16* Q, const mp_bf16* K, cons
     const long long blocks = av_max_tiles(nseq, Tq, max_q, 2 * AV_TILE) * heads;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(O);
-    cudaError_t e;
-    if (d == 64)
-        e = av_launch(attn_varlen_fwd_kernel<64>, blocks, 1, AvFwdCfg<64>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, a);
-    else if (d == 96)
-        e = av_launch(attn_varlen_fwd_kernel<96>, blocks, 1, AvFwdCfg<96>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, a);
-    else
-        e = av_launch(attn_varlen_fwd_kernel<128>, blocks, 1, AvFwdCfg<128>::SMEM, s, tq, tk, tv, to, o, ldo, LSE, a);
+    const int cluster = fwd_cluster(a, sms);
+    auto launch = [&](auto alone, auto joined, size_t smem) {
+        return av_launch(cluster > 1 ? joined : alone, blocks * cluster, cluster, smem, s, tq, tk, tv, to, o, ldo, LSE, cluster, a);
+    };
+    const cudaError_t e =
+        d == 64   ? launch(attn_varlen_fwd_kernel<64, false>, attn_varlen_fwd_kernel<64, true>, AvFwdCfg<64>::SMEM)
+        : d == 96 ? launch(attn_varlen_fwd_kernel<96, false>, attn_varlen_fwd_kernel<96, true>, AvFwdCfg<96>::SMEM)
+                  : launch(attn_varlen_fwd_kernel<128, false>, attn_varlen_fwd_kernel<128, true>, AvFwdCfg<128>::SMEM);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }

@@ -136,6 +136,22 @@ def test_attn_varlen_many_sequences(nseq, same, causal):
     _check(_run(inp, cu_q, cu_k, causal), inp, cu_q, cu_k, causal)
 
 
+@pytest.mark.parametrize("q_lens,k_lens,heads,kv", [
+    ([1], [9000], 4, 1),                       # clusters of eight CTAs share a query's keys
+    ([1, 3, 2], [2100, 4097, 1], 2, 2),
+    ([130, 1], [4000, 3900], 3, 1),            # of four; a second query tile of two rows
+    ([1100], [1100], 2, 1),                    # causal: parts that some rows see nothing of
+    ([900], [1500], 1, 1),
+    ([2300, 40], [2200, 900], 2, 2),           # rows without keys where causal
+])
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attn_varlen_long_keys_for_few_queries(q_lens, k_lens, heads, kv, d, causal):
+    cu_q, cu_k = _cu(q_lens), _cu(k_lens)
+    inp = _inputs(sum(q_lens), sum(k_lens), heads, kv, d, seed=22700 + sum(q_lens) + d)
+    _check(_run(inp, cu_q, cu_k, causal), inp, cu_q, cu_k, causal)
+
+
 def test_attn_varlen_scale_and_large_scores():
     # scores up to +-200 and a jump of the running maximum at every key tile
     lens = [400]
