@@ -238,6 +238,14 @@ inline AvArgs av_args(const int32_t* cu_q, const int32_t* cu_k, int nseq, int Tq
     return a;
 }
 
+// Key tiles that a query tile sees on average, estimated: the lengths are on the device, so the sum over the sequences is
+// taken between that of equal ones and that of the longest.
+inline double av_mean_keys(const AvArgs& a) {
+    const double keys = 0.5 * (a.max_k + double(a.Tk) / a.nseq);
+    const double hidden = a.causal ? 0.25 * (a.max_q + double(a.Tq) / a.nseq) : 0.0;
+    return (keys > hidden ? keys - hidden : 0.0) / AV_TILE + 0.5;
+}
+
 // CTAs that share an item: 1, 2, 4 or 8, by the larger of the longest CTA and of all the work over the SMs that clusters of
 // the size can use. `items` CTAs without sharing, the longest of `longest` iterations, all of `total`; extra[i]: what a
 // CTA costs beside its iterations in clusters of 2^i; part_least: iterations that the longest keeps at least.

@@ -26,7 +26,7 @@
 //   for a second S^T or for P^T beside it: S^T runs ahead and the warps never wait for it.
 //   Where whole key tiles would balance badly (few of them, many queries each), a cluster of two to eight CTAs
 //   shares one: each takes a part of its (head, query tile) pairs, and the fp32 sums are joined through
-//   distributed shared memory in rank order.
+//   distributed shared memory in rank order. The dQ kernel shares a query tile's keys the same way.
 // In the first, a softmax thread has one row and 64 of its 128 columns; in the second, four keys' fragments.
 // Both are bound by the hand-overs between softmax and products (tensor core 65 to 67 % active at D = 128): 4096
 // tokens, 19 heads, not causal, dQ 113, 132, 158 us and dK with dV 138, 179, 208 us for D = 64, 96, 128 (1.08 to 1.55
@@ -60,16 +60,18 @@ struct AvDqCfg {
     static constexpr int NUM_BARS = 2 + 2 * KST + 2 * VST + 2 + 4 + 1;
     static constexpr size_t SMEM = 1024 + (2 + KST + VST) * size_t(T::BYTES) + 2 * AV_TILE * 4 + 8 * NUM_BARS + 16;
     static_assert(SMEM <= SMEM_LIMIT, "shared memory per block");
+    static_assert((KST + VST) * T::BYTES >= 8 * AV_TILE * 128, "a chunk of every part at the join");
     static constexpr uint32_t TMEM_COLS = 512;  // S(even), S(odd) at 0, 128; dP at 256; dQ at 384
 };
 
-template <int D>
+template <int D, bool JOIN>
 __global__ void __launch_bounds__(AV_THREADS, 1)
     attn_varlen_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                           const __grid_constant__ CUtensorMap tmdQ, const __nv_bfloat16* O, long long ldo,
                           const __nv_bfloat16* dO, long long lddo, const float* LSE, float* delta, __nv_bfloat16* dQ,
-                          long long lddq, const AvArgs args) {
+                          long long lddq, int cluster_size, const AvArgs args) {
+    const int cluster = JOIN ? cluster_size : 1;
     using Cfg = AvDqCfg<D>;
     using T = AvTile<D>;
     constexpr int NB = T::NB, KST = Cfg::KST, VST = Cfg::VST;
@@ -98,23 +100,29 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int head = static_cast<int>(blockIdx.x) % args.heads;
+    const int item = static_cast<int>(blockIdx.x) / cluster;
+    const int rank = JOIN ? static_cast<int>(cluster_ctarank()) : 0;
+    const int head = item % args.heads;
     const int kvh = head / args.group;
 
     grid_dependency_wait();
     AvSpan sp;
     int qt;
-    if (!av_pick<AV_TILE, true>(args, static_cast<int>(blockIdx.x) / args.heads, sp, qt))
+    if (!av_pick<AV_TILE, true>(args, item / args.heads, sp, qt))
         return;
     const int i0 = qt * AV_TILE;
-    const int n = av_key_tiles(sp, i0, args.causal);
-    const int k_tail = n * AV_TILE > sp.nk ? sp.nk - (n - 1) * AV_TILE : AV_TILE;
+    const int n_all = av_key_tiles(sp, i0, args.causal);
+    // this CTA's part of the key tiles
+    auto part_begin = [&](int r) { return n_all * r / cluster; };
+    const int n = part_begin(rank + 1) - part_begin(rank);
+    const int kb = part_begin(rank) * AV_TILE, k_row = sp.k0 + kb;
+    const int k_tail = n * AV_TILE > sp.nk - kb ? sp.nk - kb - (n - 1) * AV_TILE : AV_TILE;
 
     // The softmax warps' rows of LSE, O and dO are asked for before the set-up, which takes as long as they do.
     // delta = rowsum(dO * O): each warp sums 16 rows, whole rows side by side, 16 bytes a lane. (Row by row, a row
     // to a thread, they took 8000 cycles at D = 96: the shared memory leaves no cache to hold a line for the next
     // piece.) With one key tile the loop sums delta instead.
-    const bool one_tile = n == 1;
+    const bool one_tile = n_all == 1;
     constexpr int LANES = D / 8, ROWS = 32 / LANES, LOADS = 16 / ROWS;  // lanes a row, rows a load, loads a warp
     uint4 o_part[LOADS], do_part[LOADS];
     const long long row_at = static_cast<long long>(head) * args.Tq + sp.q0 + i0 + (warp & 3) * 32 + lane;
@@ -158,9 +166,9 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         fence_mbarrier_init();
         fence_proxy_async_smem();
         if (n > 0) {
-            av_load<D>(sK, &tmK, &k_full[0], kvh, sp.k0);
+            av_load<D>(sK, &tmK, &k_full[0], kvh, k_row);
             av_load<D>(sQ, &tmQ, q_full, head, sp.q0 + i0);
-            av_load<D>(sV, &tmV, &v_full[0], kvh, sp.k0);
+            av_load<D>(sV, &tmV, &v_full[0], kvh, k_row);
             av_load<D>(sdO, &tmdO, do_full, head, sp.q0 + i0);
         }
     }
@@ -189,11 +197,11 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     int st = j % KST;
                     ok = wait_bounded(&k_empty[st], ((j / KST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sK + st * T::BYTES, &tmK, &k_full[st], kvh, sp.k0 + j * AV_TILE);
+                    av_load<D>(sK + st * T::BYTES, &tmK, &k_full[st], kvh, k_row + j * AV_TILE);
                     st = j % VST;
                     ok = wait_bounded(&v_empty[st], ((j / VST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sV + st * T::BYTES, &tmV, &v_full[st], kvh, sp.k0 + j * AV_TILE);
+                    av_load<D>(sV + st * T::BYTES, &tmV, &v_full[st], kvh, k_row + j * AV_TILE);
                 }
             }
         } else if (warp == 1) {
@@ -312,8 +320,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         const uint32_t s_addr = tmem_base + lane_addr + hf * 64;
         const uint32_t dp_addr = tmem_base + lane_addr + 256 + hf * 64;
         const int off = sp.nk - sp.nq;
-        const int see = args.causal ? min(sp.nk, qi + off + 1) : sp.nk;
-        const int see_w = args.causal ? min(sp.nk, w0 + off + 1) : sp.nk;
+        const int see = (args.causal ? min(sp.nk, qi + off + 1) : sp.nk) - kb;
+        const int see_w = (args.causal ? min(sp.nk, w0 + off + 1) : sp.nk) - kb;
         const float2 c2v = make_float2(args.scale_log2, args.scale_log2);
         const float2 nl = make_float2(-lse2, -lse2);
         bool ok = true;
@@ -384,11 +392,11 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(ds_full);
         }
-        if (ok && row_ok && hf == 0) delta[row_at] = dl;
-        if (ok && rows_ok > 0) {
-            constexpr int HALF = (NB + 1) / 2;
-            const int c0 = hf ? HALF : 0, c1 = hf ? NB : HALF;
-            const int r0 = sp.q0 + w0;
+        if (ok && row_ok && hf == 0 && (JOIN && one_tile ? n > 0 : rank == 0)) delta[row_at] = dl;
+        constexpr int HALF = (NB + 1) / 2;
+        const int c0 = hf ? HALF : 0, c1 = hf ? NB : HALF;
+        const int r0 = sp.q0 + w0;
+        if (!JOIN && ok && rows_ok > 0) {
             if (n == 0) {
                 av_store_zero_rows(c0, c1, head * D, r0, dQ, lddq, rows_ok, lane);
             } else if (wait_all(dq_full, 0)) {
@@ -397,6 +405,74 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                               dQ, lddq, rows_ok, lane);
             }
         }
+        if constexpr (JOIN) {
+            if (ok && n > 0) {
+                ok = wait_all(dq_full, 0);
+                tc_fence_after();
+            }
+            // Chunk c (32 columns) is finished by rank c % cluster. The others send it their rows, eight pieces of 16
+            // bytes a row, into the rings: [source rank][chunk of the owner][piece][128 queries].
+            constexpr int CHUNK = 8 * AV_TILE;
+            const int owned = (NB + cluster - 1) / cluster;
+            float4* recv = reinterpret_cast<float4*>(sK) + q * 32 + lane;
+            const uint32_t acc = tmem_base + lane_addr + 384;
+            __syncwarp();
+            cluster_sync_all();  // every CTA of the cluster has used its rings
+            for (int c = c0; c < c1 && ok && n > 0; ++c) {
+                const int owner = c % cluster;
+                if (owner == rank) continue;
+                uint32_t o[32];
+                tmem_ld32(acc + c * 32, o);
+                tmem_ld_wait(o);
+                const uint32_t to = mapa_shared(smem_u32(recv + (rank * owned + c / cluster) * CHUNK), owner);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    st_cluster_v4(to + k * (AV_TILE * 16), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+            __syncwarp();
+            cluster_sync_all();
+            for (int c = c0; c < c1 && ok && *abort_flag == 0u && rows_ok > 0; ++c) {
+                if (c % cluster != rank) continue;
+                uint32_t mine[32];
+                if (n > 0) {
+                    tmem_ld32(acc + c * 32, mine);
+                    tmem_ld_wait(mine);
+                }
+                float sum[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) sum[k] = 0.0f;
+                for (int s = 0; s < cluster; ++s) {
+                    if (part_begin(s + 1) == part_begin(s)) continue;
+                    const float4* from = recv + (s * owned + c / cluster) * CHUNK;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 v = s == rank ? make_float4(__uint_as_float(mine[4 * k]), __uint_as_float(mine[4 * k + 1]),
+                                                                 __uint_as_float(mine[4 * k + 2]), __uint_as_float(mine[4 * k + 3]))
+                                                   : from[k * AV_TILE];
+                        sum[4 * k] += v.x;
+                        sum[4 * k + 1] += v.y;
+                        sum[4 * k + 2] += v.z;
+                        sum[4 * k + 3] += v.w;
+                    }
+                }
+                if (row_ok) {
+                    uint4* dst = reinterpret_cast<uint4*>(dQ + static_cast<long long>(r0 + lane) * lddq + head * D + c * 32);
+                    const float f = args.scale;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dst[k] = make_uint4(pack_bf16x2(sum[8 * k] * f, sum[8 * k + 1] * f),
+                                            pack_bf16x2(sum[8 * k + 2] * f, sum[8 * k + 3] * f),
+                                            pack_bf16x2(sum[8 * k + 4] * f, sum[8 * k + 5] * f),
+                                            pack_bf16x2(sum[8 * k + 6] * f, sum[8 * k + 7] * f));
+                }
+            }
+        }
+    }
+    if (JOIN && warp < 4) {
+        // (the softmax warps' two barriers)
+        __syncwarp();
+        cluster_sync_all();
+        cluster_sync_all();
     }
 
     // ---------------- teardown ----------------
@@ -947,6 +1023,15 @@ static int dkv_cluster(const AvArgs& a, int sms) {
     return av_cluster(tiles * a.kv_heads, longest, total, extra, 4, sms);
 }
 
+// CTAs that share a query tile, as the key kernel below shares key tiles; iterations are key tiles. A CTA costs five more
+// than its own, one of a cluster nine to fourteen. Measured with 1, 2, 4, 8, both kernels: one query on 16,384 keys, eight
+// heads, d = 128, 157, 100, 71, 60 us; 4096 causal queries, d = 64, one head 44, 34, 29, 40, eight heads 64, 80, 106, 180.
+static int dq_cluster(const AvArgs& a, int sms) {
+    const double items = double(av_max_tiles(a.nseq, a.Tq, a.max_q, AV_TILE)) * a.heads;
+    const double extra[4] = {5.0, 9.0, 12.0, 14.0};
+    return av_cluster(items, ceil_div(a.max_k, AV_TILE), items * av_mean_keys(a), extra, 2, sms);
+}
+
 struct AvBwdMaps {
     CUtensorMap q, k, v, d_o, dq, dk, dv;
 };
@@ -958,10 +1043,13 @@ static cudaError_t launch_bwd(const AvBwdMaps& m, const mp_bf16* O, long long ld
     auto bf = [](auto* p) { return reinterpret_cast<__nv_bfloat16*>(const_cast<mp_bf16*>(p)); };
     const long long qtiles = av_max_tiles(a.nseq, a.Tq, a.max_q, AV_TILE), ktiles = av_max_tiles(a.nseq, a.Tk, a.max_k, AV_TILE);
     cudaError_t e = cudaSuccess;
-    if (qtiles > 0)
-        e = av_launch(attn_varlen_dq_kernel<D>, qtiles * a.heads, 1, AvDqCfg<D>::SMEM, s, m.q,
-                      m.k, m.v, m.d_o, m.dq, static_cast<const __nv_bfloat16*>(bf(O)), ldo,
-                      static_cast<const __nv_bfloat16*>(bf(dO)), lddo, LSE, delta, bf(dQ), lddq, a);
+    if (qtiles > 0) {
+        const int cluster = dq_cluster(a, sms);
+        auto kern = cluster > 1 ? attn_varlen_dq_kernel<D, true> : attn_varlen_dq_kernel<D, false>;
+        e = av_launch(kern, qtiles * a.heads * cluster, cluster, AvDqCfg<D>::SMEM, s, m.q, m.k, m.v, m.d_o, m.dq,
+                      static_cast<const __nv_bfloat16*>(bf(O)), ldo, static_cast<const __nv_bfloat16*>(bf(dO)), lddo, LSE, delta,
+                      bf(dQ), lddq, cluster, a);
+    }
     if (e == cudaSuccess && ktiles > 0) {
         const int cluster = dkv_cluster(a, sms);
         auto kern = cluster > 1 ? attn_varlen_dkv_kernel<D, true> : attn_varlen_dkv_kernel<D, false>;

@@ -456,10 +456,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 // eight heads 46, 36, 58, 112; four prompts of 33 to 1025 queries, 20 heads, d = 96, 29, 43, 80, 179.
 static int fwd_cluster(const AvArgs& a, int sms) {
     const double items = double(av_max_tiles(a.nseq, a.Tq, a.max_q, 2 * AV_TILE)) * a.heads;
-    const double keys = 0.5 * (a.max_k + double(a.Tk) / a.nseq), hidden = a.causal ? 0.25 * (a.max_q + double(a.Tq) / a.nseq) : 0.0;
-    const double mean = (keys > hidden ? keys - hidden : 0.0) / AV_TILE + 0.5;
     const double extra[4] = {2.7, 5.4, 6.4, 10.0};
-    return av_cluster(items, ceil_div(a.max_k, AV_TILE), items * mean, extra, 2, sms);
+    return av_cluster(items, ceil_div(a.max_k, AV_TILE), items * av_mean_keys(a), extra, 2, sms);
 }
 
 }  // namespace mptp
