@@ -822,7 +822,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<BN, EPI, NE>
                         const bool here = wait_bounded(&aux_full[e * Cfg::AUX_BUFS + seq % 4], (seq / 4) & 1, ctl);
                         if (!__all_sync(0xffffffffu, here)) return false;
                         const int col0 = n_blk * BN + c * 32;
-                        if (col0 >= p.N) return true;
+                        if (col0 >= p.N) {
+                            // Nothing to store, but a group all the same: the wait above counts one a chunk. Without
+                            // it the last store of a tile whose columns end here could still be reading its boxes
+                            // when the chunk four further on is loaded into them.
+                            if (lane == 0) bulk_commit_group();
+                            return true;
+                        }
                         uint8_t* box = stg + (seq % 4) * 4096;
                         uint8_t* line = box + lane * 64;
 #pragma unroll

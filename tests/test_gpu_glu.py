@@ -97,6 +97,31 @@ def test_glu_matches_oracle_on_large_tiles(T, h, f, t, act):
     test_glu_matches_oracle(T, h, f, t, act)
 
 
+@pytest.mark.parametrize("T,h,f", [
+    (400, 64, 64),           # one tile a launch: its loads behind the last column are zero fills
+    (400, 64, 128),
+    (400, 64, 192),
+    (2600, 128, 2112),       # 99 tiles, more than CTA pairs: a pair's second tile follows one that ends early
+    (2600, 128, 2176),
+    (2600, 128, 2240),
+])
+def test_glu_gradients_where_columns_end_inside_a_tile(T, h, f):
+    # Large tiles are 256 columns wide; the gradients' boxes of the last columns are stored before they are loaded again.
+    inp = _inputs(T, h, f, seed=21170)
+    first = _run(inp, 1, "silu")
+    x = {k: f64(v) for k, v in inp.items()}
+    want = oracle.glu_bwd(x["X"], x["W"], x["Wd"], x["dZ"], "silu")
+    errs = {k: rel_fro(f64(first[k].cpu()), want[k]) for k in want}
+    assert all(errs[k] <= TOL[k] for k in errs), errs
+    d = {k: v.cuda() for k, v in inp.items()}
+    for _ in range(20):
+        o = {"dX": _nan(T, h), "dW": _nan(h, 2 * f), "dWd": _nan(f, h), "dGU": _nan(T, 2 * f)}
+        mp().mp_glu_bwd(d["X"], d["W"], d["Wd"], first["GU"], first["Y"], d["dZ"], o["dX"], o["dW"], o["dWd"], o["dGU"],
+                        t=1, act="silu")
+        for k in o:
+            assert torch.equal(o[k], first[k]), k
+
+
 def test_glu_large_tiles_do_not_depend_on_shards():
     inp = _inputs(2600, 256, 1024, seed=21150)
     ref = _run(inp, 1, "silu")
