@@ -421,7 +421,8 @@ MP_API mp_status mp_rope_axes(const mp_bf16* x, mp_bf16* y, const int32_t* pos,
  *   S = scale Q K^T,  LSE = log sum_k exp S,  O = exp(S - LSE) V
  * causal != 0: the last query of a sequence sees its last key, so query i sees keys
  * 0 .. i + (keys - queries). A row that sees no key gets O = 0 and LSE = -inf. Rows outside every
- * sequence are not written. Values of other sequences (infinities and NaN included) reach no row.
+ * sequence are not written. Values of other sequences (infinities and NaN included) reach no row; a NaN among the
+ * scores that a row sees makes its O and LSE NaN.
  *   Q, O [Tq, heads, d], K, V [Tk, kv_heads, d] bf16: a row's heads are contiguous, rows are ldq, ldo,
  *   ldk, ldv elements apart (views of a packed projection are fine); LSE [heads, Tq] fp32.
  *   cu_q, cu_k [nseq + 1] int32 in device memory, ascending, within the tensors; max_q, max_k: at

@@ -281,9 +281,12 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 l *= alpha;
                 rescale = true;
             }
-            // P = exp2(s c2 - m c2); column pair k packed as bf16x2 into word k (words <= 2k are read).
+            // P = exp2(s c2 - m c2); column pair k packed as bf16x2 into word k (words <= 2k are read). A maximum of
+            // -inf is no number to subtract: nothing was visible yet, or only scores of -inf (P = 0) and NaN (P, and
+            // through it the sum, NaN: the maximum passes NaN over).
             const float2 c2v = make_float2(c2, c2);
-            const float2 nmb = make_float2(-m * c2, -m * c2);
+            const float mb = m > -INFINITY ? -m * c2 : 0.0f;
+            const float2 nmb = make_float2(mb, mb);
             float2 s4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) s4[k] = make_float2(0.0f, 0.0f);
@@ -330,12 +333,12 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             const int row = sp.q0 + w0;
             if (lane < rows_ok)
                 LSE[static_cast<long long>(head) * args.Tq + row + lane] =
-                    l > 0.0f ? fmaf(m, args.scale, logf(l)) : -INFINITY;
+                    l == 0.0f ? -INFINITY : fmaf(m, args.scale, logf(l));
             if (ng == 0) {
                 av_store_zero_rows(0, NB, head * D, row, O, ldo, rows_ok, lane);
             } else if (wait_all(&o_full[g], 0)) {
                 tc_fence_after();
-                av_store_rows(o_addr, l > 0.0f ? 1.0f / l : 0.0f, 0, NB, sQ + g * T::BYTES + q * (NB * 2048), &tmO,
+                av_store_rows(o_addr, l == 0.0f ? 0.0f : 1.0f / l, 0, NB, sQ + g * T::BYTES + q * (NB * 2048), &tmO,
                               head * D, row, O, ldo, rows_ok, lane);
             }
         }
@@ -375,20 +378,21 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             if (ok && *abort_flag == 0u && rows_ok > 0) {
                 float top = -INFINITY, sum = 0.0f;
                 for (int s = 0; s < cluster; ++s) top = fmaxf(top, stat[s * 2 * AV_TILE].x);
-                // a part's factor: zero where the row saw none of its keys, whose O_g may not have been computed
+                // a part's factor: its sum, NaN or 0, where that is NaN or the row saw none of its keys (whose O_g may
+                // not have been computed)
                 auto factor = [&](int s) {
-                    const float part = stat[s * 2 * AV_TILE].x;
-                    return part > -INFINITY ? ex2_approx((part - top) * c2) : 0.0f;
+                    const float2 part = stat[s * 2 * AV_TILE];
+                    return part.x > -INFINITY && part.y == part.y ? ex2_approx((part.x - top) * c2) : part.y;
                 };
                 for (int s = 0; s < cluster; ++s) {
                     const float f = factor(s);
-                    if (f > 0.0f) sum = fmaf(stat[s * 2 * AV_TILE].y, f, sum);
+                    if (f != 0.0f) sum = fmaf(stat[s * 2 * AV_TILE].y, f, sum);
                 }
                 const int row = sp.q0 + w0 + lane;
                 if (rank == 0 && lane < rows_ok)
                     LSE[static_cast<long long>(head) * args.Tq + row] =
-                        sum > 0.0f ? fmaf(top, args.scale, logf(sum)) : -INFINITY;
-                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                        sum == 0.0f ? -INFINITY : fmaf(top, args.scale, logf(sum));
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 for (int c = 0; c < NB; ++c) {
                     const int id = g * NB + c;
                     if (id % cluster != rank) continue;
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     for (int k = 0; k < 32; ++k) o[k] = 0.0f;
                     for (int s = 0; s < cluster; ++s) {
                         const float f = factor(s);
-                        if (!(f > 0.0f)) continue;
+                        if (f == 0.0f) continue;
                         const float4* from = recv + (s * owned + id / cluster) * CHUNK + tile_row;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
