@@ -422,7 +422,8 @@ MP_API mp_status mp_rope_axes(const mp_bf16* x, mp_bf16* y, const int32_t* pos,
  * causal != 0: the last query of a sequence sees its last key, so query i sees keys
  * 0 .. i + (keys - queries). A row that sees no key gets O = 0 and LSE = -inf. Rows outside every
  * sequence are not written. Values of other sequences (infinities and NaN included) reach no row; a NaN among the
- * scores that a row sees makes its O and LSE NaN.
+ * scores that a row sees makes its O and LSE NaN, and an infinity or NaN in V of a key that a causal row does not see
+ * may make its O NaN too (its weight is zero in the product).
  *   Q, O [Tq, heads, d], K, V [Tk, kv_heads, d] bf16: a row's heads are contiguous, rows are ldq, ldo,
  *   ldk, ldv elements apart (views of a packed projection are fine); LSE [heads, Tq] fp32.
  *   cu_q, cu_k [nseq + 1] int32 in device memory, ascending, within the tensors; max_q, max_k: at
@@ -448,7 +449,8 @@ MP_API mp_status mp_attn_varlen_fwd(const mp_bf16* Q, const mp_bf16* K, const mp
  * dK and dV of a shared key head are the sums over its query heads. Deterministic: no atomics.
  *   dO, dQ [Tq, heads, d], dK, dV [Tk, kv_heads, d] with pitches lddo, lddq, lddk, lddv;
  *   delta_ws [heads, Tq] fp32: workspace (caller-owned); holds delta on return.
- *   Everything else as mp_attn_varlen_fwd; a row that saw no key gives no gradient and gets dQ = 0.
+ *   Everything else as mp_attn_varlen_fwd; a row that saw no key gives no gradient, whatever its Q and dO hold, and
+ *   gets dQ = 0 and delta = 0.
  */
 MP_API mp_status mp_attn_varlen_bwd(const mp_bf16* Q, const mp_bf16* K, const mp_bf16* V,
                              const mp_bf16* O, const float* LSE, const mp_bf16* dO,

@@ -129,7 +129,8 @@ __device__ __forceinline__ void av_clear_rows(uint8_t* tile, int from, int lane)
 
 // Chunks [c0, c1) (32 columns each) of a warp's 32 accumulator rows, times f, as bf16: through shared
 // memory and TMA where all 32 rows belong to the sequence (rows_ok = 32), else row by row. `acc` is the
-// warp's TMEM address, `stg` its 2 KB boxes, one per chunk of the tile.
+// warp's TMEM address, `stg` its 2 KB boxes, one per chunk of the tile. A row whose f is 0 saw no key and is
+// zero: its accumulators may hold NaN, zero weights times infinities among the keys of its tile.
 __device__ __forceinline__ void av_store_rows(uint32_t acc, float f, int c0, int c1, uint8_t* stg,
                                               const CUtensorMap* map, int col, int row, __nv_bfloat16* out,
                                               long long ld, int rows_ok, int lane) {
@@ -147,6 +148,10 @@ __device__ __forceinline__ void av_store_rows(uint32_t acc, float f, int c0, int
                               pack_bf16x2(__uint_as_float(o[8 * v + 2]) * f, __uint_as_float(o[8 * v + 3]) * f),
                               pack_bf16x2(__uint_as_float(o[8 * v + 4]) * f, __uint_as_float(o[8 * v + 5]) * f),
                               pack_bf16x2(__uint_as_float(o[8 * v + 6]) * f, __uint_as_float(o[8 * v + 7]) * f));
+        if (f == 0.0f) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) w[v] = make_uint4(0u, 0u, 0u, 0u);
+        }
         if (rows_ok >= 32) {
             uint8_t* r = stg + c * 2048 + lane * 64;
 #pragma unroll

@@ -34,8 +34,9 @@
 // of remainders, and no clearing between a wait and a product, took dQ from 139 and 166 us at D = 96 and 128. Sixteen softmax warps of half the columns each were 1 to 10 % slower.
 //
 // P and dS are rounded to bf16 for their products (the tensor core's operand type); the exponent,
-// delta, and every sum are fp32. Hidden pairs are replaced by zero after the arithmetic, and rows of a
-// tile behind the sequence's end are cleared in shared memory where they would be summed over.
+// delta, and every sum are fp32. Hidden pairs' dS (for dQ) and P (for dV, and through it dS for dK) are replaced by zero
+// after the arithmetic; rows of a tile behind the sequence's end are cleared in shared memory where they would be summed
+// over, and queries that see no key are not loaded.
 #include <type_traits>
 
 #include "mptp_attn_varlen.cuh"
@@ -392,16 +393,18 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(ds_full);
         }
-        if (ok && row_ok && hf == 0 && (JOIN && one_tile ? n > 0 : rank == 0)) delta[row_at] = dl;
+        const bool dead = nl.x == -INFINITY;  // the row saw no key: its dO gives nothing, whatever it holds
+        if (ok && row_ok && hf == 0 && (JOIN && one_tile ? n > 0 : rank == 0)) delta[row_at] = dead ? 0.0f : dl;
         constexpr int HALF = (NB + 1) / 2;
         const int c0 = hf ? HALF : 0, c1 = hf ? NB : HALF;
         const int r0 = sp.q0 + w0;
+        const float dq_scale = dead ? 0.0f : args.scale;
         if (!JOIN && ok && rows_ok > 0) {
             if (n == 0) {
                 av_store_zero_rows(c0, c1, head * D, r0, dQ, lddq, rows_ok, lane);
             } else if (wait_all(dq_full, 0)) {
                 tc_fence_after();
-                av_store_rows(tmem_base + lane_addr + 384, args.scale, c0, c1, sQ + q * (NB * 2048), &tmdQ, head * D, r0,
+                av_store_rows(tmem_base + lane_addr + 384, dq_scale, c0, c1, sQ + q * (NB * 2048), &tmdQ, head * D, r0,
                               dQ, lddq, rows_ok, lane);
             }
         }
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 32; ++k) sum[k] = 0.0f;
                 for (int s = 0; s < cluster; ++s) {
-                    if (part_begin(s + 1) == part_begin(s)) continue;
+                    if (part_begin(s + 1) == part_begin(s) || dq_scale == 0.0f) continue;
                     const float4* from = recv + (s * owned + c / cluster) * CHUNK;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 }
                 if (row_ok) {
                     uint4* dst = reinterpret_cast<uint4*>(dQ + static_cast<long long>(r0 + lane) * lddq + head * D + c * 32);
-                    const float f = args.scale;
+                    const float f = dq_scale;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         dst[k] = make_uint4(pack_bf16x2(sum[8 * k] * f, sum[8 * k + 1] * f),
@@ -566,28 +569,29 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     if (!av_pick<AV_TILE, false>(args, item / args.kv_heads, sp, kt)) return;
     const int j0 = kt * AV_TILE;
     const int off = sp.nk - sp.nq;
-    // query tiles [t0, t1) see some key of this tile
-    const int t1 = (sp.nq + AV_TILE - 1) / AV_TILE;
-    const int t0 = args.causal ? max(0, j0 - off) / AV_TILE : 0;
-    const int per_head = max(0, t1 - t0);
-    const int n_all = per_head * args.group;
+    // Query tiles start at the first query that sees a key of this tile, not at a multiple of 128: those before it give
+    // nothing, and nothing of theirs (a query without keys may hold anything) comes into a product.
+    const int qf = args.causal ? max(0, j0 - off) : 0;
+    const int rows = max(0, sp.nq - qf), q_row = sp.q0 + qf;
+    const int tiles = (rows + AV_TILE - 1) / AV_TILE;
+    const int n_all = tiles * args.group;
     // this CTA's part of the iterations
     auto part_begin = [&](int r) { return static_cast<int>(static_cast<long long>(n_all) * r / cluster); };
     const int it0 = part_begin(rank);
     const int n = part_begin(rank + 1) - it0;
-    const int q_tail = t1 * AV_TILE > sp.nq ? sp.nq - (t1 - 1) * AV_TILE : AV_TILE;
-    // Iterations: the group's heads in turn, of each the query tiles t0 .. t1 - 1. Every role walks them
+    const int q_tail = tiles * AV_TILE > rows ? rows - (tiles - 1) * AV_TILE : AV_TILE;
+    // Iterations: the group's heads in turn, of each the query tiles. Every role walks them
     // with counters (a division an iteration was a tenth of the loop).
     struct Walk {
-        int head, tile, t0, t1;
+        int head, tile, tiles;
         __device__ __forceinline__ void next() {
-            if (++tile == t1) {
-                tile = t0;
+            if (++tile == tiles) {
+                tile = 0;
                 ++head;
             }
         }
     };
-    const Walk first{kvh * args.group + (n > 0 ? it0 / per_head : 0), t0 + (n > 0 ? it0 % per_head : 0), t0, t1};
+    const Walk first{kvh * args.group + (n > 0 ? it0 / tiles : 0), n > 0 ? it0 % tiles : 0, tiles};
 
     // Row statistics of a query tile, four rows a lane of warp 2; the first are asked for before the set-up.
     constexpr int ST_ROWS = AV_TILE / 32;
@@ -595,10 +599,10 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
     Walk st_walk = first;
     auto st_fetch = [&]() {
         const int i0 = st_walk.tile * AV_TILE + lane;
-        const long long at = static_cast<long long>(st_walk.head) * args.Tq + sp.q0 + i0;
+        const long long at = static_cast<long long>(st_walk.head) * args.Tq + q_row + i0;
 #pragma unroll
         for (int r = 0; r < ST_ROWS; ++r) {
-            const bool row_ok = i0 + r * 32 < sp.nq;
+            const bool row_ok = i0 + r * 32 < rows;
             st_lse[r] = row_ok ? LSE[at + r * 32] : -INFINITY;
             st_delta[r] = row_ok ? delta[at + r * 32] : 0.0f;
         }
@@ -633,9 +637,9 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         fence_proxy_async_smem();
         if (n > 0) {
             av_load<D>(sK, &tmK, kv_full, kvh, sp.k0 + j0);
-            av_load<D>(sQ, &tmQ, &q_full[0], first.head, sp.q0 + first.tile * AV_TILE);
+            av_load<D>(sQ, &tmQ, &q_full[0], first.head, q_row + first.tile * AV_TILE);
             av_load<D>(sV, &tmV, kv_full, kvh, sp.k0 + j0);
-            av_load<D>(sdO, &tmdO, &do_full[0], first.head, sp.q0 + first.tile * AV_TILE);
+            av_load<D>(sdO, &tmdO, &do_full[0], first.head, q_row + first.tile * AV_TILE);
         }
     }
     if (warp == 1) {
@@ -665,11 +669,11 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                     int st = it % QST;
                     ok = wait_bounded(&q_empty[st], ((it / QST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sQ + st * T::BYTES, &tmQ, &q_full[st], w.head, sp.q0 + w.tile * AV_TILE);
+                    av_load<D>(sQ + st * T::BYTES, &tmQ, &q_full[st], w.head, q_row + w.tile * AV_TILE);
                     st = it % OST;
                     ok = wait_bounded(&do_empty[st], ((it / OST) & 1) ^ 1u, ctl);
                     if (!ok) break;
-                    av_load<D>(sdO + st * T::BYTES, &tmdO, &do_full[st], w.head, sp.q0 + w.tile * AV_TILE);
+                    av_load<D>(sdO + st * T::BYTES, &tmdO, &do_full[st], w.head, q_row + w.tile * AV_TILE);
                 }
             }
         } else if (warp == 1) {
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             Walk ahead = first;  // the iteration whose tiles have been waited for
             auto tiles_wait = [&]() {
                 if (!wait_all(&q_full[q_ahead.st], q_ahead.ph) || !wait_all(&do_full[do_ahead.st], do_ahead.ph)) return false;
-                if (q_tail < AV_TILE && ahead.tile == t1 - 1) {
+                if (q_tail < AV_TILE && ahead.tile == tiles - 1) {
                     av_clear_rows<D>(sQ + q_ahead.st * T::BYTES, q_tail, lane);
                     av_clear_rows<D>(sdO + do_ahead.st * T::BYTES, q_tail, lane);
                 }
@@ -842,7 +846,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 if (lane == 0) mbar_arrive(s_read);
             }
             // causal: a key is visible from column lo on; lo_w, the most, is the warp's last key's
-            const int lo_w = args.causal ? w0 + 31 - off - at.tile * AV_TILE - hf * 64 : 0;
+            const int lo_w = args.causal ? w0 + 31 - off - qf - at.tile * AV_TILE - hf * 64 : 0;
             const int lo = lo_w - 31 + (lane >> 2) - 2 * (lane & 3);  // of key lane / 4, against column 8 i + c
             auto prob = [&](auto masked) {
 #pragma unroll

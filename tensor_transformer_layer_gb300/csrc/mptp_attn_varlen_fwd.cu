@@ -21,8 +21,10 @@
 // faster; the two tiles taking turns at the exponentials made it 9 % slower.
 // Where few query tiles have long rows of keys, a cluster of two to eight CTAs shares a pair of query tiles: each takes a
 // part of its key tiles, and maxima, sums and fp32 outputs are joined through distributed shared memory in rank order.
-// Masked scores are replaced, not added to, so no value of a key outside a row's range reaches it. A
-// row without keys gets O = 0 and LSE = -inf.
+// Masked scores are replaced, not added to, and other sequences' rows of V are cleared, so that no value of theirs
+// reaches a row. A hidden key of the row's own sequence has the weight 0 in the product with V: an infinity or NaN in
+// its V makes O of the rows of its tile NaN, as the definition's product does. A row without keys gets O = 0 and
+// LSE = -inf whatever its tile holds.
 #include <type_traits>
 
 #include "mptp_attn_varlen.cuh"

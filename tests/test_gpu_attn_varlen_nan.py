@@ -81,3 +81,42 @@ def test_scores_of_minus_infinity(q_lens, k_lens):
 
     _, b = _runs(q_lens, k_lens, False, all_keys, grad=False)
     assert torch.isneginf(b["LSE"]).all() and not b["O"].any()
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [
+    ([200], [70]),           # 130 rows without keys: a whole tile, and two of the next
+    ([2300], [2200]),        # 100, where clusters share keys and queries
+    ([90, 300, 5], [40, 171, 0]),
+])
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_rows_without_keys_give_nothing(q_lens, k_lens, d):
+    # causal rows before the first key: whatever their Q and dO hold, no gradient comes from them
+    cu, at = _cu(q_lens), []
+    for i, (nq, nk) in enumerate(zip(q_lens, k_lens)):
+        at += range(int(cu[i]), int(cu[i]) + (nq if nk == 0 else max(0, nq - nk)))
+
+    def dirty(x):
+        x["Q"][at[0::2]] = NAN
+        x["Q"][at[1::2]] = float("inf")
+        x["dO"][at[0::3]] = float("inf")
+        x["dO"][at[1::3]] = NAN
+
+    a, b = _runs(q_lens, k_lens, True, dirty, d)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+    assert not b["O"][at].any() and not b["dQ"][at].any() and torch.isneginf(b["LSE"][:, at]).all()
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [([200], [70]), ([2300], [2200])])
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_rows_without_keys_stay_zero_beside_a_nan_key(q_lens, k_lens, d):
+    # K and V of a key in the tile that such rows' products run over
+    nq, nk = q_lens[0], k_lens[0]
+
+    def dirty(x):
+        x["K"][2] = NAN
+        x["V"][2] = float("inf")
+
+    _, b = _runs(q_lens, k_lens, True, dirty, d)
+    dead = nq - nk
+    assert not b["O"][:dead].any() and not b["dQ"][:dead].any() and torch.isneginf(b["LSE"][:, :dead]).all()
