@@ -114,6 +114,23 @@ __device__ __forceinline__ void av_load(uint8_t* dst, const CUtensorMap* map, ui
     tma_load_3d(dst, map, bar, 0, row, head * C::NB);
 }
 
+// A wait budget of zero stands for loads that never arrive, in every CTA or, of a cluster, in its last one: its first
+// tiles are not asked for, so that its waits do run out.
+__device__ __forceinline__ bool av_starved(const AvArgs& a, int rank, int cluster) {
+    return a.budget_ns == 0 && rank == cluster - 1;
+}
+
+// The part that the loading and issuing warps take in a cluster's join: its two barriers. Between them a CTA that gave up
+// makes the others of its cluster give up too: it sends them nothing, and what they would add in its place is old tiles.
+__device__ __forceinline__ void av_join_barriers(volatile uint32_t* abort_flag, int cluster, int warp, int lane) {
+    __syncwarp();
+    cluster_sync_all();
+    if (warp == 0 && lane < cluster && *abort_flag != 0u)
+        st_cluster_b32(mapa_shared(smem_u32(const_cast<uint32_t*>(abort_flag)), lane), 1u);
+    __syncwarp();
+    cluster_sync_all();
+}
+
 // One warp clears rows [from, 128) of a tile in shared memory. A tile that reaches past its sequence
 // holds the next one's rows: their products with zero weights would still carry infinities and NaN.
 template <int D>

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         *abort_flag = 0u;
         fence_mbarrier_init();
         fence_proxy_async_smem();
-        if (n > 0) {
+        if (n > 0 && !av_starved(args, rank, cluster)) {
             av_load<D>(sK, &tmK, &k_full[0], kvh, k_row);
             av_load<D>(sQ, &tmQ, q_full, head, sp.q0 + i0);
             av_load<D>(sV, &tmV, &v_full[0], kvh, k_row);
@@ -471,12 +471,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             }
         }
     }
-    if (JOIN && warp < 4) {
-        // (the softmax warps' two barriers)
-        __syncwarp();
-        cluster_sync_all();
-        cluster_sync_all();
-    }
+    if (JOIN && warp < 4) av_join_barriers(abort_flag, cluster, warp, lane);
 
     // ---------------- teardown ----------------
     tc_fence_before();
@@ -635,7 +630,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         *abort_flag = 0u;
         fence_mbarrier_init();
         fence_proxy_async_smem();
-        if (n > 0) {
+        if (n > 0 && !av_starved(args, rank, cluster)) {
             av_load<D>(sK, &tmK, kv_full, kvh, sp.k0 + j0);
             av_load<D>(sQ, &tmQ, &q_full[0], first.head, q_row + first.tile * AV_TILE);
             av_load<D>(sV, &tmV, kv_full, kvh, sp.k0 + j0);
@@ -953,7 +948,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             __syncwarp();
             cluster_sync_all();
             const float f = hf ? args.scale : 1.0f;
-            for (int c = 0; c < NB && ok; ++c) {
+            for (int c = 0; c < NB && ok && *abort_flag == 0u; ++c) {
                 const int id = hf * NB + c;
                 if (id % cluster != rank) continue;
                 uint32_t mine[32];
@@ -990,12 +985,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             }
         }
     }
-    if (JOIN && warp < 4) {
-        // (the softmax warps' two barriers)
-        __syncwarp();
-        cluster_sync_all();
-        cluster_sync_all();
-    }
+    if (JOIN && warp < 4) av_join_barriers(abort_flag, cluster, warp, lane);
 
     // ---------------- teardown ----------------
     tc_fence_before();

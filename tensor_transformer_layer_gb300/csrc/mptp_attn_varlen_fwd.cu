@@ -118,9 +118,10 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
         fence_mbarrier_init();
         fence_proxy_async_smem();
         // The first loads overlap the rest of the set-up.
-        if (n > 0) av_load<D>(sK, &tmK, &k_full[0], kvh, k_row);
+        const bool starved = av_starved(args, rank, cluster);
+        if (n > 0 && !starved) av_load<D>(sK, &tmK, &k_full[0], kvh, k_row);
         for (int g = 0; g < 2; ++g)
-            if (nt[g] > 0) av_load<D>(sQ + g * T::BYTES, &tmQ, &q_full[g], head, sp.q0 + qt[g] * AV_TILE);
+            if (nt[g] > 0 && !starved) av_load<D>(sQ + g * T::BYTES, &tmQ, &q_full[g], head, sp.q0 + qt[g] * AV_TILE);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
@@ -435,12 +436,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             }
         }
     }
-    if (JOIN && warp < 4) {
-        // (the softmax warps' two barriers)
-        __syncwarp();
-        cluster_sync_all();
-        cluster_sync_all();
-    }
+    if (JOIN && warp < 4) av_join_barriers(abort_flag, cluster, warp, lane);
 
     // ---------------- teardown ----------------
     tc_fence_before();
