@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
     grid_launch_dependents();
 
     if (warp == 0) {
-        if (lane == 0) {
+        // A wait budget of zero stands for loads that never arrive, of a cluster's in its last CTA.
+        if (lane == 0 && !(args.budget_ns == 0 && rank == cluster - 1)) {
             int st = 0;
             uint32_t ph = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -261,6 +262,9 @@ __global__ void __launch_bounds__(few_threads(FEW_MAX_PARTS)) gemm_few_kernel(co
                 }
             }
         }
+    } else if (warp == 0 && lane < cluster && cluster > 1 && *abort_flag != 0u) {
+        // This CTA gave up and sends nothing: the others would add old stages in its place. They give up too.
+        st_cluster_b32(mapa_shared(smem_u32(const_cast<uint32_t*>(abort_flag)), lane), 1u);
     }
     __syncwarp();
     if (cluster > 1)

@@ -241,3 +241,23 @@ def test_glu_bwd_wait_budget_exhaustion_with_few_tokens(monkeypatch):
     again = _run(inp, 1, "silu")
     for k in good:
         assert torch.equal(again[k], good[k]), k
+
+
+@pytest.mark.parametrize("T,h,f", [(9, 1536, 4096), (64, 512, 2048), (1, 64, 64)])
+def test_glu_with_few_tokens_stores_nothing_without_a_part(T, h, f, monkeypatch):
+    # Under a wait budget of zero the last CTA of every cluster (or each CTA alone) has no loads: no CTA of it stores.
+    inp = _inputs(T, h, f, seed=21700)
+    good = _run(inp, 1, "silu")
+    d = {k: v.cuda() for k, v in inp.items()}
+    o = {"Z": _nan(T, h), "Y": _nan(T, f), "GU": _nan(T, 2 * f), "dX": _nan(T, h), "dGU": _nan(T, 2 * f)}
+    dW, dWd = _nan(h, 2 * f), _nan(f, h)
+    monkeypatch.setenv("MPTP_WAIT_BUDGET_NS", "0")
+    mp().mp_glu_fwd(d["X"], d["W"], d["Wd"], o["Z"], o["Y"], o["GU"], t=1, act="silu")
+    mp().mp_glu_bwd(d["X"], d["W"], d["Wd"], good["GU"], good["Y"], d["dZ"], o["dX"], dW, dWd, o["dGU"], t=1, act="silu")
+    torch.cuda.synchronize()
+    for k, v in o.items():
+        assert torch.isnan(v.float()).all(), k
+    monkeypatch.delenv("MPTP_WAIT_BUDGET_NS")
+    again = _run(inp, 1, "silu")
+    for k in good:
+        assert torch.equal(again[k], good[k]), k
