@@ -219,6 +219,12 @@ inline bool av_tmap(CUtensorMap* m, const void* base, int cols, int rows, long l
     return make_tmap_bf16_sw64_3d(m, base, cols, rows, ld, AV_TILE, d / 32);
 }
 
+// Tiles of `rows` rows that sequences of no more than T rows together, `longest` each, can have.
+inline long long av_max_tiles(int nseq, int T, int longest, int rows) {
+    const long long each = static_cast<long long>(nseq) * ceil_div(longest, rows), all = T / rows + static_cast<long long>(nseq);
+    return each < all ? each : all;
+}
+
 // Sizes, pitches and pointers that the forward and the backward refuse alike.
 inline mp_status av_check(int nseq, int Tq, int Tk, int max_q, int max_k, int heads, int kv_heads, int d, float scale) {
     if (nseq < 0 || Tq < 0 || Tk < 0 || max_q < 0 || max_k < 0 || heads <= 0 || kv_heads <= 0 || d <= 0 ||
@@ -227,15 +233,11 @@ inline mp_status av_check(int nseq, int Tq, int Tk, int max_q, int max_k, int he
     if (heads % kv_heads != 0 || (d != 64 && d != 96 && d != 128) || max_q > Tq || max_k > Tk ||
         static_cast<long long>(heads) * d > 0x3fffffff)
         return MP_ERR_UNSUPPORTED_SHAPE;
-    // CTAs of the largest launch: one per sequence, head and tile of the longest sequence
-    const long long tiles = (max_q > max_k ? max_q : max_k) / AV_TILE + 1;
-    if (tiles * nseq > 0x7fffffffLL / AV_MAX_CLUSTER / heads) return MP_ERR_UNSUPPORTED_SHAPE;
+    // CTAs of the largest launches: the tiles that can exist, of every head, in the largest clusters
+    const long long most = 0x7fffffffLL / AV_MAX_CLUSTER;
+    if (av_max_tiles(nseq, Tq, max_q, AV_TILE) > most / heads || av_max_tiles(nseq, Tk, max_k, AV_TILE) > most / kv_heads)
+        return MP_ERR_UNSUPPORTED_SHAPE;
     return MP_OK;
-}
-// Tiles of `rows` rows that sequences of no more than T rows together, `longest` each, can have.
-inline long long av_max_tiles(int nseq, int T, int longest, int rows) {
-    const long long each = static_cast<long long>(nseq) * ceil_div(longest, rows), all = T / rows + static_cast<long long>(nseq);
-    return each < all ? each : all;
 }
 inline bool av_bad_pitch(long long ld, long long row) { return ld < row || ld % 8 != 0 || ld > (1LL << 36); }
 

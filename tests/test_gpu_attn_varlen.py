@@ -336,3 +336,27 @@ def test_attn_varlen_shared_key_tiles(lens, heads, kv, d):
         again = _run(inp, cu, cu, causal)
         for k in got:
             assert torch.equal(got[k], again[k]), k
+
+
+@pytest.mark.parametrize("same", [True, False])
+def test_attn_varlen_a_thousand_sequences(same):
+    # most of a token or two, or empty; a long one among the last
+    rng = np.random.default_rng(23500)
+    q_lens = rng.choice([0, 1, 1, 2, 3, 17], 1100)
+    k_lens = q_lens if same else rng.choice([0, 1, 2, 5, 40], 1100)
+    q_lens[1090] = k_lens[1090] = 700
+    cu_q, cu_k = _cu(q_lens), _cu(k_lens)
+    inp = _inputs(int(sum(q_lens)), int(sum(k_lens)), 2, 1, 64, seed=23510)
+    got = _run(inp, cu_q, cu_k, True, max_q=700, max_k=int(sum(k_lens)))
+    _check(got, inp, cu_q, cu_k, True)
+
+
+def test_attn_varlen_a_bad_sequence_far_back_is_reported():
+    # the sequence behind a thousand others is too long: the call says so, and the others are right
+    lens = [3] * 1000 + [50]
+    cu = _cu(lens)
+    inp = _inputs(sum(lens), sum(lens), 2, 2, 64, seed=23600)
+    want = _run(inp, cu, cu, True)
+    got = _run(inp, cu, cu, True, max_q=40, max_k=40, status=mp().MP_DEV_SEQ_RANGE)
+    for k in ("O", "dQ", "dK", "dV"):
+        assert torch.equal(got[k][:3000], want[k][:3000]) and torch.isnan(got[k][3000:].float()).all(), k

@@ -118,3 +118,13 @@ def test_attn_varlen_no_sequences_is_a_noop(L):
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device answer")
 def test_attn_varlen_no_device_answer(L):
     assert _attn(L) == 4
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device answer")
+def test_attn_varlen_takes_many_sequences_under_a_long_maximum(L):
+    # 4096 sequences of which one may be 131,072 long: the tiles that can exist are few
+    kw = dict(nseq=4096, max_q=131072, max_k=131072, heads=64, kv=8)
+    assert _attn(L, Tq=1 << 20, Tk=1 << 20, **kw) == 4
+    # more tiles than a grid has CTAs
+    assert _attn(L, Tq=2147483647, Tk=2147483647, **{**kw, "nseq": 1 << 22}) == 2
+    assert _attn(L, Tq=1 << 20, Tk=2147483647, **{**kw, "nseq": 1 << 22, "max_q": 100}) == 2
