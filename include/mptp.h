@@ -400,7 +400,8 @@ MP_API mp_status mp_glu_bwd(const mp_bf16* X, const mp_bf16* W, const mp_bf16* W
  *   A = pos[axis][token] * base^(-i / n), or with MP_ROPE_PER_AXIS base^(-j / sections[axis])
  *   for the j-th pair of its axis.
  * MP_ROPE_INVERSE rotates back by -A: the gradient of the rotation. Elements [2n, d) pass through.
- * Angles are exact to 2^-20 turns for every int32 position (64-bit binary fractions of a turn).
+ * For every int32 position angles are exact to 2^-20 turns where base >= 1 (64-bit binary fractions of a turn), and
+ * below to 2^-20 / base turns: the frequencies, up to 1 / base radians a step, are computed in double.
  *   x, y [T, heads, d], rows ldx, ldy elements apart (views of a packed projection are fine);
  *   y may be x itself (then ldx == ldy), and must not overlap it otherwise. pos [axes, T] int32.
  *   sections: `axes` ints in host memory, read during the call.

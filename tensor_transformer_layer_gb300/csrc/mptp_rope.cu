@@ -11,7 +11,7 @@
 // and pos * F modulo 2^64 is the exact fraction of a turn that the position stands for: one
 // 64-bit integer product, whose top 32 bits go to sincospif. F is within 2^-53 of the frequency
 // (the host's double), so at position 2^31 the angle is off by less than 2^-21 turns, and the
-// conversion to float adds 2^-25 turns.
+// conversion to float adds 2^-25 turns. (For a base below 1, 1 / base times that.)
 //
 // Bound by memory: x is read and y written once. One warp takes one token (or a share of its
 // heads when tokens are few): a lane owns VEC neighbouring pairs, computes their sines once and
@@ -200,7 +200,9 @@ extern "C" mp_status mp_rope_axes(const mp_bf16* x, mp_bf16* y, const int32_t* p
         for (int j = 0; j < sections[ax]; ++j, ++i) {
             const double e = (flags & MP_ROPE_PER_AXIS) ? static_cast<double>(j) / sections[ax]
                                                         : static_cast<double>(i) / static_cast<double>(pairs);
-            // base < 1 turns faster than one radian a step: only the fraction of a turn matters.
+            // base < 1 turns faster than one radian a step: only the fraction of a turn matters, of which the double
+            // has lost what the frequency's whole turns take (at position 2^31: 1.4e-7 turns at base 0.5, 7.9e-6 at
+            // 0.01, 1.2e-3 at 1e-4; 7e-8 at most from base 1 on).
             double f = std::pow(base, -e) * 0.15915494309189533577;
             f -= std::floor(f);
             const double scaled = std::ldexp(f, 64);

@@ -100,3 +100,31 @@ def test_rope_empty_batch_and_other_stream():
     mp().mp_rope_axes(dev, y, p, sections=(32,), stream=s)
     s.synchronize()
     _check(y.cpu(), xs, pos, (32,), 10000.0)
+
+
+@pytest.mark.parametrize("base", [2.0, 1.0, 0.5, 0.01])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_farthest_positions_at_small_bases(base, inverse):
+    # Angles from 80 decimal digits: within 2^-20 turns, or 2^-20 / base where the base is below 1; on the pair's two
+    # elements as radians, with half a bf16 step of the result and the fp32 arithmetic (three roundings, 2^-24 each).
+    from decimal import Decimal, getcontext
+    getcontext().prec = 80
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534")
+    n, pos = 48, [2147483647, -2147483648, 2147480001, 1999999973, -1234567891, 77]
+    turns = np.zeros((len(pos), n))
+    for i in range(n):
+        f = Decimal(base) ** (-Decimal(i) / Decimal(n)) / two_pi
+        for k, p in enumerate(pos):
+            t = p * f
+            turns[k, i] = float(t - t.to_integral_value())
+    ang = 2 * np.pi * turns * (-1 if inverse else 1)
+    x = synth.normal_bf16((len(pos), 3, 2 * n), 1.0, 20500)
+    y = torch.empty(len(pos), 3, 2 * n, dtype=torch.bfloat16, device="cuda")
+    mp().mp_rope_axes(x.cuda(), y, torch.tensor([pos], dtype=torch.int32, device="cuda"), sections=(n,), base=base,
+                      inverse=inverse)
+    a, b = f64(x)[..., :n], f64(x)[..., n:]
+    c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+    want = np.concatenate([a * c - b * s, b * c + a * s], -1)
+    size = np.concatenate([np.abs(a) + np.abs(b)] * 2, -1)
+    tol = 2.0 ** -8 * np.abs(want) + (2 * np.pi * 2.0 ** -20 / min(base, 1.0) + 2.0 ** -22) * size
+    assert np.all(np.abs(f64(y.cpu()) - want) <= tol)
