@@ -248,9 +248,7 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             }
             // One wait on the softmax an iteration, and three products behind it: dP(j+1), which it needs next,
             // dQ(j), and S(j+2) over dS(j) once that has been used. (With a wait before each of the products the
-            // tensor core ran dry at every one: 2140 cycles an iteration at D = 128, 1536 of them products.) With
-            // four K tiles the one of S(j+2) is here before that wait.
-            constexpr bool K_EARLY = false;
+            // tensor core ran dry at every one: 2140 cycles an iteration at D = 128, 1536 of them products.)
             if (ok && n > 1 && (ok = k_wait())) {
                 tc_fence_after();
                 s_mma(1);
@@ -258,7 +256,6 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
             for (int j = 0; j < n && ok; ++j) {
                 const bool more = j + 1 < n, ahead = j + 2 < n;
                 if (more && !(ok = v_wait())) break;
-                if (K_EARLY && ahead && !(ok = k_wait())) break;
                 // The foreign rows of the last key tile, which dQ sums over: S needs no clearing, its columns are masked.
                 if (!more && k_tail < AV_TILE) av_clear_rows<D>(sK + k_sum.st * T::BYTES, k_tail, lane);
                 if (!(ok = wait_all(ds_full, j & 1))) break;
@@ -273,10 +270,8 @@ __global__ void __launch_bounds__(AV_THREADS, 1)
                 umma_commit_elect(&k_empty[k_sum.st]);
                 k_sum.next();
                 if (ahead) {
-                    if (!K_EARLY) {
-                        if (!(ok = k_wait())) break;
-                        tc_fence_after();
-                    }
+                    if (!(ok = k_wait())) break;
+                    tc_fence_after();
                     s_mma(j & 1);
                 }
             }
