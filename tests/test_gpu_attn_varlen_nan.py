@@ -120,3 +120,25 @@ def test_rows_without_keys_stay_zero_beside_a_nan_key(q_lens, k_lens, d):
     _, b = _runs(q_lens, k_lens, True, dirty, d)
     dead = nq - nk
     assert not b["O"][:dead].any() and not b["dQ"][:dead].any() and torch.isneginf(b["LSE"][:, :dead]).all()
+
+
+@pytest.mark.parametrize("q_lens,k_lens,heads,kv", [
+    ([40, 30, 5], [4500, 4333, 3000], 2, 1),     # clusters share the keys (forward, dQ)
+    ([900, 130, 77], [900, 130, 77], 8, 1),      # clusters share the queries (dK, dV)
+])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_other_sequences_do_not_leak_through_clusters(q_lens, k_lens, heads, kv, causal, d):
+    # the second sequence is all NaN, the third infinite: the first is as without them
+    nq, nk = q_lens[0], k_lens[0]
+
+    def dirty(x):
+        for k, v in x.items():
+            lens = k_lens if k in ("K", "V") else q_lens
+            v[lens[0]:lens[0] + lens[1]] = NAN
+            v[lens[0] + lens[1]:] = float("inf")
+
+    a, b = _runs(q_lens, k_lens, causal, dirty, d, heads=heads, kv=kv)
+    for k in a:
+        sl = (slice(None), slice(0, nq)) if k == "LSE" else slice(0, nk if k in ("dK", "dV") else nq)
+        assert torch.equal(a[k][sl], b[k][sl]), k
