@@ -402,6 +402,14 @@ def mp_attn_fwd(X, Wqkv, Wo, out, QKV, O, *, b: int, s: int, heads: int, t: int,
     _check("mp_attn_fwd", code)
 
 
+def _i32(x, name):
+    """x as an int that a C int holds: ctypes would keep the low 32 bits of a larger one."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 ACTS = {"silu": 0, "gelu": 1}
 
 
@@ -413,12 +421,13 @@ def _act(act):
 
 def mp_glu_fwd(X, W, Wd, Z, Y, GU_save=None, *, t: int, act: str = "silu", d_status=None, stream=None) -> None:
     """Gated feed-forward block: [G | U] = X W, Y = act(G) * U, Z = Y Wd; W [h, 2f], act "silu" or "gelu"."""
+    t = _i32(t, "t")
     T, h = X.shape
     f = Wd.shape[0]
     code = lib().mp_glu_fwd(
         _ptr(X, "X", shape=(T, h)), _ptr(W, "W", shape=(h, 2 * f)), _ptr(Wd, "Wd", shape=(f, h)),
         _ptr(Z, "Z", shape=(T, h)), _ptr(Y, "Y", shape=(T, f)),
-        _ptr(GU_save, "GU_save", shape=(T, 2 * f), allow_none=True), T, h, f, int(t), _act(act),
+        _ptr(GU_save, "GU_save", shape=(T, 2 * f), allow_none=True), T, h, f, t, _act(act),
         _status_ptr(d_status), _stream(stream))
     _check("mp_glu_fwd", code)
 
@@ -426,13 +435,14 @@ def mp_glu_fwd(X, W, Wd, Z, Y, GU_save=None, *, t: int, act: str = "silu", d_sta
 def mp_glu_bwd(X, W, Wd, GU, Y, dZ, dX, dW, dWd, dGU_ws, *, t: int, act: str = "silu", d_status=None,
                stream=None) -> None:
     """Backward of mp_glu_fwd from its GU_save and Y: dX [T,h], dW [h,2f], dWd [f,h]; dGU_ws [T,2f] workspace."""
+    t = _i32(t, "t")
     T, h = X.shape
     f = Wd.shape[0]
     code = lib().mp_glu_bwd(
         _ptr(X, "X", shape=(T, h)), _ptr(W, "W", shape=(h, 2 * f)), _ptr(Wd, "Wd", shape=(f, h)),
         _ptr(GU, "GU", shape=(T, 2 * f)), _ptr(Y, "Y", shape=(T, f)), _ptr(dZ, "dZ", shape=(T, h)),
         _ptr(dX, "dX", shape=(T, h)), _ptr(dW, "dW", shape=(h, 2 * f)), _ptr(dWd, "dWd", shape=(f, h)),
-        _ptr(dGU_ws, "dGU_ws", shape=(T, 2 * f)), T, h, f, int(t), _act(act), _status_ptr(d_status), _stream(stream))
+        _ptr(dGU_ws, "dGU_ws", shape=(T, 2 * f)), T, h, f, t, _act(act), _status_ptr(d_status), _stream(stream))
     _check("mp_glu_bwd", code)
 
 
@@ -472,7 +482,7 @@ def _heads_view(x, name, shape=None):
 @functools.lru_cache(maxsize=64)
 def _int_array(values):
     """Length and C array of a tuple of ints (read only)."""
-    return len(values), (_I * max(len(values), 1))(*(int(v) for v in values))
+    return len(values), (_I * max(len(values), 1))(*(_i32(v, "sections") for v in values))
 
 
 def mp_rope_axes(x, y, pos, *, sections, base: float = 10000.0, interleaved: bool = False, per_axis: bool = False,
@@ -510,13 +520,14 @@ def mp_attn_varlen_fwd(Q, K, V, O, LSE, cu_q, cu_k, *, max_q: int, max_k: int, c
     """Attention over packed sequences: O [Tq, heads, d] and LSE [heads, Tq] fp32 from Q [Tq, heads, d], K, V
     [Tk, kv_heads, d] (rows may be strided). cu_q, cu_k [nseq + 1] int32: sequence i owns rows cu[i] .. cu[i+1]-1;
     max_q, max_k: at least the longest. causal: the last query sees the last key. scale: 1 / sqrt(d) by default."""
+    max_q, max_k = _i32(max_q, "max_q"), _i32(max_k, "max_k")
     nseq, qs, ks, pcq, pck = _packed_shapes(Q, K, cu_q, cu_k)
     (Tq, heads, d), (Tk, kv, _) = qs, ks
     (pq, ldq), (pk, ldk) = _heads_view(Q, "Q", qs), _heads_view(K, "K", ks)
     (pv, ldv), (po, ldo) = _heads_view(V, "V", ks), _heads_view(O, "O", qs)
     code = lib().mp_attn_varlen_fwd(
-        pq, pk, pv, po, _ptr(LSE, "LSE", torch.float32, (heads, Tq)), pcq, pck, nseq, Tq, Tk, int(max_q),
-        int(max_k), heads, kv, d, ldq, ldk, ldv, ldo, 1 if causal else 0, d ** -0.5 if scale is None else float(scale),
+        pq, pk, pv, po, _ptr(LSE, "LSE", torch.float32, (heads, Tq)), pcq, pck, nseq, Tq, Tk, max_q,
+        max_k, heads, kv, d, ldq, ldk, ldv, ldo, 1 if causal else 0, d ** -0.5 if scale is None else float(scale),
         _status_ptr(d_status), _stream(stream))
     _check("mp_attn_varlen_fwd", code)
 
@@ -525,6 +536,7 @@ def mp_attn_varlen_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, delta_ws, cu_q, cu_k, *,
                        scale: float | None = None, d_status=None, stream=None) -> None:
     """Backward of mp_attn_varlen_fwd from its O and LSE: dQ, dK, dV (rows may be strided, e.g. the parts of a
     packed projection's gradient); delta_ws [heads, Tq] fp32 workspace."""
+    max_q, max_k = _i32(max_q, "max_q"), _i32(max_k, "max_k")
     nseq, qs, ks, pcq, pck = _packed_shapes(Q, K, cu_q, cu_k)
     (Tq, heads, d), (Tk, kv, _) = qs, ks
     (pq, ldq), (pk, ldk), (pv, ldv) = _heads_view(Q, "Q", qs), _heads_view(K, "K", ks), _heads_view(V, "V", ks)
@@ -534,7 +546,7 @@ def mp_attn_varlen_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, delta_ws, cu_q, cu_k, *,
     f32 = torch.float32, (heads, Tq)
     code = lib().mp_attn_varlen_bwd(
         pq, pk, pv, po, _ptr(LSE, "LSE", *f32), pdo, pdq, pdk, pdv, _ptr(delta_ws, "delta_ws", *f32), pcq, pck, nseq,
-        Tq, Tk, int(max_q), int(max_k), heads, kv, d, ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv, 1 if causal else 0,
+        Tq, Tk, max_q, max_k, heads, kv, d, ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv, 1 if causal else 0,
         d ** -0.5 if scale is None else float(scale), _status_ptr(d_status), _stream(stream))
     _check("mp_attn_varlen_bwd", code)
 

@@ -128,3 +128,21 @@ def test_attn_varlen_takes_many_sequences_under_a_long_maximum(L):
     # more tiles than a grid has CTAs
     assert _attn(L, Tq=2147483647, Tk=2147483647, **{**kw, "nseq": 1 << 22}) == 2
     assert _attn(L, Tq=1 << 20, Tk=2147483647, **{**kw, "nseq": 1 << 22, "max_q": 100}) == 2
+
+
+def test_binding_refuses_numbers_that_a_c_int_would_cut():
+    # 2^32 would arrive as 0: a call that does nothing and says that all is well
+    import tensor_transformer_layer_gb300 as mp
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    f, cu = torch.zeros(2, 4), torch.tensor([0, 4], dtype=torch.int32)
+    for kw in (dict(max_q=1 << 32, max_k=4), dict(max_q=4, max_k=(1 << 32) + 4)):
+        with pytest.raises(ValueError, match="32 bits"):
+            mp.mp_attn_varlen_fwd(x, x, x, x, f, cu, cu, causal=True, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            mp.mp_attn_varlen_bwd(x, x, x, x, f, x, x, x, x, f, cu, cu, causal=True, **kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        mp.mp_glu_fwd(x[0], x[0], x[0], x[0], x[0], t=(1 << 32) + 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        mp.mp_glu_bwd(*[x[0]] * 10, t=(1 << 32) + 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        mp._int_array(((1 << 32) + 16,))
