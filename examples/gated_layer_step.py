@@ -9,6 +9,7 @@
     Y       = H + (act(H Wg) * (H Wu)) Wd  (mp_glu_fwd / _bwd)
     loss    = mean((Y - target)^2) / 2
 
+A step goes down h times its gradient, that of the tokens' mean squared error.
 The layer has no normalisation, to keep to the point. Every buffer is made once, in `Layer`; a step
 allocates only torch's matrix products.
 """

@@ -430,9 +430,12 @@ MP_API mp_status mp_rope_axes(const mp_bf16* x, mp_bf16* y, const int32_t* pos,
  *   cu_q, cu_k [nseq + 1] int32 in device memory, ascending, within the tensors; max_q, max_k: at
  *   least the longest sequence's rows. A sequence that breaks this is left out (its outputs are not
  *   written) and sets MP_DEV_SEQ_RANGE; where offsets that descend make others overlap, rows of theirs
- *   may be left out too.
+ *   may be left out too. max_q == 0 (backward: max_q == max_k == 0) says that there is nothing to do: MP_OK, and the
+ *   offsets are not read.
  *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; max_q <= Tq, max_k <= Tk; pitches at
  *   least a row and multiples of 8; scale > 0 and finite.
+ *   A tile finds its sequence by a search through the offsets, 32 at a time, so many very short sequences cost more than
+ *   their number: 512 of 8 tokens (eight heads on two, d = 64) 0.17 ms, 4096 3.2 ms.
  */
 MP_API mp_status mp_attn_varlen_fwd(const mp_bf16* Q, const mp_bf16* K, const mp_bf16* V,
                              mp_bf16* O, float* LSE,

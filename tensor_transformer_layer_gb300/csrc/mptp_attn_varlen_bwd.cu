@@ -9,7 +9,8 @@
 // products per pair of tiles where five would do, but no gradient is summed across CTAs: no atomics,
 // no fp32 gradient in memory, a fixed order and so the same bits every run. (One kernel with five
 // products would also be bound by shared memory: at D = 128 its dS goes through it once more and 64 KB
-// of fp32 dQ per pair of tiles leave through it, against 64 KB a tile of K or Q loads for each here.)
+// of fp32 dQ per pair of tiles leave through it, against 64 KB a tile of K or Q loads for each here. That is an estimate
+// for D = 128; at D = 64, where both kernels wait for the same softmax, one kernel has not been measured.)
 //
 // dQ kernel: CTA = (sequence, query head, 128 queries). Per key tile S = Q K^T, dP = dO V^T and
 //   dQ += dS K with dS (bf16) read from tensor memory. S has two buffers and is computed two tiles ahead,
@@ -29,11 +30,12 @@
 //   distributed shared memory in rank order. The dQ kernel shares a query tile's keys the same way.
 // In the first, a softmax thread has one row and 64 of its 128 columns; in the second, four keys' fragments.
 // Both are bound by the hand-overs between softmax and products (tensor core 65 to 67 % active at D = 128): 4096
-// tokens, 19 heads, not causal, dQ 113, 132, 158 us and dK with dV 138, 179, 208 us for D = 64, 96, 128 (1.08 to 1.55
-// and 1.18 to 1.57 PFLOP/s). The warp that issues the products is on the way between them: rings counted along instead
+// tokens, 19 heads, not causal, dQ 114, 134, 158 us and dK with dV 139, 180, 210 us for D = 64, 96, 128 (1.07 to 1.55
+// and 1.17 to 1.55 PFLOP/s). The warp that issues the products is on the way between them: rings counted along instead
 // of remainders, and no clearing between a wait and a product, took dQ from 139 and 166 us at D = 96 and 128. Sixteen softmax warps of half the columns each were 1 to 10 % slower.
 //
-// P and dS are rounded to bf16 for their products (the tensor core's operand type); the exponent,
+// P and dS are rounded to bf16 for their products (the tensor core's operand type; with the results' own rounding, dQ,
+// dK and dV are 2.4e-3 of their norm off, the results of fp32 products rounded once 1.7e-3); the exponent,
 // delta, and every sum are fp32. Hidden pairs' dS (for dQ) and P (for dV, and through it dS for dK) are replaced by zero
 // after the arithmetic; rows of a tile behind the sequence's end are cleared in shared memory where they would be summed
 // over, and queries that see no key are not loaded.
@@ -1014,7 +1016,7 @@ static int dkv_cluster(const AvArgs& a, int sms) {
 
 // CTAs that share a query tile, as the key kernel below shares key tiles; iterations are key tiles. A CTA costs five more
 // than its own, one of a cluster nine to fourteen. Measured with 1, 2, 4, 8, both kernels: one query on 16,384 keys, eight
-// heads, d = 128, 157, 100, 71, 60 us; 4096 causal queries, d = 64, one head 44, 34, 29, 40, eight heads 64, 80, 106, 180.
+// heads, d = 128, the same tensors every time, 157, 100, 71, 60 us (88 where they come from memory); 4096 causal queries, d = 64, one head 44, 34, 29, 40, eight heads 64, 80, 106, 180.
 static int dq_cluster(const AvArgs& a, int sms) {
     const double items = double(av_max_tiles(a.nseq, a.Tq, a.max_q, AV_TILE)) * a.heads;
     const double extra[4] = {5.0, 9.0, 12.0, 14.0};

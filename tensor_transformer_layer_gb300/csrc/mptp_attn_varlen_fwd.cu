@@ -16,7 +16,7 @@
 //           unrounded probabilities, which are rounded to bf16 for the product with V.
 // Bound by the hand-overs between softmax and products, not by either's rate: a pair of key tiles takes 2800 to 3060
 // cycles, in which the tensor core has 1024 (D = 64) to 2048 (D = 128) of work and the exponentials 1024. 4096 tokens,
-// 19 heads, not causal: 92, 100 and 112 us for D = 64, 96, 128 (0.88, 1.22, 1.46 PFLOP/s). At D = 64, P in columns of
+// 19 heads, not causal: 93, 101 and 113 us for D = 64, 96, 128 (0.88, 1.22, 1.44 PFLOP/s). At D = 64, P in columns of
 // its own, so that the next scores are computed beside the softmax, made this kernel 5 % faster and a training step no
 // faster; the two tiles taking turns at the exponentials made it 9 % slower.
 // Where few query tiles have long rows of keys, a cluster of two to eight CTAs shares a pair of query tiles: each takes a

@@ -18,8 +18,12 @@
 // (mptp_gemm_few.cuh).
 // Backward: one GEMM gives dY, whose epilogue reads G and U and writes dG and dU (dY never reaches
 // memory); dX, dW and dWd are three GEMMs, side by side where that is shorter (mptp_mlp_host.cuh).
-// Bound by the tensor core: T = 8192, h = 2304, f = 6144, SiLU, 1.287 ms forward and backward, 1.62 PFLOP/s, 94 % of
-// the library's sustained rate for a plain product. Alone, the launches take 245 us ([G | U] and Y), 120 (Z), 157 (dG
+// Roundings to bf16: Y, dG and dU as operands of the next product, which the tensor core wants in 16 bits, and G and U
+// between the passes, as U of the GeLU block is: fp32 would add 200 MB to the 500 MB that bound the kernel of dG and dU,
+// computing them again in the backward 22 % of a step's products. Each costs what one rounding of the result does: Z and
+// dWd are 2.3e-3 of their norm off, dX and dW 3.0e-3, results of fp32 products rounded once 1.7e-3.
+// Bound by the tensor core: T = 8192, h = 2304, f = 6144, SiLU, 1.26 to 1.31 ms forward and backward, 1.59 to 1.65 PFLOP/s,
+// 93 to 96 % of the library's sustained rate for a plain product. Alone, the launches take 245 us ([G | U] and Y), 120 (Z), 157 (dG
 // and dU: 119 without the epilogue, whose gates, ups and gradients are 500 MB beside the K loop), 241, 240 and 122.
 #include <algorithm>
 
