@@ -72,7 +72,8 @@ typedef enum mp_status {
     MP_ERR_TIMEOUT = 6,           /* device bit MP_DEV_TIMEOUT was found (see mp_status_from_device) */
     MP_ERR_TARGET_RANGE = 7,      /* device bit MP_DEV_TARGET_RANGE was found */
     MP_ERR_WORKSPACE = 8,         /* workspace too small */
-    MP_ERR_SEQ_RANGE = 9          /* device bit MP_DEV_SEQ_RANGE was found */
+    MP_ERR_SEQ_RANGE = 9,         /* device bit MP_DEV_SEQ_RANGE was found */
+    MP_ERR_PAGE_RANGE = 10        /* device bit MP_DEV_PAGE_RANGE was found */
 } mp_status;
 
 typedef uint16_t mp_bf16; /* raw bfloat16 bits */
@@ -81,6 +82,7 @@ typedef uint16_t mp_bf16; /* raw bfloat16 bits */
 #define MP_DEV_TIMEOUT 0x1u
 #define MP_DEV_TARGET_RANGE 0x2u
 #define MP_DEV_SEQ_RANGE 0x4u
+#define MP_DEV_PAGE_RANGE 0x8u
 
 /*
  * Forward of the sharded MLP block.
@@ -466,6 +468,107 @@ MP_API mp_status mp_attn_varlen_bwd(const mp_bf16* Q, const mp_bf16* K, const mp
                              long long lddo, long long lddq, long long lddk, long long lddv,
                              int causal, float scale,
                              uint32_t* d_status, void* stream);
+
+/*
+ * Norm of queries and keys for each head, with their rotation in the same pass: x [T, heads, d] holds q_heads query heads,
+ * then the key heads (a view of a packed projection is fine). Of each head
+ *   n = x / sqrt(mean(x^2) + eps),  y = R(w * n),  w = wq for the first q_heads heads, wk for the others,
+ * R the rotation of mp_rope_axes (pos, axes, sections, base, MP_ROPE_INTERLEAVED and MP_ROPE_PER_AXIS as there). fp32
+ * throughout, one rounding to bf16.
+ *   x, y [T, heads, d], rows ldx, ldy elements apart; y may be x itself (then ldx == ldy), and must not overlap it
+ *   otherwise. wq, wk [d]: the one that no head takes may be NULL. pos [axes, T] int32.
+ *   Size rules as mp_rope_axes; 0 <= q_heads <= heads; eps > 0 and finite. Squares are fp32: a head whose mean square
+ *   passes 2^127 gives zeros.
+ */
+MP_API mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16* wq, const mp_bf16* wk, const int32_t* pos,
+                          int T, int heads, int q_heads, int d, long long ldx, long long ldy,
+                          int axes, const int* sections, double base, float eps, uint32_t flags,
+                          void* stream);
+
+/*
+ * Its backward, from x and dy (the gradient of y); the norms are computed again:
+ *   g = R^-1 dy,  dw = sum over tokens and heads of g * n,  dx = (w * g - n mean(w * g * n)) / sqrt(mean(x^2) + eps)
+ *   dwq, dwk [d] fp32 (the one that no head takes may be NULL), dx [T, heads, d] with pitch lddx; dx may be dy or x
+ *   itself (then their pitches are equal). workspace: mp_qk_norm_rope_bwd_workspace_bytes(T, heads, d) bytes (0 for
+ *   sizes outside the rules), whatever they hold. T = 0 zeroes dwq and dwk. Everything else as mp_qk_norm_rope.
+ */
+MP_API size_t mp_qk_norm_rope_bwd_workspace_bytes(int T, int heads, int d);
+MP_API mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp_bf16* dx, const mp_bf16* wq,
+                              const mp_bf16* wk, float* dwq, float* dwk, const int32_t* pos,
+                              void* workspace, size_t workspace_bytes,
+                              int T, int heads, int q_heads, int d, long long ldx, long long lddy, long long lddx,
+                              int axes, const int* sections, double base, float eps, uint32_t flags,
+                              void* stream);
+
+/*
+ * A cache of keys and values in 8 bits. The pool has `pages` pages of `page` tokens (16, 32, 64 or 128): kc, vc
+ * [pages][kv_heads][page][d] e4m3 codes and ks, vs [pages][kv_heads] fp32 scales; a value is code * scale. Codes of a page
+ * are contiguous, pages ld_kc, ld_vc bytes apart (keys and values may lie side by side in one pool); a page's scales are
+ * contiguous, ld_ks, ld_vs floats from page to page. Sequence i's token at position j lies in page page_table[i][j / page],
+ * slot j % page; page_table [nseq][max_pages] int32.
+ *
+ * mp_kv_cache_write: rows [cu[i], cu[i+1]) of K, V [T, kv_heads, d] bf16 (rows ldk, ldv elements apart) become positions
+ * start[i] ... of sequence i. A page's scale for a head is the smallest power of two s with |x| <= 448 s for every
+ * finite value x written there (at least 2^-100), and a code x / s rounded to nearest; codes that a part-filled page holds
+ * already (slots before start) keep the larger of its scale (rounded up to a power of two) and the new rows', and are
+ * rounded again if that is a larger one. An infinity or NaN becomes the code NaN, and so do all codes of a part-filled page whose
+ * scale is not in (0, 2^120]. Pages are written by one sequence a call: two that name the same page to write race.
+ *
+ * mp_kv_cache_read: the same rows back, K, V = code * scale rounded to bf16: packed rows as mp_attn_varlen_fwd takes them.
+ * start NULL: every sequence from position 0.
+ *
+ *   cu [nseq + 1], start [nseq] int32 in device memory; max_n: at least the longest sequence's rows. A sequence whose rows lie
+ *   outside [0, T], pass max_n or reach behind its max_pages * page positions is left out and sets MP_DEV_SEQ_RANGE; where
+ *   offsets that descend make others overlap, rows of theirs may be left out too. A page outside the pool is left out and sets
+ *   MP_DEV_PAGE_RANGE. Rows, slots and pages of no sequence stay as they were. max_n == 0: nothing to do.
+ *   Size rules: d % 16 == 0, d <= 256; max_n <= T; ldk, ldv at least a row and multiples of 8; ld_kc, ld_vc at least
+ *   kv_heads * page * d and multiples of 16; ld_ks, ld_vs >= kv_heads; pages, max_pages >= 1; max_pages * page < 2^31.
+ */
+MP_API mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V,
+                            uint8_t* kc, uint8_t* vc, float* ks, float* vs, const int32_t* page_table,
+                            const int32_t* cu, const int32_t* start,
+                            int nseq, int T, int max_n, int kv_heads, int d, int page, int pages, int max_pages,
+                            long long ldk, long long ldv, long long ld_kc, long long ld_vc,
+                            long long ld_ks, long long ld_vs,
+                            uint32_t* d_status, void* stream);
+MP_API mp_status mp_kv_cache_read(const uint8_t* kc, const uint8_t* vc, const float* ks, const float* vs,
+                           mp_bf16* K, mp_bf16* V, const int32_t* page_table,
+                           const int32_t* cu, const int32_t* start,
+                           int nseq, int T, int max_n, int kv_heads, int d, int page, int pages, int max_pages,
+                           long long ldk, long long ldv, long long ld_kc, long long ld_vc,
+                           long long ld_ks, long long ld_vs,
+                           uint32_t* d_status, void* stream);
+
+/*
+ * Attention over that cache: rows [cu_q[i], cu_q[i+1]) of Q are queries of sequence i, whose cache holds lens[i] tokens (the
+ * queries' own among them). Query head j reads key head j / (heads / kv_heads).
+ *   S = scale Q K^T,  LSE = log sum_k exp S,  O = exp(S - LSE) V,  K, V = code * scale
+ * causal != 0: the last query sees the last token, as in mp_attn_varlen_fwd. A row that sees no key gets O = 0 and
+ * LSE = -inf. Made for the few new tokens of a decoding step; a longer prompt's queries are faster through
+ * mp_kv_cache_read and mp_attn_varlen_fwd.
+ *   Q, O [Tq, heads, d] bf16, rows ldq, ldo elements apart; LSE [heads, Tq] fp32; the pool as above, of which slots at
+ *   lens[i] and behind may hold anything, and scales are not negative. A NaN among the scores that a row sees makes its O
+ *   and LSE NaN; a NaN in V of a token of the sequence that a causal row does not see may make its O NaN too.
+ *   max_q: at least the longest sequence's queries. A sequence with rows outside [0, Tq], more than max_q queries or a
+ *   length outside [0, max_pages * page] is left out and sets MP_DEV_SEQ_RANGE; a page outside the pool sets
+ *   MP_DEV_PAGE_RANGE and gives the rows that would see it O = LSE = NaN. Rows of no sequence are not written.
+ *   workspace: mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q) bytes (0 for sizes outside the rules), whose first
+ *   MP_ATTN_CACHE_COUNTER_BYTES are zero before the first call; every call leaves them zero, so one workspace serves any number of
+ *   calls, of any sizes it is large enough for, one after another. Calls that may overlap need one each.
+ *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; max_q <= Tq; max_q * heads < 2^31 - 64; ldq, ldo at least a
+ *   row and multiples of 8; the pool's as above; scale > 0 and finite.
+ */
+#define MP_ATTN_CACHE_COUNTER_BYTES 4096
+MP_API size_t mp_attn_cache_workspace_bytes(int heads, int kv_heads, int d, int max_q);
+MP_API mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, const uint8_t* vc, const float* ks, const float* vs,
+                            mp_bf16* O, float* LSE, const int32_t* page_table,
+                            const int32_t* cu_q, const int32_t* lens,
+                            void* workspace, size_t workspace_bytes,
+                            int nseq, int Tq, int max_q, int heads, int kv_heads, int d,
+                            int page, int pages, int max_pages,
+                            long long ldq, long long ldo, long long ld_kc, long long ld_vc,
+                            long long ld_ks, long long ld_vs, int causal, float scale,
+                            uint32_t* d_status, void* stream);
 
 /*
  * mp_vocab_ce for callers that cannot allocate device memory. The paper has no

@@ -27,7 +27,8 @@ of the softmax cross-entropy, pinned by finite differences.
 
 The gated block, the rotation with several axes and the packed attention with its
 gradients are written from the definitions in their modules, and pinned by finite
-differences, closed forms and the ops they reduce to.
+differences, closed forms and the ops they reduce to. So are the norm of queries and
+keys, the 8-bit cache and the attention over it.
 
 Pins (tests marked "not gpu"): GELU values printed in [p5] §2.2, the [p5] §3.1
 worked example and its wrong row cut, closed forms of GELU, finite differences
@@ -52,6 +53,8 @@ from .padding import pad_vocab
 from .embed import embed_sharded
 from .attn import attention_heads, attn_fwd, attn_fwd_sharded, attn_fwd_rows
 from .attn_varlen import attn_varlen_fwd, attn_varlen_bwd
+from .qk_norm import qk_norm_rope, qk_norm_rope_bwd
+from .kv_cache import e4m3_round, page_scale, kv_cache_write, kv_cache_rows, attn_cache_fwd
 from .glu import glu_act, glu_fwd, glu_bwd, glu_sharded_fwd
 from .rope import rope, rope_angles
 
@@ -66,4 +69,6 @@ __all__ = [
     "attn_varlen_fwd", "attn_varlen_bwd",
     "glu_act", "glu_fwd", "glu_bwd", "glu_sharded_fwd",
     "rope", "rope_angles",
+    "qk_norm_rope", "qk_norm_rope_bwd",
+    "e4m3_round", "page_scale", "kv_cache_write", "kv_cache_rows", "attn_cache_fwd",
 ]

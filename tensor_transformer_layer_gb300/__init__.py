@@ -17,6 +17,14 @@ Shapes (row-major, contiguous):
   mp_attn_varlen_fwd(Q[Tq,heads,d], K[Tk,kv,d], V[Tk,kv,d], O[Tq,heads,d], LSE[heads,Tq] fp32, cu_q, cu_k int32)
   mp_attn_varlen_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, delta_ws[heads,Tq] fp32, cu_q, cu_k)
       (these three take rows of any pitch, e.g. parts of a packed projection)
+  mp_qk_norm_rope(x[T,heads,d], y[T,heads,d], wq[d], wk[d], pos[axes,T] int32, q_heads, sections)
+  mp_qk_norm_rope_bwd(x, dy, dx, wq, wk, dwq[d] fp32, dwk[d] fp32, pos, workspace, q_heads, sections)
+  mp_kv_cache_write(K[T,kv,d], V[T,kv,d], kc[pages,kv,page,d] e4m3, vc, ks[pages,kv] fp32, vs,
+                    page_table[nseq,max_pages] int32, cu[nseq+1] int32, start[nseq] int32, max_n)
+  mp_kv_cache_read(kc, vc, ks, vs, K, V, page_table, cu, start, max_n)
+  mp_attn_cache_fwd(Q[Tq,heads,d], kc, vc, ks, vs, O[Tq,heads,d], LSE[heads,Tq] fp32, page_table, cu_q[nseq+1],
+                    lens[nseq] int32, workspace, max_q, causal)
+      (the pools may be views of one pool, e.g. pool[:, 0] and pool[:, 1])
   mp_glu_fwd(X[T,h], W[h,2f], Wd[f,h], Z[T,h], Y[T,f], GU_save[T,2f] | None, t, act)
   mp_glu_bwd(X, W, Wd, GU, Y, dZ[T,h], dX[T,h], dW[h,2f], dWd[f,h], dGU_ws[T,2f], t, act)
 """
@@ -35,10 +43,11 @@ MP_OK = 0
 MP_DEV_TIMEOUT = 0x1
 MP_DEV_TARGET_RANGE = 0x2
 MP_DEV_SEQ_RANGE = 0x4
+MP_DEV_PAGE_RANGE = 0x8
 STATUS_NAMES = {
     0: "MP_OK", 1: "MP_ERR_INVALID_ARG", 2: "MP_ERR_UNSUPPORTED_SHAPE", 3: "MP_ERR_MISALIGNED",
     4: "MP_ERR_NO_DEVICE", 5: "MP_ERR_CUDA", 6: "MP_ERR_TIMEOUT", 7: "MP_ERR_TARGET_RANGE",
-    8: "MP_ERR_WORKSPACE", 9: "MP_ERR_SEQ_RANGE",
+    8: "MP_ERR_WORKSPACE", 9: "MP_ERR_SEQ_RANGE", 10: "MP_ERR_PAGE_RANGE",
 }
 # Every symbol include/mptp.h declares.
 EXPORTS = ("mp_mlp_fwd", "mp_mlp_bwd", "mp_mlp_fwd_shards", "mp_mlp_bwd_shards", "mp_mlp_fused_workspace_bytes",
@@ -47,7 +56,9 @@ EXPORTS = ("mp_mlp_fwd", "mp_mlp_bwd", "mp_mlp_fwd_shards", "mp_mlp_bwd_shards",
            "mp_vocab_ce_noalloc", "mp_vocab_ce_bwd_workspace_bytes", "mp_vocab_ce_bwd_workspace_bytes_one_pass",
            "mp_vocab_ce_bwd", "mp_vocab_ce_lse", "mp_vocab_ce_bwd_lse", "mp_vocab_embed",
            "mp_attn_fwd", "mp_glu_fwd", "mp_glu_bwd", "mp_rope_axes",
-           "mp_attn_varlen_fwd", "mp_attn_varlen_bwd")
+           "mp_attn_varlen_fwd", "mp_attn_varlen_bwd", "mp_qk_norm_rope", "mp_qk_norm_rope_bwd_workspace_bytes",
+           "mp_qk_norm_rope_bwd", "mp_kv_cache_write", "mp_kv_cache_read", "mp_attn_cache_workspace_bytes",
+           "mp_attn_cache_fwd")
 
 
 class MptpError(RuntimeError):
@@ -115,6 +126,21 @@ def lib() -> ctypes.CDLL:
         L.mp_attn_varlen_fwd.restype = _I
         L.mp_attn_varlen_bwd.argtypes = [_P] * 12 + [_I] * 8 + [_L] * 8 + [_I, _F, _P, _P]
         L.mp_attn_varlen_bwd.restype = _I
+        L.mp_qk_norm_rope.argtypes = [_P] * 5 + [_I] * 4 + [_L] * 2 + [_I, _P, ctypes.c_double, _F, ctypes.c_uint32, _P]
+        L.mp_qk_norm_rope.restype = _I
+        L.mp_qk_norm_rope_bwd_workspace_bytes.argtypes = [_I] * 3
+        L.mp_qk_norm_rope_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.mp_qk_norm_rope_bwd.argtypes = ([_P] * 9 + [ctypes.c_size_t] + [_I] * 4 + [_L] * 3 +
+                                          [_I, _P, ctypes.c_double, _F, ctypes.c_uint32, _P])
+        L.mp_qk_norm_rope_bwd.restype = _I
+        L.mp_kv_cache_write.argtypes = [_P] * 9 + [_I] * 8 + [_L] * 6 + [_P, _P]
+        L.mp_kv_cache_write.restype = _I
+        L.mp_kv_cache_read.argtypes = [_P] * 9 + [_I] * 8 + [_L] * 6 + [_P, _P]
+        L.mp_kv_cache_read.restype = _I
+        L.mp_attn_cache_workspace_bytes.argtypes = [_I] * 4
+        L.mp_attn_cache_workspace_bytes.restype = ctypes.c_size_t
+        L.mp_attn_cache_fwd.argtypes = [_P] * 11 + [ctypes.c_size_t] + [_I] * 9 + [_L] * 6 + [_I, _F, _P, _P]
+        L.mp_attn_cache_fwd.restype = _I
         L.mp_vocab_embed.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P]
         L.mp_vocab_embed.restype = _I
         L.mp_vocab_ce_noalloc.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]
@@ -279,6 +305,12 @@ def _ws(workspace):
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous torch.Tensor")
     return workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
+
+
+def _cuda_ws(workspace):
+    if isinstance(workspace, torch.Tensor) and workspace.numel() > 0 and not workspace.is_cuda:
+        raise ValueError("workspace must be a CUDA tensor")
+    return _ws(workspace)
 
 
 def mp_vocab_ce(X, E, target, loss, workspace, *, v_valid: int, t: int, d_status=None, stream=None) -> None:
@@ -549,6 +581,161 @@ def mp_attn_varlen_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, delta_ws, cu_q, cu_k, *,
         Tq, Tk, max_q, max_k, heads, kv, d, ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv, 1 if causal else 0,
         d ** -0.5 if scale is None else float(scale), _status_ptr(d_status), _stream(stream))
     _check("mp_attn_varlen_bwd", code)
+
+
+def _weight(w, name, d, needed):
+    return _ptr(w, name, shape=(d,), allow_none=not needed)
+
+
+def _norm_heads(x, q_heads):
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a [tokens, heads, d] tensor")
+    return tuple(x.shape), _i32(q_heads, "q_heads")
+
+
+def mp_qk_norm_rope(x, y, wq, wk, pos, *, q_heads: int, sections, base: float = 10000.0, eps: float = 1e-6,
+                    interleaved: bool = False, per_axis: bool = False, stream=None) -> None:
+    """Norm of each query and key head with the rotation of mp_rope_axes in one pass: y = R(w x / sqrt(mean(x^2) + eps)),
+    w = wq for the first q_heads heads, wk for the others. x, y [T, heads, d] (rows may be strided; y may be x), wq, wk [d],
+    pos [axes, T] int32."""
+    size, nq = _norm_heads(x, q_heads)
+    T, heads, d = size
+    (px, ldx), (py, ldy) = _heads_view(x, "x", size), _heads_view(y, "y", size)
+    axes, sec = _int_array(tuple(sections))
+    flags = (1 if interleaved else 0) | (2 if per_axis else 0)
+    code = lib().mp_qk_norm_rope(px, py, _weight(wq, "wq", d, nq > 0), _weight(wk, "wk", d, nq < heads),
+                                 _ptr(pos, "pos", torch.int32, (axes, T)), T, heads, nq, d, ldx, ldy, axes, sec,
+                                 float(base), float(eps), flags, _stream(stream))
+    _check("mp_qk_norm_rope", code)
+
+
+def mp_qk_norm_rope_bwd_workspace_bytes(T: int, heads: int, d: int) -> int:
+    return int(lib().mp_qk_norm_rope_bwd_workspace_bytes(_i32(T, "T"), _i32(heads, "heads"), _i32(d, "d")))
+
+
+def mp_qk_norm_rope_bwd(x, dy, dx, wq, wk, dwq, dwk, pos, workspace, *, q_heads: int, sections, base: float = 10000.0,
+                        eps: float = 1e-6, interleaved: bool = False, per_axis: bool = False, stream=None) -> None:
+    """Backward of mp_qk_norm_rope from its x: dx [T, heads, d] (rows may be strided; may be dy or x), dwq, dwk [d] fp32;
+    workspace: mp_qk_norm_rope_bwd_workspace_bytes(T, heads, d) bytes."""
+    size, nq = _norm_heads(x, q_heads)
+    T, heads, d = size
+    (px, ldx), (pg, ldg), (pd, ldd) = (_heads_view(x, "x", size), _heads_view(dy, "dy", size),
+                                       _heads_view(dx, "dx", size))
+    axes, sec = _int_array(tuple(sections))
+    flags = (1 if interleaved else 0) | (2 if per_axis else 0)
+    wp, wb = _cuda_ws(workspace)
+    code = lib().mp_qk_norm_rope_bwd(
+        px, pg, pd, _weight(wq, "wq", d, nq > 0), _weight(wk, "wk", d, nq < heads),
+        _ptr(dwq, "dwq", torch.float32, (d,), nq == 0), _ptr(dwk, "dwk", torch.float32, (d,), nq == heads),
+        _ptr(pos, "pos", torch.int32, (axes, T)), wp, wb, T, heads, nq, d, ldx, ldg, ldd, axes, sec, float(base),
+        float(eps), flags, _stream(stream))
+    _check("mp_qk_norm_rope_bwd", code)
+
+
+def _page_views(x, y, names, dtype, size):
+    """Pointers and page pitches of two tensors [pages, ...] of this size whose pages are contiguous."""
+    inner = 1
+    for n in size[1:]:
+        inner *= n
+    out = []
+    for t, name in ((x, names[0]), (y, names[1])):
+        # What a right call passes, in as few steps as it takes; everything else is told apart below.
+        if type(t) is torch.Tensor and t.dtype is dtype and t.shape == size and t.is_cuda and size[0] > 1 and \
+                t[0].is_contiguous():
+            out.append((t.data_ptr(), t.stride(0)))
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != size:
+            raise ValueError(f"{name} must have shape {tuple(size)}, got {tuple(t.shape)}")
+        if size[0] > 0 and not t[0].is_contiguous():
+            raise ValueError(f"{name}: what a page holds must be contiguous")
+        if t.numel() > 0 and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        out.append((t.data_ptr() or None, t.stride(0) if size[0] > 1 else inner))
+    return out
+
+
+def _pool(kc, vc, ks, vs, page_table, nseq):
+    """Pointers and pitches of a cache's pool, its table's pointer and its sizes: codes [pages, kv_heads, page, d] e4m3,
+    scales [pages, kv_heads] fp32, page_table [nseq, max_pages] int32."""
+    if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
+        raise ValueError("kc must be a [pages, kv_heads, page, d] tensor")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != nseq:
+        raise ValueError(f"page_table must be a [{nseq}, max_pages] tensor")
+    pages, kv, page, d = size = kc.shape
+    out = _page_views(ks, vs, ("ks", "vs"), torch.float32, size[:2])
+    out = _page_views(kc, vc, ("kc", "vc"), torch.float8_e4m3fn, size) + out
+    return out, _ptr(page_table, "page_table", torch.int32), pages, page_table.shape[1], page, kv, d
+
+
+def _sequences(cu, name):
+    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError(f"{name} must be a tensor with at least one entry")
+    nseq = cu.shape[0] - 1
+    return nseq, _ptr(cu, name, torch.int32, (nseq + 1,))
+
+
+def _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, start, max_n):
+    nseq, pcu = _sequences(cu, "cu")
+    pool, pt, pages, max_pages, page, kv, d = _pool(kc, vc, ks, vs, page_table, nseq)
+    if not isinstance(K, torch.Tensor) or K.dim() != 3:
+        raise ValueError("K must be a [tokens, kv_heads, d] tensor")
+    size = (K.shape[0], kv, d)
+    (pk, ldk), (pv, ldv) = _heads_view(K, "K", size), _heads_view(V, "V", size)
+    sizes = (nseq, size[0], _i32(max_n, "max_n"), kv, d, page, pages, max_pages, ldk, ldv, *(x[1] for x in pool))
+    return pk, pv, [x[0] for x in pool], pt, pcu, start, nseq, sizes
+
+
+def mp_kv_cache_write(K, V, kc, vc, ks, vs, page_table, cu, start, *, max_n: int, d_status=None, stream=None) -> None:
+    """New keys and values into an e4m3 cache: rows cu[i] .. cu[i+1]-1 of K, V [T, kv_heads, d] (rows may be strided)
+    become positions start[i] ... of sequence i, in page page_table[i, position // page]. kc, vc [pages, kv_heads, page, d],
+    ks, vs [pages, kv_heads] (pages may be strided). max_n: at least the longest sequence's rows."""
+    pk, pv, pool, pt, pcu, start, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, start, max_n)
+    code = lib().mp_kv_cache_write(pk, pv, *pool, pt, pcu, _ptr(start, "start", torch.int32, (nseq,)), *sizes,
+                                   _status_ptr(d_status), _stream(stream))
+    _check("mp_kv_cache_write", code)
+
+
+def mp_kv_cache_read(kc, vc, ks, vs, K, V, page_table, cu, start=None, *, max_n: int, d_status=None,
+                     stream=None) -> None:
+    """Cached rows back to bf16: the arguments of mp_kv_cache_write, K and V written. start None: from position 0."""
+    pk, pv, pool, pt, pcu, start, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, start, max_n)
+    code = lib().mp_kv_cache_read(*pool, pk, pv, pt, pcu, _ptr(start, "start", torch.int32, (nseq,), True), *sizes,
+                                  _status_ptr(d_status), _stream(stream))
+    _check("mp_kv_cache_read", code)
+
+
+def mp_attn_cache_workspace_bytes(heads: int, kv_heads: int, d: int, max_q: int) -> int:
+    return int(lib().mp_attn_cache_workspace_bytes(_i32(heads, "heads"), _i32(kv_heads, "kv_heads"), _i32(d, "d"),
+                                                   _i32(max_q, "max_q")))
+
+
+def mp_attn_cache_workspace(heads: int, kv_heads: int, d: int, max_q: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for mp_attn_cache_fwd (every call leaves its counters zero)."""
+    return torch.zeros(mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q), dtype=torch.uint8, device=device)
+
+
+def mp_attn_cache_fwd(Q, kc, vc, ks, vs, O, LSE, page_table, cu_q, lens, workspace, *, max_q: int, causal: bool = True,
+                      scale: float | None = None, d_status=None, stream=None) -> None:
+    """Attention of the last tokens of each sequence over its e4m3 cache (mp_kv_cache_write): O [Tq, heads, d] and LSE
+    [heads, Tq] fp32 from Q [Tq, heads, d] (rows may be strided). cu_q [nseq + 1]: sequence i's queries; lens [nseq]: its
+    cached tokens, the queries' own among them. causal: the last query sees the last token. scale: 1 / sqrt(d) by default."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
+        raise ValueError("Q must be a [tokens, heads, d] tensor")
+    nseq, pcu = _sequences(cu_q, "cu_q")
+    pool, pt, pages, max_pages, page, kv, d = _pool(kc, vc, ks, vs, page_table, nseq)
+    size = (Q.shape[0], Q.shape[1], d)
+    (pq, ldq), (po, ldo) = _heads_view(Q, "Q", size), _heads_view(O, "O", size)
+    wp, wb = _cuda_ws(workspace)
+    code = lib().mp_attn_cache_fwd(
+        pq, *(x[0] for x in pool), po, _ptr(LSE, "LSE", torch.float32, (size[1], size[0])), pt, pcu,
+        _ptr(lens, "lens", torch.int32, (nseq,)), wp, wb, nseq, size[0], _i32(max_q, "max_q"), size[1], kv, d, page, pages,
+        max_pages, ldq, ldo, *(x[1] for x in pool), 1 if causal else 0, d ** -0.5 if scale is None else float(scale),
+        _status_ptr(d_status), _stream(stream))
+    _check("mp_attn_cache_fwd", code)
 
 
 def mp_status_from_device(bits: int) -> int:

@@ -1,0 +1,707 @@
+// Entry point of the attention over the 8-bit cache: mp_attn_cache_fwd.
+//
+// The last nq tokens of a sequence attend to its cached keys and values as they are held, e4m3 codes with a scale for each
+// page and head. A key head's rows are the nq * group queries that read it (group = heads / kv_heads):
+//   S = scale * scale_k * (q . code_k),  P = exp(S - max),  O = sum P * scale_v * code_v / sum P
+//
+// Bound by memory: every cached byte is read once and meets `rows` queries, 2 * rows flops a byte. So a warp reads 32 tokens'
+// codes into its own ring in shared memory (cp.async, 16 bytes a lane, two tiles ahead), turns them into halves in
+// registers (exact) and feeds mma.sync m16n8k16 with the cache as the 16-row operand and the queries as the 8-column one:
+//   S^T [keys x queries] = K Q^T: a lane's 16 bytes of a key row are its elements of four products (the summed index
+//     may be taken in any order, the same for Q);
+//   O^T [d x queries] += V^T P^T: bytes of two key rows are interleaved into pairs of keys, P^T comes from S^T by
+//     transposing 8x8 blocks (movmatrix).
+// With the queries as columns, eight rows fill a product that sixteen would share otherwise, and a column's statistics
+// and its sums in O^T lie in the same lane. The tensor cores' 5th-generation products (tcgen05) would need the halves in shared
+// or tensor memory, one more trip for every cached byte, for 128 rows of which a decoded token has eight.
+//
+// Numbers. Q is scaled per row by a power of two into [1, 2) at its largest, then rounded to halves: exact, but for
+// elements below 2^-14 of the largest, which keep 2^-25 of it. P = 2^(s - m + 7), s within m + 8 of the reference m, is
+// rounded to halves (2^-11 of its value, at least 2^-25 absolutely, 2^-32 of a probability of m) times the value's scale over the
+// largest value scale met so far. Statistics and sums are fp32.
+//
+// Work. Tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, split evenly among the CTAs;
+// within its run of an item a CTA's warps take tiles in turn and are joined in shared memory. An item that several
+// CTAs share leaves its parts in the workspace, and the CTA that comes last (a counter) adds them in order.
+#include "mptp_kv_cache.cuh"
+#include "mptp_launch.cuh"
+
+namespace mptp {
+
+constexpr int AC_WARPS = 8;
+constexpr int AC_THREADS = AC_WARPS * 32;
+constexpr int AC_TILE = 32;     // keys
+constexpr int AC_STAGES = 3;
+constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
+#define AC_NONE __int_as_float(0xff800000)  // -inf: no key seen
+constexpr float AC_BIAS = 7.0f;    // exponent that P carries into halves
+constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference before sums are scaled down
+constexpr float AC_LOG2E = 1.4426950408889634f;
+constexpr float AC_LN2 = 0.6931471805599453f;
+
+struct AcArgs {
+    const __nv_bfloat16* Q;
+    __nv_bfloat16* O;
+    float* LSE;
+    const int32_t* cu_q;
+    const int32_t* lens;
+    uint32_t* counters;  // [AC_CTAS], zero between calls
+    float* parts;        // [2 AC_CTAS][rows][d + 2]
+    long long ldq, ldo;
+    int nseq, Tq, max_q, heads, group, causal;
+    float scale_log2;
+    uint32_t* status;
+};
+
+// Shared-memory place of 16-byte chunk c of row r (of 32). The swizzles keep both reads free of bank conflicts: of K, a
+// quarter warp takes four chunks of two neighbouring rows; of V, two chunks of rows two apart.
+template <int D>
+__device__ __forceinline__ int ac_place(int r, int c) {
+    if constexpr (D == 128) return r * 128 + ((c ^ (r & 6) ^ ((r & 1) << 2)) << 4);
+    if constexpr (D == 64) return (r ^ ((r >> 1) & 1)) * 64 + ((c ^ ((r >> 1) & 2)) << 4);
+    return r * D + (c << 4);
+}
+
+__device__ __forceinline__ void ac_copy16(uint32_t dst, const void* src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ac_copy4(uint32_t dst, const void* src, bool take) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void ac_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ac_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ac_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t ac_transpose(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t ac_half2(float lo, float hi) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float ac_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D, int NT>
+struct AcShape {
+    static constexpr int ROWS = 8 * NT;              // queries of a row tile
+    static constexpr int STAGE = 2 * AC_TILE * D;    // bytes of K and V
+    static constexpr int RING = AC_STAGES * STAGE;   // a warp's
+    static constexpr int SCALES = AC_STAGES * 16;    // a warp's: two of K, two of V
+    static constexpr int JOIN = AC_WARPS * ROWS * D * 4;
+    static constexpr int BODY = AC_WARPS * RING > JOIN ? AC_WARPS * RING : JOIN;
+    static constexpr int SMEM = BODY + AC_WARPS * SCALES + AC_WARPS * ROWS * 8 + 64;
+    static constexpr int PART = ROWS * (D + 2);      // floats of a part
+};
+
+// One sequence's place in the line of tiles.
+struct AcSeq {
+    int q0, nq, len, tiles, items;  // tiles of one item; items = row tiles * key heads
+};
+template <int ROWS>
+__device__ __forceinline__ AcSeq ac_seq(const AcArgs& a, const KvPool& p, int seq) {
+    AcSeq s;
+    s.q0 = a.cu_q[seq];
+    const int q1 = a.cu_q[seq + 1];
+    s.len = a.lens[seq];
+    s.nq = q1 - s.q0;
+    if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || s.nq > a.max_q || s.len < 0 ||
+        static_cast<long long>(s.len) > static_cast<long long>(p.max_pages) * p.page) {
+        if (a.status != nullptr) atomicOr(a.status, KV_SEQ_RANGE);
+        s.nq = s.len = 0;
+    }
+    s.tiles = max(1, (s.len + AC_TILE - 1) / AC_TILE);
+    s.items = (s.nq * a.group + ROWS - 1) / ROWS * p.kv_heads;
+    return s;
+}
+
+// Float2 index within a row of the join buffer: eight lanes that write the same j land in different banks.
+__device__ __forceinline__ int ac_join(int i, int row) { return i ^ (((i >> 4) & 1) | ((row & 6))); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs a, const KvPool p) {
+    using C = AcShape<D, NT>;
+    constexpr int KS = D / 16;   // products along d of one score tile; also tiles of 16 rows of O^T
+    constexpr int CH = D / 16;   // 16-byte chunks a key row
+    extern __shared__ __align__(128) uint8_t smem[];
+    float* stat = reinterpret_cast<float*>(smem + C::BODY + AC_WARPS * C::SCALES);  // [warp][row]{m, l}
+    __shared__ long long sh_total[AC_WARPS];
+    __shared__ long long sh_start;
+    __shared__ int sh_seq, sh_last;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // The line of tiles: its length, then this CTA's share [pos, end) and the sequence that holds its first tile.
+    long long total = 0;
+    for (int base = 0; base < a.nseq; base += AC_THREADS) {
+        long long w = 0;
+        if (base + tid < a.nseq) {
+            const AcSeq s = ac_seq<C::ROWS>(a, p, base + tid);
+            w = static_cast<long long>(s.items) * s.tiles;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+        total += w;
+    }
+    if (lane == 0) sh_total[warp] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int k = 0; k < AC_WARPS; ++k) total += sh_total[k];
+    __syncthreads();
+    // As many CTAs as have a tile for each of their warps.
+    const long long want = (total + AC_WARPS - 1) / AC_WARPS;
+    const int ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : static_cast<long long>(gridDim.x));
+    const int cta = blockIdx.x;
+    if (cta >= ctas) return;
+    long long pos = total * cta / ctas;
+    const long long end = total * (cta + 1) / ctas;
+    const long long first_pos = pos;
+    long long before = 0;
+    for (int base = 0; base < a.nseq; base += AC_THREADS) {
+        long long w = 0;
+        if (base + tid < a.nseq) {
+            const AcSeq s = ac_seq<C::ROWS>(a, p, base + tid);
+            w = static_cast<long long>(s.items) * s.tiles;
+        }
+        long long upto = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += v;
+        }
+        if (lane == 31) sh_total[warp] = upto;
+        __syncthreads();
+        long long all = 0;
+#pragma unroll
+        for (int k = 0; k < AC_WARPS; ++k) {
+            if (k < warp) upto += sh_total[k];
+            all += sh_total[k];
+        }
+        if (before + upto > pos && before + upto - w <= pos && w > 0) {
+            sh_seq = base + tid;
+            sh_start = before + upto - w;
+        }
+        __syncthreads();
+        before += all;
+        if (before > pos) break;
+    }
+    int seq = sh_seq;
+    long long seq_start = sh_start;
+    AcSeq s = ac_seq<C::ROWS>(a, p, seq);
+
+    uint8_t* ring = smem + warp * C::RING;
+    const uint32_t ring_u = smem_u32(ring);
+    float* ring_scales = reinterpret_cast<float*>(smem + C::BODY + warp * C::SCALES);
+    const uint32_t ring_scales_u = smem_u32(ring_scales);
+
+    while (pos < end) {
+        while (pos >= seq_start + static_cast<long long>(s.items) * s.tiles) {
+            seq_start += static_cast<long long>(s.items) * s.tiles;
+            s = ac_seq<C::ROWS>(a, p, ++seq);
+        }
+        const int local = static_cast<int>((pos - seq_start) / s.tiles);
+        const int tile0 = static_cast<int>((pos - seq_start) % s.tiles);
+        const int tile1 = static_cast<int>(min(static_cast<long long>(s.tiles), tile0 + (end - pos)));
+        const int head = local % p.kv_heads;
+        const int row0 = local / p.kv_heads * C::ROWS;
+        const int rows = min(C::ROWS, s.nq * a.group - row0);
+        const int32_t* table = p.table + static_cast<long long>(seq) * p.max_pages;
+
+        // Queries: lane (g, t) has row g of each eight, the elements that its bytes of a key row meet.
+        uint32_t qf[NT][KS][2];
+        float fq[NT][2];   // factor from a product to a score in powers of two, for columns 2t, 2t + 1
+        int limit[NT][2];  // keys that those columns see
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = row0 + n * 8 + g;
+            const int qi = row / a.group, hd = head * a.group + row % a.group;
+            constexpr int NV = D / 32;  // 16-byte vectors of a lane
+            union {
+                uint4 v[NV];
+                uint32_t w[NV * 4];
+            } x;
+            const __nv_bfloat16* src = a.Q + (s.q0 + qi) * a.ldq + hd * D;
+            float m = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                // D = 128: 16 elements of each half; else D / 4 neighbouring ones
+                const int at = D == 128 ? (k >> 1) * 64 + t * 16 + (k & 1) * 8 : t * (D / 4) + k * 8;
+                x.v[k] = make_uint4(0, 0, 0, 0);
+                if (n * 8 + g < rows) x.v[k] = *reinterpret_cast<const uint4*>(src + at);
+            }
+#pragma unroll
+            for (int k = 0; k < NV * 4; ++k)
+                m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x.w[k] << 16)), fabsf(__uint_as_float(x.w[k] & 0xffff0000u))));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const int e = m > 0.0f && m < __int_as_float(0x7f800000)
+                              ? max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -126)
+                              : 0;
+            // 2^-e in two factors: e = 127 has no normal one
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - (e >> 1)) << 23);
+            const float down2 = __uint_as_float(static_cast<uint32_t>(127 - (e - (e >> 1))) << 23);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t w = x.w[2 * k + j];
+                    qf[n][k][j] = ac_half2(__uint_as_float(w << 16) * down * down2,
+                                           __uint_as_float(w & 0xffff0000u) * down * down2);
+                }
+            const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * a.scale_log2;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                fq[n][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
+                const int col = n * 8 + 2 * t + j;
+                limit[n][j] = col < rows && a.causal ? s.len - s.nq + (row0 + col) / a.group + 1 : s.len;
+            }
+        }
+        // Below this tile no column is masked.
+        const int clear = a.causal ? s.len - s.nq + row0 / a.group + 1 : s.len;
+
+        float o[KS][NT][4];
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = AC_NONE;
+            l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KS; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
+        }
+        float ref = 0.0f, inv_ref = 0.0f;  // largest value scale met
+
+        // Copies of tile k into stage k % AC_STAGES. Pages are looked up one tile earlier.
+        const int mine = (tile1 - tile0 - warp + AC_WARPS - 1) / AC_WARPS;  // tiles of this warp
+        int id[2];
+        auto look = [&](int k) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = (tile0 + warp + k * AC_WARPS) * AC_TILE + h * 16;
+                id[h] = -1;
+                if (k < mine && key < s.len) id[h] = __ldg(table + key / p.page);
+            }
+        };
+        auto issue = [&](int k) {
+            if (k < mine) {
+                const int key0 = (tile0 + warp + k * AC_WARPS) * AC_TILE;
+                const int st = k % AC_STAGES;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool inside = id[h] >= 0 && id[h] < p.pages;
+                    const bool bad = key0 + h * 16 < s.len && !inside;
+                    const long long page = inside ? id[h] : 0;
+                    const int slot = (key0 + h * 16) % p.page;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint8_t* src = p.head_codes(kv, page, head) + slot * D;
+                        const uint32_t dst = ring_u + st * C::STAGE + kv * AC_TILE * D;
+#pragma unroll
+                        for (int i = 0; i < CH / 2; ++i) {  // 16 rows, 32 chunks a step
+                            const int c = i * 32 + lane, r = h * 16 + c / CH;
+                            ac_copy16(dst + ac_place<D>(r, c % CH), src + c * 16, inside && key0 + r < s.len);
+                        }
+                    }
+                    if (lane < 2) {
+                        float* to = ring_scales + st * 4 + lane * 2 + h;
+                        if (bad) {
+                            *to = __int_as_float(0x7fffffff);  // NaN: a page that is not in the pool
+                            if (a.status != nullptr) atomicOr(a.status, KV_PAGE_RANGE);
+                        } else {
+                            ac_copy4(ring_scales_u + (st * 4 + lane * 2 + h) * 4,
+                                     p.head_scale(lane, page, head), inside);
+                        }
+                    }
+                }
+            }
+            ac_commit();
+        };
+        look(0);
+#pragma unroll
+        for (int k = 0; k < AC_STAGES - 1; ++k) {
+            issue(k);
+            look(k + 1);
+        }
+        for (int k = 0; k < mine; ++k) {
+            ac_wait<AC_STAGES - 2>();
+            __syncwarp();
+            issue(k + AC_STAGES - 1);
+            look(k + AC_STAGES);
+            const int st = k % AC_STAGES;
+            const uint8_t* kt = ring + st * C::STAGE;
+            const uint8_t* vt = kt + AC_TILE * D;
+            const float* sc = ring_scales + st * 4;
+            const int key0 = (tile0 + warp + k * AC_WARPS) * AC_TILE;
+
+            float z[2][NT][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) z[h][n][0] = z[h][n][1] = z[h][n][2] = z[h][n][3] = 0.0f;
+                uint32_t kw[2][KS];  // words of rows g and g + 8
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = h * 16 + r * 8 + g;
+                    if constexpr (D == 96) {
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(kt + row * D + t * 24 + i * 8);
+                            kw[r][2 * i] = v.x;
+                            kw[r][2 * i + 1] = v.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(kt + ac_place<D>(row, i * 4 + t));
+                            kw[r][4 * i] = v.x;
+                            kw[r][4 * i + 1] = v.y;
+                            kw[r][4 * i + 2] = v.z;
+                            kw[r][4 * i + 3] = v.w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    const uint32_t f[4] = {e4m3x2_to_f16x2(kw[0][i] & 0xffffu), e4m3x2_to_f16x2(kw[1][i] & 0xffffu),
+                                           e4m3x2_to_f16x2(kw[0][i] >> 16), e4m3x2_to_f16x2(kw[1][i] >> 16)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) ac_mma(z[h][n], f, qf[n][i][0], qf[n][i][1]);
+                }
+            }
+
+            // Scores in powers of two; lane (g, t) has keys g, g + 8 of each 16 and queries 2t, 2t + 1 of each 8.
+            const bool masked = key0 + AC_TILE > clear;
+            bool higher = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float k_scale = sc[h];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v = z[h][n][c] * (k_scale * fq[n][c & 1]);
+                        if (masked && key0 + h * 16 + (c >> 1) * 8 + g >= limit[n][c & 1]) v = AC_NONE;
+                        z[h][n][c] = v;
+                        higher |= v > m[n][c & 1] + AC_SLACK;
+                    }
+                }
+            if (__any_sync(0xffffffffu, higher)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float v = fmaxf(fmaxf(z[0][n][j], z[0][n][2 + j]), fmaxf(z[1][n][j], z[1][n][2 + j]));
+                        v = fmaxf(v, m[n][j]);
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                        // Equal references leave the sums alone, both -inf (nothing seen yet) among them.
+                        const float f = v == m[n][j] ? 1.0f : ac_ex2(m[n][j] - v);
+                        m[n][j] = v;
+                        l[n][j] *= f;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            o[i][n][j] *= f;
+                            o[i][n][2 + j] *= f;
+                        }
+                    }
+            }
+            // Values' scales relative to the largest so far.
+            float vr[2];
+            {
+                const float big = fmaxf(sc[2], sc[3]);
+                if (big > ref) {
+                    const float f = ref / big;
+                    ref = big;
+                    inv_ref = 1.0f / big;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[i][n][c] *= f;
+                }
+                vr[0] = sc[2] * inv_ref;
+                vr[1] = sc[3] * inv_ref;
+            }
+            uint32_t pt[2][NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float m0 = m[n][0] == AC_NONE ? 0.0f : m[n][0] - AC_BIAS;
+                const float m1 = m[n][1] == AC_NONE ? 0.0f : m[n][1] - AC_BIAS;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = ac_ex2(z[h][n][0] - m0), p1 = ac_ex2(z[h][n][1] - m1);
+                    const float p2 = ac_ex2(z[h][n][2] - m0), p3 = ac_ex2(z[h][n][3] - m1);
+                    l[n][0] += p0 + p2;
+                    l[n][1] += p1 + p3;
+                    pt[h][n][0] = ac_transpose(ac_half2(p0 * vr[h], p1 * vr[h]));
+                    pt[h][n][1] = ac_transpose(ac_half2(p2 * vr[h], p3 * vr[h]));
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                constexpr int VW = D / 32;  // words of a lane in one key row
+                uint32_t vw[4][VW];         // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = h * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(vt + ac_place<D>(row, g));
+                        vw[r][0] = v.x;
+                        vw[r][1] = v.y;
+                        vw[r][2] = v.z;
+                        vw[r][3] = v.w;
+                    } else if constexpr (D == 64) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(vt + ac_place<D>(row, g >> 1) + (g & 1) * 8);
+                        vw[r][0] = v.x;
+                        vw[r][1] = v.y;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VW; ++i)
+                            vw[r][i] = *reinterpret_cast<const uint32_t*>(vt + row * D + g * 12 + i * 4);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
+                    const uint32_t lo = __byte_perm(vw[0][j / 2], vw[1][j / 2], sel);
+                    const uint32_t hi = __byte_perm(vw[2][j / 2], vw[3][j / 2], sel);
+                    const uint32_t f[4] = {e4m3x2_to_f16x2(lo & 0xffffu), e4m3x2_to_f16x2(lo >> 16),
+                                           e4m3x2_to_f16x2(hi & 0xffffu), e4m3x2_to_f16x2(hi >> 16)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) ac_mma(o[j][n], f, pt[h][n][0], pt[h][n][1]);
+                }
+            }
+        }
+        ac_wait<0>();
+
+        // Join of the warps: statistics, then every warp's sums in units of the common reference.
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
+                if (g == 0) {
+                    float* to = stat + (warp * C::ROWS + n * 8 + 2 * t + j) * 2;
+                    to[0] = m[n][j];
+                    to[1] = l[n][j];
+                }
+            }
+        __syncthreads();  // rings are free, statistics are there
+        float2* join = reinterpret_cast<float2*>(smem);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = n * 8 + 2 * t + j;
+                float top = AC_NONE;
+#pragma unroll
+                for (int w = 0; w < AC_WARPS; ++w) top = fmaxf(top, stat[(w * C::ROWS + row) * 2]);
+                const float f = m[n][j] == top ? ref : ref * ac_ex2(m[n][j] - top);
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+                    join[(warp * C::ROWS + row) * (D / 2) + ac_join(g * (D / 16) + i, row)] =
+                        make_float2(o[i][n][j] * f, o[i][n][2 + j] * f);
+            }
+        __syncthreads();
+        const bool whole = tile0 == 0 && tile1 == s.tiles;
+        const int slot = cta * 2 + (pos == first_pos ? 0 : 1);
+        float* part = a.parts + static_cast<long long>(slot) * C::PART;
+        for (int i = tid; i < rows * (D / 4); i += AC_THREADS) {
+            const int row = i / (D / 4), c = i % (D / 4) * 2;
+            float top = AC_NONE, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < AC_WARPS; ++w) top = fmaxf(top, stat[(w * C::ROWS + row) * 2]);
+            float2 x = make_float2(0.0f, 0.0f), y = x;
+#pragma unroll
+            for (int w = 0; w < AC_WARPS; ++w) {
+                const float mw = stat[(w * C::ROWS + row) * 2], lw = stat[(w * C::ROWS + row) * 2 + 1];
+                sum += mw == top ? lw : lw * ac_ex2(mw - top);
+                const float2* from = join + (w * C::ROWS + row) * (D / 2);
+                const float2 u = from[ac_join(c, row)], v = from[ac_join(c + 1, row)];
+                x.x += u.x;
+                x.y += u.y;
+                y.x += v.x;
+                y.y += v.y;
+            }
+            if (whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const int qi = (row0 + row) / a.group, hd = head * a.group + (row0 + row) % a.group;
+                uint2 out = make_uint2(0, 0);
+                if (sum != 0.0f) {
+                    __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), b1 = __floats2bfloat162_rn(y.x * inv, y.y * inv);
+                    out = make_uint2(*reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1));
+                }
+                *reinterpret_cast<uint2*>(a.O + (s.q0 + qi) * a.ldo + hd * D + c * 2) = out;
+                if (c == 0)
+                    a.LSE[static_cast<long long>(hd) * a.Tq + s.q0 + qi] =
+                        sum == 0.0f ? AC_NONE : (top + log2f(sum) - AC_BIAS) * AC_LN2;
+            } else {
+                *reinterpret_cast<float4*>(part + row * D + c * 2) = make_float4(x.x, x.y, y.x, y.y);
+                if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = make_float2(top, sum);
+            }
+        }
+        if (!whole) {
+            // The item's parts: of the CTAs that hold its first to its last tile.
+            const long long u0 = pos - tile0, u1 = u0 + s.tiles - 1;
+            const int c0 = static_cast<int>(((u0 + 1) * ctas - 1) / total), c1 = static_cast<int>(((u1 + 1) * ctas - 1) / total);
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();
+                // wraps to zero with the last one
+                sh_last = atomicInc(a.counters + c0, static_cast<unsigned>(c1 - c0)) == static_cast<unsigned>(c1 - c0);
+                __threadfence();
+            }
+            __syncthreads();
+            if (sh_last) {
+                const int n_parts = c1 - c0 + 1;
+                const int slot0 = c0 * 2 + (total * c0 / ctas == u0 ? 0 : 1);
+                for (int i = tid; i < rows * (D / 4); i += AC_THREADS) {
+                    const int row = i / (D / 4), c = i % (D / 4) * 4;
+                    float top = AC_NONE, sum = 0.0f;
+                    for (int k = 0; k < n_parts; ++k) {
+                        const float* from = a.parts + static_cast<long long>(k == 0 ? slot0 : (c0 + k) * 2) * C::PART;
+                        top = fmaxf(top, __ldcg(from + C::ROWS * D + row * 2));
+                    }
+                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                    for (int k = 0; k < n_parts; ++k) {
+                        const float* from = a.parts + static_cast<long long>(k == 0 ? slot0 : (c0 + k) * 2) * C::PART;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + C::ROWS * D + row * 2));
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(from + row * D + c));
+                        const float f = ml.x == top ? 1.0f : ac_ex2(ml.x - top);
+                        sum += ml.y * f;
+                        x.x += v.x * f;
+                        x.y += v.y * f;
+                        x.z += v.z * f;
+                        x.w += v.w * f;
+                    }
+                    const float inv = 1.0f / sum;
+                    const int qi = (row0 + row) / a.group, hd = head * a.group + (row0 + row) % a.group;
+                    uint2 out = make_uint2(0, 0);
+                    if (sum != 0.0f) {
+                        __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), b1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+                        out = make_uint2(*reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1));
+                    }
+                    *reinterpret_cast<uint2*>(a.O + (s.q0 + qi) * a.ldo + hd * D + c) = out;
+                    if (c == 0)
+                        a.LSE[static_cast<long long>(hd) * a.Tq + s.q0 + qi] =
+                            sum == 0.0f ? AC_NONE : (top + log2f(sum) - AC_BIAS) * AC_LN2;
+                }
+            }
+        }
+        __syncthreads();  // the join's buffer becomes rings again
+        pos += tile1 - tile0;
+    }
+}
+
+template <int D, int NT>
+static cudaError_t launch_attn_cache(const AcArgs& a, const KvPool& p, cudaStream_t s) {
+    using C = AcShape<D, NT>;
+    auto kernel = attn_cache_kernel<D, NT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(AC_CTAS), dim3(AC_THREADS), C::SMEM, s, a, p);
+}
+
+// Row tiles of eight queries where no sequence has more of a key head, else of sixteen.
+static int ac_rows(int max_q, int group) { return static_cast<long long>(max_q) * group <= 8 ? 8 : 16; }
+
+}  // namespace mptp
+
+using namespace mptp;
+
+extern "C" size_t mp_attn_cache_workspace_bytes(int heads, int kv_heads, int d, int max_q) {
+    if (heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || (d != 64 && d != 96 && d != 128) || max_q <= 0) return 0;
+    const size_t part = static_cast<size_t>(ac_rows(max_q, heads / kv_heads)) * (d + 2) * sizeof(float);
+    return MP_ATTN_CACHE_COUNTER_BYTES + 2 * AC_CTAS * part;
+}
+static_assert(AC_CTAS * sizeof(uint32_t) <= MP_ATTN_CACHE_COUNTER_BYTES, "counters");
+
+extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, const uint8_t* vc, const float* ks,
+                                       const float* vs, mp_bf16* O, float* LSE, const int32_t* page_table,
+                                       const int32_t* cu_q, const int32_t* lens, void* workspace, size_t workspace_bytes,
+                                       int nseq, int Tq, int max_q, int heads, int kv_heads, int d, int page, int pages,
+                                       int max_pages, long long ldq, long long ldo, long long ld_kc, long long ld_vc,
+                                       long long ld_ks, long long ld_vs, int causal, float scale, uint32_t* d_status,
+                                       void* stream) {
+    if (nseq < 0 || Tq < 0 || max_q < 0 || heads <= 0 || kv_heads <= 0 || d <= 0 || pages < 0 || max_pages < 0 ||
+        !(scale > 0.0f) || !(scale <= 3.4028234663852886e38f))
+        return MP_ERR_INVALID_ARG;
+    const long long row = static_cast<long long>(heads) * d;
+    if ((d != 64 && d != 96 && d != 128) || heads % kv_heads != 0 || row > 0x7fffffffLL || max_q > Tq || ldq < row ||
+        ldo < row || ldq % 8 != 0 || ldo % 8 != 0 ||
+        static_cast<long long>(max_q) * heads > 0x7fffffffLL - 64 ||
+        !kv_pool_sizes(pages, max_pages, page, kv_heads, d, ld_kc, ld_vc, ld_ks, ld_vs))
+        return MP_ERR_UNSUPPORTED_SHAPE;
+    if (nseq == 0 || max_q == 0) return MP_OK;
+    if (!Q || !O || !LSE || !cu_q || !lens) return MP_ERR_INVALID_ARG;
+    mp_status st = kv_pool_pointers(kc, vc, ks, vs, page_table);
+    if (st != MP_OK) return st;
+    auto word = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+    if (!aligned16(Q) || !aligned16(O) || !word(LSE) || !word(cu_q) || !word(lens) || !word(d_status))
+        return MP_ERR_MISALIGNED;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q))
+        return MP_ERR_WORKSPACE;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != MP_OK) return st;
+
+    KvPool p{};
+    p.codes[0] = const_cast<uint8_t*>(kc);
+    p.codes[1] = const_cast<uint8_t*>(vc);
+    p.scales[0] = const_cast<float*>(ks);
+    p.scales[1] = const_cast<float*>(vs);
+    p.ld_codes[0] = ld_kc;
+    p.ld_codes[1] = ld_vc;
+    p.ld_scales[0] = ld_ks;
+    p.ld_scales[1] = ld_vs;
+    p.table = page_table;
+    p.pages = pages;
+    p.max_pages = max_pages;
+    p.page = page;
+    p.kv_heads = kv_heads;
+    p.d = d;
+    AcArgs a{};
+    a.Q = reinterpret_cast<const __nv_bfloat16*>(Q);
+    a.O = reinterpret_cast<__nv_bfloat16*>(O);
+    a.LSE = LSE;
+    a.cu_q = cu_q;
+    a.lens = lens;
+    a.counters = static_cast<uint32_t*>(workspace);
+    a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + MP_ATTN_CACHE_COUNTER_BYTES);
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.nseq = nseq;
+    a.Tq = Tq;
+    a.max_q = max_q;
+    a.heads = heads;
+    a.group = heads / kv_heads;
+    a.causal = causal != 0;
+    a.scale_log2 = scale * AC_LOG2E;
+    a.status = d_status;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool few = ac_rows(max_q, a.group) == 8;
+    cudaError_t e;
+    if (d == 64)
+        e = few ? launch_attn_cache<64, 1>(a, p, s) : launch_attn_cache<64, 2>(a, p, s);
+    else if (d == 96)
+        e = few ? launch_attn_cache<96, 1>(a, p, s) : launch_attn_cache<96, 2>(a, p, s);
+    else
+        e = few ? launch_attn_cache<128, 1>(a, p, s) : launch_attn_cache<128, 2>(a, p, s);
+    return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
+}

@@ -281,6 +281,7 @@ extern "C" const char* mp_status_string(mp_status s) {
         case MP_ERR_TIMEOUT: return "MP_ERR_TIMEOUT: a bounded wait inside a kernel ran out";
         case MP_ERR_TARGET_RANGE: return "MP_ERR_TARGET_RANGE: a target id is outside [0, v_valid)";
         case MP_ERR_SEQ_RANGE: return "MP_ERR_SEQ_RANGE: a sequence's rows lie outside the tensors or exceed the given maximum";
+        case MP_ERR_PAGE_RANGE: return "MP_ERR_PAGE_RANGE: a page table names a page outside the pool";
         case MP_ERR_WORKSPACE: return "MP_ERR_WORKSPACE: workspace smaller than required";
     }
     return "MP_ERR_UNKNOWN";
@@ -290,6 +291,7 @@ extern "C" mp_status mp_status_from_device(uint32_t bits) {
     if (bits & MP_DEV_TIMEOUT) return MP_ERR_TIMEOUT;
     if (bits & MP_DEV_TARGET_RANGE) return MP_ERR_TARGET_RANGE;
     if (bits & MP_DEV_SEQ_RANGE) return MP_ERR_SEQ_RANGE;
+    if (bits & MP_DEV_PAGE_RANGE) return MP_ERR_PAGE_RANGE;
     return MP_OK;
 }
 

@@ -1,0 +1,390 @@
+// Entry points of the 8-bit cache of keys and values: mp_kv_cache_write, mp_kv_cache_read.
+//
+// Write. Of a page's new rows and a head: amax, then the scale s, the smallest power of two with amax <= 448 s (448
+// is the largest e4m3 value; not below 2^-100), then codes rn(x / s). A power of two loses nothing: e4m3 is a floating
+// type, so a scale within a factor of two changes no relative error but at the bottom of its range, x / s is exact, and
+// a part-filled page whose new rows need a larger scale keeps its old codes exact too (they are shifted, and rounded
+// again only where they become subnormal). The codes follow from the inputs bit for bit.
+//
+// Read. code * scale, rounded to bf16 (exact for scales that a write left, short of bf16's own subnormals).
+//
+// Both are bound by memory: 2 bytes in and 1 out for each element, or 1 in and 2 out. A group of threads takes the rows of one
+// page, head and kind (keys or values), all of them in registers at once, so that the amax and the codes come from one read.
+#include "mptp_kv_cache.cuh"
+#include "mptp_launch.cuh"
+
+namespace mptp {
+
+constexpr int KV_THREADS = 256;
+
+struct KvRows {
+    const __nv_bfloat16* in[2];  // write: new keys and values
+    __nv_bfloat16* out[2];       // read
+    long long ld[2];
+    const int32_t* cu;     // [nseq + 1]
+    const int32_t* start;  // [nseq] or null: zeros
+    int nseq, T, max_n;
+    int per_seq;  // pages a sequence may touch: page `item` is that of sequence item / per_seq. 0: found by a search
+    int group;    // threads per page, head and kind: 32 to KV_THREADS
+    uint32_t* status;
+};
+
+// The rows of one page that a call touches.
+struct KvPage {
+    int row;      // packed row of the first
+    int id;       // page in the pool
+    int a, b;     // slots [a, b)
+};
+
+// A sequence that breaks the rules is reported and left out.
+__device__ __forceinline__ void kv_span(const KvRows& r, const KvPool& p, int seq, int& row0, int& first, int& n) {
+    row0 = r.cu[seq];
+    const int end = r.cu[seq + 1];
+    first = r.start != nullptr ? r.start[seq] : 0;
+    n = end - row0;
+    if (row0 < 0 || end < row0 || end > r.T || n > r.max_n || first < 0 ||
+        static_cast<long long>(first) + n > static_cast<long long>(p.max_pages) * p.page) {
+        if (r.status != nullptr) atomicOr(r.status, KV_SEQ_RANGE);
+        n = 0;
+    }
+}
+__device__ __forceinline__ int kv_touched(const KvPool& p, int first, int n) {
+    return n > 0 ? (first + n - 1) / p.page - first / p.page + 1 : 0;
+}
+
+// The `item`-th page that the call touches; false where there are no so many. With few pages a sequence (per_seq) the
+// place follows from the number; else each warp searches, a lane a sequence.
+__device__ __forceinline__ bool kv_pick(const KvRows& r, const KvPool& p, int item, KvPage& out) {
+    int seq = -1, row0 = 0, first = 0, n = 0, at = 0;
+    if (r.per_seq > 0) {
+        seq = item / r.per_seq;
+        at = item % r.per_seq;
+        if (seq >= r.nseq) return false;
+        kv_span(r, p, seq, row0, first, n);
+        if (at >= kv_touched(p, first, n)) return false;
+    } else {
+        const int lane = threadIdx.x & 31;
+        for (int base = 0; base < r.nseq; base += 32) {
+            if (base + lane < r.nseq) kv_span(r, p, base + lane, row0, first, n);
+            else n = 0;
+            const int mine = kv_touched(p, first, n);
+            int upto = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += v;
+            }
+            const int all = __shfl_sync(0xffffffffu, upto, 31);
+            if (item >= all) {
+                item -= all;
+                continue;
+            }
+            const int who = __ffs(__ballot_sync(0xffffffffu, item < upto)) - 1;
+            seq = base + who;
+            at = item - __shfl_sync(0xffffffffu, upto - mine, who);
+            row0 = __shfl_sync(0xffffffffu, row0, who);
+            first = __shfl_sync(0xffffffffu, first, who);
+            n = __shfl_sync(0xffffffffu, n, who);
+            break;
+        }
+        if (seq < 0) return false;
+    }
+    const int logical = first / p.page + at;
+    const int begin = logical * p.page;
+    out.a = max(first - begin, 0);
+    out.b = min(first + n - begin, p.page);
+    out.row = row0 + (begin + out.a - first);
+    out.id = p.table[static_cast<long long>(seq) * p.max_pages + logical];
+    if (out.id < 0 || out.id >= p.pages) {
+        if (r.status != nullptr) atomicOr(r.status, KV_PAGE_RANGE);
+        return false;
+    }
+    return true;
+}
+
+// The scale that an amax (a bf16 value, finite) needs, as its exponent: the smallest e with amax <= 448 * 2^e.
+__device__ __forceinline__ int kv_exponent(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // 448 = 1.75 * 2^8
+    return max(e, -100);
+}
+__device__ __forceinline__ float kv_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+__device__ __forceinline__ float kv_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float kv_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Largest finite magnitude of two bf16 values and `m`.
+__device__ __forceinline__ float kv_amax_finite(uint32_t w, float m) {
+    const float a = fabsf(kv_lo(w)), b = fabsf(kv_hi(w));
+    m = a < __int_as_float(0x7f800000) ? fmaxf(m, a) : m;
+    return b < __int_as_float(0x7f800000) ? fmaxf(m, b) : m;
+}
+
+__device__ __forceinline__ uint32_t kv_quant2(uint32_t w, float inv) {
+    float a = kv_lo(w) * inv, b = kv_hi(w) * inv;
+    // e4m3 has no infinity: one becomes NaN, so that whoever reads it sees that it was there
+    if (isinf(a)) a = __int_as_float(0x7fffffff);
+    if (isinf(b)) b = __int_as_float(0x7fffffff);
+    return float2_to_e4m3x2(a, b);
+}
+
+// Four codes times a ratio <= 1, rounded again.
+__device__ __forceinline__ uint32_t kv_requant4(uint32_t c, float ratio) {
+    const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(c & 0xffffu)), b = f16x2_to_float2(e4m3x2_to_f16x2(c >> 16));
+    return float2_to_e4m3x2(a.x * ratio, a.y * ratio) | float2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
+}
+
+// NV: vectors of eight elements that a thread holds.
+template <int NV>
+__global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvRows r, const KvPool p) {
+    __shared__ float red[KV_THREADS / 32];
+    const int per_cta = KV_THREADS / r.group;  // heads (of keys, then of values) that a CTA takes
+    const int parts = (2 * p.kv_heads + per_cta - 1) / per_cta;
+    const int item = blockIdx.x / parts;
+    const int unit = blockIdx.x % parts * per_cta + threadIdx.x / r.group;
+    const int tid = threadIdx.x % r.group;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    KvPage at;
+    if (!kv_pick(r, p, item, at)) return;
+    const bool live = unit < 2 * p.kv_heads;
+    const int kind = live && unit >= p.kv_heads ? 1 : 0;
+    const int head = live ? unit - kind * p.kv_heads : 0;
+    const int wide = p.d / 8;  // vectors a row
+    const int count = live ? (at.b - at.a) * wide : 0;
+    const long long ld = kind ? r.ld[1] : r.ld[0];
+    const __nv_bfloat16* src = (kind ? r.in[1] : r.in[0]) + at.row * ld + head * p.d;
+    uint8_t* page = p.head_codes(kind, at.id, head);
+    float* scale_at = p.head_scale(kind, at.id, head);
+
+    const float before = at.a > 0 && live ? *scale_at : 0.0f;
+    uint4 x[NV];
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = tid + k * r.group;
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (v < count) x[k] = *reinterpret_cast<const uint4*>(src + v / wide * ld + v % wide * 8);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        m = kv_amax_finite(x[k].x, kv_amax_finite(x[k].y, kv_amax_finite(x[k].z, kv_amax_finite(x[k].w, m))));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (r.group > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+        __syncthreads();
+        const int w0 = threadIdx.x / r.group * (r.group / 32);
+        for (int k = 0; k < r.group / 32; ++k) m = fmaxf(m, red[w0 + k]);
+    }
+    int e = kv_exponent(m);
+    float ratio = 1.0f;  // old codes' factor
+    if (at.a > 0) {
+        // The page's scale so far; one that no write can have left (not in (0, 2^120]) makes its old codes NaN.
+        if (before > 0.0f && before <= kv_pow2(120)) {
+            const uint32_t u = __float_as_uint(before);
+            e = max(e, static_cast<int>(u >> 23) - 127 + ((u & 0x7fffffu) != 0 ? 1 : 0));
+            ratio = before * kv_pow2(-e);
+        } else {
+            ratio = __int_as_float(0x7fffffff);
+        }
+    }
+    const float inv = kv_pow2(-e);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = tid + k * r.group;
+        if (v < count) {
+            uint2 c;
+            c.x = kv_quant2(x[k].x, inv) | kv_quant2(x[k].y, inv) << 16;
+            c.y = kv_quant2(x[k].z, inv) | kv_quant2(x[k].w, inv) << 16;
+            *reinterpret_cast<uint2*>(page + at.a * p.d + v * 8) = c;
+        }
+    }
+    if (live && at.a > 0 && ratio != 1.0f) {
+        uint2* old = reinterpret_cast<uint2*>(page);
+        for (int v = tid; v < at.a * wide; v += r.group) {
+            uint2 c = old[v];
+            c.x = kv_requant4(c.x, ratio);
+            c.y = kv_requant4(c.y, ratio);
+            old[v] = c;
+        }
+    }
+    if (live && tid == 0) *scale_at = kv_pow2(e);
+}
+
+__global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvRows r, const KvPool p) {
+    const int per_cta = KV_THREADS / r.group;
+    const int parts = (2 * p.kv_heads + per_cta - 1) / per_cta;
+    const int item = blockIdx.x / parts;
+    const int unit = blockIdx.x % parts * per_cta + threadIdx.x / r.group;
+    const int tid = threadIdx.x % r.group;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    KvPage at;
+    if (!kv_pick(r, p, item, at)) return;
+    if (unit >= 2 * p.kv_heads) return;
+    const int kind = unit >= p.kv_heads ? 1 : 0;
+    const int head = unit - kind * p.kv_heads;
+    const int wide = p.d / 16;
+    const int count = (at.b - at.a) * wide;
+    const long long ld = kind ? r.ld[1] : r.ld[0];
+    __nv_bfloat16* dst = (kind ? r.out[1] : r.out[0]) + at.row * ld + head * p.d;
+    const uint4* src = reinterpret_cast<const uint4*>(p.head_codes(kind, at.id, head) + at.a * p.d);
+    const float scale = *p.head_scale(kind, at.id, head);
+    for (int v0 = tid; v0 < count; v0 += 4 * r.group) {
+        uint4 c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (v0 + k * r.group < count) c[k] = src[v0 + k * r.group];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int v = v0 + k * r.group;
+            if (v >= count) continue;
+            const uint32_t in[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(in[j / 2] >> (j % 2 * 16)));
+                __nv_bfloat162 b = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+                o[j] = *reinterpret_cast<uint32_t*>(&b);
+            }
+            uint4* to = reinterpret_cast<uint4*>(dst + v / wide * ld + v % wide * 16);
+            to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
+}
+
+// Checks that the write and the read share, then the rows' part of the launch: the pages that the call may touch.
+static mp_status kv_rows_check(const void* K, const void* V, const void* kc, const void* vc, const void* ks, const void* vs,
+                               const void* table, const void* cu, const void* start, bool start_needed, int nseq, int T,
+                               int max_n, int kv_heads, int d, int page, int pages, int max_pages, long long ldk,
+                               long long ldv, long long ld_kc, long long ld_vc, long long ld_ks, long long ld_vs,
+                               const void* d_status, bool* nothing) {
+    if (nseq < 0 || T < 0 || max_n < 0 || kv_heads <= 0 || d <= 0 || pages < 0 || max_pages < 0)
+        return MP_ERR_INVALID_ARG;
+    if (d % 16 != 0 || d > 256 || max_n > T || ldk < static_cast<long long>(kv_heads) * d ||
+        ldv < static_cast<long long>(kv_heads) * d || ldk % 8 != 0 || ldv % 8 != 0 ||
+        !kv_pool_sizes(pages, max_pages, page, kv_heads, d, ld_kc, ld_vc, ld_ks, ld_vs))
+        return MP_ERR_UNSUPPORTED_SHAPE;
+    *nothing = nseq == 0 || max_n == 0;
+    if (*nothing) return MP_OK;
+    const mp_status st = kv_pool_pointers(kc, vc, ks, vs, table);
+    if (!K || !V || !cu || (start_needed && !start)) return MP_ERR_INVALID_ARG;
+    if (st != MP_OK) return st;
+    auto word = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+    return aligned16(K) && aligned16(V) && word(cu) && word(start) && word(d_status) ? MP_OK : MP_ERR_MISALIGNED;
+}
+
+// Pages in the launch (-1: more than a grid holds), and how a CTA finds its own.
+static long long kv_plan(KvRows& r, const KvPool& p) {
+    // A sequence's n rows touch at most this many pages, all sequences' at most `bound`.
+    const long long per_seq = (static_cast<long long>(r.max_n) + p.page - 2) / p.page + 1;
+    const long long bound = r.T / p.page + 2LL * r.nseq;
+    const long long direct = per_seq * r.nseq;
+    r.per_seq = direct <= 2 * bound ? static_cast<int>(per_seq) : 0;
+    return r.per_seq > 0 ? direct : bound;
+}
+
+static KvPool kv_pool(uint8_t* kc, uint8_t* vc, float* ks, float* vs, const int32_t* table, int pages, int max_pages,
+                      int page, int kv_heads, int d, long long ld_kc, long long ld_vc, long long ld_ks, long long ld_vs) {
+    KvPool p{};
+    p.codes[0] = kc;
+    p.codes[1] = vc;
+    p.scales[0] = ks;
+    p.scales[1] = vs;
+    p.ld_codes[0] = ld_kc;
+    p.ld_codes[1] = ld_vc;
+    p.ld_scales[0] = ld_ks;
+    p.ld_scales[1] = ld_vs;
+    p.table = table;
+    p.pages = pages;
+    p.max_pages = max_pages;
+    p.page = page;
+    p.kv_heads = kv_heads;
+    p.d = d;
+    return p;
+}
+
+// Threads per page, head and kind: a warp, doubled while a thread would hold more than `most` vectors.
+static int kv_group(long long vectors, int most) {
+    int g = 32;
+    while (g < KV_THREADS && vectors > static_cast<long long>(g) * most) g *= 2;
+    return g;
+}
+
+}  // namespace mptp
+
+using namespace mptp;
+
+extern "C" mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V, uint8_t* kc, uint8_t* vc, float* ks, float* vs,
+                                       const int32_t* page_table, const int32_t* cu, const int32_t* start, int nseq,
+                                       int T, int max_n, int kv_heads, int d, int page, int pages, int max_pages,
+                                       long long ldk, long long ldv, long long ld_kc, long long ld_vc, long long ld_ks,
+                                       long long ld_vs, uint32_t* d_status, void* stream) {
+    bool nothing = false;
+    mp_status st = kv_rows_check(K, V, kc, vc, ks, vs, page_table, cu, start, true, nseq, T, max_n, kv_heads, d, page, pages,
+                                 max_pages, ldk, ldv, ld_kc, ld_vc, ld_ks, ld_vs, d_status, &nothing);
+    if (st != MP_OK || nothing) return st;
+    const KvPool p = kv_pool(kc, vc, ks, vs, page_table, pages, max_pages, page, kv_heads, d, ld_kc, ld_vc, ld_ks, ld_vs);
+    KvRows r{};
+    r.in[0] = reinterpret_cast<const __nv_bfloat16*>(K);
+    r.in[1] = reinterpret_cast<const __nv_bfloat16*>(V);
+    r.ld[0] = ldk;
+    r.ld[1] = ldv;
+    r.cu = cu;
+    r.start = start;
+    r.nseq = nseq;
+    r.T = T;
+    r.max_n = max_n;
+    r.status = d_status;
+    const long long vectors = static_cast<long long>(max_n < page ? max_n : page) * (d / 8);
+    r.group = kv_group(vectors, 8);
+    const int per_cta = KV_THREADS / r.group;
+    const long long grid = kv_plan(r, p) * ((2LL * kv_heads + per_cta - 1) / per_cta);
+    if (grid > 0x7fffffffLL) return MP_ERR_UNSUPPORTED_SHAPE;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != MP_OK) return st;
+    auto kernel = vectors <= 2LL * r.group   ? kv_write_kernel<2>
+                  : vectors <= 8LL * r.group ? kv_write_kernel<8>
+                                             : kv_write_kernel<16>;
+    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(KV_THREADS), 0,
+                                     static_cast<cudaStream_t>(stream), r, p);
+    return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
+}
+
+extern "C" mp_status mp_kv_cache_read(const uint8_t* kc, const uint8_t* vc, const float* ks, const float* vs, mp_bf16* K,
+                                      mp_bf16* V, const int32_t* page_table, const int32_t* cu, const int32_t* start,
+                                      int nseq, int T, int max_n, int kv_heads, int d, int page, int pages, int max_pages,
+                                      long long ldk, long long ldv, long long ld_kc, long long ld_vc, long long ld_ks,
+                                      long long ld_vs, uint32_t* d_status, void* stream) {
+    bool nothing = false;
+    mp_status st = kv_rows_check(K, V, kc, vc, ks, vs, page_table, cu, start, false, nseq, T, max_n, kv_heads, d, page,
+                                 pages, max_pages, ldk, ldv, ld_kc, ld_vc, ld_ks, ld_vs, d_status, &nothing);
+    if (st != MP_OK || nothing) return st;
+    const KvPool p = kv_pool(const_cast<uint8_t*>(kc), const_cast<uint8_t*>(vc), const_cast<float*>(ks),
+                             const_cast<float*>(vs), page_table, pages, max_pages, page, kv_heads, d, ld_kc, ld_vc, ld_ks,
+                             ld_vs);
+    KvRows r{};
+    r.out[0] = reinterpret_cast<__nv_bfloat16*>(K);
+    r.out[1] = reinterpret_cast<__nv_bfloat16*>(V);
+    r.ld[0] = ldk;
+    r.ld[1] = ldv;
+    r.cu = cu;
+    r.start = start;
+    r.nseq = nseq;
+    r.T = T;
+    r.max_n = max_n;
+    r.status = d_status;
+    r.group = kv_group(static_cast<long long>(max_n < page ? max_n : page) * (d / 16), 4);
+    const int per_cta = KV_THREADS / r.group;
+    const long long grid = kv_plan(r, p) * ((2LL * kv_heads + per_cta - 1) / per_cta);
+    if (grid > 0x7fffffffLL) return MP_ERR_UNSUPPORTED_SHAPE;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != MP_OK) return st;
+    const cudaError_t e = launch_pdl(kv_read_kernel, dim3(static_cast<unsigned>(grid)), dim3(KV_THREADS), 0,
+                                     static_cast<cudaStream_t>(stream), r, p);
+    return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
+}
