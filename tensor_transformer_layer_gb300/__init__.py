@@ -632,43 +632,41 @@ def mp_qk_norm_rope_bwd(x, dy, dx, wq, wk, dwq, dwk, pos, workspace, *, q_heads:
     _check("mp_qk_norm_rope_bwd", code)
 
 
-def _page_views(x, y, names, dtype, size):
-    """Pointers and page pitches of two tensors [pages, ...] of this size whose pages are contiguous."""
-    inner = 1
-    for n in size[1:]:
-        inner *= n
-    out = []
-    for t, name in ((x, names[0]), (y, names[1])):
-        # What a right call passes, in as few steps as it takes; everything else is told apart below.
-        if type(t) is torch.Tensor and t.dtype is dtype and t.shape == size and t.is_cuda and size[0] > 1 and \
-                t[0].is_contiguous():
-            out.append((t.data_ptr(), t.stride(0)))
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != size:
-            raise ValueError(f"{name} must have shape {tuple(size)}, got {tuple(t.shape)}")
-        if size[0] > 0 and not t[0].is_contiguous():
-            raise ValueError(f"{name}: what a page holds must be contiguous")
-        if t.numel() > 0 and not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        out.append((t.data_ptr() or None, t.stride(0) if size[0] > 1 else inner))
-    return out
+def _page_view(t, name, dtype, size, inner):
+    """Pointer and page pitch of a tensor [pages, ...] of this size whose pages are contiguous (strides `inner`)."""
+    # What a right call passes, in as few steps as it takes; everything else is told apart below.
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == size and t.is_cuda:
+        pitch, *rest = t.stride()
+        if rest == inner and size[0] > 1:
+            return t.data_ptr(), pitch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != size:
+        raise ValueError(f"{name} must have shape {tuple(size)}, got {tuple(t.shape)}")
+    if size[0] > 0 and not t[0].is_contiguous():
+        raise ValueError(f"{name}: what a page holds must be contiguous")
+    if t.numel() > 0 and not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.data_ptr() or None, t.stride(0) if size[0] > 1 else size[1] * inner[0]
 
 
 def _pool(kc, vc, ks, vs, page_table, nseq):
-    """Pointers and pitches of a cache's pool, its table's pointer and its sizes: codes [pages, kv_heads, page, d] e4m3,
-    scales [pages, kv_heads] fp32, page_table [nseq, max_pages] int32."""
+    """Pointers and pitches of a cache's pool (codes [pages, kv_heads, page, d] e4m3, scales [pages, kv_heads] fp32), the
+    pointer of its table [nseq, max_pages] int32, and (pages, max_pages, page, kv_heads, d)."""
     if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
         raise ValueError("kc must be a [pages, kv_heads, page, d] tensor")
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != nseq:
-        raise ValueError(f"page_table must be a [{nseq}, max_pages] tensor")
-    pages, kv, page, d = size = kc.shape
-    out = _page_views(ks, vs, ("ks", "vs"), torch.float32, size[:2])
-    out = _page_views(kc, vc, ("kc", "vc"), torch.float8_e4m3fn, size) + out
-    return out, _ptr(page_table, "page_table", torch.int32), pages, page_table.shape[1], page, kv, d
+    size = pages, kv, page, d = kc.shape
+    f8, f32, inner, scales = torch.float8_e4m3fn, torch.float32, [page * d, d, 1], (pages, kv)
+    psk, ldsk = _page_view(ks, "ks", f32, scales, [1])
+    psv, ldsv = _page_view(vs, "vs", f32, scales, [1])
+    pk, ldk = _page_view(kc, "kc", f8, size, inner)
+    pv, ldv = _page_view(vc, "vc", f8, size, inner)
+    pt = _ptr(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != nseq:
+        raise ValueError(f"page_table must have shape [{nseq}, max_pages], got {tuple(page_table.shape)}")
+    return (pk, pv, psk, psv), (ldk, ldv, ldsk, ldsv), pt, (pages, page_table.shape[1], page, kv, d)
 
 
 def _sequences(cu, name):
@@ -678,22 +676,23 @@ def _sequences(cu, name):
     return nseq, _ptr(cu, name, torch.int32, (nseq + 1,))
 
 
-def _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, start, max_n):
+def _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, max_n):
     nseq, pcu = _sequences(cu, "cu")
-    pool, pt, pages, max_pages, page, kv, d = _pool(kc, vc, ks, vs, page_table, nseq)
+    pool, pitches, pt, (pages, max_pages, page, kv, d) = _pool(kc, vc, ks, vs, page_table, nseq)
     if not isinstance(K, torch.Tensor) or K.dim() != 3:
         raise ValueError("K must be a [tokens, kv_heads, d] tensor")
-    size = (K.shape[0], kv, d)
-    (pk, ldk), (pv, ldv) = _heads_view(K, "K", size), _heads_view(V, "V", size)
-    sizes = (nseq, size[0], _i32(max_n, "max_n"), kv, d, page, pages, max_pages, ldk, ldv, *(x[1] for x in pool))
-    return pk, pv, [x[0] for x in pool], pt, pcu, start, nseq, sizes
+    T = K.shape[0]
+    size = T, kv, d
+    pk, ldk = _heads_view(K, "K", size)
+    pv, ldv = _heads_view(V, "V", size)
+    return pk, pv, pool, pt, pcu, nseq, (nseq, T, _i32(max_n, "max_n"), kv, d, page, pages, max_pages, ldk, ldv, *pitches)
 
 
 def mp_kv_cache_write(K, V, kc, vc, ks, vs, page_table, cu, start, *, max_n: int, d_status=None, stream=None) -> None:
     """New keys and values into an e4m3 cache: rows cu[i] .. cu[i+1]-1 of K, V [T, kv_heads, d] (rows may be strided)
     become positions start[i] ... of sequence i, in page page_table[i, position // page]. kc, vc [pages, kv_heads, page, d],
     ks, vs [pages, kv_heads] (pages may be strided). max_n: at least the longest sequence's rows."""
-    pk, pv, pool, pt, pcu, start, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, start, max_n)
+    pk, pv, pool, pt, pcu, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, max_n)
     code = lib().mp_kv_cache_write(pk, pv, *pool, pt, pcu, _ptr(start, "start", torch.int32, (nseq,)), *sizes,
                                    _status_ptr(d_status), _stream(stream))
     _check("mp_kv_cache_write", code)
@@ -702,7 +701,7 @@ def mp_kv_cache_write(K, V, kc, vc, ks, vs, page_table, cu, start, *, max_n: int
 def mp_kv_cache_read(kc, vc, ks, vs, K, V, page_table, cu, start=None, *, max_n: int, d_status=None,
                      stream=None) -> None:
     """Cached rows back to bf16: the arguments of mp_kv_cache_write, K and V written. start None: from position 0."""
-    pk, pv, pool, pt, pcu, start, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, start, max_n)
+    pk, pv, pool, pt, pcu, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, max_n)
     code = lib().mp_kv_cache_read(*pool, pk, pv, pt, pcu, _ptr(start, "start", torch.int32, (nseq,), True), *sizes,
                                   _status_ptr(d_status), _stream(stream))
     _check("mp_kv_cache_read", code)
@@ -726,15 +725,16 @@ def mp_attn_cache_fwd(Q, kc, vc, ks, vs, O, LSE, page_table, cu_q, lens, workspa
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
         raise ValueError("Q must be a [tokens, heads, d] tensor")
     nseq, pcu = _sequences(cu_q, "cu_q")
-    pool, pt, pages, max_pages, page, kv, d = _pool(kc, vc, ks, vs, page_table, nseq)
-    size = (Q.shape[0], Q.shape[1], d)
-    (pq, ldq), (po, ldo) = _heads_view(Q, "Q", size), _heads_view(O, "O", size)
+    pool, pitches, pt, (pages, max_pages, page, kv, d) = _pool(kc, vc, ks, vs, page_table, nseq)
+    T, heads, _ = Q.shape
+    size = T, heads, d
+    pq, ldq = _heads_view(Q, "Q", size)
+    po, ldo = _heads_view(O, "O", size)
     wp, wb = _cuda_ws(workspace)
     code = lib().mp_attn_cache_fwd(
-        pq, *(x[0] for x in pool), po, _ptr(LSE, "LSE", torch.float32, (size[1], size[0])), pt, pcu,
-        _ptr(lens, "lens", torch.int32, (nseq,)), wp, wb, nseq, size[0], _i32(max_q, "max_q"), size[1], kv, d, page, pages,
-        max_pages, ldq, ldo, *(x[1] for x in pool), 1 if causal else 0, d ** -0.5 if scale is None else float(scale),
-        _status_ptr(d_status), _stream(stream))
+        pq, *pool, po, _ptr(LSE, "LSE", torch.float32, (heads, T)), pt, pcu, _ptr(lens, "lens", torch.int32, (nseq,)), wp,
+        wb, nseq, T, _i32(max_q, "max_q"), heads, kv, d, page, pages, max_pages, ldq, ldo, *pitches, 1 if causal else 0,
+        d ** -0.5 if scale is None else float(scale), _status_ptr(d_status), _stream(stream))
     _check("mp_attn_cache_fwd", code)
 
 

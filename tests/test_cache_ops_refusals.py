@@ -161,10 +161,10 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         mp.mp_qk_norm_rope_bwd(x, x, x, w, w, f, f, pos, u8, **how)
     with pytest.raises(TypeError):
-        mp._page_views(x[0], x[0], ("ks", "vs"), torch.float32, x[0].shape)
+        mp._page_view(x[0], "ks", torch.float32, x[0].shape, [1])
     codes = torch.zeros(5, 2, 2, 16, 64).to(torch.float8_e4m3fn)
     with pytest.raises(ValueError, match="contiguous"):
-        mp._page_views(codes[..., ::2], codes[..., ::2], ("kc", "vc"), codes.dtype, codes[..., ::2].shape)
+        mp._page_view(codes[..., ::2], "kc", codes.dtype, codes[..., ::2].shape, [512, 256, 32, 1])
     scales = torch.ones(5, 2, 2)
     pool = (codes[:, 0], codes[:, 1], scales[:, 0], scales[:, 1])
     table, cu = torch.zeros(1, 2, dtype=torch.int32), torch.tensor([0, 4], dtype=torch.int32)
