@@ -20,9 +20,11 @@
 // rounded to halves (2^-11 of its value, at least 2^-25 absolutely, 2^-32 of a probability of m) times the value's scale over the
 // largest value scale met so far. Statistics and sums are fp32.
 //
-// Work. Tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, split evenly among the CTAs;
-// within its run of an item a CTA's warps take tiles in turn and are joined in shared memory. An item that several
-// CTAs share leaves its parts in the workspace, and the CTA that comes last (a counter) adds them in order.
+// Work. The tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, AC_ITEM places for what an item
+// costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
+// walks its run alone, without a barrier: an item that lies within it is finished from registers. Runs that begin or
+// end inside an item leave a record in shared memory, joined once at the CTA's end; an item that several CTAs share leaves
+// a part of each in the workspace, and the CTA that comes last (a counter) adds them in order.
 #include "mptp_kv_cache.cuh"
 #include "mptp_launch.cuh"
 
@@ -31,7 +33,7 @@ namespace mptp {
 constexpr int AC_WARPS = 8;
 constexpr int AC_THREADS = AC_WARPS * 32;
 constexpr int AC_TILE = 32;     // keys
-constexpr int AC_STAGES = 3;
+constexpr int AC_ITEM = 4;      // places of an item besides its tiles
 constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
 #define AC_NONE __int_as_float(0xff800000)  // -inf: no key seen
 constexpr float AC_BIAS = 7.0f;    // exponent that P carries into halves
@@ -97,13 +99,24 @@ __device__ __forceinline__ float ac_ex2(float x) {
 template <int D, int NT>
 struct AcShape {
     static constexpr int ROWS = 8 * NT;              // queries of a row tile
+    static constexpr int STAGES = D == 128 && NT == 2 ? 2 : 3;
     static constexpr int STAGE = 2 * AC_TILE * D;    // bytes of K and V
-    static constexpr int RING = AC_STAGES * STAGE;   // a warp's
-    static constexpr int SCALES = AC_STAGES * 16;    // a warp's: two of K, two of V
-    static constexpr int JOIN = AC_WARPS * ROWS * D * 4;
-    static constexpr int BODY = AC_WARPS * RING > JOIN ? AC_WARPS * RING : JOIN;
-    static constexpr int SMEM = BODY + AC_WARPS * SCALES + AC_WARPS * ROWS * 8 + 64;
+    static constexpr int RING = STAGES * STAGE;      // a warp's; then the record of the item that its run ends in
+    static constexpr int HEAD = ROWS * D * 4;        // the record of the item that its run begins in
+    static constexpr int WARP = RING + HEAD;
+    static constexpr int SCALES = STAGES * 16;       // a warp's: two of K, two of V
+    static constexpr int STATS = 2 * ROWS * 8;       // a warp's: (reference, sum) of the records' rows
+    static constexpr int SMEM = AC_WARPS * (WARP + SCALES + STATS);
     static constexpr int PART = ROWS * (D + 2);      // floats of a part
+    static_assert(HEAD <= RING && SMEM <= 226 * 1024, "shared memory");
+    static_assert(AC_CTAS * ROWS * 8 + AC_WARPS * HEAD <= AC_WARPS * WARP, "the parts' statistics beside the warps' sums");
+};
+
+// What a warp leaves of an item that it has not done alone: tiles [tile0, tile1) of `tiles`, first at place u0.
+struct AcRecord {
+    long long u0;  // -1: none
+    int tile0, tile1, tiles;
+    int q0, row0, rows, head;
 };
 
 // One sequence's place in the line of tiles.
@@ -130,54 +143,68 @@ __device__ __forceinline__ AcSeq ac_seq(const AcArgs& a, const KvPool& p, int se
 // Float2 index within a row of the join buffer: eight lanes that write the same j land in different banks.
 __device__ __forceinline__ int ac_join(int i, int row) { return i ^ (((i >> 4) & 1) | ((row & 6))); }
 
+// The output of row `row` of an item, from its sums x in units of the values and sum of probabilities: four elements at d.
+__device__ __forceinline__ void ac_store(const AcArgs& a, int q0, int head, int row, int d, int D, const float4& x, float top,
+                                         float sum) {
+    const int hd = head * a.group + row % a.group;
+    const long long q = q0 + row / a.group;
+    const float inv = 1.0f / sum;
+    uint2 out = make_uint2(0, 0);  // a row that sees no key, whatever its sums hold
+    if (sum != 0.0f) {
+        const __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), b1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+        out = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+    }
+    *reinterpret_cast<uint2*>(a.O + q * a.ldo + hd * D + d) = out;
+    if (d == 0) a.LSE[static_cast<long long>(hd) * a.Tq + q] = sum == 0.0f ? AC_NONE : (top + log2f(sum) - AC_BIAS) * AC_LN2;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs a, const KvPool p) {
     using C = AcShape<D, NT>;
     constexpr int KS = D / 16;   // products along d of one score tile; also tiles of 16 rows of O^T
     constexpr int CH = D / 16;   // 16-byte chunks a key row
     extern __shared__ __align__(128) uint8_t smem[];
-    float* stat = reinterpret_cast<float*>(smem + C::BODY + AC_WARPS * C::SCALES);  // [warp][row]{m, l}
     __shared__ long long sh_total[AC_WARPS];
-    __shared__ long long sh_start;
-    __shared__ int sh_seq, sh_last;
+    __shared__ long long sh_start[AC_WARPS];
+    __shared__ int sh_seq[AC_WARPS];
+    __shared__ AcRecord rec[2 * AC_WARPS];
+    __shared__ int sh_last[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    float* stats = reinterpret_cast<float*>(smem + AC_WARPS * (C::WARP + C::SCALES));  // [warp][2][row]{m, l}
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // The line of tiles: its length, then this CTA's share [pos, end) and the sequence that holds its first tile.
-    long long total = 0;
-    for (int base = 0; base < a.nseq; base += AC_THREADS) {
-        long long w = 0;
-        if (base + tid < a.nseq) {
-            const AcSeq s = ac_seq<C::ROWS>(a, p, base + tid);
-            w = static_cast<long long>(s.items) * s.tiles;
-        }
+    // The line's length, then the CTA's run, its warps' and the sequences that hold their first places.
+    auto places = [&](int seq) {
+        if (seq >= a.nseq) return 0ll;
+        const AcSeq s = ac_seq<C::ROWS>(a, p, seq);
+        return static_cast<long long>(s.items) * (s.tiles + AC_ITEM);
+    };
+    const long long mine0 = places(tid);
+    long long total = mine0;
+    for (int base = AC_THREADS; base < a.nseq; base += AC_THREADS) total += places(base + tid);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
-        total += w;
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    if (lane == 0) {
+        sh_total[warp] = total;
+        rec[2 * warp].u0 = rec[2 * warp + 1].u0 = -1;
     }
-    if (lane == 0) sh_total[warp] = total;
     __syncthreads();
     total = 0;
 #pragma unroll
     for (int k = 0; k < AC_WARPS; ++k) total += sh_total[k];
     __syncthreads();
-    // As many CTAs as have a tile for each of their warps.
-    const long long want = (total + AC_WARPS - 1) / AC_WARPS;
+    // As many CTAs as have a few places for each of their warps.
+    const long long want = (total + 2 * AC_WARPS - 1) / (2 * AC_WARPS);
     const int ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : static_cast<long long>(gridDim.x));
     const int cta = blockIdx.x;
     if (cta >= ctas) return;
-    long long pos = total * cta / ctas;
-    const long long end = total * (cta + 1) / ctas;
-    const long long first_pos = pos;
+    const long long cta_pos = total * cta / ctas, cta_end = total * (cta + 1) / ctas;
+    auto run = [&](int w) { return cta_pos + (cta_end - cta_pos) * w / AC_WARPS; };
     long long before = 0;
-    for (int base = 0; base < a.nseq; base += AC_THREADS) {
-        long long w = 0;
-        if (base + tid < a.nseq) {
-            const AcSeq s = ac_seq<C::ROWS>(a, p, base + tid);
-            w = static_cast<long long>(s.items) * s.tiles;
-        }
-        long long upto = w;
+    for (int base = 0; base < a.nseq && before <= run(AC_WARPS - 1); base += AC_THREADS) {
+        const long long n = base == 0 ? mine0 : places(base + tid);
+        long long upto = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, upto, off);
@@ -191,35 +218,94 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             if (k < warp) upto += sh_total[k];
             all += sh_total[k];
         }
-        if (before + upto > pos && before + upto - w <= pos && w > 0) {
-            sh_seq = base + tid;
-            sh_start = before + upto - w;
-        }
-        __syncthreads();
+        upto += before;
+#pragma unroll
+        for (int w = 0; w < AC_WARPS; ++w)
+            if (run(w) < upto && run(w) >= upto - n) {
+                sh_seq[w] = base + tid;
+                sh_start[w] = upto - n;
+            }
         before += all;
-        if (before > pos) break;
+        __syncthreads();
     }
-    int seq = sh_seq;
-    long long seq_start = sh_start;
+    long long pos = run(warp);
+    const long long end = run(warp + 1);
+    int seq = sh_seq[warp];
+    long long seq_start = sh_start[warp];
     AcSeq s = ac_seq<C::ROWS>(a, p, seq);
 
-    uint8_t* ring = smem + warp * C::RING;
+    uint8_t* ring = smem + warp * C::WARP;
     const uint32_t ring_u = smem_u32(ring);
-    float* ring_scales = reinterpret_cast<float*>(smem + C::BODY + warp * C::SCALES);
+    float* ring_scales = reinterpret_cast<float*>(smem + AC_WARPS * C::WARP + warp * C::SCALES);
     const uint32_t ring_scales_u = smem_u32(ring_scales);
 
     while (pos < end) {
-        while (pos >= seq_start + static_cast<long long>(s.items) * s.tiles) {
-            seq_start += static_cast<long long>(s.items) * s.tiles;
+        while (pos >= seq_start + static_cast<long long>(s.items) * (s.tiles + AC_ITEM)) {
+            seq_start += static_cast<long long>(s.items) * (s.tiles + AC_ITEM);
             s = ac_seq<C::ROWS>(a, p, ++seq);
         }
-        const int local = static_cast<int>((pos - seq_start) / s.tiles);
-        const int tile0 = static_cast<int>((pos - seq_start) % s.tiles);
-        const int tile1 = static_cast<int>(min(static_cast<long long>(s.tiles), tile0 + (end - pos)));
+        const int span = s.tiles + AC_ITEM;
+        const int local = static_cast<int>((pos - seq_start) / span);
+        const int off0 = static_cast<int>((pos - seq_start) - static_cast<long long>(local) * span);
+        const int take = static_cast<int>(min(static_cast<long long>(span - off0), end - pos));
+        const int tile0 = max(off0 - AC_ITEM, 0), tile1 = off0 + take - AC_ITEM;
+        pos += take;
+        if (tile1 <= tile0) continue;
         const int head = local % p.kv_heads;
         const int row0 = local / p.kv_heads * C::ROWS;
         const int rows = min(C::ROWS, s.nq * a.group - row0);
         const int32_t* table = p.table + static_cast<long long>(seq) * p.max_pages;
+
+        // Copies of tile k of this run into stage k % STAGES. Pages are looked up one tile earlier.
+        const int mine = tile1 - tile0;
+        int id[2];
+        auto look = [&](int k) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = (tile0 + k) * AC_TILE + h * 16;
+                id[h] = -1;
+                if (k < mine && key < s.len) id[h] = __ldg(table + key / p.page);
+            }
+        };
+        auto issue = [&](int k) {
+            if (k < mine) {
+                const int key0 = (tile0 + k) * AC_TILE;
+                const int st = k % C::STAGES;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool inside = id[h] >= 0 && id[h] < p.pages;
+                    const bool bad = key0 + h * 16 < s.len && !inside;
+                    const long long page = inside ? id[h] : 0;
+                    const int slot = (key0 + h * 16) % p.page;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint8_t* src = p.head_codes(kv, page, head) + slot * D;
+                        const uint32_t dst = ring_u + st * C::STAGE + kv * AC_TILE * D;
+#pragma unroll
+                        for (int i = 0; i < CH / 2; ++i) {  // 16 rows, 32 chunks a step
+                            const int c = i * 32 + lane, r = h * 16 + c / CH;
+                            ac_copy16(dst + ac_place<D>(r, c % CH), src + c * 16, inside && key0 + r < s.len);
+                        }
+                    }
+                    if (lane < 2) {
+                        float* to = ring_scales + st * 4 + lane * 2 + h;
+                        if (bad) {
+                            *to = __int_as_float(0x7fffffff);  // NaN: a page that is not in the pool
+                            if (a.status != nullptr) atomicOr(a.status, KV_PAGE_RANGE);
+                        } else {
+                            ac_copy4(ring_scales_u + (st * 4 + lane * 2 + h) * 4, p.head_scale(lane, page, head), inside);
+                        }
+                    }
+                }
+            }
+            ac_commit();
+        };
+        look(0);
+#pragma unroll
+        for (int k = 0; k < C::STAGES - 1; ++k) {
+            issue(k);
+            look(k + 1);
+        }
 
         // Queries: lane (g, t) has row g of each eight, the elements that its bytes of a key row meet.
         uint32_t qf[NT][KS][2];
@@ -283,68 +369,16 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < KS; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
         }
         float ref = 0.0f, inv_ref = 0.0f;  // largest value scale met
-
-        // Copies of tile k into stage k % AC_STAGES. Pages are looked up one tile earlier.
-        const int mine = (tile1 - tile0 - warp + AC_WARPS - 1) / AC_WARPS;  // tiles of this warp
-        int id[2];
-        auto look = [&](int k) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int key = (tile0 + warp + k * AC_WARPS) * AC_TILE + h * 16;
-                id[h] = -1;
-                if (k < mine && key < s.len) id[h] = __ldg(table + key / p.page);
-            }
-        };
-        auto issue = [&](int k) {
-            if (k < mine) {
-                const int key0 = (tile0 + warp + k * AC_WARPS) * AC_TILE;
-                const int st = k % AC_STAGES;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const bool inside = id[h] >= 0 && id[h] < p.pages;
-                    const bool bad = key0 + h * 16 < s.len && !inside;
-                    const long long page = inside ? id[h] : 0;
-                    const int slot = (key0 + h * 16) % p.page;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const uint8_t* src = p.head_codes(kv, page, head) + slot * D;
-                        const uint32_t dst = ring_u + st * C::STAGE + kv * AC_TILE * D;
-#pragma unroll
-                        for (int i = 0; i < CH / 2; ++i) {  // 16 rows, 32 chunks a step
-                            const int c = i * 32 + lane, r = h * 16 + c / CH;
-                            ac_copy16(dst + ac_place<D>(r, c % CH), src + c * 16, inside && key0 + r < s.len);
-                        }
-                    }
-                    if (lane < 2) {
-                        float* to = ring_scales + st * 4 + lane * 2 + h;
-                        if (bad) {
-                            *to = __int_as_float(0x7fffffff);  // NaN: a page that is not in the pool
-                            if (a.status != nullptr) atomicOr(a.status, KV_PAGE_RANGE);
-                        } else {
-                            ac_copy4(ring_scales_u + (st * 4 + lane * 2 + h) * 4,
-                                     p.head_scale(lane, page, head), inside);
-                        }
-                    }
-                }
-            }
-            ac_commit();
-        };
-        look(0);
-#pragma unroll
-        for (int k = 0; k < AC_STAGES - 1; ++k) {
-            issue(k);
-            look(k + 1);
-        }
         for (int k = 0; k < mine; ++k) {
-            ac_wait<AC_STAGES - 2>();
+            ac_wait<C::STAGES - 2>();
             __syncwarp();
-            issue(k + AC_STAGES - 1);
-            look(k + AC_STAGES);
-            const int st = k % AC_STAGES;
+            issue(k + C::STAGES - 1);
+            look(k + C::STAGES);
+            const int st = k % C::STAGES;
             const uint8_t* kt = ring + st * C::STAGE;
             const uint8_t* vt = kt + AC_TILE * D;
             const float* sc = ring_scales + st * 4;
-            const int key0 = (tile0 + warp + k * AC_WARPS) * AC_TILE;
+            const int key0 = (tile0 + k) * AC_TILE;
 
             float z[2][NT][4];
 #pragma unroll
@@ -487,125 +521,171 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             }
         }
         ac_wait<0>();
+        __syncwarp();  // the ring and the scales are free
 
-        // Join of the warps: statistics, then every warp's sums in units of the common reference.
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
-                if (g == 0) {
-                    float* to = stat + (warp * C::ROWS + n * 8 + 2 * t + j) * 2;
-                    to[0] = m[n][j];
-                    to[1] = l[n][j];
+        if (tile0 == 0 && tile1 == s.tiles) {
+            // The whole item: lane (g, t) has D / 8 neighbouring elements of queries 2t and 2t + 1 of each eight.
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = n * 8 + 2 * t + j;
+                    if (row >= rows) continue;
+#pragma unroll
+                    for (int i = 0; i < KS; i += 2)
+                        ac_store(a, s.q0, head, row0 + row, g * (D / 8) + 2 * i, D,
+                                 make_float4(o[i][n][j] * ref, o[i][n][2 + j] * ref, o[i + 1][n][j] * ref, o[i + 1][n][2 + j] * ref),
+                                 m[n][j], l[n][j]);
                 }
-            }
-        __syncthreads();  // rings are free, statistics are there
-        float2* join = reinterpret_cast<float2*>(smem);
+            continue;
+        }
+        const int which = tile1 < s.tiles ? 1 : 0;  // the run ends in the item, or began in it
+        float2* to = reinterpret_cast<float2*>(which ? ring : ring + C::RING);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int row = n * 8 + 2 * t + j;
-                float top = AC_NONE;
-#pragma unroll
-                for (int w = 0; w < AC_WARPS; ++w) top = fmaxf(top, stat[(w * C::ROWS + row) * 2]);
-                const float f = m[n][j] == top ? ref : ref * ac_ex2(m[n][j] - top);
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
-                    join[(warp * C::ROWS + row) * (D / 2) + ac_join(g * (D / 16) + i, row)] =
-                        make_float2(o[i][n][j] * f, o[i][n][2 + j] * f);
+                    to[row * (D / 2) + ac_join(g * (D / 16) + i, row)] = make_float2(o[i][n][j] * ref, o[i][n][2 + j] * ref);
+                if (g == 0)
+                    *reinterpret_cast<float2*>(stats + ((warp * 2 + which) * C::ROWS + row) * 2) = make_float2(m[n][j], l[n][j]);
             }
-        __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == s.tiles;
-        const int slot = cta * 2 + (pos == first_pos ? 0 : 1);
-        float* part = a.parts + static_cast<long long>(slot) * C::PART;
-        for (int i = tid; i < rows * (D / 4); i += AC_THREADS) {
+        if (lane == 0) {
+            AcRecord& r = rec[warp * 2 + which];
+            r.u0 = seq_start + static_cast<long long>(local) * span;
+            r.tile0 = tile0;
+            r.tile1 = tile1;
+            r.tiles = s.tiles;
+            r.q0 = s.q0;
+            r.row0 = row0;
+            r.rows = rows;
+            r.head = head;
+        }
+    }
+    __syncthreads();
+
+    // Join of the records, which stand in the line's order: those of one item follow one another.
+    int shared_item[2] = {-1, -1};  // records of the items that other CTAs share: begun before this one, and here
+    for (int r0 = 0; r0 < 2 * AC_WARPS;) {
+        const AcRecord r = rec[r0];
+        if (r.u0 < 0) {
+            ++r0;
+            continue;
+        }
+        int r1 = r0, tile1 = r.tile1;  // the item's last record
+        for (int k = r0 + 1; k < 2 * AC_WARPS; ++k)
+            if (rec[k].u0 == r.u0) {
+                r1 = k;
+                tile1 = rec[k].tile1;
+            }
+        const bool whole = r.tile0 == 0 && tile1 == r.tiles;
+        const int slot = r.tile0 > 0 ? 0 : 1;
+        if (!whole) shared_item[slot] = r0;
+        float* part = a.parts + static_cast<long long>(cta * 2 + slot) * C::PART;
+        for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
             const int row = i / (D / 4), c = i % (D / 4) * 2;
-            float top = AC_NONE, sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < AC_WARPS; ++w) top = fmaxf(top, stat[(w * C::ROWS + row) * 2]);
-            float2 x = make_float2(0.0f, 0.0f), y = x;
-#pragma unroll
-            for (int w = 0; w < AC_WARPS; ++w) {
-                const float mw = stat[(w * C::ROWS + row) * 2], lw = stat[(w * C::ROWS + row) * 2 + 1];
-                sum += mw == top ? lw : lw * ac_ex2(mw - top);
-                const float2* from = join + (w * C::ROWS + row) * (D / 2);
+            float top = AC_NONE;
+            for (int k = r0; k <= r1; ++k)
+                if (rec[k].u0 >= 0) top = fmaxf(top, stats[(k * C::ROWS + row) * 2]);
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float sum = 0.0f;
+            for (int k = r0; k <= r1; ++k) {
+                if (rec[k].u0 < 0) continue;
+                const float2 ml = *reinterpret_cast<const float2*>(stats + (k * C::ROWS + row) * 2);
+                const float f = ml.x == top ? 1.0f : ac_ex2(ml.x - top);
+                const float2* from = reinterpret_cast<const float2*>(smem + (k >> 1) * C::WARP + (k & 1 ? 0 : C::RING)) + row * (D / 2);
                 const float2 u = from[ac_join(c, row)], v = from[ac_join(c + 1, row)];
-                x.x += u.x;
-                x.y += u.y;
-                y.x += v.x;
-                y.y += v.y;
+                sum += ml.y * f;
+                x.x += u.x * f;
+                x.y += u.y * f;
+                x.z += v.x * f;
+                x.w += v.y * f;
             }
             if (whole) {
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const int qi = (row0 + row) / a.group, hd = head * a.group + (row0 + row) % a.group;
-                uint2 out = make_uint2(0, 0);
-                if (sum != 0.0f) {
-                    __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), b1 = __floats2bfloat162_rn(y.x * inv, y.y * inv);
-                    out = make_uint2(*reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1));
-                }
-                *reinterpret_cast<uint2*>(a.O + (s.q0 + qi) * a.ldo + hd * D + c * 2) = out;
-                if (c == 0)
-                    a.LSE[static_cast<long long>(hd) * a.Tq + s.q0 + qi] =
-                        sum == 0.0f ? AC_NONE : (top + log2f(sum) - AC_BIAS) * AC_LN2;
+                ac_store(a, r.q0, r.head, r.row0 + row, c * 2, D, x, top, sum);
             } else {
-                *reinterpret_cast<float4*>(part + row * D + c * 2) = make_float4(x.x, x.y, y.x, y.y);
+                *reinterpret_cast<float4*>(part + row * D + c * 2) = x;
                 if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = make_float2(top, sum);
             }
         }
-        if (!whole) {
-            // The item's parts: of the CTAs that hold its first to its last tile.
-            const long long u0 = pos - tile0, u1 = u0 + s.tiles - 1;
-            const int c0 = static_cast<int>(((u0 + 1) * ctas - 1) / total), c1 = static_cast<int>(((u1 + 1) * ctas - 1) / total);
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();
-                // wraps to zero with the last one
-                sh_last = atomicInc(a.counters + c0, static_cast<unsigned>(c1 - c0)) == static_cast<unsigned>(c1 - c0);
-                __threadfence();
-            }
-            __syncthreads();
-            if (sh_last) {
-                const int n_parts = c1 - c0 + 1;
-                const int slot0 = c0 * 2 + (total * c0 / ctas == u0 ? 0 : 1);
-                for (int i = tid; i < rows * (D / 4); i += AC_THREADS) {
-                    const int row = i / (D / 4), c = i % (D / 4) * 4;
-                    float top = AC_NONE, sum = 0.0f;
-                    for (int k = 0; k < n_parts; ++k) {
-                        const float* from = a.parts + static_cast<long long>(k == 0 ? slot0 : (c0 + k) * 2) * C::PART;
-                        top = fmaxf(top, __ldcg(from + C::ROWS * D + row * 2));
-                    }
-                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                    for (int k = 0; k < n_parts; ++k) {
-                        const float* from = a.parts + static_cast<long long>(k == 0 ? slot0 : (c0 + k) * 2) * C::PART;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + C::ROWS * D + row * 2));
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(from + row * D + c));
-                        const float f = ml.x == top ? 1.0f : ac_ex2(ml.x - top);
-                        sum += ml.y * f;
-                        x.x += v.x * f;
-                        x.y += v.y * f;
-                        x.z += v.z * f;
-                        x.w += v.w * f;
-                    }
-                    const float inv = 1.0f / sum;
-                    const int qi = (row0 + row) / a.group, hd = head * a.group + (row0 + row) % a.group;
-                    uint2 out = make_uint2(0, 0);
-                    if (sum != 0.0f) {
-                        __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), b1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-                        out = make_uint2(*reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1));
-                    }
-                    *reinterpret_cast<uint2*>(a.O + (s.q0 + qi) * a.ldo + hd * D + c) = out;
-                    if (c == 0)
-                        a.LSE[static_cast<long long>(hd) * a.Tq + s.q0 + qi] =
-                            sum == 0.0f ? AC_NONE : (top + log2f(sum) - AC_BIAS) * AC_LN2;
-                }
-            }
+        r0 = r1 + 1;
+    }
+    if (shared_item[0] < 0 && shared_item[1] < 0) return;
+
+    // Parts of an item come from the CTAs of its first to its last tile: one counter each, at the first.
+    auto cta_of = [&](long long place) { return static_cast<int>(((place + 1) * ctas - 1) / total); };
+    __syncthreads();  // the parts are written
+    if (tid < 2) {
+        sh_last[tid] = 0;
+        if (shared_item[tid] >= 0) {
+            const AcRecord& r = rec[shared_item[tid]];
+            const int c0 = cta_of(r.u0 + AC_ITEM), c1 = cta_of(r.u0 + AC_ITEM + r.tiles - 1);
+            __threadfence();
+            // wraps to zero with the last one
+            sh_last[tid] = atomicInc(a.counters + c0, static_cast<unsigned>(c1 - c0)) == static_cast<unsigned>(c1 - c0);
+            __threadfence();
         }
-        __syncthreads();  // the join's buffer becomes rings again
-        pos += tile1 - tile0;
+    }
+    __syncthreads();
+    for (int which = 0; which < 2; ++which) {
+        if (!sh_last[which]) continue;
+        const AcRecord r = rec[shared_item[which]];
+        const int c0 = cta_of(r.u0 + AC_ITEM), n_parts = cta_of(r.u0 + AC_ITEM + r.tiles - 1) - c0 + 1;
+        // the first CTA began the item, the others found it begun
+        auto part = [&](int k) { return a.parts + static_cast<long long>((c0 + k) * 2 + (k == 0 ? 1 : 0)) * C::PART; };
+        float2* ml = reinterpret_cast<float2*>(smem);                                     // [part][row]
+        float4* sums = reinterpret_cast<float4*>(smem + AC_WARPS * (C::WARP - C::HEAD));  // [warp][row][D / 4]
+        for (int i = tid; i < n_parts * C::ROWS; i += AC_THREADS)
+            if (i % C::ROWS < r.rows)
+                ml[i] = __ldcg(reinterpret_cast<const float2*>(part(i / C::ROWS) + C::ROWS * D) + i % C::ROWS);
+        __syncthreads();
+        // A warp takes every eighth part.
+        for (int i = lane; i < r.rows * (D / 4); i += 32) {
+            const int row = i / (D / 4);
+            float top = AC_NONE;
+            for (int k = 0; k < n_parts; ++k) top = fmaxf(top, ml[k * C::ROWS + row].x);
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int k = warp; k < n_parts; k += AC_WARPS) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(part(k)) + i);
+                const float mk = ml[k * C::ROWS + row].x;
+                const float f = mk == top ? 1.0f : ac_ex2(mk - top);
+                x.x += v.x * f;
+                x.y += v.y * f;
+                x.z += v.z * f;
+                x.w += v.w * f;
+            }
+            sums[warp * (C::ROWS * D / 4) + i] = x;
+        }
+        __syncthreads();
+        for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
+            const int row = i / (D / 4);
+            float top = AC_NONE, sum = 0.0f;
+            for (int k = 0; k < n_parts; ++k) top = fmaxf(top, ml[k * C::ROWS + row].x);
+            for (int k = 0; k < n_parts; ++k) {
+                const float2 v = ml[k * C::ROWS + row];
+                sum += v.y * (v.x == top ? 1.0f : ac_ex2(v.x - top));
+            }
+            float4 x = sums[i];
+#pragma unroll
+            for (int w = 1; w < AC_WARPS; ++w) {
+                const float4 v = sums[w * (C::ROWS * D / 4) + i];
+                x.x += v.x;
+                x.y += v.y;
+                x.z += v.z;
+                x.w += v.w;
+            }
+            ac_store(a, r.q0, r.head, r.row0 + row, i % (D / 4) * 4, D, x, top, sum);
+        }
+        __syncthreads();
     }
 }
 

@@ -51,7 +51,7 @@ def _run(Q, codes, scales, table, new, lens, causal=True, scale=None, status=0, 
     return O.cpu(), LSE.cpu()
 
 
-def _check(got, Q, codes, scales, table, new, lens, causal=True, scale=None):
+def _check(got, Q, codes, scales, table, new, lens, causal=True, scale=None, skip=None):
     O, LSE = f64(got[0]), f64(got[1])
     heads, d, kv, page = Q.shape[1], Q.shape[2], codes.shape[2], codes.shape[3]
     scale = d ** -0.5 if scale is None else scale
@@ -60,6 +60,8 @@ def _check(got, Q, codes, scales, table, new, lens, causal=True, scale=None):
         k, v = (oracle.kv_cache_rows(f64(codes[:, j]), f64(scales[:, j]), table[i].tolist(), page, 0, nk) for j in (0, 1))
         at = slice(row, row + nq)
         row += nq
+        if i == skip:
+            continue
         wo, wl = oracle.attn_varlen_fwd(q[at], k, v, [0, nq], [0, nk], causal, scale)
         wa, _ = oracle.attn_varlen_fwd(q[at], k, np.abs(v), [0, nq], [0, nk], causal, scale)
         seen = np.isfinite(wl)
@@ -186,12 +188,11 @@ def test_nan_in_the_cache_reaches_the_rows_that_see_it():
 def test_bad_sequences_and_pages():
     new, lens = [1, 2, 1], [100, 50, 60]
     Q, codes, scales, table = _make(new, lens, 4, 2, 64, 16, 23900)
-    clean = _run(Q, codes, scales, table, new, lens)
 
     def rows_left(got, lo, hi):
+        # The others by their own tolerance: how the work is split, and so the order of sums, goes by all sequences.
         assert torch.isnan(got[0][lo:hi]).all() and torch.isnan(got[1][:, lo:hi]).all()
-        keep = [i for i in range(4) if not lo <= i < hi]
-        assert torch.equal(got[0][keep], clean[0][keep]) and torch.equal(got[1][:, keep], clean[1][:, keep])
+        _check(got, Q, codes, scales, table, new, lens, skip=1 if lo == 1 else 2)
 
     for bad in (-1, table.shape[1] * 16 + 1):
         rows_left(_run(Q, codes, scales, table, new, [100, bad, 60], status=4), 1, 3)
