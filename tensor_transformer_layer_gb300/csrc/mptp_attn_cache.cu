@@ -5,20 +5,21 @@
 //   S = scale * scale_k * (q . code_k),  P = exp(S - max),  O = sum P * scale_v * code_v / sum P
 //
 // Bound by memory: every cached byte is read once and meets `rows` queries, 2 * rows flops a byte. So a warp reads 32 tokens'
-// codes into its own ring in shared memory (cp.async, 16 bytes a lane, two tiles ahead), turns them into halves in
-// registers (exact) and feeds mma.sync m16n8k16 with the cache as the 16-row operand and the queries as the 8-column one:
-//   S^T [keys x queries] = K Q^T: a lane's 16 bytes of a key row are its elements of four products (the summed index
-//     may be taken in any order, the same for Q);
-//   O^T [d x queries] += V^T P^T: bytes of two key rows are interleaved into pairs of keys, P^T comes from S^T by
-//     transposing 8x8 blocks (movmatrix).
+// codes into its own ring in shared memory (cp.async, 16 bytes a lane, two tiles ahead) and feeds mma.sync with the cache as
+// the 16-row operand and the queries as the 8-column one:
+//   S^T [keys x queries] = K Q^T in m16n8k32 of e4m3, the codes as they are: a lane's 16 bytes of a key row are its elements
+//     of two products (the summed index may be taken in any order, the same for Q);
+//   O^T [d x queries] += V^T P^T in m16n8k16 of halves: bytes of two key rows are interleaved into pairs of keys and turned
+//     into halves (exact), P^T comes from S^T by transposing 8x8 blocks (movmatrix).
 // With the queries as columns, eight rows fill a product that sixteen would share otherwise, and a column's statistics
-// and its sums in O^T lie in the same lane. The tensor cores' 5th-generation products (tcgen05) would need the halves in shared
-// or tensor memory, one more trip for every cached byte, for 128 rows of which a decoded token has eight.
+// and its sums in O^T lie in the same lane. The tensor cores' 5th-generation products (tcgen05) would need their operands in
+// shared or tensor memory, V one more trip for every cached byte, for 128 rows of which a decoded token has eight.
 //
-// Numbers. Q is scaled per row by a power of two into [1, 2) at its largest, then rounded to halves: exact, but for
-// elements below 2^-14 of the largest, which keep 2^-25 of it. P = 2^(s - m + 7), s within m + 8 of the reference m, is
-// rounded to halves (2^-11 of its value, at least 2^-25 absolutely, 2^-32 of a probability of m) times the value's scale over the
-// largest value scale met so far. Statistics and sums are fp32.
+// Numbers. Q is scaled per row by a power of two into [128, 256) at its largest and split into two e4m3 pieces, q1 + q2 / 32:
+// four of bf16's eight bits each, exact but for elements below 2^-13 of the largest, which keep 2^-22 of it. Both pieces have
+// sums of their own (fp32, as every sum and statistic here). P = 2^(s - m + 7), s within m + 8 of the reference m, is
+// rounded to halves (2^-11 of its value, at least 2^-25 absolutely, 2^-32 of a probability of m) times the value's scale over
+// the largest value scale met so far.
 //
 // Work. The tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, AC_ITEM places for what an item
 // costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
@@ -52,6 +53,7 @@ struct AcArgs {
     long long ldq, ldo;
     int nseq, Tq, max_q, heads, group, causal;
     float scale_log2;
+    int page_shift;  // log2 of the page
     uint32_t* status;
 };
 
@@ -64,7 +66,10 @@ __device__ __forceinline__ int ac_place(int r, int c) {
     return r * D + (c << 4);
 }
 
-__device__ __forceinline__ void ac_copy16(uint32_t dst, const void* src, bool take) {
+__device__ __forceinline__ void ac_copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ac_copy16(uint32_t dst, const void* src, bool take) {  // zeros where not taken
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void ac_copy4(uint32_t dst, const void* src, bool take) {
@@ -80,6 +85,12 @@ __device__ __forceinline__ void ac_mma(float (&c)[4], const uint32_t (&a)[4], ui
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ac_mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t ac_transpose(uint32_t x) {
     uint32_t y;
@@ -258,39 +269,52 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 
         // Copies of tile k of this run into stage k % STAGES. Pages are looked up one tile earlier.
         const int mine = tile1 - tile0;
+        const uint8_t* k_codes = p.head_codes(0, 0, head) + lane * 16;
+        const uint8_t* v_codes = p.head_codes(1, 0, head) + lane * 16;
         int id[2];
         auto look = [&](int k) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int key = (tile0 + k) * AC_TILE + h * 16;
-                id[h] = -1;
-                if (k < mine && key < s.len) id[h] = __ldg(table + key / p.page);
+            const int key = (tile0 + k) * AC_TILE;
+            id[0] = id[1] = -1;
+            if (k < mine) {
+                if (key < s.len) id[0] = __ldg(table + (key >> a.page_shift));
+                if (key + 16 < s.len) id[1] = __ldg(table + ((key + 16) >> a.page_shift));
             }
         };
         auto issue = [&](int k) {
             if (k < mine) {
                 const int key0 = (tile0 + k) * AC_TILE;
                 const int st = k % C::STAGES;
+                const uint32_t dst = ring_u + st * C::STAGE;
+                const bool full = key0 + AC_TILE <= s.len && static_cast<unsigned>(id[0]) < static_cast<unsigned>(p.pages) &&
+                                  static_cast<unsigned>(id[1]) < static_cast<unsigned>(p.pages);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const bool inside = id[h] >= 0 && id[h] < p.pages;
-                    const bool bad = key0 + h * 16 < s.len && !inside;
-                    const long long page = inside ? id[h] : 0;
-                    const int slot = (key0 + h * 16) % p.page;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const uint8_t* src = p.head_codes(kv, page, head) + slot * D;
-                        const uint32_t dst = ring_u + st * C::STAGE + kv * AC_TILE * D;
+                    const int slot = ((key0 + h * 16) & (p.page - 1)) * D;
+                    const bool inside = static_cast<unsigned>(id[h]) < static_cast<unsigned>(p.pages);
+                    const int page = inside ? id[h] : 0;
+                    const uint8_t* ks = k_codes + page * p.ld_codes[0] + slot;
+                    const uint8_t* vs = v_codes + page * p.ld_codes[1] + slot;
+                    if (full) {
 #pragma unroll
                         for (int i = 0; i < CH / 2; ++i) {  // 16 rows, 32 chunks a step
+                            const int c = i * 32 + lane;
+                            const uint32_t at = dst + ac_place<D>(h * 16 + c / CH, c % CH);
+                            ac_copy16(at, ks + i * 512);
+                            ac_copy16(at + AC_TILE * D, vs + i * 512);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < CH / 2; ++i) {
                             const int c = i * 32 + lane, r = h * 16 + c / CH;
-                            ac_copy16(dst + ac_place<D>(r, c % CH), src + c * 16, inside && key0 + r < s.len);
+                            const uint32_t at = dst + ac_place<D>(r, c % CH);
+                            const bool live = inside && key0 + r < s.len;
+                            ac_copy16(at, ks + i * 512, live);
+                            ac_copy16(at + AC_TILE * D, vs + i * 512, live);
                         }
                     }
                     if (lane < 2) {
-                        float* to = ring_scales + st * 4 + lane * 2 + h;
-                        if (bad) {
-                            *to = __int_as_float(0x7fffffff);  // NaN: a page that is not in the pool
+                        if (key0 + h * 16 < s.len && !inside) {
+                            ring_scales[st * 4 + lane * 2 + h] = __int_as_float(0x7fffffff);  // NaN: a page outside the pool
                             if (a.status != nullptr) atomicOr(a.status, KV_PAGE_RANGE);
                         } else {
                             ac_copy4(ring_scales_u + (st * 4 + lane * 2 + h) * 4, p.head_scale(lane, page, head), inside);
@@ -308,9 +332,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         }
 
         // Queries: lane (g, t) has row g of each eight, the elements that its bytes of a key row meet.
-        uint32_t qf[NT][KS][2];
-        float fq[NT][2];   // factor from a product to a score in powers of two, for columns 2t, 2t + 1
-        int limit[NT][2];  // keys that those columns see
+        uint32_t qf[2][NT][KS];  // pieces q1, q2
+        float fq[NT][2];         // factor from a product to a score in powers of two, for columns 2t, 2t + 1
+        int limit[NT][2];        // keys that those columns see
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int row = row0 + n * 8 + g;
@@ -334,21 +358,26 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x.w[k] << 16)), fabsf(__uint_as_float(x.w[k] & 0xffff0000u))));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const int e = m > 0.0f && m < __int_as_float(0x7f800000)
-                              ? max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -126)
-                              : 0;
-            // 2^-e in two factors: e = 127 has no normal one
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - (e >> 1)) << 23);
-            const float down2 = __uint_as_float(static_cast<uint32_t>(127 - (e - (e >> 1))) << 23);
+            // An infinity in the row makes all of it NaN (e4m3 would hold it as 448).
+            const float nan = m < __int_as_float(0x7f800000) ? 0.0f : __int_as_float(0x7fffffff);
+            const int e = max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100) - 7;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - min(e, 120)) << 23);
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+            for (int k = 0; k < KS; ++k) {
+                uint32_t piece[2] = {0, 0};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t w = x.w[2 * k + j];
-                    qf[n][k][j] = ac_half2(__uint_as_float(w << 16) * down * down2,
-                                           __uint_as_float(w & 0xffff0000u) * down * down2);
+                    const float q0 = __uint_as_float(w << 16) * down + nan, q1 = __uint_as_float(w & 0xffff0000u) * down + nan;
+                    const uint32_t c = float2_to_e4m3x2(q0, q1);
+                    const float2 held = f16x2_to_float2(e4m3x2_to_f16x2(c));
+                    piece[0] |= c << (16 * j);
+                    piece[1] |= float2_to_e4m3x2((q0 - held.x) * 32.0f, (q1 - held.y) * 32.0f) << (16 * j);
                 }
-            const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * a.scale_log2;
+                qf[0][n][k] = piece[0];
+                qf[1][n][k] = piece[1];
+            }
+            const float f = __uint_as_float(static_cast<uint32_t>(min(e, 120) + 127) << 23) * a.scale_log2;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 fq[n][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
@@ -383,8 +412,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             float z[2][NT][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                float z2[NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) z[h][n][0] = z[h][n][1] = z[h][n][2] = z[h][n][3] = 0.0f;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) z[h][n][c] = z2[n][c] = 0.0f;
                 uint32_t kw[2][KS];  // words of rows g and g + 8
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
@@ -408,37 +440,44 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const uint32_t f[4] = {e4m3x2_to_f16x2(kw[0][i] & 0xffffu), e4m3x2_to_f16x2(kw[1][i] & 0xffffu),
-                                           e4m3x2_to_f16x2(kw[0][i] >> 16), e4m3x2_to_f16x2(kw[1][i] >> 16)};
+                for (int i = 0; i < KS; i += 2)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) ac_mma(z[h][n], f, qf[n][i][0], qf[n][i][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        ac_mma8(z[h][n], kw[0][i], kw[1][i], kw[0][i + 1], kw[1][i + 1], qf[0][n][i], qf[0][n][i + 1]);
+                        ac_mma8(z2[n], kw[0][i], kw[1][i], kw[0][i + 1], kw[1][i + 1], qf[1][n][i], qf[1][n][i + 1]);
+                    }
+                // Scores in powers of two; lane (g, t) has keys g, g + 8 of each 16 and queries 2t, 2t + 1 of each 8.
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float f[2] = {sc[h] * fq[n][0], sc[h] * fq[n][1]};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) z[h][n][c] = fmaf(z2[n][c], 0.03125f, z[h][n][c]) * f[c & 1];
                 }
             }
-
-            // Scores in powers of two; lane (g, t) has keys g, g + 8 of each 16 and queries 2t, 2t + 1 of each 8.
-            const bool masked = key0 + AC_TILE > clear;
+            if (key0 + AC_TILE > clear) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (key0 + h * 16 + (c >> 1) * 8 + g >= limit[n][c & 1]) z[h][n][c] = AC_NONE;
+            }
+            float high[NT][2];
             bool higher = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float k_scale = sc[h];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v = z[h][n][c] * (k_scale * fq[n][c & 1]);
-                        if (masked && key0 + h * 16 + (c >> 1) * 8 + g >= limit[n][c & 1]) v = AC_NONE;
-                        z[h][n][c] = v;
-                        higher |= v > m[n][c & 1] + AC_SLACK;
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    high[n][j] = fmaxf(fmaxf(z[0][n][j], z[0][n][2 + j]), fmaxf(z[1][n][j], z[1][n][2 + j]));
+                    higher |= high[n][j] > m[n][j] + AC_SLACK;
                 }
             if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float v = fmaxf(fmaxf(z[0][n][j], z[0][n][2 + j]), fmaxf(z[1][n][j], z[1][n][2 + j]));
-                        v = fmaxf(v, m[n][j]);
+                        float v = fmaxf(high[n][j], m[n][j]);
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
                         // Equal references leave the sums alone, both -inf (nothing seen yet) among them.
@@ -513,8 +552,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                     const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
                     const uint32_t lo = __byte_perm(vw[0][j / 2], vw[1][j / 2], sel);
                     const uint32_t hi = __byte_perm(vw[2][j / 2], vw[3][j / 2], sel);
-                    const uint32_t f[4] = {e4m3x2_to_f16x2(lo & 0xffffu), e4m3x2_to_f16x2(lo >> 16),
-                                           e4m3x2_to_f16x2(hi & 0xffffu), e4m3x2_to_f16x2(hi >> 16)};
+                    const uint32_t f[4] = {e4m3x2_to_f16x2(lo), e4m3x2_hi_to_f16x2(lo), e4m3x2_to_f16x2(hi),
+                                           e4m3x2_hi_to_f16x2(hi)};
 #pragma unroll
                     for (int n = 0; n < NT; ++n) ac_mma(o[j][n], f, pt[h][n][0], pt[h][n][1]);
                 }
@@ -773,6 +812,7 @@ extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, cons
     a.group = heads / kv_heads;
     a.causal = causal != 0;
     a.scale_log2 = scale * AC_LOG2E;
+    a.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     a.status = d_status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool few = ac_rows(max_q, a.group) == 8;

@@ -130,7 +130,7 @@ __device__ __forceinline__ uint32_t kv_quant2(uint32_t w, float inv) {
 
 // Four codes times a ratio <= 1, rounded again.
 __device__ __forceinline__ uint32_t kv_requant4(uint32_t c, float ratio) {
-    const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(c & 0xffffu)), b = f16x2_to_float2(e4m3x2_to_f16x2(c >> 16));
+    const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(c)), b = f16x2_to_float2(e4m3x2_hi_to_f16x2(c));
     return float2_to_e4m3x2(a.x * ratio, a.y * ratio) | float2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
 }
 
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvRows r, con
             uint32_t o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(in[j / 2] >> (j % 2 * 16)));
+                const float2 f = f16x2_to_float2(j % 2 ? e4m3x2_hi_to_f16x2(in[j / 2]) : e4m3x2_to_f16x2(in[j / 2]));
                 __nv_bfloat162 b = __floats2bfloat162_rn(f.x * scale, f.y * scale);
                 o[j] = *reinterpret_cast<uint32_t*>(&b);
             }

@@ -29,10 +29,16 @@ struct KvPool {
     }
 };
 
-// Two e4m3 codes as two halves (exact: every e4m3 value is a half).
+// The lower two codes as two halves (exact: every e4m3 value is a half).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
     uint32_t r;
-    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(two));
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(two));
+    return r;
+}
+// The same of the upper two of four.
+__device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t four) {
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(four));
     return r;
 }
 __device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
