@@ -38,6 +38,7 @@ constexpr int AC_ITEM = 4;      // places of an item besides its tiles
 constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
 #define AC_NONE __int_as_float(0xff800000)  // -inf: no key seen
 constexpr float AC_BIAS = 7.0f;    // exponent that P carries into halves
+constexpr int AC_SEQS = 4;         // sequences a lane looks at in one step
 constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference before sums are scaled down
 constexpr float AC_LOG2E = 1.4426950408889634f;
 constexpr float AC_LN2 = 0.6931471805599453f;
@@ -116,10 +117,10 @@ struct AcShape {
     static constexpr int HEAD = ROWS * D * 4;        // the record of the item that its run begins in
     static constexpr int WARP = RING + HEAD;
     static constexpr int SCALES = STAGES * 16;       // a warp's: two of K, two of V
-    static constexpr int STATS = 2 * ROWS * 8;       // a warp's: (reference, sum) of the records' rows
+    static constexpr int STATS = 2 * ROWS * 12;      // a warp's: (reference, sum) of its records' rows, and the items' largest
     static constexpr int SMEM = AC_WARPS * (WARP + SCALES + STATS);
     static constexpr int PART = ROWS * (D + 2);      // floats of a part
-    static_assert(HEAD <= RING && SMEM <= 226 * 1024, "shared memory");
+    static_assert(HEAD <= RING && SMEM <= 231424, "shared memory");
     static_assert(AC_CTAS * ROWS * 8 + AC_WARPS * HEAD <= AC_WARPS * WARP, "the parts' statistics beside the warps' sums");
 };
 
@@ -136,10 +137,11 @@ struct AcSeq {
 };
 template <int ROWS>
 __device__ __forceinline__ AcSeq ac_seq(const AcArgs& a, const KvPool& p, int seq) {
-    AcSeq s;
-    s.q0 = a.cu_q[seq];
-    const int q1 = a.cu_q[seq + 1];
-    s.len = a.lens[seq];
+    AcSeq s{0, 0, 0, 1, 0};
+    if (seq >= a.nseq) return s;
+    s.q0 = __ldg(a.cu_q + seq);
+    const int q1 = __ldg(a.cu_q + seq + 1);
+    s.len = __ldg(a.lens + seq);
     s.nq = q1 - s.q0;
     if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || s.nq > a.max_q || s.len < 0 ||
         static_cast<long long>(s.len) > static_cast<long long>(p.max_pages) * p.page) {
@@ -175,9 +177,6 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     constexpr int KS = D / 16;   // products along d of one score tile; also tiles of 16 rows of O^T
     constexpr int CH = D / 16;   // 16-byte chunks a key row
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long sh_total[AC_WARPS];
-    __shared__ long long sh_start[AC_WARPS];
-    __shared__ int sh_seq[AC_WARPS];
     __shared__ AcRecord rec[2 * AC_WARPS];
     __shared__ int sh_last[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -185,65 +184,72 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // The line's length, then the CTA's run, its warps' and the sequences that hold their first places.
-    auto places = [&](int seq) {
-        if (seq >= a.nseq) return 0ll;
-        const AcSeq s = ac_seq<C::ROWS>(a, p, seq);
-        return static_cast<long long>(s.items) * (s.tiles + AC_ITEM);
-    };
-    const long long mine0 = places(tid);
-    long long total = mine0;
-    for (int base = AC_THREADS; base < a.nseq; base += AC_THREADS) total += places(base + tid);
+    // The line's length, then the warp's run and the sequence that holds its first place: each warp by itself, lanes taking
+    // AC_SEQS neighbouring sequences each (loads side by side, no barrier).
+    auto places = [&](const AcSeq& q) { return static_cast<long long>(q.items) * (q.tiles + AC_ITEM); };
+    AcSeq first[AC_SEQS];
+    long long total = 0;
+    for (int base = 0; base < a.nseq; base += 32 * AC_SEQS)
+#pragma unroll
+        for (int k = 0; k < AC_SEQS; ++k) {
+            const AcSeq q = ac_seq<C::ROWS>(a, p, base + lane * AC_SEQS + k);
+            if (base == 0) first[k] = q;
+            total += places(q);
+        }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    if (lane == 0) {
-        sh_total[warp] = total;
-        rec[2 * warp].u0 = rec[2 * warp + 1].u0 = -1;
-    }
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int k = 0; k < AC_WARPS; ++k) total += sh_total[k];
-    __syncthreads();
     // As many CTAs as have a few places for each of their warps.
     const long long want = (total + 2 * AC_WARPS - 1) / (2 * AC_WARPS);
     const int ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : static_cast<long long>(gridDim.x));
     const int cta = blockIdx.x;
     if (cta >= ctas) return;
+    if (lane < 2) rec[2 * warp + lane].u0 = -1;
     const long long cta_pos = total * cta / ctas, cta_end = total * (cta + 1) / ctas;
-    auto run = [&](int w) { return cta_pos + (cta_end - cta_pos) * w / AC_WARPS; };
-    long long before = 0;
-    for (int base = 0; base < a.nseq && before <= run(AC_WARPS - 1); base += AC_THREADS) {
-        const long long n = base == 0 ? mine0 : places(base + tid);
-        long long upto = n;
+    long long pos = cta_pos + (cta_end - cta_pos) * warp / AC_WARPS;
+    const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / AC_WARPS;
+    int seq = 0;
+    long long seq_start = 0;
+    AcSeq s = first[0];
+    for (int base = 0; base < a.nseq; base += 32 * AC_SEQS) {
+        long long mine = 0;
+        if (base > 0)
+#pragma unroll
+            for (int k = 0; k < AC_SEQS; ++k) first[k] = ac_seq<C::ROWS>(a, p, base + lane * AC_SEQS + k);
+#pragma unroll
+        for (int k = 0; k < AC_SEQS; ++k) mine += places(first[k]);
+        long long upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += v;
         }
-        if (lane == 31) sh_total[warp] = upto;
-        __syncthreads();
-        long long all = 0;
-#pragma unroll
-        for (int k = 0; k < AC_WARPS; ++k) {
-            if (k < warp) upto += sh_total[k];
-            all += sh_total[k];
+        upto += seq_start;
+        const unsigned here = __ballot_sync(0xffffffffu, pos < upto);
+        if (here == 0) {
+            seq_start = __shfl_sync(0xffffffffu, upto, 31);
+            continue;
         }
-        upto += before;
+        // The lane that holds it walks its own sequences, then tells the others.
+        const int who = __ffs(here) - 1;
+        long long start = upto - mine;
+        int k = 0;
+        s = first[0];
 #pragma unroll
-        for (int w = 0; w < AC_WARPS; ++w)
-            if (run(w) < upto && run(w) >= upto - n) {
-                sh_seq[w] = base + tid;
-                sh_start[w] = upto - n;
+        for (int j = 1; j < AC_SEQS; ++j)
+            if (k == j - 1 && pos >= start + places(s)) {
+                start += places(s);
+                s = first[j];
+                k = j;
             }
-        before += all;
-        __syncthreads();
+        seq = base + who * AC_SEQS + __shfl_sync(0xffffffffu, k, who);
+        seq_start = __shfl_sync(0xffffffffu, start, who);
+        s.q0 = __shfl_sync(0xffffffffu, s.q0, who);
+        s.nq = __shfl_sync(0xffffffffu, s.nq, who);
+        s.len = __shfl_sync(0xffffffffu, s.len, who);
+        s.tiles = __shfl_sync(0xffffffffu, s.tiles, who);
+        s.items = __shfl_sync(0xffffffffu, s.items, who);
+        break;
     }
-    long long pos = run(warp);
-    const long long end = run(warp + 1);
-    int seq = sh_seq[warp];
-    long long seq_start = sh_start[warp];
-    AcSeq s = ac_seq<C::ROWS>(a, p, seq);
 
     uint8_t* ring = smem + warp * C::WARP;
     const uint32_t ring_u = smem_u32(ring);
@@ -325,37 +331,40 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             ac_commit();
         };
         look(0);
+        // Queries: lane (g, t) has row g of each eight, the elements that its bytes of a key row meet. Asked for before the
+        // copies, used behind them.
+        constexpr int NV = D / 32;  // 16-byte vectors of a lane
+        union {
+            uint4 v[NV];
+            uint32_t w[NV * 4];
+        } x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = row0 + n * 8 + g;
+            const __nv_bfloat16* src = a.Q + (s.q0 + row / a.group) * a.ldq + (head * a.group + row % a.group) * D;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                // D = 128: 16 elements of each half; else D / 4 neighbouring ones
+                const int at = D == 128 ? (k >> 1) * 64 + t * 16 + (k & 1) * 8 : t * (D / 4) + k * 8;
+                x[n].v[k] = make_uint4(0, 0, 0, 0);
+                if (n * 8 + g < rows) x[n].v[k] = *reinterpret_cast<const uint4*>(src + at);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < C::STAGES - 1; ++k) {
             issue(k);
             look(k + 1);
         }
 
-        // Queries: lane (g, t) has row g of each eight, the elements that its bytes of a key row meet.
         uint32_t qf[2][NT][KS];  // pieces q1, q2
         float fq[NT][2];         // factor from a product to a score in powers of two, for columns 2t, 2t + 1
         int limit[NT][2];        // keys that those columns see
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int row = row0 + n * 8 + g;
-            const int qi = row / a.group, hd = head * a.group + row % a.group;
-            constexpr int NV = D / 32;  // 16-byte vectors of a lane
-            union {
-                uint4 v[NV];
-                uint32_t w[NV * 4];
-            } x;
-            const __nv_bfloat16* src = a.Q + (s.q0 + qi) * a.ldq + hd * D;
             float m = 0.0f;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                // D = 128: 16 elements of each half; else D / 4 neighbouring ones
-                const int at = D == 128 ? (k >> 1) * 64 + t * 16 + (k & 1) * 8 : t * (D / 4) + k * 8;
-                x.v[k] = make_uint4(0, 0, 0, 0);
-                if (n * 8 + g < rows) x.v[k] = *reinterpret_cast<const uint4*>(src + at);
-            }
-#pragma unroll
             for (int k = 0; k < NV * 4; ++k)
-                m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x.w[k] << 16)), fabsf(__uint_as_float(x.w[k] & 0xffff0000u))));
+                m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[n].w[k] << 16)), fabsf(__uint_as_float(x[n].w[k] & 0xffff0000u))));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
             // An infinity in the row makes all of it NaN (e4m3 would hold it as 448).
@@ -367,7 +376,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 uint32_t piece[2] = {0, 0};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t w = x.w[2 * k + j];
+                    const uint32_t w = x[n].w[2 * k + j];
                     const float q0 = __uint_as_float(w << 16) * down + nan, q1 = __uint_as_float(w & 0xffff0000u) * down + nan;
                     const uint32_t c = float2_to_e4m3x2(q0, q1);
                     const float2 held = f16x2_to_float2(e4m3x2_to_f16x2(c));
@@ -611,17 +620,58 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     }
     __syncthreads();
 
-    // Join of the records, which stand in the line's order: those of one item follow one another.
+    // Join of the records, which stand in the line's order: those of one item follow one another. First each record's factor
+    // for a row, 2^(reference - largest), in its reference's place; the item's largest and sum go with its first record.
+    constexpr int RECS = 2 * AC_WARPS;
+    float* tops = stats + 2 * RECS * C::ROWS;  // [record][row]
+    float2 held[NT / 2 + 1];
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+        for (int i = 0; i * AC_THREADS < RECS * C::ROWS; ++i) {
+            const int at = i * AC_THREADS + tid, k = at / C::ROWS, row = at % C::ROWS;
+            if (at >= RECS * C::ROWS || rec[k].u0 < 0) continue;
+            float2* ml = reinterpret_cast<float2*>(stats) + row;
+            if (pass == 1) {
+                ml[k * C::ROWS] = held[i];
+                continue;
+            }
+            const long long u0 = rec[k].u0;
+            float top = AC_NONE;
+            bool lead = true;
+#pragma unroll
+            for (int j = 0; j < RECS; ++j)
+                if (rec[j].u0 == u0) {
+                    top = fmaxf(top, ml[j * C::ROWS].x);
+                    lead = lead && j >= k;
+                }
+            const float mk = ml[k * C::ROWS].x;
+            held[i] = make_float2(mk == top ? 1.0f : ac_ex2(mk - top), 0.0f);
+            if (lead) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < RECS; ++j)
+                    if (rec[j].u0 == u0) {
+                        const float2 v = ml[j * C::ROWS];
+                        sum += v.y * (v.x == top ? 1.0f : ac_ex2(v.x - top));
+                    }
+                tops[k * C::ROWS + row] = top;
+                held[i].y = sum;
+            }
+        }
+        __syncthreads();
+    }
     int shared_item[2] = {-1, -1};  // records of the items that other CTAs share: begun before this one, and here
-    for (int r0 = 0; r0 < 2 * AC_WARPS;) {
+    for (int r0 = 0; r0 < RECS;) {
         const AcRecord r = rec[r0];
         if (r.u0 < 0) {
             ++r0;
             continue;
         }
         int r1 = r0, tile1 = r.tile1;  // the item's last record
-        for (int k = r0 + 1; k < 2 * AC_WARPS; ++k)
-            if (rec[k].u0 == r.u0) {
+#pragma unroll
+        for (int k = 1; k < RECS; ++k)
+            if (k > r0 && rec[k].u0 == r.u0) {
                 r1 = k;
                 tile1 = rec[k].tile1;
             }
@@ -631,28 +681,24 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         float* part = a.parts + static_cast<long long>(cta * 2 + slot) * C::PART;
         for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
             const int row = i / (D / 4), c = i % (D / 4) * 2;
-            float top = AC_NONE;
-            for (int k = r0; k <= r1; ++k)
-                if (rec[k].u0 >= 0) top = fmaxf(top, stats[(k * C::ROWS + row) * 2]);
+            const float2 total_row = make_float2(tops[r0 * C::ROWS + row], stats[(r0 * C::ROWS + row) * 2 + 1]);
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float sum = 0.0f;
+#pragma unroll 4
             for (int k = r0; k <= r1; ++k) {
                 if (rec[k].u0 < 0) continue;
-                const float2 ml = *reinterpret_cast<const float2*>(stats + (k * C::ROWS + row) * 2);
-                const float f = ml.x == top ? 1.0f : ac_ex2(ml.x - top);
+                const float f = stats[(k * C::ROWS + row) * 2];
                 const float2* from = reinterpret_cast<const float2*>(smem + (k >> 1) * C::WARP + (k & 1 ? 0 : C::RING)) + row * (D / 2);
                 const float2 u = from[ac_join(c, row)], v = from[ac_join(c + 1, row)];
-                sum += ml.y * f;
                 x.x += u.x * f;
                 x.y += u.y * f;
                 x.z += v.x * f;
                 x.w += v.y * f;
             }
             if (whole) {
-                ac_store(a, r.q0, r.head, r.row0 + row, c * 2, D, x, top, sum);
+                ac_store(a, r.q0, r.head, r.row0 + row, c * 2, D, x, total_row.x, total_row.y);
             } else {
                 *reinterpret_cast<float4*>(part + row * D + c * 2) = x;
-                if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = make_float2(top, sum);
+                if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = total_row;
             }
         }
         r0 = r1 + 1;
@@ -680,49 +726,65 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const int c0 = cta_of(r.u0 + AC_ITEM), n_parts = cta_of(r.u0 + AC_ITEM + r.tiles - 1) - c0 + 1;
         // the first CTA began the item, the others found it begun
         auto part = [&](int k) { return a.parts + static_cast<long long>((c0 + k) * 2 + (k == 0 ? 1 : 0)) * C::PART; };
+        float2* totals = reinterpret_cast<float2*>(stats);                                // [row]
         float2* ml = reinterpret_cast<float2*>(smem);                                     // [part][row]
         float4* sums = reinterpret_cast<float4*>(smem + AC_WARPS * (C::WARP - C::HEAD));  // [warp][row][D / 4]
         for (int i = tid; i < n_parts * C::ROWS; i += AC_THREADS)
             if (i % C::ROWS < r.rows)
                 ml[i] = __ldcg(reinterpret_cast<const float2*>(part(i / C::ROWS) + C::ROWS * D) + i % C::ROWS);
         __syncthreads();
-        // A warp takes every eighth part.
-        for (int i = lane; i < r.rows * (D / 4); i += 32) {
-            const int row = i / (D / 4);
-            float top = AC_NONE;
-            for (int k = 0; k < n_parts; ++k) top = fmaxf(top, ml[k * C::ROWS + row].x);
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int k = warp; k < n_parts; k += AC_WARPS) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(part(k)) + i);
-                const float mk = ml[k * C::ROWS + row].x;
-                const float f = mk == top ? 1.0f : ac_ex2(mk - top);
-                x.x += v.x * f;
-                x.y += v.y * f;
-                x.z += v.z * f;
-                x.w += v.w * f;
+        // Factors of the parts in their references' place, the largest and the sum of each row: a warp a row.
+        for (int row = warp; row < r.rows; row += AC_WARPS) {
+            float top = AC_NONE, sum = 0.0f;
+            for (int k = lane; k < n_parts; k += 32) top = fmaxf(top, ml[k * C::ROWS + row].x);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            for (int k = lane; k < n_parts; k += 32) {
+                float2 v = ml[k * C::ROWS + row];
+                v.x = v.x == top ? 1.0f : ac_ex2(v.x - top);
+                sum += v.x * v.y;
+                ml[k * C::ROWS + row].x = v.x;
             }
-            sums[warp * (C::ROWS * D / 4) + i] = x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (lane == 0) totals[row] = make_float2(top, sum);
         }
         __syncthreads();
-        for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
-            const int row = i / (D / 4);
-            float top = AC_NONE, sum = 0.0f;
-            for (int k = 0; k < n_parts; ++k) top = fmaxf(top, ml[k * C::ROWS + row].x);
-            for (int k = 0; k < n_parts; ++k) {
-                const float2 v = ml[k * C::ROWS + row];
-                sum += v.y * (v.x == top ? 1.0f : ac_ex2(v.x - top));
+        // A warp takes every eighth part, its lanes four elements of each 128.
+        constexpr int E = C::ROWS * D / 128;
+        float4 x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+        for (int k = warp; k < n_parts; k += AC_WARPS) {
+            const float4* from = reinterpret_cast<const float4*>(part(k)) + lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int row = (e * 32 + lane) / (D / 4);
+                if (row >= r.rows) continue;
+                const float4 v = __ldcg(from + e * 32);
+                const float f = ml[k * C::ROWS + row].x;
+                x[e].x += v.x * f;
+                x[e].y += v.y * f;
+                x[e].z += v.z * f;
+                x[e].w += v.w * f;
             }
-            float4 x = sums[i];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[warp * (C::ROWS * D / 4) + e * 32 + lane] = x[e];
+        __syncthreads();
+        for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
+            float4 y = sums[i];
 #pragma unroll
             for (int w = 1; w < AC_WARPS; ++w) {
                 const float4 v = sums[w * (C::ROWS * D / 4) + i];
-                x.x += v.x;
-                x.y += v.y;
-                x.z += v.z;
-                x.w += v.w;
+                y.x += v.x;
+                y.y += v.y;
+                y.z += v.z;
+                y.w += v.w;
             }
-            ac_store(a, r.q0, r.head, r.row0 + row, i % (D / 4) * 4, D, x, top, sum);
+            const float2 all = totals[i / (D / 4)];
+            ac_store(a, r.q0, r.head, r.row0 + i / (D / 4), i % (D / 4) * 4, D, y, all.x, all.y);
         }
         __syncthreads();
     }
