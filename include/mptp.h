@@ -552,13 +552,11 @@ MP_API mp_status mp_kv_cache_read(const uint8_t* kc, const uint8_t* vc, const fl
  *   max_q: at least the longest sequence's queries. A sequence with rows outside [0, Tq], more than max_q queries or a
  *   length outside [0, max_pages * page] is left out and sets MP_DEV_SEQ_RANGE; a page outside the pool sets
  *   MP_DEV_PAGE_RANGE and gives the rows that would see it O = LSE = NaN. Rows of no sequence are not written.
- *   workspace: mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q) bytes (0 for sizes outside the rules), whose first
- *   MP_ATTN_CACHE_COUNTER_BYTES are zero before the first call; every call leaves them zero, so one workspace serves any number of
- *   calls, of any sizes it is large enough for, one after another. Calls that may overlap need one each.
+ *   workspace: mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q) bytes (0 for sizes outside the rules), whatever they
+ *   hold; calls that may overlap need one each.
  *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; max_q <= Tq; max_q * heads < 2^31 - 64; ldq, ldo at least a
  *   row and multiples of 8; the pool's as above; scale > 0 and finite.
  */
-#define MP_ATTN_CACHE_COUNTER_BYTES 4096
 MP_API size_t mp_attn_cache_workspace_bytes(int heads, int kv_heads, int d, int max_q);
 MP_API mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, const uint8_t* vc, const float* ks, const float* vs,
                             mp_bf16* O, float* LSE, const int32_t* page_table,

@@ -712,11 +712,6 @@ def mp_attn_cache_workspace_bytes(heads: int, kv_heads: int, d: int, max_q: int)
                                                    _i32(max_q, "max_q")))
 
 
-def mp_attn_cache_workspace(heads: int, kv_heads: int, d: int, max_q: int, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace for mp_attn_cache_fwd (every call leaves its counters zero)."""
-    return torch.zeros(mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q), dtype=torch.uint8, device=device)
-
-
 def mp_attn_cache_fwd(Q, kc, vc, ks, vs, O, LSE, page_table, cu_q, lens, workspace, *, max_q: int, causal: bool = True,
                       scale: float | None = None, d_status=None, stream=None) -> None:
     """Attention of the last tokens of each sequence over its e4m3 cache (mp_kv_cache_write): O [Tq, heads, d] and LSE

@@ -25,7 +25,8 @@
 // costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
 // walks its run alone, without a barrier: an item that lies within it is finished from registers. Runs that begin or
 // end inside an item leave a record in shared memory, joined once at the CTA's end; an item that several CTAs share leaves
-// a part of each in the workspace, and the CTA that comes last (a counter) adds them in order.
+// a part of each in the workspace, which a second kernel adds in order, a block a row (it starts while the first ends; the CTA that
+// comes last adding them alone took 6 us longer for one sequence's 76 parts, 3 us for three).
 #include "mptp_kv_cache.cuh"
 #include "mptp_launch.cuh"
 
@@ -43,14 +44,19 @@ constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference bef
 constexpr float AC_LOG2E = 1.4426950408889634f;
 constexpr float AC_LN2 = 0.6931471805599453f;
 
+// An item that a CTA began and others went on with: their number, its own among them (0: none).
+struct AcItem {
+    int parts, q0, row0, rows, head;
+};
+
 struct AcArgs {
     const __nv_bfloat16* Q;
     __nv_bfloat16* O;
     float* LSE;
     const int32_t* cu_q;
     const int32_t* lens;
-    uint32_t* counters;  // [AC_CTAS], zero between calls
-    float* parts;        // [2 AC_CTAS][rows][d + 2]
+    AcItem* items;  // [AC_CTAS]
+    float* parts;   // [2 AC_CTAS][rows][d + 2]
     long long ldq, ldo;
     int nseq, Tq, max_q, heads, group, causal;
     float scale_log2;
@@ -117,11 +123,10 @@ struct AcShape {
     static constexpr int HEAD = ROWS * D * 4;        // the record of the item that its run begins in
     static constexpr int WARP = RING + HEAD;
     static constexpr int SCALES = STAGES * 16;       // a warp's: two of K, two of V
-    static constexpr int STATS = 2 * ROWS * 12;      // a warp's: (reference, sum) of its records' rows, and the items' largest
+    static constexpr int STATS = 2 * ROWS * 8;       // a warp's: (reference, sum) of its records' rows
     static constexpr int SMEM = AC_WARPS * (WARP + SCALES + STATS);
     static constexpr int PART = ROWS * (D + 2);      // floats of a part
     static_assert(HEAD <= RING && SMEM <= 231424, "shared memory");
-    static_assert(AC_CTAS * ROWS * 8 + AC_WARPS * HEAD <= AC_WARPS * WARP, "the parts' statistics beside the warps' sums");
 };
 
 // What a warp leaves of an item that it has not done alone: tiles [tile0, tile1) of `tiles`, first at place u0.
@@ -130,6 +135,12 @@ struct AcRecord {
     int tile0, tile1, tiles;
     int q0, row0, rows, head;
 };
+
+// Where the c-th of n equal shares of the line begins; in 32 bits where they hold the product.
+__device__ __forceinline__ long long ac_share(long long total, int c, int n) {
+    const unsigned long long x = static_cast<unsigned long long>(total) * static_cast<unsigned>(c);
+    return x >> 32 ? static_cast<long long>(x / static_cast<unsigned>(n)) : static_cast<unsigned>(x) / static_cast<unsigned>(n);
+}
 
 // One sequence's place in the line of tiles.
 struct AcSeq {
@@ -178,7 +189,6 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     constexpr int CH = D / 16;   // 16-byte chunks a key row
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ AcRecord rec[2 * AC_WARPS];
-    __shared__ int sh_last[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     float* stats = reinterpret_cast<float*>(smem + AC_WARPS * (C::WARP + C::SCALES));  // [warp][2][row]{m, l}
     grid_dependency_wait();
@@ -187,58 +197,61 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     // The line's length, then the warp's run and the sequence that holds its first place: each warp by itself, lanes taking
     // AC_SEQS neighbouring sequences each (loads side by side, no barrier).
     auto places = [&](const AcSeq& q) { return static_cast<long long>(q.items) * (q.tiles + AC_ITEM); };
-    AcSeq first[AC_SEQS];
-    long long total = 0;
-    for (int base = 0; base < a.nseq; base += 32 * AC_SEQS)
+    AcSeq held[AC_SEQS];
+    long long mine = 0;  // places of the lane's sequences
+    auto look_at = [&](int base) {
+        mine = 0;
 #pragma unroll
-        for (int k = 0; k < AC_SEQS; ++k) {
-            const AcSeq q = ac_seq<C::ROWS>(a, p, base + lane * AC_SEQS + k);
-            if (base == 0) first[k] = q;
-            total += places(q);
-        }
+        for (int k = 0; k < AC_SEQS; ++k) held[k] = ac_seq<C::ROWS>(a, p, base + lane * AC_SEQS + k);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    // As many CTAs as have a few places for each of their warps.
-    const long long want = (total + 2 * AC_WARPS - 1) / (2 * AC_WARPS);
-    const int ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : static_cast<long long>(gridDim.x));
-    const int cta = blockIdx.x;
-    if (cta >= ctas) return;
-    if (lane < 2) rec[2 * warp + lane].u0 = -1;
-    const long long cta_pos = total * cta / ctas, cta_end = total * (cta + 1) / ctas;
-    long long pos = cta_pos + (cta_end - cta_pos) * warp / AC_WARPS;
-    const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / AC_WARPS;
-    int seq = 0;
-    long long seq_start = 0;
-    AcSeq s = first[0];
-    for (int base = 0; base < a.nseq; base += 32 * AC_SEQS) {
-        long long mine = 0;
-        if (base > 0)
-#pragma unroll
-            for (int k = 0; k < AC_SEQS; ++k) first[k] = ac_seq<C::ROWS>(a, p, base + lane * AC_SEQS + k);
-#pragma unroll
-        for (int k = 0; k < AC_SEQS; ++k) mine += places(first[k]);
+        for (int k = 0; k < AC_SEQS; ++k) mine += places(held[k]);
         long long upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += v;
         }
-        upto += seq_start;
+        return upto;
+    };
+    long long upto = look_at(0);
+    long long total = __shfl_sync(0xffffffffu, upto, 31);
+    if (a.nseq > 32 * AC_SEQS) {
+        for (int base = 32 * AC_SEQS; base < a.nseq; base += 32 * AC_SEQS)
+            total += __shfl_sync(0xffffffffu, look_at(base), 31);
+        upto = look_at(0);
+    }
+    // As many CTAs as have a few places for each of their warps.
+    const long long want = (total + 2 * AC_WARPS - 1) / (2 * AC_WARPS);
+    const int ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : static_cast<long long>(gridDim.x));
+    const int cta = blockIdx.x;
+    AcItem* left = a.items + cta;
+    if (tid == 0) left->parts = 0;
+    if (cta >= ctas) return;
+    if (lane < 2) rec[2 * warp + lane].u0 = -1;
+    const long long cta_pos = ac_share(total, cta, ctas), cta_end = ac_share(total, cta + 1, ctas);
+    long long pos = cta_pos + (cta_end - cta_pos) * warp / AC_WARPS;
+    const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / AC_WARPS;
+    int seq = 0;
+    long long seq_start = 0;
+    AcSeq s = held[0];
+    for (int base = 0; base < a.nseq;) {
         const unsigned here = __ballot_sync(0xffffffffu, pos < upto);
-        if (here == 0) {
+        if (here == 0) {  // pos lies before the line's end, so some step finds it
             seq_start = __shfl_sync(0xffffffffu, upto, 31);
+            base += 32 * AC_SEQS;
+            upto = look_at(base) + seq_start;
             continue;
         }
         // The lane that holds it walks its own sequences, then tells the others.
         const int who = __ffs(here) - 1;
         long long start = upto - mine;
         int k = 0;
-        s = first[0];
+        s = held[0];
 #pragma unroll
         for (int j = 1; j < AC_SEQS; ++j)
             if (k == j - 1 && pos >= start + places(s)) {
                 start += places(s);
-                s = first[j];
+                s = held[j];
                 k = j;
             }
         seq = base + who * AC_SEQS + __shfl_sync(0xffffffffu, k, who);
@@ -257,13 +270,15 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     const uint32_t ring_scales_u = smem_u32(ring_scales);
 
     while (pos < end) {
-        while (pos >= seq_start + static_cast<long long>(s.items) * (s.tiles + AC_ITEM)) {
-            seq_start += static_cast<long long>(s.items) * (s.tiles + AC_ITEM);
+        while (seq < a.nseq && pos >= seq_start + places(s)) {
+            seq_start += places(s);
             s = ac_seq<C::ROWS>(a, p, ++seq);
         }
+        if (seq >= a.nseq) break;
         const int span = s.tiles + AC_ITEM;
-        const int local = static_cast<int>((pos - seq_start) / span);
-        const int off0 = static_cast<int>((pos - seq_start) - static_cast<long long>(local) * span);
+        const long long ahead = pos - seq_start;
+        const int local = ahead <= 0x7fffffff ? static_cast<int>(ahead) / span : static_cast<int>(ahead / span);
+        const int off0 = static_cast<int>(ahead - static_cast<long long>(local) * span);
         const int take = static_cast<int>(min(static_cast<long long>(span - off0), end - pos));
         const int tile0 = max(off0 - AC_ITEM, 0), tile1 = off0 + take - AC_ITEM;
         pos += take;
@@ -273,21 +288,21 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const int rows = min(C::ROWS, s.nq * a.group - row0);
         const int32_t* table = p.table + static_cast<long long>(seq) * p.max_pages;
 
-        // Copies of tile k of this run into stage k % STAGES. Pages are looked up one tile earlier.
-        const int mine = tile1 - tile0;
+        // Copies of tile k of this run into stage k % STAGES. Pages are looked up one tile earlier, the first ones at once.
+        const int tiles = tile1 - tile0;
         const uint8_t* k_codes = p.head_codes(0, 0, head) + lane * 16;
         const uint8_t* v_codes = p.head_codes(1, 0, head) + lane * 16;
         int id[2];
-        auto look = [&](int k) {
+        auto look = [&](int k, int (&id)[2]) {
             const int key = (tile0 + k) * AC_TILE;
             id[0] = id[1] = -1;
-            if (k < mine) {
+            if (k < tiles) {
                 if (key < s.len) id[0] = __ldg(table + (key >> a.page_shift));
                 if (key + 16 < s.len) id[1] = __ldg(table + ((key + 16) >> a.page_shift));
             }
         };
-        auto issue = [&](int k) {
-            if (k < mine) {
+        auto issue = [&](int k, const int (&id)[2]) {
+            if (k < tiles) {
                 const int key0 = (tile0 + k) * AC_TILE;
                 const int st = k % C::STAGES;
                 const uint32_t dst = ring_u + st * C::STAGE;
@@ -330,7 +345,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             }
             ac_commit();
         };
-        look(0);
+        int ids[C::STAGES][2];
+#pragma unroll
+        for (int k = 0; k < C::STAGES; ++k) look(k, ids[k]);
         // Queries: lane (g, t) has row g of each eight, the elements that its bytes of a key row meet. Asked for before the
         // copies, used behind them.
         constexpr int NV = D / 32;  // 16-byte vectors of a lane
@@ -351,10 +368,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             }
         }
 #pragma unroll
-        for (int k = 0; k < C::STAGES - 1; ++k) {
-            issue(k);
-            look(k + 1);
-        }
+        for (int k = 0; k < C::STAGES - 1; ++k) issue(k, ids[k]);
+        id[0] = ids[C::STAGES - 1][0];
+        id[1] = ids[C::STAGES - 1][1];
 
         uint32_t qf[2][NT][KS];  // pieces q1, q2
         float fq[NT][2];         // factor from a product to a score in powers of two, for columns 2t, 2t + 1
@@ -407,11 +423,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < KS; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
         }
         float ref = 0.0f, inv_ref = 0.0f;  // largest value scale met
-        for (int k = 0; k < mine; ++k) {
+        for (int k = 0; k < tiles; ++k) {
             ac_wait<C::STAGES - 2>();
             __syncwarp();
-            issue(k + C::STAGES - 1);
-            look(k + C::STAGES);
+            issue(k + C::STAGES - 1, id);
+            look(k + C::STAGES, id);
             const int st = k % C::STAGES;
             const uint8_t* kt = ring + st * C::STAGE;
             const uint8_t* vt = kt + AC_TILE * D;
@@ -620,174 +636,107 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     }
     __syncthreads();
 
-    // Join of the records, which stand in the line's order: those of one item follow one another. First each record's factor
-    // for a row, 2^(reference - largest), in its reference's place; the item's largest and sum go with its first record.
+    // Join of the records, which stand in the line's order: those of one item follow one another.
     constexpr int RECS = 2 * AC_WARPS;
-    float* tops = stats + 2 * RECS * C::ROWS;  // [record][row]
-    float2 held[NT / 2 + 1];
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll
-        for (int i = 0; i * AC_THREADS < RECS * C::ROWS; ++i) {
-            const int at = i * AC_THREADS + tid, k = at / C::ROWS, row = at % C::ROWS;
-            if (at >= RECS * C::ROWS || rec[k].u0 < 0) continue;
-            float2* ml = reinterpret_cast<float2*>(stats) + row;
-            if (pass == 1) {
-                ml[k * C::ROWS] = held[i];
-                continue;
-            }
-            const long long u0 = rec[k].u0;
-            float top = AC_NONE;
-            bool lead = true;
-#pragma unroll
-            for (int j = 0; j < RECS; ++j)
-                if (rec[j].u0 == u0) {
-                    top = fmaxf(top, ml[j * C::ROWS].x);
-                    lead = lead && j >= k;
-                }
-            const float mk = ml[k * C::ROWS].x;
-            held[i] = make_float2(mk == top ? 1.0f : ac_ex2(mk - top), 0.0f);
-            if (lead) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < RECS; ++j)
-                    if (rec[j].u0 == u0) {
-                        const float2 v = ml[j * C::ROWS];
-                        sum += v.y * (v.x == top ? 1.0f : ac_ex2(v.x - top));
-                    }
-                tops[k * C::ROWS + row] = top;
-                held[i].y = sum;
-            }
-        }
-        __syncthreads();
-    }
-    int shared_item[2] = {-1, -1};  // records of the items that other CTAs share: begun before this one, and here
-    for (int r0 = 0; r0 < RECS;) {
+    const long long my_u0 = rec[lane % RECS].u0;
+    const unsigned mates = __match_any_sync(0xffffffffu, my_u0) & ((1u << RECS) - 1);
+    unsigned todo = __ballot_sync(0xffffffffu, my_u0 >= 0) & ((1u << RECS) - 1);
+    while (todo != 0) {
+        const int r0 = __ffs(todo) - 1;
+        const unsigned chain = __shfl_sync(0xffffffffu, mates, r0);
+        todo &= ~chain;
         const AcRecord r = rec[r0];
-        if (r.u0 < 0) {
-            ++r0;
-            continue;
-        }
-        int r1 = r0, tile1 = r.tile1;  // the item's last record
-#pragma unroll
-        for (int k = 1; k < RECS; ++k)
-            if (k > r0 && rec[k].u0 == r.u0) {
-                r1 = k;
-                tile1 = rec[k].tile1;
-            }
-        const bool whole = r.tile0 == 0 && tile1 == r.tiles;
-        const int slot = r.tile0 > 0 ? 0 : 1;
-        if (!whole) shared_item[slot] = r0;
-        float* part = a.parts + static_cast<long long>(cta * 2 + slot) * C::PART;
+        const bool whole = r.tile0 == 0 && rec[31 - __clz(chain)].tile1 == r.tiles;
+        const bool begun = r.tile0 > 0;  // in an earlier CTA
+        float* part = a.parts + static_cast<long long>(cta * 2 + (begun ? 0 : 1)) * C::PART;
         for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
             const int row = i / (D / 4), c = i % (D / 4) * 2;
-            const float2 total_row = make_float2(tops[r0 * C::ROWS + row], stats[(r0 * C::ROWS + row) * 2 + 1]);
+            float2 ml[RECS];
+            float top = AC_NONE, sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < RECS; ++k) {
+                ml[k] = *reinterpret_cast<const float2*>(stats + (k * C::ROWS + row) * 2);
+                if (chain >> k & 1) top = fmaxf(top, ml[k].x);
+            }
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int k = r0; k <= r1; ++k) {
-                if (rec[k].u0 < 0) continue;
-                const float f = stats[(k * C::ROWS + row) * 2];
+#pragma unroll
+            for (int k = 0; k < RECS; ++k) {
+                if (!(chain >> k & 1)) continue;
+                const float f = ml[k].x == top ? 1.0f : ac_ex2(ml[k].x - top);
                 const float2* from = reinterpret_cast<const float2*>(smem + (k >> 1) * C::WARP + (k & 1 ? 0 : C::RING)) + row * (D / 2);
                 const float2 u = from[ac_join(c, row)], v = from[ac_join(c + 1, row)];
+                sum += ml[k].y * f;
                 x.x += u.x * f;
                 x.y += u.y * f;
                 x.z += v.x * f;
                 x.w += v.y * f;
             }
             if (whole) {
-                ac_store(a, r.q0, r.head, r.row0 + row, c * 2, D, x, total_row.x, total_row.y);
+                ac_store(a, r.q0, r.head, r.row0 + row, c * 2, D, x, top, sum);
             } else {
                 *reinterpret_cast<float4*>(part + row * D + c * 2) = x;
-                if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = total_row;
+                if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = make_float2(top, sum);
             }
         }
-        r0 = r1 + 1;
+        if (!whole && !begun && tid == 0) {
+            // begun here: the CTAs up to that of its last tile have parts too
+            left->parts = static_cast<int>(((r.u0 + AC_ITEM + r.tiles) * ctas - 1) / total) - cta + 1;
+            left->q0 = r.q0;
+            left->row0 = r.row0;
+            left->rows = r.rows;
+            left->head = r.head;
+        }
     }
-    if (shared_item[0] < 0 && shared_item[1] < 0) return;
+}
 
-    // Parts of an item come from the CTAs of its first to its last tile: one counter each, at the first.
-    auto cta_of = [&](long long place) { return static_cast<int>(((place + 1) * ctas - 1) / total); };
-    __syncthreads();  // the parts are written
-    if (tid < 2) {
-        sh_last[tid] = 0;
-        if (shared_item[tid] >= 0) {
-            const AcRecord& r = rec[shared_item[tid]];
-            const int c0 = cta_of(r.u0 + AC_ITEM), c1 = cta_of(r.u0 + AC_ITEM + r.tiles - 1);
-            __threadfence();
-            // wraps to zero with the last one
-            sh_last[tid] = atomicInc(a.counters + c0, static_cast<unsigned>(c1 - c0)) == static_cast<unsigned>(c1 - c0);
-            __threadfence();
+// Adds the parts of the item that CTA blockIdx.x / ROWS of the kernel before began and did not finish, if there is one: a
+// block a row, four warps a quarter of the parts each.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) attn_cache_join_kernel(const AcArgs a) {
+    using C = AcShape<D, NT>;
+    __shared__ float4 red[4][D / 4];
+    __shared__ float red_sum[4];
+    const int cta = blockIdx.x / C::ROWS, row = blockIdx.x % C::ROWS, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const AcItem it = a.items[cta];
+    if (it.parts == 0 || row >= it.rows) return;
+    // the first CTA began the item, the others found it begun
+    auto part = [&](int k) { return a.parts + static_cast<long long>((cta + k) * 2 + (k == 0 ? 1 : 0)) * C::PART; };
+    auto stat = [&](int k) { return *reinterpret_cast<const float2*>(part(k) + C::ROWS * D + row * 2); };
+    float top = AC_NONE;
+    for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, stat(k).x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int k = warp; k < it.parts; k += 4) {
+        const float2 ml = stat(k);
+        const float f = ml.x == top ? 1.0f : ac_ex2(ml.x - top);
+        sum += ml.y * f;
+        if (lane < D / 4) {
+            const float4 v = *(reinterpret_cast<const float4*>(part(k) + row * D) + lane);
+            x.x += v.x * f;
+            x.y += v.y * f;
+            x.z += v.z * f;
+            x.w += v.w * f;
         }
     }
+    if (lane < D / 4) red[warp][lane] = x;
+    if (lane == 0) red_sum[warp] = sum;
     __syncthreads();
-    for (int which = 0; which < 2; ++which) {
-        if (!sh_last[which]) continue;
-        const AcRecord r = rec[shared_item[which]];
-        const int c0 = cta_of(r.u0 + AC_ITEM), n_parts = cta_of(r.u0 + AC_ITEM + r.tiles - 1) - c0 + 1;
-        // the first CTA began the item, the others found it begun
-        auto part = [&](int k) { return a.parts + static_cast<long long>((c0 + k) * 2 + (k == 0 ? 1 : 0)) * C::PART; };
-        float2* totals = reinterpret_cast<float2*>(stats);                                // [row]
-        float2* ml = reinterpret_cast<float2*>(smem);                                     // [part][row]
-        float4* sums = reinterpret_cast<float4*>(smem + AC_WARPS * (C::WARP - C::HEAD));  // [warp][row][D / 4]
-        for (int i = tid; i < n_parts * C::ROWS; i += AC_THREADS)
-            if (i % C::ROWS < r.rows)
-                ml[i] = __ldcg(reinterpret_cast<const float2*>(part(i / C::ROWS) + C::ROWS * D) + i % C::ROWS);
-        __syncthreads();
-        // Factors of the parts in their references' place, the largest and the sum of each row: a warp a row.
-        for (int row = warp; row < r.rows; row += AC_WARPS) {
-            float top = AC_NONE, sum = 0.0f;
-            for (int k = lane; k < n_parts; k += 32) top = fmaxf(top, ml[k * C::ROWS + row].x);
+    if (warp != 0 || lane >= D / 4) return;
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            for (int k = lane; k < n_parts; k += 32) {
-                float2 v = ml[k * C::ROWS + row];
-                v.x = v.x == top ? 1.0f : ac_ex2(v.x - top);
-                sum += v.x * v.y;
-                ml[k * C::ROWS + row].x = v.x;
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (lane == 0) totals[row] = make_float2(top, sum);
-        }
-        __syncthreads();
-        // A warp takes every eighth part, its lanes four elements of each 128.
-        constexpr int E = C::ROWS * D / 128;
-        float4 x[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-        for (int k = warp; k < n_parts; k += AC_WARPS) {
-            const float4* from = reinterpret_cast<const float4*>(part(k)) + lane;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int row = (e * 32 + lane) / (D / 4);
-                if (row >= r.rows) continue;
-                const float4 v = __ldcg(from + e * 32);
-                const float f = ml[k * C::ROWS + row].x;
-                x[e].x += v.x * f;
-                x[e].y += v.y * f;
-                x[e].z += v.z * f;
-                x[e].w += v.w * f;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) sums[warp * (C::ROWS * D / 4) + e * 32 + lane] = x[e];
-        __syncthreads();
-        for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
-            float4 y = sums[i];
-#pragma unroll
-            for (int w = 1; w < AC_WARPS; ++w) {
-                const float4 v = sums[w * (C::ROWS * D / 4) + i];
-                y.x += v.x;
-                y.y += v.y;
-                y.z += v.z;
-                y.w += v.w;
-            }
-            const float2 all = totals[i / (D / 4)];
-            ac_store(a, r.q0, r.head, r.row0 + i / (D / 4), i % (D / 4) * 4, D, y, all.x, all.y);
-        }
-        __syncthreads();
+    for (int w = 1; w < 4; ++w) {
+        const float4 v = red[w][lane];
+        x.x += v.x;
+        x.y += v.y;
+        x.z += v.z;
+        x.w += v.w;
+        sum += red_sum[w];
     }
+    ac_store(a, it.q0, it.head, it.row0 + row, lane * 4, D, x, top, sum);
 }
 
 template <int D, int NT>
@@ -796,8 +745,12 @@ static cudaError_t launch_attn_cache(const AcArgs& a, const KvPool& p, cudaStrea
     auto kernel = attn_cache_kernel<D, NT>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(AC_CTAS), dim3(AC_THREADS), C::SMEM, s, a, p);
+    const cudaError_t f = launch_pdl(kernel, dim3(AC_CTAS), dim3(AC_THREADS), C::SMEM, s, a, p);
+    if (f != cudaSuccess) return f;
+    return launch_pdl(attn_cache_join_kernel<D, NT>, dim3(AC_CTAS * C::ROWS), dim3(128), 0, s, a);
 }
+
+constexpr size_t AC_ITEM_BYTES = (AC_CTAS * sizeof(AcItem) + 15) / 16 * 16;
 
 // Row tiles of eight queries where no sequence has more of a key head, else of sixteen.
 static int ac_rows(int max_q, int group) { return static_cast<long long>(max_q) * group <= 8 ? 8 : 16; }
@@ -809,9 +762,8 @@ using namespace mptp;
 extern "C" size_t mp_attn_cache_workspace_bytes(int heads, int kv_heads, int d, int max_q) {
     if (heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || (d != 64 && d != 96 && d != 128) || max_q <= 0) return 0;
     const size_t part = static_cast<size_t>(ac_rows(max_q, heads / kv_heads)) * (d + 2) * sizeof(float);
-    return MP_ATTN_CACHE_COUNTER_BYTES + 2 * AC_CTAS * part;
+    return AC_ITEM_BYTES + 2 * AC_CTAS * part;
 }
-static_assert(AC_CTAS * sizeof(uint32_t) <= MP_ATTN_CACHE_COUNTER_BYTES, "counters");
 
 extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, const uint8_t* vc, const float* ks,
                                        const float* vs, mp_bf16* O, float* LSE, const int32_t* page_table,
@@ -863,8 +815,8 @@ extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, cons
     a.LSE = LSE;
     a.cu_q = cu_q;
     a.lens = lens;
-    a.counters = static_cast<uint32_t*>(workspace);
-    a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + MP_ATTN_CACHE_COUNTER_BYTES);
+    a.items = static_cast<AcItem*>(workspace);
+    a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + AC_ITEM_BYTES);
     a.ldq = ldq;
     a.ldo = ldo;
     a.nseq = nseq;

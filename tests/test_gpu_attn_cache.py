@@ -35,19 +35,23 @@ def _make(new, lens, heads, kv, d, page, seed, spread=2, q=1.0):
     return Q, codes, scales, table
 
 
+def _workspace(heads, kv, d, max_q):
+    """Full of NaN: nothing in it needs to be set before a call."""
+    return torch.full((mp().mp_attn_cache_workspace_bytes(heads, kv, d, max_q),), 0xff, dtype=torch.uint8, device="cuda")
+
+
 def _run(Q, codes, scales, table, new, lens, causal=True, scale=None, status=0, max_q=None, cu=None, ws=None):
     T, heads, d = Q.shape
     kv = codes.shape[2]
     c, s, st = codes.cuda(), scales.cuda(), status_tensor()
     mq = max(new) if max_q is None else max_q
-    ws = mp().mp_attn_cache_workspace(heads, kv, d, mq) if ws is None else ws
+    ws = _workspace(heads, kv, d, mq) if ws is None else ws
     O, LSE = _nan(T, heads, d), _nan(heads, T, dtype=torch.float32)
     mp().mp_attn_cache_fwd(Q.cuda(), c[:, 0], c[:, 1], s[:, 0], s[:, 1], O, LSE, table.cuda(),
                            (cu_of(new) if cu is None else cu).cuda(), ints(lens).cuda(), ws, max_q=mq, causal=causal,
                            scale=scale, d_status=st)
     torch.cuda.synchronize()
     assert int(st.item()) == status, int(st.item())
-    assert not ws[:4096].any()
     return O.cpu(), LSE.cpu()
 
 
@@ -114,8 +118,8 @@ def test_every_width_at_row_counts_around_a_tile(d, rows):
     _check(_run(*inp, new, lens), *inp, new, lens)
 
 
-def test_repeats_bit_for_bit_and_leaves_the_workspace_for_other_sizes():
-    ws = mp().mp_attn_cache_workspace(16, 1, 128, 4)
+def test_repeats_bit_for_bit_with_one_workspace_for_other_sizes():
+    ws = _workspace(16, 1, 128, 4)
     a = _make([1, 1], [3000, 900], 16, 2, 128, 64, 23300)
     b = _make([4], [6000], 12, 1, 64, 16, 23301)
     first = _run(*a, [1, 1], [3000, 900], ws=ws)
@@ -214,7 +218,7 @@ def test_strided_rows_contiguous_pools_and_replayed_graph():
            scales[:, 1].contiguous().cuda()]
     rows, out = torch.zeros(3, heads + 3, d, dtype=torch.bfloat16, device="cuda"), _nan(3, heads + 1, d)
     rows[:, 2:2 + heads] = Q.cuda()
-    LSE, ws = _nan(heads, 3, dtype=torch.float32), mp().mp_attn_cache_workspace(heads, kv, d, 1)
+    LSE, ws = _nan(heads, 3, dtype=torch.float32), _workspace(heads, kv, d, 1)
     args = (table.cuda(), cu_of(new).cuda(), ints(lens).cuda(), ws)
 
     def call(**kw):
@@ -248,7 +252,7 @@ def test_decoding_steps_agree_with_the_whole_prompt():
     codes, scales = pool(pages, kv, page, d, 24101, nan=True)
     c, s, td = codes.cuda(), scales.cuda(), table.cuda()
     w = (1 + 0.1 * torch.randn(2, d, generator=torch.Generator().manual_seed(3))).to(torch.bfloat16).cuda()
-    ws = mp().mp_attn_cache_workspace(heads, kv, d, 70)
+    ws = _workspace(heads, kv, d, 70)
     at = [0, 0]
     for k, new in enumerate([lens] + steps):
         T = sum(new)
