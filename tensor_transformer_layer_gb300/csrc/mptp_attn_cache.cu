@@ -39,6 +39,8 @@ constexpr int AC_ITEM = 4;      // places of an item besides its tiles
 constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
 #define AC_NONE __int_as_float(0xff800000)  // -inf: no key seen
 constexpr float AC_BIAS = 7.0f;    // exponent that P carries into halves
+constexpr int AC_JOIN_WARPS = 4;   // warps of a row of the join
+constexpr int AC_BATCH = 10;       // parts in flight in each
 constexpr int AC_SEQS = 4;         // sequences a lane looks at in one step
 constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference before sums are scaled down
 constexpr float AC_LOG2E = 1.4426950408889634f;
@@ -292,7 +294,6 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const int tiles = tile1 - tile0;
         const uint8_t* k_codes = p.head_codes(0, 0, head) + lane * 16;
         const uint8_t* v_codes = p.head_codes(1, 0, head) + lane * 16;
-        int id[2];
         auto look = [&](int k, int (&id)[2]) {
             const int key = (tile0 + k) * AC_TILE;
             id[0] = id[1] = -1;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 #pragma unroll
         for (int k = 0; k < C::STAGES; ++k) look(k, ids[k]);
         // Queries: lane (g, t) has row g of each eight, the elements that its bytes of a key row meet. Asked for before the
-        // copies, used behind them.
+        // copies.
         constexpr int NV = D / 32;  // 16-byte vectors of a lane
         union {
             uint4 v[NV];
@@ -369,8 +370,6 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         }
 #pragma unroll
         for (int k = 0; k < C::STAGES - 1; ++k) issue(k, ids[k]);
-        id[0] = ids[C::STAGES - 1][0];
-        id[1] = ids[C::STAGES - 1][1];
 
         uint32_t qf[2][NT][KS];  // pieces q1, q2
         float fq[NT][2];         // factor from a product to a score in powers of two, for columns 2t, 2t + 1
@@ -423,6 +422,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < KS; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
         }
         float ref = 0.0f, inv_ref = 0.0f;  // largest value scale met
+        int id[2] = {ids[C::STAGES - 1][0], ids[C::STAGES - 1][1]};
         for (int k = 0; k < tiles; ++k) {
             ac_wait<C::STAGES - 2>();
             __syncwarp();
@@ -690,12 +690,12 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 }
 
 // Adds the parts of the item that CTA blockIdx.x / ROWS of the kernel before began and did not finish, if there is one: a
-// block a row, four warps a quarter of the parts each.
+// block a row, each warp a quarter of the parts, AC_BATCH of them asked for at once.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) attn_cache_join_kernel(const AcArgs a) {
+__global__ void __launch_bounds__(AC_JOIN_WARPS * 32) attn_cache_join_kernel(const AcArgs a) {
     using C = AcShape<D, NT>;
-    __shared__ float4 red[4][D / 4];
-    __shared__ float red_sum[4];
+    __shared__ float4 red[AC_JOIN_WARPS][D / 4];
+    __shared__ float red_sum[AC_JOIN_WARPS];
     const int cta = blockIdx.x / C::ROWS, row = blockIdx.x % C::ROWS, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -706,29 +706,42 @@ __global__ void __launch_bounds__(128) attn_cache_join_kernel(const AcArgs a) {
     auto stat = [&](int k) { return *reinterpret_cast<const float2*>(part(k) + C::ROWS * D + row * 2); };
     float top = AC_NONE;
     for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, stat(k).x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sum = 0.0f;
-#pragma unroll 8
-    for (int k = warp; k < it.parts; k += 4) {
-        const float2 ml = stat(k);
-        const float f = ml.x == top ? 1.0f : ac_ex2(ml.x - top);
-        sum += ml.y * f;
-        if (lane < D / 4) {
-            const float4 v = *(reinterpret_cast<const float4*>(part(k) + row * D) + lane);
-            x.x += v.x * f;
-            x.y += v.y * f;
-            x.z += v.z * f;
-            x.w += v.w * f;
+    for (int k0 = warp; k0 < it.parts; k0 += AC_JOIN_WARPS * AC_BATCH) {
+        float2 ml[AC_BATCH];
+        float4 v[AC_BATCH];
+#pragma unroll
+        for (int j = 0; j < AC_BATCH; ++j) {
+            const int k = k0 + j * AC_JOIN_WARPS;
+            ml[j] = make_float2(AC_NONE, 0.0f);
+            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k >= it.parts) continue;
+            ml[j] = stat(k);
+            if (lane < D / 4) v[j] = *(reinterpret_cast<const float4*>(part(k) + row * D) + lane);
+        }
+        if (k0 == warp)
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+#pragma unroll
+        for (int j = 0; j < AC_BATCH; ++j) {
+            if (k0 + j * AC_JOIN_WARPS >= it.parts) continue;
+            const float f = ml[j].x == top ? 1.0f : ac_ex2(ml[j].x - top);
+            sum += ml[j].y * f;
+            x.x += v[j].x * f;
+            x.y += v[j].y * f;
+            x.z += v[j].z * f;
+            x.w += v[j].w * f;
         }
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     if (lane < D / 4) red[warp][lane] = x;
     if (lane == 0) red_sum[warp] = sum;
     __syncthreads();
     if (warp != 0 || lane >= D / 4) return;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
+    for (int w = 1; w < AC_JOIN_WARPS; ++w) {
         const float4 v = red[w][lane];
         x.x += v.x;
         x.y += v.y;
@@ -747,7 +760,7 @@ static cudaError_t launch_attn_cache(const AcArgs& a, const KvPool& p, cudaStrea
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_pdl(kernel, dim3(AC_CTAS), dim3(AC_THREADS), C::SMEM, s, a, p);
     if (f != cudaSuccess) return f;
-    return launch_pdl(attn_cache_join_kernel<D, NT>, dim3(AC_CTAS * C::ROWS), dim3(128), 0, s, a);
+    return launch_pdl(attn_cache_join_kernel<D, NT>, dim3(AC_CTAS * C::ROWS), dim3(AC_JOIN_WARPS * 32), 0, s, a);
 }
 
 constexpr size_t AC_ITEM_BYTES = (AC_CTAS * sizeof(AcItem) + 15) / 16 * 16;
