@@ -308,6 +308,8 @@ def _ws(workspace):
 
 
 def _cuda_ws(workspace):
+    if type(workspace) is torch.Tensor and workspace.is_cuda and workspace.is_contiguous():
+        return workspace.data_ptr() or None, workspace.nbytes
     if isinstance(workspace, torch.Tensor) and workspace.numel() > 0 and not workspace.is_cuda:
         raise ValueError("workspace must be a CUDA tensor")
     return _ws(workspace)
@@ -634,11 +636,6 @@ def mp_qk_norm_rope_bwd(x, dy, dx, wq, wk, dwq, dwk, pos, workspace, *, q_heads:
 
 def _page_view(t, name, dtype, size, inner):
     """Pointer and page pitch of a tensor [pages, ...] of this size whose pages are contiguous (strides `inner`)."""
-    # What a right call passes, in as few steps as it takes; everything else is told apart below.
-    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == size and t.is_cuda:
-        pitch, *rest = t.stride()
-        if rest == inner and size[0] > 1:
-            return t.data_ptr(), pitch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -652,28 +649,46 @@ def _page_view(t, name, dtype, size, inner):
     return t.data_ptr() or None, t.stride(0) if size[0] > 1 else size[1] * inner[0]
 
 
+_F8, _F32 = torch.float8_e4m3fn, torch.float32
+
+
 def _pool(kc, vc, ks, vs, page_table, nseq):
     """Pointers and pitches of a cache's pool (codes [pages, kv_heads, page, d] e4m3, scales [pages, kv_heads] fp32), the
     pointer of its table [nseq, max_pages] int32, and (pages, max_pages, page, kv_heads, d)."""
     if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
         raise ValueError("kc must be a [pages, kv_heads, page, d] tensor")
-    size = pages, kv, page, d = kc.shape
-    f8, f32, inner, scales = torch.float8_e4m3fn, torch.float32, [page * d, d, 1], (pages, kv)
-    psk, ldsk = _page_view(ks, "ks", f32, scales, [1])
-    psv, ldsv = _page_view(vs, "vs", f32, scales, [1])
-    pk, ldk = _page_view(kc, "kc", f8, size, inner)
-    pv, ldv = _page_view(vc, "vc", f8, size, inner)
+    size = kc.shape
+    pages, kv, page, d = size
+    run = page * d
+    # What a right call passes, in as few steps as it takes; everything else is told apart below.
+    if type(kc) is type(vc) is type(ks) is type(vs) is torch.Tensor and kc.dtype is _F8 and vc.dtype is _F8 and \
+            ks.dtype is _F32 and vs.dtype is _F32 and vc.shape == size and ks.shape == vs.shape == (pages, kv) and \
+            kc.is_cuda and vc.is_cuda and ks.is_cuda and vs.is_cuda and pages > 1:
+        a, b, c, e = kc.stride()
+        (f, g), (h, i) = ks.stride(), vs.stride()
+        ldv = vc.stride(0)
+        if b == run and c == d and e == 1 and g == 1 and i == 1 and vc.stride() == (ldv, run, d, 1):
+            pool, pitches = (kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()), (a, ldv, f, h)
+            return pool, pitches, _page_table(page_table, nseq), (pages, page_table.shape[1], page, kv, d)
+    psk, ldsk = _page_view(ks, "ks", _F32, (pages, kv), [1])
+    psv, ldsv = _page_view(vs, "vs", _F32, (pages, kv), [1])
+    pk, ldk = _page_view(kc, "kc", _F8, size, [run, d, 1])
+    pv, ldv = _page_view(vc, "vc", _F8, size, [run, d, 1])
+    pt = _page_table(page_table, nseq)
+    return (pk, pv, psk, psv), (ldk, ldv, ldsk, ldsv), pt, (pages, page_table.shape[1], page, kv, d)
+
+
+def _page_table(page_table, nseq):
     pt = _ptr(page_table, "page_table", torch.int32)
     if page_table.dim() != 2 or page_table.shape[0] != nseq:
         raise ValueError(f"page_table must have shape [{nseq}, max_pages], got {tuple(page_table.shape)}")
-    return (pk, pv, psk, psv), (ldk, ldv, ldsk, ldsv), pt, (pages, page_table.shape[1], page, kv, d)
+    return pt
 
 
 def _sequences(cu, name):
     if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError(f"{name} must be a tensor with at least one entry")
-    nseq = cu.shape[0] - 1
-    return nseq, _ptr(cu, name, torch.int32, (nseq + 1,))
+    return cu.shape[0] - 1, _ptr(cu, name, torch.int32)
 
 
 def _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, max_n):

@@ -6,12 +6,17 @@
 //             dx = r (w * g - n mean(w * g * n))
 // r is computed again from x, which the backward pass reads anyway: nothing is kept between the two.
 //
-// Bound by memory: x once in and y once out; backward x and dy in and dx out. A warp takes a token (or a share of its
-// heads where tokens are few): a head lies across G = d / (2 VEC) lanes, VEC rotated pairs in each, or as many
-// unrotated elements (cosine 1, sine 0), so that the sums of squares are a few shuffles within the G lanes and the
-// angles' sines are computed once for all heads of the token. All of it is fp32 in registers; each output is rounded once.
-// The weights' gradients: a lane keeps its columns' sums in registers over all its tokens, a block adds its lanes' in
-// shared memory and writes one row of the workspace, a second kernel adds the rows: fixed order, no atomics.
+// Bound by memory: x once in and y once out; backward x and dy in and dx out. A head lies across G = d / (2 VEC) lanes, VEC
+// rotated pairs in each, or as many unrotated elements (cosine 1, sine 0), so that the sums of squares are a few shuffles
+// within the G lanes. A warp walks tokens (or a share of a token's heads where tokens are few), as many heads at once as
+// it has lanes for, with the next steps' loads in flight: the angles' sines are computed once a token, and with the weight they
+// make two coefficients an element, y = r (x P + partner Q). All of it is fp32, two elements an instruction, and each
+// output is rounded once.
+// The weights' gradients: a warp of the backward pass walks query heads or key heads, its lanes keep their columns' sums in
+// registers over all its tokens, a block adds its lanes' in shared memory and writes one row of the workspace, a second
+// kernel adds the rows: fixed order, no atomics.
+#include <type_traits>
+
 #include "mptp_internal.h"
 #include "mptp_launch.cuh"
 #include "mptp_ptx.cuh"
@@ -19,10 +24,11 @@
 
 namespace mptp {
 
-constexpr int QKN_WARPS = 8;
-constexpr int QKN_UNROLL = 4;        // forward: heads in flight per lane
-constexpr int QKN_BWD_UNROLL = 2;    // backward: two vectors more of each
-constexpr int QKN_BWD_BLOCKS = 304;  // two blocks on each of 152 SMs: the rows of the workspace
+constexpr int QKN_WARPS = 4;         // warps of a block
+constexpr int QKN_PER_SM = 5;        // forward: blocks on an SM
+constexpr int QKN_UNROLL = 2;        // and a warp's steps whose loads are in flight together
+constexpr int QKN_BWD_PER_SM = 3;
+constexpr int QKN_BWD_BLOCKS = QKN_BWD_PER_SM * 152;  // backward: rows of the workspace at most
 
 struct QkNormArgs {
     const __nv_bfloat16* x;
@@ -31,9 +37,12 @@ struct QkNormArgs {
     const __nv_bfloat16* wq;
     const __nv_bfloat16* wk;
     const int32_t* pos;  // [axes][T]
-    float* sums;         // [blocks][2][d]
+    float* sums;         // [blocks][d]
     long long ldx, ldy, lddy;
-    int T, heads, q_heads, d, pairs, shares;
+    int T, heads, q_heads, d, pairs;
+    int shares;    // log2 of the warps that share a token; backward: of query heads,
+    int k_shares;  // and of key heads,
+    int q_blocks;  // and the blocks that walk query heads, the others key heads
     float eps, inv_d;
 };
 
@@ -55,58 +64,70 @@ struct QkLane {
     }
 };
 
-// Sum over the `groups` lanes of a head, in all of them; every lane of the warp takes part.
-template <int N>
+// Sum over the `groups` lanes of a head, in all of them (POW2: they are a power of two); every lane of the warp takes part.
+template <bool POW2, int N>
 __device__ __forceinline__ void qk_head_sum(float (&v)[N], int groups, int g, int lane) {
-    if ((groups & (groups - 1)) == 0) {
-        for (int off = groups >> 1; off > 0; off >>= 1)
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-        return;
-    }
-    for (int off = 1; off < groups; off <<= 1)
+    for (int off = 1; off < 32; off <<= 1) {
+        if (off >= groups) break;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const float o = __shfl_down_sync(0xffffffffu, v[k], off);
-            if (g + off < groups) v[k] += o;
+            if constexpr (POW2) {
+                v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+            } else {
+                const float o = __shfl_down_sync(0xffffffffu, v[k], off);
+                if (g + off < groups) v[k] += o;
+            }
         }
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], lane - g);
-}
-
-template <int VEC>
-__device__ __forceinline__ void qk_unpack(const uint32_t (&u)[VEC / 2], const uint32_t (&v)[VEC / 2],
-                                          float (&f)[2 * VEC]) {
-#pragma unroll
-    for (int j = 0; j < VEC / 2; ++j) {
-        f[2 * j] = rope_lo(u[j]);
-        f[2 * j + 1] = rope_hi(u[j]);
-        f[VEC + 2 * j] = rope_lo(v[j]);
-        f[VEC + 2 * j + 1] = rope_hi(v[j]);
     }
-}
-
-// The pairs of a lane turned by the angles of (c, s).
-template <int VEC, bool INTER>
-__device__ __forceinline__ void qk_turn(float (&f)[2 * VEC], const float (&c)[VEC], const float (&s)[VEC]) {
+    if constexpr (!POW2)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : j + VEC;
-        const float a = f[ia], b = f[ib];
-        f[ia] = a * c[j] - b * s[j];
-        f[ib] = b * c[j] + a * s[j];
-    }
+        for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], lane - g);
 }
 
+// A lane's 2 VEC elements of one head as loaded: VEC words, the first vector's, then the second's.
 template <int VEC>
-union QkVec {
-    typename RopeVec<VEC>::T v;
-    uint32_t w[VEC / 2];
+union QkRaw {
+    typename RopeVec<VEC>::T v[2];
+    uint32_t w[VEC];
 };
-
 template <int VEC, bool INTER>
-__device__ __forceinline__ void qk_angles(const RopeTable& tab, const QkNormArgs& a, const QkLane<VEC, INTER>& L,
-                                          int token, int sign, float (&c)[VEC], float (&s)[VEC]) {
+__device__ __forceinline__ void qk_load(QkRaw<VEC>& x, const __nv_bfloat16* head, const QkLane<VEC, INTER>& L) {
+    using V = typename RopeVec<VEC>::T;
+    x.v[0] = *reinterpret_cast<const V*>(head + L.o0);
+    x.v[1] = *reinterpret_cast<const V*>(head + L.o1);
+}
+template <int VEC, bool INTER>
+__device__ __forceinline__ void qk_store(const float2 (&f)[VEC], __nv_bfloat16* head, const QkLane<VEC, INTER>& L) {
+    using V = typename RopeVec<VEC>::T;
+    QkRaw<VEC> x;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) x.w[k] = rope_pack(f[k].x, f[k].y);
+    *reinterpret_cast<V*>(head + L.o0) = x.v[0];
+    *reinterpret_cast<V*>(head + L.o1) = x.v[1];
+}
+template <int VEC>
+__device__ __forceinline__ void qk_floats(const QkRaw<VEC>& x, float2 (&f)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) f[k] = make_float2(rope_lo(x.w[k]), rope_hi(x.w[k]));
+}
+
+// f[k] P[k] + partner Q[k]: an element's partner is the other one of its pair.
+template <int VEC, bool INTER>
+__device__ __forceinline__ void qk_turn(const float2 (&f)[VEC], const float2 (&P)[VEC], const float2 (&Q)[VEC],
+                                        float2 (&out)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        const float2 partner = INTER ? make_float2(f[k].y, f[k].x) : f[(k + VEC / 2) % VEC];
+        out[k] = fma2(f[k], P[k], mul2(partner, Q[k]));
+    }
+}
+
+// Cosines and sines of a lane's pairs (sign -1: of the rotation back). `at`: the token's position on the axis of all its
+// pairs, where `one_axis`. sin.approx and cos.approx stay within 2^-21 on [-pi, pi], far below a bf16 step.
+template <int VEC, bool INTER>
+__device__ __forceinline__ void qk_angles(const RopeTable& tab, const QkNormArgs& a, const QkLane<VEC, INTER>& L, int token,
+                                          int at, bool one_axis, int sign, float (&c)[VEC], float (&s)[VEC]) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
         c[j] = 1.0f;
@@ -116,234 +137,293 @@ __device__ __forceinline__ void qk_angles(const RopeTable& tab, const QkNormArgs
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
         const int i = L.g * VEC + j;
-        const long long p = a.pos[static_cast<long long>(tab.axis[i]) * a.T + token];
-        rope_sincos(tab, i, p * sign, &s[j], &c[j]);
+        const long long p = one_axis ? at : a.pos[static_cast<long long>(tab.axis[i]) * a.T + token];
+        const float half_turns = rope_half_turns(tab, i, p * sign);
+        __sincosf(half_turns * 3.14159265358979f, &s[j], &c[j]);
     }
 }
 
-// A lane's elements of a weight, packed; zeros where the call has none of its heads.
+// Coefficients of qk_turn for elements weighted by w (null: by one).
 template <int VEC, bool INTER>
-__device__ __forceinline__ void qk_weight(const __nv_bfloat16* w, const QkLane<VEC, INTER>& L, QkVec<VEC>& u, QkVec<VEC>& v) {
-    using V = typename RopeVec<VEC>::T;
-    u.v = V{};
-    v.v = V{};
-    if (w != nullptr) {
-        u.v = *reinterpret_cast<const V*>(w + L.o0);
-        v.v = *reinterpret_cast<const V*>(w + L.o1);
+__device__ __forceinline__ void qk_coefficients(const float (&c)[VEC], const float (&s)[VEC], const float2* w,
+                                                float2 (&P)[VEC], float2 (&Q)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        if constexpr (INTER) {
+            P[k] = make_float2(c[k], c[k]);
+            Q[k] = make_float2(-s[k], s[k]);
+        } else {
+            const int j = 2 * k % VEC;
+            P[k] = make_float2(c[j], c[j + 1]);
+            Q[k] = k < VEC / 2 ? make_float2(-s[j], -s[j + 1]) : make_float2(s[j], s[j + 1]);
+        }
+        if (w != nullptr) {
+            P[k] = mul2(P[k], w[k]);
+            Q[k] = mul2(Q[k], INTER ? make_float2(w[k].y, w[k].x) : w[(k + VEC / 2) % VEC]);
+        }
     }
 }
 
+// A lane's elements of a weight; zeros where the call has none of its heads.
 template <int VEC, bool INTER>
-__global__ void __launch_bounds__(QKN_WARPS * 32) qk_norm_kernel(const __grid_constant__ RopeTable tab,
-                                                                 const QkNormArgs a) {
-    using V = typename RopeVec<VEC>::T;
+__device__ __forceinline__ void qk_weight(const __nv_bfloat16* w, const QkLane<VEC, INTER>& L, QkRaw<VEC>& x) {
+    x = QkRaw<VEC>{};
+    if (w != nullptr) qk_load(x, w, L);
+}
+
+// Whether each lane's pairs lie on one axis.
+template <int VEC, bool INTER>
+__device__ __forceinline__ bool qk_one_axis(const RopeTable& tab, const QkLane<VEC, INTER>& L) {
+    return __all_sync(0xffffffffu, !L.turns || tab.axis[L.g * VEC] == tab.axis[L.g * VEC + VEC - 1]);
+}
+
+// One kind's heads (queries' or keys') of a token, or a share of them, a warp.
+template <int VEC, bool INTER, bool POW2>
+__global__ void __launch_bounds__(QKN_WARPS * 32, QKN_PER_SM) qk_norm_kernel(const __grid_constant__ RopeTable tab,
+                                                                             const QkNormArgs a) {
+    constexpr int U = QKN_UNROLL;
     const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * QKN_WARPS + (threadIdx.x >> 5);
-    const int token = static_cast<int>(w / a.shares);
-    const int share = static_cast<int>(w % a.shares);
     const QkLane<VEC, INTER> L(a.d, a.pairs, lane);
+    const bool keys = blockIdx.x >= static_cast<unsigned>(a.q_blocks);
+    const unsigned block = keys ? blockIdx.x - a.q_blocks : blockIdx.x;
+    const int shares = keys ? a.k_shares : a.shares;
+    const unsigned item = block * QKN_WARPS + (threadIdx.x >> 5);
+    const int token = static_cast<int>(item >> shares);
+    const bool one_axis = qk_one_axis(tab, L);
+    const int axis = L.turns ? tab.axis[L.g * VEC] : 0;
     grid_dependency_wait();
     grid_launch_dependents();
     if (token >= a.T) return;
-    const __nv_bfloat16* xr = a.x + token * a.ldx;
-    __nv_bfloat16* yr = a.y + token * a.ldy;
-    QkVec<VEC> wq[2], wk[2];
-    qk_weight(a.wq, L, wq[0], wq[1]);
-    qk_weight(a.wk, L, wk[0], wk[1]);
-    float c[VEC], s[VEC];
-    qk_angles(tab, a, L, token, 1, c, s);
-    const int step = L.per_warp * a.shares;
-    for (int base = share * L.per_warp; base < a.heads; base += QKN_UNROLL * step) {
-        QkVec<VEC> u[QKN_UNROLL], v[QKN_UNROLL];
-        float ss[QKN_UNROLL];
+    const int h1 = keys ? a.heads : a.q_heads;
+    const int wide = L.per_warp << shares;  // heads of a step, all shares'
+    // The lane's first head; behind the last one it reads that one again and writes nothing.
+    int h = (keys ? a.q_heads : 0) + static_cast<int>(item & ((1u << shares) - 1)) * L.per_warp;
+    const int last = h1 - 1 - (L.live ? L.sub : 0);
+    const __nv_bfloat16* x = a.x + token * a.ldx + (L.live ? L.sub : 0) * a.d;
+    __nv_bfloat16* y = a.y + token * a.ldy + L.sub * a.d;
+    QkRaw<VEC> raw[U], wr;
+    auto load = [&](int h) {
 #pragma unroll
-        for (int k = 0; k < QKN_UNROLL; ++k) {
-            const int hd = base + L.sub + k * step;
-            u[k].v = V{};
-            v[k].v = V{};
-            if (L.live && hd < a.heads) {
-                u[k].v = *reinterpret_cast<const V*>(xr + hd * a.d + L.o0);
-                v[k].v = *reinterpret_cast<const V*>(xr + hd * a.d + L.o1);
-            }
+        for (int k = 0; k < U; ++k) qk_load(raw[k], x + min(h + k * wide, last) * a.d, L);
+    };
+    load(h);
+    const int at = a.pos[static_cast<long long>(axis) * a.T + token];
+    qk_weight(keys ? a.wk : a.wq, L, wr);
+    float2 P[VEC], Q[VEC];
+    {
+        float c[VEC], s[VEC];
+        float2 w[VEC];
+        qk_angles(tab, a, L, token, at, one_axis, 1, c, s);
+        qk_floats(wr, w);
+        qk_coefficients<VEC, INTER>(c, s, w, P, Q);
+    }
+    for (;;) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            float2 f[VEC], out[VEC], ss = make_float2(0.0f, 0.0f);
+            qk_floats(raw[k], f);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) ss = fma2(f[j], f[j], ss);
+            float sum[1] = {ss.x + ss.y};
+            qk_head_sum<POW2>(sum, L.groups, L.g, lane);
+            const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
+            qk_turn<VEC, INTER>(f, P, Q, out);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) out[j] = mul2(out[j], make_float2(r, r));
+            if (L.live && h + k * wide <= last) qk_store(out, y + (h + k * wide) * a.d, L);
         }
-#pragma unroll
-        for (int k = 0; k < QKN_UNROLL; ++k) {
-            float f[2 * VEC];
-            qk_unpack<VEC>(u[k].w, v[k].w, f);
-            ss[k] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 2 * VEC; ++j) ss[k] += f[j] * f[j];
-        }
-        qk_head_sum(ss, L.groups, L.g, lane);
-#pragma unroll
-        for (int k = 0; k < QKN_UNROLL; ++k) {
-            const int hd = base + L.sub + k * step;
-            const bool q = hd < a.q_heads;
-            const float r = rsqrtf(ss[k] * a.inv_d + a.eps);
-            float f[2 * VEC], wf[2 * VEC];
-            QkVec<VEC> w0, w1;
-#pragma unroll
-            for (int j = 0; j < VEC / 2; ++j) {
-                w0.w[j] = q ? wq[0].w[j] : wk[0].w[j];
-                w1.w[j] = q ? wq[1].w[j] : wk[1].w[j];
-            }
-            qk_unpack<VEC>(u[k].w, v[k].w, f);
-            qk_unpack<VEC>(w0.w, w1.w, wf);
-#pragma unroll
-            for (int j = 0; j < 2 * VEC; ++j) f[j] = f[j] * r * wf[j];
-            qk_turn<VEC, INTER>(f, c, s);
-            if (L.live && hd < a.heads) {
-#pragma unroll
-                for (int j = 0; j < VEC / 2; ++j) {
-                    u[k].w[j] = rope_pack(f[2 * j], f[2 * j + 1]);
-                    v[k].w[j] = rope_pack(f[VEC + 2 * j], f[VEC + 2 * j + 1]);
-                }
-                *reinterpret_cast<V*>(yr + hd * a.d + L.o0) = u[k].v;
-                *reinterpret_cast<V*>(yr + hd * a.d + L.o1) = v[k].v;
-            }
-        }
+        h += U * wide;
+        if (h > h1 - 1) break;
+        load(h);
     }
 }
 
-template <int VEC, bool INTER>
-__global__ void __launch_bounds__(QKN_WARPS * 32, 2) qk_norm_bwd_kernel(const __grid_constant__ RopeTable tab,
-                                                                        const QkNormArgs a) {
-    using V = typename RopeVec<VEC>::T;
-    constexpr int U = QKN_BWD_UNROLL;
-    // [warp, sub][queries', keys'][d]: 32 lanes of 2 VEC columns a warp and kind
-    __shared__ float red[QKN_WARPS * 32 * 2 * VEC * 2];
+template <int VEC, bool INTER, bool POW2>
+__global__ void __launch_bounds__(QKN_WARPS * 32, QKN_BWD_PER_SM) qk_norm_bwd_kernel(
+    const __grid_constant__ RopeTable tab, const QkNormArgs a) {
+    __shared__ float red[QKN_WARPS * 32 * 2 * VEC];  // [warp, sub][d]: 32 lanes of 2 VEC columns a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const QkLane<VEC, INTER> L(a.d, a.pairs, lane);
+    const bool one_axis = qk_one_axis(tab, L);
+    const int axis = L.turns ? tab.axis[L.g * VEC] : 0;
     grid_dependency_wait();
     grid_launch_dependents();
-    QkVec<VEC> wq[2], wk[2];
-    qk_weight(a.wq, L, wq[0], wq[1]);
-    qk_weight(a.wk, L, wk[0], wk[1]);
-    float aq[2 * VEC], ak[2 * VEC];
+    // Query heads or key heads, by the block.
+    const bool keys = static_cast<int>(blockIdx.x) >= a.q_blocks;
+    const int block = keys ? blockIdx.x - a.q_blocks : blockIdx.x;
+    const int h1 = keys ? a.heads : a.q_heads;
+    const int shares = keys ? a.k_shares : a.shares;
+    QkRaw<VEC> wr;
+    qk_weight(keys ? a.wk : a.wq, L, wr);
+    float2 w[VEC], acc[VEC], P[VEC], Q[VEC];
+    qk_floats(wr, w);
 #pragma unroll
-    for (int j = 0; j < 2 * VEC; ++j) aq[j] = ak[j] = 0.0f;
-    const long long items = static_cast<long long>(a.T) * a.shares;
-    for (long long w = static_cast<long long>(blockIdx.x) * QKN_WARPS + warp; w < items;
-         w += static_cast<long long>(gridDim.x) * QKN_WARPS) {
-        const int token = static_cast<int>(w / a.shares);
-        const int share = static_cast<int>(w % a.shares);
-        const __nv_bfloat16* xr = a.x + token * a.ldx;
-        const __nv_bfloat16* gr = a.dy + token * a.lddy;
-        __nv_bfloat16* dr = a.y + token * a.ldy;
-        float c[VEC], s[VEC];
-        qk_angles(tab, a, L, token, -1, c, s);
-        const int step = L.per_warp * a.shares;
-        for (int base = share * L.per_warp; base < a.heads; base += U * step) {
-            QkVec<VEC> x0[U], x1[U], g0[U], g1[U];
+    for (int k = 0; k < VEC; ++k) acc[k] = make_float2(0.0f, 0.0f);
+    const unsigned items = static_cast<unsigned>(a.T) << shares;
+    const unsigned stride = (keys ? gridDim.x - a.q_blocks : a.q_blocks) * QKN_WARPS;
+    const int wide = L.per_warp << shares;
+    const int sub = L.live ? L.sub : 0, last = h1 - 1 - sub;
+    auto head0 = [&](unsigned item) {
+        return (keys ? a.q_heads : 0) + static_cast<int>(item & ((1u << shares) - 1)) * L.per_warp;
+    };
+    unsigned item = block * QKN_WARPS + warp;
+    // Two steps' loads are in flight: `next` stands at the one to be asked for. Behind the last head a lane reads that one
+    // again, writes nothing and adds nothing.
+    unsigned next = item;
+    int next_h = head0(item);
+    const __nv_bfloat16 *xt = nullptr, *gt = nullptr;
+    const int32_t* pos = a.pos + static_cast<long long>(axis) * a.T;
+    auto start = [&]() {
+        const int token = static_cast<int>(next >> shares);
+        xt = a.x + token * a.ldx + sub * a.d;
+        gt = a.dy + token * a.lddy + sub * a.d;
+        next_h = head0(next);
+    };
+    auto fetch = [&](QkRaw<VEC>& x, QkRaw<VEC>& g, int& at) {
+        if (next >= items) return;
+        const int o = min(next_h, last) * a.d;
+        qk_load(x, xt + o, L);
+        qk_load(g, gt + o, L);
+        at = pos[next >> shares];
+        next_h += wide;
+        if (next_h >= h1) {
+            next += stride;
+            start();
+        }
+    };
+    QkRaw<VEC> xr[2], gr[2];
+    int at[2];
+    start();
+    fetch(xr[0], gr[0], at[0]);
+    bool fresh = true;  // the next step is its token's first
+    int h = head0(item);
+    __nv_bfloat16* dt = nullptr;
+    while (item < items) {
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int hd = base + L.sub + k * step;
-                x0[k].v = x1[k].v = g0[k].v = g1[k].v = V{};
-                if (L.live && hd < a.heads) {
-                    x0[k].v = *reinterpret_cast<const V*>(xr + hd * a.d + L.o0);
-                    x1[k].v = *reinterpret_cast<const V*>(xr + hd * a.d + L.o1);
-                    g0[k].v = *reinterpret_cast<const V*>(gr + hd * a.d + L.o0);
-                    g1[k].v = *reinterpret_cast<const V*>(gr + hd * a.d + L.o1);
-                }
+        for (int k = 0; k < 2; ++k) {
+            if (item >= items) break;
+            if (fresh) {
+                const int token = static_cast<int>(item >> shares);
+                float c[VEC], s[VEC];
+                qk_angles(tab, a, L, token, at[k], one_axis, -1, c, s);
+                qk_coefficients<VEC, INTER>(c, s, nullptr, P, Q);
+                dt = a.y + token * a.ldy + sub * a.d;
+                fresh = false;
             }
+            fetch(xr[k ^ 1], gr[k ^ 1], at[k ^ 1]);
+            float2 x[VEC], g[VEC], t[VEC];
+            qk_floats(gr[k], t);
+            qk_floats(xr[k], x);
+            qk_turn<VEC, INTER>(t, P, Q, g);
+            float2 ss = make_float2(0.0f, 0.0f), dot = ss;
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int hd = base + L.sub + k * step;
-                const bool q = hd < a.q_heads;
-                float x[2 * VEC], g[2 * VEC], wf[2 * VEC];
-                QkVec<VEC> w0, w1;
+            for (int j = 0; j < VEC; ++j) {
+                ss = fma2(x[j], x[j], ss);
+                t[j] = mul2(w[j], g[j]);
+                dot = fma2(t[j], x[j], dot);
+            }
+            float sum[2] = {ss.x + ss.y, dot.x + dot.y};  // x^2, w g x
+            qk_head_sum<POW2>(sum, L.groups, L.g, lane);
+            const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
+            const float rm = -(sum[1] * a.inv_d * r) * r;  // -r mean(w g n)
+            const bool mine = L.live && h <= last;
 #pragma unroll
-                for (int j = 0; j < VEC / 2; ++j) {
-                    w0.w[j] = q ? wq[0].w[j] : wk[0].w[j];
-                    w1.w[j] = q ? wq[1].w[j] : wk[1].w[j];
-                }
-                qk_unpack<VEC>(x0[k].w, x1[k].w, x);
-                qk_unpack<VEC>(g0[k].w, g1[k].w, g);
-                qk_unpack<VEC>(w0.w, w1.w, wf);
-                qk_turn<VEC, INTER>(g, c, s);
-                float sum[2] = {0.0f, 0.0f};  // x^2, w g x
-#pragma unroll
-                for (int j = 0; j < 2 * VEC; ++j) {
-                    sum[0] += x[j] * x[j];
-                    wf[j] *= g[j];
-                    sum[1] += wf[j] * x[j];
-                }
-                qk_head_sum(sum, L.groups, L.g, lane);
-                const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
-                const float m = sum[1] * a.inv_d * r;  // mean(w g n)
-#pragma unroll
-                for (int j = 0; j < 2 * VEC; ++j) {
-                    const float n = x[j] * r;
-                    const float gn = g[j] * n;
-                    if (q)
-                        aq[j] += gn;
-                    else
-                        ak[j] += gn;
-                    wf[j] = r * (wf[j] - n * m);
-                }
-                if (L.live && hd < a.heads) {
-#pragma unroll
-                    for (int j = 0; j < VEC / 2; ++j) {
-                        x0[k].w[j] = rope_pack(wf[2 * j], wf[2 * j + 1]);
-                        x1[k].w[j] = rope_pack(wf[VEC + 2 * j], wf[VEC + 2 * j + 1]);
-                    }
-                    *reinterpret_cast<V*>(dr + hd * a.d + L.o0) = x0[k].v;
-                    *reinterpret_cast<V*>(dr + hd * a.d + L.o1) = x1[k].v;
-                }
+            for (int j = 0; j < VEC; ++j) {
+                const float2 n = mul2(x[j], make_float2(r, r));
+                if (mine) acc[j] = fma2(g[j], n, acc[j]);
+                t[j] = fma2(n, make_float2(rm, rm), mul2(t[j], make_float2(r, r)));
+            }
+            if (mine) qk_store(t, dt + h * a.d, L);
+            h += wide;
+            if (h >= h1) {
+                item += stride;
+                h = head0(item);
+                fresh = true;
             }
         }
     }
     if (L.live) {
-        float* row = red + (warp * L.per_warp + L.sub) * 2 * a.d;
+        float* row = red + (warp * L.per_warp + L.sub) * a.d;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            row[L.o0 + j] = aq[j];
-            row[L.o1 + j] = aq[VEC + j];
-            row[a.d + L.o0 + j] = ak[j];
-            row[a.d + L.o1 + j] = ak[VEC + j];
+        for (int k = 0; k < VEC; ++k) {
+            const int o = k < VEC / 2 ? L.o0 + 2 * k : L.o1 + 2 * k - VEC;
+            row[o] = acc[k].x;
+            row[o + 1] = acc[k].y;
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.d; i += QKN_WARPS * 32) {
+    for (int i = threadIdx.x; i < a.d; i += QKN_WARPS * 32) {
         float t = 0.0f;
-        for (int k = 0; k < QKN_WARPS * L.per_warp; ++k) t += red[k * 2 * a.d + i];
-        a.sums[static_cast<long long>(blockIdx.x) * 2 * a.d + i] = t;
+        for (int k = 0; k < QKN_WARPS * L.per_warp; ++k) t += red[k * a.d + i];
+        a.sums[static_cast<long long>(blockIdx.x) * a.d + i] = t;
     }
 }
 
-// dwq and dwk from the blocks' rows: a block takes 32 of the 2 d columns, eight warps a share of the rows each.
-__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float* sums, float* dwq, float* dwk, int rows, int d) {
+// dwq and dwk from the blocks' rows, the first q_rows of them queries': a block takes 32 of d columns of one of the two,
+// eight warps a share of the rows each.
+__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float* sums, float* dwq, float* dwk, int q_rows, int rows,
+                                                         int d) {
     __shared__ float red[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
+    const int half = gridDim.x / 2;
+    const bool keys = static_cast<int>(blockIdx.x) >= half;
+    const int col = (blockIdx.x - (keys ? half : 0)) * 32 + lane;
     grid_dependency_wait();
     grid_launch_dependents();
     float t = 0.0f;
-    if (col < 2 * d)
-        for (int r = warp; r < rows; r += 8) t += sums[static_cast<long long>(r) * 2 * d + col];
+    if (col < d)
+#pragma unroll 8
+        for (int r = (keys ? q_rows : 0) + warp; r < (keys ? rows : q_rows); r += 8)
+            t += sums[static_cast<long long>(r) * d + col];
     red[warp][lane] = t;
     __syncthreads();
-    if (warp != 0 || col >= 2 * d) return;
+    float* out = keys ? dwk : dwq;
+    if (warp != 0 || col >= d || out == nullptr) return;
 #pragma unroll
     for (int k = 1; k < 8; ++k) t += red[k][lane];
-    float* out = col < d ? dwq : dwk;
-    if (out != nullptr) out[col < d ? col : col - d] = t;
+    out[col] = t;
 }
 
 // The lanes' vectors are 16 bytes where each half of a head and what is not rotated divide into them, else 8.
 static bool qk_wide(int d, long long pairs) { return d % 16 == 0 && pairs % 8 == 0; }
 
-// Warps that share a token's heads: doubled while there would be fewer than eight warps on each of 152 SMs.
+// Log2 of the warps that share a token's heads: doubled while there would be fewer than eight warps on each of 152 SMs.
 static int qk_shares(int T, int heads, int d, bool wide) {
     const int in_hand = 32 / (d / (wide ? 16 : 8));
-    int shares = 1;
-    while (static_cast<long long>(T) * shares < 8LL * 152 && shares * in_hand < heads) shares *= 2;
+    int shares = 0;
+    while ((static_cast<long long>(T) << shares) < 8LL * 152 && in_hand << shares < heads) ++shares;
     return shares;
 }
 
-static int qk_bwd_blocks(int T, int shares) {
-    const long long blocks = (static_cast<long long>(T) * shares + QKN_WARPS - 1) / QKN_WARPS;
-    return static_cast<int>(blocks < QKN_BWD_BLOCKS ? blocks : QKN_BWD_BLOCKS);
+// Shares of query heads and of key heads, and the blocks that walk each. Forward: one warp a token and share. Backward:
+// the blocks that the chip holds at most, divided by the two kinds' steps (a token's angles cost about two).
+static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
+    const int in_hand = 32 / (a.d / (wide ? 16 : 8));
+    const int n[2] = {a.q_heads, a.heads - a.q_heads};
+    const double cost[2] = {n[0] ? 2.0 + (n[0] + in_hand - 1) / in_hand : 0.0, n[1] ? 2.0 + (n[1] + in_hand - 1) / in_hand : 0.0};
+    for (int i = 0; i < 2; ++i) {
+        const int shares = qk_shares(a.T, n[i], a.d, wide);
+        (i == 0 ? a.shares : a.k_shares) = shares;
+        const long long most = ((static_cast<long long>(a.T) << shares) + QKN_WARPS - 1) / QKN_WARPS;
+        long long b = static_cast<long long>(QKN_BWD_BLOCKS * cost[i] / (cost[0] + cost[1]) + 0.5);
+        b = b < 1 ? 1 : b > QKN_BWD_BLOCKS - 1 && n[1 - i] ? QKN_BWD_BLOCKS - 1 : b;
+        blocks[i] = n[i] == 0 ? 0 : static_cast<int>(backward && b < most ? b : most);
+    }
+    a.q_blocks = blocks[0];
+}
+
+// f with the kernel's constants: VEC, INTER, POW2.
+template <typename F>
+static cudaError_t qk_dispatch(int d, bool wide, bool inter, F f) {
+    using B = std::true_type;
+    using N = std::false_type;
+    const int groups = d / (wide ? 16 : 8);
+    const bool pow2 = (groups & (groups - 1)) == 0;
+    auto with = [&](auto vec) {
+        if (inter) return pow2 ? f(vec, B{}, B{}) : f(vec, B{}, N{});
+        return pow2 ? f(vec, N{}, B{}) : f(vec, N{}, N{});
+    };
+    return wide ? with(std::integral_constant<int, 8>{}) : with(std::integral_constant<int, 4>{});
 }
 
 static mp_status qk_check(int T, int heads, int q_heads, int d, int axes, const int* sections, double base, float eps,
@@ -366,7 +446,6 @@ static QkNormArgs qk_args(int T, int heads, int q_heads, int d, long long pairs,
     a.q_heads = q_heads;
     a.d = d;
     a.pairs = static_cast<int>(pairs);
-    a.shares = qk_shares(T, heads, d, qk_wide(d, pairs));
     a.eps = eps;
     a.inv_d = 1.0f / static_cast<float>(d);
     return a;
@@ -402,19 +481,19 @@ extern "C" mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16
     a.pos = pos;
     a.ldx = ldx;
     a.ldy = ldy;
-    const bool inter = (flags & MP_ROPE_INTERLEAVED) != 0;
-    auto kernel = qk_wide(d, pairs) ? (inter ? qk_norm_kernel<8, true> : qk_norm_kernel<8, false>)
-                                    : (inter ? qk_norm_kernel<4, true> : qk_norm_kernel<4, false>);
-    const long long blocks = (static_cast<long long>(T) * a.shares + QKN_WARPS - 1) / QKN_WARPS;
-    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(QKN_WARPS * 32), 0,
-                                     static_cast<cudaStream_t>(stream), tab, a);
+    const bool wide = qk_wide(d, pairs);
+    int blocks[2];
+    qk_blocks(a, wide, false, blocks);
+    const cudaError_t e = qk_dispatch(d, wide, (flags & MP_ROPE_INTERLEAVED) != 0, [&](auto vec, auto inter, auto pow2) {
+        return launch_pdl(qk_norm_kernel<vec.value, inter.value, pow2.value>, dim3(static_cast<unsigned>(blocks[0] + blocks[1])),
+                          dim3(QKN_WARPS * 32), 0, static_cast<cudaStream_t>(stream), tab, a);
+    });
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
 
 extern "C" size_t mp_qk_norm_rope_bwd_workspace_bytes(int T, int heads, int d) {
     if (T <= 0 || heads <= 0 || d <= 0 || d % 8 != 0 || d > 2 * ROPE_MAX_PAIRS) return 0;
-    // narrow vectors hold fewer heads, so they never take fewer shares than wide ones
-    return static_cast<size_t>(qk_bwd_blocks(T, qk_shares(T, heads, d, false))) * 2 * d * sizeof(float);
+    return static_cast<size_t>(QKN_BWD_BLOCKS) * d * sizeof(float);
 }
 
 extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp_bf16* dx, const mp_bf16* wq,
@@ -443,7 +522,7 @@ extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp
     st = check_device(&sms);
     if (st != MP_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int blocks = 0;
+    int blocks[2] = {0, 0};
     if (T > 0) {
         RopeTable tab{};
         rope_fill(tab, axes, sections, pairs, base, flags);
@@ -458,16 +537,16 @@ extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp
         a.ldx = ldx;
         a.lddy = lddy;
         a.ldy = lddx;
-        blocks = qk_bwd_blocks(T, a.shares);
-        const bool inter = (flags & MP_ROPE_INTERLEAVED) != 0;
-        auto kernel = qk_wide(d, pairs) ? (inter ? qk_norm_bwd_kernel<8, true> : qk_norm_bwd_kernel<8, false>)
-                                        : (inter ? qk_norm_bwd_kernel<4, true> : qk_norm_bwd_kernel<4, false>);
-        const cudaError_t e =
-            launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(QKN_WARPS * 32), 0, s, tab, a);
+        const bool wide = qk_wide(d, pairs);
+        qk_blocks(a, wide, true, blocks);
+        const cudaError_t e = qk_dispatch(d, wide, (flags & MP_ROPE_INTERLEAVED) != 0, [&](auto vec, auto inter, auto pow2) {
+            return launch_pdl(qk_norm_bwd_kernel<vec.value, inter.value, pow2.value>,
+                              dim3(static_cast<unsigned>(blocks[0] + blocks[1])), dim3(QKN_WARPS * 32), 0, s, tab, a);
+        });
         if (e != cudaSuccess) return MP_ERR_CUDA;
     }
     // T = 0: no rows, the sums are zero.
-    const cudaError_t e = launch_pdl(qk_norm_dw_kernel, dim3(static_cast<unsigned>((2 * d + 31) / 32)), dim3(256), 0, s,
-                                     static_cast<const float*>(workspace), dwq, dwk, blocks, d);
+    const cudaError_t e = launch_pdl(qk_norm_dw_kernel, dim3(static_cast<unsigned>(2 * ((d + 31) / 32))), dim3(256), 0, s,
+                                     static_cast<const float*>(workspace), dwq, dwk, blocks[0], blocks[0] + blocks[1], d);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
