@@ -8,15 +8,13 @@
 //
 // Bound by memory: x once in and y once out; backward x and dy in and dx out. A head lies across G = d / (2 VEC) lanes, VEC
 // rotated pairs in each, or as many unrotated elements (cosine 1, sine 0), so that the sums of squares are a few shuffles
-// within the G lanes. A warp walks tokens (or a share of a token's heads where tokens are few), as many heads at once as
-// it has lanes for, with the next steps' loads in flight: the angles' sines are computed once a token, and with the weight they
-// make two coefficients an element, y = r (x P + partner Q). All of it is fp32, two elements an instruction, and each
-// output is rounded once.
-// The weights' gradients: a warp of the backward pass walks query heads or key heads, its lanes keep their columns' sums in
-// registers over all its tokens, a block adds its lanes' in shared memory and writes one row of the workspace, a second
-// kernel adds the rows: fixed order, no atomics.
-#include <type_traits>
-
+// within the G lanes. A warp walks tokens (or a share of a token's heads where tokens are few), query heads or key heads, as
+// many heads at once as it has lanes for; the angles' sines are computed once a token, and with the weight they make two
+// coefficients an element, y = r (x P + partner Q). All of it is fp32, two elements an instruction, and each output is
+// rounded once.
+// The weights' gradients: a lane of the backward pass keeps its columns' sums in registers over all its tokens, a block
+// adds its lanes' in shared memory and writes one row of the workspace, a second kernel adds the rows: fixed order, no
+// atomics.
 #include "mptp_internal.h"
 #include "mptp_launch.cuh"
 #include "mptp_ptx.cuh"
@@ -25,10 +23,10 @@
 namespace mptp {
 
 constexpr int QKN_WARPS = 4;         // warps of a block
-constexpr int QKN_PER_SM = 5;        // forward: blocks on an SM
-constexpr int QKN_UNROLL = 2;        // and a warp's steps whose loads are in flight together
+constexpr int QKN_STAGES = 4;        // steps in flight, and the one in hand
+constexpr int QKN_PER_SM = 4;        // blocks on an SM
 constexpr int QKN_BWD_PER_SM = 3;
-constexpr int QKN_BWD_BLOCKS = QKN_BWD_PER_SM * 152;  // backward: rows of the workspace at most
+constexpr int QKN_BWD_BLOCKS = QKN_BWD_PER_SM * 152;  // rows of the workspace at most
 
 struct QkNormArgs {
     const __nv_bfloat16* x;
@@ -164,198 +162,205 @@ __device__ __forceinline__ void qk_coefficients(const float (&c)[VEC], const flo
     }
 }
 
-// A lane's elements of a weight; zeros where the call has none of its heads.
+// A lane's elements of a weight.
 template <int VEC, bool INTER>
-__device__ __forceinline__ void qk_weight(const __nv_bfloat16* w, const QkLane<VEC, INTER>& L, QkRaw<VEC>& x) {
-    x = QkRaw<VEC>{};
-    if (w != nullptr) qk_load(x, w, L);
+__device__ __forceinline__ void qk_weight(const __nv_bfloat16* w, const QkLane<VEC, INTER>& L, float2 (&f)[VEC]) {
+    QkRaw<VEC> x;
+    qk_load(x, w, L);
+    qk_floats(x, f);
 }
 
-// Whether each lane's pairs lie on one axis.
-template <int VEC, bool INTER>
-__device__ __forceinline__ bool qk_one_axis(const RopeTable& tab, const QkLane<VEC, INTER>& L) {
-    return __all_sync(0xffffffffu, !L.turns || tab.axis[L.g * VEC] == tab.axis[L.g * VEC + VEC - 1]);
+template <int BYTES>
+__device__ __forceinline__ void qk_copy(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
-// One kind's heads (queries' or keys') of a token, or a share of them, a warp.
-template <int VEC, bool INTER, bool POW2>
-__global__ void __launch_bounds__(QKN_WARPS * 32, QKN_PER_SM) qk_norm_kernel(const __grid_constant__ RopeTable tab,
-                                                                             const QkNormArgs a) {
-    constexpr int U = QKN_UNROLL;
-    const int lane = threadIdx.x & 31;
-    const QkLane<VEC, INTER> L(a.d, a.pairs, lane);
-    const bool keys = blockIdx.x >= static_cast<unsigned>(a.q_blocks);
-    const unsigned block = keys ? blockIdx.x - a.q_blocks : blockIdx.x;
-    const int shares = keys ? a.k_shares : a.shares;
-    const unsigned item = block * QKN_WARPS + (threadIdx.x >> 5);
-    const int token = static_cast<int>(item >> shares);
-    const bool one_axis = qk_one_axis(tab, L);
-    const int axis = L.turns ? tab.axis[L.g * VEC] : 0;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (token >= a.T) return;
-    const int h1 = keys ? a.heads : a.q_heads;
-    const int wide = L.per_warp << shares;  // heads of a step, all shares'
-    // The lane's first head; behind the last one it reads that one again and writes nothing.
-    int h = (keys ? a.q_heads : 0) + static_cast<int>(item & ((1u << shares) - 1)) * L.per_warp;
-    const int last = h1 - 1 - (L.live ? L.sub : 0);
-    const __nv_bfloat16* x = a.x + token * a.ldx + (L.live ? L.sub : 0) * a.d;
-    __nv_bfloat16* y = a.y + token * a.ldy + L.sub * a.d;
-    QkRaw<VEC> raw[U], wr;
-    auto load = [&](int h) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) qk_load(raw[k], x + min(h + k * wide, last) * a.d, L);
-    };
-    load(h);
-    const int at = a.pos[static_cast<long long>(axis) * a.T + token];
-    qk_weight(keys ? a.wk : a.wq, L, wr);
-    float2 P[VEC], Q[VEC];
-    {
-        float c[VEC], s[VEC];
-        float2 w[VEC];
-        qk_angles(tab, a, L, token, at, one_axis, 1, c, s);
-        qk_floats(wr, w);
-        qk_coefficients<VEC, INTER>(c, s, w, P, Q);
+// The walk of a warp: items (a token's heads of one kind, or a share of them) `stride` apart, each in steps of as many heads
+// as the warp has lanes for. A step's loads go to the lane's own places in shared memory (cp.async: nothing of them waits in
+// registers, and no lane reads another's), QKN_STAGES - 1 steps ahead; N arrays are read, and the token's position.
+template <int VEC, bool INTER, int N>
+struct QkWalk {
+    static constexpr int BYTES = 2 * VEC;                           // of a vector
+    static constexpr int STAGE = N * 2 * BYTES * 32 + 4 * 32;       // of a warp's stage
+    const QkLane<VEC, INTER>& L;
+    const __nv_bfloat16* src[N];
+    long long ld[N];
+    const __nv_bfloat16* row[N];
+    const int32_t* pos;
+    uint32_t ring;   // the lane's
+    unsigned items, stride, next;
+    int shares, h0, h1, wide, last, d, next_h, stage;
+
+    __device__ __forceinline__ int first_head(unsigned item) const {
+        return h0 + static_cast<int>(item & ((1u << shares) - 1)) * L.per_warp;
     }
-    for (;;) {
+    __device__ __forceinline__ void start() {
+        const int token = static_cast<int>(next >> shares);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            float2 f[VEC], out[VEC], ss = make_float2(0.0f, 0.0f);
-            qk_floats(raw[k], f);
+        for (int n = 0; n < N; ++n) row[n] = src[n] + token * ld[n];
+        next_h = first_head(next);
+    }
+    // Asks for the next step. Behind the last head a lane reads that one again.
+    __device__ __forceinline__ void fetch() {
+        if (next < items) {
+            const int o = min(next_h, last) * d;
+            const uint32_t at = ring + stage * STAGE;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) ss = fma2(f[j], f[j], ss);
-            float sum[1] = {ss.x + ss.y};
-            qk_head_sum<POW2>(sum, L.groups, L.g, lane);
-            const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
-            qk_turn<VEC, INTER>(f, P, Q, out);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) out[j] = mul2(out[j], make_float2(r, r));
-            if (L.live && h + k * wide <= last) qk_store(out, y + (h + k * wide) * a.d, L);
+            for (int n = 0; n < N; ++n) {
+                qk_copy<BYTES>(at + (2 * n) * BYTES * 32, row[n] + o + L.o0);
+                qk_copy<BYTES>(at + (2 * n + 1) * BYTES * 32, row[n] + o + L.o1);
+            }
+            const uint32_t lane4 = (threadIdx.x & 31) * 4;
+            qk_copy<4>(at - (threadIdx.x & 31) * BYTES + N * 2 * BYTES * 32 + lane4, pos + (next >> shares));
+            next_h += wide;
+            if (next_h >= h1) {
+                next += stride;
+                start();
+            }
         }
-        h += U * wide;
-        if (h > h1 - 1) break;
-        load(h);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        stage = stage == QKN_STAGES - 1 ? 0 : stage + 1;
     }
+};
+
+template <int VEC>
+__device__ __forceinline__ void qk_take(const uint8_t* at, float2 (&f)[VEC]) {
+    using V = typename RopeVec<VEC>::T;
+    QkRaw<VEC> x;
+    x.v[0] = *reinterpret_cast<const V*>(at);
+    x.v[1] = *reinterpret_cast<const V*>(at + 2 * VEC * 32);
+    qk_floats(x, f);
 }
 
-template <int VEC, bool INTER, bool POW2>
-__global__ void __launch_bounds__(QKN_WARPS * 32, QKN_BWD_PER_SM) qk_norm_bwd_kernel(
+// A warp walks query heads or key heads, by its block.
+template <int VEC, bool INTER, bool POW2, bool BACKWARD>
+__global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QKN_PER_SM) qk_norm_kernel(
     const __grid_constant__ RopeTable tab, const QkNormArgs a) {
-    __shared__ float red[QKN_WARPS * 32 * 2 * VEC];  // [warp, sub][d]: 32 lanes of 2 VEC columns a warp
+    using Walk = QkWalk<VEC, INTER, BACKWARD ? 2 : 1>;
+    extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const QkLane<VEC, INTER> L(a.d, a.pairs, lane);
-    const bool one_axis = qk_one_axis(tab, L);
+    // Whether each lane's pairs lie on one axis.
+    const bool one_axis = __all_sync(0xffffffffu, !L.turns || tab.axis[L.g * VEC] == tab.axis[L.g * VEC + VEC - 1]);
     const int axis = L.turns ? tab.axis[L.g * VEC] : 0;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    // Query heads or key heads, by the block.
     const bool keys = static_cast<int>(blockIdx.x) >= a.q_blocks;
     const int block = keys ? blockIdx.x - a.q_blocks : blockIdx.x;
-    const int h1 = keys ? a.heads : a.q_heads;
-    const int shares = keys ? a.k_shares : a.shares;
-    QkRaw<VEC> wr;
-    qk_weight(keys ? a.wk : a.wq, L, wr);
+    const int sub = L.live ? L.sub : 0;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    const uint8_t* ring = smem + warp * QKN_STAGES * Walk::STAGE + lane * Walk::BYTES;
+    Walk walk{L};
+    walk.src[0] = a.x + sub * a.d;
+    walk.ld[0] = a.ldx;
+    if constexpr (BACKWARD) {
+        walk.src[1] = a.dy + sub * a.d;
+        walk.ld[1] = a.lddy;
+    }
+    walk.pos = a.pos + static_cast<long long>(axis) * a.T;
+    walk.ring = smem_u32(ring);
+    walk.shares = keys ? a.k_shares : a.shares;
+    walk.items = static_cast<unsigned>(a.T) << walk.shares;
+    walk.stride = (keys ? gridDim.x - a.q_blocks : a.q_blocks) * QKN_WARPS;
+    walk.h0 = keys ? a.q_heads : 0;
+    walk.h1 = keys ? a.heads : a.q_heads;
+    walk.wide = L.per_warp << walk.shares;  // heads of a step, all shares'
+    walk.last = walk.h1 - 1 - sub;
+    walk.d = a.d;
+    walk.stage = 0;
+    unsigned item = block * QKN_WARPS + warp;
+    walk.next = item;
+    walk.start();
+#pragma unroll
+    for (int k = 0; k < QKN_STAGES - 1; ++k) walk.fetch();
+
     float2 w[VEC], acc[VEC], P[VEC], Q[VEC];
-    qk_floats(wr, w);
+    qk_weight(keys ? a.wk : a.wq, L, w);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = make_float2(0.0f, 0.0f);
-    const unsigned items = static_cast<unsigned>(a.T) << shares;
-    const unsigned stride = (keys ? gridDim.x - a.q_blocks : a.q_blocks) * QKN_WARPS;
-    const int wide = L.per_warp << shares;
-    const int sub = L.live ? L.sub : 0, last = h1 - 1 - sub;
-    auto head0 = [&](unsigned item) {
-        return (keys ? a.q_heads : 0) + static_cast<int>(item & ((1u << shares) - 1)) * L.per_warp;
-    };
-    unsigned item = block * QKN_WARPS + warp;
-    // Two steps' loads are in flight: `next` stands at the one to be asked for. Behind the last head a lane reads that one
-    // again, writes nothing and adds nothing.
-    unsigned next = item;
-    int next_h = head0(item);
-    const __nv_bfloat16 *xt = nullptr, *gt = nullptr;
-    const int32_t* pos = a.pos + static_cast<long long>(axis) * a.T;
-    auto start = [&]() {
-        const int token = static_cast<int>(next >> shares);
-        xt = a.x + token * a.ldx + sub * a.d;
-        gt = a.dy + token * a.lddy + sub * a.d;
-        next_h = head0(next);
-    };
-    auto fetch = [&](QkRaw<VEC>& x, QkRaw<VEC>& g, int& at) {
-        if (next >= items) return;
-        const int o = min(next_h, last) * a.d;
-        qk_load(x, xt + o, L);
-        qk_load(g, gt + o, L);
-        at = pos[next >> shares];
-        next_h += wide;
-        if (next_h >= h1) {
-            next += stride;
-            start();
+    int h = walk.first_head(item), stage = 0;
+    bool fresh = true;  // a token's first step
+    __nv_bfloat16* out = nullptr;
+    while (item < walk.items) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(QKN_STAGES - 2) : "memory");
+        const uint8_t* at = ring + stage * Walk::STAGE;
+        if (fresh) {
+            const int token = static_cast<int>(item >> walk.shares);
+            const int p = *reinterpret_cast<const int*>(smem + (warp * QKN_STAGES + stage) * Walk::STAGE + Walk::STAGE - 128 + lane * 4);
+            float c[VEC], s[VEC];
+            qk_angles(tab, a, L, token, p, one_axis, BACKWARD ? -1 : 1, c, s);
+            qk_coefficients<VEC, INTER>(c, s, BACKWARD ? nullptr : w, P, Q);
+            out = a.y + token * a.ldy + sub * a.d;
+            fresh = false;
         }
-    };
-    QkRaw<VEC> xr[2], gr[2];
-    int at[2];
-    start();
-    fetch(xr[0], gr[0], at[0]);
-    bool fresh = true;  // the next step is its token's first
-    int h = head0(item);
-    __nv_bfloat16* dt = nullptr;
-    while (item < items) {
+        float2 x[VEC], y[VEC];
+        qk_take<VEC>(at, x);
+        float2 ss = make_float2(0.0f, 0.0f);
+        const bool mine = L.live && h <= walk.last;
+        if constexpr (!BACKWARD) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (item >= items) break;
-            if (fresh) {
-                const int token = static_cast<int>(item >> shares);
-                float c[VEC], s[VEC];
-                qk_angles(tab, a, L, token, at[k], one_axis, -1, c, s);
-                qk_coefficients<VEC, INTER>(c, s, nullptr, P, Q);
-                dt = a.y + token * a.ldy + sub * a.d;
-                fresh = false;
-            }
-            fetch(xr[k ^ 1], gr[k ^ 1], at[k ^ 1]);
-            float2 x[VEC], g[VEC], t[VEC];
-            qk_floats(gr[k], t);
-            qk_floats(xr[k], x);
-            qk_turn<VEC, INTER>(t, P, Q, g);
-            float2 ss = make_float2(0.0f, 0.0f), dot = ss;
+            for (int j = 0; j < VEC; ++j) ss = fma2(x[j], x[j], ss);
+            float sum[1] = {ss.x + ss.y};
+            qk_head_sum<POW2>(sum, L.groups, L.g, lane);
+            walk.fetch();
+            const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
+            qk_turn<VEC, INTER>(x, P, Q, y);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[j] = mul2(y[j], make_float2(r, r));
+        } else {
+            float2 g[VEC], dot = ss;
+            qk_take<VEC>(at + 4 * VEC * 32, y);
+            qk_turn<VEC, INTER>(y, P, Q, g);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 ss = fma2(x[j], x[j], ss);
-                t[j] = mul2(w[j], g[j]);
-                dot = fma2(t[j], x[j], dot);
+                y[j] = mul2(w[j], g[j]);
+                dot = fma2(y[j], x[j], dot);
             }
             float sum[2] = {ss.x + ss.y, dot.x + dot.y};  // x^2, w g x
             qk_head_sum<POW2>(sum, L.groups, L.g, lane);
+            walk.fetch();
             const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
             const float rm = -(sum[1] * a.inv_d * r) * r;  // -r mean(w g n)
-            const bool mine = L.live && h <= last;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const float2 n = mul2(x[j], make_float2(r, r));
                 if (mine) acc[j] = fma2(g[j], n, acc[j]);
-                t[j] = fma2(n, make_float2(rm, rm), mul2(t[j], make_float2(r, r)));
-            }
-            if (mine) qk_store(t, dt + h * a.d, L);
-            h += wide;
-            if (h >= h1) {
-                item += stride;
-                h = head0(item);
-                fresh = true;
+                y[j] = fma2(n, make_float2(rm, rm), mul2(y[j], make_float2(r, r)));
             }
         }
+        if (mine) qk_store(y, out + h * a.d, L);
+        stage = stage == QKN_STAGES - 1 ? 0 : stage + 1;
+        h += walk.wide;
+        if (h >= walk.h1) {
+            item += walk.stride;
+            h = walk.first_head(item);
+            fresh = true;
+        }
     }
-    if (L.live) {
-        float* row = red + (warp * L.per_warp + L.sub) * a.d;
+    if constexpr (BACKWARD) {
+        // Sums of the block's lanes: rows [warp, sub][d], where the rings were.
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        float* red = reinterpret_cast<float*>(smem);
+        if (L.live) {
+            float* row = red + (warp * L.per_warp + L.sub) * a.d;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const int o = k < VEC / 2 ? L.o0 + 2 * k : L.o1 + 2 * k - VEC;
-            row[o] = acc[k].x;
-            row[o + 1] = acc[k].y;
+            for (int k = 0; k < VEC; ++k) {
+                const int o = k < VEC / 2 ? L.o0 + 2 * k : L.o1 + 2 * k - VEC;
+                row[o] = acc[k].x;
+                row[o + 1] = acc[k].y;
+            }
         }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.d; i += QKN_WARPS * 32) {
-        float t = 0.0f;
-        for (int k = 0; k < QKN_WARPS * L.per_warp; ++k) t += red[k * a.d + i];
-        a.sums[static_cast<long long>(blockIdx.x) * a.d + i] = t;
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.d; i += QKN_WARPS * 32) {
+            float t = 0.0f;
+            for (int k = 0; k < QKN_WARPS * L.per_warp; ++k) t += red[k * a.d + i];
+            a.sums[static_cast<long long>(blockIdx.x) * a.d + i] = t;
+        }
     }
 }
 
@@ -395,9 +400,9 @@ static int qk_shares(int T, int heads, int d, bool wide) {
     return shares;
 }
 
-// Shares of query heads and of key heads, and the blocks that walk each. Forward: one warp a token and share. Backward:
-// the blocks that the chip holds at most, divided by the two kinds' steps (a token's angles cost about two).
-static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
+// Shares of query heads and of key heads, and the blocks that walk each: those that the chip holds at most, divided by
+// the two kinds' steps (a token's angles cost about two).
+static void qk_blocks(QkNormArgs& a, bool wide, int resident, int* blocks) {
     const int in_hand = 32 / (a.d / (wide ? 16 : 8));
     const int n[2] = {a.q_heads, a.heads - a.q_heads};
     const double cost[2] = {n[0] ? 2.0 + (n[0] + in_hand - 1) / in_hand : 0.0, n[1] ? 2.0 + (n[1] + in_hand - 1) / in_hand : 0.0};
@@ -405,25 +410,32 @@ static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
         const int shares = qk_shares(a.T, n[i], a.d, wide);
         (i == 0 ? a.shares : a.k_shares) = shares;
         const long long most = ((static_cast<long long>(a.T) << shares) + QKN_WARPS - 1) / QKN_WARPS;
-        long long b = static_cast<long long>(QKN_BWD_BLOCKS * cost[i] / (cost[0] + cost[1]) + 0.5);
-        b = b < 1 ? 1 : b > QKN_BWD_BLOCKS - 1 && n[1 - i] ? QKN_BWD_BLOCKS - 1 : b;
-        blocks[i] = n[i] == 0 ? 0 : static_cast<int>(backward && b < most ? b : most);
+        long long b = static_cast<long long>(resident * cost[i] / (cost[0] + cost[1]) + 0.5);
+        b = b < 1 ? 1 : b > resident - 1 && n[1 - i] ? resident - 1 : b;
+        blocks[i] = n[i] == 0 ? 0 : static_cast<int>(b < most ? b : most);
     }
     a.q_blocks = blocks[0];
 }
 
-// f with the kernel's constants: VEC, INTER, POW2.
-template <typename F>
-static cudaError_t qk_dispatch(int d, bool wide, bool inter, F f) {
-    using B = std::true_type;
-    using N = std::false_type;
-    const int groups = d / (wide ? 16 : 8);
-    const bool pow2 = (groups & (groups - 1)) == 0;
-    auto with = [&](auto vec) {
-        if (inter) return pow2 ? f(vec, B{}, B{}) : f(vec, B{}, N{});
-        return pow2 ? f(vec, N{}, B{}) : f(vec, N{}, N{});
-    };
-    return wide ? with(std::integral_constant<int, 8>{}) : with(std::integral_constant<int, 4>{});
+template <int VEC, bool INTER, bool POW2, bool BACKWARD>
+static cudaError_t qk_launch(const RopeTable& tab, const QkNormArgs& a, int blocks, cudaStream_t s) {
+    constexpr int ring = QKN_WARPS * QKN_STAGES * QkWalk<VEC, INTER, BACKWARD ? 2 : 1>::STAGE;
+    constexpr int red = BACKWARD ? QKN_WARPS * 32 * 2 * VEC * 4 : 0;
+    constexpr int bytes = ring > red ? ring : red;
+    static_assert(bytes <= 48 * 1024, "shared memory");
+    return launch_pdl(qk_norm_kernel<VEC, INTER, POW2, BACKWARD>, dim3(static_cast<unsigned>(blocks)), dim3(QKN_WARPS * 32),
+                      bytes, s, tab, a);
+}
+
+template <bool BACKWARD>
+static cudaError_t qk_dispatch(const RopeTable& tab, const QkNormArgs& a, bool wide, bool inter, int blocks, cudaStream_t s) {
+    const int groups = a.d / (wide ? 16 : 8);
+    if ((groups & (groups - 1)) == 0) {
+        if (wide) return (inter ? qk_launch<8, true, true, BACKWARD> : qk_launch<8, false, true, BACKWARD>)(tab, a, blocks, s);
+        return (inter ? qk_launch<4, true, true, BACKWARD> : qk_launch<4, false, true, BACKWARD>)(tab, a, blocks, s);
+    }
+    if (wide) return (inter ? qk_launch<8, true, false, BACKWARD> : qk_launch<8, false, false, BACKWARD>)(tab, a, blocks, s);
+    return (inter ? qk_launch<4, true, false, BACKWARD> : qk_launch<4, false, false, BACKWARD>)(tab, a, blocks, s);
 }
 
 static mp_status qk_check(int T, int heads, int q_heads, int d, int axes, const int* sections, double base, float eps,
@@ -483,11 +495,9 @@ extern "C" mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16
     a.ldy = ldy;
     const bool wide = qk_wide(d, pairs);
     int blocks[2];
-    qk_blocks(a, wide, false, blocks);
-    const cudaError_t e = qk_dispatch(d, wide, (flags & MP_ROPE_INTERLEAVED) != 0, [&](auto vec, auto inter, auto pow2) {
-        return launch_pdl(qk_norm_kernel<vec.value, inter.value, pow2.value>, dim3(static_cast<unsigned>(blocks[0] + blocks[1])),
-                          dim3(QKN_WARPS * 32), 0, static_cast<cudaStream_t>(stream), tab, a);
-    });
+    qk_blocks(a, wide, QKN_PER_SM * 152, blocks);
+    const cudaError_t e = qk_dispatch<false>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks[0] + blocks[1],
+                                             static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
 
@@ -538,11 +548,9 @@ extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp
         a.lddy = lddy;
         a.ldy = lddx;
         const bool wide = qk_wide(d, pairs);
-        qk_blocks(a, wide, true, blocks);
-        const cudaError_t e = qk_dispatch(d, wide, (flags & MP_ROPE_INTERLEAVED) != 0, [&](auto vec, auto inter, auto pow2) {
-            return launch_pdl(qk_norm_bwd_kernel<vec.value, inter.value, pow2.value>,
-                              dim3(static_cast<unsigned>(blocks[0] + blocks[1])), dim3(QKN_WARPS * 32), 0, s, tab, a);
-        });
+        qk_blocks(a, wide, QKN_BWD_BLOCKS, blocks);
+        const cudaError_t e =
+            qk_dispatch<true>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks[0] + blocks[1], s);
         if (e != cudaSuccess) return MP_ERR_CUDA;
     }
     // T = 0: no rows, the sums are zero.
