@@ -121,11 +121,13 @@ __device__ __forceinline__ void qk_turn(const float2 (&f)[VEC], const float2 (&P
     }
 }
 
-// Cosines and sines of a lane's pairs (sign -1: of the rotation back). `at`: the token's position on the axis of all its
-// pairs, where `one_axis`. sin.approx and cos.approx stay within 2^-21 on [-pi, pi], far below a bf16 step.
-template <int VEC, bool INTER>
-__device__ __forceinline__ void qk_angles(const RopeTable& tab, const QkNormArgs& a, const QkLane<VEC, INTER>& L, int token,
-                                          int at, bool one_axis, int sign, float (&c)[VEC], float (&s)[VEC]) {
+// Cosines and sines of a lane's pairs (BACK: of the rotation back). `at`: the token's position on the axis of all its pairs,
+// where `one_axis`. `turns`: the table in shared memory (lanes read different places of it, which the constant bank serves
+// one by one). sin.approx and cos.approx stay within 2^-21 on [-pi, pi], far below a bf16 step.
+template <int VEC, bool INTER, bool BACK>
+__device__ __forceinline__ void qk_angles(const RopeTable& tab, const uint4* turns, const QkNormArgs& a,
+                                          const QkLane<VEC, INTER>& L, int token, int at, bool one_axis, float (&c)[VEC],
+                                          float (&s)[VEC]) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
         c[j] = 1.0f;
@@ -133,11 +135,18 @@ __device__ __forceinline__ void qk_angles(const RopeTable& tab, const QkNormArgs
     }
     if (!L.turns) return;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const int i = L.g * VEC + j;
-        const long long p = one_axis ? at : a.pos[static_cast<long long>(tab.axis[i]) * a.T + token];
-        const float half_turns = rope_half_turns(tab, i, p * sign);
-        __sincosf(half_turns * 3.14159265358979f, &s[j], &c[j]);
+    for (int j = 0; j < VEC; j += 2) {
+        const uint4 two = turns[(L.g * VEC + j) / 2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int p = one_axis ? at : a.pos[static_cast<long long>(tab.axis[L.g * VEC + j + k]) * a.T + token];
+            // the upper 32 bits of p times the 64-bit turns: a signed fraction of a turn in [-1/2, 1/2)
+            const uint32_t lo = k ? two.z : two.x, hi = k ? two.w : two.y, u = static_cast<uint32_t>(p);
+            const uint32_t top = u * hi + __umulhi(u, lo) - (p < 0 ? lo : 0u);
+            // 2 pi / 2^32
+            const float angle = static_cast<float>(static_cast<int32_t>(top)) * (BACK ? -1.4629180792671596e-9f : 1.4629180792671596e-9f);
+            __sincosf(angle, &s[j + k], &c[j + k]);
+        }
     }
 }
 
@@ -190,7 +199,8 @@ struct QkWalk {
     long long ld[N];
     const __nv_bfloat16* row[N];
     const int32_t* pos;
-    uint32_t ring;   // the lane's
+    uint32_t ring, pos_ring;  // the lane's
+    bool fresh;               // the next step is its token's first
     unsigned items, stride, next;
     int shares, h0, h1, wide, last, d, next_h, stage;
 
@@ -202,6 +212,7 @@ struct QkWalk {
 #pragma unroll
         for (int n = 0; n < N; ++n) row[n] = src[n] + token * ld[n];
         next_h = first_head(next);
+        fresh = true;
     }
     // Asks for the next step. Behind the last head a lane reads that one again.
     __device__ __forceinline__ void fetch() {
@@ -213,8 +224,8 @@ struct QkWalk {
                 qk_copy<BYTES>(at + (2 * n) * BYTES * 32, row[n] + o + L.o0);
                 qk_copy<BYTES>(at + (2 * n + 1) * BYTES * 32, row[n] + o + L.o1);
             }
-            const uint32_t lane4 = (threadIdx.x & 31) * 4;
-            qk_copy<4>(at - (threadIdx.x & 31) * BYTES + N * 2 * BYTES * 32 + lane4, pos + (next >> shares));
+            if (fresh) qk_copy<4>(pos_ring + stage * STAGE, pos + (next >> shares));
+            fresh = false;
             next_h += wide;
             if (next_h >= h1) {
                 next += stride;
@@ -249,6 +260,13 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
     const bool keys = static_cast<int>(blockIdx.x) >= a.q_blocks;
     const int block = keys ? blockIdx.x - a.q_blocks : blockIdx.x;
     const int sub = L.live ? L.sub : 0;
+    uint4* turns = reinterpret_cast<uint4*>(smem + QKN_WARPS * QKN_STAGES * Walk::STAGE);
+    for (int i = threadIdx.x; 2 * i < a.pairs; i += QKN_WARPS * 32) {
+        const unsigned long long t0 = tab.turns[2 * i], t1 = tab.turns[2 * i + 1];
+        turns[i] = make_uint4(static_cast<uint32_t>(t0), static_cast<uint32_t>(t0 >> 32), static_cast<uint32_t>(t1),
+                              static_cast<uint32_t>(t1 >> 32));
+    }
+    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -262,6 +280,8 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
     }
     walk.pos = a.pos + static_cast<long long>(axis) * a.T;
     walk.ring = smem_u32(ring);
+    const uint8_t* pos_ring = smem + warp * QKN_STAGES * Walk::STAGE + Walk::STAGE - 128 + lane * 4;
+    walk.pos_ring = smem_u32(pos_ring);
     walk.shares = keys ? a.k_shares : a.shares;
     walk.items = static_cast<unsigned>(a.T) << walk.shares;
     walk.stride = (keys ? gridDim.x - a.q_blocks : a.q_blocks) * QKN_WARPS;
@@ -289,9 +309,9 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
         const uint8_t* at = ring + stage * Walk::STAGE;
         if (fresh) {
             const int token = static_cast<int>(item >> walk.shares);
-            const int p = *reinterpret_cast<const int*>(smem + (warp * QKN_STAGES + stage) * Walk::STAGE + Walk::STAGE - 128 + lane * 4);
+            const int p = *reinterpret_cast<const int*>(pos_ring + stage * Walk::STAGE);
             float c[VEC], s[VEC];
-            qk_angles(tab, a, L, token, p, one_axis, BACKWARD ? -1 : 1, c, s);
+            qk_angles<VEC, INTER, BACKWARD>(tab, turns, a, L, token, p, one_axis, c, s);
             qk_coefficients<VEC, INTER>(c, s, BACKWARD ? nullptr : w, P, Q);
             out = a.y + token * a.ldy + sub * a.d;
             fresh = false;
@@ -317,19 +337,19 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 ss = fma2(x[j], x[j], ss);
-                y[j] = mul2(w[j], g[j]);
-                dot = fma2(y[j], x[j], dot);
+                y[j] = mul2(g[j], x[j]);
+                dot = fma2(y[j], w[j], dot);
             }
             float sum[2] = {ss.x + ss.y, dot.x + dot.y};  // x^2, w g x
             qk_head_sum<POW2>(sum, L.groups, L.g, lane);
             walk.fetch();
             const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
-            const float rm = -(sum[1] * a.inv_d * r) * r;  // -r mean(w g n)
+            const float m = -(sum[1] * a.inv_d * r) * r;  // -r mean(w g n)
+            const float add = mine ? r : 0.0f;            // a step behind the last head adds nothing
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float2 n = mul2(x[j], make_float2(r, r));
-                if (mine) acc[j] = fma2(g[j], n, acc[j]);
-                y[j] = fma2(n, make_float2(rm, rm), mul2(y[j], make_float2(r, r)));
+                acc[j] = fma2(y[j], make_float2(add, add), acc[j]);
+                y[j] = mul2(fma2(x[j], make_float2(m, m), mul2(w[j], g[j])), make_float2(r, r));
             }
         }
         if (mine) qk_store(y, out + h * a.d, L);
@@ -419,7 +439,7 @@ static void qk_blocks(QkNormArgs& a, bool wide, int resident, int* blocks) {
 
 template <int VEC, bool INTER, bool POW2, bool BACKWARD>
 static cudaError_t qk_launch(const RopeTable& tab, const QkNormArgs& a, int blocks, cudaStream_t s) {
-    constexpr int ring = QKN_WARPS * QKN_STAGES * QkWalk<VEC, INTER, BACKWARD ? 2 : 1>::STAGE;
+    constexpr int ring = QKN_WARPS * QKN_STAGES * QkWalk<VEC, INTER, BACKWARD ? 2 : 1>::STAGE + ROPE_MAX_PAIRS * 8;
     constexpr int red = BACKWARD ? QKN_WARPS * 32 * 2 * VEC * 4 : 0;
     constexpr int bytes = ring > red ? ring : red;
     static_assert(bytes <= 48 * 1024, "shared memory");
