@@ -62,15 +62,21 @@ struct QkLane {
     }
 };
 
-// Sum over the `groups` lanes of a head, in all of them (POW2: they are a power of two); every lane of the warp takes part.
-template <bool POW2, int N>
-__device__ __forceinline__ void qk_head_sum(float (&v)[N], int groups, int g, int lane) {
+// How the sum over a head's lanes is taken: G a power of two, three times one, or any other.
+enum { QK_POW2, QK_THREE, QK_ANY };
+
+// Sum over the G lanes of a head, in all of them; every lane of the warp takes part. Heads begin at multiples of G, so
+// exchanges within a power of two that divides G stay in the head; for three times one, the other two thirds lie G / 3 and
+// 2 G / 3 lanes further round the head (turn[0], turn[1]).
+template <int SUM, int N>
+__device__ __forceinline__ void qk_head_sum(float (&v)[N], int groups, int g, int lane, const int (&turn)[2]) {
+    const int pow2 = SUM == QK_THREE ? groups / 3 : groups;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        if (off >= groups) break;
+        if (off >= pow2) break;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            if constexpr (POW2) {
+            if constexpr (SUM != QK_ANY) {
                 v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
             } else {
                 const float o = __shfl_down_sync(0xffffffffu, v[k], off);
@@ -78,9 +84,12 @@ __device__ __forceinline__ void qk_head_sum(float (&v)[N], int groups, int g, in
             }
         }
     }
-    if constexpr (!POW2)
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], lane - g);
+    for (int k = 0; k < N; ++k) {
+        if constexpr (SUM == QK_THREE)
+            v[k] += __shfl_sync(0xffffffffu, v[k], turn[0]) + __shfl_sync(0xffffffffu, v[k], turn[1]);
+        if constexpr (SUM == QK_ANY) v[k] = __shfl_sync(0xffffffffu, v[k], lane - g);
+    }
 }
 
 // A lane's 2 VEC elements of one head as loaded: VEC words, the first vector's, then the second's.
@@ -179,53 +188,50 @@ __device__ __forceinline__ void qk_weight(const __nv_bfloat16* w, const QkLane<V
     qk_floats(x, f);
 }
 
+// `take` bytes from src, zeros behind them.
 template <int BYTES>
-__device__ __forceinline__ void qk_copy(uint32_t dst, const void* src) {
+__device__ __forceinline__ void qk_copy(uint32_t dst, const void* src, int take) {
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(take) : "memory");
 }
 
 // The walk of a warp: items (a token's heads of one kind, or a share of them) `stride` apart, each in steps of as many heads
 // as the warp has lanes for. A step's loads go to the lane's own places in shared memory (cp.async: nothing of them waits in
-// registers, and no lane reads another's), QKN_STAGES - 1 steps ahead; N arrays are read, and the token's position.
-template <int VEC, bool INTER, int N>
+// registers, and no lane reads another's), QKN_STAGES - 1 steps ahead; N arrays are read, and the token's position with its
+// first step. Lanes behind the last head get zeros.
+template <int VEC, int N>
 struct QkWalk {
-    static constexpr int BYTES = 2 * VEC;                           // of a vector
-    static constexpr int STAGE = N * 2 * BYTES * 32 + 4 * 32;       // of a warp's stage
-    const QkLane<VEC, INTER>& L;
-    const __nv_bfloat16* src[N];
+    static constexpr int BYTES = 2 * VEC;                      // of a vector
+    static constexpr int STAGE = N * 2 * BYTES * 32 + 4 * 32;  // of a warp's stage
+    const __nv_bfloat16* src[N];   // the lane's first vector of head 0 of token 0
+    const __nv_bfloat16* at[N];    // and of the step to be asked for
     long long ld[N];
-    const __nv_bfloat16* row[N];
     const int32_t* pos;
-    uint32_t ring, pos_ring;  // the lane's
-    bool fresh;               // the next step is its token's first
+    uint32_t ring, pos_ring;       // the lane's places in the first stage
     unsigned items, stride, next;
-    int shares, h0, h1, wide, last, d, next_h, stage;
+    int shares, per_warp, h0, h1, wide, last, d, second, next_h, stage;
 
     __device__ __forceinline__ int first_head(unsigned item) const {
-        return h0 + static_cast<int>(item & ((1u << shares) - 1)) * L.per_warp;
+        return h0 + static_cast<int>(item & ((1u << shares) - 1)) * per_warp;
     }
     __device__ __forceinline__ void start() {
-        const int token = static_cast<int>(next >> shares);
-#pragma unroll
-        for (int n = 0; n < N; ++n) row[n] = src[n] + token * ld[n];
         next_h = first_head(next);
-        fresh = true;
+#pragma unroll
+        for (int n = 0; n < N; ++n) at[n] = src[n] + (next >> shares) * ld[n] + next_h * d;
     }
-    // Asks for the next step. Behind the last head a lane reads that one again.
     __device__ __forceinline__ void fetch() {
         if (next < items) {
-            const int o = min(next_h, last) * d;
-            const uint32_t at = ring + stage * STAGE;
+            const int take = next_h <= last ? BYTES : 0;
+            const uint32_t to = ring + stage * STAGE;
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                qk_copy<BYTES>(at + (2 * n) * BYTES * 32, row[n] + o + L.o0);
-                qk_copy<BYTES>(at + (2 * n + 1) * BYTES * 32, row[n] + o + L.o1);
+                qk_copy<BYTES>(to + (2 * n) * BYTES * 32, at[n], take);
+                qk_copy<BYTES>(to + (2 * n + 1) * BYTES * 32, at[n] + second, take);
+                at[n] += wide * d;
             }
-            if (fresh) qk_copy<4>(pos_ring + stage * STAGE, pos + (next >> shares));
-            fresh = false;
+            if (next_h < h0 + wide) qk_copy<4>(pos_ring + stage * STAGE, pos + (next >> shares), 4);
             next_h += wide;
             if (next_h >= h1) {
                 next += stride;
@@ -247,10 +253,10 @@ __device__ __forceinline__ void qk_take(const uint8_t* at, float2 (&f)[VEC]) {
 }
 
 // A warp walks query heads or key heads, by its block.
-template <int VEC, bool INTER, bool POW2, bool BACKWARD>
+template <int VEC, bool INTER, int SUM, bool BACKWARD>
 __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QKN_PER_SM) qk_norm_kernel(
     const __grid_constant__ RopeTable tab, const QkNormArgs a) {
-    using Walk = QkWalk<VEC, INTER, BACKWARD ? 2 : 1>;
+    using Walk = QkWalk<VEC, BACKWARD ? 2 : 1>;
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const QkLane<VEC, INTER> L(a.d, a.pairs, lane);
@@ -271,11 +277,11 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
     grid_launch_dependents();
 
     const uint8_t* ring = smem + warp * QKN_STAGES * Walk::STAGE + lane * Walk::BYTES;
-    Walk walk{L};
-    walk.src[0] = a.x + sub * a.d;
+    Walk walk;
+    walk.src[0] = a.x + sub * a.d + L.o0;
     walk.ld[0] = a.ldx;
     if constexpr (BACKWARD) {
-        walk.src[1] = a.dy + sub * a.d;
+        walk.src[1] = a.dy + sub * a.d + L.o0;
         walk.ld[1] = a.lddy;
     }
     walk.pos = a.pos + static_cast<long long>(axis) * a.T;
@@ -288,8 +294,10 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
     walk.h0 = keys ? a.q_heads : 0;
     walk.h1 = keys ? a.heads : a.q_heads;
     walk.wide = L.per_warp << walk.shares;  // heads of a step, all shares'
-    walk.last = walk.h1 - 1 - sub;
+    walk.per_warp = L.per_warp;
+    walk.last = L.live ? walk.h1 - 1 - sub : -1;
     walk.d = a.d;
+    walk.second = L.o1 - L.o0;
     walk.stage = 0;
     unsigned item = block * QKN_WARPS + warp;
     walk.next = item;
@@ -301,6 +309,7 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
     qk_weight(keys ? a.wk : a.wq, L, w);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = make_float2(0.0f, 0.0f);
+    const int turn[2] = {lane - L.g + (L.g + L.groups / 3) % L.groups, lane - L.g + (L.g + L.groups / 3 * 2) % L.groups};
     int h = walk.first_head(item), stage = 0;
     bool fresh = true;  // a token's first step
     __nv_bfloat16* out = nullptr;
@@ -313,18 +322,18 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
             float c[VEC], s[VEC];
             qk_angles<VEC, INTER, BACKWARD>(tab, turns, a, L, token, p, one_axis, c, s);
             qk_coefficients<VEC, INTER>(c, s, BACKWARD ? nullptr : w, P, Q);
-            out = a.y + token * a.ldy + sub * a.d;
+            out = a.y + token * a.ldy + (sub + h) * a.d;
             fresh = false;
         }
         float2 x[VEC], y[VEC];
         qk_take<VEC>(at, x);
         float2 ss = make_float2(0.0f, 0.0f);
-        const bool mine = L.live && h <= walk.last;
+        const bool mine = h <= walk.last;
         if constexpr (!BACKWARD) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss = fma2(x[j], x[j], ss);
             float sum[1] = {ss.x + ss.y};
-            qk_head_sum<POW2>(sum, L.groups, L.g, lane);
+            qk_head_sum<SUM>(sum, L.groups, L.g, lane, turn);
             walk.fetch();
             const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
             qk_turn<VEC, INTER>(x, P, Q, y);
@@ -341,18 +350,18 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
                 dot = fma2(y[j], w[j], dot);
             }
             float sum[2] = {ss.x + ss.y, dot.x + dot.y};  // x^2, w g x
-            qk_head_sum<POW2>(sum, L.groups, L.g, lane);
+            qk_head_sum<SUM>(sum, L.groups, L.g, lane, turn);
             walk.fetch();
             const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
             const float m = -(sum[1] * a.inv_d * r) * r;  // -r mean(w g n)
-            const float add = mine ? r : 0.0f;            // a step behind the last head adds nothing
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                acc[j] = fma2(y[j], make_float2(add, add), acc[j]);
+                acc[j] = fma2(y[j], make_float2(r, r), acc[j]);
                 y[j] = mul2(fma2(x[j], make_float2(m, m), mul2(w[j], g[j])), make_float2(r, r));
             }
         }
-        if (mine) qk_store(y, out + h * a.d, L);
+        if (mine) qk_store(y, out, L);
+        out += walk.wide * a.d;
         stage = stage == QKN_STAGES - 1 ? 0 : stage + 1;
         h += walk.wide;
         if (h >= walk.h1) {
@@ -437,25 +446,29 @@ static void qk_blocks(QkNormArgs& a, bool wide, int resident, int* blocks) {
     a.q_blocks = blocks[0];
 }
 
-template <int VEC, bool INTER, bool POW2, bool BACKWARD>
+template <int VEC, bool INTER, int SUM, bool BACKWARD>
 static cudaError_t qk_launch(const RopeTable& tab, const QkNormArgs& a, int blocks, cudaStream_t s) {
-    constexpr int ring = QKN_WARPS * QKN_STAGES * QkWalk<VEC, INTER, BACKWARD ? 2 : 1>::STAGE + ROPE_MAX_PAIRS * 8;
+    constexpr int ring = QKN_WARPS * QKN_STAGES * QkWalk<VEC, BACKWARD ? 2 : 1>::STAGE + ROPE_MAX_PAIRS * 8;
     constexpr int red = BACKWARD ? QKN_WARPS * 32 * 2 * VEC * 4 : 0;
     constexpr int bytes = ring > red ? ring : red;
     static_assert(bytes <= 48 * 1024, "shared memory");
-    return launch_pdl(qk_norm_kernel<VEC, INTER, POW2, BACKWARD>, dim3(static_cast<unsigned>(blocks)), dim3(QKN_WARPS * 32),
+    return launch_pdl(qk_norm_kernel<VEC, INTER, SUM, BACKWARD>, dim3(static_cast<unsigned>(blocks)), dim3(QKN_WARPS * 32),
                       bytes, s, tab, a);
+}
+
+template <int SUM, bool BACKWARD>
+static cudaError_t qk_launch_as(const RopeTable& tab, const QkNormArgs& a, bool wide, bool inter, int blocks, cudaStream_t s) {
+    if (wide) return (inter ? qk_launch<8, true, SUM, BACKWARD> : qk_launch<8, false, SUM, BACKWARD>)(tab, a, blocks, s);
+    return (inter ? qk_launch<4, true, SUM, BACKWARD> : qk_launch<4, false, SUM, BACKWARD>)(tab, a, blocks, s);
 }
 
 template <bool BACKWARD>
 static cudaError_t qk_dispatch(const RopeTable& tab, const QkNormArgs& a, bool wide, bool inter, int blocks, cudaStream_t s) {
-    const int groups = a.d / (wide ? 16 : 8);
-    if ((groups & (groups - 1)) == 0) {
-        if (wide) return (inter ? qk_launch<8, true, true, BACKWARD> : qk_launch<8, false, true, BACKWARD>)(tab, a, blocks, s);
-        return (inter ? qk_launch<4, true, true, BACKWARD> : qk_launch<4, false, true, BACKWARD>)(tab, a, blocks, s);
-    }
-    if (wide) return (inter ? qk_launch<8, true, false, BACKWARD> : qk_launch<8, false, false, BACKWARD>)(tab, a, blocks, s);
-    return (inter ? qk_launch<4, true, false, BACKWARD> : qk_launch<4, false, false, BACKWARD>)(tab, a, blocks, s);
+    const int groups = a.d / (wide ? 16 : 8), third = groups / 3;
+    if ((groups & (groups - 1)) == 0) return qk_launch_as<QK_POW2, BACKWARD>(tab, a, wide, inter, blocks, s);
+    if (groups % 3 == 0 && (third & (third - 1)) == 0)
+        return qk_launch_as<QK_THREE, BACKWARD>(tab, a, wide, inter, blocks, s);
+    return qk_launch_as<QK_ANY, BACKWARD>(tab, a, wide, inter, blocks, s);
 }
 
 static mp_status qk_check(int T, int heads, int q_heads, int d, int axes, const int* sections, double base, float eps,
