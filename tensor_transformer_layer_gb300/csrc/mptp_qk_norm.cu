@@ -25,6 +25,7 @@ namespace mptp {
 constexpr int QKN_WARPS = 4;         // warps of a block
 constexpr int QKN_STAGES = 4;        // steps in flight, and the one in hand
 constexpr int QKN_PER_SM = 4;        // blocks on an SM
+constexpr int QKN_RUN = 64;          // steps of a warp of the forward pass
 constexpr int QKN_BWD_PER_SM = 3;
 constexpr int QKN_BWD_BLOCKS = QKN_BWD_PER_SM * 152;  // rows of the workspace at most
 
@@ -305,8 +306,9 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
 #pragma unroll
     for (int k = 0; k < QKN_STAGES - 1; ++k) walk.fetch();
 
+    const __nv_bfloat16* weight = keys ? a.wk : a.wq;
     float2 w[VEC], acc[VEC], P[VEC], Q[VEC];
-    qk_weight(keys ? a.wk : a.wq, L, w);
+    if constexpr (BACKWARD) qk_weight(weight, L, w);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = make_float2(0.0f, 0.0f);
     const int turn[2] = {lane - L.g + (L.g + L.groups / 3) % L.groups, lane - L.g + (L.g + L.groups / 3 * 2) % L.groups};
@@ -321,6 +323,7 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
             const int p = *reinterpret_cast<const int*>(pos_ring + stage * Walk::STAGE);
             float c[VEC], s[VEC];
             qk_angles<VEC, INTER, BACKWARD>(tab, turns, a, L, token, p, one_axis, c, s);
+            if constexpr (!BACKWARD) qk_weight(weight, L, w);  // again for each token: sixteen registers less
             qk_coefficients<VEC, INTER>(c, s, BACKWARD ? nullptr : w, P, Q);
             out = a.y + token * a.ldy + (sub + h) * a.d;
             fresh = false;
@@ -394,10 +397,10 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
 }
 
 // dwq and dwk from the blocks' rows, the first q_rows of them queries': a block takes 32 of d columns of one of the two,
-// eight warps a share of the rows each.
-__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float* sums, float* dwq, float* dwk, int q_rows, int rows,
+// 32 warps a share of the rows each.
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* sums, float* dwq, float* dwk, int q_rows, int rows,
                                                          int d) {
-    __shared__ float red[8][32];
+    __shared__ float red[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int half = gridDim.x / 2;
     const bool keys = static_cast<int>(blockIdx.x) >= half;
@@ -407,14 +410,14 @@ __global__ void __launch_bounds__(256) qk_norm_dw_kernel(const float* sums, floa
     float t = 0.0f;
     if (col < d)
 #pragma unroll 8
-        for (int r = (keys ? q_rows : 0) + warp; r < (keys ? rows : q_rows); r += 8)
+        for (int r = (keys ? q_rows : 0) + warp; r < (keys ? rows : q_rows); r += 32)
             t += sums[static_cast<long long>(r) * d + col];
     red[warp][lane] = t;
     __syncthreads();
     float* out = keys ? dwk : dwq;
     if (warp != 0 || col >= d || out == nullptr) return;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) t += red[k][lane];
+    for (int k = 1; k < 32; ++k) t += red[k][lane];
     out[col] = t;
 }
 
@@ -429,19 +432,43 @@ static int qk_shares(int T, int heads, int d, bool wide) {
     return shares;
 }
 
-// Shares of query heads and of key heads, and the blocks that walk each: those that the chip holds at most, divided by
-// the two kinds' steps (a token's angles cost about two).
-static void qk_blocks(QkNormArgs& a, bool wide, int resident, int* blocks) {
+// Shares of query heads and of key heads, and the blocks that walk each. Forward: a warp walks about QKN_RUN steps, so that
+// the blocks that end late are small. Backward: as many blocks as the chip holds at most (each leaves a row of sums),
+// divided so that neither kind's last warp ends much later than the other's; a token's angles cost about one step.
+static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
     const int in_hand = 32 / (a.d / (wide ? 16 : 8));
-    const int n[2] = {a.q_heads, a.heads - a.q_heads};
-    const double cost[2] = {n[0] ? 2.0 + (n[0] + in_hand - 1) / in_hand : 0.0, n[1] ? 2.0 + (n[1] + in_hand - 1) / in_hand : 0.0};
+    long long items[2], most[2], cost[2];
     for (int i = 0; i < 2; ++i) {
-        const int shares = qk_shares(a.T, n[i], a.d, wide);
+        const int n = i == 0 ? a.q_heads : a.heads - a.q_heads;
+        const int shares = qk_shares(a.T, n, a.d, wide);
         (i == 0 ? a.shares : a.k_shares) = shares;
-        const long long most = ((static_cast<long long>(a.T) << shares) + QKN_WARPS - 1) / QKN_WARPS;
-        long long b = static_cast<long long>(resident * cost[i] / (cost[0] + cost[1]) + 0.5);
-        b = b < 1 ? 1 : b > resident - 1 && n[1 - i] ? resident - 1 : b;
-        blocks[i] = n[i] == 0 ? 0 : static_cast<int>(b < most ? b : most);
+        const int steps = n == 0 ? 0 : (n + (in_hand << shares) - 1) / (in_hand << shares);
+        items[i] = n == 0 ? 0 : static_cast<long long>(a.T) << shares;
+        cost[i] = 1 + steps;
+        const int run = steps == 0 || steps > QKN_RUN ? 1 : QKN_RUN / steps;
+        most[i] = (items[i] + QKN_WARPS - 1) / QKN_WARPS;
+        blocks[i] = static_cast<int>(backward ? most[i] : (items[i] + run * QKN_WARPS - 1) / (run * QKN_WARPS));
+        if (!backward && blocks[i] < QKN_PER_SM * 152) blocks[i] = static_cast<int>(most[i] < QKN_PER_SM * 152 ? most[i] : QKN_PER_SM * 152);
+    }
+    if (backward && most[0] + most[1] > QKN_BWD_BLOCKS) {
+        if (items[0] == 0 || items[1] == 0) {
+            blocks[items[0] == 0] = QKN_BWD_BLOCKS;
+        } else {
+            auto rounds = [&](int i, int b) { return (items[i] + b * QKN_WARPS - 1) / (b * QKN_WARPS) * cost[i]; };
+            const double share = static_cast<double>(items[0] * cost[0]) / (items[0] * cost[0] + items[1] * cost[1]);
+            const int guess = static_cast<int>(QKN_BWD_BLOCKS * share);
+            int best = guess < 1 ? 1 : guess > QKN_BWD_BLOCKS - 1 ? QKN_BWD_BLOCKS - 1 : guess;
+            long long span = -1;
+            for (int b = guess - 24 > 1 ? guess - 24 : 1; b <= guess + 24 && b < QKN_BWD_BLOCKS; ++b) {
+                const long long q = rounds(0, b), k = rounds(1, QKN_BWD_BLOCKS - b), t = q > k ? q : k;
+                if (span < 0 || t < span) {
+                    span = t;
+                    best = b;
+                }
+            }
+            blocks[0] = best;
+            blocks[1] = QKN_BWD_BLOCKS - best;
+        }
     }
     a.q_blocks = blocks[0];
 }
@@ -528,7 +555,7 @@ extern "C" mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16
     a.ldy = ldy;
     const bool wide = qk_wide(d, pairs);
     int blocks[2];
-    qk_blocks(a, wide, QKN_PER_SM * 152, blocks);
+    qk_blocks(a, wide, false, blocks);
     const cudaError_t e = qk_dispatch<false>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks[0] + blocks[1],
                                              static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
@@ -581,13 +608,13 @@ extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp
         a.lddy = lddy;
         a.ldy = lddx;
         const bool wide = qk_wide(d, pairs);
-        qk_blocks(a, wide, QKN_BWD_BLOCKS, blocks);
+        qk_blocks(a, wide, true, blocks);
         const cudaError_t e =
             qk_dispatch<true>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks[0] + blocks[1], s);
         if (e != cudaSuccess) return MP_ERR_CUDA;
     }
     // T = 0: no rows, the sums are zero.
-    const cudaError_t e = launch_pdl(qk_norm_dw_kernel, dim3(static_cast<unsigned>(2 * ((d + 31) / 32))), dim3(256), 0, s,
+    const cudaError_t e = launch_pdl(qk_norm_dw_kernel, dim3(static_cast<unsigned>(2 * ((d + 31) / 32))), dim3(1024), 0, s,
                                      static_cast<const float*>(workspace), dwq, dwk, blocks[0], blocks[0] + blocks[1], d);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
