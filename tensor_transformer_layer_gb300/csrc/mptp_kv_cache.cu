@@ -119,13 +119,25 @@ __device__ __forceinline__ float kv_amax_finite(uint32_t w, float m) {
     m = a < __int_as_float(0x7f800000) ? fmaxf(m, a) : m;
     return b < __int_as_float(0x7f800000) ? fmaxf(m, b) : m;
 }
+// Largest magnitudes of pairs of bf16 values, infinities among them; NaN is passed over.
+__device__ __forceinline__ __nv_bfloat162 kv_amax2(uint32_t w, __nv_bfloat162 m) {
+    return __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+}
 
+// Two values as codes. e4m3 has no infinity: one (INF: there are some) becomes NaN, so that whoever reads it sees it.
+template <bool INF>
 __device__ __forceinline__ uint32_t kv_quant2(uint32_t w, float inv) {
     float a = kv_lo(w) * inv, b = kv_hi(w) * inv;
-    // e4m3 has no infinity: one becomes NaN, so that whoever reads it sees that it was there
-    if (isinf(a)) a = __int_as_float(0x7fffffff);
-    if (isinf(b)) b = __int_as_float(0x7fffffff);
+    if constexpr (INF) {
+        if (isinf(a)) a = __int_as_float(0x7fffffff);
+        if (isinf(b)) b = __int_as_float(0x7fffffff);
+    }
     return float2_to_e4m3x2(a, b);
+}
+template <bool INF>
+__device__ __forceinline__ uint2 kv_quant8(const uint4& x, float inv) {
+    return make_uint2(kv_quant2<INF>(x.x, inv) | kv_quant2<INF>(x.y, inv) << 16,
+                      kv_quant2<INF>(x.z, inv) | kv_quant2<INF>(x.w, inv) << 16);
 }
 
 // Four codes times a ratio <= 1, rounded again.
@@ -159,23 +171,36 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvRows r, co
 
     const float before = at.a > 0 && live ? *scale_at : 0.0f;
     uint4 x[NV];
-    float m = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int v = tid + k * r.group;
         x[k] = make_uint4(0, 0, 0, 0);
         if (v < count) x[k] = *reinterpret_cast<const uint4*>(src + v / wide * ld + v % wide * 8);
     }
+    // Over the threads of the unit, the same in all of them.
+    auto largest = [&](float m) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-        m = kv_amax_finite(x[k].x, kv_amax_finite(x[k].y, kv_amax_finite(x[k].z, kv_amax_finite(x[k].w, m))));
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (r.group > 32) {
+            __syncthreads();
+            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+            __syncthreads();
+            const int w0 = threadIdx.x / r.group * (r.group / 32);
+            for (int k = 0; k < r.group / 32; ++k) m = fmaxf(m, red[w0 + k]);
+        }
+        return m;
+    };
+    __nv_bfloat162 m2 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (r.group > 32) {
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-        __syncthreads();
-        const int w0 = threadIdx.x / r.group * (r.group / 32);
-        for (int k = 0; k < r.group / 32; ++k) m = fmaxf(m, red[w0 + k]);
+    for (int k = 0; k < NV; ++k) m2 = kv_amax2(x[k].x, kv_amax2(x[k].y, kv_amax2(x[k].z, kv_amax2(x[k].w, m2))));
+    float m = largest(fmaxf(__low2float(m2), __high2float(m2)));
+    const bool inf = m == __int_as_float(0x7f800000);
+    if (__syncthreads_or(inf)) {  // seldom: the scale goes by the finite values
+        float f = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            f = kv_amax_finite(x[k].x, kv_amax_finite(x[k].y, kv_amax_finite(x[k].z, kv_amax_finite(x[k].w, f))));
+        m = largest(f);
     }
     int e = kv_exponent(m);
     float ratio = 1.0f;  // old codes' factor
@@ -193,12 +218,8 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvRows r, co
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int v = tid + k * r.group;
-        if (v < count) {
-            uint2 c;
-            c.x = kv_quant2(x[k].x, inv) | kv_quant2(x[k].y, inv) << 16;
-            c.y = kv_quant2(x[k].z, inv) | kv_quant2(x[k].w, inv) << 16;
-            *reinterpret_cast<uint2*>(page + at.a * p.d + v * 8) = c;
-        }
+        if (v < count)
+            *reinterpret_cast<uint2*>(page + at.a * p.d + v * 8) = inf ? kv_quant8<true>(x[k], inv) : kv_quant8<false>(x[k], inv);
     }
     if (live && at.a > 0 && ratio != 1.0f) {
         uint2* old = reinterpret_cast<uint2*>(page);
@@ -282,7 +303,7 @@ static long long kv_plan(KvRows& r, const KvPool& p) {
     const long long per_seq = (static_cast<long long>(r.max_n) + p.page - 2) / p.page + 1;
     const long long bound = r.T / p.page + 2LL * r.nseq;
     const long long direct = per_seq * r.nseq;
-    r.per_seq = direct <= 2 * bound ? static_cast<int>(per_seq) : 0;
+    r.per_seq = direct <= bound ? static_cast<int>(per_seq) : 0;
     return r.per_seq > 0 ? direct : bound;
 }
 
@@ -339,15 +360,15 @@ extern "C" mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V, uint8
     r.max_n = max_n;
     r.status = d_status;
     const long long vectors = static_cast<long long>(max_n < page ? max_n : page) * (d / 8);
-    r.group = kv_group(vectors, 8);
+    r.group = kv_group(vectors, 4);
     const int per_cta = KV_THREADS / r.group;
     const long long grid = kv_plan(r, p) * ((2LL * kv_heads + per_cta - 1) / per_cta);
     if (grid > 0x7fffffffLL) return MP_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     st = check_device(&sms);
     if (st != MP_OK) return st;
-    auto kernel = vectors <= 2LL * r.group   ? kv_write_kernel<2>
-                  : vectors <= 8LL * r.group ? kv_write_kernel<8>
+    auto kernel = vectors <= r.group         ? kv_write_kernel<1>
+                  : vectors <= 4LL * r.group ? kv_write_kernel<4>
                                              : kv_write_kernel<16>;
     const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(KV_THREADS), 0,
                                      static_cast<cudaStream_t>(stream), r, p);
