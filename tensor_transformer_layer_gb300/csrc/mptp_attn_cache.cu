@@ -62,7 +62,6 @@ struct AcArgs {
     long long ldq, ldo;
     int nseq, Tq, max_q, heads, group, causal;
     float scale_log2;
-    int page_shift;  // log2 of the page
     uint32_t* status;
 };
 
@@ -298,8 +297,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             const int key = (tile0 + k) * AC_TILE;
             id[0] = id[1] = -1;
             if (k < tiles) {
-                if (key < s.len) id[0] = __ldg(table + (key >> a.page_shift));
-                if (key + 16 < s.len) id[1] = __ldg(table + ((key + 16) >> a.page_shift));
+                if (key < s.len) id[0] = __ldg(table + (key >> p.page_shift));
+                if (key + 16 < s.len) id[1] = __ldg(table + ((key + 16) >> p.page_shift));
             }
         };
         auto issue = [&](int k, const int (&id)[2]) {
@@ -839,7 +838,7 @@ extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, cons
     a.group = heads / kv_heads;
     a.causal = causal != 0;
     a.scale_log2 = scale * AC_LOG2E;
-    a.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+    p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     a.status = d_status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool few = ac_rows(max_q, a.group) == 8;

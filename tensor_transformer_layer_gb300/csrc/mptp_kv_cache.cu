@@ -8,14 +8,16 @@
 //
 // Read. code * scale, rounded to bf16 (exact for scales that a write left, short of bf16's own subnormals).
 //
-// Both are bound by memory: 2 bytes in and 1 out for each element, or 1 in and 2 out. A group of threads takes the rows of one
-// page, head and kind (keys or values), all of them in registers at once, so that the amax and the codes come from one read.
+// Both are bound by memory: 2 bytes in and 1 out for each element, or 1 in and 2 out. A group of threads takes a unit, the rows
+// of one page, head and kind (keys or values), all of them in registers at once, so that the amax and the codes come from one
+// read. A block finds its page once and walks a share of its units.
 #include "mptp_kv_cache.cuh"
 #include "mptp_launch.cuh"
 
 namespace mptp {
 
 constexpr int KV_THREADS = 256;
+constexpr int KV_BLOCKS = 152 * 24;  // blocks that a launch is split into where it has so many units
 
 struct KvRows {
     const __nv_bfloat16* in[2];  // write: new keys and values
@@ -25,7 +27,9 @@ struct KvRows {
     const int32_t* start;  // [nseq] or null: zeros
     int nseq, T, max_n;
     int per_seq;  // pages a sequence may touch: page `item` is that of sequence item / per_seq. 0: found by a search
-    int group;    // threads per page, head and kind: 32 to KV_THREADS
+    int group_shift;     // log2 of the threads of a unit: 32 to KV_THREADS
+    int splits;          // blocks that share a page's units
+    uint32_t per_row;    // ceil(2^32 / (d / 8)): v * per_row >> 32 is the row of vector v (exact for v < 2^16, d <= 256)
     uint32_t* status;
 };
 
@@ -49,7 +53,7 @@ __device__ __forceinline__ void kv_span(const KvRows& r, const KvPool& p, int se
     }
 }
 __device__ __forceinline__ int kv_touched(const KvPool& p, int first, int n) {
-    return n > 0 ? (first + n - 1) / p.page - first / p.page + 1 : 0;
+    return n > 0 ? ((first + n - 1) >> p.page_shift) - (first >> p.page_shift) + 1 : 0;
 }
 
 // The `item`-th page that the call touches; false where there are no so many. With few pages a sequence (per_seq) the
@@ -89,8 +93,8 @@ __device__ __forceinline__ bool kv_pick(const KvRows& r, const KvPool& p, int it
         }
         if (seq < 0) return false;
     }
-    const int logical = first / p.page + at;
-    const int begin = logical * p.page;
+    const int logical = (first >> p.page_shift) + at;
+    const int begin = logical << p.page_shift;
     out.a = max(first - begin, 0);
     out.b = min(first + n - begin, p.page);
     out.row = row0 + (begin + out.a - first);
@@ -150,128 +154,131 @@ __device__ __forceinline__ uint32_t kv_requant4(uint32_t c, float ratio) {
 template <int NV>
 __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvRows r, const KvPool p) {
     __shared__ float red[KV_THREADS / 32];
-    const int per_cta = KV_THREADS / r.group;  // heads (of keys, then of values) that a CTA takes
-    const int parts = (2 * p.kv_heads + per_cta - 1) / per_cta;
-    const int item = blockIdx.x / parts;
-    const int unit = blockIdx.x % parts * per_cta + threadIdx.x / r.group;
-    const int tid = threadIdx.x % r.group;
+    const int group = 1 << r.group_shift, per_cta = KV_THREADS >> r.group_shift;
+    const int item = blockIdx.x / r.splits, split = blockIdx.x % r.splits;
+    const int tid = threadIdx.x & (group - 1), wide = p.d >> 3;
     grid_dependency_wait();
     grid_launch_dependents();
     KvPage at;
     if (!kv_pick(r, p, item, at)) return;
-    const bool live = unit < 2 * p.kv_heads;
-    const int kind = live && unit >= p.kv_heads ? 1 : 0;
-    const int head = live ? unit - kind * p.kv_heads : 0;
-    const int wide = p.d / 8;  // vectors a row
-    const int count = live ? (at.b - at.a) * wide : 0;
-    const long long ld = kind ? r.ld[1] : r.ld[0];
-    const __nv_bfloat16* src = (kind ? r.in[1] : r.in[0]) + at.row * ld + head * p.d;
-    uint8_t* page = p.head_codes(kind, at.id, head);
-    float* scale_at = p.head_scale(kind, at.id, head);
-
-    const float before = at.a > 0 && live ? *scale_at : 0.0f;
-    uint4 x[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int v = tid + k * r.group;
-        x[k] = make_uint4(0, 0, 0, 0);
-        if (v < count) x[k] = *reinterpret_cast<const uint4*>(src + v / wide * ld + v % wide * 8);
-    }
+    const int count = (at.b - at.a) * wide;
     // Over the threads of the unit, the same in all of them.
     auto largest = [&](float m) {
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        if (r.group > 32) {
+        if (group > 32) {
             __syncthreads();
             if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
             __syncthreads();
-            const int w0 = threadIdx.x / r.group * (r.group / 32);
-            for (int k = 0; k < r.group / 32; ++k) m = fmaxf(m, red[w0 + k]);
+            const int w0 = threadIdx.x >> r.group_shift << (r.group_shift - 5);
+            for (int k = 0; k < group >> 5; ++k) m = fmaxf(m, red[w0 + k]);
         }
         return m;
     };
-    __nv_bfloat162 m2 = __floats2bfloat162_rn(0.0f, 0.0f);
+    for (int unit0 = split * per_cta; unit0 < 2 * p.kv_heads; unit0 += r.splits * per_cta) {
+        const int unit = unit0 + (threadIdx.x >> r.group_shift);
+        const bool live = unit < 2 * p.kv_heads;
+        const int kind = live && unit >= p.kv_heads ? 1 : 0;
+        const int head = live ? unit - kind * p.kv_heads : 0;
+        const long long ld = kind ? r.ld[1] : r.ld[0];
+        const __nv_bfloat16* src = (kind ? r.in[1] : r.in[0]) + at.row * ld + head * p.d;
+        uint8_t* page = p.head_codes(kind, at.id, head);
+        float* scale_at = p.head_scale(kind, at.id, head);
+
+        const float before = at.a > 0 && live ? *scale_at : 0.0f;
+        uint4 x[NV];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) m2 = kv_amax2(x[k].x, kv_amax2(x[k].y, kv_amax2(x[k].z, kv_amax2(x[k].w, m2))));
-    float m = largest(fmaxf(__low2float(m2), __high2float(m2)));
-    const bool inf = m == __int_as_float(0x7f800000);
-    if (__syncthreads_or(inf)) {  // seldom: the scale goes by the finite values
-        float f = 0.0f;
+        for (int k = 0; k < NV; ++k) {
+            const int v = tid + (k << r.group_shift);
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (live && v < count) {
+                const int row = __umulhi(v, r.per_row);
+                x[k] = *reinterpret_cast<const uint4*>(src + row * ld + (v - row * wide) * 8);
+            }
+        }
+        __nv_bfloat162 m2 = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) m2 = kv_amax2(x[k].x, kv_amax2(x[k].y, kv_amax2(x[k].z, kv_amax2(x[k].w, m2))));
+        float m = largest(fmaxf(__low2float(m2), __high2float(m2)));
+        const bool inf = m == __int_as_float(0x7f800000);
+        if (__syncthreads_or(inf)) {  // seldom: the scale goes by the finite values
+            float f = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                f = kv_amax_finite(x[k].x, kv_amax_finite(x[k].y, kv_amax_finite(x[k].z, kv_amax_finite(x[k].w, f))));
+            m = largest(f);
+        }
+        int e = kv_exponent(m);
+        float ratio = 1.0f;  // old codes' factor
+        if (at.a > 0) {
+            // The page's scale so far; one that no write can have left (not in (0, 2^120]) makes its old codes NaN.
+            if (before > 0.0f && before <= kv_pow2(120)) {
+                const uint32_t u = __float_as_uint(before);
+                e = max(e, static_cast<int>(u >> 23) - 127 + ((u & 0x7fffffu) != 0 ? 1 : 0));
+                ratio = before * kv_pow2(-e);
+            } else {
+                ratio = __int_as_float(0x7fffffff);
+            }
+        }
+        if (!live) continue;
+        const float inv = kv_pow2(-e);
+        uint8_t* to = page + at.a * p.d + tid * 8;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            f = kv_amax_finite(x[k].x, kv_amax_finite(x[k].y, kv_amax_finite(x[k].z, kv_amax_finite(x[k].w, f))));
-        m = largest(f);
-    }
-    int e = kv_exponent(m);
-    float ratio = 1.0f;  // old codes' factor
-    if (at.a > 0) {
-        // The page's scale so far; one that no write can have left (not in (0, 2^120]) makes its old codes NaN.
-        if (before > 0.0f && before <= kv_pow2(120)) {
-            const uint32_t u = __float_as_uint(before);
-            e = max(e, static_cast<int>(u >> 23) - 127 + ((u & 0x7fffffu) != 0 ? 1 : 0));
-            ratio = before * kv_pow2(-e);
-        } else {
-            ratio = __int_as_float(0x7fffffff);
+            if (tid + (k << r.group_shift) < count)
+                *reinterpret_cast<uint2*>(to + (k << (r.group_shift + 3))) = inf ? kv_quant8<true>(x[k], inv) : kv_quant8<false>(x[k], inv);
+        if (at.a > 0 && ratio != 1.0f) {
+            uint2* old = reinterpret_cast<uint2*>(page);
+            for (int v = tid; v < at.a * wide; v += group) {
+                uint2 c = old[v];
+                c.x = kv_requant4(c.x, ratio);
+                c.y = kv_requant4(c.y, ratio);
+                old[v] = c;
+            }
         }
+        if (tid == 0) *scale_at = kv_pow2(e);
     }
-    const float inv = kv_pow2(-e);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int v = tid + k * r.group;
-        if (v < count)
-            *reinterpret_cast<uint2*>(page + at.a * p.d + v * 8) = inf ? kv_quant8<true>(x[k], inv) : kv_quant8<false>(x[k], inv);
-    }
-    if (live && at.a > 0 && ratio != 1.0f) {
-        uint2* old = reinterpret_cast<uint2*>(page);
-        for (int v = tid; v < at.a * wide; v += r.group) {
-            uint2 c = old[v];
-            c.x = kv_requant4(c.x, ratio);
-            c.y = kv_requant4(c.y, ratio);
-            old[v] = c;
-        }
-    }
-    if (live && tid == 0) *scale_at = kv_pow2(e);
+}
+
+// Four codes as values, rounded to bf16.
+__device__ __forceinline__ uint2 kv_values4(uint32_t c, float scale) {
+    const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(c)), b = f16x2_to_float2(e4m3x2_hi_to_f16x2(c));
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * scale, a.y * scale), hi = __floats2bfloat162_rn(b.x * scale, b.y * scale);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvRows r, const KvPool p) {
-    const int per_cta = KV_THREADS / r.group;
-    const int parts = (2 * p.kv_heads + per_cta - 1) / per_cta;
-    const int item = blockIdx.x / parts;
-    const int unit = blockIdx.x % parts * per_cta + threadIdx.x / r.group;
-    const int tid = threadIdx.x % r.group;
+    constexpr int NV = 4;
+    const int group = 1 << r.group_shift, per_cta = KV_THREADS >> r.group_shift;
+    const int item = blockIdx.x / r.splits, split = blockIdx.x % r.splits;
+    const int tid = threadIdx.x & (group - 1), wide = p.d >> 3;
     grid_dependency_wait();
     grid_launch_dependents();
     KvPage at;
     if (!kv_pick(r, p, item, at)) return;
-    if (unit >= 2 * p.kv_heads) return;
-    const int kind = unit >= p.kv_heads ? 1 : 0;
-    const int head = unit - kind * p.kv_heads;
-    const int wide = p.d / 16;
     const int count = (at.b - at.a) * wide;
-    const long long ld = kind ? r.ld[1] : r.ld[0];
-    __nv_bfloat16* dst = (kind ? r.out[1] : r.out[0]) + at.row * ld + head * p.d;
-    const uint4* src = reinterpret_cast<const uint4*>(p.head_codes(kind, at.id, head) + at.a * p.d);
-    const float scale = *p.head_scale(kind, at.id, head);
-    for (int v0 = tid; v0 < count; v0 += 4 * r.group) {
-        uint4 c[4];
+    for (int unit = split * per_cta + (threadIdx.x >> r.group_shift); unit < 2 * p.kv_heads; unit += r.splits * per_cta) {
+        const int kind = unit >= p.kv_heads ? 1 : 0;
+        const int head = unit - kind * p.kv_heads;
+        const long long ld = kind ? r.ld[1] : r.ld[0];
+        __nv_bfloat16* dst = (kind ? r.out[1] : r.out[0]) + at.row * ld + head * p.d;
+        const uint2* src = reinterpret_cast<const uint2*>(p.head_codes(kind, at.id, head) + at.a * p.d);
+        const float scale = *p.head_scale(kind, at.id, head);
+        for (int v0 = tid; v0 < count; v0 += NV << r.group_shift) {
+            uint2 c[NV];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (v0 + k * r.group < count) c[k] = src[v0 + k * r.group];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int v = v0 + k * r.group;
-            if (v >= count) continue;
-            const uint32_t in[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 f = f16x2_to_float2(j % 2 ? e4m3x2_hi_to_f16x2(in[j / 2]) : e4m3x2_to_f16x2(in[j / 2]));
-                __nv_bfloat162 b = __floats2bfloat162_rn(f.x * scale, f.y * scale);
-                o[j] = *reinterpret_cast<uint32_t*>(&b);
+            for (int k = 0; k < NV; ++k) {
+                const int v = v0 + (k << r.group_shift);
+                if (v < count) c[k] = src[v];
             }
-            uint4* to = reinterpret_cast<uint4*>(dst + v / wide * ld + v % wide * 16);
-            to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int v = v0 + (k << r.group_shift);
+                if (v >= count) break;
+                const uint2 lo = kv_values4(c[k].x, scale), hi = kv_values4(c[k].y, scale);
+                const int row = __umulhi(v, r.per_row);
+                *reinterpret_cast<uint4*>(dst + row * ld + (v - row * wide) * 8) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
         }
     }
 }
@@ -297,14 +304,23 @@ static mp_status kv_rows_check(const void* K, const void* V, const void* kc, con
     return aligned16(K) && aligned16(V) && word(cu) && word(start) && word(d_status) ? MP_OK : MP_ERR_MISALIGNED;
 }
 
-// Pages in the launch (-1: more than a grid holds), and how a CTA finds its own.
-static long long kv_plan(KvRows& r, const KvPool& p) {
+// The blocks of the launch, and how one finds its page and its units. A thread holds up to `most` of a unit's vectors.
+static long long kv_plan(KvRows& r, const KvPool& p, int most) {
+    const long long vectors = static_cast<long long>(r.max_n < p.page ? r.max_n : p.page) * (p.d / 8);
+    r.group_shift = 5;
+    while ((1 << r.group_shift) < KV_THREADS && vectors > static_cast<long long>(most) << r.group_shift) ++r.group_shift;
+    r.per_row = static_cast<uint32_t>(((1ull << 32) + p.d / 8 - 1) / (p.d / 8));
     // A sequence's n rows touch at most this many pages, all sequences' at most `bound`.
     const long long per_seq = (static_cast<long long>(r.max_n) + p.page - 2) / p.page + 1;
     const long long bound = r.T / p.page + 2LL * r.nseq;
     const long long direct = per_seq * r.nseq;
     r.per_seq = direct <= bound ? static_cast<int>(per_seq) : 0;
-    return r.per_seq > 0 ? direct : bound;
+    const long long pages = r.per_seq > 0 ? direct : bound;
+    // Enough blocks that the last ones are a small part, each with as many units as that leaves.
+    const int parts = (2 * p.kv_heads + (KV_THREADS >> r.group_shift) - 1) / (KV_THREADS >> r.group_shift);
+    const long long splits = (KV_BLOCKS + pages - 1) / pages;
+    r.splits = static_cast<int>(splits < parts ? splits : parts);
+    return pages * r.splits;
 }
 
 static KvPool kv_pool(uint8_t* kc, uint8_t* vc, float* ks, float* vs, const int32_t* table, int pages, int max_pages,
@@ -324,14 +340,8 @@ static KvPool kv_pool(uint8_t* kc, uint8_t* vc, float* ks, float* vs, const int3
     p.page = page;
     p.kv_heads = kv_heads;
     p.d = d;
+    p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     return p;
-}
-
-// Threads per page, head and kind: a warp, doubled while a thread would hold more than `most` vectors.
-static int kv_group(long long vectors, int most) {
-    int g = 32;
-    while (g < KV_THREADS && vectors > static_cast<long long>(g) * most) g *= 2;
-    return g;
 }
 
 }  // namespace mptp
@@ -359,17 +369,13 @@ extern "C" mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V, uint8
     r.T = T;
     r.max_n = max_n;
     r.status = d_status;
-    const long long vectors = static_cast<long long>(max_n < page ? max_n : page) * (d / 8);
-    r.group = kv_group(vectors, 4);
-    const int per_cta = KV_THREADS / r.group;
-    const long long grid = kv_plan(r, p) * ((2LL * kv_heads + per_cta - 1) / per_cta);
+    const long long grid = kv_plan(r, p, 4);
     if (grid > 0x7fffffffLL) return MP_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     st = check_device(&sms);
     if (st != MP_OK) return st;
-    auto kernel = vectors <= r.group         ? kv_write_kernel<1>
-                  : vectors <= 4LL * r.group ? kv_write_kernel<4>
-                                             : kv_write_kernel<16>;
+    const int vectors = ceil_div(static_cast<long long>(max_n < page ? max_n : page) * (d / 8), 1 << r.group_shift);
+    auto kernel = vectors <= 1 ? kv_write_kernel<1> : vectors <= 4 ? kv_write_kernel<4> : kv_write_kernel<16>;
     const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(KV_THREADS), 0,
                                      static_cast<cudaStream_t>(stream), r, p);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
@@ -398,9 +404,7 @@ extern "C" mp_status mp_kv_cache_read(const uint8_t* kc, const uint8_t* vc, cons
     r.T = T;
     r.max_n = max_n;
     r.status = d_status;
-    r.group = kv_group(static_cast<long long>(max_n < page ? max_n : page) * (d / 16), 4);
-    const int per_cta = KV_THREADS / r.group;
-    const long long grid = kv_plan(r, p) * ((2LL * kv_heads + per_cta - 1) / per_cta);
+    const long long grid = kv_plan(r, p, 4);
     if (grid > 0x7fffffffLL) return MP_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     st = check_device(&sms);

@@ -21,6 +21,7 @@ struct KvPool {
     long long ld_codes[2], ld_scales[2];  // from page to page
     const int32_t* table;                 // [nseq][max_pages]
     int pages, max_pages, page, kv_heads, d;
+    int page_shift;                       // log2 of the page
     __device__ __forceinline__ uint8_t* head_codes(int kind, long long id, int head) const {
         return (kind ? codes[1] + id * ld_codes[1] : codes[0] + id * ld_codes[0]) + static_cast<long long>(head) * page * d;
     }
