@@ -11,13 +11,18 @@
 // Both are bound by memory: 2 bytes in and 1 out for each element, or 1 in and 2 out. A group of threads takes a unit, the rows
 // of one page, head and kind (keys or values), all of them in registers at once, so that the amax and the codes come from one
 // read. A block finds its page once and walks a share of its units.
+#include <type_traits>
+
 #include "mptp_kv_cache.cuh"
 #include "mptp_launch.cuh"
 
 namespace mptp {
 
-constexpr int KV_THREADS = 256;
-constexpr int KV_BLOCKS = 152 * 24;  // blocks that a launch is split into where it has so many units
+// Threads of a block, and blocks that a launch is split into where it has so many units.
+constexpr int KV_WRITE_THREADS = 128;  // or twice as many, where a unit's vectors fill them
+constexpr int KV_WRITE_BLOCKS = 152 * 3;
+constexpr int KV_READ_THREADS = 256;
+constexpr int KV_READ_BLOCKS = 152 * 24;
 
 struct KvRows {
     const __nv_bfloat16* in[2];  // write: new keys and values
@@ -27,7 +32,7 @@ struct KvRows {
     const int32_t* start;  // [nseq] or null: zeros
     int nseq, T, max_n;
     int per_seq;  // pages a sequence may touch: page `item` is that of sequence item / per_seq. 0: found by a search
-    int group_shift;     // log2 of the threads of a unit: 32 to KV_THREADS
+    int group_shift;     // log2 of the threads of a unit: 32 to a block's
     int splits;          // blocks that share a page's units
     uint32_t per_row;    // ceil(2^32 / (d / 8)): v * per_row >> 32 is the row of vector v (exact for v < 2^16, d <= 256)
     uint32_t* status;
@@ -151,10 +156,10 @@ __device__ __forceinline__ uint32_t kv_requant4(uint32_t c, float ratio) {
 }
 
 // NV: vectors of eight elements that a thread holds.
-template <int NV>
-__global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvRows r, const KvPool p) {
-    __shared__ float red[KV_THREADS / 32];
-    const int group = 1 << r.group_shift, per_cta = KV_THREADS >> r.group_shift;
+template <int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_write_kernel(const KvRows r, const KvPool p) {
+    __shared__ float red[THREADS / 32];
+    const int group = 1 << r.group_shift, per_cta = THREADS >> r.group_shift;
     const int item = blockIdx.x / r.splits, split = blockIdx.x % r.splits;
     const int tid = threadIdx.x & (group - 1), wide = p.d >> 3;
     grid_dependency_wait();
@@ -175,27 +180,40 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvRows r, co
         }
         return m;
     };
-    for (int unit0 = split * per_cta; unit0 < 2 * p.kv_heads; unit0 += r.splits * per_cta) {
+    struct Unit {
+        bool live;
+        uint8_t* page;
+        float* scale;
+        float before;
+        uint4 x[NV];
+    };
+    auto load = [&](int unit0) {
+        Unit u;
         const int unit = unit0 + (threadIdx.x >> r.group_shift);
-        const bool live = unit < 2 * p.kv_heads;
-        const int kind = live && unit >= p.kv_heads ? 1 : 0;
-        const int head = live ? unit - kind * p.kv_heads : 0;
+        u.live = unit < 2 * p.kv_heads;
+        const int kind = u.live && unit >= p.kv_heads ? 1 : 0;
+        const int head = u.live ? unit - kind * p.kv_heads : 0;
         const long long ld = kind ? r.ld[1] : r.ld[0];
         const __nv_bfloat16* src = (kind ? r.in[1] : r.in[0]) + at.row * ld + head * p.d;
-        uint8_t* page = p.head_codes(kind, at.id, head);
-        float* scale_at = p.head_scale(kind, at.id, head);
-
-        const float before = at.a > 0 && live ? *scale_at : 0.0f;
-        uint4 x[NV];
+        u.page = p.head_codes(kind, at.id, head);
+        u.scale = p.head_scale(kind, at.id, head);
+        u.before = at.a > 0 && u.live ? *u.scale : 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = tid + (k << r.group_shift);
-            x[k] = make_uint4(0, 0, 0, 0);
-            if (live && v < count) {
+            u.x[k] = make_uint4(0, 0, 0, 0);
+            if (u.live && v < count) {
                 const int row = __umulhi(v, r.per_row);
-                x[k] = *reinterpret_cast<const uint4*>(src + row * ld + (v - row * wide) * 8);
+                u.x[k] = *reinterpret_cast<const uint4*>(src + row * ld + (v - row * wide) * 8);
             }
         }
+        return u;
+    };
+    const int step = r.splits * per_cta;
+    Unit next = load(split * per_cta);
+    for (int unit0 = split * per_cta; unit0 < 2 * p.kv_heads; unit0 += step) {
+        const Unit u = next;
+        const uint4(&x)[NV] = u.x;
         __nv_bfloat162 m2 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) m2 = kv_amax2(x[k].x, kv_amax2(x[k].y, kv_amax2(x[k].z, kv_amax2(x[k].w, m2))));
@@ -208,27 +226,34 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvRows r, co
                 f = kv_amax_finite(x[k].x, kv_amax_finite(x[k].y, kv_amax_finite(x[k].z, kv_amax_finite(x[k].w, f))));
             m = largest(f);
         }
+        if (unit0 + step < 2 * p.kv_heads) next = load(unit0 + step);
         int e = kv_exponent(m);
         float ratio = 1.0f;  // old codes' factor
         if (at.a > 0) {
             // The page's scale so far; one that no write can have left (not in (0, 2^120]) makes its old codes NaN.
-            if (before > 0.0f && before <= kv_pow2(120)) {
-                const uint32_t u = __float_as_uint(before);
-                e = max(e, static_cast<int>(u >> 23) - 127 + ((u & 0x7fffffu) != 0 ? 1 : 0));
-                ratio = before * kv_pow2(-e);
+            if (u.before > 0.0f && u.before <= kv_pow2(120)) {
+                const uint32_t bits = __float_as_uint(u.before);
+                e = max(e, static_cast<int>(bits >> 23) - 127 + ((bits & 0x7fffffu) != 0 ? 1 : 0));
+                ratio = u.before * kv_pow2(-e);
             } else {
                 ratio = __int_as_float(0x7fffffff);
             }
         }
-        if (!live) continue;
+        if (!u.live) continue;
         const float inv = kv_pow2(-e);
-        uint8_t* to = page + at.a * p.d + tid * 8;
+        uint8_t* to = u.page + at.a * p.d + tid * 8;
+        auto put = [&](auto with_inf) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (tid + (k << r.group_shift) < count)
-                *reinterpret_cast<uint2*>(to + (k << (r.group_shift + 3))) = inf ? kv_quant8<true>(x[k], inv) : kv_quant8<false>(x[k], inv);
+            for (int k = 0; k < NV; ++k)
+                if (tid + (k << r.group_shift) < count)
+                    *reinterpret_cast<uint2*>(to + (k << (r.group_shift + 3))) = kv_quant8<with_inf.value>(x[k], inv);
+        };
+        if (inf)
+            put(std::true_type{});
+        else
+            put(std::false_type{});
         if (at.a > 0 && ratio != 1.0f) {
-            uint2* old = reinterpret_cast<uint2*>(page);
+            uint2* old = reinterpret_cast<uint2*>(u.page);
             for (int v = tid; v < at.a * wide; v += group) {
                 uint2 c = old[v];
                 c.x = kv_requant4(c.x, ratio);
@@ -236,7 +261,7 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvRows r, co
                 old[v] = c;
             }
         }
-        if (tid == 0) *scale_at = kv_pow2(e);
+        if (tid == 0) *u.scale = kv_pow2(e);
     }
 }
 
@@ -247,9 +272,9 @@ __device__ __forceinline__ uint2 kv_values4(uint32_t c, float scale) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-__global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvRows r, const KvPool p) {
+__global__ void __launch_bounds__(KV_READ_THREADS) kv_read_kernel(const KvRows r, const KvPool p) {
     constexpr int NV = 4;
-    const int group = 1 << r.group_shift, per_cta = KV_THREADS >> r.group_shift;
+    const int group = 1 << r.group_shift, per_cta = KV_READ_THREADS >> r.group_shift;
     const int item = blockIdx.x / r.splits, split = blockIdx.x % r.splits;
     const int tid = threadIdx.x & (group - 1), wide = p.d >> 3;
     grid_dependency_wait();
@@ -305,10 +330,10 @@ static mp_status kv_rows_check(const void* K, const void* V, const void* kc, con
 }
 
 // The blocks of the launch, and how one finds its page and its units. A thread holds up to `most` of a unit's vectors.
-static long long kv_plan(KvRows& r, const KvPool& p, int most) {
+static long long kv_plan(KvRows& r, const KvPool& p, int threads, int most, int blocks) {
     const long long vectors = static_cast<long long>(r.max_n < p.page ? r.max_n : p.page) * (p.d / 8);
     r.group_shift = 5;
-    while ((1 << r.group_shift) < KV_THREADS && vectors > static_cast<long long>(most) << r.group_shift) ++r.group_shift;
+    while ((1 << r.group_shift) < threads && vectors > static_cast<long long>(most) << r.group_shift) ++r.group_shift;
     r.per_row = static_cast<uint32_t>(((1ull << 32) + p.d / 8 - 1) / (p.d / 8));
     // A sequence's n rows touch at most this many pages, all sequences' at most `bound`.
     const long long per_seq = (static_cast<long long>(r.max_n) + p.page - 2) / p.page + 1;
@@ -317,8 +342,8 @@ static long long kv_plan(KvRows& r, const KvPool& p, int most) {
     r.per_seq = direct <= bound ? static_cast<int>(per_seq) : 0;
     const long long pages = r.per_seq > 0 ? direct : bound;
     // Enough blocks that the last ones are a small part, each with as many units as that leaves.
-    const int parts = (2 * p.kv_heads + (KV_THREADS >> r.group_shift) - 1) / (KV_THREADS >> r.group_shift);
-    const long long splits = (KV_BLOCKS + pages - 1) / pages;
+    const int parts = (2 * p.kv_heads + (threads >> r.group_shift) - 1) / (threads >> r.group_shift);
+    const long long splits = (blocks + pages - 1) / pages;
     r.splits = static_cast<int>(splits < parts ? splits : parts);
     return pages * r.splits;
 }
@@ -369,14 +394,19 @@ extern "C" mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V, uint8
     r.T = T;
     r.max_n = max_n;
     r.status = d_status;
-    const long long grid = kv_plan(r, p, 4);
+    const int vectors = (max_n < page ? max_n : page) * (d / 8);  // of a unit
+    const int threads = vectors > 8 * KV_WRITE_THREADS ? 2 * KV_WRITE_THREADS : KV_WRITE_THREADS;
+    const long long grid = kv_plan(r, p, threads, 8, KV_WRITE_BLOCKS);
     if (grid > 0x7fffffffLL) return MP_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     st = check_device(&sms);
     if (st != MP_OK) return st;
-    const int vectors = ceil_div(static_cast<long long>(max_n < page ? max_n : page) * (d / 8), 1 << r.group_shift);
-    auto kernel = vectors <= 1 ? kv_write_kernel<1> : vectors <= 4 ? kv_write_kernel<4> : kv_write_kernel<16>;
-    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(KV_THREADS), 0,
+    const int held = ceil_div(vectors, 1 << r.group_shift);
+    auto kernel = held > 8                       ? kv_write_kernel<16, 2 * KV_WRITE_THREADS>
+                  : threads > KV_WRITE_THREADS ? kv_write_kernel<8, 2 * KV_WRITE_THREADS>
+                  : held > 1                   ? kv_write_kernel<8, KV_WRITE_THREADS>
+                                               : kv_write_kernel<1, KV_WRITE_THREADS>;
+    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0,
                                      static_cast<cudaStream_t>(stream), r, p);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
@@ -404,12 +434,12 @@ extern "C" mp_status mp_kv_cache_read(const uint8_t* kc, const uint8_t* vc, cons
     r.T = T;
     r.max_n = max_n;
     r.status = d_status;
-    const long long grid = kv_plan(r, p, 4);
+    const long long grid = kv_plan(r, p, KV_READ_THREADS, 4, KV_READ_BLOCKS);
     if (grid > 0x7fffffffLL) return MP_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     st = check_device(&sms);
     if (st != MP_OK) return st;
-    const cudaError_t e = launch_pdl(kv_read_kernel, dim3(static_cast<unsigned>(grid)), dim3(KV_THREADS), 0,
+    const cudaError_t e = launch_pdl(kv_read_kernel, dim3(static_cast<unsigned>(grid)), dim3(KV_READ_THREADS), 0,
                                      static_cast<cudaStream_t>(stream), r, p);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
