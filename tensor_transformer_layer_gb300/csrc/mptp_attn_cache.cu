@@ -31,9 +31,8 @@
 #include "mptp_launch.cuh"
 
 namespace mptp {
+constexpr int W641 = 8, W642 = 8, W961 = 8, W962 = 8, W1281 = 8, W1282 = 8, S641 = 3, S642 = 3, S961 = 3, S962 = 3, S1281 = 2, S1282 = 2;
 
-constexpr int AC_WARPS = 8;
-constexpr int AC_THREADS = AC_WARPS * 32;
 constexpr int AC_TILE = 32;     // keys
 constexpr int AC_ITEM = 4;      // places of an item besides its tiles
 constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
@@ -115,17 +114,22 @@ __device__ __forceinline__ float ac_ex2(float x) {
     return y;
 }
 
+// Warps of a CTA and the tiles of a warp's ring.
+constexpr int ac_warps(int d, int nt) { return d == 64 ? (nt == 1 ? W641 : W642) : d == 96 ? (nt == 1 ? W961 : W962) : (nt == 1 ? W1281 : W1282); }
+constexpr int ac_stages(int d, int nt) { return d == 64 ? (nt == 1 ? S641 : S642) : d == 96 ? (nt == 1 ? S961 : S962) : (nt == 1 ? S1281 : S1282); }
+
 template <int D, int NT>
 struct AcShape {
     static constexpr int ROWS = 8 * NT;              // queries of a row tile
-    static constexpr int STAGES = D == 128 && NT == 2 ? 2 : 3;
+    static constexpr int WARPS = ac_warps(D, NT);
+    static constexpr int STAGES = ac_stages(D, NT);
     static constexpr int STAGE = 2 * AC_TILE * D;    // bytes of K and V
     static constexpr int RING = STAGES * STAGE;      // a warp's; then the record of the item that its run ends in
     static constexpr int HEAD = ROWS * D * 4;        // the record of the item that its run begins in
     static constexpr int WARP = RING + HEAD;
     static constexpr int SCALES = STAGES * 16;       // a warp's: two of K, two of V
     static constexpr int STATS = 2 * ROWS * 8;       // a warp's: (reference, sum) of its records' rows
-    static constexpr int SMEM = AC_WARPS * (WARP + SCALES + STATS);
+    static constexpr int SMEM = WARPS * (WARP + SCALES + STATS);
     static constexpr int PART = ROWS * (D + 2);      // floats of a part
     static_assert(HEAD <= RING && SMEM <= 231424, "shared memory");
 };
@@ -184,14 +188,14 @@ __device__ __forceinline__ void ac_store(const AcArgs& a, int q0, int head, int 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs a, const KvPool p) {
+__global__ void __launch_bounds__(ac_warps(D, NT) * 32, 1) attn_cache_kernel(const AcArgs a, const KvPool p) {
     using C = AcShape<D, NT>;
     constexpr int KS = D / 16;   // products along d of one score tile; also tiles of 16 rows of O^T
     constexpr int CH = D / 16;   // 16-byte chunks a key row
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ AcRecord rec[2 * AC_WARPS];
+    __shared__ AcRecord rec[2 * C::WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    float* stats = reinterpret_cast<float*>(smem + AC_WARPS * (C::WARP + C::SCALES));  // [warp][2][row]{m, l}
+    float* stats = reinterpret_cast<float*>(smem + C::WARPS * (C::WARP + C::SCALES));  // [warp][2][row]{m, l}
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         upto = look_at(0);
     }
     // As many CTAs as have a few places for each of their warps.
-    const long long want = (total + 2 * AC_WARPS - 1) / (2 * AC_WARPS);
+    const long long want = (total + 2 * C::WARPS - 1) / (2 * C::WARPS);
     const int ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : static_cast<long long>(gridDim.x));
     const int cta = blockIdx.x;
     AcItem* left = a.items + cta;
@@ -230,8 +234,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     if (cta >= ctas) return;
     if (lane < 2) rec[2 * warp + lane].u0 = -1;
     const long long cta_pos = ac_share(total, cta, ctas), cta_end = ac_share(total, cta + 1, ctas);
-    long long pos = cta_pos + (cta_end - cta_pos) * warp / AC_WARPS;
-    const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / AC_WARPS;
+    long long pos = cta_pos + (cta_end - cta_pos) * warp / C::WARPS;
+    const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / C::WARPS;
     int seq = 0;
     long long seq_start = 0;
     AcSeq s = held[0];
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 
     uint8_t* ring = smem + warp * C::WARP;
     const uint32_t ring_u = smem_u32(ring);
-    float* ring_scales = reinterpret_cast<float*>(smem + AC_WARPS * C::WARP + warp * C::SCALES);
+    float* ring_scales = reinterpret_cast<float*>(smem + C::WARPS * C::WARP + warp * C::SCALES);
     const uint32_t ring_scales_u = smem_u32(ring_scales);
 
     while (pos < end) {
@@ -289,33 +293,42 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const int rows = min(C::ROWS, s.nq * a.group - row0);
         const int32_t* table = p.table + static_cast<long long>(seq) * p.max_pages;
 
-        // Copies of tile k of this run into stage k % STAGES. Pages are looked up one tile earlier, the first ones at once.
+        // Copies of tile k of this run into stage k % STAGES. Pages are looked up one tile earlier, the first ones at once; a
+        // tile of 32 keys lies in one page, or in two of 16.
         const int tiles = tile1 - tile0;
         const uint8_t* k_codes = p.head_codes(0, 0, head) + lane * 16;
         const uint8_t* v_codes = p.head_codes(1, 0, head) + lane * 16;
+        // Lanes 0 to 3 bring the scales: of keys, of values, of either half.
+        const float* my_scales = p.head_scale(lane >> 1 & 1, 0, head);
+        const uint32_t pitch_scales = lane & 2 ? p.pitch_scales[1] : p.pitch_scales[0];
+        auto page_at = [&](const uint8_t* base, int kind, int id) {
+            return base + (static_cast<uint64_t>(static_cast<uint32_t>(id)) * p.pitch16[kind] << 4);
+        };
+        const bool two = p.page == 16;
         auto look = [&](int k, int (&id)[2]) {
             const int key = (tile0 + k) * AC_TILE;
-            id[0] = id[1] = -1;
-            if (k < tiles) {
-                if (key < s.len) id[0] = __ldg(table + (key >> p.page_shift));
-                if (key + 16 < s.len) id[1] = __ldg(table + ((key + 16) >> p.page_shift));
-            }
+            id[0] = -1;
+            if (key < s.len) id[0] = __ldg(table + (key >> p.page_shift));
+            id[1] = id[0];
+            if (two) id[1] = key + 16 < s.len ? __ldg(table + (key >> 4) + 1) : -1;
         };
         auto issue = [&](int k, const int (&id)[2]) {
             if (k < tiles) {
                 const int key0 = (tile0 + k) * AC_TILE;
                 const int st = k % C::STAGES;
                 const uint32_t dst = ring_u + st * C::STAGE;
-                const bool full = key0 + AC_TILE <= s.len && static_cast<unsigned>(id[0]) < static_cast<unsigned>(p.pages) &&
-                                  static_cast<unsigned>(id[1]) < static_cast<unsigned>(p.pages);
+                const int slot = (key0 & (p.page - 1)) * D;
+                const bool inside0 = static_cast<unsigned>(id[0]) < static_cast<unsigned>(p.pages);
+                const bool inside1 = static_cast<unsigned>(id[1]) < static_cast<unsigned>(p.pages);
+                if (key0 + AC_TILE <= s.len && inside0 && inside1) {
+                    const uint8_t* ks = page_at(k_codes, 0, id[0]) + slot;
+                    const uint8_t* vs = page_at(v_codes, 1, id[0]) + slot;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int slot = ((key0 + h * 16) & (p.page - 1)) * D;
-                    const bool inside = static_cast<unsigned>(id[h]) < static_cast<unsigned>(p.pages);
-                    const int page = inside ? id[h] : 0;
-                    const uint8_t* ks = k_codes + page * p.ld_codes[0] + slot;
-                    const uint8_t* vs = v_codes + page * p.ld_codes[1] + slot;
-                    if (full) {
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1) {
+                            ks = two ? page_at(k_codes, 0, id[1]) : ks + 16 * D;
+                            vs = two ? page_at(v_codes, 1, id[1]) : vs + 16 * D;
+                        }
 #pragma unroll
                         for (int i = 0; i < CH / 2; ++i) {  // 16 rows, 32 chunks a step
                             const int c = i * 32 + lane;
@@ -323,7 +336,17 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                             ac_copy16(at, ks + i * 512);
                             ac_copy16(at + AC_TILE * D, vs + i * 512);
                         }
-                    } else {
+                    }
+                    if (lane < 4) ac_copy4(ring_scales_u + (st * 4 + lane) * 4, my_scales + static_cast<uint64_t>(static_cast<uint32_t>(lane & 1 ? id[1] : id[0])) * pitch_scales, true);
+                } else {
+                    // The sequence's last tile, or a page that is not in the pool: zeros where there is no token, NaN as the
+                    // scales of such a page.
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bool inside = h ? inside1 : inside0;
+                        const int page = inside ? id[h] : 0;
+                        const uint8_t* ks = page_at(k_codes, 0, page) + (two ? 0 : slot + h * 16 * D);
+                        const uint8_t* vs = page_at(v_codes, 1, page) + (two ? 0 : slot + h * 16 * D);
 #pragma unroll
                         for (int i = 0; i < CH / 2; ++i) {
                             const int c = i * 32 + lane, r = h * 16 + c / CH;
@@ -332,13 +355,13 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                             ac_copy16(at, ks + i * 512, live);
                             ac_copy16(at + AC_TILE * D, vs + i * 512, live);
                         }
-                    }
-                    if (lane < 2) {
-                        if (key0 + h * 16 < s.len && !inside) {
-                            ring_scales[st * 4 + lane * 2 + h] = __int_as_float(0x7fffffff);  // NaN: a page outside the pool
-                            if (a.status != nullptr) atomicOr(a.status, KV_PAGE_RANGE);
-                        } else {
-                            ac_copy4(ring_scales_u + (st * 4 + lane * 2 + h) * 4, p.head_scale(lane, page, head), inside);
+                        if (lane < 4 && (lane & 1) == h) {
+                            if (key0 + h * 16 < s.len && !inside) {
+                                ring_scales[st * 4 + lane] = __int_as_float(0x7fffffff);
+                                if (a.status != nullptr) atomicOr(a.status, KV_PAGE_RANGE);
+                            } else {
+                                ac_copy4(ring_scales_u + (st * 4 + lane) * 4, my_scales + static_cast<uint64_t>(page) * pitch_scales, inside);
+                            }
                         }
                     }
                 }
@@ -636,10 +659,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     __syncthreads();
 
     // Join of the records, which stand in the line's order: those of one item follow one another.
-    constexpr int RECS = 2 * AC_WARPS;
+    constexpr int RECS = 2 * C::WARPS;
     const long long my_u0 = rec[lane % RECS].u0;
-    const unsigned mates = __match_any_sync(0xffffffffu, my_u0) & ((1u << RECS) - 1);
-    unsigned todo = __ballot_sync(0xffffffffu, my_u0 >= 0) & ((1u << RECS) - 1);
+    const unsigned mates = __match_any_sync(0xffffffffu, my_u0) & (0xffffffffu >> (32 - RECS));
+    unsigned todo = __ballot_sync(0xffffffffu, my_u0 >= 0) & (0xffffffffu >> (32 - RECS));
     while (todo != 0) {
         const int r0 = __ffs(todo) - 1;
         const unsigned chain = __shfl_sync(0xffffffffu, mates, r0);
@@ -648,7 +671,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const bool whole = r.tile0 == 0 && rec[31 - __clz(chain)].tile1 == r.tiles;
         const bool begun = r.tile0 > 0;  // in an earlier CTA
         float* part = a.parts + static_cast<long long>(cta * 2 + (begun ? 0 : 1)) * C::PART;
-        for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
+        for (int i = tid; i < r.rows * (D / 4); i += C::WARPS * 32) {
             const int row = i / (D / 4), c = i % (D / 4) * 2;
             float2 ml[RECS];
             float top = AC_NONE, sum = 0.0f;
@@ -757,7 +780,7 @@ static cudaError_t launch_attn_cache(const AcArgs& a, const KvPool& p, cudaStrea
     auto kernel = attn_cache_kernel<D, NT>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    const cudaError_t f = launch_pdl(kernel, dim3(AC_CTAS), dim3(AC_THREADS), C::SMEM, s, a, p);
+    const cudaError_t f = launch_pdl(kernel, dim3(AC_CTAS), dim3(C::WARPS * 32), C::SMEM, s, a, p);
     if (f != cudaSuccess) return f;
     return launch_pdl(attn_cache_join_kernel<D, NT>, dim3(AC_CTAS * C::ROWS), dim3(AC_JOIN_WARPS * 32), 0, s, a);
 }
@@ -815,6 +838,10 @@ extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, cons
     p.ld_codes[1] = ld_vc;
     p.ld_scales[0] = ld_ks;
     p.ld_scales[1] = ld_vs;
+    p.pitch16[0] = static_cast<uint32_t>(ld_kc >> 4);
+    p.pitch16[1] = static_cast<uint32_t>(ld_vc >> 4);
+    p.pitch_scales[0] = static_cast<uint32_t>(ld_ks);
+    p.pitch_scales[1] = static_cast<uint32_t>(ld_vs);
     p.table = page_table;
     p.pages = pages;
     p.max_pages = max_pages;

@@ -19,6 +19,7 @@ struct KvPool {
     uint8_t* codes[2];  // keys, values
     float* scales[2];
     long long ld_codes[2], ld_scales[2];  // from page to page
+    uint32_t pitch16[2], pitch_scales[2];  // the same in 16-byte pieces and in floats
     const int32_t* table;                 // [nseq][max_pages]
     int pages, max_pages, page, kv_heads, d;
     int page_shift;                       // log2 of the page
@@ -65,7 +66,8 @@ inline bool kv_pool_sizes(int pages, int max_pages, int page, int kv_heads, int 
     const long long row = static_cast<long long>(kv_heads) * page * d;
     return (page == 16 || page == 32 || page == 64 || page == 128) && pages >= 1 && max_pages >= 1 &&
            static_cast<long long>(max_pages) * page <= 0x7fffffffLL && static_cast<long long>(kv_heads) * d <= 0x7fffffffLL &&
-           ld_kc >= row && ld_vc >= row && ld_kc % 16 == 0 && ld_vc % 16 == 0 && ld_ks >= kv_heads && ld_vs >= kv_heads;
+           ld_kc >= row && ld_vc >= row && ld_kc % 16 == 0 && ld_vc % 16 == 0 && ld_ks >= kv_heads && ld_vs >= kv_heads &&
+           (ld_kc | ld_vc) >> 36 == 0 && (ld_ks | ld_vs) >> 32 == 0;
 }
 
 }  // namespace mptp
