@@ -31,8 +31,9 @@
 #include "mptp_launch.cuh"
 
 namespace mptp {
-constexpr int W641 = 8, W642 = 8, W961 = 8, W962 = 8, W1281 = 8, W1282 = 8, S641 = 3, S642 = 3, S961 = 3, S962 = 3, S1281 = 2, S1282 = 2;
 
+constexpr int AC_WARPS = 8;
+constexpr int AC_THREADS = AC_WARPS * 32;
 constexpr int AC_TILE = 32;     // keys
 constexpr int AC_ITEM = 4;      // places of an item besides its tiles
 constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
@@ -114,22 +115,19 @@ __device__ __forceinline__ float ac_ex2(float x) {
     return y;
 }
 
-// Warps of a CTA and the tiles of a warp's ring.
-constexpr int ac_warps(int d, int nt) { return d == 64 ? (nt == 1 ? W641 : W642) : d == 96 ? (nt == 1 ? W961 : W962) : (nt == 1 ? W1281 : W1282); }
-constexpr int ac_stages(int d, int nt) { return d == 64 ? (nt == 1 ? S641 : S642) : d == 96 ? (nt == 1 ? S961 : S962) : (nt == 1 ? S1281 : S1282); }
-
 template <int D, int NT>
 struct AcShape {
     static constexpr int ROWS = 8 * NT;              // queries of a row tile
-    static constexpr int WARPS = ac_warps(D, NT);
-    static constexpr int STAGES = ac_stages(D, NT);
+    // Tiles of a warp's ring. Heads of 128 are as fast with two as the memory gives (three: 243 us for 128 sequences of 5.8 k
+    // tokens, two: 233); narrower ones, smaller tiles, want three (64: 61 against 56 us for 32 of 8192 and 8 key heads).
+    static constexpr int STAGES = D == 128 ? 2 : 3;
     static constexpr int STAGE = 2 * AC_TILE * D;    // bytes of K and V
     static constexpr int RING = STAGES * STAGE;      // a warp's; then the record of the item that its run ends in
     static constexpr int HEAD = ROWS * D * 4;        // the record of the item that its run begins in
     static constexpr int WARP = RING + HEAD;
     static constexpr int SCALES = STAGES * 16;       // a warp's: two of K, two of V
     static constexpr int STATS = 2 * ROWS * 8;       // a warp's: (reference, sum) of its records' rows
-    static constexpr int SMEM = WARPS * (WARP + SCALES + STATS);
+    static constexpr int SMEM = AC_WARPS * (WARP + SCALES + STATS);
     static constexpr int PART = ROWS * (D + 2);      // floats of a part
     static_assert(HEAD <= RING && SMEM <= 231424, "shared memory");
 };
@@ -188,14 +186,14 @@ __device__ __forceinline__ void ac_store(const AcArgs& a, int q0, int head, int 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(ac_warps(D, NT) * 32, 1) attn_cache_kernel(const AcArgs a, const KvPool p) {
+__global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs a, const KvPool p) {
     using C = AcShape<D, NT>;
     constexpr int KS = D / 16;   // products along d of one score tile; also tiles of 16 rows of O^T
     constexpr int CH = D / 16;   // 16-byte chunks a key row
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ AcRecord rec[2 * C::WARPS];
+    __shared__ AcRecord rec[2 * AC_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    float* stats = reinterpret_cast<float*>(smem + C::WARPS * (C::WARP + C::SCALES));  // [warp][2][row]{m, l}
+    float* stats = reinterpret_cast<float*>(smem + AC_WARPS * (C::WARP + C::SCALES));  // [warp][2][row]{m, l}
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -226,7 +224,7 @@ __global__ void __launch_bounds__(ac_warps(D, NT) * 32, 1) attn_cache_kernel(con
         upto = look_at(0);
     }
     // As many CTAs as have a few places for each of their warps.
-    const long long want = (total + 2 * C::WARPS - 1) / (2 * C::WARPS);
+    const long long want = (total + 2 * AC_WARPS - 1) / (2 * AC_WARPS);
     const int ctas = static_cast<int>(want < static_cast<long long>(gridDim.x) ? want : static_cast<long long>(gridDim.x));
     const int cta = blockIdx.x;
     AcItem* left = a.items + cta;
@@ -234,8 +232,8 @@ __global__ void __launch_bounds__(ac_warps(D, NT) * 32, 1) attn_cache_kernel(con
     if (cta >= ctas) return;
     if (lane < 2) rec[2 * warp + lane].u0 = -1;
     const long long cta_pos = ac_share(total, cta, ctas), cta_end = ac_share(total, cta + 1, ctas);
-    long long pos = cta_pos + (cta_end - cta_pos) * warp / C::WARPS;
-    const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / C::WARPS;
+    long long pos = cta_pos + (cta_end - cta_pos) * warp / AC_WARPS;
+    const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / AC_WARPS;
     int seq = 0;
     long long seq_start = 0;
     AcSeq s = held[0];
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(ac_warps(D, NT) * 32, 1) attn_cache_kernel(con
 
     uint8_t* ring = smem + warp * C::WARP;
     const uint32_t ring_u = smem_u32(ring);
-    float* ring_scales = reinterpret_cast<float*>(smem + C::WARPS * C::WARP + warp * C::SCALES);
+    float* ring_scales = reinterpret_cast<float*>(smem + AC_WARPS * C::WARP + warp * C::SCALES);
     const uint32_t ring_scales_u = smem_u32(ring_scales);
 
     while (pos < end) {
@@ -659,10 +657,10 @@ __global__ void __launch_bounds__(ac_warps(D, NT) * 32, 1) attn_cache_kernel(con
     __syncthreads();
 
     // Join of the records, which stand in the line's order: those of one item follow one another.
-    constexpr int RECS = 2 * C::WARPS;
+    constexpr int RECS = 2 * AC_WARPS;
     const long long my_u0 = rec[lane % RECS].u0;
-    const unsigned mates = __match_any_sync(0xffffffffu, my_u0) & (0xffffffffu >> (32 - RECS));
-    unsigned todo = __ballot_sync(0xffffffffu, my_u0 >= 0) & (0xffffffffu >> (32 - RECS));
+    const unsigned mates = __match_any_sync(0xffffffffu, my_u0) & ((1u << RECS) - 1);
+    unsigned todo = __ballot_sync(0xffffffffu, my_u0 >= 0) & ((1u << RECS) - 1);
     while (todo != 0) {
         const int r0 = __ffs(todo) - 1;
         const unsigned chain = __shfl_sync(0xffffffffu, mates, r0);
@@ -671,7 +669,7 @@ __global__ void __launch_bounds__(ac_warps(D, NT) * 32, 1) attn_cache_kernel(con
         const bool whole = r.tile0 == 0 && rec[31 - __clz(chain)].tile1 == r.tiles;
         const bool begun = r.tile0 > 0;  // in an earlier CTA
         float* part = a.parts + static_cast<long long>(cta * 2 + (begun ? 0 : 1)) * C::PART;
-        for (int i = tid; i < r.rows * (D / 4); i += C::WARPS * 32) {
+        for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
             const int row = i / (D / 4), c = i % (D / 4) * 2;
             float2 ml[RECS];
             float top = AC_NONE, sum = 0.0f;
@@ -780,7 +778,7 @@ static cudaError_t launch_attn_cache(const AcArgs& a, const KvPool& p, cudaStrea
     auto kernel = attn_cache_kernel<D, NT>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    const cudaError_t f = launch_pdl(kernel, dim3(AC_CTAS), dim3(C::WARPS * 32), C::SMEM, s, a, p);
+    const cudaError_t f = launch_pdl(kernel, dim3(AC_CTAS), dim3(AC_THREADS), C::SMEM, s, a, p);
     if (f != cudaSuccess) return f;
     return launch_pdl(attn_cache_join_kernel<D, NT>, dim3(AC_CTAS * C::ROWS), dim3(AC_JOIN_WARPS * 32), 0, s, a);
 }
