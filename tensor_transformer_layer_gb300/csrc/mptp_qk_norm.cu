@@ -38,7 +38,7 @@ struct QkNormArgs {
     const int32_t* pos;  // [axes][T]
     float* sums;         // [blocks][d]
     long long ldx, ldy, lddy;
-    int T, heads, q_heads, d, pairs;
+    int T, heads, q_heads, d, pairs, axes;
     int shares;    // log2 of the warps that share a token; backward: of query heads,
     int k_shares;  // and of key heads,
     int q_blocks;  // and the blocks that walk query heads, the others key heads
@@ -131,32 +131,38 @@ __device__ __forceinline__ void qk_turn(const float2 (&f)[VEC], const float2 (&P
     }
 }
 
-// Cosines and sines of a lane's pairs (BACK: of the rotation back). `at`: the token's position on the axis of all its pairs,
-// where `one_axis`. `turns`: the table in shared memory (lanes read different places of it, which the constant bank serves
-// one by one). sin.approx and cos.approx stay within 2^-21 on [-pi, pi], far below a bf16 step.
-template <int VEC, bool INTER, bool BACK>
-__device__ __forceinline__ void qk_angles(const RopeTable& tab, const uint4* turns, const QkNormArgs& a,
-                                          const QkLane<VEC, INTER>& L, int token, int at, bool one_axis, float (&c)[VEC],
-                                          float (&s)[VEC]) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        c[j] = 1.0f;
-        s[j] = 0.0f;
+// The angles of a token's pairs: each lane of the warp takes every 32nd pair (a head's lanes hold the same pairs as the next
+// head's, so a lane's own eight would be computed several times over) and leaves cosine and sine in the warp's `cs`.
+// `table`: {turns' halves, axis} of each pair, in shared memory; `pos`: the token's positions by axis, there too. BACK: of the
+// rotation back. sin.approx and cos.approx stay within 2^-20 on [-pi, pi], far below a bf16 step.
+template <bool BACK>
+__device__ __forceinline__ void qk_angles(const uint4* table, const int* pos, float* cs, int pairs, int lane) {
+    for (int i = lane; i < pairs; i += 32) {
+        const uint4 f = table[i];
+        const uint32_t p = static_cast<uint32_t>(pos[f.z]);
+        // the upper 32 bits of p times the 64-bit turns, a signed fraction of a turn in [-1/2, 1/2), times 2 pi / 2^32
+        const uint32_t top = p * f.y + __umulhi(p, f.x) - (static_cast<int32_t>(p) < 0 ? f.x : 0u);
+        const float angle = static_cast<float>(static_cast<int32_t>(top)) * (BACK ? -1.4629180792671596e-9f : 1.4629180792671596e-9f);
+        float s, c;
+        asm("sin.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(angle));
+        asm("cos.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(angle));
+        cs[i] = c;
+        cs[ROPE_MAX_PAIRS + i] = s;
     }
-    if (!L.turns) return;
+}
+
+// Those of a lane's pairs; cosine 1 and sine 0 where it has none.
+template <int VEC, bool INTER>
+__device__ __forceinline__ void qk_take_angles(const float* cs, const QkLane<VEC, INTER>& L, float (&c)[VEC], float (&s)[VEC]) {
 #pragma unroll
-    for (int j = 0; j < VEC; j += 2) {
-        const uint4 two = turns[(L.g * VEC + j) / 2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int p = one_axis ? at : a.pos[static_cast<long long>(tab.axis[L.g * VEC + j + k]) * a.T + token];
-            // the upper 32 bits of p times the 64-bit turns: a signed fraction of a turn in [-1/2, 1/2)
-            const uint32_t lo = k ? two.z : two.x, hi = k ? two.w : two.y, u = static_cast<uint32_t>(p);
-            const uint32_t top = u * hi + __umulhi(u, lo) - (p < 0 ? lo : 0u);
-            // 2 pi / 2^32
-            const float angle = static_cast<float>(static_cast<int32_t>(top)) * (BACK ? -1.4629180792671596e-9f : 1.4629180792671596e-9f);
-            __sincosf(angle, &s[j + k], &c[j + k]);
+    for (int j = 0; j < VEC; j += 4) {
+        float4 u = make_float4(1.0f, 1.0f, 1.0f, 1.0f), v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (L.turns) {
+            u = *reinterpret_cast<const float4*>(cs + L.g * VEC + j);
+            v = *reinterpret_cast<const float4*>(cs + ROPE_MAX_PAIRS + L.g * VEC + j);
         }
+        c[j] = u.x, c[j + 1] = u.y, c[j + 2] = u.z, c[j + 3] = u.w;
+        s[j] = v.x, s[j + 1] = v.y, s[j + 2] = v.z, s[j + 3] = v.w;
     }
 }
 
@@ -200,17 +206,18 @@ __device__ __forceinline__ void qk_copy(uint32_t dst, const void* src, int take)
 
 // The walk of a warp: items (a token's heads of one kind, or a share of them) `stride` apart, each in steps of as many heads
 // as the warp has lanes for. A step's loads go to the lane's own places in shared memory (cp.async: nothing of them waits in
-// registers, and no lane reads another's), QKN_STAGES - 1 steps ahead; N arrays are read, and the token's position with its
+// registers, and no lane reads another's), QKN_STAGES - 1 steps ahead; N arrays are read, and the token's positions with its
 // first step. Lanes behind the last head get zeros.
 template <int VEC, int N>
 struct QkWalk {
     static constexpr int BYTES = 2 * VEC;                      // of a vector
-    static constexpr int STAGE = N * 2 * BYTES * 32 + 4 * 32;  // of a warp's stage
+    static constexpr int STAGE = N * 2 * BYTES * 32 + 16;      // of a warp's stage: the vectors, then the positions
     const __nv_bfloat16* src[N];   // the lane's first vector of head 0 of token 0
     const __nv_bfloat16* at[N];    // and of the step to be asked for
     long long ld[N];
-    const int32_t* pos;
+    const int32_t* pos;            // lane k < axes: of axis k
     uint32_t ring, pos_ring;       // the lane's places in the first stage
+    bool has_axis;
     unsigned items, stride, next;
     int shares, per_warp, h0, h1, wide, last, d, second, next_h, stage;
 
@@ -232,7 +239,7 @@ struct QkWalk {
                 qk_copy<BYTES>(to + (2 * n + 1) * BYTES * 32, at[n] + second, take);
                 at[n] += wide * d;
             }
-            if (next_h < h0 + wide) qk_copy<4>(pos_ring + stage * STAGE, pos + (next >> shares), 4);
+            if (has_axis && next_h < h0 + wide) qk_copy<4>(pos_ring + stage * STAGE, pos + (next >> shares), 4);
             next_h += wide;
             if (next_h >= h1) {
                 next += stride;
@@ -261,18 +268,13 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const QkLane<VEC, INTER> L(a.d, a.pairs, lane);
-    // Whether each lane's pairs lie on one axis.
-    const bool one_axis = __all_sync(0xffffffffu, !L.turns || tab.axis[L.g * VEC] == tab.axis[L.g * VEC + VEC - 1]);
-    const int axis = L.turns ? tab.axis[L.g * VEC] : 0;
     const bool keys = static_cast<int>(blockIdx.x) >= a.q_blocks;
     const int block = keys ? blockIdx.x - a.q_blocks : blockIdx.x;
     const int sub = L.live ? L.sub : 0;
-    uint4* turns = reinterpret_cast<uint4*>(smem + QKN_WARPS * QKN_STAGES * Walk::STAGE);
-    for (int i = threadIdx.x; 2 * i < a.pairs; i += QKN_WARPS * 32) {
-        const unsigned long long t0 = tab.turns[2 * i], t1 = tab.turns[2 * i + 1];
-        turns[i] = make_uint4(static_cast<uint32_t>(t0), static_cast<uint32_t>(t0 >> 32), static_cast<uint32_t>(t1),
-                              static_cast<uint32_t>(t1 >> 32));
-    }
+    uint4* table = reinterpret_cast<uint4*>(smem + QKN_WARPS * QKN_STAGES * Walk::STAGE);
+    float* cs = reinterpret_cast<float*>(table + ROPE_MAX_PAIRS) + warp * 2 * ROPE_MAX_PAIRS;
+    for (int i = threadIdx.x; i < a.pairs; i += QKN_WARPS * 32)
+        table[i] = make_uint4(static_cast<uint32_t>(tab.turns[i]), static_cast<uint32_t>(tab.turns[i] >> 32), tab.axis[i], 0);
     __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
@@ -285,10 +287,11 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
         walk.src[1] = a.dy + sub * a.d + L.o0;
         walk.ld[1] = a.lddy;
     }
-    walk.pos = a.pos + static_cast<long long>(axis) * a.T;
+    walk.has_axis = lane < a.axes;
+    walk.pos = a.pos + static_cast<long long>(walk.has_axis ? lane : 0) * a.T;
     walk.ring = smem_u32(ring);
-    const uint8_t* pos_ring = smem + warp * QKN_STAGES * Walk::STAGE + Walk::STAGE - 128 + lane * 4;
-    walk.pos_ring = smem_u32(pos_ring);
+    const uint8_t* pos_ring = smem + warp * QKN_STAGES * Walk::STAGE + Walk::STAGE - 16;
+    walk.pos_ring = smem_u32(pos_ring) + (lane & 3) * 4;
     walk.shares = keys ? a.k_shares : a.shares;
     walk.items = static_cast<unsigned>(a.T) << walk.shares;
     walk.stride = (keys ? gridDim.x - a.q_blocks : a.q_blocks) * QKN_WARPS;
@@ -320,9 +323,11 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
         const uint8_t* at = ring + stage * Walk::STAGE;
         if (fresh) {
             const int token = static_cast<int>(item >> walk.shares);
-            const int p = *reinterpret_cast<const int*>(pos_ring + stage * Walk::STAGE);
             float c[VEC], s[VEC];
-            qk_angles<VEC, INTER, BACKWARD>(tab, turns, a, L, token, p, one_axis, c, s);
+            __syncwarp();  // the positions are there, and every lane has taken the last token's angles
+            qk_angles<BACKWARD>(table, reinterpret_cast<const int*>(pos_ring + stage * Walk::STAGE), cs, a.pairs, lane);
+            __syncwarp();
+            qk_take_angles(cs, L, c, s);
             if constexpr (!BACKWARD) qk_weight(weight, L, w);  // again for each token: sixteen registers less
             qk_coefficients<VEC, INTER>(c, s, BACKWARD ? nullptr : w, P, Q);
             out = a.y + token * a.ldy + (sub + h) * a.d;
@@ -434,7 +439,7 @@ static int qk_shares(int T, int heads, int d, bool wide) {
 
 // Shares of query heads and of key heads, and the blocks that walk each. Forward: a warp walks about QKN_RUN steps, so that
 // the blocks that end late are small. Backward: as many blocks as the chip holds at most (each leaves a row of sums),
-// divided so that neither kind's last warp ends much later than the other's; a token's angles cost about one step.
+// divided so that neither kind's last warp ends much later than the other's; a token's angles cost about a quarter of a step.
 static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
     const int in_hand = 32 / (a.d / (wide ? 16 : 8));
     long long items[2], most[2], cost[2];
@@ -444,7 +449,7 @@ static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
         (i == 0 ? a.shares : a.k_shares) = shares;
         const int steps = n == 0 ? 0 : (n + (in_hand << shares) - 1) / (in_hand << shares);
         items[i] = n == 0 ? 0 : static_cast<long long>(a.T) << shares;
-        cost[i] = 1 + steps;
+        cost[i] = 1 + 4 * steps;
         const int run = steps == 0 || steps > QKN_RUN ? 1 : QKN_RUN / steps;
         most[i] = (items[i] + QKN_WARPS - 1) / QKN_WARPS;
         blocks[i] = static_cast<int>(backward ? most[i] : (items[i] + run * QKN_WARPS - 1) / (run * QKN_WARPS));
@@ -475,7 +480,7 @@ static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
 
 template <int VEC, bool INTER, int SUM, bool BACKWARD>
 static cudaError_t qk_launch(const RopeTable& tab, const QkNormArgs& a, int blocks, cudaStream_t s) {
-    constexpr int ring = QKN_WARPS * QKN_STAGES * QkWalk<VEC, BACKWARD ? 2 : 1>::STAGE + ROPE_MAX_PAIRS * 8;
+    constexpr int ring = QKN_WARPS * QKN_STAGES * QkWalk<VEC, BACKWARD ? 2 : 1>::STAGE + ROPE_MAX_PAIRS * (16 + QKN_WARPS * 8);
     constexpr int red = BACKWARD ? QKN_WARPS * 32 * 2 * VEC * 4 : 0;
     constexpr int bytes = ring > red ? ring : red;
     static_assert(bytes <= 48 * 1024, "shared memory");
@@ -511,13 +516,14 @@ static mp_status qk_check(int T, int heads, int q_heads, int d, int axes, const 
 
 static bool qk_pitch(long long ld, int heads, int d) { return ld >= static_cast<long long>(heads) * d && ld % 8 == 0; }
 
-static QkNormArgs qk_args(int T, int heads, int q_heads, int d, long long pairs, float eps) {
+static QkNormArgs qk_args(int T, int heads, int q_heads, int d, int axes, long long pairs, float eps) {
     QkNormArgs a{};
     a.T = T;
     a.heads = heads;
     a.q_heads = q_heads;
     a.d = d;
     a.pairs = static_cast<int>(pairs);
+    a.axes = axes;
     a.eps = eps;
     a.inv_d = 1.0f / static_cast<float>(d);
     return a;
@@ -545,7 +551,7 @@ extern "C" mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16
     if (st != MP_OK) return st;
     RopeTable tab{};
     rope_fill(tab, axes, sections, pairs, base, flags);
-    QkNormArgs a = qk_args(T, heads, q_heads, d, pairs, eps);
+    QkNormArgs a = qk_args(T, heads, q_heads, d, axes, pairs, eps);
     a.x = reinterpret_cast<const __nv_bfloat16*>(x);
     a.y = reinterpret_cast<__nv_bfloat16*>(y);
     a.wq = reinterpret_cast<const __nv_bfloat16*>(wq);
@@ -596,7 +602,7 @@ extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp
     if (T > 0) {
         RopeTable tab{};
         rope_fill(tab, axes, sections, pairs, base, flags);
-        QkNormArgs a = qk_args(T, heads, q_heads, d, pairs, eps);
+        QkNormArgs a = qk_args(T, heads, q_heads, d, axes, pairs, eps);
         a.x = reinterpret_cast<const __nv_bfloat16*>(x);
         a.dy = reinterpret_cast<const __nv_bfloat16*>(dy);
         a.y = reinterpret_cast<__nv_bfloat16*>(dx);

@@ -55,14 +55,11 @@ inline void rope_fill(RopeTable& tab, int axes, const int* sections, long long p
         }
 }
 
-// The angle of pair i at position `p` as a fraction of half a turn, in [-1, 1).
-__device__ __forceinline__ float rope_half_turns(const RopeTable& tab, int i, long long p) {
-    const unsigned long long turn = static_cast<unsigned long long>(p) * tab.turns[i];
-    // its top 32 bits as a signed fraction of a turn in [-1/2, 1/2)
-    return static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
-}
+// Sine and cosine of the angle of pair i at position `p`.
 __device__ __forceinline__ void rope_sincos(const RopeTable& tab, int i, long long p, float* s, float* c) {
-    sincospif(rope_half_turns(tab, i, p), s, c);
+    const unsigned long long turn = static_cast<unsigned long long>(p) * tab.turns[i];
+    // top 32 bits as a signed fraction of a turn in [-1/2, 1/2); sincospif takes half turns
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, s, c);
 }
 
 // VEC pairs of a lane as fp32, from the two halves of a head or from neighbouring elements.
