@@ -25,7 +25,7 @@ namespace mptp {
 constexpr int QKN_WARPS = 4;         // warps of a block
 constexpr int QKN_STAGES = 4;        // steps in flight, and the one in hand
 constexpr int QKN_PER_SM = 4;        // blocks on an SM
-constexpr int QKN_RUN = 64;          // steps of a warp of the forward pass
+constexpr int QKN_RUN = 24;          // steps of a warp of the forward pass
 constexpr int QKN_BWD_PER_SM = 3;
 constexpr int QKN_BWD_BLOCKS = QKN_BWD_PER_SM * 152;  // rows of the workspace at most
 
