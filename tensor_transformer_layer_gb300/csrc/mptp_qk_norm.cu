@@ -464,7 +464,7 @@ static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
             const int guess = static_cast<int>(QKN_BWD_BLOCKS * share);
             int best = guess < 1 ? 1 : guess > QKN_BWD_BLOCKS - 1 ? QKN_BWD_BLOCKS - 1 : guess;
             long long span = -1;
-            for (int b = guess - 24 > 1 ? guess - 24 : 1; b <= guess + 24 && b < QKN_BWD_BLOCKS; ++b) {
+            for (int b = guess - 8 > 1 ? guess - 8 : 1; b <= guess + 8 && b < QKN_BWD_BLOCKS; ++b) {
                 const long long q = rounds(0, b), k = rounds(1, QKN_BWD_BLOCKS - b), t = q > k ? q : k;
                 if (span < 0 || t < span) {
                     span = t;
