@@ -21,7 +21,7 @@
  * Conventions for every entry point
  *   - All matrices are bf16 (raw bits in mp_bf16), row-major and contiguous,
  *     except targets (int32), loss (fp32) and workspaces (opaque bytes).
- *   - All pointers are DEVICE pointers, 16-byte aligned. The caller allocates,
+ *   - All pointers are DEVICE pointers of the current device, 16-byte aligned. The caller allocates,
  *     owns and frees every buffer; the library never allocates and keeps no
  *     device memory between calls, with one exception: the static 4 MiB array
  *     of mp_vocab_ce_noalloc, which a device holds from that entry point's
@@ -522,7 +522,8 @@ MP_API mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp_bf1
  *   offsets that descend make others overlap, rows of theirs may be left out too. A page outside the pool is left out and sets
  *   MP_DEV_PAGE_RANGE. Rows, slots and pages of no sequence stay as they were. max_n == 0: nothing to do.
  *   Size rules: d % 16 == 0, d <= 256; max_n <= T; ldk, ldv at least a row and multiples of 8; ld_kc, ld_vc at least
- *   kv_heads * page * d and multiples of 16; ld_ks, ld_vs >= kv_heads; pages, max_pages >= 1; max_pages * page < 2^31.
+ *   kv_heads * page * d, multiples of 16 and below 2^36; ld_ks, ld_vs >= kv_heads and below 2^32; pages, max_pages >= 1;
+ *   max_pages * page <= 2^31 - 256.
  */
 MP_API mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V,
                             uint8_t* kc, uint8_t* vc, float* ks, float* vs, const int32_t* page_table,
@@ -551,7 +552,8 @@ MP_API mp_status mp_kv_cache_read(const uint8_t* kc, const uint8_t* vc, const fl
  *   and LSE NaN; a NaN in V of a token of the sequence that a causal row does not see may make its O NaN too.
  *   max_q: at least the longest sequence's queries. A sequence with rows outside [0, Tq], more than max_q queries or a
  *   length outside [0, max_pages * page] is left out and sets MP_DEV_SEQ_RANGE; a page outside the pool sets
- *   MP_DEV_PAGE_RANGE and gives the rows that would see it O = LSE = NaN. Rows of no sequence are not written.
+ *   MP_DEV_PAGE_RANGE, gives the rows that would see it O = LSE = NaN, and may give the sequence's other rows O = NaN. Rows
+ *   of no sequence are not written.
  *   workspace: mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q) bytes (0 for sizes outside the rules), whatever they
  *   hold; calls that may overlap need one each.
  *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; max_q <= Tq; max_q * heads < 2^31 - 64; ldq, ldo at least a

@@ -65,7 +65,7 @@ inline bool kv_pool_sizes(int pages, int max_pages, int page, int kv_heads, int 
                           long long ld_ks, long long ld_vs) {
     const long long row = static_cast<long long>(kv_heads) * page * d;
     return (page == 16 || page == 32 || page == 64 || page == 128) && pages >= 1 && max_pages >= 1 &&
-           static_cast<long long>(max_pages) * page <= 0x7fffffffLL && static_cast<long long>(kv_heads) * d <= 0x7fffffffLL &&
+           static_cast<long long>(max_pages) * page <= 0x7fffff00LL && static_cast<long long>(kv_heads) * d <= 0x7fffffffLL &&
            ld_kc >= row && ld_vc >= row && ld_kc % 16 == 0 && ld_vc % 16 == 0 && ld_ks >= kv_heads && ld_vs >= kv_heads &&
            (ld_kc | ld_vc) >> 36 == 0 && (ld_ks | ld_vs) >> 32 == 0;
 }

@@ -235,8 +235,9 @@ struct QkWalk {
             const uint32_t to = ring + stage * STAGE;
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                qk_copy<BYTES>(to + (2 * n) * BYTES * 32, at[n], take);
-                qk_copy<BYTES>(to + (2 * n + 1) * BYTES * 32, at[n] + second, take);
+                const __nv_bfloat16* from = take != 0 ? at[n] : src[n];  // an address in the tensor either way
+                qk_copy<BYTES>(to + (2 * n) * BYTES * 32, from, take);
+                qk_copy<BYTES>(to + (2 * n + 1) * BYTES * 32, from + second, take);
                 at[n] += wide * d;
             }
             if (has_axis && next_h < h0 + wide) qk_copy<4>(pos_ring + stage * STAGE, pos + (next >> shares), 4);
