@@ -556,7 +556,7 @@ MP_API mp_status mp_kv_cache_read(const uint8_t* kc, const uint8_t* vc, const fl
  *   of no sequence are not written.
  *   workspace: mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q) bytes (0 for sizes outside the rules), whatever they
  *   hold; calls that may overlap need one each.
- *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; max_q <= Tq; max_q * heads < 2^31 - 64; ldq, ldo at least a
+ *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; heads <= 65536; max_q <= Tq; max_q * heads < 2^31 - 64; ldq, ldo at least a
  *   row and multiples of 8; the pool's as above; scale > 0 and finite.
  */
 MP_API size_t mp_attn_cache_workspace_bytes(int heads, int kv_heads, int d, int max_q);

@@ -61,6 +61,7 @@ struct AcArgs {
     float* parts;   // [2 AC_CTAS][rows][d + 2]
     long long ldq, ldo;
     int nseq, Tq, max_q, heads, group, causal;
+    float inv_group;  // 1 / group
     float scale_log2;
     uint32_t* status;
 };
@@ -170,11 +171,21 @@ __device__ __forceinline__ AcSeq ac_seq(const AcArgs& a, const KvPool& p, int se
 // Float2 index within a row of the join buffer: eight lanes that write the same j land in different banks.
 __device__ __forceinline__ int ac_join(int i, int row) { return i ^ (((i >> 4) & 1) | ((row & 6))); }
 
+// Row `col` of a row tile as a query of its sequence and a head of its group. (col + rem + 1/2) / group in fp32 lies nearer
+// to its integer than to the next for sums below 2^20.
+struct AcRow {
+    int query, member;
+};
+__device__ __forceinline__ AcRow ac_row(const AcArgs& a, int query0, int rem, int col) {
+    const int n = rem + col, q = static_cast<int>((static_cast<float>(n) + 0.5f) * a.inv_group);
+    return {query0 + q, n - q * a.group};
+}
+
 // The output of row `row` of an item, from its sums x in units of the values and sum of probabilities: four elements at d.
-__device__ __forceinline__ void ac_store(const AcArgs& a, int q0, int head, int row, int d, int D, const float4& x, float top,
-                                         float sum) {
-    const int hd = head * a.group + row % a.group;
-    const long long q = q0 + row / a.group;
+__device__ __forceinline__ void ac_store(const AcArgs& a, int q0, int head, const AcRow& row, int d, int D, const float4& x,
+                                         float top, float sum) {
+    const int hd = head * a.group + row.member;
+    const long long q = q0 + row.query;
     const float inv = 1.0f / sum;
     uint2 out = make_uint2(0, 0);  // a row that sees no key, whatever its sums hold
     if (sum != 0.0f) {
@@ -192,13 +203,14 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     constexpr int CH = D / 16;   // 16-byte chunks a key row
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ AcRecord rec[2 * AC_WARPS];
+    __shared__ long long sh_places[AC_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     float* stats = reinterpret_cast<float*>(smem + AC_WARPS * (C::WARP + C::SCALES));  // [warp][2][row]{m, l}
     grid_dependency_wait();
     grid_launch_dependents();
 
     // The line's length, then the warp's run and the sequence that holds its first place: each warp by itself, lanes taking
-    // AC_SEQS neighbouring sequences each (loads side by side, no barrier).
+    // AC_SEQS neighbouring sequences each (loads side by side, and no barrier where one step sees all of them).
     auto places = [&](const AcSeq& q) { return static_cast<long long>(q.items) * (q.tiles + AC_ITEM); };
     AcSeq held[AC_SEQS];
     long long mine = 0;  // places of the lane's sequences
@@ -216,12 +228,19 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         }
         return upto;
     };
-    long long upto = look_at(0);
+    // More sequences than a warp looks at in one step: each takes an eighth, and the eighth that holds its first place again.
+    constexpr int STEP = 32 * AC_SEQS;
+    const int part = a.nseq > STEP ? (a.nseq + AC_WARPS * STEP - 1) / (AC_WARPS * STEP) * STEP : 0;
+    long long upto = look_at(part * warp);
     long long total = __shfl_sync(0xffffffffu, upto, 31);
-    if (a.nseq > 32 * AC_SEQS) {
-        for (int base = 32 * AC_SEQS; base < a.nseq; base += 32 * AC_SEQS)
+    if (part > 0) {
+        for (int base = part * warp + STEP; base < min(part * (warp + 1), a.nseq); base += STEP)
             total += __shfl_sync(0xffffffffu, look_at(base), 31);
-        upto = look_at(0);
+        if (lane == 0) sh_places[warp] = total;
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < AC_WARPS; ++w) total += sh_places[w];
     }
     // As many CTAs as have a few places for each of their warps.
     const long long want = (total + 2 * AC_WARPS - 1) / (2 * AC_WARPS);
@@ -234,14 +253,23 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     const long long cta_pos = ac_share(total, cta, ctas), cta_end = ac_share(total, cta + 1, ctas);
     long long pos = cta_pos + (cta_end - cta_pos) * warp / AC_WARPS;
     const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / AC_WARPS;
-    int seq = 0;
+    int seq = 0, first = 0;
     long long seq_start = 0;
+    if (part > 0) {
+#pragma unroll
+        for (int w = 0; w < AC_WARPS - 1; ++w)
+            if (pos >= seq_start + sh_places[w] && first == part * w) {
+                seq_start += sh_places[w];
+                first += part;
+            }
+        upto = look_at(first) + seq_start;
+    }
     AcSeq s = held[0];
-    for (int base = 0; base < a.nseq;) {
+    for (int base = first; base < a.nseq;) {
         const unsigned here = __ballot_sync(0xffffffffu, pos < upto);
         if (here == 0) {  // pos lies before the line's end, so some step finds it
             seq_start = __shfl_sync(0xffffffffu, upto, 31);
-            base += 32 * AC_SEQS;
+            base += STEP;
             upto = look_at(base) + seq_start;
             continue;
         }
@@ -272,6 +300,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     float* ring_scales = reinterpret_cast<float*>(smem + AC_WARPS * C::WARP + warp * C::SCALES);
     const uint32_t ring_scales_u = smem_u32(ring_scales);
 
+    int last_seq = -1, local = 0, head = 0, row_tile = 0;  // of the item in hand
     while (pos < end) {
         while (seq < a.nseq && pos >= seq_start + places(s)) {
             seq_start += places(s);
@@ -280,14 +309,26 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         if (seq >= a.nseq) break;
         const int span = s.tiles + AC_ITEM;
         const long long ahead = pos - seq_start;
-        const int local = ahead <= 0x7fffffff ? static_cast<int>(ahead) / span : static_cast<int>(ahead / span);
-        const int off0 = static_cast<int>(ahead - static_cast<long long>(local) * span);
+        int off0 = 0;
+        if (seq == last_seq) {  // the item behind the last one
+            ++local;
+            if (++head == p.kv_heads) {
+                head = 0;
+                ++row_tile;
+            }
+        } else {
+            local = ahead <= 0x7fffffff ? static_cast<int>(ahead) / span : static_cast<int>(ahead / span);
+            off0 = static_cast<int>(ahead - static_cast<long long>(local) * span);
+            row_tile = local / p.kv_heads;
+            head = local - row_tile * p.kv_heads;
+            last_seq = seq;
+        }
         const int take = static_cast<int>(min(static_cast<long long>(span - off0), end - pos));
         const int tile0 = max(off0 - AC_ITEM, 0), tile1 = off0 + take - AC_ITEM;
         pos += take;
         if (tile1 <= tile0) continue;
-        const int head = local % p.kv_heads;
-        const int row0 = local / p.kv_heads * C::ROWS;
+        const int row0 = row_tile * C::ROWS;
+        const int query0 = row0 == 0 ? 0 : row0 / a.group, rem0 = row0 - query0 * a.group;
         const int rows = min(C::ROWS, s.nq * a.group - row0);
         const int32_t* table = p.table + static_cast<long long>(seq) * p.max_pages;
 
@@ -378,8 +419,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         } x[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int row = row0 + n * 8 + g;
-            const __nv_bfloat16* src = a.Q + (s.q0 + row / a.group) * a.ldq + (head * a.group + row % a.group) * D;
+            const AcRow row = ac_row(a, query0, rem0, n * 8 + g);
+            const __nv_bfloat16* src = a.Q + (s.q0 + row.query) * a.ldq + (head * a.group + row.member) * D;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 // D = 128: 16 elements of each half; else D / 4 neighbouring ones
@@ -426,11 +467,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < 2; ++j) {
                 fq[n][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
                 const int col = n * 8 + 2 * t + j;
-                limit[n][j] = col < rows && a.causal ? s.len - s.nq + (row0 + col) / a.group + 1 : s.len;
+                limit[n][j] = col < rows && a.causal ? s.len - s.nq + ac_row(a, query0, rem0, col).query + 1 : s.len;
             }
         }
         // Below this tile no column is masked.
-        const int clear = a.causal ? s.len - s.nq + row0 / a.group + 1 : s.len;
+        const int clear = a.causal ? s.len - s.nq + query0 + 1 : s.len;
 
         float o[KS][NT][4];
         float m[NT][2], l[NT][2];
@@ -621,9 +662,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 for (int j = 0; j < 2; ++j) {
                     const int row = n * 8 + 2 * t + j;
                     if (row >= rows) continue;
+                    const AcRow at = ac_row(a, query0, rem0, row);
 #pragma unroll
                     for (int i = 0; i < KS; i += 2)
-                        ac_store(a, s.q0, head, row0 + row, g * (D / 8) + 2 * i, D,
+                        ac_store(a, s.q0, head, at, g * (D / 8) + 2 * i, D,
                                  make_float4(o[i][n][j] * ref, o[i][n][2 + j] * ref, o[i + 1][n][j] * ref, o[i + 1][n][2 + j] * ref),
                                  m[n][j], l[n][j]);
                 }
@@ -692,7 +734,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 x.w += v.y * f;
             }
             if (whole) {
-                ac_store(a, r.q0, r.head, r.row0 + row, c * 2, D, x, top, sum);
+                ac_store(a, r.q0, r.head, ac_row(a, r.row0 / a.group, r.row0 % a.group, row), c * 2, D, x, top, sum);
             } else {
                 *reinterpret_cast<float4*>(part + row * D + c * 2) = x;
                 if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = make_float2(top, sum);
@@ -769,7 +811,7 @@ __global__ void __launch_bounds__(AC_JOIN_WARPS * 32) attn_cache_join_kernel(con
         x.w += v.w;
         sum += red_sum[w];
     }
-    ac_store(a, it.q0, it.head, it.row0 + row, lane * 4, D, x, top, sum);
+    ac_store(a, it.q0, it.head, ac_row(a, it.row0 / a.group, it.row0 % a.group, row), lane * 4, D, x, top, sum);
 }
 
 template <int D, int NT>
@@ -809,7 +851,7 @@ extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, cons
         !(scale > 0.0f) || !(scale <= 3.4028234663852886e38f))
         return MP_ERR_INVALID_ARG;
     const long long row = static_cast<long long>(heads) * d;
-    if ((d != 64 && d != 96 && d != 128) || heads % kv_heads != 0 || row > 0x7fffffffLL || max_q > Tq || ldq < row ||
+    if ((d != 64 && d != 96 && d != 128) || heads % kv_heads != 0 || heads > 65536 || row > 0x7fffffffLL || max_q > Tq || ldq < row ||
         ldo < row || ldq % 8 != 0 || ldo % 8 != 0 ||
         static_cast<long long>(max_q) * heads > 0x7fffffffLL - 64 ||
         !kv_pool_sizes(pages, max_pages, page, kv_heads, d, ld_kc, ld_vc, ld_ks, ld_vs))
@@ -861,6 +903,7 @@ extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, cons
     a.max_q = max_q;
     a.heads = heads;
     a.group = heads / kv_heads;
+    a.inv_group = 1.0f / static_cast<float>(a.group);
     a.causal = causal != 0;
     a.scale_log2 = scale * AC_LOG2E;
     p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;

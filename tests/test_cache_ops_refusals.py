@@ -116,7 +116,7 @@ def _attn(L, Q=FAKE, O=FAKE, LSE=FAKE, lens=FAKE, cu=FAKE, kc=FAKE, vc=FAKE, ks=
 @pytest.mark.parametrize("kw,code", POOL_REFUSALS + [
     (dict(Tq=-1), 1), (dict(max_q=-1), 1), (dict(heads=0), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1),
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(d=80), 2), (dict(d=256), 2), (dict(heads=3), 2),
-    (dict(max_q=21), 2), (dict(ldq=248), 2), (dict(ldo=260), 2), (dict(Tq=1 << 30, max_q=1 << 29), 2),
+    (dict(max_q=21), 2), (dict(heads=131072), 2), (dict(ldq=248), 2), (dict(ldo=260), 2), (dict(Tq=1 << 30, max_q=1 << 29), 2),
     (dict(Q=None), 1), (dict(O=None), 1), (dict(LSE=None), 1), (dict(lens=None), 1), (dict(Q=BAD), 3), (dict(O=BAD), 3),
     (dict(LSE=BAD), 3), (dict(lens=BAD), 3), (dict(ws=None), 8), (dict(ws=BAD), 8), (dict(wb=4096), 8),
 ])

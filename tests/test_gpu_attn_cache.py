@@ -100,6 +100,8 @@ CASES = [  # new, lens, heads, key heads, d, page
     ([70, 33], [700, 50], 4, 2, 96, 64),            # a chunk of a prompt, longer than its cache in the second
     ([1] * 300, [(i * 37) % 97 for i in range(300)], 2, 1, 64, 16),  # more sequences than the block has threads
     ([1] * 40, [200 + i for i in range(40)], 64, 8, 128, 128),
+    ([(i % 5 + 1) // 2 for i in range(1100)], [(i * 37) % 41 for i in range(1100)], 2, 1, 64, 16),  # several steps of a search
+    ([2, 5], [400, 90], 36, 3, 64, 32),             # twelve heads of a group: queries begin inside a row tile
 ]
 
 
@@ -240,6 +242,42 @@ def test_strided_rows_contiguous_pools_and_replayed_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out[:, :heads].cpu(), want[0]) and torch.equal(LSE.cpu(), want[1])
+
+
+def test_sequences_share_pages_and_rows_of_no_sequence_stay():
+    # the second sequence's cache begins with the first one's pages; rows before and behind the sequences are left alone
+    lens, new = [150, 200], [2, 1]
+    Q, codes, scales, table = _make(new, lens, 4, 2, 64, 32, 24200)
+    table[1, :4] = table[0, :4]
+    T = 7
+    wide = torch.zeros(T, 4, 64, dtype=torch.bfloat16)
+    wide[2:5] = Q
+    O, LSE = _run(wide, codes, scales, table, new, lens, cu=ints([2, 4, 5]))
+    assert torch.isnan(O[[0, 1, 5, 6]]).all() and torch.isnan(LSE[:, [0, 1, 5, 6]]).all()
+    _check((O[2:5], LSE[:, 2:5]), Q, codes, scales, table, new, lens)
+
+
+def test_two_streams_with_a_workspace_each():
+    args = []
+    for k, (new, lens) in enumerate((([1, 1], [9000, 40]), ([3], [5000]))):
+        inp = _make(new, lens, 8, 2, 128, 64, 24300 + k)
+        args.append((inp, new, lens, _run(*inp, new, lens)))
+    dev, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for (Q, codes, scales, table), new, lens, _ in args:
+        c, s = codes.cuda(), scales.cuda()
+        dev.append((Q.cuda(), c[:, 0], c[:, 1], s[:, 0], s[:, 1], table.cuda(), cu_of(new).cuda(), ints(lens).cuda(),
+                    _workspace(8, 2, 128, max(new)), max(new)))
+    torch.cuda.synchronize()
+    for rep in range(20):
+        for (Q, kc, vc, ks, vs, table, cu, ln, ws, mq), st in zip(dev, streams):
+            O, LSE = torch.empty_like(Q), torch.empty(8, Q.shape[0], device="cuda")
+            st.wait_stream(torch.cuda.current_stream())
+            mp().mp_attn_cache_fwd(Q, kc, vc, ks, vs, O, LSE, table, cu, ln, ws, max_q=mq, stream=st)
+            outs.append((O, LSE))
+    torch.cuda.synchronize()
+    for i, (O, LSE) in enumerate(outs):
+        want = args[i % 2][3]
+        assert torch.equal(O.cpu(), want[0]) and torch.equal(LSE.cpu(), want[1])
 
 
 def test_decoding_steps_agree_with_the_whole_prompt():
