@@ -4,7 +4,9 @@ Argument marshalling only: every function below checks the torch tensors'
 dtype, shape, device and contiguity, takes their device pointers and the
 current CUDA stream, and calls the C entry point of the same name. All compute
 runs in the library's CUDA kernels. There is no fallback: if the library is
-missing or fails to load, calls raise.
+missing or fails to load, calls raise. The calls of a decoding step go through
+an extension first (``_lib/_mptp_bind.so``) that marshals ordinary arguments
+faster and leaves the others to the checks here.
 
 Shapes (row-major, contiguous):
   mp_mlp_fwd(X[T,h], A[h,f], B[f,h], Z[T,h], Y[T,f], U_save[T,f] | None, t)
@@ -32,12 +34,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libmptp.so")
+BIND_PATH = os.path.join(_PKG, "_lib", "_mptp_bind.so")
 
 MP_OK = 0
 MP_DEV_TIMEOUT = 0x1
@@ -153,6 +157,27 @@ def lib() -> ctypes.CDLL:
         L.mp_version.restype = _I
         _lib = L
     return _lib
+
+
+_bind = None
+
+
+def _fast():
+    """The extension that marshals a decoding step's calls; its functions return None for what they leave to the checks here."""
+    global _bind
+    if _bind is None:
+        lib()
+        if not os.path.exists(BIND_PATH):
+            raise OSError(f"_mptp_bind.so is not built ({BIND_PATH}); run `python -m tensor_transformer_layer_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_mptp_bind", BIND_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _bind = module
+    return _bind
+
+
+def _handle(stream):
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def status_string(code: int) -> str:
@@ -600,11 +625,14 @@ def mp_qk_norm_rope(x, y, wq, wk, pos, *, q_heads: int, sections, base: float = 
     """Norm of each query and key head with the rotation of mp_rope_axes in one pass: y = R(w x / sqrt(mean(x^2) + eps)),
     w = wq for the first q_heads heads, wk for the others. x, y [T, heads, d] (rows may be strided; y may be x), wq, wk [d],
     pos [axes, T] int32."""
+    flags = (1 if interleaved else 0) | (2 if per_axis else 0)
+    code = (_bind or _fast()).qk_norm_rope(x, y, wq, wk, pos, q_heads, sections, base, eps, flags, _handle(stream))
+    if code is not None:
+        return _check("mp_qk_norm_rope", code)
     size, nq = _norm_heads(x, q_heads)
     T, heads, d = size
     (px, ldx), (py, ldy) = _heads_view(x, "x", size), _heads_view(y, "y", size)
     axes, sec = _int_array(tuple(sections))
-    flags = (1 if interleaved else 0) | (2 if per_axis else 0)
     code = lib().mp_qk_norm_rope(px, py, _weight(wq, "wq", d, nq > 0), _weight(wk, "wk", d, nq < heads),
                                  _ptr(pos, "pos", torch.int32, (axes, T)), T, heads, nq, d, ldx, ldy, axes, sec,
                                  float(base), float(eps), flags, _stream(stream))
@@ -619,12 +647,16 @@ def mp_qk_norm_rope_bwd(x, dy, dx, wq, wk, dwq, dwk, pos, workspace, *, q_heads:
                         eps: float = 1e-6, interleaved: bool = False, per_axis: bool = False, stream=None) -> None:
     """Backward of mp_qk_norm_rope from its x: dx [T, heads, d] (rows may be strided; may be dy or x), dwq, dwk [d] fp32;
     workspace: mp_qk_norm_rope_bwd_workspace_bytes(T, heads, d) bytes."""
+    flags = (1 if interleaved else 0) | (2 if per_axis else 0)
+    code = (_bind or _fast()).qk_norm_rope_bwd(x, dy, dx, wq, wk, dwq, dwk, pos, workspace, q_heads, sections, base, eps,
+                                               flags, _handle(stream))
+    if code is not None:
+        return _check("mp_qk_norm_rope_bwd", code)
     size, nq = _norm_heads(x, q_heads)
     T, heads, d = size
     (px, ldx), (pg, ldg), (pd, ldd) = (_heads_view(x, "x", size), _heads_view(dy, "dy", size),
                                        _heads_view(dx, "dx", size))
     axes, sec = _int_array(tuple(sections))
-    flags = (1 if interleaved else 0) | (2 if per_axis else 0)
     wp, wb = _cuda_ws(workspace)
     code = lib().mp_qk_norm_rope_bwd(
         px, pg, pd, _weight(wq, "wq", d, nq > 0), _weight(wk, "wk", d, nq < heads),
@@ -660,16 +692,6 @@ def _pool(kc, vc, ks, vs, page_table, nseq):
     size = kc.shape
     pages, kv, page, d = size
     run = page * d
-    # What a right call passes, in as few steps as it takes; everything else is told apart below.
-    if type(kc) is type(vc) is type(ks) is type(vs) is torch.Tensor and kc.dtype is _F8 and vc.dtype is _F8 and \
-            ks.dtype is _F32 and vs.dtype is _F32 and vc.shape == size and ks.shape == vs.shape == (pages, kv) and \
-            kc.is_cuda and vc.is_cuda and ks.is_cuda and vs.is_cuda and pages > 1:
-        a, b, c, e = kc.stride()
-        (f, g), (h, i) = ks.stride(), vs.stride()
-        ldv = vc.stride(0)
-        if b == run and c == d and e == 1 and g == 1 and i == 1 and vc.stride() == (ldv, run, d, 1):
-            pool, pitches = (kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr()), (a, ldv, f, h)
-            return pool, pitches, _page_table(page_table, nseq), (pages, page_table.shape[1], page, kv, d)
     psk, ldsk = _page_view(ks, "ks", _F32, (pages, kv), [1])
     psv, ldsv = _page_view(vs, "vs", _F32, (pages, kv), [1])
     pk, ldk = _page_view(kc, "kc", _F8, size, [run, d, 1])
@@ -707,6 +729,9 @@ def mp_kv_cache_write(K, V, kc, vc, ks, vs, page_table, cu, start, *, max_n: int
     """New keys and values into an e4m3 cache: rows cu[i] .. cu[i+1]-1 of K, V [T, kv_heads, d] (rows may be strided)
     become positions start[i] ... of sequence i, in page page_table[i, position // page]. kc, vc [pages, kv_heads, page, d],
     ks, vs [pages, kv_heads] (pages may be strided). max_n: at least the longest sequence's rows."""
+    code = (_bind or _fast()).kv_cache_write(K, V, kc, vc, ks, vs, page_table, cu, start, max_n, d_status, _handle(stream))
+    if code is not None:
+        return _check("mp_kv_cache_write", code)
     pk, pv, pool, pt, pcu, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, max_n)
     code = lib().mp_kv_cache_write(pk, pv, *pool, pt, pcu, _ptr(start, "start", torch.int32, (nseq,)), *sizes,
                                    _status_ptr(d_status), _stream(stream))
@@ -716,6 +741,9 @@ def mp_kv_cache_write(K, V, kc, vc, ks, vs, page_table, cu, start, *, max_n: int
 def mp_kv_cache_read(kc, vc, ks, vs, K, V, page_table, cu, start=None, *, max_n: int, d_status=None,
                      stream=None) -> None:
     """Cached rows back to bf16: the arguments of mp_kv_cache_write, K and V written. start None: from position 0."""
+    code = (_bind or _fast()).kv_cache_read(K, V, kc, vc, ks, vs, page_table, cu, start, max_n, d_status, _handle(stream))
+    if code is not None:
+        return _check("mp_kv_cache_read", code)
     pk, pv, pool, pt, pcu, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, max_n)
     code = lib().mp_kv_cache_read(*pool, pk, pv, pt, pcu, _ptr(start, "start", torch.int32, (nseq,), True), *sizes,
                                   _status_ptr(d_status), _stream(stream))
@@ -732,6 +760,10 @@ def mp_attn_cache_fwd(Q, kc, vc, ks, vs, O, LSE, page_table, cu_q, lens, workspa
     """Attention of the last tokens of each sequence over its e4m3 cache (mp_kv_cache_write): O [Tq, heads, d] and LSE
     [heads, Tq] fp32 from Q [Tq, heads, d] (rows may be strided). cu_q [nseq + 1]: sequence i's queries; lens [nseq]: its
     cached tokens, the queries' own among them. causal: the last query sees the last token. scale: 1 / sqrt(d) by default."""
+    code = (_bind or _fast()).attn_cache_fwd(Q, kc, vc, ks, vs, O, LSE, page_table, cu_q, lens, workspace, max_q,
+                                             1 if causal else 0, scale, d_status, _handle(stream))
+    if code is not None:
+        return _check("mp_attn_cache_fwd", code)
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
         raise ValueError("Q must be a [tokens, heads, d] tensor")
     nseq, pcu = _sequences(cu_q, "cu_q")

@@ -1,24 +1,29 @@
-"""Build libmptp.so in-tree with nvcc for sm_103a (no CMake, parallel compiles).
+"""Build libmptp.so and the Python extension beside it in-tree (nvcc for sm_103a, g++; no CMake, parallel compiles).
 
     python -m tensor_transformer_layer_gb300.build
 
 Compiles every ``csrc/*.cu`` with ``-gencode arch=compute_103a,code=sm_103a``
 into ``_lib/`` and links ``_lib/libmptp.so`` (CUDA runtime linked statically;
 the driver's tensor-map encoder is reached through the runtime's entry-point
-query, so no libcuda link is needed at build time).
+query, so no libcuda link is needed at build time). ``csrc/mptp_bind.cpp``, which reads torch
+tensors, becomes ``_lib/_mptp_bind.so``: it links libmptp.so and the installed torch.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmptp.so")
+BIND_SRC = os.path.join(CSRC, "mptp_bind.cpp")
+BIND_PATH = os.path.join(LIB_DIR, "_mptp_bind.so")
 REPO = os.path.dirname(PKG_DIR)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -35,6 +40,20 @@ def nvcc_path() -> str:
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+
+
+def bind_command(target: str, obj: bool):
+    """Compiles the extension's object, or links it."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    out = target[:-3] + ".o"
+    if obj:
+        inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"), sysconfig.get_paths()["include"],
+               os.path.join(REPO, "include")]
+        return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{p}" for p in inc), "-c", BIND_SRC, "-o", out]
+    lib = os.path.join(torch_dir, "lib")
+    return ["g++", "-shared", out, "-o", target + ".tmp", f"-L{LIB_DIR}", "-lmptp", f"-L{lib}", "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
 
 
 def _stale(target: str, deps) -> bool:
@@ -58,6 +77,9 @@ def build(verbose: bool = False, force: bool = False) -> str:
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    if force or _stale(BIND_PATH[:-3] + ".o", [BIND_SRC, os.path.join(REPO, "include", "mptp.h")]):
+        cmd = bind_command(BIND_PATH, True)
+        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -77,6 +99,12 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout.decode(errors='replace')}")
         os.replace(tmp, LIB_PATH)
+    if force or _stale(BIND_PATH, [BIND_PATH[:-3] + ".o", LIB_PATH]):
+        cmd = bind_command(BIND_PATH, False)
+        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n$ {' '.join(cmd)}\n{r.stdout.decode(errors='replace')}")
+        os.replace(BIND_PATH + ".tmp", BIND_PATH)
     return LIB_PATH
 
 
