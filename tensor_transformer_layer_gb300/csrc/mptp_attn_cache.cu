@@ -19,7 +19,7 @@
 // four of bf16's eight bits each, exact but for elements below 2^-13 of the largest, which keep 2^-22 of it. Both pieces have
 // sums of their own (fp32, as every sum and statistic here). P = 2^(s - m + 7), s within m + 8 of the reference m, is
 // rounded to halves (2^-11 of its value, at least 2^-25 absolutely, 2^-32 of a probability of m) times the value's scale over
-// the largest value scale met so far.
+// the largest value scale met so far (2^-120 at least).
 //
 // Work. The tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, AC_ITEM places for what an item
 // costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
@@ -43,6 +43,7 @@ constexpr int AC_JOIN_WARPS = 4;   // warps of a row of the join
 constexpr int AC_BATCH = 10;       // parts in flight in each
 constexpr int AC_SEQS = 4;         // sequences a lane looks at in one step
 constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference before sums are scaled down
+constexpr float AC_LEAST = 7.52316384526264e-37f;  // 2^-120: value scales below count against it, so that its inverse is finite
 constexpr float AC_LOG2E = 1.4426950408889634f;
 constexpr float AC_LN2 = 0.6931471805599453f;
 
@@ -376,7 +377,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                             ac_copy16(at + AC_TILE * D, vs + i * 512);
                         }
                     }
-                    if (lane < 4) ac_copy4(ring_scales_u + (st * 4 + lane) * 4, my_scales + static_cast<uint64_t>(static_cast<uint32_t>(lane & 1 ? id[1] : id[0])) * pitch_scales, true);
+                    if (lane < 4) {
+                        const uint32_t page = static_cast<uint32_t>(lane & 1 ? id[1] : id[0]);
+                        ac_copy4(ring_scales_u + (st * 4 + lane) * 4, my_scales + static_cast<uint64_t>(page) * pitch_scales, true);
+                    }
                 } else {
                     // The sequence's last tile, or a page that is not in the pool: zeros where there is no token, NaN as the
                     // scales of such a page.
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 #pragma unroll
             for (int j = 0; j < KS; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
         }
-        float ref = 0.0f, inv_ref = 0.0f;  // largest value scale met
+        float ref = AC_LEAST, inv_ref = 1.0f / AC_LEAST;  // largest value scale met
         int id[2] = {ids[C::STAGES - 1][0], ids[C::STAGES - 1][1]};
         for (int k = 0; k < tiles; ++k) {
             ac_wait<C::STAGES - 2>();

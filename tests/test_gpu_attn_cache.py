@@ -145,6 +145,29 @@ def test_scales_far_apart():
     _check(_run(*inp, [1, 2], [500, 300]), *inp, [1, 2], [500, 300])
 
 
+def test_scales_below_the_normal_numbers():
+    """Value scales that no write leaves: results of 1e-36 and less keep what bf16 holds of them. Halves below 2^-14 add
+    2^-25 of 2^-120 a token (P carries 2^7), bf16 half its least step, 2^-134."""
+    new, lens = [1, 2, 1], [300, 90, 40]
+    Q, codes, scales, table = _make(new, lens, 4, 2, 64, 16, 23450)
+    for i, n in enumerate(lens):
+        for j in range(0, n, 16):
+            if i != 1 or j % 32 == 0:  # the second sequence has ordinary pages between
+                scales[int(table[i, j // 16]), 1] = (2.0 ** -121, 2.0 ** -127, 2.0 ** -135, 1.4e-45)[j // 16 % 4]
+    O, LSE = _run(Q, codes, scales, table, new, lens)
+    row = 0
+    for i, (nq, nk) in enumerate(zip(new, lens)):
+        k, v = (oracle.kv_cache_rows(f64(codes[:, j]), f64(scales[:, j]), table[i].tolist(), 16, 0, nk) for j in (0, 1))
+        at = slice(row, row + nq)
+        row += nq
+        wo, wl = oracle.attn_varlen_fwd(f64(Q)[at], k, v, [0, nq], [0, nk], True, 0.125)
+        wa, _ = oracle.attn_varlen_fwd(f64(Q)[at], k, np.abs(v), [0, nq], [0, nk], True, 0.125)
+        small = nk * 2.0 ** -152 * 448 + 2.0 ** -134
+        big = 2.0 ** -32 * nk * np.abs(v).max()
+        assert np.all(np.abs(f64(O)[at] - wo) <= 2.0 ** -8 * np.abs(wo) + 2.0 ** -9 * wa + small + big), i
+        assert np.all(np.abs(f64(LSE)[:, at] - wl) <= 2.0 ** -12 * (1 + np.abs(wl)))
+
+
 def test_scales_that_are_no_powers_of_two_and_large_queries():
     Q, codes, scales, table = _make([1, 3], [700, 200], 8, 2, 96, 32, 23500)
     scales *= 1.0 + torch.rand(scales.shape, generator=torch.Generator().manual_seed(5))
