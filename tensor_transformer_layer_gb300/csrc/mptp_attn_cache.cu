@@ -25,8 +25,10 @@
 // costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
 // walks its run alone, without a barrier: an item that lies within it is finished from registers. Runs that begin or
 // end inside an item leave a record in shared memory, joined once at the CTA's end; an item that several CTAs share leaves
-// a part of each in the workspace, which a second kernel adds in order, a block a row (it starts while the first ends; the CTA that
-// comes last adding them alone took 6 us longer for one sequence's 76 parts, 3 us for three).
+// a part of each in the workspace, which a second kernel adds: one block for every CTA that an item goes on from, so that
+// an item's parts less one share its elements and a thread has two to five parts to add, whatever their number (20.9 us for
+// one sequence of 131 k tokens, 76 parts an item, 21.5 for 77 sequences, three parts or two; a block a row 21.6 and 23.3, the CTA
+// that comes last adding them alone 6 us and 3 longer).
 #include "mptp_kv_cache.cuh"
 #include "mptp_launch.cuh"
 
@@ -39,17 +41,17 @@ constexpr int AC_ITEM = 4;      // places of an item besides its tiles
 constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
 #define AC_NONE __int_as_float(0xff800000)  // -inf: no key seen
 constexpr float AC_BIAS = 7.0f;    // exponent that P carries into halves
-constexpr int AC_JOIN_WARPS = 4;   // warps of a row of the join
-constexpr int AC_BATCH = 10;       // parts in flight in each
+constexpr int AC_JOIN = 256;       // threads of a block of the join
+constexpr int AC_BATCH = 3;        // parts in flight in each
 constexpr int AC_SEQS = 4;         // sequences a lane looks at in one step
 constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference before sums are scaled down
 constexpr float AC_LEAST = 7.52316384526264e-37f;  // 2^-120: value scales below count against it, so that its inverse is finite
 constexpr float AC_LOG2E = 1.4426950408889634f;
 constexpr float AC_LN2 = 0.6931471805599453f;
 
-// An item that a CTA began and others went on with: their number, its own among them (0: none).
+// An item that goes on from a CTA into the next: the CTA that began it and the number of those that share it (0: none).
 struct AcItem {
-    int parts, q0, row0, rows, head;
+    int parts, first, query, member, rows, head;  // query and member of a group of row 0
 };
 
 struct AcArgs {
@@ -62,7 +64,7 @@ struct AcArgs {
     float* parts;   // [2 AC_CTAS][rows][d + 2]
     long long ldq, ldo;
     int nseq, Tq, max_q, heads, group, causal;
-    float inv_group;  // 1 / group
+    float inv_group, inv_kv;  // 1 / group, 1 / key heads
     float scale_log2;
     uint32_t* status;
 };
@@ -138,13 +140,35 @@ struct AcShape {
 struct AcRecord {
     long long u0;  // -1: none
     int tile0, tile1, tiles;
-    int q0, row0, rows, head;
+    int query, member, rows, head;
 };
 
-// Where the c-th of n equal shares of the line begins; in 32 bits where they hold the product.
-__device__ __forceinline__ long long ac_share(long long total, int c, int n) {
-    const unsigned long long x = static_cast<unsigned long long>(total) * static_cast<unsigned>(c);
-    return x >> 32 ? static_cast<long long>(x / static_cast<unsigned>(n)) : static_cast<unsigned>(x) / static_cast<unsigned>(n);
+// x / d. (x + 1/2) / d in fp32 lies nearer to its integer than to the next for x below 2^20; a division of integers takes as long
+// as eight such.
+__device__ __forceinline__ int ac_div(int x, int d, float inv) {
+    return x < 1 << 20 ? static_cast<int>((static_cast<float>(x) + 0.5f) * inv) : x / d;
+}
+
+// Where the c-th of n equal shares of the line begins, total * c / n; the line in 32 bits where they hold it.
+__device__ __forceinline__ void ac_share(long long total, int c, int n, long long& begin, long long& end) {
+    long long each;
+    if (total >> 32 == 0) {
+        const unsigned low = static_cast<unsigned>(total);
+        each = n == AC_CTAS ? low / AC_CTAS : low / static_cast<unsigned>(n);
+    } else {
+        each = total / n;
+    }
+    const int rest = static_cast<int>(total - each * n);  // rest * c < 2^15
+    const float inv = 1.0f / static_cast<float>(n);
+    begin = each * c + ac_div(rest * c, n, inv);
+    end = each * (c + 1) + ac_div(rest * (c + 1), n, inv);
+}
+
+// The share that holds place x.
+__device__ __forceinline__ int ac_owner(long long total, long long x, int n) {
+    const unsigned long long y = static_cast<unsigned long long>(x + 1) * static_cast<unsigned>(n) - 1;
+    return static_cast<int>(y >> 32 || total >> 32 ? y / static_cast<unsigned long long>(total)
+                                                   : static_cast<unsigned>(y) / static_cast<unsigned>(total));
 }
 
 // One sequence's place in the line of tiles.
@@ -152,13 +176,8 @@ struct AcSeq {
     int q0, nq, len, tiles, items;  // tiles of one item; items = row tiles * key heads
 };
 template <int ROWS>
-__device__ __forceinline__ AcSeq ac_seq(const AcArgs& a, const KvPool& p, int seq) {
-    AcSeq s{0, 0, 0, 1, 0};
-    if (seq >= a.nseq) return s;
-    s.q0 = __ldg(a.cu_q + seq);
-    const int q1 = __ldg(a.cu_q + seq + 1);
-    s.len = __ldg(a.lens + seq);
-    s.nq = q1 - s.q0;
+__device__ __forceinline__ AcSeq ac_seq(const AcArgs& a, const KvPool& p, int q0, int q1, int len) {
+    AcSeq s{q0, q1 - q0, len, 1, 0};
     if (s.q0 < 0 || q1 < s.q0 || q1 > a.Tq || s.nq > a.max_q || s.len < 0 ||
         static_cast<long long>(s.len) > static_cast<long long>(p.max_pages) * p.page) {
         if (a.status != nullptr) atomicOr(a.status, KV_SEQ_RANGE);
@@ -168,25 +187,38 @@ __device__ __forceinline__ AcSeq ac_seq(const AcArgs& a, const KvPool& p, int se
     s.items = (s.nq * a.group + ROWS - 1) / ROWS * p.kv_heads;
     return s;
 }
+// Of sequences seq ... seq + N - 1, none behind the last: all of them asked for before the first is looked at.
+template <int ROWS, int N>
+__device__ __forceinline__ void ac_seqs(const AcArgs& a, const KvPool& p, int seq, AcSeq (&s)[N]) {
+    int q[N + 1], len[N];
+#pragma unroll
+    for (int k = 0; k <= N; ++k) q[k] = seq + k <= a.nseq ? __ldg(a.cu_q + seq + k) : 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) len[k] = seq + k < a.nseq ? __ldg(a.lens + seq + k) : 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        s[k] = AcSeq{0, 0, 0, 1, 0};
+        if (seq + k < a.nseq) s[k] = ac_seq<ROWS>(a, p, q[k], q[k + 1], len[k]);
+    }
+}
 
 // Float2 index within a row of the join buffer: eight lanes that write the same j land in different banks.
 __device__ __forceinline__ int ac_join(int i, int row) { return i ^ (((i >> 4) & 1) | ((row & 6))); }
 
-// Row `col` of a row tile as a query of its sequence and a head of its group. (col + rem + 1/2) / group in fp32 lies nearer
-// to its integer than to the next for sums below 2^20.
+// Row `col` of a row tile whose row 0 is head `member` of a group, as a query after that one's and a head of its group.
 struct AcRow {
     int query, member;
 };
-__device__ __forceinline__ AcRow ac_row(const AcArgs& a, int query0, int rem, int col) {
-    const int n = rem + col, q = static_cast<int>((static_cast<float>(n) + 0.5f) * a.inv_group);
-    return {query0 + q, n - q * a.group};
+__device__ __forceinline__ AcRow ac_row(const AcArgs& a, int query, int member, int col) {
+    const int n = member + col, q = static_cast<int>((static_cast<float>(n) + 0.5f) * a.inv_group);  // n < 2^16 + 16: as ac_div
+    return {query + q, n - q * a.group};
 }
 
 // The output of row `row` of an item, from its sums x in units of the values and sum of probabilities: four elements at d.
-__device__ __forceinline__ void ac_store(const AcArgs& a, int q0, int head, const AcRow& row, int d, int D, const float4& x,
-                                         float top, float sum) {
+__device__ __forceinline__ void ac_store(const AcArgs& a, int head, const AcRow& row, int d, int D, const float4& x, float top,
+                                         float sum) {
     const int hd = head * a.group + row.member;
-    const long long q = q0 + row.query;
+    const long long q = row.query;
     const float inv = 1.0f / sum;
     uint2 out = make_uint2(0, 0);  // a row that sees no key, whatever its sums hold
     if (sum != 0.0f) {
@@ -217,8 +249,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     long long mine = 0;  // places of the lane's sequences
     auto look_at = [&](int base) {
         mine = 0;
-#pragma unroll
-        for (int k = 0; k < AC_SEQS; ++k) held[k] = ac_seq<C::ROWS>(a, p, base + lane * AC_SEQS + k);
+        ac_seqs<C::ROWS>(a, p, base + lane * AC_SEQS, held);
 #pragma unroll
         for (int k = 0; k < AC_SEQS; ++k) mine += places(held[k]);
         long long upto = mine;
@@ -251,7 +282,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     if (tid == 0) left->parts = 0;
     if (cta >= ctas) return;
     if (lane < 2) rec[2 * warp + lane].u0 = -1;
-    const long long cta_pos = ac_share(total, cta, ctas), cta_end = ac_share(total, cta + 1, ctas);
+    long long cta_pos, cta_end;
+    ac_share(total, cta, ctas, cta_pos, cta_end);
     long long pos = cta_pos + (cta_end - cta_pos) * warp / AC_WARPS;
     const long long end = cta_pos + (cta_end - cta_pos) * (warp + 1) / AC_WARPS;
     int seq = 0, first = 0;
@@ -305,7 +337,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     while (pos < end) {
         while (seq < a.nseq && pos >= seq_start + places(s)) {
             seq_start += places(s);
-            s = ac_seq<C::ROWS>(a, p, ++seq);
+            AcSeq one[1];
+            ac_seqs<C::ROWS>(a, p, ++seq, one);
+            s = one[0];
         }
         if (seq >= a.nseq) break;
         const int span = s.tiles + AC_ITEM;
@@ -318,9 +352,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 ++row_tile;
             }
         } else {
-            local = ahead <= 0x7fffffff ? static_cast<int>(ahead) / span : static_cast<int>(ahead / span);
+            local = ahead <= 0x7fffffff ? ac_div(static_cast<int>(ahead), span, __frcp_rn(static_cast<float>(span)))
+                                        : static_cast<int>(ahead / span);
             off0 = static_cast<int>(ahead - static_cast<long long>(local) * span);
-            row_tile = local / p.kv_heads;
+            row_tile = ac_div(local, p.kv_heads, a.inv_kv);
             head = local - row_tile * p.kv_heads;
             last_seq = seq;
         }
@@ -329,7 +364,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         pos += take;
         if (tile1 <= tile0) continue;
         const int row0 = row_tile * C::ROWS;
-        const int query0 = row0 == 0 ? 0 : row0 / a.group, rem0 = row0 - query0 * a.group;
+        const int ahead0 = ac_div(row0, a.group, a.inv_group);  // queries in front of the tile's first
+        const int query0 = s.q0 + ahead0, rem0 = row0 - ahead0 * a.group;
         const int rows = min(C::ROWS, s.nq * a.group - row0);
         const int32_t* table = p.table + static_cast<long long>(seq) * p.max_pages;
 
@@ -424,7 +460,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const AcRow row = ac_row(a, query0, rem0, n * 8 + g);
-            const __nv_bfloat16* src = a.Q + (s.q0 + row.query) * a.ldq + (head * a.group + row.member) * D;
+            const __nv_bfloat16* src = a.Q + row.query * a.ldq + (head * a.group + row.member) * D;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 // D = 128: 16 elements of each half; else D / 4 neighbouring ones
@@ -471,11 +507,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < 2; ++j) {
                 fq[n][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
                 const int col = n * 8 + 2 * t + j;
-                limit[n][j] = col < rows && a.causal ? s.len - s.nq + ac_row(a, query0, rem0, col).query + 1 : s.len;
+                limit[n][j] = col < rows && a.causal ? s.len - s.nq + ac_row(a, ahead0, rem0, col).query + 1 : s.len;
             }
         }
         // Below this tile no column is masked.
-        const int clear = a.causal ? s.len - s.nq + query0 + 1 : s.len;
+        const int clear = a.causal ? s.len - s.nq + ahead0 + 1 : s.len;
 
         float o[KS][NT][4];
         float m[NT][2], l[NT][2];
@@ -669,7 +705,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                     const AcRow at = ac_row(a, query0, rem0, row);
 #pragma unroll
                     for (int i = 0; i < KS; i += 2)
-                        ac_store(a, s.q0, head, at, g * (D / 8) + 2 * i, D,
+                        ac_store(a, head, at, g * (D / 8) + 2 * i, D,
                                  make_float4(o[i][n][j] * ref, o[i][n][2 + j] * ref, o[i + 1][n][j] * ref, o[i + 1][n][2 + j] * ref),
                                  m[n][j], l[n][j]);
                 }
@@ -694,8 +730,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             r.tile0 = tile0;
             r.tile1 = tile1;
             r.tiles = s.tiles;
-            r.q0 = s.q0;
-            r.row0 = row0;
+            r.query = query0;
+            r.member = rem0;
             r.rows = rows;
             r.head = head;
         }
@@ -712,7 +748,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const unsigned chain = __shfl_sync(0xffffffffu, mates, r0);
         todo &= ~chain;
         const AcRecord r = rec[r0];
-        const bool whole = r.tile0 == 0 && rec[31 - __clz(chain)].tile1 == r.tiles;
+        const bool on = rec[31 - __clz(chain)].tile1 < r.tiles;  // goes on in the next CTA
+        const bool whole = r.tile0 == 0 && !on;
         const bool begun = r.tile0 > 0;  // in an earlier CTA
         float* part = a.parts + static_cast<long long>(cta * 2 + (begun ? 0 : 1)) * C::PART;
         for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
@@ -738,84 +775,88 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 x.w += v.y * f;
             }
             if (whole) {
-                ac_store(a, r.q0, r.head, ac_row(a, r.row0 / a.group, r.row0 % a.group, row), c * 2, D, x, top, sum);
+                ac_store(a, r.head, ac_row(a, r.query, r.member, row), c * 2, D, x, top, sum);
             } else {
                 *reinterpret_cast<float4*>(part + row * D + c * 2) = x;
                 if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = make_float2(top, sum);
             }
         }
-        if (!whole && !begun && tid == 0) {
-            // begun here: the CTAs up to that of its last tile have parts too
-            left->parts = static_cast<int>(((r.u0 + AC_ITEM + r.tiles) * ctas - 1) / total) - cta + 1;
-            left->q0 = r.q0;
-            left->row0 = r.row0;
+        if (on && tid == 0) {
+            left->first = ac_owner(total, r.u0 + AC_ITEM, ctas);
+            left->parts = ac_owner(total, r.u0 + AC_ITEM + r.tiles - 1, ctas) - left->first + 1;
+            left->query = r.query;
+            left->member = r.member;
             left->rows = r.rows;
             left->head = r.head;
         }
     }
 }
 
-// Adds the parts of the item that CTA blockIdx.x / ROWS of the kernel before began and did not finish, if there is one: a
-// block a row, each warp a quarter of the parts, AC_BATCH of them asked for at once.
+// Adds the parts of the item that goes on from CTA blockIdx.x of the kernel before, if there is one: of its float4 elements
+// those that fall to this block, a few threads of a warp for each, every one a share of the parts.
 template <int D, int NT>
-__global__ void __launch_bounds__(AC_JOIN_WARPS * 32) attn_cache_join_kernel(const AcArgs a) {
+__global__ void __launch_bounds__(AC_JOIN) attn_cache_join_kernel(const AcArgs a) {
     using C = AcShape<D, NT>;
-    __shared__ float4 red[AC_JOIN_WARPS][D / 4];
-    __shared__ float red_sum[AC_JOIN_WARPS];
-    const int cta = blockIdx.x / C::ROWS, row = blockIdx.x % C::ROWS, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
-    const AcItem it = a.items[cta];
-    if (it.parts == 0 || row >= it.rows) return;
-    // the first CTA began the item, the others found it begun
-    auto part = [&](int k) { return a.parts + static_cast<long long>((cta + k) * 2 + (k == 0 ? 1 : 0)) * C::PART; };
-    auto stat = [&](int k) { return *reinterpret_cast<const float2*>(part(k) + C::ROWS * D + row * 2); };
-    float top = AC_NONE;
-    for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, stat(k).x);
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
-    for (int k0 = warp; k0 < it.parts; k0 += AC_JOIN_WARPS * AC_BATCH) {
-        float2 ml[AC_BATCH];
-        float4 v[AC_BATCH];
+    const AcItem it = a.items[blockIdx.x];
+    if (it.parts == 0) return;
+    const int all = it.rows * (D / 4), blocks = it.parts - 1;
+    const int mine = ac_div(all + blocks - 1, blocks, __frcp_rn(static_cast<float>(blocks)));
+    const int begin = (static_cast<int>(blockIdx.x) - it.first) * mine, end = min(begin + mine, all);
+    // Elements of a warp at a time: a power of two that all warps together hold `mine` with, of 32 at most.
+    const int shift = min(5, 32 - __clz((mine - 1) / (AC_JOIN / 32))), wide = 1 << shift;
+    const int share = 32 >> shift, k0 = lane >> shift;
+    for (int at = begin + (warp << shift); at < end; at += AC_JOIN / 32 << shift) {
+        const int i = at + (lane & (wide - 1)), row = i / (D / 4), c = i % (D / 4);
+        const bool live = i < end;
+        float top = AC_NONE, sum = 0.0f;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k1 = k0; k1 < it.parts; k1 += share * AC_BATCH) {
+            float2 ml[AC_BATCH];
+            float4 v[AC_BATCH];
+            float high = top;
 #pragma unroll
-        for (int j = 0; j < AC_BATCH; ++j) {
-            const int k = k0 + j * AC_JOIN_WARPS;
-            ml[j] = make_float2(AC_NONE, 0.0f);
-            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (k >= it.parts) continue;
-            ml[j] = stat(k);
-            if (lane < D / 4) v[j] = *(reinterpret_cast<const float4*>(part(k) + row * D) + lane);
+            for (int j = 0; j < AC_BATCH; ++j) {
+                const int k = k1 + j * share;
+                ml[j] = make_float2(AC_NONE, 0.0f);
+                v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (!live || k >= it.parts) continue;
+                // the first CTA began the item, the others found it begun
+                const float* part = a.parts + static_cast<long long>((it.first + k) * 2 + (k == 0 ? 1 : 0)) * C::PART;
+                ml[j] = *reinterpret_cast<const float2*>(part + C::ROWS * D + row * 2);
+                v[j] = *reinterpret_cast<const float4*>(part + i * 4);
+            }
+#pragma unroll
+            for (int j = 0; j < AC_BATCH; ++j) high = fmaxf(high, ml[j].x);
+            const float down = top == high ? 1.0f : ac_ex2(top - high);
+            top = high;
+            sum *= down;
+            x = make_float4(x.x * down, x.y * down, x.z * down, x.w * down);
+#pragma unroll
+            for (int j = 0; j < AC_BATCH; ++j) {
+                const float f = ml[j].x == top ? 1.0f : ac_ex2(ml[j].x - top);
+                sum += ml[j].y * f;
+                x.x += v[j].x * f;
+                x.y += v[j].y * f;
+                x.z += v[j].z * f;
+                x.w += v[j].w * f;
+            }
         }
-        if (k0 == warp)
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-#pragma unroll
-        for (int j = 0; j < AC_BATCH; ++j) {
-            if (k0 + j * AC_JOIN_WARPS >= it.parts) continue;
-            const float f = ml[j].x == top ? 1.0f : ac_ex2(ml[j].x - top);
-            sum += ml[j].y * f;
-            x.x += v[j].x * f;
-            x.y += v[j].y * f;
-            x.z += v[j].z * f;
-            x.w += v[j].w * f;
+        for (int off = wide; off < 32; off <<= 1) {
+            const float other = __shfl_xor_sync(0xffffffffu, top, off), high = fmaxf(top, other);
+            const float f = top == high ? 1.0f : ac_ex2(top - high), g = other == high ? 1.0f : ac_ex2(other - high);
+            top = high;
+            sum = sum * f + __shfl_xor_sync(0xffffffffu, sum, off) * g;
+            x.x = x.x * f + __shfl_xor_sync(0xffffffffu, x.x, off) * g;
+            x.y = x.y * f + __shfl_xor_sync(0xffffffffu, x.y, off) * g;
+            x.z = x.z * f + __shfl_xor_sync(0xffffffffu, x.z, off) * g;
+            x.w = x.w * f + __shfl_xor_sync(0xffffffffu, x.w, off) * g;
         }
+        if (live && lane < wide)
+            ac_store(a, it.head, ac_row(a, it.query, it.member, row), c * 4, D, x, top, sum);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (lane < D / 4) red[warp][lane] = x;
-    if (lane == 0) red_sum[warp] = sum;
-    __syncthreads();
-    if (warp != 0 || lane >= D / 4) return;
-#pragma unroll
-    for (int w = 1; w < AC_JOIN_WARPS; ++w) {
-        const float4 v = red[w][lane];
-        x.x += v.x;
-        x.y += v.y;
-        x.z += v.z;
-        x.w += v.w;
-        sum += red_sum[w];
-    }
-    ac_store(a, it.q0, it.head, ac_row(a, it.row0 / a.group, it.row0 % a.group, row), lane * 4, D, x, top, sum);
 }
 
 template <int D, int NT>
@@ -826,7 +867,7 @@ static cudaError_t launch_attn_cache(const AcArgs& a, const KvPool& p, cudaStrea
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_pdl(kernel, dim3(AC_CTAS), dim3(AC_THREADS), C::SMEM, s, a, p);
     if (f != cudaSuccess) return f;
-    return launch_pdl(attn_cache_join_kernel<D, NT>, dim3(AC_CTAS * C::ROWS), dim3(AC_JOIN_WARPS * 32), 0, s, a);
+    return launch_pdl(attn_cache_join_kernel<D, NT>, dim3(AC_CTAS), dim3(AC_JOIN), 0, s, a);
 }
 
 constexpr size_t AC_ITEM_BYTES = (AC_CTAS * sizeof(AcItem) + 15) / 16 * 16;
@@ -908,6 +949,7 @@ extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, cons
     a.heads = heads;
     a.group = heads / kv_heads;
     a.inv_group = 1.0f / static_cast<float>(a.group);
+    a.inv_kv = 1.0f / static_cast<float>(kv_heads);
     a.causal = causal != 0;
     a.scale_log2 = scale * AC_LOG2E;
     p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
