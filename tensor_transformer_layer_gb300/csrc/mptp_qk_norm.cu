@@ -8,12 +8,14 @@
 //
 // Bound by memory: x once in and y once out; backward x and dy in and dx out. A head lies across G = d / (2 VEC) lanes, VEC
 // rotated pairs in each, or as many unrotated elements (cosine 1, sine 0), so that the sums of squares are a few shuffles
-// within the G lanes. A warp walks tokens (or a share of a token's heads where tokens are few), query heads or key heads, as
-// many heads at once as it has lanes for; the angles' sines are computed once a token, and with the weight they make two
-// coefficients an element, y = r (x P + partner Q). All of it is fp32, two elements an instruction, and each output is
-// rounded once.
+// within the G lanes. A warp walks tokens (or a share of a token's steps where tokens are few), as many heads at once as it has
+// lanes for; the angles' sines are computed once a token, and with the weight they make two coefficients an element, y = r (x P +
+// partner Q). All of it is fp32, two elements an instruction, and each output is rounded once.
+// A lane keeps to query heads or to key heads. Where lanes for both kinds side by side take no more steps than warps for
+// // either kind alone (16 and 4 heads of 96, five at once: four steps, not four and one), a warp has both (16,384 tokens of those
+// 22.6 us forward and 38.2 backward, apart 27.7 and 41.0; 1111 tokens of 16 and 16 heads of 64 3.3 and 8.0, apart 4.2 and 9.7).
 // The weights' gradients: a lane of the backward pass keeps its columns' sums in registers over all its tokens, a block
-// adds its lanes' in shared memory and writes one row of the workspace, a second kernel adds the rows: fixed order, no
+// adds its lanes' in shared memory and writes two rows of the workspace, a second kernel adds the rows: fixed order, no
 // atomics.
 #include "mptp_internal.h"
 #include "mptp_launch.cuh"
@@ -25,9 +27,10 @@ namespace mptp {
 constexpr int QKN_WARPS = 4;         // warps of a block
 constexpr int QKN_STAGES = 4;        // steps in flight, and the one in hand
 constexpr int QKN_PER_SM = 4;        // blocks on an SM
-constexpr int QKN_RUN = 24;          // steps of a warp of the forward pass
+constexpr int QKN_FULL = QKN_PER_SM * 152;
+constexpr int QKN_RUN = 48;          // steps of a warp of the forward pass
 constexpr int QKN_BWD_PER_SM = 3;
-constexpr int QKN_BWD_BLOCKS = QKN_BWD_PER_SM * 152;  // rows of the workspace at most
+constexpr int QKN_BWD_BLOCKS = QKN_BWD_PER_SM * 152;  // pairs of rows of the workspace at most
 
 struct QkNormArgs {
     const __nv_bfloat16* x;
@@ -36,12 +39,15 @@ struct QkNormArgs {
     const __nv_bfloat16* wq;
     const __nv_bfloat16* wk;
     const int32_t* pos;  // [axes][T]
-    float* sums;         // [blocks][d]
+    float* sums;         // [blocks][2][d]
     long long ldx, ldy, lddy;
     int T, heads, q_heads, d, pairs, axes;
-    int shares;    // log2 of the warps that share a token; backward: of query heads,
-    int k_shares;  // and of key heads,
-    int q_blocks;  // and the blocks that walk query heads, the others key heads
+    // Of warps that have query heads, or both kinds, and of those of the blocks from q_blocks on, key heads alone:
+    int shares, k_shares;  // log2 of the warps that share a token's steps
+    int q_slots;           // heads at once that are queries', of the first
+    int q_own, k_own;      // heads of the first lanes of either kind
+    int steps, k_steps;    // of a token
+    int q_blocks;
     float eps, inv_d;
 };
 
@@ -204,45 +210,43 @@ __device__ __forceinline__ void qk_copy(uint32_t dst, const void* src, int take)
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(take) : "memory");
 }
 
-// The walk of a warp: items (a token's heads of one kind, or a share of them) `stride` apart, each in steps of as many heads
-// as the warp has lanes for. A step's loads go to the lane's own places in shared memory (cp.async: nothing of them waits in
+// The walk of a warp: items (a token's steps, or every 2^shares-th of them) `stride` apart; in step k each G lanes take the k-th of
+// their heads, `hop` elements apart. A step's loads go to the lane's own places in shared memory (cp.async: nothing of them waits in
 // registers, and no lane reads another's), QKN_STAGES - 1 steps ahead; N arrays are read, and the token's positions with its
-// first step. Lanes behind the last head get zeros.
+// first step. Lanes without a head get zeros.
 template <int VEC, int N>
 struct QkWalk {
     static constexpr int BYTES = 2 * VEC;                      // of a vector
     static constexpr int STAGE = N * 2 * BYTES * 32 + 16;      // of a warp's stage: the vectors, then the positions
-    const __nv_bfloat16* src[N];   // the lane's first vector of head 0 of token 0
+    const __nv_bfloat16* src[N];   // the lane's first vector of its first head, of token 0
     const __nv_bfloat16* at[N];    // and of the step to be asked for
     long long ld[N];
     const int32_t* pos;            // lane k < axes: of axis k
     uint32_t ring, pos_ring;       // the lane's places in the first stage
     bool has_axis;
     unsigned items, stride, next;
-    int shares, per_warp, h0, h1, wide, last, d, second, next_h, stage;
+    int shares, steps, own, hop, second, next_k, stage;  // own: the lane's heads
 
-    __device__ __forceinline__ int first_head(unsigned item) const {
-        return h0 + static_cast<int>(item & ((1u << shares) - 1)) * per_warp;
-    }
+    __device__ __forceinline__ int first_step(unsigned item) const { return static_cast<int>(item & ((1u << shares) - 1)); }
     __device__ __forceinline__ void start() {
-        next_h = first_head(next);
+        next_k = first_step(next);
 #pragma unroll
-        for (int n = 0; n < N; ++n) at[n] = src[n] + (next >> shares) * ld[n] + next_h * d;
+        for (int n = 0; n < N; ++n) at[n] = src[n] + (next >> shares) * ld[n] + next_k * hop;
     }
     __device__ __forceinline__ void fetch() {
         if (next < items) {
-            const int take = next_h <= last ? BYTES : 0;
+            const int take = next_k < own ? BYTES : 0;
             const uint32_t to = ring + stage * STAGE;
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 const __nv_bfloat16* from = take != 0 ? at[n] : src[n];  // an address in the tensor either way
                 qk_copy<BYTES>(to + (2 * n) * BYTES * 32, from, take);
                 qk_copy<BYTES>(to + (2 * n + 1) * BYTES * 32, from + second, take);
-                at[n] += wide * d;
+                at[n] += hop << shares;
             }
-            if (has_axis && next_h < h0 + wide) qk_copy<4>(pos_ring + stage * STAGE, pos + (next >> shares), 4);
-            next_h += wide;
-            if (next_h >= h1) {
+            if (has_axis && next_k >> shares == 0) qk_copy<4>(pos_ring + stage * STAGE, pos + (next >> shares), 4);
+            next_k += 1 << shares;
+            if (next_k >= steps) {
                 next += stride;
                 start();
             }
@@ -261,7 +265,6 @@ __device__ __forceinline__ void qk_take(const uint8_t* at, float2 (&f)[VEC]) {
     qk_floats(x, f);
 }
 
-// A warp walks query heads or key heads, by its block.
 template <int VEC, bool INTER, int SUM, bool BACKWARD>
 __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QKN_PER_SM) qk_norm_kernel(
     const __grid_constant__ RopeTable tab, const QkNormArgs a) {
@@ -269,9 +272,14 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const QkLane<VEC, INTER> L(a.d, a.pairs, lane);
-    const bool keys = static_cast<int>(blockIdx.x) >= a.q_blocks;
-    const int block = keys ? blockIdx.x - a.q_blocks : blockIdx.x;
-    const int sub = L.live ? L.sub : 0;
+    // The lane's heads: every slots-th of its kind, `own` of them from head0 on.
+    const bool second = static_cast<int>(blockIdx.x) >= a.q_blocks;  // keys alone
+    const int q_slots = second ? 0 : a.q_slots;
+    const bool keys = L.sub >= q_slots;
+    const int slots = keys ? L.per_warp - q_slots : q_slots, first = keys ? a.q_heads + L.sub - q_slots : L.sub;
+    const int most = keys ? a.k_own : a.q_own;
+    const int own = L.live ? most - (first + (most - 1) * slots >= (keys ? a.heads : a.q_heads) ? 1 : 0) : 0;
+    const int head0 = own > 0 ? first : 0;
     uint4* table = reinterpret_cast<uint4*>(smem + QKN_WARPS * QKN_STAGES * Walk::STAGE);
     float* cs = reinterpret_cast<float*>(table + ROPE_MAX_PAIRS) + warp * 2 * ROPE_MAX_PAIRS;
     for (int i = threadIdx.x; i < a.pairs; i += QKN_WARPS * 32)
@@ -282,10 +290,10 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
 
     const uint8_t* ring = smem + warp * QKN_STAGES * Walk::STAGE + lane * Walk::BYTES;
     Walk walk;
-    walk.src[0] = a.x + sub * a.d + L.o0;
+    walk.src[0] = a.x + head0 * a.d + L.o0;
     walk.ld[0] = a.ldx;
     if constexpr (BACKWARD) {
-        walk.src[1] = a.dy + sub * a.d + L.o0;
+        walk.src[1] = a.dy + head0 * a.d + L.o0;
         walk.ld[1] = a.lddy;
     }
     walk.has_axis = lane < a.axes;
@@ -293,30 +301,27 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
     walk.ring = smem_u32(ring);
     const uint8_t* pos_ring = smem + warp * QKN_STAGES * Walk::STAGE + Walk::STAGE - 16;
     walk.pos_ring = smem_u32(pos_ring) + (lane & 3) * 4;
-    walk.shares = keys ? a.k_shares : a.shares;
+    walk.shares = second ? a.k_shares : a.shares;
     walk.items = static_cast<unsigned>(a.T) << walk.shares;
-    walk.stride = (keys ? gridDim.x - a.q_blocks : a.q_blocks) * QKN_WARPS;
-    walk.h0 = keys ? a.q_heads : 0;
-    walk.h1 = keys ? a.heads : a.q_heads;
-    walk.wide = L.per_warp << walk.shares;  // heads of a step, all shares'
-    walk.per_warp = L.per_warp;
-    walk.last = L.live ? walk.h1 - 1 - sub : -1;
-    walk.d = a.d;
+    walk.stride = (second ? gridDim.x - a.q_blocks : a.q_blocks) * QKN_WARPS;
+    walk.steps = second ? a.k_steps : a.steps;
+    walk.own = own;
+    walk.hop = slots * a.d;
     walk.second = L.o1 - L.o0;
     walk.stage = 0;
-    unsigned item = block * QKN_WARPS + warp;
+    unsigned item = (second ? blockIdx.x - a.q_blocks : blockIdx.x) * QKN_WARPS + warp;
     walk.next = item;
     walk.start();
 #pragma unroll
     for (int k = 0; k < QKN_STAGES - 1; ++k) walk.fetch();
 
-    const __nv_bfloat16* weight = keys ? a.wk : a.wq;
+    const __nv_bfloat16* weight = (own > 0 ? keys : a.q_heads == 0) ? a.wk : a.wq;
     float2 w[VEC], acc[VEC], P[VEC], Q[VEC];
     if constexpr (BACKWARD) qk_weight(weight, L, w);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = make_float2(0.0f, 0.0f);
     const int turn[2] = {lane - L.g + (L.g + L.groups / 3) % L.groups, lane - L.g + (L.g + L.groups / 3 * 2) % L.groups};
-    int h = walk.first_head(item), stage = 0;
+    int step = walk.first_step(item), stage = 0;
     bool fresh = true;  // a token's first step
     __nv_bfloat16* out = nullptr;
     while (item < walk.items) {
@@ -331,13 +336,12 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
             qk_take_angles(cs, L, c, s);
             if constexpr (!BACKWARD) qk_weight(weight, L, w);  // again for each token: sixteen registers less
             qk_coefficients<VEC, INTER>(c, s, BACKWARD ? nullptr : w, P, Q);
-            out = a.y + token * a.ldy + (sub + h) * a.d;
+            out = a.y + token * a.ldy + head0 * a.d + step * walk.hop;
             fresh = false;
         }
         float2 x[VEC], y[VEC];
         qk_take<VEC>(at, x);
         float2 ss = make_float2(0.0f, 0.0f);
-        const bool mine = h <= walk.last;
         if constexpr (!BACKWARD) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss = fma2(x[j], x[j], ss);
@@ -369,13 +373,13 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
                 y[j] = mul2(fma2(x[j], make_float2(m, m), mul2(w[j], g[j])), make_float2(r, r));
             }
         }
-        if (mine) qk_store(y, out, L);
-        out += walk.wide * a.d;
+        if (step < own) qk_store(y, out, L);
+        out += walk.hop << walk.shares;
         stage = stage == QKN_STAGES - 1 ? 0 : stage + 1;
-        h += walk.wide;
-        if (h >= walk.h1) {
+        step += 1 << walk.shares;
+        if (step >= walk.steps) {
             item += walk.stride;
-            h = walk.first_head(item);
+            step = walk.first_step(item);
             fresh = true;
         }
     }
@@ -394,18 +398,24 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QK
             }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < a.d; i += QKN_WARPS * 32) {
+        // Queries' columns, then keys'; of warps with one kind that kind's.
+        const int from = q_slots == 0 ? a.d : 0, to = q_slots == L.per_warp ? a.d : 2 * a.d;
+        for (int i = from + threadIdx.x; i < to; i += QKN_WARPS * 32) {
+            const bool k = i >= a.d;
+            const float* col = red + (k ? q_slots * a.d + i - a.d : i);
             float t = 0.0f;
-            for (int k = 0; k < QKN_WARPS * L.per_warp; ++k) t += red[k * a.d + i];
-            a.sums[static_cast<long long>(blockIdx.x) * a.d + i] = t;
+            for (int u = k ? L.per_warp - q_slots : q_slots; u > 0; --u, col += a.d)
+#pragma unroll
+                for (int v = 0; v < QKN_WARPS; ++v) t += col[v * L.per_warp * a.d];
+            a.sums[static_cast<long long>(blockIdx.x) * 2 * a.d + i] = t;
         }
     }
 }
 
-// dwq and dwk from the blocks' rows, the first q_rows of them queries': a block takes 32 of d columns of one of the two,
-// 32 warps a share of the rows each.
-__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* sums, float* dwq, float* dwk, int q_rows, int rows,
-                                                         int d) {
+// dwq and dwk from the blocks' rows [2][d], queries' in the first q_rows and keys' from k_row on: a block takes 32 of d columns
+// of one of the two, 32 warps a share of the rows each.
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* sums, float* dwq, float* dwk, int q_rows, int k_row,
+                                                         int rows, int d) {
     __shared__ float red[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int half = gridDim.x / 2;
@@ -413,11 +423,11 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* sums, flo
     const int col = (blockIdx.x - (keys ? half : 0)) * 32 + lane;
     grid_dependency_wait();
     grid_launch_dependents();
+    const float* at = sums + (keys ? d : 0) + col;
     float t = 0.0f;
     if (col < d)
 #pragma unroll 8
-        for (int r = (keys ? q_rows : 0) + warp; r < (keys ? rows : q_rows); r += 32)
-            t += sums[static_cast<long long>(r) * d + col];
+        for (int r = (keys ? k_row : 0) + warp; r < (keys ? rows : q_rows); r += 32) t += at[static_cast<long long>(r) * 2 * d];
     red[warp][lane] = t;
     __syncthreads();
     float* out = keys ? dwk : dwq;
@@ -430,35 +440,72 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float* sums, flo
 // The lanes' vectors are 16 bytes where each half of a head and what is not rotated divide into them, else 8.
 static bool qk_wide(int d, long long pairs) { return d % 16 == 0 && pairs % 8 == 0; }
 
-// Log2 of the warps that share a token's heads: doubled while there would be fewer than eight warps on each of 152 SMs.
-static int qk_shares(int T, int heads, int d, bool wide) {
-    const int in_hand = 32 / (d / (wide ? 16 : 8));
-    int shares = 0;
-    while ((static_cast<long long>(T) << shares) < 8LL * 152 && in_hand << shares < heads) ++shares;
-    return shares;
-}
+static int qk_steps(int heads, int slots) { return (heads + slots - 1) / slots; }
 
-// Shares of query heads and of key heads, and the blocks that walk each. Forward: a warp walks about QKN_RUN steps, so that
-// the blocks that end late are small. Backward: as many blocks as the chip holds at most (each leaves a row of sums),
-// divided so that neither kind's last warp ends much later than the other's; a token's angles cost about a quarter of a step.
-static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
-    const int in_hand = 32 / (a.d / (wide ? 16 : 8));
+// How heads are dealt to lanes, warps and blocks. A warp has both kinds of heads where that takes no more steps than warps for
+// either. A token's steps are shared while there would be fewer than eight warps on each of 152 SMs. Forward: a warp walks about
+// QKN_RUN steps, so that the blocks that end late are small. Backward: as many blocks as the chip holds at most (each leaves
+// a row of sums of either kind), divided so that neither kind's last warp ends much later than the other's; a token's angles
+// cost about a quarter of a step.
+// Steps of a warp: 48 or no limit 29.6 us for 16,384 tokens of 20 heads of 128, 24 31.0; for 28,350 of 36 heads 48 81 us, no
+// limit 82.9.
+static int qk_blocks(QkNormArgs& a, bool wide, bool backward) {
+    const int in_hand = 32 / (a.d / (wide ? 16 : 8)), n[2] = {a.q_heads, a.heads - a.q_heads};
+    int steps[2] = {qk_steps(n[0], in_hand), qk_steps(n[1], in_hand)};
+    a.q_slots = n[0] > 0 ? in_hand : 0;
+    a.q_own = steps[0];
+    a.k_own = steps[1];
+    if (n[0] == 0) {
+        steps[0] = steps[1];
+        steps[1] = 0;
+    } else if (n[1] > 0) {
+        int both = steps[0] + steps[1] + 1, slots = 0;
+        for (int q = 1; q < in_hand; ++q) {
+            const int x = qk_steps(n[0], q), y = qk_steps(n[1], in_hand - q);
+            if ((x > y ? x : y) < both) {
+                both = x > y ? x : y;
+                slots = q;
+            }
+        }
+        if (slots > 0) {
+            a.q_slots = slots;
+            a.q_own = qk_steps(n[0], slots);
+            a.k_own = qk_steps(n[1], in_hand - slots);
+            steps[0] = both;
+            steps[1] = 0;
+        }
+    }
+    a.steps = steps[0];
+    a.k_steps = steps[1];
     long long items[2], most[2], cost[2];
+    int blocks[2];
     for (int i = 0; i < 2; ++i) {
-        const int n = i == 0 ? a.q_heads : a.heads - a.q_heads;
-        const int shares = qk_shares(a.T, n, a.d, wide);
-        (i == 0 ? a.shares : a.k_shares) = shares;
-        const int steps = n == 0 ? 0 : (n + (in_hand << shares) - 1) / (in_hand << shares);
-        items[i] = n == 0 ? 0 : static_cast<long long>(a.T) << shares;
-        cost[i] = 1 + 4 * steps;
-        const int run = steps == 0 || steps > QKN_RUN ? 1 : QKN_RUN / steps;
+        int& shares = i == 0 ? a.shares : a.k_shares;
+        shares = 0;
+        while ((static_cast<long long>(a.T) << shares) < 8LL * 152 && 1 << shares < steps[i]) ++shares;
+        items[i] = steps[i] == 0 ? 0 : static_cast<long long>(a.T) << shares;
+        const int each = (steps[i] + (1 << shares) - 1) >> shares;  // steps of an item
+        cost[i] = 1 + 4 * each;
+        const int run = each == 0 || each > QKN_RUN ? 1 : QKN_RUN / each;
         most[i] = (items[i] + QKN_WARPS - 1) / QKN_WARPS;
         blocks[i] = static_cast<int>(backward ? most[i] : (items[i] + run * QKN_WARPS - 1) / (run * QKN_WARPS));
-        if (!backward && blocks[i] < QKN_PER_SM * 152) blocks[i] = static_cast<int>(most[i] < QKN_PER_SM * 152 ? most[i] : QKN_PER_SM * 152);
+        if (!backward && blocks[i] < QKN_FULL) blocks[i] = static_cast<int>(most[i] < QKN_FULL ? most[i] : QKN_FULL);
+    }
+    const int all = blocks[0] + blocks[1];
+    if (!backward && all > QKN_FULL && blocks[0] < most[0]) {
+        // Whole rounds of the chip, where warps walk several items (683 blocks, where 608 fit, took 28.9 us for what 608 do in
+        // 22.6; with an item a warp 5.2 us for 700 tokens, as they come 4.3).
+        const double by = static_cast<double>((all + QKN_FULL / 2) / QKN_FULL) * QKN_FULL / all;
+        for (int i = 0; i < 2; ++i) {
+            const long long b = static_cast<long long>(blocks[i] * by + 0.5);
+            if (blocks[i] > 0) blocks[i] = static_cast<int>(b < 1 ? 1 : b < most[i] ? b : most[i]);
+        }
     }
     if (backward && most[0] + most[1] > QKN_BWD_BLOCKS) {
-        if (items[0] == 0 || items[1] == 0) {
-            blocks[items[0] == 0] = QKN_BWD_BLOCKS;
+        if (items[1] == 0) {
+            // no more than what gives every warp as many items
+            const long long rounds = (most[0] + QKN_BWD_BLOCKS - 1) / QKN_BWD_BLOCKS;
+            blocks[0] = static_cast<int>((most[0] + rounds - 1) / rounds);
         } else {
             auto rounds = [&](int i, int b) { return (items[i] + b * QKN_WARPS - 1) / (b * QKN_WARPS) * cost[i]; };
             const double share = static_cast<double>(items[0] * cost[0]) / (items[0] * cost[0] + items[1] * cost[1]);
@@ -477,6 +524,7 @@ static void qk_blocks(QkNormArgs& a, bool wide, bool backward, int* blocks) {
         }
     }
     a.q_blocks = blocks[0];
+    return blocks[0] + blocks[1];
 }
 
 template <int VEC, bool INTER, int SUM, bool BACKWARD>
@@ -561,16 +609,15 @@ extern "C" mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16
     a.ldx = ldx;
     a.ldy = ldy;
     const bool wide = qk_wide(d, pairs);
-    int blocks[2];
-    qk_blocks(a, wide, false, blocks);
-    const cudaError_t e = qk_dispatch<false>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks[0] + blocks[1],
+    const int blocks = qk_blocks(a, wide, false);
+    const cudaError_t e = qk_dispatch<false>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks,
                                              static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
 
 extern "C" size_t mp_qk_norm_rope_bwd_workspace_bytes(int T, int heads, int d) {
     if (T <= 0 || heads <= 0 || d <= 0 || d % 8 != 0 || d > 2 * ROPE_MAX_PAIRS) return 0;
-    return static_cast<size_t>(QKN_BWD_BLOCKS) * d * sizeof(float);
+    return static_cast<size_t>(QKN_BWD_BLOCKS) * 2 * d * sizeof(float);
 }
 
 extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp_bf16* dx, const mp_bf16* wq,
@@ -599,7 +646,7 @@ extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp
     st = check_device(&sms);
     if (st != MP_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int blocks[2] = {0, 0};
+    int blocks = 0, q_rows = 0, k_row = 0;
     if (T > 0) {
         RopeTable tab{};
         rope_fill(tab, axes, sections, pairs, base, flags);
@@ -615,13 +662,14 @@ extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp
         a.lddy = lddy;
         a.ldy = lddx;
         const bool wide = qk_wide(d, pairs);
-        qk_blocks(a, wide, true, blocks);
-        const cudaError_t e =
-            qk_dispatch<true>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks[0] + blocks[1], s);
+        blocks = qk_blocks(a, wide, true);
+        q_rows = a.q_slots > 0 ? a.q_blocks : 0;
+        k_row = a.k_steps > 0 ? a.q_blocks : 0;
+        const cudaError_t e = qk_dispatch<true>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks, s);
         if (e != cudaSuccess) return MP_ERR_CUDA;
     }
     // T = 0: no rows, the sums are zero.
     const cudaError_t e = launch_pdl(qk_norm_dw_kernel, dim3(static_cast<unsigned>(2 * ((d + 31) / 32))), dim3(1024), 0, s,
-                                     static_cast<const float*>(workspace), dwq, dwk, blocks[0], blocks[0] + blocks[1], d);
+                                     static_cast<const float*>(workspace), dwq, dwk, q_rows, k_row, blocks, d);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }

@@ -98,6 +98,22 @@ def test_norm_and_gradients_match_oracle(T, heads, nq, d, sections, top, interle
     _check(_run(inp, nq, **kw), inp, nq, **kw)
 
 
+@pytest.mark.parametrize("T,heads,nq,d", [
+    (9, 8, 4, 64),        # both kinds in a warp, lanes halved
+    (9, 9, 7, 64),        # the last query lane has one head less
+    (2600, 10, 5, 96),    # five lanes for five and five heads: apart, a step each
+    (1300, 5, 4, 96),     # one step of both
+    (70, 7, 1, 128),      # one query head, six key heads
+    (1250, 40, 32, 128),  # apart, more blocks than the chip holds
+    (2500, 4, 2, 256),    # two lanes' width
+    (11, 3, 2, 176),      # two heads at once, eleven lanes each
+])
+def test_query_and_key_heads_dealt_to_warps(T, heads, nq, d):
+    inp = _inputs(T, heads, d, 2, 5000, 21700 + T + d)
+    kw = dict(sections=(d // 4, d // 4), base=10000.0, interleaved=T % 2 == 0, per_axis=False)
+    _check(_run(inp, nq, **kw), inp, nq, **kw)
+
+
 def test_strided_rows_and_in_place():
     inp = _inputs(77, 6, 64, 3, 1000, 21500)
     sec = (8, 12, 12)
