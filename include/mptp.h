@@ -521,8 +521,8 @@ MP_API mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp_bf1
  *   outside [0, T], pass max_n or reach behind its max_pages * page positions is left out and sets MP_DEV_SEQ_RANGE; where
  *   offsets that descend make others overlap, rows of theirs may be left out too. A page outside the pool is left out and sets
  *   MP_DEV_PAGE_RANGE. Rows, slots and pages of no sequence stay as they were. max_n == 0: nothing to do.
- *   Size rules: d % 16 == 0, d <= 256; max_n <= T; ldk, ldv at least a row and multiples of 8; ld_kc, ld_vc at least
- *   kv_heads * page * d, multiples of 16 and below 2^36; ld_ks, ld_vs >= kv_heads and below 2^32; pages, max_pages >= 1;
+ *   Size rules: d % 16 == 0, d <= 256; max_n <= T; ldk, ldv at least a row, multiples of 8 and below 2^28; ld_kc, ld_vc at
+ *   least kv_heads * page * d, multiples of 16 and below 2^36; ld_ks, ld_vs >= kv_heads and below 2^32; pages, max_pages >= 1;
  *   max_pages * page <= 2^31 - 256.
  */
 MP_API mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V,

@@ -10,7 +10,9 @@
 //
 // Both are bound by memory: 2 bytes in and 1 out for each element, or 1 in and 2 out. A group of threads takes a unit, the rows
 // of one page, head and kind (keys or values), all of them in registers at once, so that the amax and the codes come from one
-// read. A block finds its page once and walks a share of its units.
+// read. A block finds its page once and walks a share of its units; a write's come through shared memory two units ahead,
+// each thread's own places, at offsets that are the same in every unit (15.5 k tokens of 8 heads of 96 18.6 us, with the next unit in
+// registers and its addresses anew 19.5; 156 k 122 and 139).
 #include <type_traits>
 
 #include "mptp_kv_cache.cuh"
@@ -21,6 +23,7 @@ namespace mptp {
 // Threads of a block, and blocks that a launch is split into where it has so many units.
 constexpr int KV_WRITE_THREADS = 128;  // or twice as many, where a unit's vectors fill them
 constexpr int KV_WRITE_BLOCKS = 152 * 3;
+constexpr int KV_WRITE_STAGES = 3;  // a block's units in flight, and the one in hand (two: 18.4 and 121 us; 29 k tokens 32.4, three 30.2)
 constexpr int KV_READ_THREADS = 256;
 constexpr int KV_READ_BLOCKS = 152 * 24;
 
@@ -28,12 +31,14 @@ struct KvRows {
     const __nv_bfloat16* in[2];  // write: new keys and values
     __nv_bfloat16* out[2];       // read
     long long ld[2];
+    uint32_t ld16[2];  // the same in 16-byte pieces
     const int32_t* cu;     // [nseq + 1]
     const int32_t* start;  // [nseq] or null: zeros
     int nseq, T, max_n;
     int per_seq;  // pages a sequence may touch: page `item` is that of sequence item / per_seq. 0: found by a search
     int group_shift;     // log2 of the threads of a unit: 32 to a block's
     int splits;          // blocks that share a page's units
+    int held;            // write: vectors of a thread
     uint32_t per_row;    // ceil(2^32 / (d / 8)): v * per_row >> 32 is the row of vector v (exact for v < 2^16, d <= 256)
     uint32_t* status;
 };
@@ -133,10 +138,13 @@ __device__ __forceinline__ __nv_bfloat162 kv_amax2(uint32_t w, __nv_bfloat162 m)
     return __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
 }
 
-// Two values as codes. e4m3 has no infinity: one (INF: there are some) becomes NaN, so that whoever reads it sees it.
+// Two values as codes; inv: the scale's inverse twice. Their product is exact in bf16 but for magnitudes below 2^-126, whose code
+// is zero in any case. e4m3 has no infinity: one (INF: there are some) becomes NaN, so that whoever reads it sees it.
 template <bool INF>
-__device__ __forceinline__ uint32_t kv_quant2(uint32_t w, float inv) {
-    float a = kv_lo(w) * inv, b = kv_hi(w) * inv;
+__device__ __forceinline__ uint32_t kv_quant2(uint32_t w, __nv_bfloat162 inv) {
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), inv);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&x);
+    float a = kv_lo(u), b = kv_hi(u);
     if constexpr (INF) {
         if (isinf(a)) a = __int_as_float(0x7fffffff);
         if (isinf(b)) b = __int_as_float(0x7fffffff);
@@ -144,7 +152,7 @@ __device__ __forceinline__ uint32_t kv_quant2(uint32_t w, float inv) {
     return float2_to_e4m3x2(a, b);
 }
 template <bool INF>
-__device__ __forceinline__ uint2 kv_quant8(const uint4& x, float inv) {
+__device__ __forceinline__ uint2 kv_quant8(const uint4& x, __nv_bfloat162 inv) {
     return make_uint2(kv_quant2<INF>(x.x, inv) | kv_quant2<INF>(x.y, inv) << 16,
                       kv_quant2<INF>(x.z, inv) | kv_quant2<INF>(x.w, inv) << 16);
 }
@@ -155,9 +163,25 @@ __device__ __forceinline__ uint32_t kv_requant4(uint32_t c, float ratio) {
     return float2_to_e4m3x2(a.x * ratio, a.y * ratio) | float2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
 }
 
-// NV: vectors of eight elements that a thread holds.
+// 16 or 4 bytes of a thread into its own place in shared memory; zeros where they are not taken.
+__device__ __forceinline__ void kv_copy16(uint32_t dst, const void* src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void kv_copy4(uint32_t dst, const void* src, bool take) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
+}
+
+// NV: vectors of eight elements that a thread holds at most.
+template <int NV, int THREADS>
+struct KvStage {
+    static constexpr int VECTORS = NV * THREADS * 16;
+    static constexpr int BYTES = VECTORS + THREADS * 4;  // then the page's scale so far
+    static constexpr int SMEM = KV_WRITE_STAGES * BYTES;
+};
 template <int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) kv_write_kernel(const KvRows r, const KvPool p) {
+    using S = KvStage<NV, THREADS>;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[THREADS / 32];
     const int group = 1 << r.group_shift, per_cta = THREADS >> r.group_shift;
     const int item = blockIdx.x / r.splits, split = blockIdx.x % r.splits;
@@ -180,68 +204,86 @@ __global__ void __launch_bounds__(THREADS) kv_write_kernel(const KvRows r, const
         }
         return m;
     };
-    struct Unit {
-        bool live;
-        uint8_t* page;
-        float* scale;
-        float before;
-        uint4 x[NV];
-    };
-    auto load = [&](int unit0) {
-        Unit u;
-        const int unit = unit0 + (threadIdx.x >> r.group_shift);
-        u.live = unit < 2 * p.kv_heads;
-        const int kind = u.live && unit >= p.kv_heads ? 1 : 0;
-        const int head = u.live ? unit - kind * p.kv_heads : 0;
-        const long long ld = kind ? r.ld[1] : r.ld[0];
-        const __nv_bfloat16* src = (kind ? r.in[1] : r.in[0]) + at.row * ld + head * p.d;
-        u.page = p.head_codes(kind, at.id, head);
-        u.scale = p.head_scale(kind, at.id, head);
-        u.before = at.a > 0 && u.live ? *u.scale : 0.0f;
+    const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;
+    // The thread's vectors within a unit, the same in every one.
+    uint32_t rows[NV], cols[NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int v = tid + (k << r.group_shift);
-            u.x[k] = make_uint4(0, 0, 0, 0);
-            if (u.live && v < count) {
-                const int row = __umulhi(v, r.per_row);
-                u.x[k] = *reinterpret_cast<const uint4*>(src + row * ld + (v - row * wide) * 8);
+    for (int k = 0; k < NV; ++k) {
+        const int v = tid + (k << r.group_shift);
+        rows[k] = __umulhi(v, r.per_row);
+        cols[k] = v - rows[k] * wide;
+    }
+    auto ask = [&](int unit0, int stage) {
+        if (unit0 < 2 * p.kv_heads) {
+            const int unit = unit0 + (threadIdx.x >> r.group_shift);
+            const bool live = unit < 2 * p.kv_heads;
+            const int kind = live && unit >= p.kv_heads ? 1 : 0, head = live ? unit - kind * p.kv_heads : 0;
+            const uint32_t ld16 = kind ? r.ld16[1] : r.ld16[0];
+            const uint4* src = reinterpret_cast<const uint4*>(kind ? r.in[1] : r.in[0]) + (at.row * static_cast<long long>(ld16) + head * wide);
+            const uint32_t to = ring + stage * S::BYTES;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (k >= r.held) break;
+                const bool take = live && tid + (k << r.group_shift) < count;
+                kv_copy16(to + k * (THREADS * 16), src + (take ? rows[k] * ld16 + cols[k] : 0u), take);
             }
+            if (at.a > 0) kv_copy4(to + S::VECTORS - threadIdx.x * 12, p.head_scale(kind, at.id, head), live);
         }
-        return u;
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const int step = r.splits * per_cta;
-    Unit next = load(split * per_cta);
+    int stage = 0;
+#pragma unroll
+    for (int k = 0; k < KV_WRITE_STAGES - 1; ++k) ask(split * per_cta + k * step, k);
     for (int unit0 = split * per_cta; unit0 < 2 * p.kv_heads; unit0 += step) {
-        const Unit u = next;
-        const uint4(&x)[NV] = u.x;
+        const int unit = unit0 + (threadIdx.x >> r.group_shift);
+        const bool live = unit < 2 * p.kv_heads;
+        const int kind = live && unit >= p.kv_heads ? 1 : 0, head = live ? unit - kind * p.kv_heads : 0;
+        uint8_t* page = p.head_codes(kind, at.id, head);
+        float* scale = p.head_scale(kind, at.id, head);
+        asm volatile("cp.async.wait_group %0;" ::"n"(KV_WRITE_STAGES - 2) : "memory");
+        const uint8_t* from = smem + stage * S::BYTES + threadIdx.x * 16;
+        uint4 x[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k >= r.held) break;
+            x[k] = *reinterpret_cast<const uint4*>(from + k * (THREADS * 16));
+        }
+        const float before = at.a > 0 ? *reinterpret_cast<const float*>(from + S::VECTORS - threadIdx.x * 12) : 0.0f;
+        ask(unit0 + (KV_WRITE_STAGES - 1) * step, stage == 0 ? KV_WRITE_STAGES - 1 : stage - 1);
+        stage = stage == KV_WRITE_STAGES - 1 ? 0 : stage + 1;
         __nv_bfloat162 m2 = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) m2 = kv_amax2(x[k].x, kv_amax2(x[k].y, kv_amax2(x[k].z, kv_amax2(x[k].w, m2))));
+        for (int k = 0; k < NV; ++k) {
+            if (k >= r.held) break;
+            m2 = kv_amax2(x[k].x, kv_amax2(x[k].y, kv_amax2(x[k].z, kv_amax2(x[k].w, m2))));
+        }
         float m = largest(fmaxf(__low2float(m2), __high2float(m2)));
         const bool inf = m == __int_as_float(0x7f800000);
         if (__syncthreads_or(inf)) {  // seldom: the scale goes by the finite values
             float f = 0.0f;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+            for (int k = 0; k < NV; ++k) {
+                if (k >= r.held) break;
                 f = kv_amax_finite(x[k].x, kv_amax_finite(x[k].y, kv_amax_finite(x[k].z, kv_amax_finite(x[k].w, f))));
+            }
             m = largest(f);
         }
-        if (unit0 + step < 2 * p.kv_heads) next = load(unit0 + step);
         int e = kv_exponent(m);
         float ratio = 1.0f;  // old codes' factor
         if (at.a > 0) {
             // The page's scale so far; one that no write can have left (not in (0, 2^120]) makes its old codes NaN.
-            if (u.before > 0.0f && u.before <= kv_pow2(120)) {
-                const uint32_t bits = __float_as_uint(u.before);
+            if (before > 0.0f && before <= kv_pow2(120)) {
+                const uint32_t bits = __float_as_uint(before);
                 e = max(e, static_cast<int>(bits >> 23) - 127 + ((bits & 0x7fffffu) != 0 ? 1 : 0));
-                ratio = u.before * kv_pow2(-e);
+                ratio = before * kv_pow2(-e);
             } else {
                 ratio = __int_as_float(0x7fffffff);
             }
         }
-        if (!u.live) continue;
-        const float inv = kv_pow2(-e);
-        uint8_t* to = u.page + at.a * p.d + tid * 8;
+        if (!live) continue;
+        const __nv_bfloat162 inv = __float2bfloat162_rn(kv_pow2(-e));
+        uint8_t* to = page + at.a * p.d + tid * 8;
         auto put = [&](auto with_inf) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
@@ -253,7 +295,7 @@ __global__ void __launch_bounds__(THREADS) kv_write_kernel(const KvRows r, const
         else
             put(std::false_type{});
         if (at.a > 0 && ratio != 1.0f) {
-            uint2* old = reinterpret_cast<uint2*>(u.page);
+            uint2* old = reinterpret_cast<uint2*>(page);
             for (int v = tid; v < at.a * wide; v += group) {
                 uint2 c = old[v];
                 c.x = kv_requant4(c.x, ratio);
@@ -261,7 +303,7 @@ __global__ void __launch_bounds__(THREADS) kv_write_kernel(const KvRows r, const
                 old[v] = c;
             }
         }
-        if (tid == 0) *u.scale = kv_pow2(e);
+        if (tid == 0) *scale = kv_pow2(e);
     }
 }
 
@@ -317,7 +359,7 @@ static mp_status kv_rows_check(const void* K, const void* V, const void* kc, con
     if (nseq < 0 || T < 0 || max_n < 0 || kv_heads <= 0 || d <= 0 || pages < 0 || max_pages < 0)
         return MP_ERR_INVALID_ARG;
     if (d % 16 != 0 || d > 256 || max_n > T || ldk < static_cast<long long>(kv_heads) * d ||
-        ldv < static_cast<long long>(kv_heads) * d || ldk % 8 != 0 || ldv % 8 != 0 ||
+        ldv < static_cast<long long>(kv_heads) * d || ldk % 8 != 0 || ldv % 8 != 0 || (ldk | ldv) >> 28 != 0 ||
         !kv_pool_sizes(pages, max_pages, page, kv_heads, d, ld_kc, ld_vc, ld_ks, ld_vs))
         return MP_ERR_UNSUPPORTED_SHAPE;
     *nothing = nseq == 0 || max_n == 0;
@@ -401,13 +443,21 @@ extern "C" mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V, uint8
     int sms = 0;
     st = check_device(&sms);
     if (st != MP_OK) return st;
-    const int held = ceil_div(vectors, 1 << r.group_shift);
-    auto kernel = held > 8                       ? kv_write_kernel<16, 2 * KV_WRITE_THREADS>
-                  : threads > KV_WRITE_THREADS ? kv_write_kernel<8, 2 * KV_WRITE_THREADS>
-                  : held > 1                   ? kv_write_kernel<8, KV_WRITE_THREADS>
-                                               : kv_write_kernel<1, KV_WRITE_THREADS>;
-    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), 0,
-                                     static_cast<cudaStream_t>(stream), r, p);
+    r.held = ceil_div(vectors, 1 << r.group_shift);
+    r.ld16[0] = static_cast<uint32_t>(ldk >> 3);
+    r.ld16[1] = static_cast<uint32_t>(ldv >> 3);
+    auto launch = [&](auto kernel, int smem) {
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, static_cast<cudaStream_t>(stream), r, p);
+    };
+    constexpr int N = KV_WRITE_THREADS;
+    const cudaError_t e = r.held > 8      ? launch(kv_write_kernel<16, 2 * N>, KvStage<16, 2 * N>::SMEM)
+                          : threads > N ? launch(kv_write_kernel<8, 2 * N>, KvStage<8, 2 * N>::SMEM)
+                          : r.held > 1    ? launch(kv_write_kernel<8, N>, KvStage<8, N>::SMEM)
+                                        : launch(kv_write_kernel<1, N>, KvStage<1, N>::SMEM);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }
 

@@ -91,7 +91,7 @@ POOL_REFUSALS = [
 
 @pytest.mark.parametrize("kw,code", POOL_REFUSALS + [
     (dict(T=-1), 1), (dict(max_n=-1), 1), (dict(max_n=101), 2), (dict(d=72), 2), (dict(d=272), 2), (dict(ldk=120), 2),
-    (dict(ldv=132), 2), (dict(K=None), 1), (dict(V=None), 1), (dict(start=None), 1), (dict(K=BAD), 3), (dict(V=BAD), 3),
+    (dict(ldk=1 << 28), 2), (dict(ldv=1 << 28), 2), (dict(ldv=132), 2), (dict(K=None), 1), (dict(V=None), 1), (dict(start=None), 1), (dict(K=BAD), 3), (dict(V=BAD), 3),
     (dict(start=BAD), 3),
     (dict(nseq=0x7fffffff, T=0x7fffffff, max_n=33), 2),   # more pages than a grid has CTAs
 ])
