@@ -13,6 +13,8 @@
 // read. A block finds its page once and walks a share of its units; a write's come through shared memory two units ahead,
 // each thread's own places, at offsets that are the same in every unit (15.5 k tokens of 8 heads of 96 18.6 us, with the next unit in
 // registers and its addresses anew 19.5; 156 k 122 and 139).
+// Measured: a write of 156 k tokens 5.9 TB/s, of 15.5 k 3.8 (three reads in a row before the first code, then eight steps in blocks
+// that are all there at once); a read of 102 k tokens of 8 heads of 128 97 us, 6.5 TB/s, 96 % of a copy's rate.
 #include <type_traits>
 
 #include "mptp_kv_cache.cuh"
