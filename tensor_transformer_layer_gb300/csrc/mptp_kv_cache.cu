@@ -25,7 +25,8 @@ namespace mptp {
 // Threads of a block, and blocks that a launch is split into where it has so many units.
 constexpr int KV_WRITE_THREADS = 128;  // or twice as many, where a unit's vectors fill them
 constexpr int KV_WRITE_BLOCKS = 152 * 3;
-constexpr int KV_WRITE_STAGES = 3;  // a block's units in flight, and the one in hand (two: 18.4 and 121 us; 29 k tokens 32.4, three 30.2)
+// A block's units in flight, and the one in hand (two: 18.4 and 121 us for the sizes above; 29 k tokens 32.4, three 30.2).
+constexpr int KV_WRITE_STAGES = 3;
 constexpr int KV_READ_THREADS = 256;
 constexpr int KV_READ_BLOCKS = 152 * 24;
 
@@ -221,7 +222,8 @@ __global__ void __launch_bounds__(THREADS) kv_write_kernel(const KvRows r, const
             const bool live = unit < 2 * p.kv_heads;
             const int kind = live && unit >= p.kv_heads ? 1 : 0, head = live ? unit - kind * p.kv_heads : 0;
             const uint32_t ld16 = kind ? r.ld16[1] : r.ld16[0];
-            const uint4* src = reinterpret_cast<const uint4*>(kind ? r.in[1] : r.in[0]) + (at.row * static_cast<long long>(ld16) + head * wide);
+            const uint4* src = reinterpret_cast<const uint4*>(kind ? r.in[1] : r.in[0]) +
+                               (at.row * static_cast<long long>(ld16) + head * wide);
             const uint32_t to = ring + stage * S::BYTES;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -456,9 +458,9 @@ extern "C" mp_status mp_kv_cache_write(const mp_bf16* K, const mp_bf16* V, uint8
         return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, static_cast<cudaStream_t>(stream), r, p);
     };
     constexpr int N = KV_WRITE_THREADS;
-    const cudaError_t e = r.held > 8      ? launch(kv_write_kernel<16, 2 * N>, KvStage<16, 2 * N>::SMEM)
+    const cudaError_t e = r.held > 8    ? launch(kv_write_kernel<16, 2 * N>, KvStage<16, 2 * N>::SMEM)
                           : threads > N ? launch(kv_write_kernel<8, 2 * N>, KvStage<8, 2 * N>::SMEM)
-                          : r.held > 1    ? launch(kv_write_kernel<8, N>, KvStage<8, N>::SMEM)
+                          : r.held > 1  ? launch(kv_write_kernel<8, N>, KvStage<8, N>::SMEM)
                                         : launch(kv_write_kernel<1, N>, KvStage<1, N>::SMEM);
     return e == cudaSuccess ? MP_OK : MP_ERR_CUDA;
 }

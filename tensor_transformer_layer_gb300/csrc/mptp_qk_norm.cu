@@ -27,11 +27,11 @@ namespace mptp {
 
 constexpr int QKN_WARPS = 4;         // warps of a block
 constexpr int QKN_STAGES = 4;        // steps in flight, and the one in hand
-constexpr int QKN_PER_SM = 4;        // blocks on an SM
-constexpr int QKN_FULL = QKN_PER_SM * 152;
 constexpr int QKN_RUN = 48;          // steps of a warp of the forward pass
-constexpr int QKN_BWD_PER_SM = 3;
-constexpr int QKN_BWD_BLOCKS = QKN_BWD_PER_SM * 152;  // pairs of rows of the workspace at most
+// Blocks on an SM, as many as registers allow without spills: narrow lanes (VEC 4) one more (8192 tokens of 20 heads of 72 16.5 us
+// forward with five, 19.6 with four, 18.3 with six; backward 24.4 with four, 25.5 with three, 26.7 with five).
+constexpr int qkn_per_sm(bool wide, bool backward) { return wide ? (backward ? 3 : 4) : backward ? 4 : 5; }
+constexpr int QKN_BWD_ROWS = 4 * 152;  // pairs of rows of the workspace at most: blocks of the backward pass
 
 struct QkNormArgs {
     const __nv_bfloat16* x;
@@ -267,7 +267,7 @@ __device__ __forceinline__ void qk_take(const uint8_t* at, float2 (&f)[VEC]) {
 }
 
 template <int VEC, bool INTER, int SUM, bool BACKWARD>
-__global__ void __launch_bounds__(QKN_WARPS * 32, BACKWARD ? QKN_BWD_PER_SM : QKN_PER_SM) qk_norm_kernel(
+__global__ void __launch_bounds__(QKN_WARPS * 32, qkn_per_sm(VEC == 8, BACKWARD)) qk_norm_kernel(
     const __grid_constant__ RopeTable tab, const QkNormArgs a) {
     using Walk = QkWalk<VEC, BACKWARD ? 2 : 1>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -444,13 +444,15 @@ static bool qk_wide(int d, long long pairs) { return d % 16 == 0 && pairs % 8 ==
 static int qk_steps(int heads, int slots) { return (heads + slots - 1) / slots; }
 
 // How heads are dealt to lanes, warps and blocks. A warp has both kinds of heads where that takes no more steps than warps for
-// either. A token's steps are shared while there would be fewer than eight warps on each of 152 SMs. Forward: a warp walks about
-// QKN_RUN steps, so that the blocks that end late are small. Backward: as many blocks as the chip holds at most (each leaves
-// a row of sums of either kind), divided so that neither kind's last warp ends much later than the other's; a token's angles
-// cost about a quarter of a step.
+// either. A token's steps are shared while there would be fewer than four warps on each of 152 SMs (eight: backward of 1111
+// tokens of 32 heads of 72 8.3 us instead of 7.8, forward of 300 of 40 of 128 3.9 instead of 2.8, but of 700 4.2 instead of 5.0).
+// Forward: a warp walks about QKN_RUN steps, so that the blocks that end late are small. Backward: as many blocks as the chip
+// holds at most (each leaves a row of sums of either kind), divided so that neither kind's last warp ends much later than the
+// other's; a token's angles cost about a quarter of a step.
 // Steps of a warp: 48 or no limit 29.6 us for 16,384 tokens of 20 heads of 128, 24 31.0; for 28,350 of 36 heads 48 81 us, no
 // limit 82.9.
 static int qk_blocks(QkNormArgs& a, bool wide, bool backward) {
+    const int full = qkn_per_sm(wide, backward) * 152;  // blocks that the chip holds
     const int in_hand = 32 / (a.d / (wide ? 16 : 8)), n[2] = {a.q_heads, a.heads - a.q_heads};
     int steps[2] = {qk_steps(n[0], in_hand), qk_steps(n[1], in_hand)};
     a.q_slots = n[0] > 0 ? in_hand : 0;
@@ -483,45 +485,45 @@ static int qk_blocks(QkNormArgs& a, bool wide, bool backward) {
     for (int i = 0; i < 2; ++i) {
         int& shares = i == 0 ? a.shares : a.k_shares;
         shares = 0;
-        while ((static_cast<long long>(a.T) << shares) < 8LL * 152 && 1 << shares < steps[i]) ++shares;
+        while ((static_cast<long long>(a.T) << shares) < 4LL * 152 && 1 << shares < steps[i]) ++shares;
         items[i] = steps[i] == 0 ? 0 : static_cast<long long>(a.T) << shares;
         const int each = (steps[i] + (1 << shares) - 1) >> shares;  // steps of an item
         cost[i] = 1 + 4 * each;
         const int run = each == 0 || each > QKN_RUN ? 1 : QKN_RUN / each;
         most[i] = (items[i] + QKN_WARPS - 1) / QKN_WARPS;
         blocks[i] = static_cast<int>(backward ? most[i] : (items[i] + run * QKN_WARPS - 1) / (run * QKN_WARPS));
-        if (!backward && blocks[i] < QKN_FULL) blocks[i] = static_cast<int>(most[i] < QKN_FULL ? most[i] : QKN_FULL);
+        if (!backward && blocks[i] < full) blocks[i] = static_cast<int>(most[i] < full ? most[i] : full);
     }
     const int all = blocks[0] + blocks[1];
-    if (!backward && all > QKN_FULL && blocks[0] < most[0]) {
+    if (!backward && all > full && blocks[0] < most[0]) {
         // Whole rounds of the chip, where warps walk several items (683 blocks, where 608 fit, took 28.9 us for what 608 do in
         // 22.6; with an item a warp 5.2 us for 700 tokens, as they come 4.3).
-        const double by = static_cast<double>((all + QKN_FULL / 2) / QKN_FULL) * QKN_FULL / all;
+        const double by = static_cast<double>((all + full / 2) / full) * full / all;
         for (int i = 0; i < 2; ++i) {
             const long long b = static_cast<long long>(blocks[i] * by + 0.5);
             if (blocks[i] > 0) blocks[i] = static_cast<int>(b < 1 ? 1 : b < most[i] ? b : most[i]);
         }
     }
-    if (backward && most[0] + most[1] > QKN_BWD_BLOCKS) {
+    if (backward && most[0] + most[1] > full) {
         if (items[1] == 0) {
             // no more than what gives every warp as many items
-            const long long rounds = (most[0] + QKN_BWD_BLOCKS - 1) / QKN_BWD_BLOCKS;
+            const long long rounds = (most[0] + full - 1) / full;
             blocks[0] = static_cast<int>((most[0] + rounds - 1) / rounds);
         } else {
             auto rounds = [&](int i, int b) { return (items[i] + b * QKN_WARPS - 1) / (b * QKN_WARPS) * cost[i]; };
             const double share = static_cast<double>(items[0] * cost[0]) / (items[0] * cost[0] + items[1] * cost[1]);
-            const int guess = static_cast<int>(QKN_BWD_BLOCKS * share);
-            int best = guess < 1 ? 1 : guess > QKN_BWD_BLOCKS - 1 ? QKN_BWD_BLOCKS - 1 : guess;
+            const int guess = static_cast<int>(full * share);
+            int best = guess < 1 ? 1 : guess > full - 1 ? full - 1 : guess;
             long long span = -1;
-            for (int b = guess - 8 > 1 ? guess - 8 : 1; b <= guess + 8 && b < QKN_BWD_BLOCKS; ++b) {
-                const long long q = rounds(0, b), k = rounds(1, QKN_BWD_BLOCKS - b), t = q > k ? q : k;
+            for (int b = guess - 8 > 1 ? guess - 8 : 1; b <= guess + 8 && b < full; ++b) {
+                const long long q = rounds(0, b), k = rounds(1, full - b), t = q > k ? q : k;
                 if (span < 0 || t < span) {
                     span = t;
                     best = b;
                 }
             }
             blocks[0] = best;
-            blocks[1] = QKN_BWD_BLOCKS - best;
+            blocks[1] = full - best;
         }
     }
     a.q_blocks = blocks[0];
@@ -618,7 +620,7 @@ extern "C" mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16
 
 extern "C" size_t mp_qk_norm_rope_bwd_workspace_bytes(int T, int heads, int d) {
     if (T <= 0 || heads <= 0 || d <= 0 || d % 8 != 0 || d > 2 * ROPE_MAX_PAIRS) return 0;
-    return static_cast<size_t>(QKN_BWD_BLOCKS) * 2 * d * sizeof(float);
+    return static_cast<size_t>(QKN_BWD_ROWS) * 2 * d * sizeof(float);
 }
 
 extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp_bf16* dx, const mp_bf16* wq,
