@@ -488,9 +488,9 @@ MP_API mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16* wq
 /*
  * Its backward, from x and dy (the gradient of y); the norms are computed again:
  *   g = R^-1 dy,  dw = sum over tokens and heads of g * n,  dx = (w * g - n mean(w * g * n)) / sqrt(mean(x^2) + eps)
- *   dwq, dwk [d] fp32 (the one that no head takes may be NULL), dx [T, heads, d] with pitch lddx; dx may be dy or x
- *   itself (then their pitches are equal). workspace: mp_qk_norm_rope_bwd_workspace_bytes(T, heads, d) bytes (0 for
- *   sizes outside the rules), whatever they hold. T = 0 zeroes dwq and dwk. Everything else as mp_qk_norm_rope.
+ *   dwq, dwk [d] fp32 (the one that no head takes may be NULL; given, it becomes zeros), dx [T, heads, d] with pitch lddx;
+ *   dx may be dy or x itself (then their pitches are equal). workspace: mp_qk_norm_rope_bwd_workspace_bytes(T, heads, d) bytes
+ *   (0 for sizes outside the rules), whatever they hold. T = 0 zeroes dwq and dwk. Everything else as mp_qk_norm_rope.
  */
 MP_API size_t mp_qk_norm_rope_bwd_workspace_bytes(int T, int heads, int d);
 MP_API mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp_bf16* dx, const mp_bf16* wq,

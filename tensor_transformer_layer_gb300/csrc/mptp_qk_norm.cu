@@ -667,7 +667,8 @@ extern "C" mp_status mp_qk_norm_rope_bwd(const mp_bf16* x, const mp_bf16* dy, mp
         const bool wide = qk_wide(d, pairs);
         blocks = qk_blocks(a, wide, true);
         q_rows = a.q_slots > 0 ? a.q_blocks : 0;
-        k_row = a.k_steps > 0 ? a.q_blocks : 0;
+        // Keys' rows: those of the blocks that have keys alone, or of all blocks, or none where there is no key head.
+        k_row = q_heads == heads || a.k_steps > 0 ? a.q_blocks : 0;
         const cudaError_t e = qk_dispatch<true>(tab, a, wide, (flags & MP_ROPE_INTERLEAVED) != 0, blocks, s);
         if (e != cudaSuccess) return MP_ERR_CUDA;
     }
