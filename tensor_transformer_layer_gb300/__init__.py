@@ -169,6 +169,10 @@ def _fast():
         lib()
         if not os.path.exists(BIND_PATH):
             raise OSError(f"_mptp_bind.so is not built ({BIND_PATH}); run `python -m tensor_transformer_layer_gb300.build`")
+        from . import build
+        if build.bind_built_for() != build.bind_for():  # it holds the layout of another torch's classes
+            raise OSError(f"_mptp_bind.so was built for {build.bind_built_for()}, installed is {build.bind_for()}; run "
+                          "`python -m tensor_transformer_layer_gb300.build`")
         spec = importlib.util.spec_from_file_location("_mptp_bind", BIND_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
