@@ -64,7 +64,7 @@ struct AcArgs {
     const int32_t* cu_q;
     const int32_t* lens;
     AcItem* items;  // [AC_CTAS]
-    float* parts;   // [2 AC_CTAS][rows][d + 2]
+    float* parts;   // [2 AC_CTAS][rows][d + 2]: what a CTA's tiles give by themselves, then (reference, sum) of each row
     long long ldq, ldo;
     int nseq, Tq, max_q, heads, group, causal;
     float inv_group, inv_kv;  // 1 / group, 1 / key heads
@@ -121,6 +121,9 @@ __device__ __forceinline__ float ac_ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// 1 / sum; 0 where nothing was summed.
+__device__ __forceinline__ float ac_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 
 template <int D, int NT>
 struct AcShape {
@@ -217,15 +220,14 @@ __device__ __forceinline__ AcRow ac_row(const AcArgs& a, int query, int member, 
     return {query + q, n - q * a.group};
 }
 
-// The output of row `row` of an item, from its sums x in units of the values and sum of probabilities: four elements at d.
+// The output x of row `row` of an item and its sum of probabilities: four elements at d.
 __device__ __forceinline__ void ac_store(const AcArgs& a, int head, const AcRow& row, int d, int D, const float4& x, float top,
                                          float sum) {
     const int hd = head * a.group + row.member;
     const long long q = row.query;
-    const float inv = 1.0f / sum;
-    uint2 out = make_uint2(0, 0);  // a row that sees no key, whatever its sums hold
+    uint2 out = make_uint2(0, 0);  // a row that sees no key, whatever x holds
     if (sum != 0.0f) {
-        const __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), b1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+        const __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x, x.y), b1 = __floats2bfloat162_rn(x.z, x.w);
         out = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
     }
     *reinterpret_cast<uint2*>(a.O + q * a.ldo + hd * D + d) = out;
@@ -697,6 +699,12 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
+        // What a row's tiles give by themselves, the sums over their probabilities' sum: as large as the values at most, where the
+        // sums in units of the values would pass fp32's range before them. Zeros where the row saw no key here.
+        auto own = [&](int i, int n, int c) {
+            const float sum = l[n][c & 1];
+            return sum == 0.0f ? 0.0f : o[i][n][c] * ac_inverse(sum) * ref;
+        };
         if (tile0 == 0 && tile1 == s.tiles) {
             // The whole item: lane (g, t) has D / 8 neighbouring elements of queries 2t and 2t + 1 of each eight.
 #pragma unroll
@@ -709,8 +717,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 #pragma unroll
                     for (int i = 0; i < KS; i += 2)
                         ac_store(a, head, at, g * (D / 8) + 2 * i, D,
-                                 make_float4(o[i][n][j] * ref, o[i][n][2 + j] * ref, o[i + 1][n][j] * ref, o[i + 1][n][2 + j] * ref),
-                                 m[n][j], l[n][j]);
+                                 make_float4(own(i, n, j), own(i, n, 2 + j), own(i + 1, n, j), own(i + 1, n, 2 + j)), m[n][j],
+                                 l[n][j]);
                 }
             continue;
         }
@@ -723,7 +731,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 const int row = n * 8 + 2 * t + j;
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
-                    to[row * (D / 2) + ac_join(g * (D / 16) + i, row)] = make_float2(o[i][n][j] * ref, o[i][n][2 + j] * ref);
+                    to[row * (D / 2) + ac_join(g * (D / 16) + i, row)] = make_float2(own(i, n, j), own(i, n, 2 + j));
                 if (g == 0)
                     *reinterpret_cast<float2*>(stats + ((warp * 2 + which) * C::ROWS + row) * 2) = make_float2(m[n][j], l[n][j]);
             }
@@ -741,10 +749,33 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     }
     __syncthreads();
 
-    // Join of the records, which stand in the line's order: those of one item follow one another.
+    // Join of the records, which stand in the line's order: those of one item follow one another. First every record's share of
+    // its item's sum, row by row, a thread each.
     constexpr int RECS = 2 * AC_WARPS;
+    __shared__ float shares[RECS][C::ROWS];
+    __shared__ float2 joined[RECS][C::ROWS];  // (reference, sum) of the item
     const long long my_u0 = rec[lane % RECS].u0;
     const unsigned mates = __match_any_sync(0xffffffffu, my_u0) & ((1u << RECS) - 1);
+    if (tid < RECS * C::ROWS) {
+        const int k = tid % RECS, row = tid / RECS;
+        float2 ml[RECS];
+        float top = AC_NONE, sum = 0.0f, mine = 0.0f;
+#pragma unroll
+        for (int j = 0; j < RECS; ++j) {
+            ml[j] = *reinterpret_cast<const float2*>(stats + (j * C::ROWS + row) * 2);
+            if (mates >> j & 1) top = fmaxf(top, ml[j].x);
+        }
+        const float from = top == AC_NONE ? 0.0f : top;
+#pragma unroll
+        for (int j = 0; j < RECS; ++j) {
+            const float f = mates >> j & 1 ? ml[j].y * ac_ex2(ml[j].x - from) : 0.0f;
+            sum += f;
+            if (j == k) mine = f;
+        }
+        shares[k][row] = mine * ac_inverse(sum);
+        joined[k][row] = make_float2(top, sum);
+    }
+    __syncthreads();
     unsigned todo = __ballot_sync(0xffffffffu, my_u0 >= 0) & ((1u << RECS) - 1);
     while (todo != 0) {
         const int r0 = __ffs(todo) - 1;
@@ -757,31 +788,24 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         float* part = a.parts + static_cast<long long>(cta * 2 + (begun ? 0 : 1)) * C::PART;
         for (int i = tid; i < r.rows * (D / 4); i += AC_THREADS) {
             const int row = i / (D / 4), c = i % (D / 4) * 2;
-            float2 ml[RECS];
-            float top = AC_NONE, sum = 0.0f;
-#pragma unroll
-            for (int k = 0; k < RECS; ++k) {
-                ml[k] = *reinterpret_cast<const float2*>(stats + (k * C::ROWS + row) * 2);
-                if (chain >> k & 1) top = fmaxf(top, ml[k].x);
-            }
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < RECS; ++k) {
                 if (!(chain >> k & 1)) continue;
-                const float f = ml[k].x == top ? 1.0f : ac_ex2(ml[k].x - top);
+                const float f = shares[k][row];
                 const float2* from = reinterpret_cast<const float2*>(smem + (k >> 1) * C::WARP + (k & 1 ? 0 : C::RING)) + row * (D / 2);
                 const float2 u = from[ac_join(c, row)], v = from[ac_join(c + 1, row)];
-                sum += ml[k].y * f;
                 x.x += u.x * f;
                 x.y += u.y * f;
                 x.z += v.x * f;
                 x.w += v.y * f;
             }
+            const float2 at = joined[r0][row];
             if (whole) {
-                ac_store(a, r.head, ac_row(a, r.query, r.member, row), c * 2, D, x, top, sum);
+                ac_store(a, r.head, ac_row(a, r.query, r.member, row), c * 2, D, x, at.x, at.y);
             } else {
                 *reinterpret_cast<float4*>(part + row * D + c * 2) = x;
-                if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = make_float2(top, sum);
+                if (c == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + row * 2) = at;
             }
         }
         if (on && tid == 0) {
@@ -833,25 +857,36 @@ __global__ void __launch_bounds__(AC_JOIN) attn_cache_join_kernel(const AcArgs a
             }
 #pragma unroll
             for (int j = 0; j < AC_BATCH; ++j) high = fmaxf(high, ml[j].x);
-            const float down = top == high ? 1.0f : ac_ex2(top - high);
+            // x is the output of the parts so far, each with its share of the sum.
+            const float before = sum * (top == high ? 1.0f : ac_ex2(top - high));
             top = high;
-            sum *= down;
-            x = make_float4(x.x * down, x.y * down, x.z * down, x.w * down);
+            sum = before;
+            float f[AC_BATCH];
 #pragma unroll
             for (int j = 0; j < AC_BATCH; ++j) {
-                const float f = ml[j].x == top ? 1.0f : ac_ex2(ml[j].x - top);
-                sum += ml[j].y * f;
-                x.x += v[j].x * f;
-                x.y += v[j].y * f;
-                x.z += v[j].z * f;
-                x.w += v[j].w * f;
+                f[j] = ml[j].y * (ml[j].x == top ? 1.0f : ac_ex2(ml[j].x - top));
+                sum += f[j];
+            }
+            const float inv = ac_inverse(sum), keep = before * inv;
+            x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+#pragma unroll
+            for (int j = 0; j < AC_BATCH; ++j) {
+                f[j] *= inv;
+                x.x += v[j].x * f[j];
+                x.y += v[j].y * f[j];
+                x.z += v[j].z * f[j];
+                x.w += v[j].w * f[j];
             }
         }
         for (int off = wide; off < 32; off <<= 1) {
             const float other = __shfl_xor_sync(0xffffffffu, top, off), high = fmaxf(top, other);
-            const float f = top == high ? 1.0f : ac_ex2(top - high), g = other == high ? 1.0f : ac_ex2(other - high);
+            float f = sum * (top == high ? 1.0f : ac_ex2(top - high));
+            float g = __shfl_xor_sync(0xffffffffu, sum, off) * (other == high ? 1.0f : ac_ex2(other - high));
             top = high;
-            sum = sum * f + __shfl_xor_sync(0xffffffffu, sum, off) * g;
+            sum = f + g;
+            const float inv = ac_inverse(sum);
+            f *= inv;
+            g *= inv;
             x.x = x.x * f + __shfl_xor_sync(0xffffffffu, x.x, off) * g;
             x.y = x.y * f + __shfl_xor_sync(0xffffffffu, x.y, off) * g;
             x.z = x.z * f + __shfl_xor_sync(0xffffffffu, x.z, off) * g;
