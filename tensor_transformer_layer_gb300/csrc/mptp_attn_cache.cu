@@ -17,9 +17,12 @@
 //
 // Numbers. Q is scaled per row by a power of two into [128, 256) at its largest and split into two e4m3 pieces, q1 + q2 / 32:
 // four of bf16's eight bits each, exact but for elements below 2^-13 of the largest, which keep 2^-22 of it. Both pieces have
-// sums of their own (fp32, as every sum and statistic here). P = 2^(s - m + 7), s within m + 8 of the reference m, is
-// rounded to halves (2^-11 of its value, at least 2^-25 absolutely, 2^-32 of a probability of m) times the value's scale over
-// the largest value scale met so far (2^-120 at least).
+// sums of their own (fp32, as every sum and statistic here). Each row has two references, which the largest so far passes by 8 at
+// most: m of its scores s, in powers of two, and m - dm of s + log2(scale_v). P = 2^(s - m + 7) goes into the row's sum, and
+// P * scale_v * 2^dm, 2^7 or more at its largest, is rounded to halves: 2^-11 of its value, at least 2^-25 absolutely, 2^-32 of
+// the largest P * scale_v among the tokens that the row sees, whatever scales other pages have. (With one reference for all
+// rows of a warp's run, the largest scale met, pages 2^21 below it lost bits and 2^32 below it everything.) Within a run P is
+// 2^80 times that, so that pages with less than 2^-126 of a row's probability count while their scales are 2^200 times others'.
 //
 // Work. The tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, AC_ITEM places for what an item
 // costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
@@ -43,12 +46,13 @@ constexpr int AC_TILE = 32;     // keys
 constexpr int AC_ITEM = 4;      // places of an item besides its tiles
 constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
 #define AC_NONE __int_as_float(0xff800000)  // -inf: no key seen
-constexpr float AC_BIAS = 7.0f;    // exponent that P carries into halves
+constexpr float AC_BIAS = 7.0f;    // exponent that P carries
 constexpr int AC_JOIN = 256;       // threads of a block of the join
 constexpr int AC_BATCH = 3;        // parts in flight in each
 constexpr int AC_SEQS = 4;         // sequences a lane looks at in one step
 constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference before sums are scaled down
-constexpr float AC_LEAST = 7.52316384526264e-37f;  // 2^-120: value scales below count against it, so that its inverse is finite
+constexpr float AC_LIFT = 80.0f, AC_UNLIFT = 8.271806125530277e-25f;  // by so much more within a run; 2^-80
+constexpr float AC_UNSEEN = 200.0f;  // dm of a row whose tokens so far have the value scale zero: below any other (2^-149)
 constexpr float AC_LOG2E = 1.4426950408889634f;
 constexpr float AC_LN2 = 0.6931471805599453f;
 
@@ -122,8 +126,16 @@ __device__ __forceinline__ float ac_ex2(float x) {
     return y;
 }
 
+// 2^((m - top) / 2), 1 where nothing was seen in either.
+__device__ __forceinline__ float ac_half(float m, float top) { return m == top ? 1.0f : ac_ex2(0.5f * (m - top)); }
 // 1 / sum; 0 where nothing was summed.
 __device__ __forceinline__ float ac_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+
+__device__ __forceinline__ float ac_lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 template <int D, int NT>
 struct AcShape {
@@ -519,15 +531,16 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const int clear = a.causal ? s.len - s.nq + ahead0 + 1 : s.len;
 
         float o[KS][NT][4];
-        float m[NT][2], l[NT][2];
+        float m[NT][2], l[NT][2];  // reference and sum of the probabilities
+        float dm[NT][2];           // the reference of o, of probabilities times the values' scales, is m - dm
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = AC_NONE;
+            dm[n][0] = dm[n][1] = AC_UNSEEN;
             l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
             for (int j = 0; j < KS; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
         }
-        float ref = AC_LEAST, inv_ref = 1.0f / AC_LEAST;  // largest value scale met
         int id[2] = {ids[C::STAGES - 1][0], ids[C::STAGES - 1][1]};
         for (int k = 0; k < tiles; ++k) {
             ac_wait<C::STAGES - 2>();
@@ -580,7 +593,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 // Scores in powers of two; lane (g, t) has keys g, g + 8 of each 16 and queries 2t, 2t + 1 of each 8.
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float f[2] = {sc[h] * fq[n][0], sc[h] * fq[n][1]};
+                    // a value scale that is NaN or infinite shows in the scores, so in the rows that see them alone
+                    const float ks = fmaf(sc[2 + h], 0.0f, sc[h]);
+                    const float f[2] = {ks * fq[n][0], ks * fq[n][1]};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) z[h][n][c] = fmaf(z2[n][c], 0.03125f, z[h][n][c]) * f[c & 1];
                 }
@@ -594,27 +609,39 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                         for (int c = 0; c < 4; ++c)
                             if (key0 + h * 16 + (c >> 1) * 8 + g >= limit[n][c & 1]) z[h][n][c] = AC_NONE;
             }
-            float high[NT][2];
+            const float lv[2] = {ac_lg2(sc[2]) - AC_LIFT, ac_lg2(sc[3]) - AC_LIFT};  // the values' scales in powers of two
+            float high[NT][2][2];  // largest score of either half
             bool higher = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    high[n][j] = fmaxf(fmaxf(z[0][n][j], z[0][n][2 + j]), fmaxf(z[1][n][j], z[1][n][2 + j]));
-                    higher |= high[n][j] > m[n][j] + AC_SLACK;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) high[n][j][h] = fmaxf(z[h][n][j], z[h][n][2 + j]);
+                    // (differences: s may be so large that a scale's power of two is lost beside it)
+                    const float h0 = high[n][j][0] - m[n][j], h1 = high[n][j][1] - m[n][j];
+                    higher |= fmaxf(h0, h1) > AC_SLACK;
+                    higher |= fmaxf(h0 + (lv[0] + dm[n][j]), h1 + (lv[1] + dm[n][j])) > AC_SLACK - AC_LIFT;
                 }
             if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float v = fmaxf(high[n][j], m[n][j]);
+                        const float before = m[n][j], d0 = dm[n][j];
+                        float v = fmaxf(fmaxf(high[n][j][0], high[n][j][1]), before);
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                        // Equal references leave the sums alone, both -inf (nothing seen yet) among them.
-                        const float f = v == m[n][j] ? 1.0f : ac_ex2(m[n][j] - v);
+                        const float down = before == AC_NONE ? 0.0f : before - v;  // nothing seen yet: the sums are zero
+                        // The largest s + log2(scale_v) less v, o's reference so far among them.
+                        float w = before == AC_NONE ? AC_NONE : down - d0;
+                        if (v != AC_NONE) w = fmaxf(w, fmaxf(high[n][j][0] - v + lv[0], high[n][j][1] - v + lv[1]) + AC_LIFT);
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, off));
                         m[n][j] = v;
-                        l[n][j] *= f;
+                        dm[n][j] = w == AC_NONE ? AC_UNSEEN : -w;
+                        l[n][j] *= ac_ex2(down);
+                        const float f = before == AC_NONE ? 1.0f : ac_ex2(down + (dm[n][j] - d0));
 #pragma unroll
                         for (int i = 0; i < KS; ++i) {
                             o[i][n][j] *= f;
@@ -622,37 +649,21 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                         }
                     }
             }
-            // Values' scales relative to the largest so far.
-            float vr[2];
-            {
-                const float big = fmaxf(sc[2], sc[3]);
-                if (big > ref) {
-                    const float f = ref / big;
-                    ref = big;
-                    inv_ref = 1.0f / big;
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) o[i][n][c] *= f;
-                }
-                vr[0] = sc[2] * inv_ref;
-                vr[1] = sc[3] * inv_ref;
-            }
             uint32_t pt[2][NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float m0 = m[n][0] == AC_NONE ? 0.0f : m[n][0] - AC_BIAS;
-                const float m1 = m[n][1] == AC_NONE ? 0.0f : m[n][1] - AC_BIAS;
+                const float m0 = m[n][0] == AC_NONE ? 0.0f : m[n][0] - (AC_BIAS + AC_LIFT);
+                const float m1 = m[n][1] == AC_NONE ? 0.0f : m[n][1] - (AC_BIAS + AC_LIFT);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    // Beyond 2^207 a page's scale would meet probabilities that are zero.
+                    const float w0 = ac_ex2(fminf(lv[h] + dm[n][0], 127.0f)), w1 = ac_ex2(fminf(lv[h] + dm[n][1], 127.0f));
                     const float p0 = ac_ex2(z[h][n][0] - m0), p1 = ac_ex2(z[h][n][1] - m1);
                     const float p2 = ac_ex2(z[h][n][2] - m0), p3 = ac_ex2(z[h][n][3] - m1);
                     l[n][0] += p0 + p2;
                     l[n][1] += p1 + p3;
-                    pt[h][n][0] = ac_transpose(ac_half2(p0 * vr[h], p1 * vr[h]));
-                    pt[h][n][1] = ac_transpose(ac_half2(p2 * vr[h], p3 * vr[h]));
+                    pt[h][n][0] = ac_transpose(ac_half2(p0 * w0, p1 * w1));
+                    pt[h][n][1] = ac_transpose(ac_half2(p2 * w0, p3 * w1));
                 }
             }
 #pragma unroll
@@ -699,12 +710,19 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
-        // What a row's tiles give by themselves, the sums over their probabilities' sum: as large as the values at most, where the
-        // sums in units of the values would pass fp32's range before them. Zeros where the row saw no key here.
-        auto own = [&](int i, int n, int c) {
-            const float sum = l[n][c & 1];
-            return sum == 0.0f ? 0.0f : o[i][n][c] * ac_inverse(sum) * ref;
-        };
+#pragma unroll
+        for (int n = 0; n < NT; ++n) l[n][0] *= AC_UNLIFT, l[n][1] *= AC_UNLIFT;
+        // What a row's tiles give by themselves: the sums over their probabilities' sum, from o's reference to theirs (in two
+        // steps, as the way may pass what a number holds), as large as the values at most.
+        float to_own[NT][2], back[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                back[n][j] = ac_ex2(-0.5f * dm[n][j]);
+                to_own[n][j] = back[n][j] * ac_inverse(l[n][j]);
+            }
+        auto own = [&](int i, int n, int c) { return o[i][n][c] * to_own[n][c & 1] * back[n][c & 1]; };
         if (tile0 == 0 && tile1 == s.tiles) {
             // The whole item: lane (g, t) has D / 8 neighbouring elements of queries 2t and 2t + 1 of each eight.
 #pragma unroll
@@ -729,9 +747,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int row = n * 8 + 2 * t + j;
+                const bool none = l[n][j] == 0.0f;  // no key seen: zeros, whatever the sums hold
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
-                    to[row * (D / 2) + ac_join(g * (D / 16) + i, row)] = make_float2(own(i, n, j), own(i, n, 2 + j));
+                    to[row * (D / 2) + ac_join(g * (D / 16) + i, row)] =
+                        none ? make_float2(0.0f, 0.0f) : make_float2(own(i, n, j), own(i, n, 2 + j));
                 if (g == 0)
                     *reinterpret_cast<float2*>(stats + ((warp * 2 + which) * C::ROWS + row) * 2) = make_float2(m[n][j], l[n][j]);
             }
@@ -752,14 +772,15 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     // Join of the records, which stand in the line's order: those of one item follow one another. First every record's share of
     // its item's sum, row by row, a thread each.
     constexpr int RECS = 2 * AC_WARPS;
-    __shared__ float shares[RECS][C::ROWS];
+    __shared__ float2 shares[RECS][C::ROWS];  // as two factors: one number may not hold it where the values make up for it
     __shared__ float2 joined[RECS][C::ROWS];  // (reference, sum) of the item
     const long long my_u0 = rec[lane % RECS].u0;
     const unsigned mates = __match_any_sync(0xffffffffu, my_u0) & ((1u << RECS) - 1);
     if (tid < RECS * C::ROWS) {
         const int k = tid % RECS, row = tid / RECS;
         float2 ml[RECS];
-        float top = AC_NONE, sum = 0.0f, mine = 0.0f;
+        float top = AC_NONE, sum = 0.0f;
+        float2 mine = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < RECS; ++j) {
             ml[j] = *reinterpret_cast<const float2*>(stats + (j * C::ROWS + row) * 2);
@@ -770,9 +791,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         for (int j = 0; j < RECS; ++j) {
             const float f = mates >> j & 1 ? ml[j].y * ac_ex2(ml[j].x - from) : 0.0f;
             sum += f;
-            if (j == k) mine = f;
+            if (j == k) mine = ml[j];
         }
-        shares[k][row] = mine * ac_inverse(sum);
+        const float h = ac_ex2(0.5f * (mine.x - from));
+        shares[k][row] = make_float2(h, mine.y * h * ac_inverse(sum));
         joined[k][row] = make_float2(top, sum);
     }
     __syncthreads();
@@ -792,13 +814,13 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 #pragma unroll
             for (int k = 0; k < RECS; ++k) {
                 if (!(chain >> k & 1)) continue;
-                const float f = shares[k][row];
+                const float2 f = shares[k][row];
                 const float2* from = reinterpret_cast<const float2*>(smem + (k >> 1) * C::WARP + (k & 1 ? 0 : C::RING)) + row * (D / 2);
                 const float2 u = from[ac_join(c, row)], v = from[ac_join(c + 1, row)];
-                x.x += u.x * f;
-                x.y += u.y * f;
-                x.z += v.x * f;
-                x.w += v.y * f;
+                x.x += u.x * f.x * f.y;
+                x.y += u.y * f.x * f.y;
+                x.z += v.x * f.x * f.y;
+                x.w += v.y * f.x * f.y;
             }
             const float2 at = joined[r0][row];
             if (whole) {
@@ -857,40 +879,43 @@ __global__ void __launch_bounds__(AC_JOIN) attn_cache_join_kernel(const AcArgs a
             }
 #pragma unroll
             for (int j = 0; j < AC_BATCH; ++j) high = fmaxf(high, ml[j].x);
-            // x is the output of the parts so far, each with its share of the sum.
-            const float before = sum * (top == high ? 1.0f : ac_ex2(top - high));
+            // x is the output of the parts so far, each with its share of the sum, which is taken in two factors (as above).
+            const float down = ac_half(top, high);
             top = high;
-            sum = before;
-            float f[AC_BATCH];
+            sum *= down;
+            float next = sum * down;
+            float2 f[AC_BATCH];
 #pragma unroll
             for (int j = 0; j < AC_BATCH; ++j) {
-                f[j] = ml[j].y * (ml[j].x == top ? 1.0f : ac_ex2(ml[j].x - top));
-                sum += f[j];
+                f[j].x = ac_half(ml[j].x, top);
+                f[j].y = ml[j].y * f[j].x;
+                next += f[j].x * f[j].y;
             }
-            const float inv = ac_inverse(sum), keep = before * inv;
-            x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+            const float inv = ac_inverse(next), keep = sum * inv;
+            sum = next;
+            x = make_float4(x.x * down * keep, x.y * down * keep, x.z * down * keep, x.w * down * keep);
 #pragma unroll
             for (int j = 0; j < AC_BATCH; ++j) {
-                f[j] *= inv;
-                x.x += v[j].x * f[j];
-                x.y += v[j].y * f[j];
-                x.z += v[j].z * f[j];
-                x.w += v[j].w * f[j];
+                f[j].y *= inv;
+                x.x += v[j].x * f[j].x * f[j].y;
+                x.y += v[j].y * f[j].x * f[j].y;
+                x.z += v[j].z * f[j].x * f[j].y;
+                x.w += v[j].w * f[j].x * f[j].y;
             }
         }
+        // The lanes of an element: their reference and sum first, then each one's share of it.
+        const float mine = top;
+        for (int off = wide; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float h = ac_half(mine, top), own = sum * h;
+        sum = own * h;
+        for (int off = wide; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const float share = own * ac_inverse(sum);
+        x = make_float4(x.x * h * share, x.y * h * share, x.z * h * share, x.w * h * share);
         for (int off = wide; off < 32; off <<= 1) {
-            const float other = __shfl_xor_sync(0xffffffffu, top, off), high = fmaxf(top, other);
-            float f = sum * (top == high ? 1.0f : ac_ex2(top - high));
-            float g = __shfl_xor_sync(0xffffffffu, sum, off) * (other == high ? 1.0f : ac_ex2(other - high));
-            top = high;
-            sum = f + g;
-            const float inv = ac_inverse(sum);
-            f *= inv;
-            g *= inv;
-            x.x = x.x * f + __shfl_xor_sync(0xffffffffu, x.x, off) * g;
-            x.y = x.y * f + __shfl_xor_sync(0xffffffffu, x.y, off) * g;
-            x.z = x.z * f + __shfl_xor_sync(0xffffffffu, x.z, off) * g;
-            x.w = x.w * f + __shfl_xor_sync(0xffffffffu, x.w, off) * g;
+            x.x += __shfl_xor_sync(0xffffffffu, x.x, off);
+            x.y += __shfl_xor_sync(0xffffffffu, x.y, off);
+            x.z += __shfl_xor_sync(0xffffffffu, x.z, off);
+            x.w += __shfl_xor_sync(0xffffffffu, x.w, off);
         }
         if (live && lane < wide)
             ac_store(a, it.head, ac_row(a, it.query, it.member, row), c * 4, D, x, top, sum);
