@@ -477,8 +477,7 @@ MP_API mp_status mp_attn_varlen_bwd(const mp_bf16* Q, const mp_bf16* K, const mp
  * throughout, one rounding to bf16.
  *   x, y [T, heads, d], rows ldx, ldy elements apart; y may be x itself (then ldx == ldy), and must not overlap it
  *   otherwise. wq, wk [d]: the one that no head takes may be NULL. pos [axes, T] int32.
- *   Size rules as mp_rope_axes; 0 <= q_heads <= heads; eps > 0 and finite. Squares are fp32: a head whose mean square
- *   passes 2^127 gives zeros.
+ *   Size rules as mp_rope_axes; 0 <= q_heads <= heads; eps > 0 and finite.
  */
 MP_API mp_status mp_qk_norm_rope(const mp_bf16* x, mp_bf16* y, const mp_bf16* wq, const mp_bf16* wk, const int32_t* pos,
                           int T, int heads, int q_heads, int d, long long ldx, long long ldy,

@@ -28,6 +28,9 @@ namespace mptp {
 constexpr int QKN_WARPS = 4;         // warps of a block
 constexpr int QKN_STAGES = 4;        // steps in flight, and the one in hand
 constexpr int QKN_RUN = 48;          // steps of a warp of the forward pass
+// Of 32 lanes' squares of a head, none larger than this, the sum lies within fp32's range. (The test comes before the lanes' sum: behind
+// it, where it could wait for the exchanges, 8192 tokens of 20 heads of 72 take 15.5 us forward, not 15.0.)
+constexpr float QKN_MOST = 4.0e36f;
 // Blocks on an SM, as many as registers allow without spills: narrow lanes (VEC 4) one more (8192 tokens of 20 heads of 72 16.5 us
 // forward with five, 19.6 with four, 18.3 with six; backward 24.4 with four, 25.5 with three, 26.7 with five).
 constexpr int qkn_per_sm(bool wide, bool backward) { return wide ? (backward ? 3 : 4) : backward ? 4 : 5; }
@@ -266,6 +269,16 @@ __device__ __forceinline__ void qk_take(const uint8_t* at, float2 (&f)[VEC]) {
     qk_floats(x, f);
 }
 
+// Of a head whose squares may pass fp32's range (by its width, a root mean square from 2^57 to 2^61 on): its elements times 2^-80,
+// whose squares it holds, and those that count stay normal. Returns the factor, 1 for other heads.
+template <int VEC>
+__device__ __forceinline__ float qk_scale_down(float2 (&x)[VEC], float sum) {
+    const float down = sum > QKN_MOST ? 8.271806125530277e-25f : 1.0f;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) x[j] = mul2(x[j], make_float2(down, down));
+    return down;
+}
+
 template <int VEC, bool INTER, int SUM, bool BACKWARD>
 __global__ void __launch_bounds__(QKN_WARPS * 32, qkn_per_sm(VEC == 8, BACKWARD)) qk_norm_kernel(
     const __grid_constant__ RopeTable tab, const QkNormArgs a) {
@@ -342,36 +355,62 @@ __global__ void __launch_bounds__(QKN_WARPS * 32, qkn_per_sm(VEC == 8, BACKWARD)
         }
         float2 x[VEC], y[VEC];
         qk_take<VEC>(at, x);
-        float2 ss = make_float2(0.0f, 0.0f);
+        float down = 1.0f, eps = a.eps;  // x stands for x / down
         if constexpr (!BACKWARD) {
+            float sum[1];
+            auto squares = [&] {
+                float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) ss = fma2(x[j], x[j], ss);
-            float sum[1] = {ss.x + ss.y};
+                for (int j = 0; j < VEC; ++j) ss = fma2(x[j], x[j], ss);
+                sum[0] = ss.x + ss.y;
+            };
+            squares();
+            if (__any_sync(0xffffffffu, sum[0] > QKN_MOST)) {
+                float all[1] = {sum[0]};
+                qk_head_sum<SUM>(all, L.groups, L.g, lane, turn);
+                down = qk_scale_down(x, all[0]);
+                eps = eps * down * down;
+                squares();
+            }
             qk_head_sum<SUM>(sum, L.groups, L.g, lane, turn);
             walk.fetch();
-            const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
+            const float r = rsqrtf(sum[0] * a.inv_d + eps);
             qk_turn<VEC, INTER>(x, P, Q, y);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) y[j] = mul2(y[j], make_float2(r, r));
         } else {
-            float2 g[VEC], dot = ss;
+            float2 g[VEC];
             qk_take<VEC>(at + 4 * VEC * 32, y);
             qk_turn<VEC, INTER>(y, P, Q, g);
+            float sum[2];  // x^2, w g x
+            auto products = [&] {
+                float2 ss = make_float2(0.0f, 0.0f), dot = ss;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                ss = fma2(x[j], x[j], ss);
-                y[j] = mul2(g[j], x[j]);
-                dot = fma2(y[j], w[j], dot);
+                for (int j = 0; j < VEC; ++j) {
+                    ss = fma2(x[j], x[j], ss);
+                    y[j] = mul2(g[j], x[j]);
+                    dot = fma2(y[j], w[j], dot);
+                }
+                sum[0] = ss.x + ss.y;
+                sum[1] = dot.x + dot.y;
+            };
+            products();
+            if (__any_sync(0xffffffffu, sum[0] > QKN_MOST)) {
+                float all[1] = {sum[0]};
+                qk_head_sum<SUM>(all, L.groups, L.g, lane, turn);
+                down = qk_scale_down(x, all[0]);
+                eps = eps * down * down;
+                products();
             }
-            float sum[2] = {ss.x + ss.y, dot.x + dot.y};  // x^2, w g x
             qk_head_sum<SUM>(sum, L.groups, L.g, lane, turn);
             walk.fetch();
-            const float r = rsqrtf(sum[0] * a.inv_d + a.eps);
+            const float r = rsqrtf(sum[0] * a.inv_d + eps);
             const float m = -(sum[1] * a.inv_d * r) * r;  // -r mean(w g n)
+            const float out_r = r * down;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 acc[j] = fma2(y[j], make_float2(r, r), acc[j]);
-                y[j] = mul2(fma2(x[j], make_float2(m, m), mul2(w[j], g[j])), make_float2(r, r));
+                y[j] = mul2(fma2(x[j], make_float2(m, m), mul2(w[j], g[j])), make_float2(out_r, out_r));
             }
         }
         if (step < own) qk_store(y, out, L);
