@@ -210,9 +210,9 @@ template <int ROWS, int N>
 __device__ __forceinline__ void ac_seqs(const AcArgs& a, const KvPool& p, int seq, AcSeq (&s)[N]) {
     int q[N + 1], len[N];
 #pragma unroll
-    for (int k = 0; k <= N; ++k) q[k] = seq + k <= a.nseq ? __ldg(a.cu_q + seq + k) : 0;
+    for (int k = 0; k <= N; ++k) q[k] = seq + k <= a.nseq ? a.cu_q[seq + k] : 0;
 #pragma unroll
-    for (int k = 0; k < N; ++k) len[k] = seq + k < a.nseq ? __ldg(a.lens + seq + k) : 0;
+    for (int k = 0; k < N; ++k) len[k] = seq + k < a.nseq ? a.lens[seq + k] : 0;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         s[k] = AcSeq{0, 0, 0, 1, 0};
@@ -401,9 +401,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         auto look = [&](int k, int (&id)[2]) {
             const int key = (tile0 + k) * AC_TILE;
             id[0] = -1;
-            if (key < s.len) id[0] = __ldg(table + (key >> p.page_shift));
+            if (key < s.len) id[0] = table[key >> p.page_shift];
             id[1] = id[0];
-            if (two) id[1] = key + 16 < s.len ? __ldg(table + (key >> 4) + 1) : -1;
+            if (two) id[1] = key + 16 < s.len ? table[(key >> 4) + 1] : -1;
         };
         auto issue = [&](int k, const int (&id)[2]) {
             if (k < tiles) {
