@@ -100,6 +100,7 @@ PyObject* call(PyObject* const* a, Py_ssize_t n, Py_ssize_t want, F f) {
         const int code = f(args);
         if (args.ok) return PyLong_FromLong(code);
     } catch (...) {  // a tensor that does not answer like an ordinary one
+        PyErr_Clear();   // nor does what its answers in Python raised stay set
     }
     Py_RETURN_NONE;
 }
