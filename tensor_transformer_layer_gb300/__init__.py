@@ -180,6 +180,17 @@ def _fast():
     return _bind
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
+def _here(**tensors):
+    """Refuses tensors of another GPU than the current one, where a kernel would take their addresses for its own."""
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
+            raise ValueError(f"{name} lies on cuda:{t.get_device()}, the current device is cuda:{_current_device()}")
+
+
 def _handle(stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
@@ -633,6 +644,7 @@ def mp_qk_norm_rope(x, y, wq, wk, pos, *, q_heads: int, sections, base: float = 
     code = (_bind or _fast()).qk_norm_rope(x, y, wq, wk, pos, q_heads, sections, base, eps, flags, _handle(stream))
     if code is not None:
         return _check("mp_qk_norm_rope", code)
+    _here(x=x, y=y, wq=wq, wk=wk, pos=pos)
     size, nq = _norm_heads(x, q_heads)
     T, heads, d = size
     (px, ldx), (py, ldy) = _heads_view(x, "x", size), _heads_view(y, "y", size)
@@ -656,6 +668,7 @@ def mp_qk_norm_rope_bwd(x, dy, dx, wq, wk, dwq, dwk, pos, workspace, *, q_heads:
                                                flags, _handle(stream))
     if code is not None:
         return _check("mp_qk_norm_rope_bwd", code)
+    _here(x=x, dy=dy, dx=dx, wq=wq, wk=wk, dwq=dwq, dwk=dwk, pos=pos, workspace=workspace)
     size, nq = _norm_heads(x, q_heads)
     T, heads, d = size
     (px, ldx), (pg, ldg), (pd, ldd) = (_heads_view(x, "x", size), _heads_view(dy, "dy", size),
@@ -736,6 +749,7 @@ def mp_kv_cache_write(K, V, kc, vc, ks, vs, page_table, cu, start, *, max_n: int
     code = (_bind or _fast()).kv_cache_write(K, V, kc, vc, ks, vs, page_table, cu, start, max_n, d_status, _handle(stream))
     if code is not None:
         return _check("mp_kv_cache_write", code)
+    _here(K=K, V=V, kc=kc, vc=vc, ks=ks, vs=vs, page_table=page_table, cu=cu, start=start, d_status=d_status)
     pk, pv, pool, pt, pcu, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, max_n)
     code = lib().mp_kv_cache_write(pk, pv, *pool, pt, pcu, _ptr(start, "start", torch.int32, (nseq,)), *sizes,
                                    _status_ptr(d_status), _stream(stream))
@@ -748,6 +762,7 @@ def mp_kv_cache_read(kc, vc, ks, vs, K, V, page_table, cu, start=None, *, max_n:
     code = (_bind or _fast()).kv_cache_read(K, V, kc, vc, ks, vs, page_table, cu, start, max_n, d_status, _handle(stream))
     if code is not None:
         return _check("mp_kv_cache_read", code)
+    _here(K=K, V=V, kc=kc, vc=vc, ks=ks, vs=vs, page_table=page_table, cu=cu, start=start, d_status=d_status)
     pk, pv, pool, pt, pcu, nseq, sizes = _kv_rows(K, V, kc, vc, ks, vs, page_table, cu, max_n)
     code = lib().mp_kv_cache_read(*pool, pk, pv, pt, pcu, _ptr(start, "start", torch.int32, (nseq,), True), *sizes,
                                   _status_ptr(d_status), _stream(stream))
@@ -768,6 +783,8 @@ def mp_attn_cache_fwd(Q, kc, vc, ks, vs, O, LSE, page_table, cu_q, lens, workspa
                                              1 if causal else 0, scale, d_status, _handle(stream))
     if code is not None:
         return _check("mp_attn_cache_fwd", code)
+    _here(Q=Q, kc=kc, vc=vc, ks=ks, vs=vs, O=O, LSE=LSE, page_table=page_table, cu_q=cu_q, lens=lens, workspace=workspace,
+          d_status=d_status)
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
         raise ValueError("Q must be a [tokens, heads, d] tensor")
     nseq, pcu = _sequences(cu_q, "cu_q")

@@ -4,10 +4,11 @@
 // 4.7 against 14.7, the norm 4.4 against 9.5; a launch alone is 2 to 3 of it.
 //
 // It takes what a right call passes and nothing else: each function returns the entry point's status, or None where anything
-// is out of the ordinary (another type, an unusual stride, an empty tensor, a number beyond 32 bits). The Python binding then
+// is out of the ordinary (another type or device, an unusual stride, an empty tensor, a number beyond 32 bits). The Python binding then
 // goes through its own checks, which say what is wrong or make the call.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -22,11 +23,17 @@ namespace {
 struct Args {
     PyObject* const* a;
     bool ok = true;
+    int device = -1;  // the current one, asked for with the first tensor
 
+    bool here(const at::Tensor& t) {
+        if (device < 0) device = c10::cuda::current_device();
+        return t.get_device() == device;
+    }
     const at::Tensor* tensor(int i, at::ScalarType type) {
         if (!ok || !THPVariable_Check(a[i])) return fail();
         const at::Tensor& t = THPVariable_Unpack(a[i]);
-        if (t.scalar_type() != type || !t.is_cuda() || t.layout() != at::kStrided || t.numel() == 0) return fail();
+        if (t.scalar_type() != type || !t.is_cuda() || t.layout() != at::kStrided || t.numel() == 0 || !here(t))
+            return fail();
         return &t;
     }
     // Contiguous, of this shape.
@@ -63,7 +70,8 @@ struct Args {
     void* workspace(int i, size_t* bytes) {
         if (!ok || !THPVariable_Check(a[i])) return ok = false, nullptr;
         const at::Tensor& t = THPVariable_Unpack(a[i]);
-        if (!t.is_cuda() || t.layout() != at::kStrided || t.numel() == 0 || !t.is_contiguous()) return ok = false, nullptr;
+        if (!t.is_cuda() || t.layout() != at::kStrided || t.numel() == 0 || !here(t) || !t.is_contiguous())
+            return ok = false, nullptr;
         *bytes = t.nbytes();
         return t.data_ptr();
     }
