@@ -18,11 +18,12 @@
 // Numbers. Q is scaled per row by a power of two into [128, 256) at its largest and split into two e4m3 pieces, q1 + q2 / 32:
 // four of bf16's eight bits each, exact but for elements below 2^-13 of the largest, which keep 2^-22 of it. Both pieces have
 // sums of their own (fp32, as every sum and statistic here). Each row has two references, which the largest so far passes by 8 at
-// most: m of its scores s, in powers of two, and m - dm of s + log2(scale_v). P = 2^(s - m + 7) goes into the row's sum, and
-// P * scale_v * 2^dm, 2^7 or more at its largest, is rounded to halves: 2^-11 of its value, at least 2^-25 absolutely, 2^-32 of
-// the largest P * scale_v among the tokens that the row sees, whatever scales other pages have. (With one reference for all
-// rows of a warp's run, the largest scale met, pages 2^21 below it lost bits and 2^32 below it everything.) Within a run P is
-// 2^80 times that, so that pages with less than 2^-126 of a row's probability count while their scales are 2^200 times others'.
+// most, of its scores s in powers of two and of s + log2(scale_v). Relative to the second, probabilities times scales, 2^7 or
+// more at their largest, are rounded to halves: 2^-11 of a value, at least 2^-25 absolutely, 2^-32 of the largest P * scale_v
+// among the tokens that the row sees, whatever scales other pages have. (With one reference for all rows of a warp's run, the
+// largest scale met, pages 2^21 below it lost bits and 2^32 below it everything.) Relative to the first, P is 2^87 at its
+// largest within a run (fp32; l with 2^31 keys still holds it), so that pages with less than 2^-126 of a row's probability count
+// while their scales are 2^200 times others'.
 //
 // Work. The tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, AC_ITEM places for what an item
 // costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
@@ -51,8 +52,10 @@ constexpr int AC_JOIN = 256;       // threads of a block of the join
 constexpr int AC_BATCH = 3;        // parts in flight in each
 constexpr int AC_SEQS = 4;         // sequences a lane looks at in one step
 constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference before sums are scaled down
-constexpr float AC_LIFT = 80.0f, AC_UNLIFT = 8.271806125530277e-25f;  // by so much more within a run; 2^-80
-constexpr float AC_UNSEEN = 200.0f;  // dm of a row whose tokens so far have the value scale zero: below any other (2^-149)
+constexpr float AC_LIFT = 87.0f;   // exponent that P carries within a run, while scores are
+constexpr float AC_NEAR = 1048576.0f;  // below 2^20 and such a difference is not lost beside them; else none
+constexpr float AC_FAR = -3.0e38f;     // a row that has seen no key, as its reference: no score comes so low
+constexpr float AC_UNSEEN = 200.0f;    // dm of a row whose tokens so far have the value scale zero: below any other (2^-149)
 constexpr float AC_LOG2E = 1.4426950408889634f;
 constexpr float AC_LN2 = 0.6931471805599453f;
 
@@ -131,6 +134,13 @@ __device__ __forceinline__ float ac_half(float m, float top) { return m == top ?
 // 1 / sum; 0 where nothing was summed.
 __device__ __forceinline__ float ac_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 
+// Exponent that P carries beside the reference m0.
+__device__ __forceinline__ float ac_lift(float m0) { return fabsf(m0) < AC_NEAR ? AC_LIFT : 0.0f; }
+// The reference for scores up to v.
+__device__ __forceinline__ float ac_reference(float v) {
+    const float low = v - AC_LIFT;
+    return fabsf(low) < AC_NEAR ? low : fabsf(v) < AC_NEAR ? -AC_NEAR : v;
+}
 __device__ __forceinline__ float ac_lg2(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -531,11 +541,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const int clear = a.causal ? s.len - s.nq + ahead0 + 1 : s.len;
 
         float o[KS][NT][4];
-        float m[NT][2], l[NT][2];  // reference and sum of the probabilities
-        float dm[NT][2];           // the reference of o, of probabilities times the values' scales, is m - dm
+        // P = 2^(s - m0) and its sum; o is the sum of P * scale_v * 2^dm times the values' codes.
+        float m0[NT][2], l[NT][2], dm[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = AC_NONE;
+            m0[n][0] = m0[n][1] = AC_FAR;
             dm[n][0] = dm[n][1] = AC_UNSEEN;
             l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
@@ -609,7 +619,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                         for (int c = 0; c < 4; ++c)
                             if (key0 + h * 16 + (c >> 1) * 8 + g >= limit[n][c & 1]) z[h][n][c] = AC_NONE;
             }
-            const float lv[2] = {ac_lg2(sc[2]) - AC_LIFT, ac_lg2(sc[3]) - AC_LIFT};  // the values' scales in powers of two
+            const float lv[2] = {ac_lg2(sc[2]), ac_lg2(sc[3])};  // the values' scales in powers of two
             float high[NT][2][2];  // largest score of either half
             bool higher = false;
 #pragma unroll
@@ -618,30 +628,30 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 for (int j = 0; j < 2; ++j) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) high[n][j][h] = fmaxf(z[h][n][j], z[h][n][2 + j]);
-                    // (differences: s may be so large that a scale's power of two is lost beside it)
-                    const float h0 = high[n][j][0] - m[n][j], h1 = high[n][j][1] - m[n][j];
-                    higher |= fmaxf(h0, h1) > AC_SLACK;
-                    higher |= fmaxf(h0 + (lv[0] + dm[n][j]), h1 + (lv[1] + dm[n][j])) > AC_SLACK - AC_LIFT;
+                    const float h0 = high[n][j][0] - m0[n][j], h1 = high[n][j][1] - m0[n][j];
+                    higher |= fmaxf(h0, h1) > ac_lift(m0[n][j]) + AC_SLACK;
+                    higher |= fmaxf(h0 + (lv[0] + dm[n][j]), h1 + (lv[1] + dm[n][j])) > AC_BIAS + AC_SLACK;
                 }
             if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float before = m[n][j], d0 = dm[n][j];
-                        float v = fmaxf(fmaxf(high[n][j][0], high[n][j][1]), before);
+                        const float before = m0[n][j], d0 = dm[n][j];
+                        float v = fmaxf(fmaxf(high[n][j][0], high[n][j][1]), before + ac_lift(before));
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                        const float down = before == AC_NONE ? 0.0f : before - v;  // nothing seen yet: the sums are zero
-                        // The largest s + log2(scale_v) less v, o's reference so far among them.
-                        float w = before == AC_NONE ? AC_NONE : down - d0;
-                        if (v != AC_NONE) w = fmaxf(w, fmaxf(high[n][j][0] - v + lv[0], high[n][j][1] - v + lv[1]) + AC_LIFT);
+                        const float after = v > AC_FAR ? ac_reference(v) : AC_FAR;
+                        const float down = before - after;
+                        // The largest exponent of P * scale_v, that of o's reference so far among them.
+                        float w = before == AC_FAR ? AC_NONE : AC_BIAS - d0 + down;
+                        w = fmaxf(w, fmaxf(high[n][j][0] - after + lv[0], high[n][j][1] - after + lv[1]));
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, off));
-                        m[n][j] = v;
-                        dm[n][j] = w == AC_NONE ? AC_UNSEEN : -w;
+                        m0[n][j] = after;
+                        dm[n][j] = w == AC_NONE ? AC_UNSEEN : AC_BIAS - w;
                         l[n][j] *= ac_ex2(down);
-                        const float f = before == AC_NONE ? 1.0f : ac_ex2(down + (dm[n][j] - d0));
+                        const float f = ac_ex2(down + (dm[n][j] - d0));
 #pragma unroll
                         for (int i = 0; i < KS; ++i) {
                             o[i][n][j] *= f;
@@ -651,21 +661,18 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             }
             uint32_t pt[2][NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float m0 = m[n][0] == AC_NONE ? 0.0f : m[n][0] - (AC_BIAS + AC_LIFT);
-                const float m1 = m[n][1] == AC_NONE ? 0.0f : m[n][1] - (AC_BIAS + AC_LIFT);
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // Beyond 2^207 a page's scale would meet probabilities that are zero.
                     const float w0 = ac_ex2(fminf(lv[h] + dm[n][0], 127.0f)), w1 = ac_ex2(fminf(lv[h] + dm[n][1], 127.0f));
-                    const float p0 = ac_ex2(z[h][n][0] - m0), p1 = ac_ex2(z[h][n][1] - m1);
-                    const float p2 = ac_ex2(z[h][n][2] - m0), p3 = ac_ex2(z[h][n][3] - m1);
+                    const float p0 = ac_ex2(z[h][n][0] - m0[n][0]), p1 = ac_ex2(z[h][n][1] - m0[n][1]);
+                    const float p2 = ac_ex2(z[h][n][2] - m0[n][0]), p3 = ac_ex2(z[h][n][3] - m0[n][1]);
                     l[n][0] += p0 + p2;
                     l[n][1] += p1 + p3;
                     pt[h][n][0] = ac_transpose(ac_half2(p0 * w0, p1 * w1));
                     pt[h][n][1] = ac_transpose(ac_half2(p2 * w0, p3 * w1));
                 }
-            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 constexpr int VW = D / 32;  // words of a lane in one key row
@@ -710,16 +717,18 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) l[n][0] *= AC_UNLIFT, l[n][1] *= AC_UNLIFT;
-        // What a row's tiles give by themselves: the sums over their probabilities' sum, from o's reference to theirs (in two
-        // steps, as the way may pass what a number holds), as large as the values at most.
-        float to_own[NT][2], back[NT][2];
+        // Reference and sum as the joins take them, P with AC_BIAS. What a row's tiles give by themselves: the sums over the
+        // probabilities' sum, in the values' units (in two steps, as the way may pass what a number holds): as large as the values
+        // at most.
+        float m[NT][2], to_own[NT][2], back[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                back[n][j] = ac_ex2(-0.5f * dm[n][j]);
+                const float lift = ac_lift(m0[n][j]);
+                m[n][j] = m0[n][j] == AC_FAR ? AC_NONE : m0[n][j] + lift;
+                l[n][j] *= lift == 0.0f ? 128.0f : 8.271806125530277e-25f;  // 2^(AC_BIAS - lift)
+                back[n][j] = ac_ex2(0.5f * (AC_BIAS - lift - dm[n][j]));
                 to_own[n][j] = back[n][j] * ac_inverse(l[n][j]);
             }
         auto own = [&](int i, int n, int c) { return o[i][n][c] * to_own[n][c & 1] * back[n][c & 1]; };

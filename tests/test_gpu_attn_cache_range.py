@@ -144,3 +144,26 @@ def test_small_probabilities_of_large_values(by, first, page):
             scales[pg, 1] = 2.0 ** (110 - (0 if far else by))
     how = dict(scale=by * float(np.log(2.0)) / 448)
     _check(_run(*inp, new, lens, **how), inp, new, lens, only=(0, 11, 12), **how)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("top", [1e3, 1e5, 1.05e6, 4.2e6, 1e8, 1e9, 1e12, 1e20, 1e37])
+@pytest.mark.parametrize("n,at", [(90, 3), (90, 88), (3000, 1501)])
+def test_large_scores_give_the_value_of_the_largest(sign, top, n, at):
+    # one key's score is 7 % or more above all others', so that its value is the result
+    heads, kv, d, page = 4, 2, 64, 32
+    Q, codes, scales, table = _make([1, 1], [n, 40], heads, kv, d, page, 26600, spread=0)
+    g = torch.Generator().manual_seed(1)
+    Q[:] = 0
+    Q[0, :, 7] = float(np.float32(top))  # bf16 rounds it, for all keys alike
+    scales[:, 0] = 1.0 / 448
+    for k in range(-(-n // page)):
+        low = torch.randint(1, 13, (kv, page), generator=g).float() * 32  # 32 .. 384
+        codes[int(table[0, k]), 0, :, :, 7] = low if sign > 0 else -448.0
+    codes[int(table[0, at // page]), 0, :, at % page, 7] = 448.0 if sign > 0 else -416.0
+    O, LSE = _run(Q, codes, scales, table, [1, 1], [n, 40], scale=1.0)
+    pg = int(table[0, at // page])
+    want = codes[pg, 1, :, at % page].float() * scales[pg, 1][:, None]
+    assert torch.equal(O[0].float(), want.repeat_interleave(2, 0))
+    s = float(Q[0, 0, 7]) * (1.0 if sign > 0 else -416.0 / 448)
+    assert torch.all((LSE[:, 0].double() - s).abs() <= 2.0 ** -19 * abs(s))
