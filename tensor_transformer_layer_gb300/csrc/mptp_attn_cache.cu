@@ -4,9 +4,13 @@
 // page and head. A key head's rows are the nq * group queries that read it (group = heads / kv_heads):
 //   S = scale * scale_k * (q . code_k),  P = exp(S - max),  O = sum P * scale_v * code_v / sum P
 //
-// Bound by memory: every cached byte is read once and meets `rows` queries, 2 * rows flops a byte. So a warp reads 32 tokens'
-// codes into its own ring in shared memory (cp.async, 16 bytes a lane, two tiles ahead) and feeds mma.sync with the cache as
-// the 16-row operand and the queries as the 8-column one:
+// Bound by memory with up to eight rows: every cached byte comes from memory once and meets `rows` queries, 2 * rows flops a
+// byte. With more rows the warps' own instructions bound: 32 sequences of 8192 tokens and eight key heads take 91 us for 8 rows,
+// 116 for 16 and 212 for 32, while two warps on each scheduler issue in half of its cycles. (A head's row tiles beyond the first
+// read the cache again, from L2 where they follow soon: 32 rows took 545 MB from memory for 537 of cache.)
+//
+// A warp reads 32 tokens' codes into its own ring in shared memory (cp.async, 16 bytes a lane, two tiles ahead) and feeds mma.sync
+// with the cache as the 16-row operand and the queries as the 8-column one:
 //   S^T [keys x queries] = K Q^T in m16n8k32 of e4m3, the codes as they are: a lane's 16 bytes of a key row are its elements
 //     of two products (the summed index may be taken in any order, the same for Q);
 //   O^T [d x queries] += V^T P^T in m16n8k16 of halves: bytes of two key rows are interleaved into pairs of keys and turned
@@ -30,11 +34,12 @@
 // walks its run alone, without a barrier: an item that lies within it is finished from registers. Runs that begin or
 // end inside an item leave a record in shared memory, joined once at the CTA's end; an item that several CTAs share leaves
 // a part of each in the workspace, which a second kernel adds: one block for every CTA that an item goes on from, so that
-// an item's parts less one share its elements and a thread has two to five parts to add, whatever their number (20.9 us for
-// one sequence of 131 k tokens, 76 parts an item, 21.5 for 77 sequences, three parts or two; a block a row 21.6 and 23.3, the CTA
-// that comes last adding them alone 6 us and 3 longer).
+// an item's parts less one share its elements and a thread has two to five parts to add, whatever their number (20.5 us for
+// one sequence of 131 k tokens, 76 parts an item, 21.2 for 77 sequences, three parts or two; a block a row 0.7 and 1.8 longer, the CTA
+// that comes last adding them alone 6 and 3). A record and a part are the output of their own tiles with its sum, and a join
+// weighs them by their shares of all sums: sums in units of the values would pass fp32's range where values come near bf16's.
 //
-// Measured: 128 sequences of 3190 to 8192 tokens, 64 heads of 128 on eight, 231 us, 6.5 TB/s, 96 % of a copy's rate; a call takes
+// Measured: 128 sequences of 3190 to 8192 tokens, 64 heads of 128 on eight, 229 us, 6.5 TB/s, 96 % of a copy's rate; a call takes
 // 11 us besides its bytes (a warp's first tile is there after 3.7, lengths, table and codes in a row; joins and their launch 4).
 #include "mptp_kv_cache.cuh"
 #include "mptp_launch.cuh"
@@ -779,7 +784,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
     __syncthreads();
 
     // Join of the records, which stand in the line's order: those of one item follow one another. First every record's share of
-    // its item's sum, row by row, a thread each.
+    // its item's sum, row by row, a thread each (by each element's thread for itself: 22.9 us, not 21.2, for 77 sequences).
     constexpr int RECS = 2 * AC_WARPS;
     __shared__ float2 shares[RECS][C::ROWS];  // as two factors: one number may not hold it where the values make up for it
     __shared__ float2 joined[RECS][C::ROWS];  // (reference, sum) of the item
@@ -944,7 +949,9 @@ static cudaError_t launch_attn_cache(const AcArgs& a, const KvPool& p, cudaStrea
 
 constexpr size_t AC_ITEM_BYTES = (AC_CTAS * sizeof(AcItem) + 15) / 16 * 16;
 
-// Row tiles of eight queries where no sequence has more of a key head, else of sixteen.
+// Row tiles of eight queries where no sequence has more of a key head, else of sixteen. Those take 255 registers a thread and spill
+// (heads of 128: 124 bytes stored, 188 loaded; of 96: 12 and 12), and twice the rows take 1.3 times as long (32 sequences of 8192
+// tokens, eight key heads: 116 us instead of 91; heads of 64 71 instead of 53).
 static int ac_rows(int max_q, int group) { return static_cast<long long>(max_q) * group <= 8 ? 8 : 16; }
 
 }  // namespace mptp
