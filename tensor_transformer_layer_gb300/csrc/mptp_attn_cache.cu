@@ -26,8 +26,10 @@
 // more at their largest, are rounded to halves: 2^-11 of a value, at least 2^-25 absolutely, 2^-32 of the largest P * scale_v
 // among the tokens that the row sees, whatever scales other pages have. (With one reference for all rows of a warp's run, the
 // largest scale met, pages 2^21 below it lost bits and 2^32 below it everything.) Relative to the first, P is 2^87 at its
-// largest within a run (fp32; l with 2^31 keys still holds it), so that pages with less than 2^-126 of a row's probability count
-// while their scales are 2^200 times others'.
+// largest within a run (fp32; the sum over 2^31 keys still holds it), so that pages with less than 2^-126 of a row's probability
+// count while their scales are 2^200 times others'. A score's difference from its reference is rounded at 2^-18 so: the log-sum-exp is
+// within 2.6e-6 (2^7 instead: 1.6e-6, but scales then 2^119 times others' at most; 2^80 more only in runs that meet such scales: two
+// more registers, 126 us instead of 116 with 16 rows).
 //
 // Work. The tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, AC_ITEM places for what an item
 // costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
