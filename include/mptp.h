@@ -554,7 +554,7 @@ MP_API mp_status mp_kv_cache_read(const uint8_t* kc, const uint8_t* vc, const fl
  *   length outside [0, max_pages * page] is left out and sets MP_DEV_SEQ_RANGE; a page outside the pool sets
  *   MP_DEV_PAGE_RANGE, gives the rows that would see it O = LSE = NaN, and may give the sequence's other rows O = NaN. Rows
  *   of no sequence are not written. A token's weight, its probability times its page's value scale, is held to 2^-11 of itself
- *   and 2^-32 of the largest that its row sees, while no two scales that it sees differ by more than 2^200.
+ *   and 2^-32 of the largest that its row sees, while no two scales that it sees differ by more than 2^250.
  *   workspace: mp_attn_cache_workspace_bytes(heads, kv_heads, d, max_q) bytes (0 for sizes outside the rules), whatever they
  *   hold; calls that may overlap need one each.
  *   Size rules: d in {64, 96, 128}; heads % kv_heads == 0; heads <= 65536; max_q <= Tq; max_q * heads < 2^31 - 64; ldq, ldo at least a

@@ -21,15 +21,12 @@
 //
 // Numbers. Q is scaled per row by a power of two into [128, 256) at its largest and split into two e4m3 pieces, q1 + q2 / 32:
 // four of bf16's eight bits each, exact but for elements below 2^-13 of the largest, which keep 2^-22 of it. Both pieces have
-// sums of their own (fp32, as every sum and statistic here). Each row has two references, which the largest so far passes by 8 at
-// most, of its scores s in powers of two and of s + log2(scale_v). Relative to the second, probabilities times scales, 2^7 or
-// more at their largest, are rounded to halves: 2^-11 of a value, at least 2^-25 absolutely, 2^-32 of the largest P * scale_v
-// among the tokens that the row sees, whatever scales other pages have. (With one reference for all rows of a warp's run, the
-// largest scale met, pages 2^21 below it lost bits and 2^32 below it everything.) Relative to the first, P is 2^87 at its
-// largest within a run (fp32; the sum over 2^31 keys still holds it), so that pages with less than 2^-126 of a row's probability
-// count while their scales are 2^200 times others'. A score's difference from its reference is rounded at 2^-18 so: the log-sum-exp is
-// within 2.6e-6 (2^7 instead: 1.6e-6, but scales then 2^119 times others' at most; 2^80 more only in runs that meet such scales: two
-// more registers, 126 us instead of 116 with 16 rows).
+// sums of their own (fp32, as every sum and statistic here). Each row has two references, which the largest so far passes by 8
+// powers of two at most, of its scores and of its scores plus the logarithm of scale_v. Relative to the second, probabilities times
+// scales, 2^7 or more at their largest, are rounded to halves: 2^-11 of a value, at least 2^-25 absolutely, 2^-32 of the largest
+// P * scale_v among the tokens that the row sees, whatever scales other pages have. (With one reference for all rows of a warp's
+// run, the largest scale met, pages 2^21 below it lost bits and 2^32 below it everything.) Exponentials give the roots of P
+// and of a scale over its reference, which are multiplied and squared: P below 2^-126 counts where scale_v makes up for it.
 //
 // Work. The tiles of 32 keys of all (sequence, row tile, key head) items stand in one line, AC_ITEM places for what an item
 // costs besides in front of each item's; the line is split evenly among the CTAs and a CTA's run among its warps. A warp
@@ -54,15 +51,14 @@ constexpr int AC_TILE = 32;     // keys
 constexpr int AC_ITEM = 4;      // places of an item besides its tiles
 constexpr int AC_CTAS = 152;    // one on each SM: the workspace's parts
 #define AC_NONE __int_as_float(0xff800000)  // -inf: no key seen
-constexpr float AC_BIAS = 7.0f;    // exponent that P carries
 constexpr int AC_JOIN = 256;       // threads of a block of the join
 constexpr int AC_BATCH = 3;        // parts in flight in each
 constexpr int AC_SEQS = 4;         // sequences a lane looks at in one step
-constexpr float AC_SLACK = 8.0f;   // how far a score may pass its reference before sums are scaled down
-constexpr float AC_LIFT = 87.0f;   // exponent that P carries within a run, while scores are
-constexpr float AC_NEAR = 1048576.0f;  // below 2^20 and such a difference is not lost beside them; else none
-constexpr float AC_FAR = -3.0e38f;     // a row that has seen no key, as its reference: no score comes so low
-constexpr float AC_UNSEEN = 200.0f;    // dm of a row whose tokens so far have the value scale zero: below any other (2^-149)
+// In powers of four, as every score, reference and scale in logarithms here: where the largest P and the largest P * scale_v that a
+// reference is made for come to lie, and how far they may come before it is made anew (2^15: halves end at 2^16).
+constexpr float AC_P = 4.0f, AC_PV = 3.5f, AC_TOP = 7.5f;
+constexpr float AC_FAR = -3.0e38f;   // a row that has seen no key, as its reference: no score comes so low
+constexpr float AC_UNSEEN = 100.0f;  // dm of a row whose tokens so far have the value scale zero: below any other (2^-149)
 constexpr float AC_LOG2E = 1.4426950408889634f;
 constexpr float AC_LN2 = 0.6931471805599453f;
 
@@ -82,7 +78,7 @@ struct AcArgs {
     long long ldq, ldo;
     int nseq, Tq, max_q, heads, group, causal;
     float inv_group, inv_kv;  // 1 / group, 1 / key heads
-    float scale_log2;
+    float scale_log4;
     uint32_t* status;
 };
 
@@ -136,18 +132,11 @@ __device__ __forceinline__ float ac_ex2(float x) {
     return y;
 }
 
-// 2^((m - top) / 2), 1 where nothing was seen in either.
-__device__ __forceinline__ float ac_half(float m, float top) { return m == top ? 1.0f : ac_ex2(0.5f * (m - top)); }
+// The root of 4^(m - top), 1 where nothing was seen in either.
+__device__ __forceinline__ float ac_root(float m, float top) { return m == top ? 1.0f : ac_ex2(m - top); }
 // 1 / sum; 0 where nothing was summed.
 __device__ __forceinline__ float ac_inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 
-// Exponent that P carries beside the reference m0.
-__device__ __forceinline__ float ac_lift(float m0) { return fabsf(m0) < AC_NEAR ? AC_LIFT : 0.0f; }
-// The reference for scores up to v.
-__device__ __forceinline__ float ac_reference(float v) {
-    const float low = v - AC_LIFT;
-    return fabsf(low) < AC_NEAR ? low : fabsf(v) < AC_NEAR ? -AC_NEAR : v;
-}
 __device__ __forceinline__ float ac_lg2(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -260,7 +249,7 @@ __device__ __forceinline__ void ac_store(const AcArgs& a, int head, const AcRow&
         out = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
     }
     *reinterpret_cast<uint2*>(a.O + q * a.ldo + hd * D + d) = out;
-    if (d == 0) a.LSE[static_cast<long long>(hd) * a.Tq + q] = sum == 0.0f ? AC_NONE : (top + log2f(sum) - AC_BIAS) * AC_LN2;
+    if (d == 0) a.LSE[static_cast<long long>(hd) * a.Tq + q] = sum == 0.0f ? AC_NONE : (2.0f * (top + AC_P) + log2f(sum * 0.00390625f)) * AC_LN2;
 }
 
 template <int D, int NT>
@@ -507,7 +496,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         for (int k = 0; k < C::STAGES - 1; ++k) issue(k, ids[k]);
 
         uint32_t qf[2][NT][KS];  // pieces q1, q2
-        float fq[NT][2];         // factor from a product to a score in powers of two, for columns 2t, 2t + 1
+        float fq[NT][2];         // factor from a product to a score in powers of four, for columns 2t, 2t + 1
         int limit[NT][2];        // keys that those columns see
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -536,7 +525,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                 qf[0][n][k] = piece[0];
                 qf[1][n][k] = piece[1];
             }
-            const float f = __uint_as_float(static_cast<uint32_t>(min(e, 120) + 127) << 23) * a.scale_log2;
+            const float f = __uint_as_float(static_cast<uint32_t>(min(e, 120) + 127) << 23) * a.scale_log4;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 fq[n][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4);
@@ -548,7 +537,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const int clear = a.causal ? s.len - s.nq + ahead0 + 1 : s.len;
 
         float o[KS][NT][4];
-        // P = 2^(s - m0) and its sum; o is the sum of P * scale_v * 2^dm times the values' codes.
+        // P = 4^(s - m0) and its sum; o is the sum of P * scale_v * 4^dm times the values' codes.
         float m0[NT][2], l[NT][2], dm[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -607,7 +596,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                         ac_mma8(z[h][n], kw[0][i], kw[1][i], kw[0][i + 1], kw[1][i + 1], qf[0][n][i], qf[0][n][i + 1]);
                         ac_mma8(z2[n], kw[0][i], kw[1][i], kw[0][i + 1], kw[1][i + 1], qf[1][n][i], qf[1][n][i + 1]);
                     }
-                // Scores in powers of two; lane (g, t) has keys g, g + 8 of each 16 and queries 2t, 2t + 1 of each 8.
+                // Scores in powers of four; lane (g, t) has keys g, g + 8 of each 16 and queries 2t, 2t + 1 of each 8.
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     // a value scale that is NaN or infinite shows in the scores, so in the rows that see them alone
@@ -626,7 +615,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
                         for (int c = 0; c < 4; ++c)
                             if (key0 + h * 16 + (c >> 1) * 8 + g >= limit[n][c & 1]) z[h][n][c] = AC_NONE;
             }
-            const float lv[2] = {ac_lg2(sc[2]), ac_lg2(sc[3])};  // the values' scales in powers of two
+            const float lv[2] = {0.5f * ac_lg2(sc[2]), 0.5f * ac_lg2(sc[3])};  // the values' scales
             float high[NT][2][2];  // largest score of either half
             bool higher = false;
 #pragma unroll
@@ -636,8 +625,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 #pragma unroll
                     for (int h = 0; h < 2; ++h) high[n][j][h] = fmaxf(z[h][n][j], z[h][n][2 + j]);
                     const float h0 = high[n][j][0] - m0[n][j], h1 = high[n][j][1] - m0[n][j];
-                    higher |= fmaxf(h0, h1) > ac_lift(m0[n][j]) + AC_SLACK;
-                    higher |= fmaxf(h0 + (lv[0] + dm[n][j]), h1 + (lv[1] + dm[n][j])) > AC_BIAS + AC_SLACK;
+                    higher |= fmaxf(fmaxf(h0, h1), fmaxf(h0 + (lv[0] + dm[n][j]), h1 + (lv[1] + dm[n][j]))) > AC_TOP;
                 }
             if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
@@ -645,20 +633,20 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float before = m0[n][j], d0 = dm[n][j];
-                        float v = fmaxf(fmaxf(high[n][j][0], high[n][j][1]), before + ac_lift(before));
+                        float v = fmaxf(fmaxf(high[n][j][0], high[n][j][1]), before + AC_P);
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                        const float after = v > AC_FAR ? ac_reference(v) : AC_FAR;
+                        const float after = v > AC_FAR ? v - AC_P : AC_FAR;
                         const float down = before - after;
                         // The largest exponent of P * scale_v, that of o's reference so far among them.
-                        float w = before == AC_FAR ? AC_NONE : AC_BIAS - d0 + down;
+                        float w = before == AC_FAR ? AC_NONE : AC_PV - d0 + down;
                         w = fmaxf(w, fmaxf(high[n][j][0] - after + lv[0], high[n][j][1] - after + lv[1]));
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, off));
                         m0[n][j] = after;
-                        dm[n][j] = w == AC_NONE ? AC_UNSEEN : AC_BIAS - w;
-                        l[n][j] *= ac_ex2(down);
-                        const float f = ac_ex2(down + (dm[n][j] - d0));
+                        dm[n][j] = w == AC_NONE ? AC_UNSEEN : AC_PV - w;
+                        l[n][j] *= ac_ex2(2.0f * down);
+                        const float f = ac_ex2(2.0f * (down + (dm[n][j] - d0)));
 #pragma unroll
                         for (int i = 0; i < KS; ++i) {
                             o[i][n][j] *= f;
@@ -668,17 +656,18 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             }
             uint32_t pt[2][NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // Beyond 2^207 a page's scale would meet probabilities that are zero.
+                for (int n = 0; n < NT; ++n) {
+                    // Roots: their products hold what P and a scale far apart alone may not.
                     const float w0 = ac_ex2(fminf(lv[h] + dm[n][0], 127.0f)), w1 = ac_ex2(fminf(lv[h] + dm[n][1], 127.0f));
                     const float p0 = ac_ex2(z[h][n][0] - m0[n][0]), p1 = ac_ex2(z[h][n][1] - m0[n][1]);
                     const float p2 = ac_ex2(z[h][n][2] - m0[n][0]), p3 = ac_ex2(z[h][n][3] - m0[n][1]);
-                    l[n][0] += p0 + p2;
-                    l[n][1] += p1 + p3;
-                    pt[h][n][0] = ac_transpose(ac_half2(p0 * w0, p1 * w1));
-                    pt[h][n][1] = ac_transpose(ac_half2(p2 * w0, p3 * w1));
+                    l[n][0] += fmaf(p0, p0, p2 * p2);
+                    l[n][1] += fmaf(p1, p1, p3 * p3);
+                    const float v0 = p0 * w0, v1 = p1 * w1, v2 = p2 * w0, v3 = p3 * w1;
+                    pt[h][n][0] = ac_transpose(ac_half2(v0 * v0, v1 * v1));
+                    pt[h][n][1] = ac_transpose(ac_half2(v2 * v2, v3 * v3));
                 }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -724,18 +713,15 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
-        // Reference and sum as the joins take them, P with AC_BIAS. What a row's tiles give by themselves: the sums over the
-        // probabilities' sum, in the values' units (in two steps, as the way may pass what a number holds): as large as the values
-        // at most.
+        // What a row's tiles give by themselves: the sums over the probabilities' sum, in the values' units (in two steps, as the way
+        // may pass what a number holds): as large as the values at most.
         float m[NT][2], to_own[NT][2], back[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float lift = ac_lift(m0[n][j]);
-                m[n][j] = m0[n][j] == AC_FAR ? AC_NONE : m0[n][j] + lift;
-                l[n][j] *= lift == 0.0f ? 128.0f : 8.271806125530277e-25f;  // 2^(AC_BIAS - lift)
-                back[n][j] = ac_ex2(0.5f * (AC_BIAS - lift - dm[n][j]));
+                m[n][j] = m0[n][j] == AC_FAR ? AC_NONE : m0[n][j];
+                back[n][j] = ac_ex2(-dm[n][j]);
                 to_own[n][j] = back[n][j] * ac_inverse(l[n][j]);
             }
         auto own = [&](int i, int n, int c) { return o[i][n][c] * to_own[n][c & 1] * back[n][c & 1]; };
@@ -805,11 +791,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1) attn_cache_kernel(const AcArgs 
         const float from = top == AC_NONE ? 0.0f : top;
 #pragma unroll
         for (int j = 0; j < RECS; ++j) {
-            const float f = mates >> j & 1 ? ml[j].y * ac_ex2(ml[j].x - from) : 0.0f;
+            const float f = mates >> j & 1 ? ml[j].y * ac_ex2(2.0f * (ml[j].x - from)) : 0.0f;
             sum += f;
             if (j == k) mine = ml[j];
         }
-        const float h = ac_ex2(0.5f * (mine.x - from));
+        const float h = ac_ex2(mine.x - from);
         shares[k][row] = make_float2(h, mine.y * h * ac_inverse(sum));
         joined[k][row] = make_float2(top, sum);
     }
@@ -896,14 +882,14 @@ __global__ void __launch_bounds__(AC_JOIN) attn_cache_join_kernel(const AcArgs a
 #pragma unroll
             for (int j = 0; j < AC_BATCH; ++j) high = fmaxf(high, ml[j].x);
             // x is the output of the parts so far, each with its share of the sum, which is taken in two factors (as above).
-            const float down = ac_half(top, high);
+            const float down = ac_root(top, high);
             top = high;
             sum *= down;
             float next = sum * down;
             float2 f[AC_BATCH];
 #pragma unroll
             for (int j = 0; j < AC_BATCH; ++j) {
-                f[j].x = ac_half(ml[j].x, top);
+                f[j].x = ac_root(ml[j].x, top);
                 f[j].y = ml[j].y * f[j].x;
                 next += f[j].x * f[j].y;
             }
@@ -922,7 +908,7 @@ __global__ void __launch_bounds__(AC_JOIN) attn_cache_join_kernel(const AcArgs a
         // The lanes of an element: their reference and sum first, then each one's share of it.
         const float mine = top;
         for (int off = wide; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float h = ac_half(mine, top), own = sum * h;
+        const float h = ac_root(mine, top), own = sum * h;
         sum = own * h;
         for (int off = wide; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         const float share = own * ac_inverse(sum);
@@ -952,8 +938,8 @@ static cudaError_t launch_attn_cache(const AcArgs& a, const KvPool& p, cudaStrea
 constexpr size_t AC_ITEM_BYTES = (AC_CTAS * sizeof(AcItem) + 15) / 16 * 16;
 
 // Row tiles of eight queries where no sequence has more of a key head, else of sixteen. Those take 255 registers a thread and spill
-// (heads of 128: 124 bytes stored, 188 loaded; of 96: 12 and 12), and twice the rows take 1.3 times as long (32 sequences of 8192
-// tokens, eight key heads: 116 us instead of 91; heads of 64 71 instead of 53).
+// (heads of 128: 124 bytes stored, 184 loaded; of 96: 12 and 12), and twice the rows take 1.3 times as long (32 sequences of 8192
+// tokens, eight key heads: 116 us instead of 91; heads of 64 72 instead of 52).
 static int ac_rows(int max_q, int group) { return static_cast<long long>(max_q) * group <= 8 ? 8 : 16; }
 
 }  // namespace mptp
@@ -1032,7 +1018,7 @@ extern "C" mp_status mp_attn_cache_fwd(const mp_bf16* Q, const uint8_t* kc, cons
     a.inv_group = 1.0f / static_cast<float>(a.group);
     a.inv_kv = 1.0f / static_cast<float>(kv_heads);
     a.causal = causal != 0;
-    a.scale_log2 = scale * AC_LOG2E;
+    a.scale_log4 = scale * (0.5f * AC_LOG2E);
     p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     a.status = d_status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

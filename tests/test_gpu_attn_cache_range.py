@@ -126,7 +126,7 @@ def test_a_scale_that_is_no_number_reaches_the_rows_that_see_it(bad):
     assert torch.equal(O[~hit], clean[0][~hit]) and torch.equal(LSE.t()[~hit], clean[1].t()[~hit])
 
 
-@pytest.mark.parametrize("by", [30, 100, 125, 150, 190])
+@pytest.mark.parametrize("by", [30, 100, 125, 150, 190, 215])
 @pytest.mark.parametrize("first", [0, 1, 2])
 @pytest.mark.parametrize("page", [16, 64])
 def test_small_probabilities_of_large_values(by, first, page):
@@ -167,3 +167,22 @@ def test_large_scores_give_the_value_of_the_largest(sign, top, n, at):
     assert torch.equal(O[0].float(), want.repeat_interleave(2, 0))
     s = float(Q[0, 0, 7]) * (1.0 if sign > 0 else -416.0 / 448)
     assert torch.all((LSE[:, 0].double() - s).abs() <= 2.0 ** -19 * abs(s))
+
+
+def test_log_sum_exp_of_few_keys():
+    """Scores of one product each, up to 4: what is left are roundings. A score's (two of 2^-24 of it, 1.4e-7 in the mean square at
+    4), its difference's from the reference (half a step below 8 in powers of four: 2^-22, 1.9e-7), the exponential's and the
+    logarithm's (2^-22 and less, 1.5e-7 each), the result's (2^-24 of 7, 2.5e-7 at most): 4e-7 together, half as much again
+    allowed."""
+    lens = list(range(1, 41))
+    Q, codes, scales, table = _make([1] * 40, lens, 16, 4, 64, 16, 26700, spread=0)
+    Q[:] = 0
+    Q[:, :, 11] = 1.0
+    scales[:, 0] = 2.0 ** -6
+    codes[:, 0] = codes[:, 0].float().nan_to_num(0).clamp(-256, 256).to(codes.dtype)
+    O, LSE = _run(Q, codes, scales, table, [1] * 40, lens, scale=1.0)
+    off = []
+    for i, n in enumerate(lens):
+        k = oracle.kv_cache_rows(f64(codes[:, 0]), f64(scales[:, 0]), table[i].tolist(), 16, 0, n)
+        off.append(f64(LSE[:, i]) - np.log(np.exp(np.repeat(k[:, :, 11], 4, axis=1)).sum(0)))
+    assert np.sqrt(np.mean(np.square(off))) < 6e-7
